@@ -433,6 +433,69 @@ FP8Q_API fp8q_status fp8q_quantize_blockwise(const void* x, int32_t dt, int64_t 
                                              float* scale_inv, uint8_t* q_t, float* scale_inv_t, void* stream);
 
 /*
+ * The product of two blockwise FP8 tensors, both stored with the reduction
+ * last (the copies fp8q_quantize_blockwise writes):
+ *   out[i][j] = sum_kb sa[i][kb] * sb(j, kb) * sum_{k in block kb} A[i][k] * B[j][k]
+ * with A, B the values of the codes and sa, sb their scale_inv ("混合精度与
+ * FP8 训练" 10.2-10.5: 1x128 activations, 128x128 weights, blocks along the
+ * reduction).  The inner sums are the tensor core's, the outer sum is FP32;
+ * BF16 output is rounded once, to nearest even.  The three products of a
+ * linear layer y = x W^T (x [T][K], W [N][K]):
+ *   Fprop  a = x.q     b = W.q    (128x128)   out [T][N]
+ *   Dgrad  a = dy.q    b = W.q_t  (128x128)   out [T][K]
+ *   Wgrad  a = dy.q_t  b = x.q_t  (1x128)     out [N][K]
+ *   a            device uint8 [m][k], 16-byte aligned, a_fmt codes
+ *   a_scale_inv  device float [m][ceil(k/128)]
+ *   b            device uint8 [n][k], 16-byte aligned, b_fmt codes (the
+ *                formats may differ)
+ *   b_scale_inv  device float: FP8Q_BLOCK_1X128 -> [n][ceil(k/128)];
+ *                FP8Q_BLOCK_128X128 -> [ceil(n/128)][ceil(k/128)]
+ *   out          device BF16 or FP32 [m][n] (out_dt, fp8q_out_dtype)
+ *   accumulate   nonzero: out += the product (FP32 output only)
+ * m and n are any, k % 16 == 0 (FP8Q_ERR_UNSUPPORTED otherwise); k == 0
+ * gives zeros.  NaN and Inf codes propagate as in the sum above.
+ */
+FP8Q_API fp8q_status fp8q_matmul_blockwise(const uint8_t* a, const float* a_scale_inv, int32_t a_fmt,
+                                           const uint8_t* b, const float* b_scale_inv, int32_t b_fmt,
+                                           int32_t b_block, int64_t m, int64_t n, int64_t k, int32_t out_dt,
+                                           int32_t accumulate, void* out, void* stream);
+
+/*
+ * The experts' products: rows of group g of a times the g-th matrix of b,
+ *   out[i][j] = sum_k A[i][k] * B[g][j][k],  group_offsets[g] <= i < group_offsets[g + 1],
+ * with the scales of fp8q_matmul_blockwise (b in 128x128 blocks).  Groups
+ * may start at any row and be empty; rows in no group are not written.
+ *   a              device uint8 [rows][k];  a_scale_inv [rows][ceil(k/128)]
+ *   b              device uint8 [num_groups][n][k]
+ *   b_scale_inv    device float [num_groups][ceil(n/128)][ceil(k/128)]
+ *   group_offsets  device int64 [num_groups + 1], required
+ *   out            device BF16 or FP32 [rows][n]
+ */
+FP8Q_API fp8q_status fp8q_matmul_grouped(const uint8_t* a, const float* a_scale_inv, int32_t a_fmt,
+                                         const uint8_t* b, const float* b_scale_inv, int32_t b_fmt,
+                                         const int64_t* group_offsets, int32_t num_groups, int64_t rows, int64_t n,
+                                         int64_t k, int32_t out_dt, void* out, void* stream);
+
+/*
+ * The experts' weight gradients: a reduction over each group's rows of two
+ * transposed copies,
+ *   out[g][i][j] = sum over the rows r of group g of A[i][r] * B[j][r].
+ *   a_t            device uint8 [m][rows];  a_scale_inv_t [m][ceil(rows/128)]
+ *   b_t            device uint8 [n][rows];  b_scale_inv_t [n][ceil(rows/128)]
+ *   group_offsets  device int64 [num_groups + 1]: multiples of 128, so that
+ *                  no 128x1 scale group spans two groups; the last may be
+ *                  rows itself.  (Others give unspecified values.)
+ *   out            device BF16 or FP32 [num_groups][m][n]; an empty group's
+ *                  matrix is zero (left as it is with accumulate)
+ * rows % 16 == 0 (FP8Q_ERR_UNSUPPORTED otherwise); accumulate as above.
+ */
+FP8Q_API fp8q_status fp8q_matmul_grouped_wgrad(const uint8_t* a_t, const float* a_scale_inv_t, int32_t a_fmt,
+                                               const uint8_t* b_t, const float* b_scale_inv_t, int32_t b_fmt,
+                                               const int64_t* group_offsets, int32_t num_groups, int64_t rows,
+                                               int64_t m, int64_t n, int32_t out_dt, int32_t accumulate, void* out,
+                                               void* stream);
+
+/*
  * NVFP4 ("混合精度与 FP8 训练" 13.2): E2M1 elements (0, 0.5, 1, 1.5, 2, 3,
  * 4, 6 and negatives), one E4M3 scale per 16 elements along a row, and one
  * FP32 scale for the tensor.  Each step is one IEEE single operation:

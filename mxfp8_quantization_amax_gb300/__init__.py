@@ -31,6 +31,7 @@ __all__ = [
     "fp8q_qstats_workspace_bytes", "fp8q_qstats_per_tensor", "mxfp8_qstats", "qstats_dict",
     "E2M1", "E2M3", "E3M2", "mx_quantize_fp4_fp6", "mx_scales_to_mma_layout",
     "SCALES_ROW_MAJOR", "SCALES_MMA", "mxfp8_mma_scale_bytes",
+    "fp8q_matmul_blockwise", "fp8q_matmul_grouped", "fp8q_matmul_grouped_wgrad",
 ]
 
 E4M3 = 0
@@ -65,6 +66,12 @@ _SIGS = {
     "mxfp8_mma_scale_bytes": (_c.c_int64, [_c.c_int64, _c.c_int64]),
     "fp8q_quantize_blockwise": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32,
                                            _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P]),
+    "fp8q_matmul_blockwise": (_c.c_int, [_P, _P, _c.c_int32, _P, _P, _c.c_int32, _c.c_int32, _c.c_int64, _c.c_int64,
+                                         _c.c_int64, _c.c_int32, _c.c_int32, _P, _P]),
+    "fp8q_matmul_grouped": (_c.c_int, [_P, _P, _c.c_int32, _P, _P, _c.c_int32, _P, _c.c_int32, _c.c_int64, _c.c_int64,
+                                       _c.c_int64, _c.c_int32, _P, _P]),
+    "fp8q_matmul_grouped_wgrad": (_c.c_int, [_P, _P, _c.c_int32, _P, _P, _c.c_int32, _P, _c.c_int32, _c.c_int64,
+                                             _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _P, _P]),
     "fp8q_quantize_nvfp4": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _P, _P, _P]),
     "fp8q_dequantize_per_tensor": (_c.c_int, [_P, _c.c_int64, _c.c_int64, _P, _c.c_int32, _c.c_int32, _P,
                                               _c.c_int32, _P, _P]),
@@ -647,6 +654,116 @@ def fp8q_quantize_blockwise(x: torch.Tensor, fmt: int = E4M3, block: int = BLOCK
                                          direction, _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t), _stream()),
            "fp8q_quantize_blockwise")
     return {"q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
+
+
+# ---------------------------------------------------------------------------
+# products of blockwise FP8 tensors
+# ---------------------------------------------------------------------------
+def _codes(t: torch.Tensor, name: str, dims: int):
+    if not t.is_cuda or t.dtype != torch.uint8 or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dims}-D uint8 CUDA tensor")
+
+
+def _floats(t: torch.Tensor, name: str, shape: tuple):
+    if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {shape}")
+
+
+def _result(out, shape: tuple, dtype, device):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not out.is_cuda or out.dtype != dtype or tuple(out.shape) != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dtype} CUDA tensor of shape {shape}")
+    return out
+
+
+def _group_offsets(group_offsets, device):
+    if group_offsets is None:
+        raise ValueError("group_offsets is required")
+    off, groups = _offsets(group_offsets, device)
+    if groups < 1:
+        raise ValueError("group_offsets must hold num_groups + 1 values")
+    return off, groups
+
+
+def fp8q_matmul_blockwise(a: torch.Tensor, a_scale_inv: torch.Tensor, b: torch.Tensor, b_scale_inv: torch.Tensor,
+                          a_fmt: int = E4M3, b_fmt: int = E4M3, b_block: int = BLOCK_128X128,
+                          out_dtype=torch.bfloat16, accumulate: bool = False,
+                          out: torch.Tensor | None = None) -> torch.Tensor:
+    """a [m, k] times b [n, k] transposed, codes of fp8q_quantize_blockwise with
+    their scale_inv (a in 1x128 groups; b in 128x128 blocks, or in 1x128 groups
+    with b_block BLOCK_1X128): out [m, n] in out_dtype.
+
+    Fprop: x.q, W.q.  Dgrad: dy.q, W.q_t.  Wgrad: dy.q_t, x.q_t with
+    BLOCK_1X128.  accumulate adds to a given float32 out."""
+    _codes(a, "a", 2)
+    _codes(b, "b", 2)
+    m, k = a.shape
+    n = b.shape[0]
+    if b.shape[1] != k:
+        raise ValueError("a and b must have the same reduction length")
+    kb = (k + 127) // 128
+    _floats(a_scale_inv, "a_scale_inv", (m, kb))
+    _floats(b_scale_inv, "b_scale_inv", (n if b_block == BLOCK_1X128 else (n + 127) // 128, kb))
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    y = _result(out, (m, n), out_dtype, a.device)
+    _check(lib().fp8q_matmul_blockwise(_ptr(a), _ptr(a_scale_inv), a_fmt, _ptr(b), _ptr(b_scale_inv), b_fmt, b_block,
+                                       m, n, k, _out_dtype(out_dtype), 1 if accumulate else 0, _ptr(y), _stream()),
+           "fp8q_matmul_blockwise")
+    return y
+
+
+def fp8q_matmul_grouped(a: torch.Tensor, a_scale_inv: torch.Tensor, b: torch.Tensor, b_scale_inv: torch.Tensor,
+                        group_offsets, a_fmt: int = E4M3, b_fmt: int = E4M3, out_dtype=torch.bfloat16,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows [group_offsets[g], group_offsets[g+1]) of a [rows, k] times b[g]
+    (b [groups, n, k], 128x128 blocks) transposed: out [rows, n].  Rows in no
+    group are not written."""
+    _codes(a, "a", 2)
+    _codes(b, "b", 3)
+    rows, k = a.shape
+    groups, n = b.shape[:2]
+    if b.shape[2] != k:
+        raise ValueError("a and b must have the same reduction length")
+    kb = (k + 127) // 128
+    _floats(a_scale_inv, "a_scale_inv", (rows, kb))
+    _floats(b_scale_inv, "b_scale_inv", (groups, (n + 127) // 128, kb))
+    off, g = _group_offsets(group_offsets, a.device)
+    if g != groups:
+        raise ValueError("b must hold one matrix per group")
+    y = _result(out, (rows, n), out_dtype, a.device)
+    _check(lib().fp8q_matmul_grouped(_ptr(a), _ptr(a_scale_inv), a_fmt, _ptr(b), _ptr(b_scale_inv), b_fmt, _ptr(off),
+                                     groups, rows, n, k, _out_dtype(out_dtype), _ptr(y), _stream()),
+           "fp8q_matmul_grouped")
+    return y
+
+
+def fp8q_matmul_grouped_wgrad(a_t: torch.Tensor, a_scale_inv_t: torch.Tensor, b_t: torch.Tensor,
+                              b_scale_inv_t: torch.Tensor, group_offsets, a_fmt: int = E4M3, b_fmt: int = E4M3,
+                              out_dtype=torch.float32, accumulate: bool = False,
+                              out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[g] = a_t[:, rows of g] times b_t[:, rows of g] transposed, for the
+    transposed copies a_t [m, rows] and b_t [n, rows] (128x1 groups along the
+    rows): out [groups, m, n].  group_offsets are multiples of 128."""
+    _codes(a_t, "a_t", 2)
+    _codes(b_t, "b_t", 2)
+    m, rows = a_t.shape
+    n = b_t.shape[0]
+    if b_t.shape[1] != rows:
+        raise ValueError("a_t and b_t must have the same number of rows to reduce over")
+    rb = (rows + 127) // 128
+    _floats(a_scale_inv_t, "a_scale_inv_t", (m, rb))
+    _floats(b_scale_inv_t, "b_scale_inv_t", (n, rb))
+    off, groups = _group_offsets(group_offsets, a_t.device)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    y = _result(out, (groups, m, n), out_dtype, a_t.device)
+    _check(lib().fp8q_matmul_grouped_wgrad(_ptr(a_t), _ptr(a_scale_inv_t), a_fmt, _ptr(b_t), _ptr(b_scale_inv_t),
+                                           b_fmt, _ptr(off), groups, rows, m, n, _out_dtype(out_dtype),
+                                           1 if accumulate else 0, _ptr(y), _stream()),
+           "fp8q_matmul_grouped_wgrad")
+    return y
 
 
 # ---------------------------------------------------------------------------

@@ -124,14 +124,15 @@ const char* fp8q_last_error_string(void) { return g_err; }
 
 fp8q_status fp8q_check_device(void* stream) {
   g_err[0] = 0;
-  unsigned mx = 0, pt = 0, bw = 0, lo = 0, qs = 0;
+  unsigned mx = 0, pt = 0, bw = 0, lo = 0, qs = 0, mm = 0;
   fp8q_status r = mx_device_status((cudaStream_t)stream, true, &mx);
   if (r != FP8Q_OK) return r;
   if ((r = pt_device_status(true, &pt)) != FP8Q_OK) return r;
   if ((r = bw_device_status(true, &bw)) != FP8Q_OK) return r;
   if ((r = low_device_status(true, &lo)) != FP8Q_OK) return r;
   if ((r = qs_device_status(true, &qs)) != FP8Q_OK) return r;
-  if ((mx | pt | bw | lo | qs) & 1u)
+  if ((r = mm_device_status(true, &mm)) != FP8Q_OK) return r;
+  if ((mx | pt | bw | lo | qs | mm) & 1u)
     return fail(FP8Q_ERR_TIMEOUT, "a bounded device-side wait gave up; the outputs of that call are incomplete");
   return FP8Q_OK;
 }
@@ -142,6 +143,7 @@ fp8q_status fp8q_set_wait_budget_ns(uint64_t ns) {
   if (r == FP8Q_OK) r = pt_set_wait_budget((unsigned long long)ns);
   if (r == FP8Q_OK) r = low_set_wait_budget((unsigned long long)ns);
   if (r == FP8Q_OK) r = qs_set_wait_budget((unsigned long long)ns);
+  if (r == FP8Q_OK) r = mm_set_wait_budget((unsigned long long)ns);
   return r != FP8Q_OK ? r : bw_set_wait_budget((unsigned long long)ns);
 }
 
@@ -458,6 +460,122 @@ fp8q_status fp8q_quantize_blockwise(const void* x, int32_t dt, int64_t rows, int
   }
   return launch_blockwise(x, rows, cols, fmt, block, pow2_scales ? 1 : 0, dir, q, scale_inv, q_t, scale_inv_t,
                           (cudaStream_t)stream);
+}
+
+// Every argument check of the product entry points.
+static fp8q_status check_matmul(const MatmulLaunch& L) {
+  if (!fmt_ok(L.a_fmt) || !fmt_ok(L.b_fmt)) return fail(FP8Q_ERR_INVALID_ARG, "a_fmt and b_fmt must be FP8Q_E4M3 or FP8Q_E5M2");
+  if (L.b_block != FP8Q_BLOCK_1X128 && L.b_block != FP8Q_BLOCK_128X128)
+    return fail(FP8Q_ERR_INVALID_ARG, "b_block must be FP8Q_BLOCK_1X128 or FP8Q_BLOCK_128X128");
+  if (L.out_dt != FP8Q_OUT_BF16 && L.out_dt != FP8Q_OUT_FP32)
+    return fail(FP8Q_ERR_INVALID_ARG, "out_dt must be FP8Q_OUT_BF16 or FP8Q_OUT_FP32");
+  if (L.accumulate && L.out_dt != FP8Q_OUT_FP32) return fail(FP8Q_ERR_UNSUPPORTED, "accumulate needs FP32 output");
+  if (L.m < 0 || L.n < 0 || L.k < 0) return fail(FP8Q_ERR_INVALID_ARG, "sizes must be >= 0");
+  if (L.groups < 1 || L.groups > FP8Q_MAX_GROUPS)
+    return fail(FP8Q_ERR_INVALID_ARG, "num_groups must be in [1, %d]", FP8Q_MAX_GROUPS);
+  if (L.kind != kMatmulDense && (!L.off || !aligned(L.off, 8)))
+    return fail(FP8Q_ERR_INVALID_ARG, "group_offsets must be an 8-byte aligned device pointer");
+  if (L.k % 16 != 0) return fail(FP8Q_ERR_UNSUPPORTED, "the product needs a reduction length that is a multiple of 16");
+  // rows and columns are 32-bit TMA coordinates, with room for a tile past the end
+  const int64_t most = INT32_MAX - 512;
+  if (L.m > most || L.k > most || L.n > most / L.groups) return fail(FP8Q_ERR_UNSUPPORTED, "a size is too large");
+  if (L.m * L.n == 0) return FP8Q_OK;
+  if (!L.out || !aligned(L.out, L.out_dt == FP8Q_OUT_FP32 ? 4 : 2))
+    return fail(FP8Q_ERR_INVALID_ARG, "out must be a device pointer aligned to its type");
+  if (L.k == 0) return FP8Q_OK;
+  if (!L.a || !L.b || !aligned(L.a, 16) || !aligned(L.b, 16))
+    return fail(FP8Q_ERR_INVALID_ARG, "a and b must be 16-byte aligned device pointers");
+  if (!L.sa || !L.sb || !aligned(L.sa, 4) || !aligned(L.sb, 4))
+    return fail(FP8Q_ERR_INVALID_ARG, "the scales must be 4-byte aligned device pointers");
+  return FP8Q_OK;
+}
+
+static fp8q_status run_matmul(const MatmulLaunch& L) {
+  const fp8q_status r = check_matmul(L);
+  if (r != FP8Q_OK) return r;
+  const int64_t values = L.m * L.n * (L.kind == kMatmulKGroups ? L.groups : 1);
+  if (values == 0) return FP8Q_OK;
+  if (L.k == 0) {  // empty sums
+    if (L.accumulate) return FP8Q_OK;
+    const cudaError_t e = cudaMemsetAsync(L.out, 0, (size_t)values * (L.out_dt == FP8Q_OUT_FP32 ? 4 : 2), L.stream);
+    return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "cudaMemsetAsync");
+  }
+  return launch_matmul(L);
+}
+
+fp8q_status fp8q_matmul_blockwise(const uint8_t* a, const float* a_scale_inv, int32_t a_fmt, const uint8_t* b,
+                                  const float* b_scale_inv, int32_t b_fmt, int32_t b_block, int64_t m, int64_t n,
+                                  int64_t k, int32_t out_dt, int32_t accumulate, void* out, void* stream) {
+  g_err[0] = 0;
+  MatmulLaunch L{};
+  L.kind = kMatmulDense;
+  L.a = a;
+  L.sa = a_scale_inv;
+  L.a_fmt = a_fmt;
+  L.b = b;
+  L.sb = b_scale_inv;
+  L.b_fmt = b_fmt;
+  L.b_block = b_block;
+  L.m = m;
+  L.n = n;
+  L.k = k;
+  L.groups = 1;
+  L.out_dt = out_dt;
+  L.accumulate = accumulate ? 1 : 0;
+  L.out = out;
+  L.stream = (cudaStream_t)stream;
+  return run_matmul(L);
+}
+
+fp8q_status fp8q_matmul_grouped(const uint8_t* a, const float* a_scale_inv, int32_t a_fmt, const uint8_t* b,
+                                const float* b_scale_inv, int32_t b_fmt, const int64_t* group_offsets,
+                                int32_t num_groups, int64_t rows, int64_t n, int64_t k, int32_t out_dt, void* out,
+                                void* stream) {
+  g_err[0] = 0;
+  MatmulLaunch L{};
+  L.kind = kMatmulRowGroups;
+  L.a = a;
+  L.sa = a_scale_inv;
+  L.a_fmt = a_fmt;
+  L.b = b;
+  L.sb = b_scale_inv;
+  L.b_fmt = b_fmt;
+  L.b_block = FP8Q_BLOCK_128X128;
+  L.m = rows;
+  L.n = n;
+  L.k = k;
+  L.off = group_offsets;
+  L.groups = num_groups;
+  L.out_dt = out_dt;
+  L.out = out;
+  L.stream = (cudaStream_t)stream;
+  return run_matmul(L);
+}
+
+fp8q_status fp8q_matmul_grouped_wgrad(const uint8_t* a_t, const float* a_scale_inv_t, int32_t a_fmt,
+                                      const uint8_t* b_t, const float* b_scale_inv_t, int32_t b_fmt,
+                                      const int64_t* group_offsets, int32_t num_groups, int64_t rows, int64_t m,
+                                      int64_t n, int32_t out_dt, int32_t accumulate, void* out, void* stream) {
+  g_err[0] = 0;
+  MatmulLaunch L{};
+  L.kind = kMatmulKGroups;
+  L.a = a_t;
+  L.sa = a_scale_inv_t;
+  L.a_fmt = a_fmt;
+  L.b = b_t;
+  L.sb = b_scale_inv_t;
+  L.b_fmt = b_fmt;
+  L.b_block = FP8Q_BLOCK_1X128;
+  L.m = m;
+  L.n = n;
+  L.k = rows;
+  L.off = group_offsets;
+  L.groups = num_groups;
+  L.out_dt = out_dt;
+  L.accumulate = accumulate ? 1 : 0;
+  L.out = out;
+  L.stream = (cudaStream_t)stream;
+  return run_matmul(L);
 }
 
 fp8q_status fp8q_quantize_nvfp4(const void* x, int32_t dt, int64_t rows, int64_t cols, uint8_t* q, uint8_t* s,

@@ -145,6 +145,24 @@ fp8q_status launch_scale(const float* amax, int G, int fmt, int margin, float* s
 fp8q_status pt_device_status(bool clear, unsigned* word);
 fp8q_status pt_set_wait_budget(unsigned long long ns);
 fp8q_status pt_set_stall_publish(bool on);
+// Products of blockwise FP8 tensors (matmul.cu).
+enum MatmulKind : int { kMatmulDense = 0, kMatmulRowGroups = 1, kMatmulKGroups = 2 };
+struct MatmulLaunch {
+  int kind;
+  const uint8_t* a;  // [m][k]
+  const float* sa;   // [m][ceil(k / 128)]
+  const uint8_t* b;  // [n][k]; row groups: [groups][n][k]
+  const float* sb;   // by b_block
+  int64_t m, n, k;
+  const int64_t* off;
+  int groups;
+  int a_fmt, b_fmt, b_block, out_dt, accumulate;
+  void* out;
+  cudaStream_t stream;
+};
+fp8q_status launch_matmul(const MatmulLaunch& L);
+fp8q_status mm_device_status(bool clear, unsigned* word);
+fp8q_status mm_set_wait_budget(unsigned long long ns);
 // Zeroes `bytes` (a multiple of 4) at p in stream order with a kernel that
 // keeps the chain of programmatic launches (a few counters or accumulators).
 fp8q_status launch_zero_words(void* p, size_t bytes, cudaStream_t s);

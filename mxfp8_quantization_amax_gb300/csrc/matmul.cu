@@ -1,0 +1,521 @@
+// matmul.cu -- the product of blockwise FP8 tensors on the tensor cores: one
+// matrix product, the products of rows sorted by expert, and the experts'
+// weight gradients.
+//
+//   D[m, n] = sum_kb sa[m, kb] * sb(n, kb) * P_kb[m, n],
+//   P_kb[m, n] = sum over the 128 values k of block kb of A[m, k] * B[n, k],
+//
+// with A and B the 8-bit codes (both K-major, as fp8q_quantize_blockwise
+// leaves them) and sa, sb their scale_inv ("混合精度与 FP8 训练" 10.2-10.5).
+// The scales change every 128 values of K, so the tensor core sums one block
+// at a time and the sum over blocks is taken in FP32 registers.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "fp8q_device.cuh"
+#include "internal.h"
+#include "umma.cuh"
+
+namespace fp8q {
+
+constexpr int kMmBlock = 128;  // values of K that share a scale
+constexpr int kMmRows = 128;   // rows of A in a tile
+constexpr int kMmEpiWarps = 8;
+constexpr int kMmThreads = (kMmEpiWarps + 2) * 32;
+constexpr uint64_t kMmDrainNs = 2000000000ull;
+
+__device__ unsigned int g_mm_error;
+__device__ unsigned long long g_mm_wait_budget_ns = 1000000000ull;
+
+// What the groups divide: nothing, the rows of A and D, or K.
+enum : int { kMmDense = 0, kMmRowGroups = 1, kMmKGroups = 2 };
+
+struct MmParams {
+  int64_t m, n, k;   // rows of A, rows of B (of one group), values along K
+  const float* sa;   // [m][sa_ld]
+  const float* sb;   // 1x128: [n][sb_ld]; 128x128: [groups][ceil(n / 128)][sb_ld]
+  int64_t sa_ld, sb_ld;
+  const int64_t* off;
+  int groups;
+  int tiles_n;
+  int accumulate;
+  uint32_t idesc;
+  void* out;         // [m][n]; K groups: [groups][m][n]
+};
+
+template <int BN>
+struct MmShape {
+  static constexpr int kABytes = kMmRows * kMmBlock;
+  static constexpr int kBBytes = BN * kMmBlock;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = BN == 256 ? 4 : 6;
+  static constexpr int kCols = BN / 2;  // columns of one epilogue warp
+};
+
+struct MmTile {
+  int g;
+  int64_t row0, row_end;  // rows of A and D
+  int64_t n0;
+  int64_t k0;             // first value of K
+  int nkb;                // blocks of K
+};
+
+__device__ __forceinline__ int64_t mm_clamped(const int64_t* off, int g, int64_t hi) {
+  const int64_t v = __ldg(off + g);
+  return v < 0 ? 0 : v > hi ? hi : v;
+}
+
+// Tile t of the grid-wide list.  Inside a group, bands of 16 row tiles are
+// walked row tile first, so the CTAs of one wave read few distinct tiles of
+// A and of B and find them in L2.
+template <int BN, int MODE>
+__device__ __forceinline__ MmTile mm_tile(const MmParams& p, const unsigned* first, uint32_t t) {
+  MmTile r;
+  r.g = 0;
+  int64_t lo = 0, hi = p.m;
+  uint32_t mt_all;
+  if constexpr (MODE == kMmRowGroups) {
+    int a = 0, b = p.groups;  // last g whose first tile is <= t
+    while (b - a > 1) {
+      const int mid = (a + b) >> 1;
+      if ((uint64_t)first[mid] * p.tiles_n <= t) a = mid; else b = mid;
+    }
+    r.g = a;
+    t -= first[a] * p.tiles_n;
+    mt_all = first[a + 1] - first[a];
+    lo = mm_clamped(p.off, a, p.m);
+    hi = mm_clamped(p.off, a + 1, p.m);
+  } else {
+    mt_all = (uint32_t)((p.m + kMmRows - 1) / kMmRows);
+    if constexpr (MODE == kMmKGroups) {
+      const uint32_t per = mt_all * p.tiles_n;
+      r.g = (int)(t / per);
+      t -= r.g * per;
+    }
+  }
+  const uint32_t per_band = 16u * p.tiles_n, band = t / per_band;
+  const uint32_t in_band = t - band * per_band, rest = mt_all - band * 16u, height = rest < 16u ? rest : 16u;
+  r.row0 = lo + (int64_t)(band * 16u + in_band % height) * kMmRows;
+  r.row_end = hi;
+  r.n0 = (int64_t)(in_band / height) * BN;
+  r.k0 = 0;
+  int64_t k1 = p.k;
+  if constexpr (MODE == kMmKGroups) {
+    // a start off the 128 grid breaks the caller's promise; rounded down it
+    // still makes an aligned TMA coordinate
+    r.k0 = mm_clamped(p.off, r.g, p.k) & ~(int64_t)(kMmBlock - 1);
+    k1 = mm_clamped(p.off, r.g + 1, p.k);
+  }
+  r.nkb = k1 > r.k0 ? (int)((k1 - r.k0 + kMmBlock - 1) / kMmBlock) : 0;
+  return r;
+}
+
+// first[g] = row tiles of the groups before g, first[groups] = all of them.
+__device__ __forceinline__ void mm_scan_groups(const MmParams& p, unsigned* first, unsigned* sums) {
+  const int tid = threadIdx.x, per = (p.groups + 255) / 256;
+  const int g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
+  uint64_t mine = 0;
+  if (tid < 256) {
+    for (int g = g0; g < g1; g++) {
+      const int64_t n = mm_clamped(p.off, g + 1, p.m) - mm_clamped(p.off, g, p.m);
+      mine += n > 0 ? (uint64_t)((n + kMmRows - 1) / kMmRows) : 0;
+    }
+    sums[tid] = (unsigned)(mine < 0x7FFFFFu ? mine : 0x7FFFFFu);
+  }
+  __syncthreads();
+  if (tid < 32) {  // exclusive scan of 256 sums: 8 per lane
+    unsigned s[8], total = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      s[i] = total;
+      total += sums[tid * 8 + i];
+    }
+    unsigned incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (tid >= o) incl += v;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) sums[tid * 8 + i] = incl - total + s[i];
+    if (tid == 31) first[p.groups] = incl;
+  }
+  __syncthreads();
+  if (tid < 256) {
+    unsigned at = sums[tid];
+    for (int g = g0; g < g1; g++) {
+      first[g] = at;
+      const int64_t n = mm_clamped(p.off, g + 1, p.m) - mm_clamped(p.off, g, p.m);
+      at += n > 0 ? (unsigned)((n + kMmRows - 1) / kMmRows) : 0;
+    }
+  }
+  __syncthreads();
+}
+
+// Stores COLS consecutive values of one row, those below column n.
+template <int COLS, bool F32>
+__device__ __forceinline__ void mm_store_row(const MmParams& p, int64_t row, int64_t c0, const uint64_t (&acc)[COLS / 2]) {
+  const int64_t left = p.n - c0;
+  if constexpr (F32) {
+    float* o = (float*)p.out + row * p.n + c0;
+    if (p.n % 8 == 0 && ((uintptr_t)p.out & 31) == 0) {
+#pragma unroll
+      for (int c = 0; c < COLS; c += 8) {
+        if (c < left) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; i++) unpack2(acc[c / 2 + i], v[2 * i], v[2 * i + 1]);
+          if (p.accumulate) {
+            const float4 a = *(const float4*)(o + c), b = *(const float4*)(o + c + 4);
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+          }
+          uint32_t d[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) d[i] = __float_as_uint(v[i]);
+          st32B(o + c, d);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < COLS; c += 2) {
+        float x, y;
+        unpack2(acc[c / 2], x, y);
+        if (c < left) o[c] = p.accumulate ? o[c] + x : x;
+        if (c + 1 < left) o[c + 1] = p.accumulate ? o[c + 1] + y : y;
+      }
+    }
+  } else {
+    uint16_t* o = (uint16_t*)p.out + row * p.n + c0;
+    if (p.n % 16 == 0 && ((uintptr_t)p.out & 31) == 0) {
+#pragma unroll
+      for (int c = 0; c < COLS; c += 16) {
+        if (c < left) {
+          uint32_t d[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            float x, y;
+            unpack2(acc[c / 2 + i], x, y);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d[i]) : "f"(y), "f"(x));
+          }
+          st32B(o + c, d);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < COLS; c += 2) {
+        float x, y;
+        uint32_t d;
+        unpack2(acc[c / 2], x, y);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(y), "f"(x));
+        if (c < left) o[c] = (uint16_t)d;
+        if (c + 1 < left) o[c + 1] = (uint16_t)(d >> 16);
+      }
+    }
+  }
+}
+
+// BN: rows of B in a tile.  COLSCALE: B has a scale for each of its rows
+// (1x128 groups), else one for each 128 of them.
+template <int BN, bool COLSCALE, bool F32, int MODE>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, MmParams p) {
+  using S = MmShape<BN>;
+  constexpr int COLS = S::kCols;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], done[2], taken[2], drained;
+  __shared__ uint32_t tmem_base;
+  __shared__ unsigned sums[256];
+  __shared__ __align__(16) float sbuf[COLSCALE ? kMmEpiWarps : 1][2][COLSCALE ? COLS : 4];
+  __shared__ volatile int abort_flag;
+  unsigned char* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  unsigned* first = (unsigned*)(stages + S::kStages * S::kStageBytes);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; s++) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; b++) {
+      mbar_init(&done[b], 1);
+      mbar_init(&taken[b], kMmEpiWarps);
+    }
+    mbar_init(&drained, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmEpiWarps) {
+    tmem_alloc(&tmem_base, 2 * BN);
+    tc_fence_before();
+    if (lane == 0) {
+      prefetch_tensormap(&map_a);
+      prefetch_tensormap(&map_b);
+    }
+  }
+  pdl_wait();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint64_t budget = g_mm_wait_budget_ns;
+
+  uint32_t tiles;
+  if constexpr (MODE == kMmRowGroups) {
+    mm_scan_groups(p, first, sums);
+    tiles = first[p.groups] * (uint32_t)p.tiles_n;
+  } else {
+    tiles = (uint32_t)((p.m + kMmRows - 1) / kMmRows) * (uint32_t)p.tiles_n * (uint32_t)p.groups;
+  }
+
+  if (warp == kMmEpiWarps) {
+    // ---------------- loads: one thread ----------------
+    if (lane == 0) {
+      uint32_t it = 0;  // blocks of K issued
+      for (uint32_t t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
+        const MmTile w = mm_tile<BN, MODE>(p, first, t);
+        const int brow = (int)(w.n0 + (MODE == kMmRowGroups ? (int64_t)w.g * p.n : 0));
+        for (int kb = 0; kb < w.nkb && !abort_flag; kb++, it++) {
+          const uint32_t s = it % S::kStages, round = it / S::kStages;
+          if (round > 0 && !mbar_wait(&empty[s], (round - 1) & 1u, budget)) {
+            atomicOr(&g_mm_error, 1u);
+            abort_flag = 1;
+            break;
+          }
+          unsigned char* st = stages + s * S::kStageBytes;
+          mbar_arrive_expect_tx(&full[s], S::kStageBytes);
+          tma_load_2d(st, &map_a, (int)(w.k0 + (int64_t)kb * kMmBlock), (int)w.row0, &full[s]);
+          tma_load_2d(st + S::kABytes, &map_b, (int)(w.k0 + (int64_t)kb * kMmBlock), brow, &full[s]);
+        }
+      }
+      pdl_launch_dependents();
+      // every issued copy lands before the CTA can exit (fixed 2 s bound)
+      for (uint32_t j = it > S::kStages ? it - S::kStages : 0; j < it; j++)
+        mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
+    }
+  } else if (warp == kMmEpiWarps + 1) {
+    // ---------------- tensor core: one thread ----------------
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (uint32_t t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
+        const MmTile w = mm_tile<BN, MODE>(p, first, t);
+        for (int kb = 0; kb < w.nkb && !abort_flag; kb++, it++) {
+          const uint32_t s = it % S::kStages, round = it / S::kStages, b = it & 1u, use = it >> 1;
+          if ((use > 0 && !mbar_wait(&taken[b], (use - 1) & 1u, budget)) || !mbar_wait(&full[s], round & 1u, budget)) {
+            atomicOr(&g_mm_error, 1u);
+            abort_flag = 1;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_u32(stages + s * S::kStageBytes);
+          const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + S::kABytes);
+#pragma unroll
+          for (int k = 0; k < kMmBlock / 32; k++) mma_f8(tmem + b * BN, da + 2 * k, db + 2 * k, p.idesc, k > 0);
+          mma_commit(&empty[s]);
+          mma_commit(&done[b]);
+        }
+      }
+      // nothing is in flight when the tensor memory is freed
+      mma_commit(&drained);
+      mbar_wait(&drained, 0, kMmDrainNs);
+    }
+  } else {
+    // ---------------- sums over the blocks and the epilogue ----------------
+    const int half = warp >> 2;               // columns [half * COLS, half * COLS + COLS)
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+    const uint32_t taddr = tmem + lanes + half * COLS;
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const MmTile w = mm_tile<BN, MODE>(p, first, t);
+      const int64_t row = w.row0 + (warp & 3) * 32 + lane;
+      const int64_t c0 = w.n0 + half * COLS;
+      const int64_t kb0 = w.k0 / kMmBlock;
+      const float* sa = p.sa + (row < p.m ? row : p.m - 1) * p.sa_ld + kb0;
+      const float* sb;
+      float nsb[COLSCALE ? COLS / 32 : 1];
+      if constexpr (COLSCALE) {
+        sb = p.sb + kb0;
+      } else {
+        const int64_t nb = (p.n + kMmBlock - 1) / kMmBlock;
+        const int64_t cb = c0 / kMmBlock < nb ? c0 / kMmBlock : nb - 1;
+        sb = p.sb + ((MODE == kMmRowGroups ? (int64_t)w.g * nb : 0) + cb) * p.sb_ld;
+      }
+      const auto load_sb = [&](int kb) {
+        if constexpr (COLSCALE) {
+#pragma unroll
+          for (int i = 0; i < COLS / 32; i++) {
+            const int64_t c = c0 + lane + 32 * i;
+            nsb[i] = __ldg(sb + (c < p.n ? c : p.n - 1) * p.sb_ld + kb);
+          }
+        } else {
+          nsb[0] = __ldg(sb + kb);
+        }
+      };
+      uint64_t acc[COLS / 2];
+#pragma unroll
+      for (int i = 0; i < COLS / 2; i++) acc[i] = 0;
+      float nsa = 0.f;
+      if (w.nkb > 0) {
+        nsa = __ldg(sa);
+        load_sb(0);
+      }
+      for (int kb = 0; kb < w.nkb; kb++, it++) {
+        const uint32_t b = it & 1u, use = it >> 1;
+        float scale = nsa;
+        if constexpr (COLSCALE) {
+#pragma unroll
+          for (int i = 0; i < COLS / 32; i++) sbuf[warp][b][lane + 32 * i] = nsb[i];
+          __syncwarp();
+        } else {
+          scale = __fmul_rn(nsa, nsb[0]);
+        }
+        if (kb + 1 < w.nkb) {
+          nsa = __ldg(sa + kb + 1);
+          load_sb(kb + 1);
+        }
+        const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
+        // one decision for the warp: its tensor-memory loads are collective
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&done[b], use & 1u, budget) && !abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < COLS; c += 32) {
+          uint32_t r[32];
+          tmem_load32(r, taddr + b * BN + c);
+          tmem_wait_loads();
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            uint64_t f0 = s2, f1 = s2;
+            if constexpr (COLSCALE) {
+              const ulonglong2 v = *(const ulonglong2*)&sbuf[warp][b][c + i];
+              f0 = mul2p(v.x, s2);
+              f1 = mul2p(v.y, s2);
+            }
+            acc[(c + i) / 2] = fma2(pack2(r[i], r[i + 1]), f0, acc[(c + i) / 2]);
+            acc[(c + i) / 2 + 1] = fma2(pack2(r[i + 2], r[i + 3]), f1, acc[(c + i) / 2 + 1]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[b]);
+      }
+      if (ok && row < w.row_end)
+        mm_store_row<COLS, F32>(p, (MODE == kMmKGroups ? (int64_t)w.g * p.m : 0) + row, c0, acc);
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(&g_mm_error, 1u);
+      abort_flag = 1;
+    }
+    pdl_launch_dependents();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmEpiWarps) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, 2 * BN);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+static PFN_cuTensorMapEncodeTiled_v12000 mm_encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
+  });
+  return fn;
+}
+
+// Codes [rows][k], boxes of 128 codes x box_rows.
+static fp8q_status mm_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int box_rows) {
+  auto enc = mm_encode_fn();
+  if (!enc) return fail(FP8Q_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)k};
+  cuuint32_t box[2] = {kMmBlock, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FP8Q_OK : fail(FP8Q_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+template <int BN, bool COLSCALE, bool F32, int MODE>
+static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt_a, int fmt_b, cudaStream_t s) {
+  using S = MmShape<BN>;
+  CUtensorMap ma, mb;
+  fp8q_status r = mm_map(&ma, a, p.m, p.k, kMmRows);
+  if (r != FP8Q_OK) return r;
+  if ((r = mm_map(&mb, b, MODE == kMmRowGroups ? p.n * p.groups : p.n, p.k, BN)) != FP8Q_OK) return r;
+  p.idesc = instr_desc_f8(fmt_a, fmt_b, kMmRows, BN);
+  p.tiles_n = (int)((p.n + BN - 1) / BN);
+  const size_t smem = 1024 + (size_t)S::kStages * S::kStageBytes + (MODE == kMmRowGroups ? 4 * ((size_t)p.groups + 1) : 0);
+  const auto kernel = matmul_kernel<BN, COLSCALE, F32, MODE>;
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      (int)(1024 + S::kStages * S::kStageBytes + (MODE == kMmRowGroups ? 4 * (FP8Q_MAX_GROUPS + 1) : 0)));
+  if (attr != cudaSuccess) return cuda_fail(attr, "matmul shared memory");
+  int64_t grid = sm_count();
+  const int64_t per = (p.m + kMmRows - 1) / kMmRows;
+  const int64_t tiles = (MODE == kMmRowGroups ? per + p.groups : MODE == kMmKGroups ? per * p.groups : per) * p.tiles_n;
+  if (tiles > INT32_MAX) return fail(FP8Q_ERR_UNSUPPORTED, "product too large: %lld output tiles", (long long)tiles);
+  if (grid > tiles) grid = tiles;
+  const cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kMmThreads), smem, s, ma, mb, p);
+  if (e != cudaSuccess) return cuda_fail(e, "matmul kernel launch");
+  return check_launch("matmul kernel");
+}
+
+template <bool COLSCALE, int MODE>
+static fp8q_status launch_mm_out(const void* a, const void* b, const MmParams& p, int fmt_a, int fmt_b, int out_dt,
+                                 cudaStream_t s) {
+  return out_dt == FP8Q_OUT_FP32 ? launch_mm_t<256, COLSCALE, true, MODE>(a, b, p, fmt_a, fmt_b, s)
+                                 : launch_mm_t<256, COLSCALE, false, MODE>(a, b, p, fmt_a, fmt_b, s);
+}
+
+fp8q_status launch_matmul(const MatmulLaunch& L) {
+  MmParams p{};
+  p.m = L.m;
+  p.n = L.n;
+  p.k = L.k;
+  p.sa = L.sa;
+  p.sb = L.sb;
+  p.sa_ld = p.sb_ld = (L.k + kMmBlock - 1) / kMmBlock;
+  p.off = L.off;
+  p.groups = L.groups;
+  p.accumulate = L.accumulate;
+  p.out = L.out;
+  if (L.kind == kMatmulRowGroups) return launch_mm_out<false, kMmRowGroups>(L.a, L.b, p, L.a_fmt, L.b_fmt, L.out_dt, L.stream);
+  if (L.kind == kMatmulKGroups) return launch_mm_out<true, kMmKGroups>(L.a, L.b, p, L.a_fmt, L.b_fmt, L.out_dt, L.stream);
+  return L.b_block == FP8Q_BLOCK_128X128
+             ? launch_mm_out<false, kMmDense>(L.a, L.b, p, L.a_fmt, L.b_fmt, L.out_dt, L.stream)
+             : launch_mm_out<true, kMmDense>(L.a, L.b, p, L.a_fmt, L.b_fmt, L.out_dt, L.stream);
+}
+
+fp8q_status mm_device_status(bool clear, unsigned* word) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_mm_error, sizeof(v));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyFromSymbol");
+  if (clear && v) {
+    const unsigned z = 0;
+    e = cudaMemcpyToSymbol(g_mm_error, &z, sizeof(z));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyToSymbol");
+  }
+  *word = v;
+  return FP8Q_OK;
+}
+
+fp8q_status mm_set_wait_budget(unsigned long long ns) {
+  cudaError_t e = cudaMemcpyToSymbol(g_mm_wait_budget_ns, &ns, sizeof(ns));
+  return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "cudaMemcpyToSymbol(wait budget)");
+}
+
+}  // namespace fp8q
