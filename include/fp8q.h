@@ -85,7 +85,10 @@ typedef enum { FP8Q_MX_RULE_UP = 0, FP8Q_MX_RULE_OCP = 1 } fp8q_mx_rule;
  * blocks transposed. */
 typedef enum { FP8Q_BLOCK_1X128 = 1, FP8Q_BLOCK_128X128 = 128 } fp8q_block;
 
-/* Output type of the dequantizers. */
+/* Scores of the routing: over all experts of a token, or of each alone. */
+typedef enum { FP8Q_SCORE_SOFTMAX = 0, FP8Q_SCORE_SIGMOID = 1 } fp8q_score;
+
+/* Output type of the dequantizers and of the products. */
 typedef enum { FP8Q_OUT_BF16 = 0, FP8Q_OUT_FP32 = 1 } fp8q_out_dtype;
 
 /* Library version (major * 10000 + minor * 100 + patch). */
@@ -416,8 +419,9 @@ FP8Q_API fp8q_status mx_quantize_fp4_fp6(const void* x, int32_t dt, int64_t rows
  * per-tensor special cases (amax 0 or non-finite -> 1, overflow -> FLT_MAX),
  * rounded down to a power of two when pow2_scales is set; q =
  * RNE_sat(fl32(x * scale)); scale_inv = fl32(1 / scale) is stored.
- *   x            device BF16 [rows][cols]; rows % 16 == 0, cols % 16 == 0
- *                (FP8Q_ERR_UNSUPPORTED otherwise, and for FP32 input)
+ *   x            device BF16 [rows][cols]; cols % 16 == 0, and rows % 16 == 0
+ *                for the transposed copy (FP8Q_ERR_UNSUPPORTED otherwise,
+ *                and for FP32 input)
  *   block        fp8q_block
  *   dir          MXFP8_ROW, MXFP8_COL or MXFP8_BOTH
  *   q            device uint8 [rows][cols] (rowwise copy)
@@ -494,6 +498,114 @@ FP8Q_API fp8q_status fp8q_matmul_grouped_wgrad(const uint8_t* a_t, const float* 
                                                const int64_t* group_offsets, int32_t num_groups, int64_t rows,
                                                int64_t m, int64_t n, int32_t out_dt, int32_t accumulate, void* out,
                                                void* stream);
+
+/*
+ * Routing of tokens to experts (the pages' MoE workload takes its group
+ * offsets as given; this and the plan below make them).  Scores s are a
+ * softmax of a token's logits, or 1 / (1 + exp(-x)) of each.  Keys are
+ * s + bias, or the logits themselves when there is neither a bias nor more
+ * than one group (the same order).  With num_groups > 1, a group of
+ * experts / num_groups consecutive experts is worth the sum of its two best
+ * keys (its only one if it has one expert) and only the top_groups best
+ * groups stay.  The top_k best keys are chosen, best first; equal keys and
+ * equal groups go to the lowest index.  Weights are
+ *   weight_scale * s_j / (sum of the chosen s)   with renormalize,
+ *   weight_scale * s_j                           without.
+ * A logit that is -inf or NaN, or whose key is, is never chosen (its key
+ * counts as -inf in its group); where fewer than top_k are left, the last
+ * ids are -1 and their weights 0.  A NaN logit, under softmax also +inf,
+ * makes all the token's weights NaN.  Arithmetic is FP32.
+ *   logits   device BF16 or FP32 (dt) [tokens][experts], experts <= 1024
+ *   top_k    1..32, at most experts / num_groups * top_groups
+ *   bias     device float [experts] or NULL
+ *   num_groups  1..32, divides experts
+ *   weights  device float [tokens][top_k]
+ *   ids      device int32 [tokens][top_k]
+ */
+FP8Q_API fp8q_status fp8q_moe_route(const void* logits, int32_t dt, int64_t tokens, int32_t experts, int32_t top_k,
+                                    int32_t score, const float* bias, int32_t num_groups, int32_t top_groups,
+                                    int32_t renormalize, float weight_scale, float* weights, int32_t* ids,
+                                    void* stream);
+
+/*
+ * The gradient of fp8q_moe_route's weights with respect to the logits; the
+ * choice (ids) and the bias are constants.  Slots with id -1 add nothing.
+ *   ids        device int32 [tokens][top_k], as routing wrote them
+ *   d_weights  device float [tokens][top_k]
+ *   d_logits   device, type dt, [tokens][experts]: written in full
+ */
+FP8Q_API fp8q_status fp8q_moe_route_backward(const void* logits, int32_t dt, int64_t tokens, int32_t experts,
+                                             int32_t top_k, int32_t score, int32_t renormalize, float weight_scale,
+                                             const int32_t* ids, const float* d_weights, void* d_logits,
+                                             void* stream);
+
+/* Rows that always hold `slots` rows when each expert's are padded to a
+ * multiple of align: (slots + min(slots, experts) * (align - 1)) rounded down
+ * to one (-1 for invalid arguments). */
+FP8Q_API int64_t fp8q_moe_rows(int64_t slots, int32_t experts, int32_t align);
+
+/* Bytes of workspace fp8q_moe_plan needs (contents do not matter). */
+FP8Q_API size_t fp8q_moe_plan_workspace_bytes(int64_t slots, int32_t experts);
+
+/*
+ * The experts' row order.  Slot t * top_k + j is token t's j-th expert; slots
+ * are sorted by expert, those of one expert in slot order, and each expert's
+ * segment is padded to a multiple of align rows (1 for none; 128 for
+ * transposed copies and weight gradients).
+ *   ids        device int32 [slots]; one that is no expert's (-1) drops its slot
+ *   experts    1..1024
+ *   rows       rows of the padded order, >= fp8q_moe_rows()
+ *   offsets    device int64 [experts + 1]: the segments' first rows (the
+ *              group offsets of every grouped entry point)
+ *   row_of     device int32 [slots]: a slot's row, -1 if dropped
+ *   src        device int32 [rows]: a row's slot, -1 for padding and for the
+ *              rows from offsets[experts] on
+ *   workspace  device, >= fp8q_moe_plan_workspace_bytes(), 4-byte aligned
+ */
+FP8Q_API fp8q_status fp8q_moe_plan(const int32_t* ids, int64_t slots, int32_t experts, int32_t align, int64_t rows,
+                                   int64_t* offsets, int32_t* row_of, int32_t* src, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * The tokens' rows in the plan's order, quantized as fp8q_quantize_blockwise
+ * quantizes the gathered matrix with 1x128 groups, in one pass: row r is
+ * token src[r] / top_k, zeros where src[r] is -1.
+ *   x    device BF16 [tokens][cols], 16-byte aligned; cols % 16 == 0
+ *   src  device int32 [rows]
+ *   q, scale_inv, q_t, scale_inv_t, dir: as there, with `rows` rows (rows %
+ *   16 == 0 for the transposed copy; align 128 keeps its 128x1 groups inside
+ *   one expert)
+ */
+FP8Q_API fp8q_status fp8q_moe_dispatch(const void* x, int32_t dt, int64_t tokens, int64_t cols, int32_t top_k,
+                                       const int32_t* src, int64_t rows, int32_t fmt, int32_t pow2_scales,
+                                       int32_t dir, uint8_t* q, float* scale_inv, uint8_t* q_t, float* scale_inv_t,
+                                       void* stream);
+
+/*
+ * The experts' rows back to the tokens:
+ *   out[t] = sum_j weights[t][j] * y[row_of[t][j]]
+ * summed in FP32 in the order of j and rounded once; dropped slots add
+ * nothing.  weights NULL counts every slot once: the gradient of the
+ * dispatch.
+ *   y        device, type dt (BF16 or FP32), [rows][cols]
+ *   row_of   device int32 [tokens][top_k], top_k <= 32
+ *   weights  device float [tokens][top_k] or NULL
+ *   out      device, type dt, [tokens][cols]
+ */
+FP8Q_API fp8q_status fp8q_moe_combine(const void* y, int32_t dt, int64_t rows, int64_t cols, const int32_t* row_of,
+                                      const float* weights, int64_t tokens, int32_t top_k, void* out, void* stream);
+
+/*
+ * The gradients of fp8q_moe_combine:
+ *   d_y[row_of[t][j]] = weights[t][j] * d_out[t],  0 for padding rows;
+ *   d_weights[t][j] = sum over columns of d_out[t] * y[row_of[t][j]],  0 for
+ *   dropped slots.
+ * Types and sizes as there; weights, src and d_weights are required.
+ */
+FP8Q_API fp8q_status fp8q_moe_combine_backward(const void* d_out, const void* y, int32_t dt, int64_t rows,
+                                               int64_t cols, const int32_t* row_of, const int32_t* src,
+                                               const float* weights, int64_t tokens, int32_t top_k, void* d_y,
+                                               float* d_weights, void* stream);
 
 /*
  * NVFP4 ("混合精度与 FP8 训练" 13.2): E2M1 elements (0, 0.5, 1, 1.5, 2, 3,

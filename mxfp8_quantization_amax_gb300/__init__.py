@@ -32,6 +32,8 @@ __all__ = [
     "E2M1", "E2M3", "E3M2", "mx_quantize_fp4_fp6", "mx_scales_to_mma_layout",
     "SCALES_ROW_MAJOR", "SCALES_MMA", "mxfp8_mma_scale_bytes",
     "fp8q_matmul_blockwise", "fp8q_matmul_grouped", "fp8q_matmul_grouped_wgrad",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "fp8q_moe_route", "fp8q_moe_route_backward", "fp8q_moe_rows", "fp8q_moe_plan",
+    "fp8q_moe_dispatch", "fp8q_moe_combine", "fp8q_moe_combine_backward",
 ]
 
 E4M3 = 0
@@ -49,6 +51,8 @@ RULE_UP = 0   # MX scale rule: X = ceil(log2(amax / destmax))
 RULE_OCP = 1  # MX scale rule: X = floor(log2(amax)) - e_max (can saturate)
 BLOCK_1X128 = 1      # blockwise groups: 1x128 (rowwise copy) / 128x1 (transposed copy)
 BLOCK_128X128 = 128  # blockwise groups: 128x128 blocks
+SCORE_SOFTMAX = 0  # routing scores: a softmax over the experts
+SCORE_SIGMOID = 1  # routing scores: 1 / (1 + exp(-x)) of each expert
 
 _c = ctypes
 _P = _c.c_void_p
@@ -72,6 +76,18 @@ _SIGS = {
                                        _c.c_int64, _c.c_int32, _P, _P]),
     "fp8q_matmul_grouped_wgrad": (_c.c_int, [_P, _P, _c.c_int32, _P, _P, _c.c_int32, _P, _c.c_int32, _c.c_int64,
                                              _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _P, _P]),
+    "fp8q_moe_route": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32, _P, _c.c_int32,
+                                  _c.c_int32, _c.c_int32, _c.c_float, _P, _P, _P]),
+    "fp8q_moe_route_backward": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32, _c.c_int32,
+                                           _c.c_float, _P, _P, _P, _P]),
+    "fp8q_moe_rows": (_c.c_int64, [_c.c_int64, _c.c_int32, _c.c_int32]),
+    "fp8q_moe_plan_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int32]),
+    "fp8q_moe_plan": (_c.c_int, [_P, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int64, _P, _P, _P, _P, _c.c_size_t, _P]),
+    "fp8q_moe_dispatch": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int32, _P, _c.c_int64, _c.c_int32,
+                                     _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P]),
+    "fp8q_moe_combine": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _c.c_int64, _c.c_int32, _P, _P]),
+    "fp8q_moe_combine_backward": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _P, _c.c_int64,
+                                             _c.c_int32, _P, _P, _P]),
     "fp8q_quantize_nvfp4": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _P, _P, _P]),
     "fp8q_dequantize_per_tensor": (_c.c_int, [_P, _c.c_int64, _c.c_int64, _P, _c.c_int32, _c.c_int32, _P,
                                               _c.c_int32, _P, _P]),
@@ -764,6 +780,150 @@ def fp8q_matmul_grouped_wgrad(a_t: torch.Tensor, a_scale_inv_t: torch.Tensor, b_
                                            1 if accumulate else 0, _ptr(y), _stream()),
            "fp8q_matmul_grouped_wgrad")
     return y
+
+
+# ---------------------------------------------------------------------------
+# the expert layer: routing, row order, gather, weighted sum
+# ---------------------------------------------------------------------------
+def _matrix(t: torch.Tensor, name: str, dtypes: tuple, shape: tuple | None = None):
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes or not t.is_contiguous() or (
+            shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor of {' or '.join(map(str, dtypes))}"
+                         + (f" and shape {shape}" if shape is not None else ""))
+
+
+_VALUES = (torch.bfloat16, torch.float32)
+
+
+def fp8q_moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None,
+                   num_groups: int = 1, top_groups: int = 1, renormalize: bool = True, weight_scale: float = 1.0,
+                   out: dict | None = None) -> dict:
+    """The top_k experts of each token and their weights, from logits [tokens,
+    experts]: dict(weights float32 [tokens, top_k], ids int32 [tokens, top_k]).
+
+    Experts are chosen by score + bias among the top_groups best of num_groups
+    groups; the weights hold the scores without the bias (see the C header)."""
+    _matrix(logits, "logits", _VALUES)
+    tokens, experts = logits.shape
+    if bias is not None and (not bias.is_cuda or bias.dtype != torch.float32 or tuple(bias.shape) != (experts,)
+                             or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous float32 CUDA tensor with one value per expert")
+    o = out or {}
+    w = _result(o.get("weights"), (tokens, top_k), torch.float32, logits.device)
+    ids = _result(o.get("ids"), (tokens, top_k), torch.int32, logits.device)
+    _check(lib().fp8q_moe_route(_ptr(logits), _dt(logits), tokens, experts, top_k, score, _ptr(bias), num_groups,
+                                top_groups, 1 if renormalize else 0, weight_scale, _ptr(w), _ptr(ids), _stream()),
+           "fp8q_moe_route")
+    return {"weights": w, "ids": ids}
+
+
+def fp8q_moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor,
+                            score: int = SCORE_SOFTMAX, renormalize: bool = True, weight_scale: float = 1.0,
+                            out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of fp8q_moe_route's weights: d_logits, shaped and typed like logits."""
+    _matrix(logits, "logits", _VALUES)
+    tokens, experts = logits.shape
+    _matrix(ids, "ids", (torch.int32,))
+    _matrix(d_weights, "d_weights", (torch.float32,), tuple(ids.shape))
+    if ids.shape[0] != tokens:
+        raise ValueError("ids must hold one row per token")
+    d = _result(out, (tokens, experts), logits.dtype, logits.device)
+    _check(lib().fp8q_moe_route_backward(_ptr(logits), _dt(logits), tokens, experts, ids.shape[1], score,
+                                         1 if renormalize else 0, weight_scale, _ptr(ids), _ptr(d_weights), _ptr(d),
+                                         _stream()), "fp8q_moe_route_backward")
+    return d
+
+
+def fp8q_moe_rows(slots: int, experts: int, align: int = 1) -> int:
+    """Rows that always hold `slots` rows when each expert's are padded to a multiple of align."""
+    return int(lib().fp8q_moe_rows(slots, experts, align))
+
+
+def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, align: int = 1, out: dict | None = None) -> dict:
+    """The experts' row order of ids [tokens, top_k]: dict(offsets int64
+    [experts + 1], row_of int32 [tokens, top_k], src int32 [rows]), each
+    expert's rows padded to a multiple of align."""
+    _matrix(ids, "ids", (torch.int32,))
+    L = lib()
+    slots = ids.numel()
+    rows = L.fp8q_moe_rows(slots, num_experts, align)
+    if rows < 0:
+        raise ValueError("num_experts and align must be at least 1")
+    o = out or {}
+    offsets = _result(o.get("offsets"), (num_experts + 1,), torch.int64, ids.device)
+    row_of = _result(o.get("row_of"), tuple(ids.shape), torch.int32, ids.device)
+    src = _result(o.get("src"), (rows,), torch.int32, ids.device)
+    need = L.fp8q_moe_plan_workspace_bytes(slots, num_experts)
+    ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    _check(L.fp8q_moe_plan(_ptr(ids), slots, num_experts, align, rows, _ptr(offsets), _ptr(row_of), _ptr(src),
+                           _ptr(ws), need, _stream()), "fp8q_moe_plan")
+    return {"offsets": offsets, "row_of": row_of, "src": src}
+
+
+def fp8q_moe_dispatch(x: torch.Tensor, plan: dict, fmt: int = E4M3, direction: int = ROW, pow2_scales: bool = False,
+                      out: dict | None = None) -> dict:
+    """x [tokens, cols] gathered in the plan's order and quantized in 1x128
+    groups: fp8q_quantize_blockwise's dict for the gathered rows (zeros where
+    the plan has padding)."""
+    _matrix(x, "x", (torch.bfloat16,))
+    tokens, cols = x.shape
+    src, row_of = plan["src"], plan["row_of"]
+    _matrix(row_of, "row_of", (torch.int32,))
+    if row_of.shape[0] != tokens:
+        raise ValueError("the plan must have one row of slots per token")
+    rows = src.numel()
+    tr, tc = (rows + 127) // 128, (cols + 127) // 128
+    o = out or {}
+    q = si = q_t = si_t = None
+    if direction & ROW:
+        q = _result(o.get("q"), (rows, cols), torch.uint8, x.device)
+        si = _result(o.get("scale_inv"), (rows, tc), torch.float32, x.device)
+    if direction & COL:
+        q_t = _result(o.get("q_t"), (cols, rows), torch.uint8, x.device)
+        si_t = _result(o.get("scale_inv_t"), (cols, tr), torch.float32, x.device)
+    _check(lib().fp8q_moe_dispatch(_ptr(x), 0, tokens, cols, max(row_of.shape[1], 1), _ptr(src), rows, fmt,
+                                   1 if pow2_scales else 0, direction, _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t),
+                                   _stream()), "fp8q_moe_dispatch")
+    return {"q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
+
+
+def fp8q_moe_combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[row_of[t, j]] for y [rows, cols] in the
+    plan's order; without weights, the gradient of the dispatch."""
+    _matrix(y, "y", _VALUES)
+    row_of = plan["row_of"]
+    _matrix(row_of, "row_of", (torch.int32,))
+    if weights is not None:
+        _matrix(weights, "weights", (torch.float32,), tuple(row_of.shape))
+    rows, cols = y.shape
+    tokens, top_k = row_of.shape
+    o = _result(out, (tokens, cols), y.dtype, y.device)
+    _check(lib().fp8q_moe_combine(_ptr(y), _dt(y), rows, cols, _ptr(row_of), _ptr(weights), tokens, top_k, _ptr(o),
+                                  _stream()), "fp8q_moe_combine")
+    return o
+
+
+def fp8q_moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, plan: dict, weights: torch.Tensor,
+                              out: dict | None = None) -> dict:
+    """The gradients of fp8q_moe_combine: dict(d_y like y, zero in padding rows;
+    d_weights float32 [tokens, top_k])."""
+    _matrix(y, "y", _VALUES)
+    row_of, src = plan["row_of"], plan["src"]
+    _matrix(row_of, "row_of", (torch.int32,))
+    tokens, top_k = row_of.shape
+    rows, cols = y.shape
+    _matrix(d_out, "d_out", (y.dtype,), (tokens, cols))
+    _matrix(weights, "weights", (torch.float32,), (tokens, top_k))
+    if src.numel() != rows:
+        raise ValueError("y must have the plan's rows")
+    o = out or {}
+    d_y = _result(o.get("d_y"), (rows, cols), y.dtype, y.device)
+    d_w = _result(o.get("d_weights"), (tokens, top_k), torch.float32, y.device)
+    _check(lib().fp8q_moe_combine_backward(_ptr(d_out), _ptr(y), _dt(y), rows, cols, _ptr(row_of), _ptr(src),
+                                           _ptr(weights), tokens, top_k, _ptr(d_y), _ptr(d_w), _stream()),
+           "fp8q_moe_combine_backward")
+    return {"d_y": d_y, "d_weights": d_w}
 
 
 # ---------------------------------------------------------------------------

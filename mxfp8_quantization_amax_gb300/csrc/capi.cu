@@ -38,6 +38,8 @@ fp8q_status fail(fp8q_status st, const char* fmt, ...) {
   return st;
 }
 
+void clear_error() { g_err[0] = 0; }
+
 fp8q_status cuda_fail(cudaError_t e, const char* what) {
   return fail(FP8Q_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -444,8 +446,9 @@ fp8q_status fp8q_quantize_blockwise(const void* x, int32_t dt, int64_t rows, int
   if (dir != MXFP8_ROW && dir != MXFP8_COL && dir != MXFP8_BOTH)
     return fail(FP8Q_ERR_INVALID_ARG, "dir must be MXFP8_ROW, MXFP8_COL or MXFP8_BOTH");
   if (rows < 0 || cols < 0) return fail(FP8Q_ERR_INVALID_ARG, "rows and cols must be >= 0");
-  if (rows % 16 != 0 || cols % 16 != 0)
-    return fail(FP8Q_ERR_UNSUPPORTED, "blockwise quantization needs rows %% 16 == 0 and cols %% 16 == 0");
+  if (cols % 16 != 0) return fail(FP8Q_ERR_UNSUPPORTED, "blockwise quantization needs cols %% 16 == 0");
+  if ((dir & MXFP8_COL) && rows % 16 != 0)
+    return fail(FP8Q_ERR_UNSUPPORTED, "the transposed blockwise copy needs rows %% 16 == 0");
   if (rows > INT32_MAX / 2 || cols > INT32_MAX / 2) return fail(FP8Q_ERR_UNSUPPORTED, "rows or cols too large");
   if (rows * cols == 0) return FP8Q_OK;
   if (!x || !aligned(x, 16)) return fail(FP8Q_ERR_INVALID_ARG, "x must be a 16-byte aligned device pointer");

@@ -1,0 +1,321 @@
+// dispatch.cu -- the order of the experts' rows, and the rows gathered in that
+// order and quantized.
+//
+// Slot t * top_k + j is token t's j-th expert.  The plan is a stable counting
+// sort of the slots by expert, each expert's segment padded to a multiple of
+// `align` rows: offsets[e] (segment starts), row_of[slot], src[row] (-1 for
+// padding).  A slot whose id is no expert's is dropped (row_of -1).
+//
+// Each CTA takes a contiguous piece of the slots, each warp a contiguous part
+// of the piece.  A first pass counts the piece's slots per expert; the second
+// adds the counts of the pieces before it and the padded totals of the
+// experts before each, and places the slots, lanes of one expert in lane
+// order.  Only integers are counted, so the result does not depend on timing.
+#include "blockwise.cuh"
+#include "fp8q_device.cuh"
+#include "internal.h"
+
+namespace fp8q {
+
+constexpr int kPlanMaxExperts = 1024;
+constexpr int kPlanThreads = 256;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanPiece = 4096;       // slots of one CTA
+constexpr int kPlanMaxPieces = 1024;   // beyond, pieces grow
+
+struct PlanParams {
+  const int* ids;
+  int64_t slots;
+  int64_t piece;
+  int pieces;
+  int experts, align;
+  int64_t rows;
+  int64_t* offsets;
+  int* row_of;
+  int* src;
+  int* counts;  // [pieces][experts]
+};
+
+__device__ __forceinline__ int plan_id(const PlanParams& p, int64_t slot, int64_t end) {
+  if (slot >= end) return -1;
+  const int id = __ldg(p.ids + slot);
+  return id >= 0 && id < p.experts ? id : -1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(PlanParams p) {
+  __shared__ int hist[kPlanMaxExperts];
+  pdl_wait();
+  for (int e = threadIdx.x; e < p.experts; e += kPlanThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * p.piece, hi = min(lo + p.piece, p.slots);
+  for (int64_t s = lo + threadIdx.x; s < hi; s += kPlanThreads) {
+    const int id = plan_id(p, s, hi);
+    if (id >= 0) atomicAdd(&hist[id], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.experts; e += kPlanThreads) p.counts[(int64_t)blockIdx.x * p.experts + e] = hist[e];
+  pdl_launch_dependents();
+}
+
+// Exclusive sum over the CTA of one value per thread; *all gets the total.
+__device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* sh, int64_t* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; w++) {
+    if (w < warp) before += sh[w];
+    total += sh[w];
+  }
+  __syncthreads();
+  *all = total;
+  return before + incl - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanParams p) {
+  extern __shared__ int next[];  // [warps][experts]: the next row of each expert for each warp
+  __shared__ int64_t sh[kPlanWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  for (int i = tid; i < kPlanWarps * p.experts; i += kPlanThreads) next[i] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * p.piece, hi = min(lo + p.piece, p.slots);
+  const int64_t part = (p.piece / kPlanWarps + 31) / 32 * 32;
+  const int64_t w0 = min(lo + warp * part, hi), w1 = min(w0 + part, hi);
+  int* mine = next + warp * p.experts;
+  for (int64_t s = w0 + lane; s < w1; s += 32) {
+    const int id = plan_id(p, s, w1);
+    if (id >= 0) atomicAdd(&mine[id], 1);
+  }
+  __syncthreads();
+  // experts in chunks of one per thread: padded totals of those before
+  int64_t base = 0;
+  for (int e0 = 0; e0 < p.experts; e0 += kPlanThreads) {
+    const int e = e0 + tid;
+    int64_t total = 0, before = 0;
+    if (e < p.experts) {
+      if (p.pieces == 1) {
+        for (int w = 0; w < kPlanWarps; w++) total += next[w * p.experts + e];
+      } else {
+        for (int b = 0; b < p.pieces; b++) {
+          const int c = __ldg(p.counts + (int64_t)b * p.experts + e);
+          if (b < (int)blockIdx.x) before += c;
+          total += c;
+        }
+      }
+    }
+    const int64_t padded = (total + p.align - 1) / p.align * p.align;
+    int64_t all;
+    const int64_t start = base + plan_scan(padded, sh, &all);
+    base += all;
+    if (e < p.experts) {
+      int64_t at = start + before;
+      for (int w = 0; w < kPlanWarps; w++) {
+        const int c = next[w * p.experts + e];
+        next[w * p.experts + e] = (int)at;
+        at += c;
+      }
+      if (blockIdx.x == 0) p.offsets[e] = start;
+      if (e % p.pieces == (int)blockIdx.x)  // the segment's padding
+        for (int64_t r = start + total; r < start + padded; r++) p.src[r] = -1;
+    }
+  }
+  if (blockIdx.x == 0 && tid == 0) p.offsets[p.experts] = base;
+  for (int64_t r = base + blockIdx.x * kPlanThreads + tid; r < p.rows; r += (int64_t)p.pieces * kPlanThreads) p.src[r] = -1;
+  __syncthreads();
+  for (int64_t s0 = w0; s0 < w1; s0 += 32) {
+    const int64_t s = s0 + lane;
+    const int id = plan_id(p, s, w1);
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    int row = -1;
+    if (id >= 0) {
+      row = mine[id] + rank;
+      p.src[row] = (int)s;
+    }
+    __syncwarp();
+    if (id >= 0 && rank == 0) mine[id] += __popc(same);
+    __syncwarp();
+    if (s < w1) p.row_of[s] = row;
+  }
+  pdl_launch_dependents();
+}
+
+// ---------------------------------------------------------------------------
+// gather and quantize
+// ---------------------------------------------------------------------------
+struct DispatchParams {
+  BwParams bw;  // of the gathered matrix
+  const uint16_t* x;
+  const int* src;
+  int64_t slots;
+  int top_k;
+};
+
+// Token of a row of the gathered matrix; -1 for padding.
+__device__ __forceinline__ int64_t dispatch_token(const DispatchParams& p, int64_t row) {
+  const int s = row < p.bw.rows ? __ldg(p.src + row) : -1;
+  return s >= 0 && s < p.slots ? s / p.top_k : -1;
+}
+
+// One CTA, one tile of 128 gathered rows x 128 columns, in the layout the
+// blockwise passes read.  Row tiles are the fast grid axis: the CTAs running
+// at a time share a few column stripes of x, whose rows (each read top_k
+// times) stay in L2.
+template <int FMT, int DIR>
+__global__ void __launch_bounds__(kBwConsumers) dispatch_kernel(DispatchParams p) {
+  __shared__ __align__(1024) unsigned char tile[kBwStageBytes];
+  __shared__ uint32_t sh_amax[4 * kBwTile];
+  const int tid = threadIdx.x;
+  const int64_t r0 = (int64_t)blockIdx.x * kBwTile, c0 = (int64_t)blockIdx.y * kBwTile;
+  pdl_wait();
+  const int part = tid & 15;  // 16 lanes fetch one row's 256 bytes
+#pragma unroll
+  for (int i = 0; i < kBwTile / 16; i++) {
+    const int r = i * 16 + (tid >> 4);
+    const int64_t t = dispatch_token(p, r0 + r);
+    const int64_t c = c0 + part * 8;
+    const bool there = t >= 0 && c < p.bw.cols;
+    const uint16_t* from = p.x + (there ? t * p.bw.cols + c : 0);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + bw_off(r, part * 8))), "l"(from),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  if constexpr (DIR & MXFP8_ROW) bw_rows<FMT, 1>(p.bw, tile, r0, c0, 1.0f, tid);
+  if constexpr (DIR & MXFP8_COL) bw_cols<FMT, 1>(p.bw, tile, r0, c0, 1.0f, tid, sh_amax);
+  pdl_launch_dependents();
+}
+
+template <int FMT>
+static fp8q_status launch_dispatch_f(const DispatchParams& p, int dir, cudaStream_t s) {
+  const dim3 grid((unsigned)p.bw.tiles_r, (unsigned)p.bw.tiles_c);
+  const auto kernel = dir == MXFP8_ROW   ? dispatch_kernel<FMT, MXFP8_ROW>
+                      : dir == MXFP8_COL ? dispatch_kernel<FMT, MXFP8_COL>
+                                         : dispatch_kernel<FMT, MXFP8_BOTH>;
+  const cudaError_t e = launch_kernel(kernel, grid, dim3(kBwConsumers), 0, s, p);
+  if (e != cudaSuccess) return cuda_fail(e, "dispatch kernel launch");
+  return check_launch("dispatch kernel");
+}
+
+static void plan_pieces(int64_t slots, int64_t* piece, int* pieces) {
+  *piece = kPlanPiece;
+  if (slots > (int64_t)kPlanPiece * kPlanMaxPieces) *piece = (slots + kPlanMaxPieces - 1) / kPlanMaxPieces;
+  const int64_t n = (slots + *piece - 1) / *piece;
+  *pieces = n > 0 ? (int)n : 1;
+}
+
+static fp8q_status check_plan(int64_t slots, int32_t experts, int32_t align) {
+  if (slots < 0) return fail(FP8Q_ERR_INVALID_ARG, "slots must be >= 0");
+  if (experts < 1) return fail(FP8Q_ERR_INVALID_ARG, "experts must be >= 1");
+  if (experts > kPlanMaxExperts) return fail(FP8Q_ERR_UNSUPPORTED, "a plan serves at most %d experts", kPlanMaxExperts);
+  if (align < 1 || align > 4096) return fail(FP8Q_ERR_INVALID_ARG, "align must be in [1, 4096]");
+  if (slots > INT32_MAX - (int64_t)experts * align) return fail(FP8Q_ERR_UNSUPPORTED, "too many slots");
+  return FP8Q_OK;
+}
+
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" int64_t fp8q_moe_rows(int64_t slots, int32_t experts, int32_t align) {
+  if (slots < 0 || experts < 1 || align < 1) return -1;
+  const int64_t used = slots < experts ? slots : experts;
+  return (slots + used * (align - 1)) / align * align;
+}
+
+extern "C" size_t fp8q_moe_plan_workspace_bytes(int64_t slots, int32_t experts) {
+  if (slots < 0 || experts < 1) return 0;
+  int64_t piece;
+  int pieces;
+  plan_pieces(slots, &piece, &pieces);
+  return (size_t)pieces * experts * sizeof(int);
+}
+
+extern "C" fp8q_status fp8q_moe_plan(const int32_t* ids, int64_t slots, int32_t experts, int32_t align, int64_t rows,
+                                     int64_t* offsets, int32_t* row_of, int32_t* src, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  clear_error();
+  const fp8q_status r = check_plan(slots, experts, align);
+  if (r != FP8Q_OK) return r;
+  if (rows < fp8q_moe_rows(slots, experts, align))
+    return fail(FP8Q_ERR_INVALID_ARG, "rows (%lld) is below fp8q_moe_rows() = %lld", (long long)rows,
+                (long long)fp8q_moe_rows(slots, experts, align));
+  if (rows > INT32_MAX) return fail(FP8Q_ERR_UNSUPPORTED, "too many rows");
+  if (!offsets || ((uintptr_t)offsets & 7)) return fail(FP8Q_ERR_INVALID_ARG, "offsets must be an 8-byte aligned device pointer");
+  if (slots > 0 && (!ids || !row_of || ((uintptr_t)ids & 3) || ((uintptr_t)row_of & 3)))
+    return fail(FP8Q_ERR_INVALID_ARG, "ids and row_of must be 4-byte aligned device pointers");
+  if (rows > 0 && (!src || ((uintptr_t)src & 3))) return fail(FP8Q_ERR_INVALID_ARG, "src must be a 4-byte aligned device pointer");
+  const size_t need = fp8q_moe_plan_workspace_bytes(slots, experts);
+  if (!workspace || ((uintptr_t)workspace & 3) || workspace_bytes < need)
+    return fail(FP8Q_ERR_INVALID_ARG, "workspace must be a 4-byte aligned device pointer to %zu bytes", need);
+  PlanParams p{};
+  p.ids = ids;
+  p.slots = slots;
+  plan_pieces(slots, &p.piece, &p.pieces);
+  p.experts = experts;
+  p.align = align;
+  p.rows = rows;
+  p.offsets = offsets;
+  p.row_of = row_of;
+  p.src = src;
+  p.counts = (int*)workspace;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (p.pieces > 1) {
+    const cudaError_t e = launch_kernel(plan_count_kernel, dim3(p.pieces), dim3(kPlanThreads), 0, s, p);
+    if (e != cudaSuccess) return cuda_fail(e, "plan kernel launch");
+  }
+  const cudaError_t e = launch_kernel(plan_place_kernel, dim3(p.pieces), dim3(kPlanThreads),
+                                      (size_t)kPlanWarps * experts * sizeof(int), s, p);
+  if (e != cudaSuccess) return cuda_fail(e, "plan kernel launch");
+  return check_launch("plan kernel");
+}
+
+extern "C" fp8q_status fp8q_moe_dispatch(const void* x, int32_t dt, int64_t tokens, int64_t cols, int32_t top_k,
+                                         const int32_t* src, int64_t rows, int32_t fmt, int32_t pow2_scales,
+                                         int32_t dir, uint8_t* q, float* scale_inv, uint8_t* q_t, float* scale_inv_t,
+                                         void* stream) {
+  clear_error();
+  if (dt != FP8Q_IN_BF16 && dt != FP8Q_IN_FP32) return fail(FP8Q_ERR_INVALID_ARG, "dt must be FP8Q_IN_BF16 or FP8Q_IN_FP32");
+  if (dt != FP8Q_IN_BF16) return fail(FP8Q_ERR_UNSUPPORTED, "dispatch takes BF16 input");
+  if (fmt != FP8Q_E4M3 && fmt != FP8Q_E5M2) return fail(FP8Q_ERR_INVALID_ARG, "fmt must be FP8Q_E4M3 or FP8Q_E5M2");
+  if (dir != MXFP8_ROW && dir != MXFP8_COL && dir != MXFP8_BOTH)
+    return fail(FP8Q_ERR_INVALID_ARG, "dir must be MXFP8_ROW, MXFP8_COL or MXFP8_BOTH");
+  if (tokens < 0 || cols < 0 || rows < 0) return fail(FP8Q_ERR_INVALID_ARG, "tokens, cols and rows must be >= 0");
+  if (top_k < 1) return fail(FP8Q_ERR_INVALID_ARG, "top_k must be >= 1");
+  if (cols % 16 != 0) return fail(FP8Q_ERR_UNSUPPORTED, "dispatch needs cols %% 16 == 0");
+  if ((dir & MXFP8_COL) && rows % 16 != 0) return fail(FP8Q_ERR_UNSUPPORTED, "the transposed copy needs rows %% 16 == 0");
+  if (rows > INT32_MAX || tokens > INT32_MAX / top_k || cols > 65535 * (int64_t)kBwTile)
+    return fail(FP8Q_ERR_UNSUPPORTED, "tokens, cols or rows too large");
+  if (rows * cols == 0) return FP8Q_OK;
+  if ((tokens > 0 && !x) || ((uintptr_t)x & 15)) return fail(FP8Q_ERR_INVALID_ARG, "x must be a 16-byte aligned device pointer");
+  if (!src || ((uintptr_t)src & 3)) return fail(FP8Q_ERR_INVALID_ARG, "src must be a 4-byte aligned device pointer");
+  if ((dir & MXFP8_ROW) && (!q || !scale_inv || ((uintptr_t)q & 15) || ((uintptr_t)scale_inv & 3)))
+    return fail(FP8Q_ERR_INVALID_ARG, "q (16-byte aligned) and scale_inv are required for the rowwise copy");
+  if ((dir & MXFP8_COL) && (!q_t || !scale_inv_t || ((uintptr_t)q_t & 15) || ((uintptr_t)scale_inv_t & 3)))
+    return fail(FP8Q_ERR_INVALID_ARG, "q_t (16-byte aligned) and scale_inv_t are required for the transposed copy");
+  DispatchParams p{};
+  p.bw.rows = rows;
+  p.bw.cols = cols;
+  p.bw.tiles_r = (rows + kBwTile - 1) / kBwTile;
+  p.bw.tiles_c = (cols + kBwTile - 1) / kBwTile;
+  p.bw.pow2 = pow2_scales ? 1 : 0;
+  p.bw.q = q;
+  p.bw.s = scale_inv;
+  p.bw.q_t = q_t;
+  p.bw.s_t = scale_inv_t;
+  p.x = (const uint16_t*)x;
+  p.src = src;
+  p.slots = tokens * top_k;
+  p.top_k = top_k;
+  return fmt == FP8Q_E4M3 ? launch_dispatch_f<kE4M3>(p, dir, (cudaStream_t)stream)
+                          : launch_dispatch_f<kE5M2>(p, dir, (cudaStream_t)stream);
+}

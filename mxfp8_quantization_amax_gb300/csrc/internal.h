@@ -14,6 +14,8 @@ namespace fp8q {
 
 // Records `msg` as this thread's last error and returns `st`.
 fp8q_status fail(fp8q_status st, const char* fmt, ...);
+// Forgets this thread's last error (every entry point begins with it).
+void clear_error();
 // Maps a CUDA error to FP8Q_ERR_CUDA with a message naming `what`.
 fp8q_status cuda_fail(cudaError_t e, const char* what);
 // Checks cudaGetLastError() after launches.

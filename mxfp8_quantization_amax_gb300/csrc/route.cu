@@ -1,0 +1,381 @@
+// route.cu -- routing of tokens to experts, and its gradient.
+//
+// A token's logits x[e] give scores s = softmax(x) or 1 / (1 + exp(-x)) and
+// keys to choose by: s[e] + bias[e], or, with neither bias nor groups, x[e]
+// itself (the same order without the rounding of s).  With groups, a group
+// of E / groups consecutive experts is worth the sum of its two best keys
+// and only the best groups stay.  The top_k best keys are chosen, equal keys
+// from the lowest index, and weigh
+//   w_j = c * s_j / sum_i s_i    (renormalised)    or    c * s_j.
+// A logit of -inf or NaN is never chosen (id -1, weight 0 where too few are
+// left); a NaN, under softmax also +inf, makes the token's weights NaN.
+//
+// Gradient, with d_j the gradient of w_j and g_j that of s_j:
+//   renormalised  g_j = c * (d_j - sum_i d_i s_i / S) / S,  S = sum_i s_i
+//   else          g_j = c * d_j
+//   sigmoid       dx_j = g_j s_j (1 - s_j),  0 for experts not chosen
+//   softmax       dx_e = p_e (g_e - sum_j g_j p_j); renormalised, the last
+//                 sum is zero and p_j / S a softmax over the chosen alone.
+// The bias and the choice have no gradient.
+//
+// One warp takes one token, expert e = lane + 32 i in register i.  A choice
+// is a maximum over the registers, one warp-wide integer maximum of the
+// order-preserving bits and one minimum of the indices that have it.
+#include "fp8q_device.cuh"
+#include "internal.h"
+
+namespace fp8q {
+
+constexpr int kRtWarps = 8;
+constexpr int kRtMaxExperts = 1024;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+struct RtParams {
+  const void* logits;
+  int64_t tokens;
+  int experts, top_k;
+  int renorm;
+  float weight_scale;
+  const float* bias;
+  int groups, top_groups;
+  float* weights;
+  int* ids;
+  const int* ids_in;
+  const float* d_weights;
+  void* d_logits;
+};
+
+template <int DT>
+__device__ __forceinline__ float rt_load(const void* p, int64_t i) {
+  if constexpr (DT == kBF16)
+    return __uint_as_float((uint32_t)__ldg((const uint16_t*)p + i) << 16);
+  else
+    return __ldg((const float*)p + i);
+}
+
+template <int DT>
+__device__ __forceinline__ void rt_store(void* p, int64_t i, float v) {
+  if constexpr (DT == kBF16) {
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+    ((uint16_t*)p)[i] = h;
+  } else {
+    ((float*)p)[i] = v;
+  }
+}
+
+__device__ __forceinline__ float rt_sigmoid(float x) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x))); }
+
+// Unsigned integers in the order of the floats (-0 as +0); always above 0.
+__device__ __forceinline__ uint32_t rt_order(float v) {
+  const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float rt_value(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+
+__device__ __forceinline__ float rt_warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ float rt_warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// Zeroes the keys (in shared memory, order-preserving bits) outside the best
+// groups.  32 / 2^ceil(log2 groups) lanes share a group.
+__device__ __forceinline__ void rt_keep_groups(uint32_t* keys, const RtParams& p, int lane) {
+  const int size = p.experts / p.groups;
+  int lanes = 32;
+  while (lanes * p.groups > 32) lanes >>= 1;
+  const int g = lane / lanes, j = lane % lanes;
+  uint32_t a = 0, b = 0;  // best and second best
+  if (g < p.groups) {
+    for (int i = j; i < size; i += lanes) {
+      const int e = g * size + i;
+      const uint32_t v = keys[e + (e >> 5)];
+      b = max(b, min(a, v));
+      a = max(a, v);
+    }
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    const uint32_t a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
+    b = max(min(a, a2), max(b, b2));
+    a = max(a, a2);
+  }
+  const float none = __uint_as_float(0xFF800000u);
+  const float va = a ? rt_value(a) : none, vb = b ? rt_value(b) : none;
+  const uint32_t worth = g < p.groups && j == 0 ? rt_order(size > 1 ? __fadd_rn(va, vb) : va) : 0u;
+  uint32_t mine = worth;
+  bool keep = false;
+  for (int i = 0; i < p.top_groups; i++) {
+    const uint32_t best = __reduce_max_sync(kFull, mine);
+    const unsigned who = __ballot_sync(kFull, mine == best);
+    if (lane == __ffs(who) - 1) {
+      keep = true;
+      mine = 0;
+    }
+  }
+  const unsigned kept = __ballot_sync(kFull, keep);
+  for (int e = lane; e < p.experts; e += 32)
+    if (!((kept >> (e / size * lanes)) & 1u)) keys[e + (e >> 5)] = 0;
+  __syncwarp();
+}
+
+template <int DT, bool SOFTMAX, int V>
+__global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
+  extern __shared__ uint32_t rt_smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* sh = rt_smem + warp * (V * 33);
+  pdl_wait();
+  const bool by_logit = p.bias == nullptr && p.groups == 1;
+  for (int64_t t = (int64_t)blockIdx.x * kRtWarps + warp; t < p.tokens; t += (int64_t)gridDim.x * kRtWarps) {
+    float x[V];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int e = lane + 32 * i;
+      x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : __uint_as_float(0xFF800000u);
+      nan |= x[i] != x[i] || (SOFTMAX && x[i] == __uint_as_float(0x7F800000u));
+    }
+    nan = __any_sync(kFull, nan);
+    float most = __uint_as_float(0xFF800000u), sum = 1.0f;
+    if constexpr (SOFTMAX) {
+#pragma unroll
+      for (int i = 0; i < V; i++) most = fmaxf(most, x[i]);
+      most = rt_warp_max(most);
+      if (!by_logit || !p.renorm) {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; i++) sum += x[i] == x[i] ? expf(x[i] - most) : 0.0f;
+        sum = rt_warp_sum(sum);
+      }
+    }
+    const auto score = [&](float v) { return SOFTMAX ? __fdiv_rn(expf(v - most), sum) : rt_sigmoid(v); };
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int e = lane + 32 * i;
+      float k = x[i];
+      if (!by_logit) {
+        k = score(x[i]);
+        if (p.bias != nullptr && e < p.experts) k = __fadd_rn(k, __ldg(p.bias + e));
+      }
+      const float none = __uint_as_float(0xFF800000u);
+      key[i] = x[i] > none && k > none ? rt_order(k) : 0u;
+    }
+    if (p.groups > 1) {
+#pragma unroll
+      for (int i = 0; i < V; i++) sh[lane + 33 * i] = key[i];
+      __syncwarp();
+      rt_keep_groups(sh, p, lane);
+#pragma unroll
+      for (int i = 0; i < V; i++) key[i] = sh[lane + 33 * i];
+      __syncwarp();
+    }
+    int id = -1;
+    for (int j = 0; j < p.top_k; j++) {
+      uint32_t best = 0;
+      int at = 0;
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (key[i] > best) {
+          best = key[i];
+          at = i;
+        }
+      const uint32_t top = __reduce_max_sync(kFull, best);
+      if (top == 0) break;
+      const int e = (int)__reduce_min_sync(kFull, best == top ? (unsigned)(lane + 32 * at) : 0xFFFFFFFFu);
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        if (e == lane + 32 * i) key[i] = 0;
+      if (lane == j) id = e;
+    }
+    float w = 0.0f;
+    if (id >= 0) w = score(rt_load<DT>(p.logits, t * p.experts + id));
+    if (p.renorm) {
+      const float s = rt_warp_sum(w);
+      w = s > 0.0f ? __fdiv_rn(w, s) : s == 0.0f ? 0.0f : s;
+    }
+    w = __fmul_rn(w, p.weight_scale);
+    if (nan) w = __uint_as_float(0x7FC00000u);
+    if (lane < p.top_k) {
+      p.weights[t * p.top_k + lane] = w;
+      p.ids[t * p.top_k + lane] = id;
+    }
+  }
+  pdl_launch_dependents();
+}
+
+template <int DT, bool SOFTMAX, int V>
+__global__ void __launch_bounds__(kRtWarps * 32) route_backward_kernel(RtParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  for (int64_t t = (int64_t)blockIdx.x * kRtWarps + warp; t < p.tokens; t += (int64_t)gridDim.x * kRtWarps) {
+    int id = -1;
+    float d = 0.0f, xj = __uint_as_float(0xFF800000u);
+    if (lane < p.top_k) {
+      id = __ldg(p.ids_in + t * p.top_k + lane);
+      if (id < 0 || id >= p.experts) id = -1;
+      if (id >= 0) {
+        d = __ldg(p.d_weights + t * p.top_k + lane);
+        xj = rt_load<DT>(p.logits, t * p.experts + id);
+      }
+    }
+    float s = 0.0f, g = 0.0f, dx = 0.0f, dot = 0.0f;
+    float x[V], most, sum = 1.0f;
+    if (SOFTMAX && !p.renorm) {
+      most = __uint_as_float(0xFF800000u);
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        const int e = lane + 32 * i;
+        x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : __uint_as_float(0xFF800000u);
+        most = fmaxf(most, x[i]);
+      }
+      most = rt_warp_max(most);
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        x[i] = most > __uint_as_float(0xFF800000u) ? expf(x[i] - most) : 0.0f;
+        sum += x[i];
+      }
+      sum = rt_warp_sum(sum);
+    } else {
+      most = rt_warp_max(xj);
+    }
+    if (id >= 0) s = SOFTMAX ? __fdiv_rn(expf(xj - most), sum) : rt_sigmoid(xj);
+    if (p.renorm) {
+      const float all = rt_warp_sum(s);
+      const float share = all != 0.0f ? __fdiv_rn(s, all) : 0.0f;
+      const float mean = rt_warp_sum(__fmul_rn(d, share));
+      // p_j g_j (softmax) and g_j s_j (sigmoid) are both c (d_j - mean) s_j / S
+      dx = id >= 0 ? __fmul_rn(__fmul_rn(p.weight_scale, __fsub_rn(d, mean)), share) : 0.0f;
+      if (!SOFTMAX) dx = __fmul_rn(dx, __fsub_rn(1.0f, s));
+    } else {
+      g = __fmul_rn(p.weight_scale, d);
+      if (SOFTMAX) {
+        dot = rt_warp_sum(__fmul_rn(g, s));
+        dx = __fmul_rn(s, __fsub_rn(g, dot));
+      } else {
+        dx = __fmul_rn(__fmul_rn(g, s), __fsub_rn(1.0f, s));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int e = lane + 32 * i;
+      const float rest = SOFTMAX && !p.renorm && sum > 0.0f ? -__fmul_rn(__fdiv_rn(x[i], sum), dot) : 0.0f;
+      if (e < p.experts) rt_store<DT>(p.d_logits, t * p.experts + e, rest);
+    }
+    __syncwarp();
+    if (id >= 0) rt_store<DT>(p.d_logits, t * p.experts + id, dx);
+  }
+  pdl_launch_dependents();
+}
+
+template <int DT, bool SOFTMAX, int V>
+static fp8q_status launch_route_v(const RtParams& p, bool backward, cudaStream_t s) {
+  int64_t grid = (p.tokens + kRtWarps - 1) / kRtWarps;
+  const int64_t cap = (int64_t)sm_count() * 8;
+  if (grid > cap) grid = cap;
+  const auto kernel = backward ? route_backward_kernel<DT, SOFTMAX, V> : route_kernel<DT, SOFTMAX, V>;
+  const size_t smem = !backward && p.groups > 1 ? (size_t)kRtWarps * V * 33 * 4 : 0;
+  const cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kRtWarps * 32), smem, s, p);
+  if (e != cudaSuccess) return cuda_fail(e, "route kernel launch");
+  return check_launch("route kernel");
+}
+
+template <int DT, bool SOFTMAX>
+static fp8q_status launch_route_e(const RtParams& p, bool backward, cudaStream_t s) {
+  if (p.experts <= 32) return launch_route_v<DT, SOFTMAX, 1>(p, backward, s);
+  if (p.experts <= 64) return launch_route_v<DT, SOFTMAX, 2>(p, backward, s);
+  if (p.experts <= 128) return launch_route_v<DT, SOFTMAX, 4>(p, backward, s);
+  if (p.experts <= 256) return launch_route_v<DT, SOFTMAX, 8>(p, backward, s);
+  if (p.experts <= 512) return launch_route_v<DT, SOFTMAX, 16>(p, backward, s);
+  return launch_route_v<DT, SOFTMAX, 32>(p, backward, s);
+}
+
+static fp8q_status launch_route(const RtParams& p, int dt, int score, bool backward, cudaStream_t s) {
+  if (dt == FP8Q_IN_BF16)
+    return score == FP8Q_SCORE_SOFTMAX ? launch_route_e<kBF16, true>(p, backward, s) : launch_route_e<kBF16, false>(p, backward, s);
+  return score == FP8Q_SCORE_SOFTMAX ? launch_route_e<kFP32, true>(p, backward, s) : launch_route_e<kFP32, false>(p, backward, s);
+}
+
+static fp8q_status check_route(const void* logits, int32_t dt, int64_t tokens, int32_t experts, int32_t top_k, int32_t score) {
+  if (dt != FP8Q_IN_BF16 && dt != FP8Q_IN_FP32) return fail(FP8Q_ERR_INVALID_ARG, "dt must be FP8Q_IN_BF16 or FP8Q_IN_FP32");
+  if (score != FP8Q_SCORE_SOFTMAX && score != FP8Q_SCORE_SIGMOID)
+    return fail(FP8Q_ERR_INVALID_ARG, "score must be FP8Q_SCORE_SOFTMAX or FP8Q_SCORE_SIGMOID");
+  if (tokens < 0) return fail(FP8Q_ERR_INVALID_ARG, "tokens must be >= 0");
+  if (experts < 1) return fail(FP8Q_ERR_INVALID_ARG, "experts must be >= 1");
+  if (experts > kRtMaxExperts) return fail(FP8Q_ERR_UNSUPPORTED, "routing serves at most %d experts", kRtMaxExperts);
+  if (top_k < 1 || top_k > experts) return fail(FP8Q_ERR_INVALID_ARG, "top_k must be in [1, experts]");
+  if (top_k > 32) return fail(FP8Q_ERR_UNSUPPORTED, "routing serves at most 32 experts a token");
+  if (tokens > INT64_MAX / 8 / experts) return fail(FP8Q_ERR_INVALID_ARG, "tokens * experts too large");
+  if (tokens > 0 && (!logits || ((uintptr_t)logits & (dt == FP8Q_IN_BF16 ? 1 : 3))))
+    return fail(FP8Q_ERR_INVALID_ARG, "logits must be a device pointer aligned to its type");
+  return FP8Q_OK;
+}
+
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" fp8q_status fp8q_moe_route(const void* logits, int32_t dt, int64_t tokens, int32_t experts, int32_t top_k,
+                                      int32_t score, const float* bias, int32_t num_groups, int32_t top_groups,
+                                      int32_t renormalize, float weight_scale, float* weights, int32_t* ids,
+                                      void* stream) {
+  clear_error();
+  const fp8q_status r = check_route(logits, dt, tokens, experts, top_k, score);
+  if (r != FP8Q_OK) return r;
+  if (num_groups < 1 || num_groups > 32 || experts % num_groups != 0)
+    return fail(FP8Q_ERR_INVALID_ARG, "num_groups must be in [1, 32] and divide experts");
+  if (top_groups < 1 || top_groups > num_groups) return fail(FP8Q_ERR_INVALID_ARG, "top_groups must be in [1, num_groups]");
+  if (top_k > experts / num_groups * top_groups)
+    return fail(FP8Q_ERR_INVALID_ARG, "top_k exceeds the experts of top_groups groups");
+  if ((uintptr_t)bias & 3) return fail(FP8Q_ERR_INVALID_ARG, "bias must be 4-byte aligned");
+  if (tokens == 0) return FP8Q_OK;
+  if (!weights || !ids || ((uintptr_t)weights & 3) || ((uintptr_t)ids & 3))
+    return fail(FP8Q_ERR_INVALID_ARG, "weights and ids must be 4-byte aligned device pointers");
+  RtParams p{};
+  p.logits = logits;
+  p.tokens = tokens;
+  p.experts = experts;
+  p.top_k = top_k;
+  p.renorm = renormalize ? 1 : 0;
+  p.weight_scale = weight_scale;
+  p.bias = bias;
+  p.groups = num_groups;
+  p.top_groups = top_groups;
+  p.weights = weights;
+  p.ids = ids;
+  return launch_route(p, dt, score, false, (cudaStream_t)stream);
+}
+
+extern "C" fp8q_status fp8q_moe_route_backward(const void* logits, int32_t dt, int64_t tokens, int32_t experts,
+                                               int32_t top_k, int32_t score, int32_t renormalize, float weight_scale,
+                                               const int32_t* ids, const float* d_weights, void* d_logits,
+                                               void* stream) {
+  clear_error();
+  const fp8q_status r = check_route(logits, dt, tokens, experts, top_k, score);
+  if (r != FP8Q_OK) return r;
+  if (tokens == 0) return FP8Q_OK;
+  if (!ids || !d_weights || ((uintptr_t)ids & 3) || ((uintptr_t)d_weights & 3))
+    return fail(FP8Q_ERR_INVALID_ARG, "ids and d_weights must be 4-byte aligned device pointers");
+  if (!d_logits || ((uintptr_t)d_logits & (dt == FP8Q_IN_BF16 ? 1 : 3)))
+    return fail(FP8Q_ERR_INVALID_ARG, "d_logits must be a device pointer aligned to its type");
+  RtParams p{};
+  p.logits = logits;
+  p.tokens = tokens;
+  p.experts = experts;
+  p.top_k = top_k;
+  p.renorm = renormalize ? 1 : 0;
+  p.weight_scale = weight_scale;
+  p.ids_in = ids;
+  p.d_weights = d_weights;
+  p.d_logits = d_logits;
+  p.groups = 1;
+  return launch_route(p, dt, score, true, (cudaStream_t)stream);
+}
