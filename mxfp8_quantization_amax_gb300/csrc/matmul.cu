@@ -20,9 +20,15 @@
 namespace fp8q {
 
 constexpr int kMmBlock = 128;  // values of K that share a scale
-constexpr int kMmRows = 128;   // rows of A in a tile
+constexpr int kMmRows = 128;   // rows of A of one CTA in a tile
+constexpr int kMmCols = 256;   // columns of a tile
 constexpr int kMmEpiWarps = 8;
-constexpr int kMmThreads = (kMmEpiWarps + 2) * 32;
+constexpr int kMmThreads = (kMmEpiWarps + 4) * 32;
+// Registers a thread: 168 at launch, moved from the warpgroup of the loads
+// and the tensor core to the two that hold the sums (128 of them each).
+constexpr int kMmRegsLaunch = 168, kMmRegsEpi = 216, kMmRegsLoad = 72;
+static_assert(kMmEpiWarps * 32 * kMmRegsEpi + 128 * kMmRegsLoad <= kMmThreads * kMmRegsLaunch, "register split");
+constexpr int kMmScaleSlots = 3;  // ring of scales, four blocks of K each
 constexpr uint64_t kMmDrainNs = 2000000000ull;
 
 __device__ unsigned int g_mm_error;
@@ -44,13 +50,15 @@ struct MmParams {
   void* out;         // [m][n]; K groups: [groups][m][n]
 };
 
-template <int BN>
+// A tile is 128 * CG rows x 256 columns, CG the CTAs that work on it: one, or a
+// pair, whose CTAs each hold 128 rows of A and half of B's.
+template <int CG>
 struct MmShape {
+  static constexpr int kTileRows = kMmRows * CG;
   static constexpr int kABytes = kMmRows * kMmBlock;
-  static constexpr int kBBytes = BN * kMmBlock;
+  static constexpr int kBBytes = kMmCols / CG * kMmBlock;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = BN == 256 ? 4 : 6;
-  static constexpr int kCols = BN / 2;  // columns of one epilogue warp
+  static constexpr int kStages = 196608 / kStageBytes;  // 192 KB
 };
 
 struct MmTile {
@@ -69,8 +77,9 @@ __device__ __forceinline__ int64_t mm_clamped(const int64_t* off, int g, int64_t
 // Tile t of the grid-wide list.  Inside a group, bands of 16 row tiles are
 // walked row tile first, so the CTAs of one wave read few distinct tiles of
 // A and of B and find them in L2.
-template <int BN, int MODE>
+template <int CG, int MODE>
 __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const unsigned* first, uint32_t t) {
+  constexpr int ROWS = MmShape<CG>::kTileRows;
   MmTile r;
   r.g = 0;
   int64_t lo = 0, hi = p.m;
@@ -87,7 +96,7 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const unsigned* fir
     lo = mm_clamped(p.off, a, p.m);
     hi = mm_clamped(p.off, a + 1, p.m);
   } else {
-    mt_all = (uint32_t)((p.m + kMmRows - 1) / kMmRows);
+    mt_all = (uint32_t)((p.m + ROWS - 1) / ROWS);
     if constexpr (MODE == kMmKGroups) {
       const uint32_t per = mt_all * p.tiles_n;
       r.g = (int)(t / per);
@@ -96,9 +105,9 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const unsigned* fir
   }
   const uint32_t per_band = 16u * p.tiles_n, band = t / per_band;
   const uint32_t in_band = t - band * per_band, rest = mt_all - band * 16u, height = rest < 16u ? rest : 16u;
-  r.row0 = lo + (int64_t)(band * 16u + in_band % height) * kMmRows;
+  r.row0 = lo + (int64_t)(band * 16u + in_band % height) * ROWS;
   r.row_end = hi;
-  r.n0 = (int64_t)(in_band / height) * BN;
+  r.n0 = (int64_t)(in_band / height) * kMmCols;
   r.k0 = 0;
   int64_t k1 = p.k;
   if constexpr (MODE == kMmKGroups) {
@@ -112,6 +121,7 @@ __device__ __forceinline__ MmTile mm_tile(const MmParams& p, const unsigned* fir
 }
 
 // first[g] = row tiles of the groups before g, first[groups] = all of them.
+template <int ROWS>
 __device__ __forceinline__ void mm_scan_groups(const MmParams& p, unsigned* first, unsigned* sums) {
   const int tid = threadIdx.x, per = (p.groups + 255) / 256;
   const int g0 = min(tid * per, p.groups), g1 = min(g0 + per, p.groups);
@@ -119,7 +129,7 @@ __device__ __forceinline__ void mm_scan_groups(const MmParams& p, unsigned* firs
   if (tid < 256) {
     for (int g = g0; g < g1; g++) {
       const int64_t n = mm_clamped(p.off, g + 1, p.m) - mm_clamped(p.off, g, p.m);
-      mine += n > 0 ? (uint64_t)((n + kMmRows - 1) / kMmRows) : 0;
+      mine += n > 0 ? (uint64_t)((n + ROWS - 1) / ROWS) : 0;
     }
     sums[tid] = (unsigned)(mine < 0x7FFFFFu ? mine : 0x7FFFFFu);
   }
@@ -147,7 +157,7 @@ __device__ __forceinline__ void mm_scan_groups(const MmParams& p, unsigned* firs
     for (int g = g0; g < g1; g++) {
       first[g] = at;
       const int64_t n = mm_clamped(p.off, g + 1, p.m) - mm_clamped(p.off, g, p.m);
-      at += n > 0 ? (unsigned)((n + kMmRows - 1) / kMmRows) : 0;
+      at += n > 0 ? (unsigned)((n + ROWS - 1) / ROWS) : 0;
     }
   }
   __syncthreads();
@@ -215,18 +225,22 @@ __device__ __forceinline__ void mm_store_row(const MmParams& p, int64_t row, int
   }
 }
 
-// BN: rows of B in a tile.  COLSCALE: B has a scale for each of its rows
+// COLSCALE: B has a scale for each of its rows
 // (1x128 groups), else one for each 128 of them.
-template <int BN, bool COLSCALE, bool F32, int MODE>
+template <int CG, bool COLSCALE, bool F32, int MODE>
 __global__ void __launch_bounds__(kMmThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, MmParams p) {
-  using S = MmShape<BN>;
-  constexpr int COLS = S::kCols;
+  using S = MmShape<CG>;
+  constexpr int COLS = kMmCols / 2;  // of one warp of sums
+  // scales of one block of K: the rows', and the columns' or the halves' two
+  constexpr int NS = kMmRows + (COLSCALE ? kMmCols : 32);
+  constexpr int SW = COLSCALE ? 2 : 1;  // warps that load them
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t full[S::kStages], empty[S::kStages], done[2], taken[2], drained;
+  __shared__ uint64_t sfull[kMmScaleSlots], sempty[kMmScaleSlots];
   __shared__ uint32_t tmem_base;
-  __shared__ unsigned sums[256];
-  __shared__ __align__(16) float sbuf[COLSCALE ? kMmEpiWarps : 1][2][COLSCALE ? COLS : 4];
+  __shared__ unsigned sums[MODE == kMmRowGroups ? 256 : 1];
+  __shared__ __align__(16) float scale[kMmScaleSlots][4][NS];
   __shared__ volatile int abort_flag;
   unsigned char* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned* first = (unsigned*)(stages + S::kStages * S::kStageBytes);
@@ -239,14 +253,18 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(&done[b], 1);
-      mbar_init(&taken[b], kMmEpiWarps);
+      mbar_init(&taken[b], kMmEpiWarps * CG);
     }
     mbar_init(&drained, 1);
+    for (int i = 0; i < kMmScaleSlots; i++) {
+      mbar_init(&sfull[i], SW);
+      mbar_init(&sempty[i], kMmEpiWarps);
+    }
     abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == kMmEpiWarps) {
-    tmem_alloc(&tmem_base, 2 * BN);
+    tmem_alloc<CG>(&tmem_base, 512);
     tc_fence_before();
     if (lane == 0) {
       prefetch_tensormap(&map_a);
@@ -255,52 +273,71 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   }
   pdl_wait();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the leader's barriers, before the other CTA uses them
   tc_fence_after();
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const uint32_t tile0 = blockIdx.x / CG, tile_step = gridDim.x / CG;
   const uint32_t tmem = tmem_base;
-  const uint64_t budget = g_mm_wait_budget_ns;
+  const uint64_t budget_ns = g_mm_wait_budget_ns;
+  const uint32_t budget = (uint32_t)(budget_ns < 4000000000000ull ? budget_ns / 1000 : 4000000000u);
 
   uint32_t tiles;
   if constexpr (MODE == kMmRowGroups) {
-    mm_scan_groups(p, first, sums);
+    mm_scan_groups<S::kTileRows>(p, first, sums);
     tiles = first[p.groups] * (uint32_t)p.tiles_n;
   } else {
-    tiles = (uint32_t)((p.m + kMmRows - 1) / kMmRows) * (uint32_t)p.tiles_n * (uint32_t)p.groups;
+    tiles = (uint32_t)((p.m + S::kTileRows - 1) / S::kTileRows) * (uint32_t)p.tiles_n * (uint32_t)p.groups;
   }
 
+  if (warp >= kMmEpiWarps) {
+  regs_dec<kMmRegsLoad>();
   if (warp == kMmEpiWarps) {
     // ---------------- loads: one thread ----------------
-    if (lane == 0) {
-      uint32_t it = 0;  // blocks of K issued
-      for (uint32_t t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
-        const MmTile w = mm_tile<BN, MODE>(p, first, t);
-        const int brow = (int)(w.n0 + (MODE == kMmRowGroups ? (int64_t)w.g * p.n : 0));
-        for (int kb = 0; kb < w.nkb && !abort_flag; kb++, it++) {
+    uint32_t it = 0;  // blocks of K issued
+    if (elect_one()) {
+      for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
+        const MmTile w = mm_tile<CG, MODE>(p, first, t);
+        const int arow = (int)w.row0 + rank * kMmRows;
+        const int brow = (int)(w.n0 + (MODE == kMmRowGroups ? (int64_t)w.g * p.n : 0)) + rank * (kMmCols / CG);
+        int at = (int)w.k0;
+        for (int kb = 0; kb < w.nkb; kb++, it++, at += kMmBlock) {
           const uint32_t s = it % S::kStages, round = it / S::kStages;
-          if (round > 0 && !mbar_wait(&empty[s], (round - 1) & 1u, budget)) {
+          if (round > 0 && !mbar_wait_counted(&empty[s], (round - 1) & 1u, budget)) {
             atomicOr(&g_mm_error, 1u);
             abort_flag = 1;
             break;
           }
           unsigned char* st = stages + s * S::kStageBytes;
-          mbar_arrive_expect_tx(&full[s], S::kStageBytes);
-          tma_load_2d(st, &map_a, (int)(w.k0 + (int64_t)kb * kMmBlock), (int)w.row0, &full[s]);
-          tma_load_2d(st + S::kABytes, &map_b, (int)(w.k0 + (int64_t)kb * kMmBlock), brow, &full[s]);
+          if constexpr (CG == 1) {
+            mbar_arrive_expect_tx(&full[s], S::kStageBytes);
+            tma_load_2d(st, &map_a, at, arow, &full[s]);
+            tma_load_2d(st + S::kABytes, &map_b, at, brow, &full[s]);
+          } else {
+            // the leader's barrier counts the bytes of both CTAs
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStageBytes);
+            const uint32_t bar = cluster_addr(&full[s], 0);
+            tma_load_2d_pair(st, &map_a, at, arow, bar);
+            tma_load_2d_pair(st + S::kABytes, &map_b, at, brow, bar);
+          }
         }
       }
-      pdl_launch_dependents();
-      // every issued copy lands before the CTA can exit (fixed 2 s bound)
-      for (uint32_t j = it > S::kStages ? it - S::kStages : 0; j < it; j++)
-        mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
+      // every issued copy lands before the CTA (the pair) can exit (fixed 2 s bound)
+      if (rank == 0)
+        for (uint32_t j = it > S::kStages ? it - S::kStages : 0; j < it; j++)
+          mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
     }
+    __syncwarp();
+    pdl_launch_dependents();
   } else if (warp == kMmEpiWarps + 1) {
-    // ---------------- tensor core: one thread ----------------
-    if (lane == 0) {
+    // ---------------- tensor core: one thread of the leader ----------------
+    if (rank == 0 && elect_one()) {
       uint32_t it = 0;
-      for (uint32_t t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
-        const MmTile w = mm_tile<BN, MODE>(p, first, t);
-        for (int kb = 0; kb < w.nkb && !abort_flag; kb++, it++) {
+      for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
+        const MmTile w = mm_tile<CG, MODE>(p, first, t);
+        for (int kb = 0; kb < w.nkb; kb++, it++) {
           const uint32_t s = it % S::kStages, round = it / S::kStages, b = it & 1u, use = it >> 1;
-          if ((use > 0 && !mbar_wait(&taken[b], (use - 1) & 1u, budget)) || !mbar_wait(&full[s], round & 1u, budget)) {
+          if (!mbar_wait_counted(&full[s], round & 1u, budget) ||
+              (use > 0 && !mbar_wait_counted(&taken[b], (use - 1) & 1u, budget))) {
             atomicOr(&g_mm_error, 1u);
             abort_flag = 1;
             break;
@@ -309,113 +346,182 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           const uint32_t st = smem_u32(stages + s * S::kStageBytes);
           const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + S::kABytes);
 #pragma unroll
-          for (int k = 0; k < kMmBlock / 32; k++) mma_f8(tmem + b * BN, da + 2 * k, db + 2 * k, p.idesc, k > 0);
-          mma_commit(&empty[s]);
-          mma_commit(&done[b]);
+          for (int k = 0; k < kMmBlock / 32; k++)
+            mma_f8<CG>(tmem + b * kMmCols, da + 2 * k, db + 2 * k, p.idesc, k > 0);
+          mma_commit<CG>(&done[b]);
+          mma_commit<CG>(&empty[s]);
         }
       }
       // nothing is in flight when the tensor memory is freed
-      mma_commit(&drained);
+      mma_commit<CG>(&drained);
       mbar_wait(&drained, 0, kMmDrainNs);
     }
-  } else {
-    // ---------------- sums over the blocks and the epilogue ----------------
-    const int half = warp >> 2;               // columns [half * COLS, half * COLS + COLS)
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-    const uint32_t taddr = tmem + lanes + half * COLS;
+    __syncwarp();
+  } else if (warp < kMmEpiWarps + 2 + SW) {
+    // ---------------- scales: SW warps, four blocks of K at a time ----------------
+    // Quads of blocks are aligned in the scale rows, so that with rows of a
+    // multiple of four a quad is one 16-byte load (a line a row: four times
+    // fewer than a load a block).
+    const bool vec = ((p.sa_ld | p.sb_ld) & 3) == 0 && (((uintptr_t)p.sa | (uintptr_t)p.sb) & 15) == 0;
+    const auto quad = [&](const float* row, int64_t ld, int64_t q) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (vec) {
+        v = __ldg((const float4*)(row + 4 * q));
+      } else {
+        v.x = __ldg(row + 4 * q);
+        if (4 * q + 1 < ld) v.y = __ldg(row + 4 * q + 1);
+        if (4 * q + 2 < ld) v.z = __ldg(row + 4 * q + 2);
+        if (4 * q + 3 < ld) v.w = __ldg(row + 4 * q + 3);
+      }
+      return v;
+    };
+    const auto put = [&](float* at, const float4& v) {  // the four blocks of one row or column
+      at[0] = v.x, at[NS] = v.y, at[2 * NS] = v.z, at[3 * NS] = v.w;
+    };
     uint32_t it = 0;
     bool ok = true;
-    for (uint32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const MmTile w = mm_tile<BN, MODE>(p, first, t);
-      const int64_t row = w.row0 + (warp & 3) * 32 + lane;
-      const int64_t c0 = w.n0 + half * COLS;
+    for (uint32_t t = tile0; t < tiles && ok; t += tile_step) {
+      const MmTile w = mm_tile<CG, MODE>(p, first, t);
+      if (w.nkb == 0) continue;
       const int64_t kb0 = w.k0 / kMmBlock;
-      const float* sa = p.sa + (row < p.m ? row : p.m - 1) * p.sa_ld + kb0;
-      const float* sb;
-      float nsb[COLSCALE ? COLS / 32 : 1];
-      if constexpr (COLSCALE) {
-        sb = p.sb + kb0;
-      } else {
-        const int64_t nb = (p.n + kMmBlock - 1) / kMmBlock;
-        const int64_t cb = c0 / kMmBlock < nb ? c0 / kMmBlock : nb - 1;
-        sb = p.sb + ((MODE == kMmRowGroups ? (int64_t)w.g * nb : 0) + cb) * p.sb_ld;
-      }
-      const auto load_sb = [&](int kb) {
-        if constexpr (COLSCALE) {
+      for (int64_t q = kb0 >> 2; q <= (kb0 + w.nkb - 1) >> 2; q++, it++) {
+        const uint32_t s = it % kMmScaleSlots, round = it / kMmScaleSlots;
+        float* at = &scale[s][0][0];
+        constexpr int N = NS / 32 / SW;
+        const int e0 = (warp - (kMmEpiWarps + 2)) * N * 32 + lane;  // of the rows, then of the columns
+        float4 v[N];
 #pragma unroll
-          for (int i = 0; i < COLS / 32; i++) {
-            const int64_t c = c0 + lane + 32 * i;
-            nsb[i] = __ldg(sb + (c < p.n ? c : p.n - 1) * p.sb_ld + kb);
+        for (int i = 0; i < N; i++) {
+          const int e = e0 + i * 32;
+          if (e < kMmRows) {
+            const int64_t r = w.row0 + rank * kMmRows + e;
+            v[i] = quad(p.sa + (r < p.m ? r : p.m - 1) * p.sa_ld, p.sa_ld, q);
+          } else if constexpr (COLSCALE) {
+            const int64_t c = w.n0 + e - kMmRows;
+            v[i] = quad(p.sb + (c < p.n ? c : p.n - 1) * p.sb_ld, p.sb_ld, q);
+          } else {
+            const int64_t nb = (p.n + kMmBlock - 1) / kMmBlock, c = w.n0 / kMmBlock + (lane & 1);
+            v[i] = quad(p.sb + ((MODE == kMmRowGroups ? (int64_t)w.g * nb : 0) + (c < nb ? c : nb - 1)) * p.sb_ld, p.sb_ld, q);
           }
-        } else {
-          nsb[0] = __ldg(sb + kb);
         }
-      };
-      uint64_t acc[COLS / 2];
-#pragma unroll
-      for (int i = 0; i < COLS / 2; i++) acc[i] = 0;
-      float nsa = 0.f;
-      if (w.nkb > 0) {
-        nsa = __ldg(sa);
-        load_sb(0);
-      }
-      for (int kb = 0; kb < w.nkb; kb++, it++) {
-        const uint32_t b = it & 1u, use = it >> 1;
-        float scale = nsa;
-        if constexpr (COLSCALE) {
-#pragma unroll
-          for (int i = 0; i < COLS / 32; i++) sbuf[warp][b][lane + 32 * i] = nsb[i];
-          __syncwarp();
-        } else {
-          scale = __fmul_rn(nsa, nsb[0]);
-        }
-        if (kb + 1 < w.nkb) {
-          nsa = __ldg(sa + kb + 1);
-          load_sb(kb + 1);
-        }
-        const uint64_t s2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
-        // one decision for the warp: its tensor-memory loads are collective
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&done[b], use & 1u, budget) && !abort_flag)) {
+        if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_counted(&sempty[s], (round - 1) & 1u, budget) && !abort_flag)) {
           ok = false;
           break;
         }
-        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < N; i++) put(at + e0 + i * 32, v[i]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[s]);
+      }
+    }
+    if (!ok) {
+      if (lane == 0) atomicOr(&g_mm_error, 1u);
+      abort_flag = 1;
+    }
+  }
+  } else {
+    regs_inc<kMmRegsEpi>();
+    // ---------------- sums over the blocks and the epilogue ----------------
+    const int half = warp >> 2;                         // columns [half * COLS, half * COLS + COLS)
+    const int quarter = warp & 3;                       // this warp's 32 lanes of tensor memory
+    const uint32_t taddr = tmem + ((uint32_t)quarter << 21) + half * COLS;
+    const uint32_t taken_at = CG == 1 ? 0 : cluster_addr(&taken[0], 0);
+    uint32_t it = 0, sit = 0;  // blocks of K and quads of scales taken
+    int kq = 0;                // the next block's place in its quad
+    float next = 0.0f;         // its row scale (and half's)
+    uint32_t r[2][32];
+    uint32_t patience = budget;
+    // Waits for a block of K and starts its way from tensor memory to
+    // registers.  The warp goes on whatever a wait says, since its loads are
+    // collective; after a wait that ran out the others do not wait long, the
+    // tile loop ends, and the error word tells that the output is worthless.
+    const auto fetch = [&](bool new_quad) {
+      const uint32_t slot = sit % kMmScaleSlots, b = it & 1u;
+      bool there = mbar_wait_counted(&done[b], (it >> 1) & 1u, patience);
+      if (new_quad) there &= mbar_wait_counted(&sfull[slot], (sit / kMmScaleSlots) & 1u, patience);
+      if (!there) patience = 0;
+      tc_fence_after();
+      __syncwarp();
+      tmem_load32(r[0], taddr + b * kMmCols);
+      next = scale[slot][kq][quarter * 32 + lane];
+      if constexpr (!COLSCALE) next = __fmul_rn(next, scale[slot][kq][kMmRows + half]);
+    };
+    for (uint32_t t = tile0; t < tiles && __all_sync(0xFFFFFFFFu, patience == budget); t += tile_step) {
+      int nkb;
+      {
+        const MmTile w = mm_tile<CG, MODE>(p, first, t);
+        nkb = w.nkb;
+        kq = (int)(w.k0 / kMmBlock) & 3;
+      }
+      uint64_t acc[COLS / 2];
+#pragma unroll
+      for (int i = 0; i < COLS / 2; i++) acc[i] = 0;
+      // Chunks of 32 columns, the next one (of the next block, too) on its
+      // way from tensor memory while this one is added.
+      if (nkb > 0) fetch(true);
+      for (; nkb > 0; nkb--) {
+        const uint32_t b = it & 1u, slot = sit % kMmScaleSlots;
+        const float* sc = scale[slot][kq];
+        const uint64_t s2 = pack2(__float_as_uint(next), __float_as_uint(next));
+        const bool quad_ends = kq == 3 || nkb == 1;
+        it++;
+        kq = (kq + 1) & 3;
+        sit += quad_ends;
 #pragma unroll
         for (int c = 0; c < COLS; c += 32) {
-          uint32_t r[32];
-          tmem_load32(r, taddr + b * BN + c);
+          uint32_t(&v)[32] = r[(c / 32) & 1];
           tmem_wait_loads();
+          if (c + 32 < COLS) {
+            tmem_load32(r[(c / 32 + 1) & 1], taddr + b * kMmCols + c + 32);
+          } else {
+            // everything of this block is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CG == 1) mbar_arrive(&taken[b]); else mbar_arrive_cluster(taken_at + 8 * b);
+            }
+            if (nkb > 1) fetch(quad_ends);
+          }
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             uint64_t f0 = s2, f1 = s2;
             if constexpr (COLSCALE) {
-              const ulonglong2 v = *(const ulonglong2*)&sbuf[warp][b][c + i];
-              f0 = mul2p(v.x, s2);
-              f1 = mul2p(v.y, s2);
+              const ulonglong2 cs = *(const ulonglong2*)&sc[kMmRows + half * COLS + c + i];
+              f0 = mul2p(cs.x, s2);
+              f1 = mul2p(cs.y, s2);
             }
-            acc[(c + i) / 2] = fma2(pack2(r[i], r[i + 1]), f0, acc[(c + i) / 2]);
-            acc[(c + i) / 2 + 1] = fma2(pack2(r[i + 2], r[i + 3]), f1, acc[(c + i) / 2 + 1]);
+            acc[(c + i) / 2] = fma2(pack2(v[i], v[i + 1]), f0, acc[(c + i) / 2]);
+            acc[(c + i) / 2 + 1] = fma2(pack2(v[i + 2], v[i + 3]), f1, acc[(c + i) / 2 + 1]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&taken[b]);
+        if (quad_ends) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[slot]);
+        }
       }
-      if (ok && row < w.row_end)
-        mm_store_row<COLS, F32>(p, (MODE == kMmKGroups ? (int64_t)w.g * p.m : 0) + row, c0, acc);
+      // the tile again, rather than its values kept through the loop
+      uint32_t t2 = t;
+      asm volatile("" : "+r"(t2));
+      const MmTile w = mm_tile<CG, MODE>(p, first, t2);
+      const int64_t row = w.row0 + rank * kMmRows + quarter * 32 + lane;
+      if (row < w.row_end)
+        mm_store_row<COLS, F32>(p, (MODE == kMmKGroups ? (int64_t)w.g * p.m : 0) + row, w.n0 + half * COLS, acc);
     }
-    if (!ok) {
-      if (lane == 0) atomicOr(&g_mm_error, 1u);
+    if (patience != budget) {
+      atomicOr(&g_mm_error, 1u);
       abort_flag = 1;
     }
     pdl_launch_dependents();
   }
   tc_fence_before();
   __syncthreads();
+  // in a pair, neither leaves while the other's copies, products or arrivals
+  // may still reach its shared memory; every wait before this one is bounded
+  if constexpr (CG == 2) cluster_sync();
   if (warp == kMmEpiWarps) {
     __syncwarp();
     tc_fence_after();
-    tmem_free(tmem, 2 * BN);
+    tmem_free<CG>(tmem, 512);
   }
 }
 
@@ -449,27 +555,49 @@ static fp8q_status mm_map(CUtensorMap* map, const void* q, int64_t rows, int64_t
   return r == CUDA_SUCCESS ? FP8Q_OK : fail(FP8Q_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
-template <int BN, bool COLSCALE, bool F32, int MODE>
+template <int CG, bool COLSCALE, bool F32, int MODE>
 static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt_a, int fmt_b, cudaStream_t s) {
-  using S = MmShape<BN>;
+  using S = MmShape<CG>;
   CUtensorMap ma, mb;
   fp8q_status r = mm_map(&ma, a, p.m, p.k, kMmRows);
   if (r != FP8Q_OK) return r;
-  if ((r = mm_map(&mb, b, MODE == kMmRowGroups ? p.n * p.groups : p.n, p.k, BN)) != FP8Q_OK) return r;
-  p.idesc = instr_desc_f8(fmt_a, fmt_b, kMmRows, BN);
-  p.tiles_n = (int)((p.n + BN - 1) / BN);
+  if ((r = mm_map(&mb, b, MODE == kMmRowGroups ? p.n * p.groups : p.n, p.k, kMmCols / CG)) != FP8Q_OK) return r;
+  p.idesc = instr_desc_f8(fmt_a, fmt_b, S::kTileRows, kMmCols);
+  p.tiles_n = (int)((p.n + kMmCols - 1) / kMmCols);
   const size_t smem = 1024 + (size_t)S::kStages * S::kStageBytes + (MODE == kMmRowGroups ? 4 * ((size_t)p.groups + 1) : 0);
-  const auto kernel = matmul_kernel<BN, COLSCALE, F32, MODE>;
+  const auto kernel = matmul_kernel<CG, COLSCALE, F32, MODE>;
   static const cudaError_t attr = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
       (int)(1024 + S::kStages * S::kStageBytes + (MODE == kMmRowGroups ? 4 * (FP8Q_MAX_GROUPS + 1) : 0)));
   if (attr != cudaSuccess) return cuda_fail(attr, "matmul shared memory");
-  int64_t grid = sm_count();
-  const int64_t per = (p.m + kMmRows - 1) / kMmRows;
+  // the kernel moves registers between its warpgroups: they must be there
+  static const int regs = [&] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs < kMmRegsLaunch) return fail(FP8Q_ERR_CUDA, "matmul kernel built with %d registers a thread", regs);
+  const int64_t per = (p.m + S::kTileRows - 1) / S::kTileRows;
   const int64_t tiles = (MODE == kMmRowGroups ? per + p.groups : MODE == kMmKGroups ? per * p.groups : per) * p.tiles_n;
   if (tiles > INT32_MAX) return fail(FP8Q_ERR_UNSUPPORTED, "product too large: %lld output tiles", (long long)tiles);
+  // pairs that fit at a time: a persistent grid must not leave any for later
+  static const int pairs = [&] {
+    if (CG == 1) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)sm_count());
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : sm_count() / CG;
+  }();
+  int64_t grid = CG == 1 ? sm_count() : pairs;
   if (grid > tiles) grid = tiles;
-  const cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kMmThreads), smem, s, ma, mb, p);
+  const cudaError_t e = launch_cluster(kernel, dim3((unsigned)grid * CG), dim3(kMmThreads), CG, smem, s, ma, mb, p);
   if (e != cudaSuccess) return cuda_fail(e, "matmul kernel launch");
   return check_launch("matmul kernel");
 }
@@ -477,8 +605,12 @@ static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt
 template <bool COLSCALE, int MODE>
 static fp8q_status launch_mm_out(const void* a, const void* b, const MmParams& p, int fmt_a, int fmt_b, int out_dt,
                                  cudaStream_t s) {
-  return out_dt == FP8Q_OUT_FP32 ? launch_mm_t<256, COLSCALE, true, MODE>(a, b, p, fmt_a, fmt_b, s)
-                                 : launch_mm_t<256, COLSCALE, false, MODE>(a, b, p, fmt_a, fmt_b, s);
+  const int64_t rows = MODE == kMmRowGroups ? p.m / p.groups : p.m;
+  if (rows > kMmRows)
+    return out_dt == FP8Q_OUT_FP32 ? launch_mm_t<2, COLSCALE, true, MODE>(a, b, p, fmt_a, fmt_b, s)
+                                   : launch_mm_t<2, COLSCALE, false, MODE>(a, b, p, fmt_a, fmt_b, s);
+  return out_dt == FP8Q_OUT_FP32 ? launch_mm_t<1, COLSCALE, true, MODE>(a, b, p, fmt_a, fmt_b, s)
+                                 : launch_mm_t<1, COLSCALE, false, MODE>(a, b, p, fmt_a, fmt_b, s);
 }
 
 fp8q_status launch_matmul(const MatmulLaunch& L) {

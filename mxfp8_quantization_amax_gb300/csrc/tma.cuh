@@ -62,6 +62,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   return true;
 }
 
+// mbar_wait for pipelines whose waits mostly last a few hundred cycles, less
+// than a reading of %globaltimer takes.  It counts instead: after 16384 tries
+// (a fraction of a millisecond) it sleeps a microsecond between tries, at most
+// budget_us times.
+__device__ __forceinline__ bool mbar_wait_counted(uint64_t* bar, uint32_t parity, uint32_t budget_us) {
+  for (uint32_t n = 0; !mbar_try_wait(bar, parity); n++) {
+    if (n >= 16384u) {
+      if (n - 16384u >= budget_us) return false;
+      __nanosleep(1000);
+    }
+  }
+  return true;
+}
+
 // Barrier over `count` threads of the CTA (a multiple of 32) on named
 // barrier `id` (0 is __syncthreads).
 __device__ __forceinline__ void named_barrier_sync(int id, int count) {
