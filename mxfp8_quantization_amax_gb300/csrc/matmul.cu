@@ -34,6 +34,15 @@ constexpr uint64_t kMmDrainNs = 2000000000ull;
 __device__ unsigned int g_mm_error;
 __device__ unsigned long long g_mm_wait_budget_ns = 1000000000ull;
 
+// Waits that mostly last a few hundred cycles: the clock is looked at only
+// once some 100 us of tries have failed, 64 by a whole warp or 8192 by the one
+// thread that polls, the tensor core's (it is the quicker to see a barrier).
+constexpr uint32_t kMmTries = 64, kMmPolls = 8192;
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t tries = kMmTries) {
+  if (mbar_try_loop(bar, parity, tries)) return true;
+  return mbar_wait(bar, parity, *(volatile unsigned long long*)&g_mm_wait_budget_ns);
+}
+
 // What the groups divide: nothing, the rows of A and D, or K.
 enum : int { kMmDense = 0, kMmRowGroups = 1, kMmKGroups = 2 };
 
@@ -278,8 +287,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
   const uint32_t tile0 = blockIdx.x / CG, tile_step = gridDim.x / CG;
   const uint32_t tmem = tmem_base;
-  const uint64_t budget_ns = g_mm_wait_budget_ns;
-  const uint32_t budget = (uint32_t)(budget_ns < 4000000000000ull ? budget_ns / 1000 : 4000000000u);
 
   uint32_t tiles;
   if constexpr (MODE == kMmRowGroups) {
@@ -293,8 +300,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   regs_dec<kMmRegsLoad>();
   if (warp == kMmEpiWarps) {
     // ---------------- loads: one thread ----------------
-    uint32_t it = 0;  // blocks of K issued
     if (elect_one()) {
+      uint32_t it = 0;  // blocks of K issued
       for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
         const MmTile w = mm_tile<CG, MODE>(p, first, t);
         const int arow = (int)w.row0 + rank * kMmRows;
@@ -302,8 +309,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         int at = (int)w.k0;
         for (int kb = 0; kb < w.nkb; kb++, it++, at += kMmBlock) {
           const uint32_t s = it % S::kStages, round = it / S::kStages;
-          if (round > 0 && !mbar_wait_counted(&empty[s], (round - 1) & 1u, budget)) {
-            atomicOr(&g_mm_error, 1u);
+          if (round > 0 && !mm_wait(&empty[s], (round - 1) & 1u, kMmPolls)) {
             abort_flag = 1;
             break;
           }
@@ -321,10 +327,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           }
         }
       }
-      // every issued copy lands before the CTA (the pair) can exit (fixed 2 s bound)
+      // Every issued copy lands before the CTA (the pair) can exit (fixed 2 s
+      // bound), and every block is used or the flag that ends the waits of the
+      // sums is up.
+      const uint32_t tail = it > S::kStages ? it - S::kStages : 0;
       if (rank == 0)
-        for (uint32_t j = it > S::kStages ? it - S::kStages : 0; j < it; j++)
-          mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
+        for (uint32_t j = tail; j < it; j++) mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
+      for (uint32_t j = tail; j < it && !abort_flag; j++)
+        if (!mm_wait(&empty[j % S::kStages], (j / S::kStages) & 1u, kMmPolls)) abort_flag = 1;
+      if (abort_flag) atomicOr(&g_mm_error, 1u);
     }
     __syncwarp();
     pdl_launch_dependents();
@@ -336,8 +347,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         const MmTile w = mm_tile<CG, MODE>(p, first, t);
         for (int kb = 0; kb < w.nkb; kb++, it++) {
           const uint32_t s = it % S::kStages, round = it / S::kStages, b = it & 1u, use = it >> 1;
-          if (!mbar_wait_counted(&full[s], round & 1u, budget) ||
-              (use > 0 && !mbar_wait_counted(&taken[b], (use - 1) & 1u, budget))) {
+          if (!mm_wait(&full[s], round & 1u, kMmPolls) || (use > 0 && !mm_wait(&taken[b], (use - 1) & 1u, kMmPolls))) {
             atomicOr(&g_mm_error, 1u);
             abort_flag = 1;
             break;
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             v[i] = quad(p.sb + ((MODE == kMmRowGroups ? (int64_t)w.g * nb : 0) + (c < nb ? c : nb - 1)) * p.sb_ld, p.sb_ld, q);
           }
         }
-        if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait_counted(&sempty[s], (round - 1) & 1u, budget) && !abort_flag)) {
+        if (!__all_sync(0xFFFFFFFFu, round == 0 || mm_wait(&sempty[s], (round - 1) & 1u))) {
           ok = false;
           break;
         }
@@ -430,23 +440,31 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     int kq = 0;                // the next block's place in its quad
     float next = 0.0f;         // its row scale (and half's)
     uint32_t r[2][32];
-    uint32_t patience = budget;
+    bool dead = false;
     // Waits for a block of K and starts its way from tensor memory to
-    // registers.  The warp goes on whatever a wait says, since its loads are
-    // collective; after a wait that ran out the others do not wait long, the
-    // tile loop ends, and the error word tells that the output is worthless.
+    // registers.  These waits count nothing (a counter costs a spilled
+    // register, 4%): they end by the flag that the loads, the tensor core and
+    // the scales raise when a wait of theirs runs out.  The warp goes on even
+    // then, since its loads are collective; its tile loop ends, and the error
+    // word tells that the output is worthless.
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+      while (!mbar_try_wait(bar, parity))
+        if (abort_flag) {
+          dead = true;
+          break;
+        }
+    };
     const auto fetch = [&](bool new_quad) {
       const uint32_t slot = sit % kMmScaleSlots, b = it & 1u;
-      bool there = mbar_wait_counted(&done[b], (it >> 1) & 1u, patience);
-      if (new_quad) there &= mbar_wait_counted(&sfull[slot], (sit / kMmScaleSlots) & 1u, patience);
-      if (!there) patience = 0;
+      wait(&done[b], (it >> 1) & 1u);
+      if (new_quad) wait(&sfull[slot], (sit / kMmScaleSlots) & 1u);
       tc_fence_after();
       __syncwarp();
       tmem_load32(r[0], taddr + b * kMmCols);
       next = scale[slot][kq][quarter * 32 + lane];
       if constexpr (!COLSCALE) next = __fmul_rn(next, scale[slot][kq][kMmRows + half]);
     };
-    for (uint32_t t = tile0; t < tiles && __all_sync(0xFFFFFFFFu, patience == budget); t += tile_step) {
+    for (uint32_t t = tile0; t < tiles && !__any_sync(0xFFFFFFFFu, dead); t += tile_step) {
       int nkb;
       {
         const MmTile w = mm_tile<CG, MODE>(p, first, t);
@@ -506,10 +524,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       const int64_t row = w.row0 + rank * kMmRows + quarter * 32 + lane;
       if (row < w.row_end)
         mm_store_row<COLS, F32>(p, (MODE == kMmKGroups ? (int64_t)w.g * p.m : 0) + row, w.n0 + half * COLS, acc);
-    }
-    if (patience != budget) {
-      atomicOr(&g_mm_error, 1u);
-      abort_flag = 1;
     }
     pdl_launch_dependents();
   }
