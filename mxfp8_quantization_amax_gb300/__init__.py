@@ -168,11 +168,17 @@ def _check(status: int, what: str):
 
 
 def _ptr(t):
-    return None if t is None else _P(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the stream's address without a Stream object around it, where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream():
-    return _P(torch.cuda.current_stream().cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _dt(x: torch.Tensor) -> int:
@@ -854,7 +860,7 @@ def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, align: int = 1, out: dict
     row_of = _result(o.get("row_of"), tuple(ids.shape), torch.int32, ids.device)
     src = _result(o.get("src"), (rows,), torch.int32, ids.device)
     need = L.fp8q_moe_plan_workspace_bytes(slots, num_experts)
-    ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
     _check(L.fp8q_moe_plan(_ptr(ids), slots, num_experts, align, rows, _ptr(offsets), _ptr(row_of), _ptr(src),
                            _ptr(ws), need, _stream()), "fp8q_moe_plan")
     return {"offsets": offsets, "row_of": row_of, "src": src}

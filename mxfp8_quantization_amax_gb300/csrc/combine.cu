@@ -14,6 +14,7 @@ namespace fp8q {
 
 constexpr int kCbThreads = 128;
 constexpr int kCbBackThreads = 256;
+constexpr int kCbBatch = 4;     // rows a thread has on their way at a time (a missing one reads row 0)
 constexpr int kCbPadRows = 64;  // rows whose padding one CTA of the backward grid looks for
 
 struct CbParams {
@@ -100,15 +101,19 @@ __global__ void __launch_bounds__(kCbThreads) combine_kernel(CbParams p) {
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; k++) acc[k] = 0.0f;
-#pragma unroll 8
-    for (int j = 0; j < p.top_k; j++) {
-      const int64_t r = cb_row(p, t * p.top_k + j);
-      if (r >= 0) {
-        const float w = p.w ? __ldg(p.w + t * p.top_k + j) : 1.0f;
-        float v[V];
-        cb_load<DT, V>(p.y, r * p.cols + c, v);
+    for (int j0 = 0; j0 < p.top_k && p.rows > 0; j0 += kCbBatch) {
+      int64_t r[kCbBatch];
+      float v[kCbBatch][V];
 #pragma unroll
-        for (int k = 0; k < V; k++) acc[k] = __fmaf_rn(w, v[k], acc[k]);
+      for (int i = 0; i < kCbBatch; i++) r[i] = j0 + i < p.top_k ? cb_row(p, t * p.top_k + j0 + i) : -1;
+#pragma unroll
+      for (int i = 0; i < kCbBatch; i++) cb_load<DT, V>(p.y, (r[i] < 0 ? 0 : r[i]) * p.cols + c, v[i]);
+#pragma unroll
+      for (int i = 0; i < kCbBatch; i++) {
+        if (r[i] < 0) continue;
+        const float w = p.w ? __ldg(p.w + t * p.top_k + j0 + i) : 1.0f;
+#pragma unroll
+        for (int k = 0; k < V; k++) acc[k] = __fmaf_rn(w, v[i][k], acc[k]);
       }
     }
     cb_store<DT, V>(p.out, t * p.cols + c, acc);
@@ -120,6 +125,8 @@ __global__ void __launch_bounds__(kCbThreads) combine_kernel(CbParams p) {
 template <int DT, int V, int KMAX>
 __global__ void __launch_bounds__(kCbBackThreads) combine_backward_kernel(CbParams p) {
   __shared__ float part[kCbBackThreads / 32][KMAX];
+  __shared__ int64_t rows[KMAX];
+  __shared__ float weights[KMAX];
   pdl_wait();
   const int tid = threadIdx.x;
   if (blockIdx.x >= p.tokens) {
@@ -134,6 +141,11 @@ __global__ void __launch_bounds__(kCbBackThreads) combine_backward_kernel(CbPara
     }
   } else {
     const int64_t t = blockIdx.x;
+    if (tid < KMAX) {
+      rows[tid] = tid < p.top_k ? cb_row(p, t * p.top_k + tid) : -1;
+      weights[tid] = tid < p.top_k ? __ldg(p.w + t * p.top_k + tid) : 0.0f;
+    }
+    __syncthreads();
     float dot[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; j++) dot[j] = 0.0f;
@@ -141,19 +153,27 @@ __global__ void __launch_bounds__(kCbBackThreads) combine_backward_kernel(CbPara
       float d[V];
       cb_load<DT, V>(p.d_out, t * p.cols + c, d);
 #pragma unroll
-      for (int j = 0; j < KMAX; j++) {
-        if (j >= p.top_k) break;
-        const int64_t r = cb_row(p, t * p.top_k + j);
-        if (r < 0) continue;
-        const float w = __ldg(p.w + t * p.top_k + j);
-        float v[V], o[V];
-        cb_load<DT, V>(p.y, r * p.cols + c, v);
+      for (int j0 = 0; j0 < KMAX; j0 += kCbBatch) {
+        if (j0 >= p.top_k || p.rows == 0) break;
+        float v[kCbBatch][V];
 #pragma unroll
-        for (int k = 0; k < V; k++) {
-          dot[j] = __fmaf_rn(d[k], v[k], dot[j]);
-          o[k] = __fmul_rn(w, d[k]);
+        for (int i = 0; i < kCbBatch; i++) {
+          const int64_t r = rows[j0 + i];
+          cb_load<DT, V>(p.y, (r < 0 ? 0 : r) * p.cols + c, v[i]);
         }
-        cb_store<DT, V>(p.d_y, r * p.cols + c, o);
+#pragma unroll
+        for (int i = 0; i < kCbBatch; i++) {
+          const int64_t r = rows[j0 + i];
+          if (r < 0) continue;
+          const float w = weights[j0 + i];
+          float o[V];
+#pragma unroll
+          for (int k = 0; k < V; k++) {
+            dot[j0 + i] = __fmaf_rn(d[k], v[i][k], dot[j0 + i]);
+            o[k] = __fmul_rn(w, d[k]);
+          }
+          cb_store<DT, V>(p.d_y, r * p.cols + c, o);
+        }
       }
     }
 #pragma unroll

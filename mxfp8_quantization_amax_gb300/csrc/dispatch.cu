@@ -11,9 +11,9 @@
 // adds the counts of the pieces before it and the padded totals of the
 // experts before each, and places the slots, lanes of one expert in lane
 // order.  Only integers are counted, so the result does not depend on timing.
-#include "blockwise.cuh"
 #include "fp8q_device.cuh"
 #include "internal.h"
+#include "tma.cuh"
 
 namespace fp8q {
 
@@ -150,58 +150,187 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanParams p) 
 
 // ---------------------------------------------------------------------------
 // gather and quantize
+//
+// One CTA, one tile of 128 gathered rows x 128 columns in shared memory: both
+// copies' groups are whole in it.  Row tiles are the fast grid axis: the CTAs
+// running at a time share a few column stripes of x, whose rows (each read
+// top_k times) stay in L2.  The arithmetic is fp8q_quantize_blockwise's: per
+// group scale = fl32(F8max / amax) with the per-tensor special cases, code =
+// RNE_sat(fl32(x * scale)), and fl32(1 / scale) stored.
+//
+// It is bound by instructions, not by memory, so a thread takes 32 values of
+// one row group, or 32 rows of two column groups: the division, the shuffles
+// and the stores (one of 32 bytes) are shared by 32 values.
 // ---------------------------------------------------------------------------
+constexpr int kDpTile = 128;
+constexpr int kDpThreads = 256;
+constexpr int kDpBoxBytes = kDpTile * 128;  // 64 columns of the tile's rows
+
 struct DispatchParams {
-  BwParams bw;  // of the gathered matrix
   const uint16_t* x;
   const int* src;
   int64_t slots;
   int top_k;
+  int64_t rows, cols;
+  int64_t tiles_r, tiles_c;
+  int pow2;
+  uint8_t* q;     // [rows][cols]
+  float* s;       // [rows][tiles_c]
+  uint8_t* q_t;   // [cols][rows]
+  float* s_t;     // [cols][tiles_r]
 };
 
 // Token of a row of the gathered matrix; -1 for padding.
-__device__ __forceinline__ int64_t dispatch_token(const DispatchParams& p, int64_t row) {
-  const int s = row < p.bw.rows ? __ldg(p.src + row) : -1;
+__device__ __forceinline__ int64_t dp_token(const DispatchParams& p, int64_t row) {
+  const int s = row < p.rows ? __ldg(p.src + row) : -1;
   return s >= 0 && s < p.slots ? s / p.top_k : -1;
 }
 
-// One CTA, one tile of 128 gathered rows x 128 columns, in the layout the
-// blockwise passes read.  Row tiles are the fast grid axis: the CTAs running
-// at a time share a few column stripes of x, whose rows (each read top_k
-// times) stay in L2.
+// Byte offset in the tile of row r, column c (c even): two boxes of 64
+// columns, 128 bytes a row, whose 16-byte chunks are permuted by the row so
+// that eight rows of one chunk, and one row's chunks, lie in different banks.
+__device__ __forceinline__ uint32_t dp_off(int r, int c) {
+  const int b = (c & 63) * 2;
+  return (uint32_t)((c >> 6) * kDpBoxBytes + r * 128 + ((((b >> 4) ^ (r & 7)) << 4) | (b & 15)));
+}
+
+template <int FMT>
+__device__ __forceinline__ float dp_scale(uint32_t amax_bits, int pow2) {
+  const float s = scale_from_amax(amax_bits, Fmt<FMT>::kMax, 0);
+  return pow2 ? __uint_as_float(__float_as_uint(s) & 0xFF800000u) : s;  // s is a positive normal float
+}
+
+// Four codes of (a, b, c, d) * s.
+template <int FMT>
+__device__ __forceinline__ uint32_t dp_codes(float a, float b, float c, float d, float s) {
+  mul2(a, b, s, s);
+  mul2(c, d, s, s);
+  return cvt4<FMT>(a, b, c, d);
+}
+
+// 32 codes of one group, contiguous: one 32-byte store where the row's length
+// allows, else 16 at a time, as many as there are.
+__device__ __forceinline__ void dp_store(uint8_t* at, const uint32_t (&d)[8], bool wide, int64_t left) {
+  if (wide) {
+    st32B(at, d);
+  } else {
+    st_stream(at, make_uint4(d[0], d[1], d[2], d[3]));
+    if (left > 16) st_stream(at + 16, make_uint4(d[4], d[5], d[6], d[7]));
+  }
+}
+
+// Row groups: a warp takes 8 rows at a time, lane = 8 * (quarter of the
+// columns) + row.
+template <int FMT>
+__device__ __forceinline__ void dp_rows(const DispatchParams& p, const unsigned char* tile, int64_t r0, int64_t c0) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = (lane >> 3) * 32;
+  const bool wide = (p.cols & 31) == 0 && ((uintptr_t)p.q & 31) == 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; pass++) {
+    const int r = pass * 64 + warp * 8 + (lane & 7);
+    uint4 v[4];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[i] = *(const uint4*)(tile + dp_off(r, c + 8 * i));
+      m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[i].x), v[i].y), v[i].z), v[i].w);
+    }
+    uint32_t a = max(m << 16, m & 0xFFFF0000u);
+    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 8));
+    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 16));
+    const float s = dp_scale<FMT>(a, p.pow2);
+    if (r0 + r >= p.rows) continue;
+    if (lane < 8) p.s[(r0 + r) * p.tiles_c + c0 / kDpTile] = __frcp_rn(s);
+    if (c0 + c >= p.cols) continue;
+    uint32_t d[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      d[2 * i] = dp_codes<FMT>(bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y), s);
+      d[2 * i + 1] = dp_codes<FMT>(bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w), s);
+    }
+    if (a > 0x7F800000u) {  // a NaN in the group
+#pragma unroll
+      for (int i = 0; i < 8; i++) d[i] = canon_nan4<FMT>(d[i]);
+    }
+    dp_store(p.q + (r0 + r) * p.cols + c0 + c, d, wide, p.cols - c0 - c);
+  }
+}
+
+// Column groups: a thread takes a column pair over 32 rows; the four quarters
+// of the rows share their maxima through shared memory.
+template <int FMT>
+__device__ __forceinline__ void dp_cols(const DispatchParams& p, const unsigned char* tile, int64_t r0, int64_t c0,
+                                        uint32_t (*sh_amax)[64]) {
+  const int pair = threadIdx.x & 63, h = threadIdx.x >> 6, c = 2 * pair;
+  uint32_t w[32], m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; i++) {
+    w[i] = *(const uint32_t*)(tile + dp_off(32 * h + i, c));
+    m = absmax_bf16x2(m, w[i]);
+  }
+  sh_amax[h][pair] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; k++) m = max_u16x2(m, sh_amax[k][pair]);
+  if (c0 + c >= p.cols) return;
+  const int64_t r = r0 + 32 * h;
+  const bool wide = (p.rows & 31) == 0 && ((uintptr_t)p.q_t & 31) == 0;
+#pragma unroll
+  for (int odd = 0; odd < 2; odd++) {
+    const uint32_t a = odd ? m & 0xFFFF0000u : m << 16;
+    const float s = dp_scale<FMT>(a, p.pow2);
+    if (h == 0) p.s_t[(c0 + c + odd) * p.tiles_r + r0 / kDpTile] = __frcp_rn(s);
+    if (r >= p.rows) continue;
+    uint32_t d[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      if (odd)
+        d[k] = dp_codes<FMT>(bf16_hi(w[4 * k]), bf16_hi(w[4 * k + 1]), bf16_hi(w[4 * k + 2]), bf16_hi(w[4 * k + 3]), s);
+      else
+        d[k] = dp_codes<FMT>(bf16_lo(w[4 * k]), bf16_lo(w[4 * k + 1]), bf16_lo(w[4 * k + 2]), bf16_lo(w[4 * k + 3]), s);
+    }
+    if (a > 0x7F800000u) {
+#pragma unroll
+      for (int k = 0; k < 8; k++) d[k] = canon_nan4<FMT>(d[k]);
+    }
+    dp_store(p.q_t + (c0 + c + odd) * p.rows + r, d, wide, p.rows - r);
+  }
+}
+
 template <int FMT, int DIR>
-__global__ void __launch_bounds__(kBwConsumers) dispatch_kernel(DispatchParams p) {
-  __shared__ __align__(1024) unsigned char tile[kBwStageBytes];
-  __shared__ uint32_t sh_amax[4 * kBwTile];
+__global__ void __launch_bounds__(kDpThreads) dispatch_kernel(DispatchParams p) {
+  __shared__ __align__(1024) unsigned char tile[2 * kDpBoxBytes];
+  __shared__ uint32_t sh_amax[4][64];
   const int tid = threadIdx.x;
-  const int64_t r0 = (int64_t)blockIdx.x * kBwTile, c0 = (int64_t)blockIdx.y * kBwTile;
+  const int64_t r0 = (int64_t)blockIdx.x * kDpTile, c0 = (int64_t)blockIdx.y * kDpTile;
   pdl_wait();
   const int part = tid & 15;  // 16 lanes fetch one row's 256 bytes
+  const int64_t c = c0 + part * 8;
 #pragma unroll
-  for (int i = 0; i < kBwTile / 16; i++) {
+  for (int i = 0; i < kDpTile / 16; i++) {
     const int r = i * 16 + (tid >> 4);
-    const int64_t t = dispatch_token(p, r0 + r);
-    const int64_t c = c0 + part * 8;
-    const bool there = t >= 0 && c < p.bw.cols;
-    const uint16_t* from = p.x + (there ? t * p.bw.cols + c : 0);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + bw_off(r, part * 8))), "l"(from),
+    const int64_t t = dp_token(p, r0 + r);
+    const bool there = t >= 0 && c < p.cols;
+    const uint16_t* from = p.x + (there ? t * p.cols + c : 0);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + dp_off(r, part * 8))), "l"(from),
                  "r"(there ? 16 : 0)
                  : "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  if constexpr (DIR & MXFP8_ROW) bw_rows<FMT, 1>(p.bw, tile, r0, c0, 1.0f, tid);
-  if constexpr (DIR & MXFP8_COL) bw_cols<FMT, 1>(p.bw, tile, r0, c0, 1.0f, tid, sh_amax);
+  if constexpr (DIR & MXFP8_ROW) dp_rows<FMT>(p, tile, r0, c0);
+  if constexpr (DIR & MXFP8_COL) dp_cols<FMT>(p, tile, r0, c0, sh_amax);
   pdl_launch_dependents();
 }
 
 template <int FMT>
 static fp8q_status launch_dispatch_f(const DispatchParams& p, int dir, cudaStream_t s) {
-  const dim3 grid((unsigned)p.bw.tiles_r, (unsigned)p.bw.tiles_c);
+  const dim3 grid((unsigned)p.tiles_r, (unsigned)p.tiles_c);
   const auto kernel = dir == MXFP8_ROW   ? dispatch_kernel<FMT, MXFP8_ROW>
                       : dir == MXFP8_COL ? dispatch_kernel<FMT, MXFP8_COL>
                                          : dispatch_kernel<FMT, MXFP8_BOTH>;
-  const cudaError_t e = launch_kernel(kernel, grid, dim3(kBwConsumers), 0, s, p);
+  const cudaError_t e = launch_kernel(kernel, grid, dim3(kDpThreads), 0, s, p);
   if (e != cudaSuccess) return cuda_fail(e, "dispatch kernel launch");
   return check_launch("dispatch kernel");
 }
@@ -237,7 +366,7 @@ extern "C" size_t fp8q_moe_plan_workspace_bytes(int64_t slots, int32_t experts) 
   int64_t piece;
   int pieces;
   plan_pieces(slots, &piece, &pieces);
-  return (size_t)pieces * experts * sizeof(int);
+  return pieces > 1 ? (size_t)pieces * experts * sizeof(int) : 0;
 }
 
 extern "C" fp8q_status fp8q_moe_plan(const int32_t* ids, int64_t slots, int32_t experts, int32_t align, int64_t rows,
@@ -255,7 +384,7 @@ extern "C" fp8q_status fp8q_moe_plan(const int32_t* ids, int64_t slots, int32_t 
     return fail(FP8Q_ERR_INVALID_ARG, "ids and row_of must be 4-byte aligned device pointers");
   if (rows > 0 && (!src || ((uintptr_t)src & 3))) return fail(FP8Q_ERR_INVALID_ARG, "src must be a 4-byte aligned device pointer");
   const size_t need = fp8q_moe_plan_workspace_bytes(slots, experts);
-  if (!workspace || ((uintptr_t)workspace & 3) || workspace_bytes < need)
+  if (need > 0 && (!workspace || ((uintptr_t)workspace & 3) || workspace_bytes < need))
     return fail(FP8Q_ERR_INVALID_ARG, "workspace must be a 4-byte aligned device pointer to %zu bytes", need);
   PlanParams p{};
   p.ids = ids;
@@ -293,7 +422,7 @@ extern "C" fp8q_status fp8q_moe_dispatch(const void* x, int32_t dt, int64_t toke
   if (top_k < 1) return fail(FP8Q_ERR_INVALID_ARG, "top_k must be >= 1");
   if (cols % 16 != 0) return fail(FP8Q_ERR_UNSUPPORTED, "dispatch needs cols %% 16 == 0");
   if ((dir & MXFP8_COL) && rows % 16 != 0) return fail(FP8Q_ERR_UNSUPPORTED, "the transposed copy needs rows %% 16 == 0");
-  if (rows > INT32_MAX || tokens > INT32_MAX / top_k || cols > 65535 * (int64_t)kBwTile)
+  if (rows > INT32_MAX || tokens > INT32_MAX / top_k || cols > 65535 * (int64_t)kDpTile)
     return fail(FP8Q_ERR_UNSUPPORTED, "tokens, cols or rows too large");
   if (rows * cols == 0) return FP8Q_OK;
   if ((tokens > 0 && !x) || ((uintptr_t)x & 15)) return fail(FP8Q_ERR_INVALID_ARG, "x must be a 16-byte aligned device pointer");
@@ -303,15 +432,15 @@ extern "C" fp8q_status fp8q_moe_dispatch(const void* x, int32_t dt, int64_t toke
   if ((dir & MXFP8_COL) && (!q_t || !scale_inv_t || ((uintptr_t)q_t & 15) || ((uintptr_t)scale_inv_t & 3)))
     return fail(FP8Q_ERR_INVALID_ARG, "q_t (16-byte aligned) and scale_inv_t are required for the transposed copy");
   DispatchParams p{};
-  p.bw.rows = rows;
-  p.bw.cols = cols;
-  p.bw.tiles_r = (rows + kBwTile - 1) / kBwTile;
-  p.bw.tiles_c = (cols + kBwTile - 1) / kBwTile;
-  p.bw.pow2 = pow2_scales ? 1 : 0;
-  p.bw.q = q;
-  p.bw.s = scale_inv;
-  p.bw.q_t = q_t;
-  p.bw.s_t = scale_inv_t;
+  p.rows = rows;
+  p.cols = cols;
+  p.tiles_r = (rows + kDpTile - 1) / kDpTile;
+  p.tiles_c = (cols + kDpTile - 1) / kDpTile;
+  p.pow2 = pow2_scales ? 1 : 0;
+  p.q = q;
+  p.s = scale_inv;
+  p.q_t = q_t;
+  p.s_t = scale_inv_t;
   p.x = (const uint16_t*)x;
   p.src = src;
   p.slots = tokens * top_k;

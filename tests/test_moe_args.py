@@ -47,7 +47,7 @@ def test_rows_and_workspace(lib):
     assert lib.fp8q_moe_rows(128, 64, 1) == 128
     assert lib.fp8q_moe_rows(1000, 8, 128) == (1000 + 8 * 127) // 128 * 128
     assert lib.fp8q_moe_rows(-1, 8, 1) == -1 and lib.fp8q_moe_rows(1, 0, 1) == -1 and lib.fp8q_moe_rows(1, 1, 0) == -1
-    assert lib.fp8q_moe_plan_workspace_bytes(1, 64) >= 256
+    assert lib.fp8q_moe_plan_workspace_bytes(4097, 64) >= 256
     assert lib.fp8q_moe_plan_workspace_bytes(-1, 64) == 0
 
 
@@ -56,7 +56,7 @@ def test_plan(lib, a):
     refused(lib.fp8q_moe_plan, base, [
         (dict(slots=-1), 1), (dict(experts=0), 1), (dict(experts=1025), 2), (dict(align=0), 1), (dict(align=5000), 1), (dict(rows=15), 1),
         (dict(align=128), 1), (dict(offsets=None), 1), (dict(offsets=a + 4), 1), (dict(ids=None), 1), (dict(row_of=a + 1), 1),
-        (dict(src=None), 1), (dict(ws=None), 1), (dict(ws_bytes=8), 1), (dict(slots=2**31, rows=2**31), 2), (dict(rows=2**31), 2)])
+        (dict(src=None), 1), (dict(slots=5000, rows=5000, ws=None), 1), (dict(slots=5000, rows=5000, ws_bytes=8), 1), (dict(slots=2**31, rows=2**31), 2), (dict(rows=2**31), 2)])
 
 
 def test_dispatch(lib, a):
