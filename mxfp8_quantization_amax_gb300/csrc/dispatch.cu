@@ -158,9 +158,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanParams p) 
 // group scale = fl32(F8max / amax) with the per-tensor special cases, code =
 // RNE_sat(fl32(x * scale)), and fl32(1 / scale) stored.
 //
-// It is bound by instructions, not by memory, so a thread takes 32 values of
-// one row group, or 32 rows of two column groups: the division, the shuffles
-// and the stores (one of 32 bytes) are shared by 32 values.
+// It is bound by instructions more than by memory, so each is done once: the
+// maxima of all 128 row groups and 128 column groups first, then one division
+// a thread for all 256 groups, then the codes, 32 of one group a thread (one
+// 32-byte store).  The tile is read twice from shared memory for that.
 // ---------------------------------------------------------------------------
 constexpr int kDpTile = 128;
 constexpr int kDpThreads = 256;
@@ -179,12 +180,6 @@ struct DispatchParams {
   uint8_t* q_t;   // [cols][rows]
   float* s_t;     // [cols][tiles_r]
 };
-
-// Token of a row of the gathered matrix; -1 for padding.
-__device__ __forceinline__ int64_t dp_token(const DispatchParams& p, int64_t row) {
-  const int s = row < p.rows ? __ldg(p.src + row) : -1;
-  return s >= 0 && s < p.slots ? s / p.top_k : -1;
-}
 
 // Byte offset in the tile of row r, column c (c even): two boxes of 64
 // columns, 128 bytes a row, whose 16-byte chunks are permuted by the row so
@@ -219,37 +214,50 @@ __device__ __forceinline__ void dp_store(uint8_t* at, const uint32_t (&d)[8], bo
   }
 }
 
+// Magnitude bits (as FP32 bits) of both halves of a packed maximum.
+__device__ __forceinline__ uint32_t dp_lo(uint32_t m) { return (m & 0x7FFFu) << 16; }
+__device__ __forceinline__ uint32_t dp_hi(uint32_t m) { return m & 0x7FFF0000u; }
+
 // Row groups: a warp takes 8 rows at a time, lane = 8 * (quarter of the
 // columns) + row.
 template <int FMT>
-__device__ __forceinline__ void dp_rows(const DispatchParams& p, const unsigned char* tile, int64_t r0, int64_t c0) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = (lane >> 3) * 32;
-  const bool wide = (p.cols & 31) == 0 && ((uintptr_t)p.q & 31) == 0;
-#pragma unroll 1
+__device__ __forceinline__ void dp_row_max(const unsigned char* tile, uint32_t* amax) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = (lane >> 3) * 32;
+#pragma unroll
   for (int pass = 0; pass < 2; pass++) {
     const int r = pass * 64 + warp * 8 + (lane & 7);
-    uint4 v[4];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      v[i] = *(const uint4*)(tile + dp_off(r, c + 8 * i));
-      m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v[i].x), v[i].y), v[i].z), v[i].w);
+      const uint4 v = *(const uint4*)(tile + dp_off(r, c + 8 * i));
+      m = absmax_nan_bf16x2(absmax_nan_bf16x2(absmax_nan_bf16x2(absmax_nan_bf16x2(m, v.x), v.y), v.z), v.w);
     }
-    uint32_t a = max(m << 16, m & 0xFFFF0000u);
+    uint32_t a = max(dp_lo(m), dp_hi(m));
     a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 8));
     a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 16));
-    const float s = dp_scale<FMT>(a, p.pow2);
-    if (r0 + r >= p.rows) continue;
-    if (lane < 8) p.s[(r0 + r) * p.tiles_c + c0 / kDpTile] = __frcp_rn(s);
-    if (c0 + c >= p.cols) continue;
+    if (lane < 8) amax[r] = a;
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void dp_rows(const DispatchParams& p, const unsigned char* tile, int64_t r0, int64_t c0,
+                                        const float* scale, const uint32_t* amax) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = (lane >> 3) * 32;
+  const bool wide = (p.cols & 31) == 0 && ((uintptr_t)p.q & 31) == 0;
+  if (c0 + c >= p.cols) return;
+#pragma unroll
+  for (int pass = 0; pass < 2; pass++) {
+    const int r = pass * 64 + warp * 8 + (lane & 7);
+    if (r0 + r >= p.rows) break;
+    const float s = scale[r];
     uint32_t d[8];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      d[2 * i] = dp_codes<FMT>(bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y), s);
-      d[2 * i + 1] = dp_codes<FMT>(bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w), s);
+      const uint4 v = *(const uint4*)(tile + dp_off(r, c + 8 * i));
+      d[2 * i] = dp_codes<FMT>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), s);
+      d[2 * i + 1] = dp_codes<FMT>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), s);
     }
-    if (a > 0x7F800000u) {  // a NaN in the group
+    if (amax[r] > 0x7F800000u) {  // a NaN in the group
 #pragma unroll
       for (int i = 0; i < 8; i++) d[i] = canon_nan4<FMT>(d[i]);
     }
@@ -257,70 +265,99 @@ __device__ __forceinline__ void dp_rows(const DispatchParams& p, const unsigned 
   }
 }
 
-// Column groups: a thread takes a column pair over 32 rows; the four quarters
-// of the rows share their maxima through shared memory.
+// Column groups: a thread takes a column pair over 32 rows; quarters[h] holds
+// the packed maxima of rows [32 h, 32 h + 32).
+__device__ __forceinline__ void dp_col_max(const unsigned char* tile, uint32_t (*quarters)[64]) {
+  const int pair = threadIdx.x & 63, h = threadIdx.x >> 6;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; i++) m = absmax_nan_bf16x2(m, *(const uint32_t*)(tile + dp_off(32 * h + i, 2 * pair)));
+  quarters[h][pair] = m;
+}
+
 template <int FMT>
 __device__ __forceinline__ void dp_cols(const DispatchParams& p, const unsigned char* tile, int64_t r0, int64_t c0,
-                                        uint32_t (*sh_amax)[64]) {
+                                        const float* scale, const uint32_t* amax) {
   const int pair = threadIdx.x & 63, h = threadIdx.x >> 6, c = 2 * pair;
-  uint32_t w[32], m = 0;
-#pragma unroll
-  for (int i = 0; i < 32; i++) {
-    w[i] = *(const uint32_t*)(tile + dp_off(32 * h + i, c));
-    m = absmax_bf16x2(m, w[i]);
-  }
-  sh_amax[h][pair] = m;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; k++) m = max_u16x2(m, sh_amax[k][pair]);
-  if (c0 + c >= p.cols) return;
   const int64_t r = r0 + 32 * h;
+  if (c0 + c >= p.cols || r >= p.rows) return;
   const bool wide = (p.rows & 31) == 0 && ((uintptr_t)p.q_t & 31) == 0;
+  const float s0 = scale[c], s1 = scale[c + 1];
+  uint32_t d0[8], d1[8];
 #pragma unroll
-  for (int odd = 0; odd < 2; odd++) {
-    const uint32_t a = odd ? m & 0xFFFF0000u : m << 16;
-    const float s = dp_scale<FMT>(a, p.pow2);
-    if (h == 0) p.s_t[(c0 + c + odd) * p.tiles_r + r0 / kDpTile] = __frcp_rn(s);
-    if (r >= p.rows) continue;
-    uint32_t d[8];
+  for (int k = 0; k < 8; k++) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = *(const uint32_t*)(tile + dp_off(32 * h + 4 * k + i, c));
+    d0[k] = dp_codes<FMT>(bf16_lo(w[0]), bf16_lo(w[1]), bf16_lo(w[2]), bf16_lo(w[3]), s0);
+    d1[k] = dp_codes<FMT>(bf16_hi(w[0]), bf16_hi(w[1]), bf16_hi(w[2]), bf16_hi(w[3]), s1);
+  }
+  if (max(amax[c], amax[c + 1]) > 0x7F800000u) {
 #pragma unroll
     for (int k = 0; k < 8; k++) {
-      if (odd)
-        d[k] = dp_codes<FMT>(bf16_hi(w[4 * k]), bf16_hi(w[4 * k + 1]), bf16_hi(w[4 * k + 2]), bf16_hi(w[4 * k + 3]), s);
-      else
-        d[k] = dp_codes<FMT>(bf16_lo(w[4 * k]), bf16_lo(w[4 * k + 1]), bf16_lo(w[4 * k + 2]), bf16_lo(w[4 * k + 3]), s);
+      d0[k] = canon_nan4<FMT>(d0[k]);
+      d1[k] = canon_nan4<FMT>(d1[k]);
     }
-    if (a > 0x7F800000u) {
-#pragma unroll
-      for (int k = 0; k < 8; k++) d[k] = canon_nan4<FMT>(d[k]);
-    }
-    dp_store(p.q_t + (c0 + c + odd) * p.rows + r, d, wide, p.rows - r);
   }
+  uint8_t* at = p.q_t + (c0 + c) * p.rows + r;
+  dp_store(at, d0, wide, p.rows - r);
+  dp_store(at + p.rows, d1, wide, p.rows - r);
 }
 
 template <int FMT, int DIR>
 __global__ void __launch_bounds__(kDpThreads) dispatch_kernel(DispatchParams p) {
   __shared__ __align__(1024) unsigned char tile[2 * kDpBoxBytes];
-  __shared__ uint32_t sh_amax[4][64];
+  __shared__ uint32_t quarters[4][64];
+  __shared__ uint32_t amax[2 * kDpTile];  // of the rows, of the columns
+  __shared__ float scale[2 * kDpTile];
+  __shared__ int token[kDpTile];
   const int tid = threadIdx.x;
   const int64_t r0 = (int64_t)blockIdx.x * kDpTile, c0 = (int64_t)blockIdx.y * kDpTile;
   pdl_wait();
-  const int part = tid & 15;  // 16 lanes fetch one row's 256 bytes
-  const int64_t c = c0 + part * 8;
+  if (tid < kDpTile) {  // -1: padding
+    const int s = r0 + tid < p.rows ? __ldg(p.src + r0 + tid) : -1;
+    token[tid] = s >= 0 && s < p.slots ? s / p.top_k : -1;
+  }
+  __syncthreads();
+  {
+    const int part = tid & 15;  // 16 lanes fetch one row's 256 bytes
+    const uint16_t* from = p.x + c0 + part * 8;
+    const bool column = c0 + part * 8 < p.cols;
 #pragma unroll
-  for (int i = 0; i < kDpTile / 16; i++) {
-    const int r = i * 16 + (tid >> 4);
-    const int64_t t = dp_token(p, r0 + r);
-    const bool there = t >= 0 && c < p.cols;
-    const uint16_t* from = p.x + (there ? t * p.cols + c : 0);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + dp_off(r, part * 8))), "l"(from),
-                 "r"(there ? 16 : 0)
-                 : "memory");
+    for (int i = 0; i < kDpTile / 16; i++) {
+      const int r = i * 16 + (tid >> 4), t = token[r];
+      const bool there = t >= 0 && column;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + dp_off(r, part * 8))),
+                   "l"(there ? from + (int64_t)t * p.cols : p.x), "r"(there ? 16 : 0)
+                   : "memory");
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  if constexpr (DIR & MXFP8_ROW) dp_rows<FMT>(p, tile, r0, c0);
-  if constexpr (DIR & MXFP8_COL) dp_cols<FMT>(p, tile, r0, c0, sh_amax);
+  if constexpr (DIR & MXFP8_ROW) dp_row_max<FMT>(tile, amax);
+  if constexpr (DIR & MXFP8_COL) dp_col_max(tile, quarters);
+  __syncthreads();
+  // one group a thread
+  const int g = tid & (kDpTile - 1);
+  if (tid < kDpTile) {
+    if constexpr (DIR & MXFP8_ROW) {
+      const float s = dp_scale<FMT>(amax[g], p.pow2);
+      scale[g] = s;
+      if (r0 + g < p.rows) p.s[(r0 + g) * p.tiles_c + blockIdx.y] = __frcp_rn(s);
+    }
+  } else if constexpr (DIR & MXFP8_COL) {
+    uint32_t m = quarters[0][g >> 1];
+#pragma unroll
+    for (int h = 1; h < 4; h++) m = absmax_nan_bf16x2(m, quarters[h][g >> 1]);
+    const uint32_t a = g & 1 ? dp_hi(m) : dp_lo(m);
+    const float s = dp_scale<FMT>(a, p.pow2);
+    amax[kDpTile + g] = a;
+    scale[kDpTile + g] = s;
+    if (c0 + g < p.cols) p.s_t[(c0 + g) * p.tiles_r + blockIdx.x] = __frcp_rn(s);
+  }
+  __syncthreads();
+  if constexpr (DIR & MXFP8_ROW) dp_rows<FMT>(p, tile, r0, c0, scale, amax);
+  if constexpr (DIR & MXFP8_COL) dp_cols<FMT>(p, tile, r0, c0, scale + kDpTile, amax + kDpTile);
   pdl_launch_dependents();
 }
 
