@@ -151,21 +151,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanParams p) 
 // ---------------------------------------------------------------------------
 // gather and quantize
 //
-// One CTA, one tile of 128 gathered rows x 128 columns in shared memory: both
-// copies' groups are whole in it.  Row tiles are the fast grid axis: the CTAs
-// running at a time share a few column stripes of x, whose rows (each read
-// top_k times) stay in L2.  The arithmetic is fp8q_quantize_blockwise's: per
-// group scale = fl32(F8max / amax) with the per-tensor special cases, code =
-// RNE_sat(fl32(x * scale)), and fl32(1 / scale) stored.
+// A CTA takes 128 gathered rows and a run of 128-column tiles of them; both
+// copies' groups are whole in a tile.  The next tile comes into shared memory
+// by cp.async while this one is quantized.  The CTAs running at a time walk
+// the columns together, so that the part of x they gather from (each row is
+// read top_k times) stays in L2.  The arithmetic is fp8q_quantize_blockwise's:
+// per group scale = fl32(F8max / amax) with the per-tensor special cases, code
+// = RNE_sat(fl32(x * scale)), and fl32(1 / scale) stored.
 //
-// It is bound by instructions more than by memory, so each is done once: the
-// maxima of all 128 row groups and 128 column groups first, then one division
-// a thread for all 256 groups, then the codes, 32 of one group a thread (one
-// 32-byte store).  The tile is read twice from shared memory for that.
+// Instructions and shared-memory traffic matter as much as memory here: each
+// group's division is done by one lane, the maxima are packed pairs, and a
+// row's maximum takes one shuffle a row and lane.
 // ---------------------------------------------------------------------------
 constexpr int kDpTile = 128;
 constexpr int kDpThreads = 256;
 constexpr int kDpBoxBytes = kDpTile * 128;  // 64 columns of the tile's rows
+constexpr int kDpTileBytes = 2 * kDpBoxBytes;
 
 struct DispatchParams {
   const uint16_t* x;
@@ -173,7 +174,8 @@ struct DispatchParams {
   int64_t slots;
   int top_k;
   int64_t rows, cols;
-  int64_t tiles_r, tiles_c;
+  int tiles_r, tiles_c;
+  int run;        // column tiles of a CTA
   int pow2;
   uint8_t* q;     // [rows][cols]
   float* s;       // [rows][tiles_c]
@@ -203,9 +205,66 @@ __device__ __forceinline__ uint32_t dp_codes(float a, float b, float c, float d,
   return cvt4<FMT>(a, b, c, d);
 }
 
-// 32 codes of one group, contiguous: one 32-byte store where the row's length
+// Magnitude bits (as FP32 bits) of both halves of a packed maximum.
+__device__ __forceinline__ uint32_t dp_lo(uint32_t m) { return (m & 0x7FFFu) << 16; }
+__device__ __forceinline__ uint32_t dp_hi(uint32_t m) { return m & 0x7FFF0000u; }
+
+// The packed maxima of 8 rows over the 16 lanes of a half-warp: at each step a
+// lane hands half of its rows over and keeps the other half, so that 8
+// shuffles do.  Lane hl ends with row dp_row_of(hl).
+__device__ __forceinline__ int dp_row_of(int hl) { return (hl >> 1) & 7; }
+__device__ __forceinline__ uint32_t dp_row_max(uint32_t (&m)[8], int hl) {
+#pragma unroll
+  for (int n = 4; n >= 1; n >>= 1) {  // lane distance 2 n
+    const bool up = hl & (2 * n);
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const uint32_t give = up ? m[i] : m[i + n], keep = up ? m[i + n] : m[i];
+      m[i] = absmax_nan_bf16x2(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 2 * n));
+    }
+  }
+  return absmax_nan_bf16x2(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 1));
+}
+
+// Row groups: 16 lanes a row, 8 rows (16 apart) a lane; nr, nc: rows and
+// columns of the tile that are there.
+template <int FMT>
+__device__ __forceinline__ void dp_rows(const DispatchParams& p, const unsigned char* tile, int64_t r0, int tc, int nr,
+                                        int nc) {
+  const int hl = threadIdx.x & 15, half = threadIdx.x & 16, r = threadIdx.x >> 4;
+  const unsigned char* from = tile + dp_off(r, hl * 8);  // 16 rows further: 2048 bytes, the same permutation
+  uint4 v[8];
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    v[i] = *(const uint4*)(from + 2048 * i);
+    m[i] = absmax_nan_bf16x2(absmax_nan_bf16x2(v[i].x, v[i].y), absmax_nan_bf16x2(v[i].z, v[i].w));
+  }
+  const uint32_t packed = dp_row_max(m, hl);
+  const uint32_t a = max(dp_lo(packed), dp_hi(packed));
+  const float s = dp_scale<FMT>(a, p.pow2);
+  const int mine = r + 16 * dp_row_of(hl);
+  if (!(hl & 1) && mine < nr) p.s[(r0 + mine) * p.tiles_c + tc] = __frcp_rn(s);
+  const bool nan = __any_sync(0xFFFFFFFFu, a > 0x7F800000u);
+  uint8_t* at = p.q + (r0 + r) * p.cols + (int64_t)tc * kDpTile + hl * 8;
+  const int64_t step = 16 * p.cols;
+  const int there = hl * 8 < nc ? nr - r : 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++, at += step) {
+    const float si = __shfl_sync(0xFFFFFFFFu, s, half | 2 * i);
+    if (16 * i < there) {
+      uint2 o;
+      o.x = dp_codes<FMT>(bf16_lo(v[i].x), bf16_hi(v[i].x), bf16_lo(v[i].y), bf16_hi(v[i].y), si);
+      o.y = dp_codes<FMT>(bf16_lo(v[i].z), bf16_hi(v[i].z), bf16_lo(v[i].w), bf16_hi(v[i].w), si);
+      if (nan) o = make_uint2(canon_nan4<FMT>(o.x), canon_nan4<FMT>(o.y));
+      st_stream(at, o);
+    }
+  }
+}
+
+// 32 codes of one column group: one 32-byte store where the column's length
 // allows, else 16 at a time, as many as there are.
-__device__ __forceinline__ void dp_store(uint8_t* at, const uint32_t (&d)[8], bool wide, int64_t left) {
+__device__ __forceinline__ void dp_store(uint8_t* at, const uint32_t (&d)[8], bool wide, int left) {
   if (wide) {
     st32B(at, d);
   } else {
@@ -214,162 +273,124 @@ __device__ __forceinline__ void dp_store(uint8_t* at, const uint32_t (&d)[8], bo
   }
 }
 
-// Magnitude bits (as FP32 bits) of both halves of a packed maximum.
-__device__ __forceinline__ uint32_t dp_lo(uint32_t m) { return (m & 0x7FFFu) << 16; }
-__device__ __forceinline__ uint32_t dp_hi(uint32_t m) { return m & 0x7FFF0000u; }
-
-// Row groups: a warp takes 8 rows at a time, lane = 8 * (quarter of the
-// columns) + row.
+// Column groups: a thread takes a column pair over 32 rows; the quarters of
+// the rows meet in shared memory, where one thread a column divides.
 template <int FMT>
-__device__ __forceinline__ void dp_row_max(const unsigned char* tile, uint32_t* amax) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = (lane >> 3) * 32;
+__device__ __forceinline__ void dp_cols(const DispatchParams& p, const unsigned char* tile, int64_t r0, int tc, int nr,
+                                        int nc, uint32_t (*quarters)[64], float* scale) {
+  const int tid = threadIdx.x, pair = tid & 63, h = tid >> 6, c = 2 * pair;
+  const int64_t c0 = (int64_t)tc * kDpTile;
+  uint32_t w[32], m = 0;
 #pragma unroll
-  for (int pass = 0; pass < 2; pass++) {
-    const int r = pass * 64 + warp * 8 + (lane & 7);
-    uint32_t m = 0;
+  for (int i = 0; i < 8; i++) {  // 8 rows further: 1024 bytes, the same permutation
+    const unsigned char* from = tile + dp_off(32 * h + i, c);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint4 v = *(const uint4*)(tile + dp_off(r, c + 8 * i));
-      m = absmax_nan_bf16x2(absmax_nan_bf16x2(absmax_nan_bf16x2(absmax_nan_bf16x2(m, v.x), v.y), v.z), v.w);
-    }
-    uint32_t a = max(dp_lo(m), dp_hi(m));
-    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 8));
-    a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 16));
-    if (lane < 8) amax[r] = a;
+    for (int j = 0; j < 4; j++) w[8 * j + i] = *(const uint32_t*)(from + 1024 * j);
   }
-}
-
-template <int FMT>
-__device__ __forceinline__ void dp_rows(const DispatchParams& p, const unsigned char* tile, int64_t r0, int64_t c0,
-                                        const float* scale, const uint32_t* amax) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = (lane >> 3) * 32;
-  const bool wide = (p.cols & 31) == 0 && ((uintptr_t)p.q & 31) == 0;
-  if (c0 + c >= p.cols) return;
 #pragma unroll
-  for (int pass = 0; pass < 2; pass++) {
-    const int r = pass * 64 + warp * 8 + (lane & 7);
-    if (r0 + r >= p.rows) break;
-    const float s = scale[r];
-    uint32_t d[8];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint4 v = *(const uint4*)(tile + dp_off(r, c + 8 * i));
-      d[2 * i] = dp_codes<FMT>(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y), s);
-      d[2 * i + 1] = dp_codes<FMT>(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w), s);
-    }
-    if (amax[r] > 0x7F800000u) {  // a NaN in the group
-#pragma unroll
-      for (int i = 0; i < 8; i++) d[i] = canon_nan4<FMT>(d[i]);
-    }
-    dp_store(p.q + (r0 + r) * p.cols + c0 + c, d, wide, p.cols - c0 - c);
-  }
-}
-
-// Column groups: a thread takes a column pair over 32 rows; quarters[h] holds
-// the packed maxima of rows [32 h, 32 h + 32).
-__device__ __forceinline__ void dp_col_max(const unsigned char* tile, uint32_t (*quarters)[64]) {
-  const int pair = threadIdx.x & 63, h = threadIdx.x >> 6;
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 32; i++) m = absmax_nan_bf16x2(m, *(const uint32_t*)(tile + dp_off(32 * h + i, 2 * pair)));
+  for (int i = 0; i < 32; i++) m = absmax_nan_bf16x2(m, w[i]);
   quarters[h][pair] = m;
-}
-
-template <int FMT>
-__device__ __forceinline__ void dp_cols(const DispatchParams& p, const unsigned char* tile, int64_t r0, int64_t c0,
-                                        const float* scale, const uint32_t* amax) {
-  const int pair = threadIdx.x & 63, h = threadIdx.x >> 6, c = 2 * pair;
-  const int64_t r = r0 + 32 * h;
-  if (c0 + c >= p.cols || r >= p.rows) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; k++) m = absmax_nan_bf16x2(m, quarters[k][pair]);
+  if (tid < kDpTile) {
+    // column c + h: the pairs' even columns by the first 64 threads, the odd by the next
+    const float s = dp_scale<FMT>(h ? dp_hi(m) : dp_lo(m), p.pow2);
+    scale[c + h] = s;
+    if (c + h < nc) p.s_t[(c0 + c + h) * p.tiles_r + r0 / kDpTile] = __frcp_rn(s);
+  }
+  __syncthreads();
+  const int left = nr - 32 * h;
+  if (c >= nc || left <= 0) return;
   const bool wide = (p.rows & 31) == 0 && ((uintptr_t)p.q_t & 31) == 0;
   const float s0 = scale[c], s1 = scale[c + 1];
   uint32_t d0[8], d1[8];
 #pragma unroll
   for (int k = 0; k < 8; k++) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) w[i] = *(const uint32_t*)(tile + dp_off(32 * h + 4 * k + i, c));
-    d0[k] = dp_codes<FMT>(bf16_lo(w[0]), bf16_lo(w[1]), bf16_lo(w[2]), bf16_lo(w[3]), s0);
-    d1[k] = dp_codes<FMT>(bf16_hi(w[0]), bf16_hi(w[1]), bf16_hi(w[2]), bf16_hi(w[3]), s1);
+    d0[k] = dp_codes<FMT>(bf16_lo(w[4 * k]), bf16_lo(w[4 * k + 1]), bf16_lo(w[4 * k + 2]), bf16_lo(w[4 * k + 3]), s0);
+    d1[k] = dp_codes<FMT>(bf16_hi(w[4 * k]), bf16_hi(w[4 * k + 1]), bf16_hi(w[4 * k + 2]), bf16_hi(w[4 * k + 3]), s1);
   }
-  if (max(amax[c], amax[c + 1]) > 0x7F800000u) {
+  if (max(dp_lo(m), dp_hi(m)) > 0x7F800000u) {  // a NaN in a group
 #pragma unroll
     for (int k = 0; k < 8; k++) {
       d0[k] = canon_nan4<FMT>(d0[k]);
       d1[k] = canon_nan4<FMT>(d1[k]);
     }
   }
-  uint8_t* at = p.q_t + (c0 + c) * p.rows + r;
-  dp_store(at, d0, wide, p.rows - r);
-  dp_store(at + p.rows, d1, wide, p.rows - r);
+  uint8_t* at = p.q_t + (c0 + c) * p.rows + r0 + 32 * h;
+  dp_store(at, d0, wide, left);
+  dp_store(at + p.rows, d1, wide, left);
 }
 
 template <int FMT, int DIR>
-__global__ void __launch_bounds__(kDpThreads) dispatch_kernel(DispatchParams p) {
-  __shared__ __align__(1024) unsigned char tile[2 * kDpBoxBytes];
+__global__ void __launch_bounds__(kDpThreads, 3) dispatch_kernel(DispatchParams p) {
+  extern __shared__ __align__(128) unsigned char tiles[];  // two
   __shared__ uint32_t quarters[4][64];
-  __shared__ uint32_t amax[2 * kDpTile];  // of the rows, of the columns
-  __shared__ float scale[2 * kDpTile];
-  __shared__ int token[kDpTile];
-  const int tid = threadIdx.x;
-  const int64_t r0 = (int64_t)blockIdx.x * kDpTile, c0 = (int64_t)blockIdx.y * kDpTile;
+  __shared__ float scale[kDpTile];
+  const int part = threadIdx.x & 15, r = threadIdx.x >> 4;  // 16 lanes fetch one row's 256 bytes
+  const int64_t r0 = (int64_t)blockIdx.x * kDpTile;
+  const int tc0 = blockIdx.y * p.run, tc1 = min(tc0 + p.run, p.tiles_c);
   pdl_wait();
-  if (tid < kDpTile) {  // -1: padding
-    const int s = r0 + tid < p.rows ? __ldg(p.src + r0 + tid) : -1;
-    token[tid] = s >= 0 && s < p.slots ? s / p.top_k : -1;
-  }
-  __syncthreads();
-  {
-    const int part = tid & 15;  // 16 lanes fetch one row's 256 bytes
-    const uint16_t* from = p.x + c0 + part * 8;
-    const bool column = c0 + part * 8 < p.cols;
+  const int nr = (int)min((int64_t)kDpTile, p.rows - r0);
+  const uint16_t* from[8];  // the rows' values of this lane's column; padding: size 0
+  uint32_t there = 0;
 #pragma unroll
-    for (int i = 0; i < kDpTile / 16; i++) {
-      const int r = i * 16 + (tid >> 4), t = token[r];
-      const bool there = t >= 0 && column;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(tile + dp_off(r, part * 8))),
-                   "l"(there ? from + (int64_t)t * p.cols : p.x), "r"(there ? 16 : 0)
+  for (int i = 0; i < 8; i++) {
+    const int s = r + 16 * i < nr ? __ldg(p.src + r0 + r + 16 * i) : -1;
+    const bool real = s >= 0 && s < p.slots;
+    from[i] = p.x + (real ? (int64_t)(s / p.top_k) * p.cols + (int64_t)tc0 * kDpTile + part * 8 : 0);
+    there |= (uint32_t)real << i;
+  }
+  const uint32_t to = smem_u32(tiles) + dp_off(r, part * 8);
+  const auto load = [&](int tc) {
+    const bool column = (int64_t)tc * kDpTile + part * 8 < p.cols;
+    const uint32_t dst = to + ((tc - tc0) & 1) * kDpTileBytes;
+    const int ahead = column ? (tc - tc0) * kDpTile : 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const bool real = column && (there >> i & 1);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + 2048 * i), "l"(from[i] + (real ? ahead : 0)),
+                   "r"(real ? 16 : 0)
                    : "memory");
     }
+  };
+  load(tc0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  for (int tc = tc0; tc < tc1; tc++) {
+    if (tc + 1 < tc1) load(tc + 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const unsigned char* tile = tiles + ((tc - tc0) & 1) * kDpTileBytes;
+    const int nc = (int)min((int64_t)kDpTile, p.cols - (int64_t)tc * kDpTile);
+    if constexpr (DIR & MXFP8_ROW) dp_rows<FMT>(p, tile, r0, tc, nr, nc);
+    if constexpr (DIR & MXFP8_COL) dp_cols<FMT>(p, tile, r0, tc, nr, nc, quarters, scale);
+    __syncthreads();  // the tile's place is loaded into next
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-  if constexpr (DIR & MXFP8_ROW) dp_row_max<FMT>(tile, amax);
-  if constexpr (DIR & MXFP8_COL) dp_col_max(tile, quarters);
-  __syncthreads();
-  // one group a thread
-  const int g = tid & (kDpTile - 1);
-  if (tid < kDpTile) {
-    if constexpr (DIR & MXFP8_ROW) {
-      const float s = dp_scale<FMT>(amax[g], p.pow2);
-      scale[g] = s;
-      if (r0 + g < p.rows) p.s[(r0 + g) * p.tiles_c + blockIdx.y] = __frcp_rn(s);
-    }
-  } else if constexpr (DIR & MXFP8_COL) {
-    uint32_t m = quarters[0][g >> 1];
-#pragma unroll
-    for (int h = 1; h < 4; h++) m = absmax_nan_bf16x2(m, quarters[h][g >> 1]);
-    const uint32_t a = g & 1 ? dp_hi(m) : dp_lo(m);
-    const float s = dp_scale<FMT>(a, p.pow2);
-    amax[kDpTile + g] = a;
-    scale[kDpTile + g] = s;
-    if (c0 + g < p.cols) p.s_t[(c0 + g) * p.tiles_r + blockIdx.x] = __frcp_rn(s);
-  }
-  __syncthreads();
-  if constexpr (DIR & MXFP8_ROW) dp_rows<FMT>(p, tile, r0, c0, scale, amax);
-  if constexpr (DIR & MXFP8_COL) dp_cols<FMT>(p, tile, r0, c0, scale + kDpTile, amax + kDpTile);
   pdl_launch_dependents();
+}
+
+template <int FMT, int DIR>
+static fp8q_status launch_dispatch_d(DispatchParams p, cudaStream_t s) {
+  static const cudaError_t attr = cudaFuncSetAttribute(dispatch_kernel<FMT, DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       2 * kDpTileBytes);
+  if (attr != cudaSuccess) return cuda_fail(attr, "dispatch shared memory");
+  // Runs as long as leave every SM 12 CTAs, at most 16 tiles.  65536 rows of
+  // 7168, both copies: 311 us; runs of one tile 409, of a whole row 346.
+  const int64_t tiles = (int64_t)p.tiles_r * p.tiles_c, ctas = (int64_t)sm_count() * 12;
+  p.run = (int)(tiles / ctas < 1 ? 1 : tiles / ctas > 16 ? 16 : tiles / ctas);
+  const dim3 grid((unsigned)p.tiles_r, (unsigned)((p.tiles_c + p.run - 1) / p.run));
+  const cudaError_t e = launch_kernel(dispatch_kernel<FMT, DIR>, grid, dim3(kDpThreads), 2 * kDpTileBytes, s, p);
+  if (e != cudaSuccess) return cuda_fail(e, "dispatch kernel launch");
+  return check_launch("dispatch kernel");
 }
 
 template <int FMT>
 static fp8q_status launch_dispatch_f(const DispatchParams& p, int dir, cudaStream_t s) {
-  const dim3 grid((unsigned)p.tiles_r, (unsigned)p.tiles_c);
-  const auto kernel = dir == MXFP8_ROW   ? dispatch_kernel<FMT, MXFP8_ROW>
-                      : dir == MXFP8_COL ? dispatch_kernel<FMT, MXFP8_COL>
-                                         : dispatch_kernel<FMT, MXFP8_BOTH>;
-  const cudaError_t e = launch_kernel(kernel, grid, dim3(kDpThreads), 0, s, p);
-  if (e != cudaSuccess) return cuda_fail(e, "dispatch kernel launch");
-  return check_launch("dispatch kernel");
+  if (dir == MXFP8_ROW) return launch_dispatch_d<FMT, MXFP8_ROW>(p, s);
+  if (dir == MXFP8_COL) return launch_dispatch_d<FMT, MXFP8_COL>(p, s);
+  return launch_dispatch_d<FMT, MXFP8_BOTH>(p, s);
 }
 
 static void plan_pieces(int64_t slots, int64_t* piece, int* pieces) {
@@ -471,8 +492,8 @@ extern "C" fp8q_status fp8q_moe_dispatch(const void* x, int32_t dt, int64_t toke
   DispatchParams p{};
   p.rows = rows;
   p.cols = cols;
-  p.tiles_r = (rows + kDpTile - 1) / kDpTile;
-  p.tiles_c = (cols + kDpTile - 1) / kDpTile;
+  p.tiles_r = (int)((rows + kDpTile - 1) / kDpTile);
+  p.tiles_c = (int)((cols + kDpTile - 1) / kDpTile);
   p.pow2 = pow2_scales ? 1 : 0;
   p.q = q;
   p.s = scale_inv;
