@@ -234,9 +234,81 @@ __device__ __forceinline__ void mm_store_row(const MmParams& p, int64_t row, int
   }
 }
 
-// COLSCALE: B has a scale for each of its rows
+// Adds a tile's sums over the CTAs of a cluster, in the order of their ranks,
+// and stores them.  Each CTA writes its sums into its own stages (free by
+// then; rows of 1 KB, 16-byte chunks permuted by the row) and takes a slice of
+// the columns from all of them: a warp reads whole lines of the others' shared
+// memory.  (Written there 16 bytes a row instead, 128 rows took 20 us.)
+// Called by the warps of sums; the others join its two barriers.
+template <int COLS, bool F32>
+__device__ __forceinline__ void mm_store_split(const MmParams& p, const MmTile& w, unsigned char* stages, int r, int half,
+                                               const uint64_t (&acc)[COLS / 2]) {
+  constexpr int kMost = 8;  // CTAs of a cluster
+  const uint32_t part = cluster_rank(), parts = cluster_size();
+  const int64_t there = w.row_end - w.row0;
+  const int rows = there < kMmRows ? (int)there : kMmRows;
+  if (r < rows) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 4) {
+      float4 v;
+      unpack2(acc[c / 2], v.x, v.y);
+      unpack2(acc[c / 2 + 1], v.z, v.w);
+      *(float4*)(stages + r * 1024 + ((((half * COLS + c) >> 2) ^ (r & 7)) << 4)) = v;
+    }
+  }
+  cluster_sync();
+  const int chunks = kMmCols / 4 / (int)parts;  // of a row of the slice
+  uint32_t at[kMost];
+#pragma unroll
+  for (uint32_t q = 0; q < kMost; q++) at[q] = cluster_addr(stages, q < parts ? q : 0);
+  const bool wide = p.n % 4 == 0 && ((uintptr_t)p.out & (F32 ? 15 : 7)) == 0;
+  for (int i = threadIdx.x; i < rows * chunks; i += kMmEpiWarps * 32) {
+    const int row = i / chunks, chunk = (int)part * chunks + i % chunks;
+    float4 u[kMost];
+#pragma unroll
+    for (uint32_t q = 0; q < kMost; q++)
+      if (q < parts) u[q] = ld_cluster4(at[q] + row * 1024 + ((chunk ^ (row & 7)) << 4));
+    float4 v = u[0];
+#pragma unroll
+    for (uint32_t q = 1; q < kMost; q++)
+      if (q < parts) v.x += u[q].x, v.y += u[q].y, v.z += u[q].z, v.w += u[q].w;
+    const int64_t c0 = w.n0 + 4 * chunk, o = (w.row0 + row) * p.n + c0;
+    if (c0 >= p.n) continue;
+    const float x[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (F32) {
+      float* out = (float*)p.out + o;
+      if (wide) {
+        if (p.accumulate) {
+          const float4 y = *(const float4*)out;
+          v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        }
+        *(float4*)out = v;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (c0 + k < p.n) out[k] = p.accumulate ? out[k] + x[k] : x[k];
+      }
+    } else {
+      uint16_t* out = (uint16_t*)p.out + o;
+      uint32_t d[2];
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d[0]) : "f"(x[1]), "f"(x[0]));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d[1]) : "f"(x[3]), "f"(x[2]));
+      if (wide) {
+        *(uint2*)out = make_uint2(d[0], d[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (c0 + k < p.n) out[k] = (uint16_t)(d[k >> 1] >> (16 * (k & 1)));
+      }
+    }
+  }
+  cluster_sync();  // no CTA leaves while another reads from it
+}
+
+// SPLIT: the CTAs of a cluster share one tile's blocks of K and add their sums
+// at the end.  COLSCALE: B has a scale for each of its rows
 // (1x128 groups), else one for each 128 of them.
-template <int CG, bool COLSCALE, bool F32, int MODE>
+template <int CG, bool SPLIT, bool COLSCALE, bool F32, int MODE>
 __global__ void __launch_bounds__(kMmThreads, 1)
     matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, MmParams p) {
   using S = MmShape<CG>;
@@ -285,10 +357,21 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   if constexpr (CG == 2) cluster_sync();  // the leader's barriers, before the other CTA uses them
   tc_fence_after();
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  const uint32_t tile0 = blockIdx.x / CG, tile_step = gridDim.x / CG;
+  const uint32_t tile0 = blockIdx.x / (SPLIT ? cluster_size() : CG);
+  const uint32_t tile_step = SPLIT ? 0x40000000u : gridDim.x / CG;  // a split has one tile a cluster
   const uint32_t tmem = tmem_base;
 
   uint32_t tiles;
+  const auto tile_of = [&](uint32_t t) {
+    MmTile w = mm_tile<CG, MODE>(p, first, t);
+    if constexpr (SPLIT) {  // this CTA's share of the blocks
+      const uint32_t part = cluster_rank(), parts = cluster_size(), n = (uint32_t)w.nkb;
+      const uint32_t kb0 = n * part / parts;
+      w.k0 += (int64_t)kb0 * kMmBlock;
+      w.nkb = (int)(n * (part + 1) / parts - kb0);
+    }
+    return w;
+  };
   if constexpr (MODE == kMmRowGroups) {
     mm_scan_groups<S::kTileRows>(p, first, sums);
     tiles = first[p.groups] * (uint32_t)p.tiles_n;
@@ -303,7 +386,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     if (elect_one()) {
       uint32_t it = 0;  // blocks of K issued
       for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
-        const MmTile w = mm_tile<CG, MODE>(p, first, t);
+        const MmTile w = tile_of(t);
         const int arow = (int)w.row0 + rank * kMmRows;
         const int brow = (int)(w.n0 + (MODE == kMmRowGroups ? (int64_t)w.g * p.n : 0)) + rank * (kMmCols / CG);
         int at = (int)w.k0;
@@ -344,7 +427,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     if (rank == 0 && elect_one()) {
       uint32_t it = 0;
       for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
-        const MmTile w = mm_tile<CG, MODE>(p, first, t);
+        const MmTile w = tile_of(t);
         for (int kb = 0; kb < w.nkb; kb++, it++) {
           const uint32_t s = it % S::kStages, round = it / S::kStages, b = it & 1u, use = it >> 1;
           if (!mm_wait(&full[s], round & 1u, kMmPolls) || (use > 0 && !mm_wait(&taken[b], (use - 1) & 1u, kMmPolls))) {
@@ -391,7 +474,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint32_t it = 0;
     bool ok = true;
     for (uint32_t t = tile0; t < tiles && ok; t += tile_step) {
-      const MmTile w = mm_tile<CG, MODE>(p, first, t);
+      const MmTile w = tile_of(t);
       if (w.nkb == 0) continue;
       const int64_t kb0 = w.k0 / kMmBlock;
       for (int64_t q = kb0 >> 2; q <= (kb0 + w.nkb - 1) >> 2; q++, it++) {
@@ -467,7 +550,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     for (uint32_t t = tile0; t < tiles && !__any_sync(0xFFFFFFFFu, dead); t += tile_step) {
       int nkb;
       {
-        const MmTile w = mm_tile<CG, MODE>(p, first, t);
+        const MmTile w = tile_of(t);
         nkb = w.nkb;
         kq = (int)(w.k0 / kMmBlock) & 3;
       }
@@ -520,12 +603,19 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       // the tile again, rather than its values kept through the loop
       uint32_t t2 = t;
       asm volatile("" : "+r"(t2));
-      const MmTile w = mm_tile<CG, MODE>(p, first, t2);
+      const MmTile w = tile_of(t2);
       const int64_t row = w.row0 + rank * kMmRows + quarter * 32 + lane;
-      if (row < w.row_end)
+      if constexpr (SPLIT)
+        mm_store_split<COLS, F32>(p, w, stages, quarter * 32 + lane, half, acc);
+      else if (row < w.row_end)
         mm_store_row<COLS, F32>(p, (MODE == kMmKGroups ? (int64_t)w.g * p.m : 0) + row, w.n0 + half * COLS, acc);
     }
     pdl_launch_dependents();
+  }
+  if (SPLIT && warp >= kMmEpiWarps && tile0 < tiles) {  // the barriers of mm_store_split
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
   }
   tc_fence_before();
   __syncthreads();
@@ -569,8 +659,42 @@ static fp8q_status mm_map(CUtensorMap* map, const void* q, int64_t rows, int64_t
   return r == CUDA_SUCCESS ? FP8Q_OK : fail(FP8Q_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
 }
 
-template <int CG, bool COLSCALE, bool F32, int MODE>
-static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt_a, int fmt_b, cudaStream_t s) {
+template <int CG, int MODE>
+static size_t mm_smem(int groups) {
+  return 1024 + (size_t)MmShape<CG>::kStages * MmShape<CG>::kStageBytes + (MODE == kMmRowGroups ? 4 * ((size_t)groups + 1) : 0);
+}
+
+// Clusters of `size` CTAs of a kernel that the GPU holds at a time (a GB300: 76
+// of 2, 36 of 4, 15 of 8, since a cluster stays inside one part of the chip).
+template <int CG, bool SPLIT, bool COLSCALE, bool F32, int MODE>
+static int mm_clusters(int size) {
+  static int found[9];
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (found[size] == 0) {
+    const auto kernel = matmul_kernel<CG, SPLIT, COLSCALE, F32, MODE>;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = size;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(sm_count() / size * size));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = mm_smem<CG, MODE>(MODE == kMmRowGroups ? FP8Q_MAX_GROUPS : 1);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    found[size] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) ==
+                              cudaSuccess &&
+                          cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0
+                      ? n
+                      : 1;
+  }
+  return found[size];
+}
+
+template <int CG, bool SPLIT, bool COLSCALE, bool F32, int MODE>
+static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt_a, int fmt_b, int parts, cudaStream_t s) {
   using S = MmShape<CG>;
   CUtensorMap ma, mb;
   fp8q_status r = mm_map(&ma, a, p.m, p.k, kMmRows);
@@ -578,11 +702,10 @@ static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt
   if ((r = mm_map(&mb, b, MODE == kMmRowGroups ? p.n * p.groups : p.n, p.k, kMmCols / CG)) != FP8Q_OK) return r;
   p.idesc = instr_desc_f8(fmt_a, fmt_b, S::kTileRows, kMmCols);
   p.tiles_n = (int)((p.n + kMmCols - 1) / kMmCols);
-  const size_t smem = 1024 + (size_t)S::kStages * S::kStageBytes + (MODE == kMmRowGroups ? 4 * ((size_t)p.groups + 1) : 0);
-  const auto kernel = matmul_kernel<CG, COLSCALE, F32, MODE>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      (int)(1024 + S::kStages * S::kStageBytes + (MODE == kMmRowGroups ? 4 * (FP8Q_MAX_GROUPS + 1) : 0)));
+  const size_t smem = mm_smem<CG, MODE>(p.groups);
+  const auto kernel = matmul_kernel<CG, SPLIT, COLSCALE, F32, MODE>;
+  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (int)mm_smem<CG, MODE>(FP8Q_MAX_GROUPS));
   if (attr != cudaSuccess) return cuda_fail(attr, "matmul shared memory");
   // the kernel moves registers between its warpgroups: they must be there
   static const int regs = [&] {
@@ -593,38 +716,39 @@ static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt
   const int64_t per = (p.m + S::kTileRows - 1) / S::kTileRows;
   const int64_t tiles = (MODE == kMmRowGroups ? per + p.groups : MODE == kMmKGroups ? per * p.groups : per) * p.tiles_n;
   if (tiles > INT32_MAX) return fail(FP8Q_ERR_UNSUPPORTED, "product too large: %lld output tiles", (long long)tiles);
-  // pairs that fit at a time: a persistent grid must not leave any for later
-  static const int pairs = [&] {
-    if (CG == 1) return 0;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CG;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)sm_count());
-    cfg.blockDim = dim3(kMmThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0 ? n : sm_count() / CG;
-  }();
-  int64_t grid = CG == 1 ? sm_count() : pairs;
-  if (grid > tiles) grid = tiles;
-  const cudaError_t e = launch_cluster(kernel, dim3((unsigned)grid * CG), dim3(kMmThreads), CG, smem, s, ma, mb, p);
+  // a persistent grid leaves no pair for later, a split no cluster
+  int64_t grid = CG == 1 ? sm_count() : mm_clusters<CG, SPLIT, COLSCALE, F32, MODE>(CG);
+  if (SPLIT || grid > tiles) grid = tiles;
+  const unsigned cluster = SPLIT ? parts : CG;
+  const cudaError_t e = launch_cluster(kernel, dim3((unsigned)grid * cluster), dim3(kMmThreads), cluster, smem, s, ma, mb, p);
   if (e != cudaSuccess) return cuda_fail(e, "matmul kernel launch");
   return check_launch("matmul kernel");
+}
+
+// Which form.  A split over K where every tile can have a cluster of 2, 4 or 8
+// CTAs at once and each CTA two blocks of K: few rows.  (1 x 4096 x 4096: 20.1
+// us unsplit, 14.5 by 2, 10.0 by 4; 8, of which only 15 run at a time, 15.1.)
+// Pairs where a tile's 256 rows are there (row groups: on average).  Else
+// single CTAs.
+template <bool COLSCALE, bool F32, int MODE>
+static fp8q_status launch_mm_form(const void* a, const void* b, const MmParams& p, int fmt_a, int fmt_b, cudaStream_t s) {
+  if constexpr (MODE != kMmKGroups) {
+    const int64_t cols = (p.n + kMmCols - 1) / kMmCols, rows = (p.m + kMmRows - 1) / kMmRows;
+    const int64_t tiles = (MODE == kMmRowGroups ? rows + p.groups : rows) * cols, kb = (p.k + kMmBlock - 1) / kMmBlock;
+    int parts = 1;
+    while (parts < 8 && kb >= parts * 4 && tiles <= mm_clusters<1, true, COLSCALE, F32, MODE>(parts * 2)) parts *= 2;
+    if (parts > 1) return launch_mm_t<1, true, COLSCALE, F32, MODE>(a, b, p, fmt_a, fmt_b, parts, s);
+  }
+  if ((MODE == kMmRowGroups ? p.m / p.groups : p.m) > kMmRows)
+    return launch_mm_t<2, false, COLSCALE, F32, MODE>(a, b, p, fmt_a, fmt_b, 1, s);
+  return launch_mm_t<1, false, COLSCALE, F32, MODE>(a, b, p, fmt_a, fmt_b, 1, s);
 }
 
 template <bool COLSCALE, int MODE>
 static fp8q_status launch_mm_out(const void* a, const void* b, const MmParams& p, int fmt_a, int fmt_b, int out_dt,
                                  cudaStream_t s) {
-  const int64_t rows = MODE == kMmRowGroups ? p.m / p.groups : p.m;
-  if (rows > kMmRows)
-    return out_dt == FP8Q_OUT_FP32 ? launch_mm_t<2, COLSCALE, true, MODE>(a, b, p, fmt_a, fmt_b, s)
-                                   : launch_mm_t<2, COLSCALE, false, MODE>(a, b, p, fmt_a, fmt_b, s);
-  return out_dt == FP8Q_OUT_FP32 ? launch_mm_t<1, COLSCALE, true, MODE>(a, b, p, fmt_a, fmt_b, s)
-                                 : launch_mm_t<1, COLSCALE, false, MODE>(a, b, p, fmt_a, fmt_b, s);
+  return out_dt == FP8Q_OUT_FP32 ? launch_mm_form<COLSCALE, true, MODE>(a, b, p, fmt_a, fmt_b, s)
+                                 : launch_mm_form<COLSCALE, false, MODE>(a, b, p, fmt_a, fmt_b, s);
 }
 
 fp8q_status launch_matmul(const MatmulLaunch& L) {
