@@ -18,9 +18,10 @@
 //                 sum is zero and p_j / S a softmax over the chosen alone.
 // The bias and the choice have no gradient.
 //
-// One warp takes one token, expert e = lane + 32 i in register i.  A choice
-// is a maximum over the registers, one warp-wide integer maximum of the
-// order-preserving bits and one minimum of the indices that have it.
+// One warp takes one token, expert e = lane + 32 i in register i.  A choice is
+// one warp-wide integer maximum of the order-preserving bits of the lanes'
+// best and a ballot of who has it (a minimum of the indices where several do).
+// Up to 256 experts each lane sorts its keys first.
 #include "fp8q_device.cuh"
 #include "internal.h"
 
@@ -126,73 +127,126 @@ __device__ __forceinline__ void rt_keep_groups(uint32_t* keys, const RtParams& p
   __syncwarp();
 }
 
-template <int DT, bool SOFTMAX, int V>
+// The order-preserving bits of +inf and of -inf, and what stands for a NaN.
+constexpr uint32_t kRtInf = 0xFF800000u, kRtNan = 0xFFFFFFFFu, kRtNone = 0x007FFFFFu;
+
+// BYLOGIT: no bias and no groups, so the logits are the keys.
+template <int DT, bool SOFTMAX, bool BYLOGIT, int V>
 __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
   extern __shared__ uint32_t rt_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* sh = rt_smem + warp * (V * 33);
+  const float none = __uint_as_float(0xFF800000u);
   pdl_wait();
-  const bool by_logit = p.bias == nullptr && p.groups == 1;
   for (int64_t t = (int64_t)blockIdx.x * kRtWarps + warp; t < p.tokens; t += (int64_t)gridDim.x * kRtWarps) {
     float x[V];
-    bool nan = false;
 #pragma unroll
     for (int i = 0; i < V; i++) {
       const int e = lane + 32 * i;
-      x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : __uint_as_float(0xFF800000u);
-      nan |= x[i] != x[i] || (SOFTMAX && x[i] == __uint_as_float(0x7F800000u));
+      x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : none;
     }
-    nan = __any_sync(kFull, nan);
-    float most = __uint_as_float(0xFF800000u), sum = 1.0f;
-    if constexpr (SOFTMAX) {
-#pragma unroll
-      for (int i = 0; i < V; i++) most = fmaxf(most, x[i]);
-      most = rt_warp_max(most);
-      if (!by_logit || !p.renorm) {
-        sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; i++) sum += x[i] == x[i] ? expf(x[i] - most) : 0.0f;
-        sum = rt_warp_sum(sum);
-      }
-    }
-    const auto score = [&](float v) { return SOFTMAX ? __fdiv_rn(expf(v - most), sum) : rt_sigmoid(v); };
     uint32_t key[V];
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int e = lane + 32 * i;
-      float k = x[i];
-      if (!by_logit) {
-        k = score(x[i]);
-        if (p.bias != nullptr && e < p.experts) k = __fadd_rn(k, __ldg(p.bias + e));
+    for (int i = 0; i < V; i++) key[i] = x[i] == x[i] ? rt_order(x[i]) : kRtNan;
+    // the largest key tells of a NaN or (under softmax) an infinity
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < V; i++) top = max(top, key[i]);
+    top = __reduce_max_sync(kFull, top);
+    const bool poison = SOFTMAX ? top >= kRtInf : top == kRtNan;
+    if (top == kRtNan) {  // the maximum of the others
+      top = 0;
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        if (key[i] == kRtNan) key[i] = 0;
+        top = max(top, key[i]);
       }
-      const float none = __uint_as_float(0xFF800000u);
-      key[i] = x[i] > none && k > none ? rt_order(k) : 0u;
+      top = __reduce_max_sync(kFull, top);
     }
-    if (p.groups > 1) {
+    const float most = top ? rt_value(top) : none;
+    float sum = 1.0f;
+    if (SOFTMAX && !(BYLOGIT && p.renorm)) {
+      sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; i++) sh[lane + 33 * i] = key[i];
-      __syncwarp();
-      rt_keep_groups(sh, p, lane);
+      for (int i = 0; i < V; i++) sum += x[i] == x[i] ? expf(x[i] - most) : 0.0f;
+      sum = rt_warp_sum(sum);
+    }
+    const auto score = [&](float v) { return SOFTMAX ? __fdiv_rn(expf(v - most), sum) : rt_sigmoid(v); };
+    if constexpr (!BYLOGIT) {
 #pragma unroll
-      for (int i = 0; i < V; i++) key[i] = sh[lane + 33 * i];
-      __syncwarp();
+      for (int i = 0; i < V; i++) {
+        const int e = lane + 32 * i;
+        float k = score(x[i]);
+        if (p.bias != nullptr && e < p.experts) k = __fadd_rn(k, __ldg(p.bias + e));
+        key[i] = x[i] > none && k > none ? rt_order(k) : 0u;
+      }
+      if (p.groups > 1) {
+#pragma unroll
+        for (int i = 0; i < V; i++) sh[lane + 33 * i] = key[i];
+        __syncwarp();
+        rt_keep_groups(sh, p, lane);
+#pragma unroll
+        for (int i = 0; i < V; i++) key[i] = sh[lane + 33 * i];
+        __syncwarp();
+      }
+    }
+    // Each lane's best first, so that a choice is one maximum of the heads and
+    // one shift of the chosen lane's queue.  Equal keys keep their order.
+    uint32_t place = 0x76543210u;  // register of each queue entry, 4 bits each
+    if constexpr (V <= 8 && V > 1) {
+      uint32_t at[V];
+#pragma unroll
+      for (int i = 0; i < V; i++) at[i] = i;
+#pragma unroll
+      for (int n = V - 1; n > 0; n--)
+#pragma unroll
+        for (int i = 0; i < n; i++) {
+          const bool swap = key[i + 1] > key[i];
+          const uint32_t k0 = max(key[i], key[i + 1]), k1 = min(key[i], key[i + 1]);
+          const uint32_t a0 = swap ? at[i + 1] : at[i], a1 = swap ? at[i] : at[i + 1];
+          key[i] = k0, key[i + 1] = k1, at[i] = a0, at[i + 1] = a1;
+        }
+      place = 0;
+#pragma unroll
+      for (int i = 0; i < V; i++) place |= at[i] << (4 * i);
     }
     int id = -1;
     for (int j = 0; j < p.top_k; j++) {
       uint32_t best = 0;
       int at = 0;
+      if constexpr (V <= 8) {
+        best = key[0];
+        at = place & 15;
+      } else {
 #pragma unroll
-      for (int i = 0; i < V; i++)
-        if (key[i] > best) {
-          best = key[i];
-          at = i;
+        for (int i = 0; i < V; i++)
+          if (key[i] > best) {
+            best = key[i];
+            at = i;
+          }
+      }
+      const uint32_t chosen = j == 0 && BYLOGIT ? top : __reduce_max_sync(kFull, best);
+      if (chosen <= kRtNone) break;
+      unsigned who = __ballot_sync(kFull, best == chosen);
+      int e;
+      if ((who & (who - 1)) == 0) {  // one lane has it
+        e = __shfl_sync(kFull, lane + 32 * at, __ffs(who) - 1);
+      } else {
+        e = (int)__reduce_min_sync(kFull, best == chosen ? (unsigned)(lane + 32 * at) : 0xFFFFFFFFu);
+        who = 1u << (e & 31);
+      }
+      if (lane == __ffs(who) - 1) {
+        if constexpr (V <= 8) {
+#pragma unroll
+          for (int i = 0; i + 1 < V; i++) key[i] = key[i + 1];
+          key[V - 1] = 0;
+          place >>= 4;
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; i++)
+            if (i == at) key[i] = 0;
         }
-      const uint32_t top = __reduce_max_sync(kFull, best);
-      if (top == 0) break;
-      const int e = (int)__reduce_min_sync(kFull, best == top ? (unsigned)(lane + 32 * at) : 0xFFFFFFFFu);
-#pragma unroll
-      for (int i = 0; i < V; i++)
-        if (e == lane + 32 * i) key[i] = 0;
+      }
       if (lane == j) id = e;
     }
     float w = 0.0f;
@@ -202,7 +256,7 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
       w = s > 0.0f ? __fdiv_rn(w, s) : s == 0.0f ? 0.0f : s;
     }
     w = __fmul_rn(w, p.weight_scale);
-    if (nan) w = __uint_as_float(0x7FC00000u);
+    if (poison) w = __uint_as_float(0x7FC00000u);
     if (lane < p.top_k) {
       p.weights[t * p.top_k + lane] = w;
       p.ids[t * p.top_k + lane] = id;
@@ -211,85 +265,134 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
   pdl_launch_dependents();
 }
 
-template <int DT, bool SOFTMAX, int V>
-__global__ void __launch_bounds__(kRtWarps * 32) route_backward_kernel(RtParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// The gradient where it reaches the chosen experts alone (sigmoid scores, or
+// renormalised softmax): L = 8, 16 or 32 lanes take a token, a slot each, after
+// the warp has cleared its tokens' rows.
+template <int DT, bool SOFTMAX, int L>
+__global__ void __launch_bounds__(kRtWarps * 32) route_backward_chosen_kernel(RtParams p) {
+  constexpr int N = 32 / L;  // tokens of a warp
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % L;
+  const auto total = [](float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+  };
   pdl_wait();
-  for (int64_t t = (int64_t)blockIdx.x * kRtWarps + warp; t < p.tokens; t += (int64_t)gridDim.x * kRtWarps) {
+  for (int64_t t0 = ((int64_t)blockIdx.x * kRtWarps + warp) * N; t0 < p.tokens; t0 += (int64_t)gridDim.x * kRtWarps * N) {
+    const int64_t t = t0 + lane / L;
     int id = -1;
-    float d = 0.0f, xj = __uint_as_float(0xFF800000u);
-    if (lane < p.top_k) {
-      id = __ldg(p.ids_in + t * p.top_k + lane);
+    float d = 0.0f, x = __uint_as_float(0xFF800000u);
+    if (t < p.tokens && j < p.top_k) {
+      id = __ldg(p.ids_in + t * p.top_k + j);
       if (id < 0 || id >= p.experts) id = -1;
       if (id >= 0) {
-        d = __ldg(p.d_weights + t * p.top_k + lane);
-        xj = rt_load<DT>(p.logits, t * p.experts + id);
+        d = __ldg(p.d_weights + t * p.top_k + j);
+        x = rt_load<DT>(p.logits, t * p.experts + id);
       }
     }
-    float s = 0.0f, g = 0.0f, dx = 0.0f, dot = 0.0f;
-    float x[V], most, sum = 1.0f;
-    if (SOFTMAX && !p.renorm) {
-      most = __uint_as_float(0xFF800000u);
-#pragma unroll
-      for (int i = 0; i < V; i++) {
-        const int e = lane + 32 * i;
-        x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : __uint_as_float(0xFF800000u);
-        most = fmaxf(most, x[i]);
-      }
-      most = rt_warp_max(most);
-      sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; i++) {
-        x[i] = most > __uint_as_float(0xFF800000u) ? expf(x[i] - most) : 0.0f;
-        sum += x[i];
-      }
-      sum = rt_warp_sum(sum);
+    // the rows' bytes, 16 at a time where they allow it
+    const int64_t size = DT == kBF16 ? 2 : 4, n = min((int64_t)N, p.tokens - t0) * p.experts;
+    char* row = (char*)p.d_logits + t0 * p.experts * size;
+    if (((uintptr_t)row & 15) == 0 && (n * size & 15) == 0) {
+      for (int64_t i = lane * 16; i < n * size; i += 512) *(uint4*)(row + i) = make_uint4(0, 0, 0, 0);
     } else {
-      most = rt_warp_max(xj);
+      for (int64_t i = lane; i < n; i += 32) rt_store<DT>(row, i, 0.0f);
     }
-    if (id >= 0) s = SOFTMAX ? __fdiv_rn(expf(xj - most), sum) : rt_sigmoid(xj);
+    float s = 0.0f, dx;
+    if constexpr (SOFTMAX) {
+      float most = x;
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+      if (id >= 0) s = expf(x - most);
+    } else if (id >= 0) {
+      s = rt_sigmoid(x);
+    }
     if (p.renorm) {
-      const float all = rt_warp_sum(s);
+      const float all = total(s);
       const float share = all != 0.0f ? __fdiv_rn(s, all) : 0.0f;
-      const float mean = rt_warp_sum(__fmul_rn(d, share));
+      const float mean = total(__fmul_rn(d, share));
       // p_j g_j (softmax) and g_j s_j (sigmoid) are both c (d_j - mean) s_j / S
-      dx = id >= 0 ? __fmul_rn(__fmul_rn(p.weight_scale, __fsub_rn(d, mean)), share) : 0.0f;
-      if (!SOFTMAX) dx = __fmul_rn(dx, __fsub_rn(1.0f, s));
+      dx = __fmul_rn(__fmul_rn(p.weight_scale, __fsub_rn(d, mean)), share);
     } else {
-      g = __fmul_rn(p.weight_scale, d);
-      if (SOFTMAX) {
-        dot = rt_warp_sum(__fmul_rn(g, s));
-        dx = __fmul_rn(s, __fsub_rn(g, dot));
-      } else {
-        dx = __fmul_rn(__fmul_rn(g, s), __fsub_rn(1.0f, s));
-      }
+      dx = __fmul_rn(__fmul_rn(p.weight_scale, d), s);
     }
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int e = lane + 32 * i;
-      const float rest = SOFTMAX && !p.renorm && sum > 0.0f ? -__fmul_rn(__fdiv_rn(x[i], sum), dot) : 0.0f;
-      if (e < p.experts) rt_store<DT>(p.d_logits, t * p.experts + e, rest);
-    }
+    if (!SOFTMAX) dx = __fmul_rn(dx, __fsub_rn(1.0f, s));
     __syncwarp();
     if (id >= 0) rt_store<DT>(p.d_logits, t * p.experts + id, dx);
   }
   pdl_launch_dependents();
 }
 
-template <int DT, bool SOFTMAX, int V>
-static fp8q_status launch_route_v(const RtParams& p, bool backward, cudaStream_t s) {
-  int64_t grid = (p.tokens + kRtWarps - 1) / kRtWarps;
+// The gradient of softmax weights that are not renormalised: every expert's.
+template <int DT, int V>
+__global__ void __launch_bounds__(kRtWarps * 32) route_backward_all_kernel(RtParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float none = __uint_as_float(0xFF800000u);
+  pdl_wait();
+  for (int64_t t = (int64_t)blockIdx.x * kRtWarps + warp; t < p.tokens; t += (int64_t)gridDim.x * kRtWarps) {
+    int id = -1;
+    float g = 0.0f, xj = none;
+    if (lane < p.top_k) {
+      id = __ldg(p.ids_in + t * p.top_k + lane);
+      if (id < 0 || id >= p.experts) id = -1;
+      if (id >= 0) {
+        g = __fmul_rn(p.weight_scale, __ldg(p.d_weights + t * p.top_k + lane));
+        xj = rt_load<DT>(p.logits, t * p.experts + id);
+      }
+    }
+    float x[V], most = none, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int e = lane + 32 * i;
+      x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : none;
+      most = fmaxf(most, x[i]);
+    }
+    most = rt_warp_max(most);
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      x[i] = most > none ? expf(x[i] - most) : 0.0f;
+      sum += x[i];
+    }
+    sum = rt_warp_sum(sum);
+    const float s = id >= 0 ? __fdiv_rn(expf(xj - most), sum) : 0.0f;
+    const float dot = rt_warp_sum(__fmul_rn(g, s));
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const int e = lane + 32 * i;
+      if (e < p.experts)
+        rt_store<DT>(p.d_logits, t * p.experts + e, most > none ? -__fmul_rn(__fdiv_rn(x[i], sum), dot) : 0.0f);
+    }
+    __syncwarp();
+    if (id >= 0) rt_store<DT>(p.d_logits, t * p.experts + id, __fmul_rn(s, __fsub_rn(g, dot)));
+  }
+  pdl_launch_dependents();
+}
+
+// One warp for each `per` tokens, at most 8 CTAs of warps an SM.
+static fp8q_status launch_rt(void (*kernel)(RtParams), const RtParams& p, int per, size_t smem, cudaStream_t s) {
+  int64_t grid = (p.tokens + per * kRtWarps - 1) / (per * kRtWarps);
   const int64_t cap = (int64_t)sm_count() * 8;
   if (grid > cap) grid = cap;
-  const auto kernel = backward ? route_backward_kernel<DT, SOFTMAX, V> : route_kernel<DT, SOFTMAX, V>;
-  const size_t smem = !backward && p.groups > 1 ? (size_t)kRtWarps * V * 33 * 4 : 0;
   const cudaError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kRtWarps * 32), smem, s, p);
   if (e != cudaSuccess) return cuda_fail(e, "route kernel launch");
   return check_launch("route kernel");
 }
 
+template <int DT, bool SOFTMAX, int V>
+static fp8q_status launch_route_v(const RtParams& p, bool backward, cudaStream_t s) {
+  if (backward) return launch_rt(route_backward_all_kernel<DT, V>, p, 1, 0, s);  // softmax only
+  if (p.bias == nullptr && p.groups == 1) return launch_rt(route_kernel<DT, SOFTMAX, true, V>, p, 1, 0, s);
+  const size_t smem = p.groups > 1 ? (size_t)kRtWarps * V * 33 * 4 : 0;
+  return launch_rt(route_kernel<DT, SOFTMAX, false, V>, p, 1, smem, s);
+}
+
 template <int DT, bool SOFTMAX>
 static fp8q_status launch_route_e(const RtParams& p, bool backward, cudaStream_t s) {
+  if (backward && (!SOFTMAX || p.renorm)) {
+    if (p.top_k <= 8) return launch_rt(route_backward_chosen_kernel<DT, SOFTMAX, 8>, p, 4, 0, s);
+    if (p.top_k <= 16) return launch_rt(route_backward_chosen_kernel<DT, SOFTMAX, 16>, p, 2, 0, s);
+    return launch_rt(route_backward_chosen_kernel<DT, SOFTMAX, 32>, p, 1, 0, s);
+  }
   if (p.experts <= 32) return launch_route_v<DT, SOFTMAX, 1>(p, backward, s);
   if (p.experts <= 64) return launch_route_v<DT, SOFTMAX, 2>(p, backward, s);
   if (p.experts <= 128) return launch_route_v<DT, SOFTMAX, 4>(p, backward, s);
