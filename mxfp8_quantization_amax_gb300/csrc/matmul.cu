@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ unsigned sums[MODE == kMmRowGroups ? 256 : 1];
   __shared__ __align__(16) float scale[kMmScaleSlots][4][NS];
-  __shared__ volatile int abort_flag;
+  __shared__ volatile int abort_flag, patience;  // the latter: tries of the sums' waits
   unsigned char* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned* first = (unsigned*)(stages + S::kStages * S::kStageBytes);
 
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       mbar_init(&sempty[i], kMmEpiWarps);
     }
     abort_flag = 0;
+    patience = (int)min(g_mm_wait_budget_ns / 1400, 2000000000ull);
     fence_barrier_init();
   }
   if (warp == kMmEpiWarps) {
@@ -411,8 +412,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
       }
       // Every issued copy lands before the CTA (the pair) can exit (fixed 2 s
-      // bound), and every block is used or the flag that ends the waits of the
-      // sums is up.
+      // bound), and every block is used or the flag that tells of a failure up.
       const uint32_t tail = it > S::kStages ? it - S::kStages : 0;
       if (rank == 0)
         for (uint32_t j = tail; j < it; j++) mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
@@ -525,14 +525,13 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint32_t r[2][32];
     bool dead = false;
     // Waits for a block of K and starts its way from tensor memory to
-    // registers.  These waits count nothing (a counter costs a spilled
-    // register, 4%): they end by the flag that the loads, the tensor core and
-    // the scales raise when a wait of theirs runs out.  The warp goes on even
-    // then, since its loads are collective; its tile loop ends, and the error
-    // word tells that the output is worthless.
+    // registers.  A failing try sleeps some 1.4 us, so a count of them bounds the
+    // wait.  After one that ran out the warp goes on without waiting, since its
+    // loads are collective; its tile loop ends, and the error word tells that
+    // the output is worthless.
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      while (!mbar_try_wait(bar, parity))
-        if (abort_flag) {
+      for (int n = 0; !mbar_try_wait(bar, parity); n++)
+        if (n >= patience || abort_flag) {
           dead = true;
           break;
         }
@@ -609,6 +608,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         mm_store_split<COLS, F32>(p, w, stages, quarter * 32 + lane, half, acc);
       else if (row < w.row_end)
         mm_store_row<COLS, F32>(p, (MODE == kMmKGroups ? (int64_t)w.g * p.m : 0) + row, w.n0 + half * COLS, acc);
+    }
+    if (dead) {
+      atomicOr(&g_mm_error, 1u);
+      abort_flag = 1;
     }
     pdl_launch_dependents();
   }
