@@ -7,8 +7,9 @@
  *     a saturating round-to-nearest-even cast to E4M3 or E5M2;
  *   - MXFP8: 1x32 blocks with one E8M0 scale each (exponent rounded up),
  *     rowwise and columnwise (transposed), optionally per ragged group;
- * and the steps around it: dequantization, blockwise FP8, NVFP4, and the
- * SQNR / zero-rate statistics of a quantized copy.
+ * and the steps around it: dequantization, blockwise FP8, NVFP4, the
+ * SQNR / zero-rate statistics of a quantized copy, the products of blockwise
+ * copies, and the expert layer that feeds and joins them.
  *
  * Conventions for every entry point:
  *   - Pointers documented as "device" are CUDA device pointers owned by the
@@ -100,8 +101,8 @@ FP8Q_API const char* fp8q_last_error_string(void);
 /*
  * Synchronizes `stream`, then reports and clears device-side failures that
  * earlier calls on this device recorded: FP8Q_ERR_TIMEOUT when a bounded
- * wait inside a kernel (the shared-memory barriers of the MXFP8 and the
- * blockwise pipelines, the grid-wide wait for the scale in the single-launch
+ * wait inside a kernel (the shared-memory barriers of the MXFP8, the
+ * blockwise and the products' pipelines, the grid-wide wait for the scale in the single-launch
  * current scaling) gave up, in which case that call's outputs are
  * incomplete.  FP8Q_OK otherwise.
  */

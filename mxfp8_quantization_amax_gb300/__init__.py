@@ -1,4 +1,5 @@
-"""Python binding of libfp8q: FP8 / MXFP8 quantization kernels for GB300.
+"""Python binding of libfp8q: FP8 / MXFP8 quantization kernels for GB300, the
+products of blockwise FP8 tensors, and the expert layer around them.
 
 Thin ctypes marshalling over the C ABI declared in include/fp8q.h: every
 function takes torch CUDA tensors, checks shapes and dtypes, allocates the
