@@ -8,7 +8,26 @@
 // with A and B the 8-bit codes (both K-major, as fp8q_quantize_blockwise
 // leaves them) and sa, sb their scale_inv ("混合精度与 FP8 训练" 10.2-10.5).
 // The scales change every 128 values of K, so the tensor core sums one block
-// at a time and the sum over blocks is taken in FP32 registers.
+// at a time into tensor memory (exact products, FP32 sums), and warps of sums
+// read each block back, scale it and add it in FP32 registers.
+//
+// A tile is 256 rows x 256 columns over a pair of CTAs (or 128 x 256 over one):
+// the widest that two blocks of tensor memory and 128 sums a thread hold, and
+// a pair, because each of its CTAs feeds its tensor core half of B only.  Warps
+// by role: eight hold the sums (216 registers a thread), one loads by TMA, one
+// issues the products, one or two bring the scales.
+//
+// Bound, 9728 x 4096 x 4096: the chain around the two blocks of tensor memory,
+// not a rate (tensor pipe 54% busy, L2 37%, DRAM 11%).  From the issue of a
+// block's products to the sums' warps 870 cycles, 600 to 800 until its place
+// is free again, 250 until the next issue: 830 cycles a block of K, of which
+// the products are 512.  A packed multiply a value for column scales makes it
+// 1390.  Measured: 12345 x 4096 x 14336 560 us (2.6 PFLOP/s; 615 in a long run
+// under the power limit), FP32 14336 x 4096 x 16384 with column scales 1108 us,
+// 65536 rows over 64 experts of 4096 x 7168 1600 us, 128 rows over them 242 us
+// (6.7 TB/s of weights).  128-column tiles with four blocks in tensor memory
+// were slower (174 against 118 us at 4864 x 2048 x 16384): a warp of sums
+// needs some 600 cycles a block whatever its columns.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -381,137 +400,137 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   }
 
   if (warp >= kMmEpiWarps) {
-  regs_dec<kMmRegsLoad>();
-  if (warp == kMmEpiWarps) {
-    // ---------------- loads: one thread ----------------
-    if (elect_one()) {
-      uint32_t it = 0;  // blocks of K issued
-      for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
-        const MmTile w = tile_of(t);
-        const int arow = (int)w.row0 + rank * kMmRows;
-        const int brow = (int)(w.n0 + (MODE == kMmRowGroups ? (int64_t)w.g * p.n : 0)) + rank * (kMmCols / CG);
-        int at = (int)w.k0;
-        for (int kb = 0; kb < w.nkb; kb++, it++, at += kMmBlock) {
-          const uint32_t s = it % S::kStages, round = it / S::kStages;
-          if (round > 0 && !mm_wait(&empty[s], (round - 1) & 1u, kMmPolls)) {
-            abort_flag = 1;
-            break;
-          }
-          unsigned char* st = stages + s * S::kStageBytes;
-          if constexpr (CG == 1) {
-            mbar_arrive_expect_tx(&full[s], S::kStageBytes);
-            tma_load_2d(st, &map_a, at, arow, &full[s]);
-            tma_load_2d(st + S::kABytes, &map_b, at, brow, &full[s]);
-          } else {
-            // the leader's barrier counts the bytes of both CTAs
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStageBytes);
-            const uint32_t bar = cluster_addr(&full[s], 0);
-            tma_load_2d_pair(st, &map_a, at, arow, bar);
-            tma_load_2d_pair(st + S::kABytes, &map_b, at, brow, bar);
+    regs_dec<kMmRegsLoad>();
+    if (warp == kMmEpiWarps) {
+      // ---------------- loads: one thread ----------------
+      if (elect_one()) {
+        uint32_t it = 0;  // blocks of K issued
+        for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
+          const MmTile w = tile_of(t);
+          const int arow = (int)w.row0 + rank * kMmRows;
+          const int brow = (int)(w.n0 + (MODE == kMmRowGroups ? (int64_t)w.g * p.n : 0)) + rank * (kMmCols / CG);
+          int at = (int)w.k0;
+          for (int kb = 0; kb < w.nkb; kb++, it++, at += kMmBlock) {
+            const uint32_t s = it % S::kStages, round = it / S::kStages;
+            if (round > 0 && !mm_wait(&empty[s], (round - 1) & 1u, kMmPolls)) {
+              abort_flag = 1;
+              break;
+            }
+            unsigned char* st = stages + s * S::kStageBytes;
+            if constexpr (CG == 1) {
+              mbar_arrive_expect_tx(&full[s], S::kStageBytes);
+              tma_load_2d(st, &map_a, at, arow, &full[s]);
+              tma_load_2d(st + S::kABytes, &map_b, at, brow, &full[s]);
+            } else {
+              // the leader's barrier counts the bytes of both CTAs
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * S::kStageBytes);
+              const uint32_t bar = cluster_addr(&full[s], 0);
+              tma_load_2d_pair(st, &map_a, at, arow, bar);
+              tma_load_2d_pair(st + S::kABytes, &map_b, at, brow, bar);
+            }
           }
         }
+        // Every issued copy lands before the CTA (the pair) can exit (fixed 2 s
+        // bound), and every block is used or the flag that tells of a failure up.
+        const uint32_t tail = it > S::kStages ? it - S::kStages : 0;
+        if (rank == 0)
+          for (uint32_t j = tail; j < it; j++) mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
+        for (uint32_t j = tail; j < it && !abort_flag; j++)
+          if (!mm_wait(&empty[j % S::kStages], (j / S::kStages) & 1u, kMmPolls)) abort_flag = 1;
+        if (abort_flag) atomicOr(&g_mm_error, 1u);
       }
-      // Every issued copy lands before the CTA (the pair) can exit (fixed 2 s
-      // bound), and every block is used or the flag that tells of a failure up.
-      const uint32_t tail = it > S::kStages ? it - S::kStages : 0;
-      if (rank == 0)
-        for (uint32_t j = tail; j < it; j++) mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1u, kMmDrainNs);
-      for (uint32_t j = tail; j < it && !abort_flag; j++)
-        if (!mm_wait(&empty[j % S::kStages], (j / S::kStages) & 1u, kMmPolls)) abort_flag = 1;
-      if (abort_flag) atomicOr(&g_mm_error, 1u);
-    }
-    __syncwarp();
-    pdl_launch_dependents();
-  } else if (warp == kMmEpiWarps + 1) {
-    // ---------------- tensor core: one thread of the leader ----------------
-    if (rank == 0 && elect_one()) {
+      __syncwarp();
+      pdl_launch_dependents();
+    } else if (warp == kMmEpiWarps + 1) {
+      // ---------------- tensor core: one thread of the leader ----------------
+      if (rank == 0 && elect_one()) {
+        uint32_t it = 0;
+        for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
+          const MmTile w = tile_of(t);
+          for (int kb = 0; kb < w.nkb; kb++, it++) {
+            const uint32_t s = it % S::kStages, round = it / S::kStages, b = it & 1u, use = it >> 1;
+            if (!mm_wait(&full[s], round & 1u, kMmPolls) || (use > 0 && !mm_wait(&taken[b], (use - 1) & 1u, kMmPolls))) {
+              atomicOr(&g_mm_error, 1u);
+              abort_flag = 1;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t st = smem_u32(stages + s * S::kStageBytes);
+            const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + S::kABytes);
+#pragma unroll
+            for (int k = 0; k < kMmBlock / 32; k++)
+              mma_f8<CG>(tmem + b * kMmCols, da + 2 * k, db + 2 * k, p.idesc, k > 0);
+            mma_commit<CG>(&done[b]);
+            mma_commit<CG>(&empty[s]);
+          }
+        }
+        // nothing is in flight when the tensor memory is freed
+        mma_commit<CG>(&drained);
+        mbar_wait(&drained, 0, kMmDrainNs);
+      }
+      __syncwarp();
+    } else if (warp < kMmEpiWarps + 2 + SW) {
+      // ---------------- scales: SW warps, four blocks of K at a time ----------------
+      // Quads of blocks are aligned in the scale rows, so that with rows of a
+      // multiple of four a quad is one 16-byte load (a line a row: four times
+      // fewer than a load a block).
+      const bool vec = ((p.sa_ld | p.sb_ld) & 3) == 0 && (((uintptr_t)p.sa | (uintptr_t)p.sb) & 15) == 0;
+      const auto quad = [&](const float* row, int64_t ld, int64_t q) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec) {
+          v = __ldg((const float4*)(row + 4 * q));
+        } else {
+          v.x = __ldg(row + 4 * q);
+          if (4 * q + 1 < ld) v.y = __ldg(row + 4 * q + 1);
+          if (4 * q + 2 < ld) v.z = __ldg(row + 4 * q + 2);
+          if (4 * q + 3 < ld) v.w = __ldg(row + 4 * q + 3);
+        }
+        return v;
+      };
+      const auto put = [&](float* at, const float4& v) {  // the four blocks of one row or column
+        at[0] = v.x, at[NS] = v.y, at[2 * NS] = v.z, at[3 * NS] = v.w;
+      };
       uint32_t it = 0;
-      for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
+      bool ok = true;
+      for (uint32_t t = tile0; t < tiles && ok; t += tile_step) {
         const MmTile w = tile_of(t);
-        for (int kb = 0; kb < w.nkb; kb++, it++) {
-          const uint32_t s = it % S::kStages, round = it / S::kStages, b = it & 1u, use = it >> 1;
-          if (!mm_wait(&full[s], round & 1u, kMmPolls) || (use > 0 && !mm_wait(&taken[b], (use - 1) & 1u, kMmPolls))) {
-            atomicOr(&g_mm_error, 1u);
-            abort_flag = 1;
+        if (w.nkb == 0) continue;
+        const int64_t kb0 = w.k0 / kMmBlock;
+        for (int64_t q = kb0 >> 2; q <= (kb0 + w.nkb - 1) >> 2; q++, it++) {
+          const uint32_t s = it % kMmScaleSlots, round = it / kMmScaleSlots;
+          float* at = &scale[s][0][0];
+          constexpr int N = NS / 32 / SW;
+          const int e0 = (warp - (kMmEpiWarps + 2)) * N * 32 + lane;  // of the rows, then of the columns
+          float4 v[N];
+#pragma unroll
+          for (int i = 0; i < N; i++) {
+            const int e = e0 + i * 32;
+            if (e < kMmRows) {
+              const int64_t r = w.row0 + rank * kMmRows + e;
+              v[i] = quad(p.sa + (r < p.m ? r : p.m - 1) * p.sa_ld, p.sa_ld, q);
+            } else if constexpr (COLSCALE) {
+              const int64_t c = w.n0 + e - kMmRows;
+              v[i] = quad(p.sb + (c < p.n ? c : p.n - 1) * p.sb_ld, p.sb_ld, q);
+            } else {
+              const int64_t nb = (p.n + kMmBlock - 1) / kMmBlock, c = w.n0 / kMmBlock + (lane & 1);
+              v[i] = quad(p.sb + ((MODE == kMmRowGroups ? (int64_t)w.g * nb : 0) + (c < nb ? c : nb - 1)) * p.sb_ld, p.sb_ld, q);
+            }
+          }
+          if (!__all_sync(0xFFFFFFFFu, round == 0 || mm_wait(&sempty[s], (round - 1) & 1u))) {
+            ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t st = smem_u32(stages + s * S::kStageBytes);
-          const uint64_t da = smem_desc_sw128(st), db = smem_desc_sw128(st + S::kABytes);
 #pragma unroll
-          for (int k = 0; k < kMmBlock / 32; k++)
-            mma_f8<CG>(tmem + b * kMmCols, da + 2 * k, db + 2 * k, p.idesc, k > 0);
-          mma_commit<CG>(&done[b]);
-          mma_commit<CG>(&empty[s]);
+          for (int i = 0; i < N; i++) put(at + e0 + i * 32, v[i]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull[s]);
         }
       }
-      // nothing is in flight when the tensor memory is freed
-      mma_commit<CG>(&drained);
-      mbar_wait(&drained, 0, kMmDrainNs);
-    }
-    __syncwarp();
-  } else if (warp < kMmEpiWarps + 2 + SW) {
-    // ---------------- scales: SW warps, four blocks of K at a time ----------------
-    // Quads of blocks are aligned in the scale rows, so that with rows of a
-    // multiple of four a quad is one 16-byte load (a line a row: four times
-    // fewer than a load a block).
-    const bool vec = ((p.sa_ld | p.sb_ld) & 3) == 0 && (((uintptr_t)p.sa | (uintptr_t)p.sb) & 15) == 0;
-    const auto quad = [&](const float* row, int64_t ld, int64_t q) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (vec) {
-        v = __ldg((const float4*)(row + 4 * q));
-      } else {
-        v.x = __ldg(row + 4 * q);
-        if (4 * q + 1 < ld) v.y = __ldg(row + 4 * q + 1);
-        if (4 * q + 2 < ld) v.z = __ldg(row + 4 * q + 2);
-        if (4 * q + 3 < ld) v.w = __ldg(row + 4 * q + 3);
-      }
-      return v;
-    };
-    const auto put = [&](float* at, const float4& v) {  // the four blocks of one row or column
-      at[0] = v.x, at[NS] = v.y, at[2 * NS] = v.z, at[3 * NS] = v.w;
-    };
-    uint32_t it = 0;
-    bool ok = true;
-    for (uint32_t t = tile0; t < tiles && ok; t += tile_step) {
-      const MmTile w = tile_of(t);
-      if (w.nkb == 0) continue;
-      const int64_t kb0 = w.k0 / kMmBlock;
-      for (int64_t q = kb0 >> 2; q <= (kb0 + w.nkb - 1) >> 2; q++, it++) {
-        const uint32_t s = it % kMmScaleSlots, round = it / kMmScaleSlots;
-        float* at = &scale[s][0][0];
-        constexpr int N = NS / 32 / SW;
-        const int e0 = (warp - (kMmEpiWarps + 2)) * N * 32 + lane;  // of the rows, then of the columns
-        float4 v[N];
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-          const int e = e0 + i * 32;
-          if (e < kMmRows) {
-            const int64_t r = w.row0 + rank * kMmRows + e;
-            v[i] = quad(p.sa + (r < p.m ? r : p.m - 1) * p.sa_ld, p.sa_ld, q);
-          } else if constexpr (COLSCALE) {
-            const int64_t c = w.n0 + e - kMmRows;
-            v[i] = quad(p.sb + (c < p.n ? c : p.n - 1) * p.sb_ld, p.sb_ld, q);
-          } else {
-            const int64_t nb = (p.n + kMmBlock - 1) / kMmBlock, c = w.n0 / kMmBlock + (lane & 1);
-            v[i] = quad(p.sb + ((MODE == kMmRowGroups ? (int64_t)w.g * nb : 0) + (c < nb ? c : nb - 1)) * p.sb_ld, p.sb_ld, q);
-          }
-        }
-        if (!__all_sync(0xFFFFFFFFu, round == 0 || mm_wait(&sempty[s], (round - 1) & 1u))) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int i = 0; i < N; i++) put(at + e0 + i * 32, v[i]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[s]);
+      if (!ok) {
+        if (lane == 0) atomicOr(&g_mm_error, 1u);
+        abort_flag = 1;
       }
     }
-    if (!ok) {
-      if (lane == 0) atomicOr(&g_mm_error, 1u);
-      abort_flag = 1;
-    }
-  }
   } else {
     regs_inc<kMmRegsEpi>();
     // ---------------- sums over the blocks and the epilogue ----------------

@@ -21,7 +21,10 @@
 // One warp takes one token, expert e = lane + 32 i in register i.  A choice is
 // one warp-wide integer maximum of the order-preserving bits of the lanes'
 // best and a ballot of who has it (a minimum of the indices where several do).
-// Up to 256 experts each lane sorts its keys first.
+// Up to 256 experts each lane sorts its keys first (53 to 56 us for 65536
+// tokens over 256 experts, 8 each; a search of all registers for each choice
+// takes 63).  Bound by instructions (77% of the issue slots), three times the
+// 10 us that reading the logits takes; the gradient, 16 us, by its stores.
 #include "fp8q_device.cuh"
 #include "internal.h"
 
