@@ -141,6 +141,16 @@ FP8Q_API fp8q_status fp8q_debug_stall_mx_producer(int32_t on);
 FP8Q_API fp8q_status fp8q_debug_stall_scale_publish(int32_t on);
 
 /*
+ * Test hook for the same failure path in the products.  While `on` is
+ * nonzero, fp8q_matmul_blockwise and the grouped products issue no loads, so
+ * their waits for data run out: fp8q_check_device reports FP8Q_ERR_TIMEOUT,
+ * and the call's output is worthless.  Applies to kernels launched
+ * afterwards on the current device; leave it off (the default) outside such
+ * tests.
+ */
+FP8Q_API fp8q_status fp8q_debug_stall_matmul_loads(int32_t on);
+
+/*
  * amax_out[g] = max |x| over group g, bit-exact: the FP32 value whose bits
  * are the largest magnitude bits in the group (BF16 widened exactly), so a
  * NaN makes the result NaN and an empty group gives 0.

@@ -154,6 +154,11 @@ fp8q_status fp8q_debug_stall_mx_producer(int32_t on) {
   return mx_set_stall_producer(on != 0);
 }
 
+fp8q_status fp8q_debug_stall_matmul_loads(int32_t on) {
+  g_err[0] = 0;
+  return mm_set_stall_loads(on != 0);
+}
+
 fp8q_status fp8q_debug_stall_scale_publish(int32_t on) {
   g_err[0] = 0;
   return pt_set_stall_publish(on != 0);

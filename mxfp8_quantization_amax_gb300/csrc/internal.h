@@ -186,6 +186,7 @@ struct MatmulLaunch {
 fp8q_status launch_matmul(const MatmulLaunch& L);
 fp8q_status mm_device_status(bool clear, unsigned* word);
 fp8q_status mm_set_wait_budget(unsigned long long ns);
+fp8q_status mm_set_stall_loads(bool on);
 // Zeroes `bytes` (a multiple of 4) at p in stream order with a kernel that
 // keeps the chain of programmatic launches (a few counters or accumulators).
 fp8q_status launch_zero_words(void* p, size_t bytes, cudaStream_t s);

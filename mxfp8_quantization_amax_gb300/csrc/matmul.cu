@@ -52,6 +52,7 @@ constexpr uint64_t kMmDrainNs = 2000000000ull;
 
 __device__ unsigned int g_mm_error;
 __device__ unsigned long long g_mm_wait_budget_ns = 1000000000ull;
+__device__ int g_mm_stall_loads;  // test hook: issue no loads
 
 // Waits that mostly last a few hundred cycles: the clock is looked at only
 // once some 100 us of tries have failed, 64 by a whole warp or 8192 by the one
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       // ---------------- loads: one thread ----------------
       if (elect_one()) {
         uint32_t it = 0;  // blocks of K issued
-        for (uint32_t t = tile0; t < tiles && !abort_flag; t += tile_step) {
+        for (uint32_t t = g_mm_stall_loads ? tiles : tile0; t < tiles && !abort_flag; t += tile_step) {
           const MmTile w = tile_of(t);
           const int arow = (int)w.row0 + rank * kMmRows;
           const int brow = (int)(w.n0 + (MODE == kMmRowGroups ? (int64_t)w.g * p.n : 0)) + rank * (kMmCols / CG);
@@ -551,6 +552,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
       for (int n = 0; !mbar_try_wait(bar, parity); n++)
         if (n >= patience || abort_flag) {
+          abort_flag = 1;  // the other warps' waits end, too
           dead = true;
           break;
         }
@@ -803,6 +805,12 @@ fp8q_status mm_device_status(bool clear, unsigned* word) {
   }
   *word = v;
   return FP8Q_OK;
+}
+
+fp8q_status mm_set_stall_loads(bool on) {
+  const int v = on ? 1 : 0;
+  const cudaError_t e = cudaMemcpyToSymbol(g_mm_stall_loads, &v, sizeof(v));
+  return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "cudaMemcpyToSymbol(stall hook)");
 }
 
 fp8q_status mm_set_wait_budget(unsigned long long ns) {

@@ -348,3 +348,28 @@ def test_python_checks():
         mm(b, s, b, one)
     with pytest.raises(fq.Fp8qError, match="FP32"):
         mm(a, s, a, one, accumulate=True, out=torch.empty(4, 4, dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 512, 2048), (130, 256, 16384), (700, 8192, 1024)])
+def test_waits_run_out_and_are_reported(m, n, k):
+    """Without loads every wait ends after the budget, whatever the form (split, one CTA, pairs): the call
+    returns, the failure is reported, nothing is written outside the output, and the next call is right."""
+    fq = require_cuda()
+    g = gen(m)
+    kb = k // 128
+    a, b = codes(g, (m, k), 0), codes(g, (n, k), 0)
+    sa, sb = scales(g, (m, kb)), scales(g, (n // 128, kb))
+    out = Guarded((m, n), torch.float32)
+    try:
+        fq.set_wait_budget_ns(20_000_000)
+        fq.debug_stall_matmul_loads(True)
+        fq.fp8q_matmul_blockwise(a, sa, b, sb, out_dtype=torch.float32, out=out.t)
+        with pytest.raises(fq.Fp8qError, match="gave up"):
+            fq.check_device()
+    finally:
+        fq.debug_stall_matmul_loads(False)
+        fq.set_wait_budget_ns(1_000_000_000)
+    out.check()
+    fq.fp8q_matmul_blockwise(a, sa, b, sb, out_dtype=torch.float32, out=out.t)
+    fq.check_device()
+    check(out.t, values(a, sa, 0, 1), values(b, sb, 0, 128))
