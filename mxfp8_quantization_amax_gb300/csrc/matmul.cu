@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const uint32_t taken_at = CG == 1 ? 0 : cluster_addr(&taken[0], 0);
     uint32_t it = 0, sit = 0;  // blocks of K and quads of scales taken
     int kq = 0;                // the next block's place in its quad
-    float next = 0.0f;         // its row scale (and half's)
+    float next = 0.0f, next_col = 0.0f;  // its row's scale, and its half's
     uint32_t r[2][32];
     bool dead = false;
     // Waits for a block of K and starts its way from tensor memory to
@@ -564,8 +564,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       tc_fence_after();
       __syncwarp();
       tmem_load32(r[0], taddr + b * kMmCols);
+      // not multiplied here: that would hold the warp until they have come
       next = scale[slot][kq][quarter * 32 + lane];
-      if constexpr (!COLSCALE) next = __fmul_rn(next, scale[slot][kq][kMmRows + half]);
+      if constexpr (!COLSCALE) next_col = scale[slot][kq][kMmRows + half];
     };
     for (uint32_t t = tile0; t < tiles && !__any_sync(0xFFFFFFFFu, dead); t += tile_step) {
       int nkb;
@@ -583,7 +584,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       for (; nkb > 0; nkb--) {
         const uint32_t b = it & 1u, slot = sit % kMmScaleSlots;
         const float* sc = scale[slot][kq];
-        const uint64_t s2 = pack2(__float_as_uint(next), __float_as_uint(next));
+        const float f = COLSCALE ? next : __fmul_rn(next, next_col);
+        const uint64_t s2 = pack2(__float_as_uint(f), __float_as_uint(f));
         const bool quad_ends = kq == 3 || nkb == 1;
         it++;
         kq = (kq + 1) & 3;
