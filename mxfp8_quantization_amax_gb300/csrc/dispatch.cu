@@ -20,8 +20,9 @@ namespace fp8q {
 constexpr int kPlanMaxExperts = 1024;
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanPiece = 4096;       // slots of one CTA
-constexpr int kPlanMaxPieces = 1024;   // beyond, pieces grow
+constexpr int kPlanAlone = 4096;       // slots that one CTA takes in one launch
+constexpr int kPlanPiece = 1024;       // slots of one CTA of more
+constexpr int kPlanMaxPieces = 128;    // beyond, pieces grow: each CTA reads all pieces' counts
 
 struct PlanParams {
   const int* ids;
@@ -82,6 +83,7 @@ __device__ __forceinline__ int64_t plan_scan(int64_t v, int64_t* sh, int64_t* al
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanParams p) {
   extern __shared__ int next[];  // [warps][experts]: the next row of each expert for each warp
   __shared__ int64_t sh[kPlanWarps];
+  __shared__ int2 pad[kPlanMaxExperts];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   for (int i = tid; i < kPlanWarps * p.experts; i += kPlanThreads) next[i] = 0;
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanParams p) 
       if (p.pieces == 1) {
         for (int w = 0; w < kPlanWarps; w++) total += next[w * p.experts + e];
       } else {
+#pragma unroll 8
         for (int b = 0; b < p.pieces; b++) {
           const int c = __ldg(p.counts + (int64_t)b * p.experts + e);
           if (b < (int)blockIdx.x) before += c;
@@ -123,11 +126,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanParams p) 
         at += c;
       }
       if (blockIdx.x == 0) p.offsets[e] = start;
-      if (e % p.pieces == (int)blockIdx.x)  // the segment's padding
-        for (int64_t r = start + total; r < start + padded; r++) p.src[r] = -1;
+      pad[e] = make_int2((int)(start + total), (int)(start + padded));
     }
   }
   if (blockIdx.x == 0 && tid == 0) p.offsets[p.experts] = base;
+  __syncthreads();
+  for (int e = blockIdx.x + warp * p.pieces; e < p.experts; e += kPlanWarps * p.pieces)  // the segments' padding
+    for (int r = pad[e].x + lane; r < pad[e].y; r += 32) p.src[r] = -1;
   for (int64_t r = base + blockIdx.x * kPlanThreads + tid; r < p.rows; r += (int64_t)p.pieces * kPlanThreads) p.src[r] = -1;
   __syncthreads();
   for (int64_t s0 = w0; s0 < w1; s0 += 32) {
@@ -415,10 +420,13 @@ static fp8q_status launch_dispatch_f(const DispatchParams& p, int dir, cudaStrea
 }
 
 static void plan_pieces(int64_t slots, int64_t* piece, int* pieces) {
-  *piece = kPlanPiece;
-  if (slots > (int64_t)kPlanPiece * kPlanMaxPieces) *piece = (slots + kPlanMaxPieces - 1) / kPlanMaxPieces;
-  const int64_t n = (slots + *piece - 1) / *piece;
-  *pieces = n > 0 ? (int)n : 1;
+  *piece = kPlanAlone;
+  *pieces = 1;
+  if (slots <= kPlanAlone) return;
+  const int64_t n = (slots + kPlanPiece - 1) / kPlanPiece;
+  *piece = (slots + (n < kPlanMaxPieces ? n : kPlanMaxPieces) - 1) / (n < kPlanMaxPieces ? n : kPlanMaxPieces);
+  *piece = (*piece + 255) / 256 * 256;
+  *pieces = (int)((slots + *piece - 1) / *piece);
 }
 
 static fp8q_status check_plan(int64_t slots, int32_t experts, int32_t align) {
