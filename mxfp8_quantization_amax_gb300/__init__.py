@@ -695,14 +695,14 @@ def _codes(t: torch.Tensor, name: str, dims: int):
 
 
 def _floats(t: torch.Tensor, name: str, shape: tuple):
-    if not t.is_cuda or t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if not t.is_cuda or t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {shape}")
 
 
 def _result(out, shape: tuple, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not out.is_cuda or out.dtype != dtype or tuple(out.shape) != shape or not out.is_contiguous():
+    if not out.is_cuda or out.dtype != dtype or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {dtype} CUDA tensor of shape {shape}")
     return out
 
@@ -710,7 +710,11 @@ def _result(out, shape: tuple, dtype, device):
 def _group_offsets(group_offsets, device):
     if group_offsets is None:
         raise ValueError("group_offsets is required")
-    off, groups = _offsets(group_offsets, device)
+    if isinstance(group_offsets, torch.Tensor) and group_offsets.dtype == torch.int64 and group_offsets.device == device \
+            and group_offsets.dim() == 1 and group_offsets.is_contiguous():
+        off, groups = group_offsets, group_offsets.numel() - 1
+    else:
+        off, groups = _offsets(group_offsets, device)
     if groups < 1:
         raise ValueError("group_offsets must hold num_groups + 1 values")
     return off, groups
@@ -738,9 +742,11 @@ def fp8q_matmul_blockwise(a: torch.Tensor, a_scale_inv: torch.Tensor, b: torch.T
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     y = _result(out, (m, n), out_dtype, a.device)
-    _check(lib().fp8q_matmul_blockwise(_ptr(a), _ptr(a_scale_inv), a_fmt, _ptr(b), _ptr(b_scale_inv), b_fmt, b_block,
-                                       m, n, k, _out_dtype(out_dtype), 1 if accumulate else 0, _ptr(y), _stream()),
-           "fp8q_matmul_blockwise")
+    st = (_lib or lib()).fp8q_matmul_blockwise(a.data_ptr(), a_scale_inv.data_ptr(), a_fmt, b.data_ptr(),
+                                               b_scale_inv.data_ptr(), b_fmt, b_block, m, n, k, _out_dtype(out_dtype),
+                                               1 if accumulate else 0, y.data_ptr(), _stream())
+    if st:
+        _check(st, "fp8q_matmul_blockwise")
     return y
 
 
@@ -801,12 +807,13 @@ def fp8q_matmul_grouped_wgrad(a_t: torch.Tensor, a_scale_inv_t: torch.Tensor, b_
 # ---------------------------------------------------------------------------
 def _matrix(t: torch.Tensor, name: str, dtypes: tuple, shape: tuple | None = None):
     if not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes or not t.is_contiguous() or (
-            shape is not None and tuple(t.shape) != shape):
+            shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor of {' or '.join(map(str, dtypes))}"
                          + (f" and shape {shape}" if shape is not None else ""))
 
 
 _VALUES = (torch.bfloat16, torch.float32)
+_IN = {torch.bfloat16: 0, torch.float32: 1}  # FP8Q_IN_*
 
 
 def fp8q_moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bias: torch.Tensor | None = None,
@@ -819,15 +826,19 @@ def fp8q_moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX,
     groups; the weights hold the scores without the bias (see the C header)."""
     _matrix(logits, "logits", _VALUES)
     tokens, experts = logits.shape
-    if bias is not None and (not bias.is_cuda or bias.dtype != torch.float32 or tuple(bias.shape) != (experts,)
+    if bias is not None and (not bias.is_cuda or bias.dtype != torch.float32 or bias.shape != (experts,)
                              or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous float32 CUDA tensor with one value per expert")
-    o = out or {}
-    w = _result(o.get("weights"), (tokens, top_k), torch.float32, logits.device)
-    ids = _result(o.get("ids"), (tokens, top_k), torch.int32, logits.device)
-    _check(lib().fp8q_moe_route(_ptr(logits), _dt(logits), tokens, experts, top_k, score, _ptr(bias), num_groups,
-                                top_groups, 1 if renormalize else 0, weight_scale, _ptr(w), _ptr(ids), _stream()),
-           "fp8q_moe_route")
+    shape, dev = (tokens, top_k), logits.device
+    if out is None:
+        w, ids = torch.empty(shape, dtype=torch.float32, device=dev), torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        w, ids = _result(out.get("weights"), shape, torch.float32, dev), _result(out.get("ids"), shape, torch.int32, dev)
+    st = (_lib or lib()).fp8q_moe_route(logits.data_ptr(), _IN[logits.dtype], tokens, experts, top_k, score, _ptr(bias),
+                                        num_groups, top_groups, 1 if renormalize else 0, weight_scale, w.data_ptr(),
+                                        ids.data_ptr(), _stream())
+    if st:
+        _check(st, "fp8q_moe_route")
     return {"weights": w, "ids": ids}
 
 
@@ -841,10 +852,12 @@ def fp8q_moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: 
     _matrix(d_weights, "d_weights", (torch.float32,), tuple(ids.shape))
     if ids.shape[0] != tokens:
         raise ValueError("ids must hold one row per token")
-    d = _result(out, (tokens, experts), logits.dtype, logits.device)
-    _check(lib().fp8q_moe_route_backward(_ptr(logits), _dt(logits), tokens, experts, ids.shape[1], score,
-                                         1 if renormalize else 0, weight_scale, _ptr(ids), _ptr(d_weights), _ptr(d),
-                                         _stream()), "fp8q_moe_route_backward")
+    d = torch.empty_like(logits) if out is None else _result(out, (tokens, experts), logits.dtype, logits.device)
+    st = (_lib or lib()).fp8q_moe_route_backward(logits.data_ptr(), _IN[logits.dtype], tokens, experts, ids.shape[1], score,
+                                                 1 if renormalize else 0, weight_scale, ids.data_ptr(),
+                                                 d_weights.data_ptr(), d.data_ptr(), _stream())
+    if st:
+        _check(st, "fp8q_moe_route_backward")
     return d
 
 
@@ -863,14 +876,21 @@ def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, align: int = 1, out: dict
     rows = L.fp8q_moe_rows(slots, num_experts, align)
     if rows < 0:
         raise ValueError("num_experts and align must be at least 1")
-    o = out or {}
-    offsets = _result(o.get("offsets"), (num_experts + 1,), torch.int64, ids.device)
-    row_of = _result(o.get("row_of"), tuple(ids.shape), torch.int32, ids.device)
-    src = _result(o.get("src"), (rows,), torch.int32, ids.device)
+    dev = ids.device
+    if out is None:
+        offsets = torch.empty(num_experts + 1, dtype=torch.int64, device=dev)
+        row_of = torch.empty_like(ids)
+        src = torch.empty(rows, dtype=torch.int32, device=dev)
+    else:
+        offsets = _result(out.get("offsets"), (num_experts + 1,), torch.int64, dev)
+        row_of = _result(out.get("row_of"), tuple(ids.shape), torch.int32, dev)
+        src = _result(out.get("src"), (rows,), torch.int32, dev)
     need = L.fp8q_moe_plan_workspace_bytes(slots, num_experts)
-    ws = torch.empty(need, dtype=torch.uint8, device=ids.device) if need else None
-    _check(L.fp8q_moe_plan(_ptr(ids), slots, num_experts, align, rows, _ptr(offsets), _ptr(row_of), _ptr(src),
-                           _ptr(ws), need, _stream()), "fp8q_moe_plan")
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    st = L.fp8q_moe_plan(ids.data_ptr(), slots, num_experts, align, rows, offsets.data_ptr(), row_of.data_ptr(),
+                         src.data_ptr(), _ptr(ws), need, _stream())
+    if st:
+        _check(st, "fp8q_moe_plan")
     return {"offsets": offsets, "row_of": row_of, "src": src}
 
 
@@ -887,17 +907,19 @@ def fp8q_moe_dispatch(x: torch.Tensor, plan: dict, fmt: int = E4M3, direction: i
         raise ValueError("the plan must have one row of slots per token")
     rows = src.numel()
     tr, tc = (rows + 127) // 128, (cols + 127) // 128
-    o = out or {}
+    o, dev = out or {}, x.device
     q = si = q_t = si_t = None
     if direction & ROW:
-        q = _result(o.get("q"), (rows, cols), torch.uint8, x.device)
-        si = _result(o.get("scale_inv"), (rows, tc), torch.float32, x.device)
+        q = _result(o.get("q"), (rows, cols), torch.uint8, dev)
+        si = _result(o.get("scale_inv"), (rows, tc), torch.float32, dev)
     if direction & COL:
-        q_t = _result(o.get("q_t"), (cols, rows), torch.uint8, x.device)
-        si_t = _result(o.get("scale_inv_t"), (cols, tr), torch.float32, x.device)
-    _check(lib().fp8q_moe_dispatch(_ptr(x), 0, tokens, cols, max(row_of.shape[1], 1), _ptr(src), rows, fmt,
-                                   1 if pow2_scales else 0, direction, _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t),
-                                   _stream()), "fp8q_moe_dispatch")
+        q_t = _result(o.get("q_t"), (cols, rows), torch.uint8, dev)
+        si_t = _result(o.get("scale_inv_t"), (cols, tr), torch.float32, dev)
+    st = (_lib or lib()).fp8q_moe_dispatch(x.data_ptr(), 0, tokens, cols, max(row_of.shape[1], 1), src.data_ptr(), rows, fmt,
+                                           1 if pow2_scales else 0, direction, _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t),
+                                           _stream())
+    if st:
+        _check(st, "fp8q_moe_dispatch")
     return {"q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
 
 
@@ -913,8 +935,10 @@ def fp8q_moe_combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None =
     rows, cols = y.shape
     tokens, top_k = row_of.shape
     o = _result(out, (tokens, cols), y.dtype, y.device)
-    _check(lib().fp8q_moe_combine(_ptr(y), _dt(y), rows, cols, _ptr(row_of), _ptr(weights), tokens, top_k, _ptr(o),
-                                  _stream()), "fp8q_moe_combine")
+    st = (_lib or lib()).fp8q_moe_combine(y.data_ptr(), _IN[y.dtype], rows, cols, row_of.data_ptr(), _ptr(weights), tokens,
+                                          top_k, o.data_ptr(), _stream())
+    if st:
+        _check(st, "fp8q_moe_combine")
     return o
 
 
@@ -931,12 +955,16 @@ def fp8q_moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, plan: dict, 
     _matrix(weights, "weights", (torch.float32,), (tokens, top_k))
     if src.numel() != rows:
         raise ValueError("y must have the plan's rows")
-    o = out or {}
-    d_y = _result(o.get("d_y"), (rows, cols), y.dtype, y.device)
-    d_w = _result(o.get("d_weights"), (tokens, top_k), torch.float32, y.device)
-    _check(lib().fp8q_moe_combine_backward(_ptr(d_out), _ptr(y), _dt(y), rows, cols, _ptr(row_of), _ptr(src),
-                                           _ptr(weights), tokens, top_k, _ptr(d_y), _ptr(d_w), _stream()),
-           "fp8q_moe_combine_backward")
+    if out is None:
+        d_y, d_w = torch.empty_like(y), torch.empty_like(weights)
+    else:
+        d_y = _result(out.get("d_y"), (rows, cols), y.dtype, y.device)
+        d_w = _result(out.get("d_weights"), (tokens, top_k), torch.float32, y.device)
+    st = (_lib or lib()).fp8q_moe_combine_backward(d_out.data_ptr(), y.data_ptr(), _IN[y.dtype], rows, cols,
+                                                   row_of.data_ptr(), src.data_ptr(), weights.data_ptr(), tokens, top_k,
+                                                   d_y.data_ptr(), d_w.data_ptr(), _stream())
+    if st:
+        _check(st, "fp8q_moe_combine_backward")
     return {"d_y": d_y, "d_weights": d_w}
 
 
