@@ -556,7 +556,7 @@ FP8Q_API fp8q_status fp8q_moe_route_backward(const void* logits, int32_t dt, int
 FP8Q_API int64_t fp8q_moe_rows(int64_t slots, int32_t experts, int32_t align);
 
 /* Bytes of workspace fp8q_moe_plan needs (contents do not matter); 0 for up
- * to 4096 slots, whose workspace may be NULL. */
+ * to 1024 slots, whose workspace may be NULL. */
 FP8Q_API size_t fp8q_moe_plan_workspace_bytes(int64_t slots, int32_t experts);
 
 /*
