@@ -20,9 +20,10 @@
 //
 // One warp takes one token, expert e = lane + 32 i in register i.  A choice is
 // one warp-wide integer maximum of the order-preserving bits of the lanes'
-// best and a ballot of who has it (a minimum of the indices where several do).
-// Up to 256 experts each lane sorts its keys first (53 to 56 us for 65536
-// tokens over 256 experts, 8 each; a search of all registers for each choice
+// best and a ballot of who has it (a minimum of the indices where several do);
+// that lane writes its expert to shared memory.
+// Up to 256 experts each lane sorts its keys first (52 us for 65536
+// tokens over 256 experts, 8 each, 31 over 64; a search of all registers for each choice
 // takes 63).  Bound by instructions (77% of the issue slots), three times the
 // 10 us that reading the logits takes; the gradient, 16 us, by its stores.
 #include "fp8q_device.cuh"
@@ -55,6 +56,22 @@ __device__ __forceinline__ float rt_load(const void* p, int64_t i) {
     return __uint_as_float((uint32_t)__ldg((const uint16_t*)p + i) << 16);
   else
     return __ldg((const float*)p + i);
+}
+
+// A token's logits, -inf beyond them; no load waits for a branch.
+template <int DT, int V>
+__device__ __forceinline__ void rt_load_row(const RtParams& p, int64_t t, int lane, float (&x)[V]) {
+  const int64_t row = t * p.experts;
+  if (p.experts == 32 * V) {
+#pragma unroll
+    for (int i = 0; i < V; i++) x[i] = rt_load<DT>(p.logits, row + lane + 32 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i++) x[i] = rt_load<DT>(p.logits, row + min(lane + 32 * i, p.experts - 1));
+#pragma unroll
+    for (int i = 0; i < V; i++)
+      if (lane + 32 * i >= p.experts) x[i] = __uint_as_float(0xFF800000u);
+  }
 }
 
 template <int DT>
@@ -138,15 +155,20 @@ template <int DT, bool SOFTMAX, bool BYLOGIT, int V>
 __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
   extern __shared__ uint32_t rt_smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int picks[kRtWarps][32];
   uint32_t* sh = rt_smem + warp * (V * 33);
   const float none = __uint_as_float(0xFF800000u);
   pdl_wait();
   for (int64_t t = (int64_t)blockIdx.x * kRtWarps + warp; t < p.tokens; t += (int64_t)gridDim.x * kRtWarps) {
     float x[V];
+    if constexpr (V > 8) {  // 1024 experts, BF16: 163 us, 360 with a question before each load; 256 experts: 54, 53
+      rt_load_row<DT, V>(p, t, lane, x);
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int e = lane + 32 * i;
-      x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : none;
+      for (int i = 0; i < V; i++) {
+        const int e = lane + 32 * i;
+        x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : none;
+      }
     }
     uint32_t key[V];
 #pragma unroll
@@ -213,8 +235,8 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
 #pragma unroll
       for (int i = 0; i < V; i++) place |= at[i] << (4 * i);
     }
-    int id = -1;
-    for (int j = 0; j < p.top_k; j++) {
+    int j = 0;
+    for (; j < p.top_k; j++) {
       uint32_t best = 0;
       int at = 0;
       if constexpr (V <= 8) {
@@ -230,15 +252,11 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
       }
       const uint32_t chosen = j == 0 && BYLOGIT ? top : __reduce_max_sync(kFull, best);
       if (chosen <= kRtNone) break;
-      unsigned who = __ballot_sync(kFull, best == chosen);
-      int e;
-      if ((who & (who - 1)) == 0) {  // one lane has it
-        e = __shfl_sync(kFull, lane + 32 * at, __ffs(who) - 1);
-      } else {
-        e = (int)__reduce_min_sync(kFull, best == chosen ? (unsigned)(lane + 32 * at) : 0xFFFFFFFFu);
-        who = 1u << (e & 31);
-      }
-      if (lane == __ffs(who) - 1) {
+      bool mine = best == chosen;
+      const unsigned who = __ballot_sync(kFull, mine);
+      if (who & (who - 1)) mine = lane == (int)(__reduce_min_sync(kFull, mine ? (unsigned)(lane + 32 * at) : kFull) & 31);
+      if (mine) {
+        picks[warp][j] = lane + 32 * at;
         if constexpr (V <= 8) {
 #pragma unroll
           for (int i = 0; i + 1 < V; i++) key[i] = key[i + 1];
@@ -250,8 +268,10 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
             if (i == at) key[i] = 0;
         }
       }
-      if (lane == j) id = e;
     }
+    __syncwarp();
+    const int id = lane < j ? picks[warp][lane] : -1;
+    __syncwarp();
     float w = 0.0f;
     if (id >= 0) w = score(rt_load<DT>(p.logits, t * p.experts + id));
     if (p.renorm) {
