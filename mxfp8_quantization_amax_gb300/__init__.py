@@ -894,6 +894,13 @@ def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, align: int = 1, out: dict
     return {"offsets": offsets, "row_of": row_of, "src": src}
 
 
+def _sources(plan: dict):
+    src = plan["src"]
+    if not src.is_cuda or src.dtype != torch.int32 or src.dim() != 1 or not src.is_contiguous():
+        raise ValueError("the plan's src must be a contiguous 1-D int32 CUDA tensor")
+    return src
+
+
 def fp8q_moe_dispatch(x: torch.Tensor, plan: dict, fmt: int = E4M3, direction: int = ROW, pow2_scales: bool = False,
                       out: dict | None = None) -> dict:
     """x [tokens, cols] gathered in the plan's order and quantized in 1x128
@@ -901,7 +908,7 @@ def fp8q_moe_dispatch(x: torch.Tensor, plan: dict, fmt: int = E4M3, direction: i
     the plan has padding)."""
     _matrix(x, "x", (torch.bfloat16,))
     tokens, cols = x.shape
-    src, row_of = plan["src"], plan["row_of"]
+    src, row_of = _sources(plan), plan["row_of"]
     _matrix(row_of, "row_of", (torch.int32,))
     if row_of.shape[0] != tokens:
         raise ValueError("the plan must have one row of slots per token")
@@ -947,7 +954,7 @@ def fp8q_moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, plan: dict, 
     """The gradients of fp8q_moe_combine: dict(d_y like y, zero in padding rows;
     d_weights float32 [tokens, top_k])."""
     _matrix(y, "y", _VALUES)
-    row_of, src = plan["row_of"], plan["src"]
+    row_of, src = plan["row_of"], _sources(plan)
     _matrix(row_of, "row_of", (torch.int32,))
     tokens, top_k = row_of.shape
     rows, cols = y.shape

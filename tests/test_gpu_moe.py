@@ -487,3 +487,17 @@ def test_python_checks():
                 lambda: fq.fp8q_moe_plan(ids, 1025)):
         with pytest.raises(fq.Fp8qError):
             bad()
+
+
+def test_a_plan_that_is_not_one_is_refused():
+    fq = require_cuda()
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    p = fq.fp8q_moe_plan(ids, 8)
+    x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    y, w = torch.zeros(8, 128, device="cuda"), torch.zeros(4, 2, device="cuda")
+    d = torch.zeros(4, 128, device="cuda")
+    for bad in (dict(p, src=p["src"].long()), dict(p, src=p["src"].cpu()), dict(p, src=p["src"].repeat(2)[::2]),
+                dict(p, src=p["src"].view(2, 4)), dict(p, row_of=p["row_of"].long()), dict(p, row_of=p["row_of"].cpu())):
+        for call in (lambda: fq.fp8q_moe_dispatch(x, bad), lambda: fq.fp8q_moe_combine_backward(d, y, bad, w)):
+            with pytest.raises(ValueError):
+                call()
