@@ -540,7 +540,9 @@ FP8Q_API fp8q_status fp8q_moe_route(const void* logits, int32_t dt, int64_t toke
 
 /*
  * The gradient of fp8q_moe_route's weights with respect to the logits; the
- * choice (ids) and the bias are constants.  Slots with id -1 add nothing.
+ * choice (ids) and the bias are constants.  Slots with id -1 add nothing.  A
+ * token whose weights a NaN (under softmax also a +inf) logit made NaN gets NaN
+ * for every logit.
  *   ids        device int32 [tokens][top_k], as routing wrote them
  *   d_weights  device float [tokens][top_k]
  *   d_logits   device, type dt, [tokens][experts]: written in full

@@ -845,7 +845,8 @@ def fp8q_moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX,
 def fp8q_moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor,
                             score: int = SCORE_SOFTMAX, renormalize: bool = True, weight_scale: float = 1.0,
                             out: torch.Tensor | None = None) -> torch.Tensor:
-    """The gradient of fp8q_moe_route's weights: d_logits, shaped and typed like logits."""
+    """The gradient of fp8q_moe_route's weights: d_logits, shaped and typed like
+    logits; NaN for every logit of a token whose weights are NaN."""
     _matrix(logits, "logits", _VALUES)
     tokens, experts = logits.shape
     _matrix(ids, "ids", (torch.int32,))

@@ -16,7 +16,8 @@
 //   sigmoid       dx_j = g_j s_j (1 - s_j),  0 for experts not chosen
 //   softmax       dx_e = p_e (g_e - sum_j g_j p_j); renormalised, the last
 //                 sum is zero and p_j / S a softmax over the chosen alone.
-// The bias and the choice have no gradient.
+// The bias and the choice have no gradient.  A token whose weights are NaN has
+// NaN for the gradient of each of its logits.
 //
 // One warp takes one token, expert e = lane + 32 i in register i.  A choice is
 // one warp-wide integer maximum of the order-preserving bits of the lanes'
@@ -288,9 +289,16 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
   pdl_launch_dependents();
 }
 
+// A logit that makes routing's weights NaN.
+template <bool SOFTMAX>
+__device__ __forceinline__ bool rt_poison(float x) {
+  return SOFTMAX ? !(x < __uint_as_float(0x7F800000u)) : x != x;
+}
+
 // The gradient where it reaches the chosen experts alone (sigmoid scores, or
 // renormalised softmax): L = 8, 16 or 32 lanes take a token, a slot each, after
-// the warp has cleared its tokens' rows.
+// the warp has cleared its tokens' rows.  All logits are read nevertheless: one
+// that is NaN is never chosen, and must not pass unseen.
 template <int DT, bool SOFTMAX, int L>
 __global__ void __launch_bounds__(kRtWarps * 32) route_backward_chosen_kernel(RtParams p) {
   constexpr int N = 32 / L;  // tokens of a warp
@@ -313,13 +321,40 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_chosen_kernel(Rt
         x = rt_load<DT>(p.logits, t * p.experts + id);
       }
     }
-    // the rows' bytes, 16 at a time where they allow it
-    const int64_t size = DT == kBF16 ? 2 : 4, n = min((int64_t)N, p.tokens - t0) * p.experts;
+    // the rows: looked through and cleared, 16 bytes at a time where they allow it
+    const int size = DT == kBF16 ? 2 : 4, n = (int)min((int64_t)N, p.tokens - t0) * p.experts;
+    const char* from = (const char*)p.logits + t0 * p.experts * size;
     char* row = (char*)p.d_logits + t0 * p.experts * size;
-    if (((uintptr_t)row & 15) == 0 && (n * size & 15) == 0) {
-      for (int64_t i = lane * 16; i < n * size; i += 512) *(uint4*)(row + i) = make_uint4(0, 0, 0, 0);
+    uint32_t bad = 0;  // bit i: token t0 + i
+    if ((((uintptr_t)row | (uintptr_t)from | (uintptr_t)(n * size)) & 15) == 0) {
+      constexpr int kBatch = 4;  // loads on their way
+      for (int i0 = lane * 16; i0 < n * size; i0 += kBatch * 512) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; k++)
+          v[k] = i0 + 512 * k < n * size ? __ldg((const uint4*)(from + i0 + 512 * k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kBatch; k++) {
+          const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          uint32_t which = 0;  // of the values of these 16 bytes
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            if constexpr (DT == kBF16) {
+              which |= (uint32_t)rt_poison<SOFTMAX>(bf16_lo(u[q])) << (2 * q);
+              which |= (uint32_t)rt_poison<SOFTMAX>(bf16_hi(u[q])) << (2 * q + 1);
+            } else {
+              which |= (uint32_t)rt_poison<SOFTMAX>(__uint_as_float(u[q])) << q;
+            }
+          }
+          for (; which; which &= which - 1) bad |= 1u << (((i0 + 512 * k) / size + __ffs(which) - 1) / p.experts);
+          if (i0 + 512 * k < n * size) *(uint4*)(row + i0 + 512 * k) = make_uint4(0, 0, 0, 0);
+        }
+      }
     } else {
-      for (int64_t i = lane; i < n; i += 32) rt_store<DT>(row, i, 0.0f);
+      for (int i = lane; i < n; i += 32) {
+        if (rt_poison<SOFTMAX>(rt_load<DT>(from, i))) bad |= 1u << (i / p.experts);
+        rt_store<DT>(row, i, 0.0f);
+      }
     }
     float s = 0.0f, dx;
     if constexpr (SOFTMAX) {
@@ -344,6 +379,12 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_chosen_kernel(Rt
     if (!SOFTMAX) dx = __fmul_rn(dx, rt_sigmoid(-x));
     __syncwarp();
     if (id >= 0) rt_store<DT>(p.d_logits, t * p.experts + id, dx);
+    bad = __reduce_or_sync(kFull, bad);
+    if (bad) {
+      __syncwarp();  // after the chosen logits' gradients
+      for (int i = lane; i < n; i += 32)
+        if (bad >> (i / p.experts) & 1u) rt_store<DT>(row, i, __uint_as_float(0x7FC00000u));
+    }
   }
   pdl_launch_dependents();
 }
@@ -366,13 +407,19 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_all_kernel(RtPar
       }
     }
     float x[V], most = none, sum = 0.0f;
+    bool bad = false;  // a NaN beside -inf alone would leave the maximum at -inf
 #pragma unroll
     for (int i = 0; i < V; i++) {
       const int e = lane + 32 * i;
       x[i] = e < p.experts ? rt_load<DT>(p.logits, t * p.experts + e) : none;
+      bad |= rt_poison<true>(x[i]);
       most = fmaxf(most, x[i]);
     }
     most = rt_warp_max(most);
+    if (__any_sync(kFull, bad)) {
+      for (int e = lane; e < p.experts; e += 32) rt_store<DT>(p.d_logits, t * p.experts + e, __uint_as_float(0x7FC00000u));
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < V; i++) {
       x[i] = most > none ? expf(x[i] - most) : 0.0f;

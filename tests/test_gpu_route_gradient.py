@@ -51,3 +51,37 @@ def test_sigmoid_gradient_of_confident_experts(experts, top_k, renorm):
         want = 2.5 * dd * s * rest
         tol = 8 * U * want.abs()
     assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("experts,top_k", [(5, 2), (64, 8), (100, 12), (257, 3), (1000, 32)])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_is_nan_where_the_weights_are(experts, top_k, score, renorm, dtype):
+    """A token whose weights routing made NaN gets NaN for every logit; its neighbours keep their gradients bit
+    for bit, whether a row starts on 16 bytes or not."""
+    fq = require_cuda()
+    x = torch.randn(23, experts, device="cuda", generator=gen(experts)).to(dtype)
+    d = torch.randn(23, top_k, device="cuda", generator=gen(2))
+    clean = fq.fp8q_moe_route(x, top_k, score, renormalize=renorm)
+    want = fq.fp8q_moe_route_backward(x, clean["ids"], d, score, renorm)
+    bad = x.clone()
+    lowest = x.float().argmin(1)  # chosen by nobody (of 5 experts 2 are chosen)
+    bad[2, lowest[2]] = float("nan")
+    bad[3, clean["ids"][3, 0].long()] = float("nan")
+    bad[9] = NEG
+    bad[9, experts - 1] = float("nan")  # a NaN is all there is
+    bad[16, 0] = -float("nan")
+    bad[22, experts // 2] = float("inf")
+    r = fq.fp8q_moe_route(bad, top_k, score, renormalize=renorm)
+    got = fq.fp8q_moe_route_backward(bad, r["ids"], d, score, renorm)
+    poisoned = torch.isnan(r["weights"]).any(1)
+    assert poisoned.nonzero()[:, 0].tolist() == [2, 3, 9, 16] + ([22] if score == 0 else [])
+    assert torch.isnan(got[poisoned]).all()
+    assert torch.isfinite(got[~poisoned]).all()
+    same = [t for t in range(23) if t not in (2, 3, 9, 16, 22)]
+    assert torch.equal(got[same], want[same])
+    # a buffer that starts off a 16-byte boundary
+    raw = torch.empty(23 * experts + 1, dtype=dtype, device="cuda")
+    off = fq.fp8q_moe_route_backward(bad, r["ids"], d, score, renorm, out=raw[1:].view(23, experts))
+    assert torch.equal(torch.nan_to_num(off.float(), nan=7e7), torch.nan_to_num(got.float(), nan=7e7))
