@@ -12,6 +12,8 @@
 //
 // Gradient, with d_j the gradient of w_j and g_j that of s_j:
 //   renormalised  g_j = c * (d_j - sum_i d_i s_i / S) / S,  S = sum_i s_i
+//                 (d less that of the best expert, r: nothing cancels where it
+//                 has nearly all of S)
 //   else          g_j = c * d_j
 //   sigmoid       dx_j = g_j s_j (1 - s_j),  0 for experts not chosen
 //   softmax       dx_e = p_e (g_e - sum_j g_j p_j); renormalised, the last
@@ -356,18 +358,18 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_chosen_kernel(Rt
         rt_store<DT>(row, i, 0.0f);
       }
     }
-    float s = 0.0f, dx;
-    if constexpr (SOFTMAX) {
-      float most = x;
+    float s = 0.0f, dx, most = x;
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-      if (id >= 0) s = expf(x - most);
-    } else if (id >= 0) {
-      s = rt_sigmoid(x);
-    }
+    for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+    if (id >= 0) s = SOFTMAX ? expf(x - most) : rt_sigmoid(x);
     if (p.renorm) {
       const float all = total(s);
       const float share = all != 0.0f ? __fdiv_rn(s, all) : 0.0f;
+      // d less the best expert's, so that what it has of the mean is exactly
+      // 0: of d - mean nothing would be left where its share is nearly 1
+      const uint32_t best = __ballot_sync(kFull, id >= 0 && x == most) >> (lane & -L) & (kFull >> (32 - L));
+      const float r = __shfl_sync(kFull, d, (lane & -L) + (best ? __ffs(best) - 1 : 0));
+      d = id >= 0 ? __fsub_rn(d, r) : 0.0f;
       const float mean = total(__fmul_rn(d, share));
       // p_j g_j (softmax) and g_j s_j (sigmoid) are both c (d_j - mean) s_j / S
       dx = __fmul_rn(__fmul_rn(p.weight_scale, __fsub_rn(d, mean)), share);
@@ -406,7 +408,8 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_all_kernel(RtPar
         xj = rt_load<DT>(p.logits, t * p.experts + id);
       }
     }
-    float x[V], most = none, sum = 0.0f;
+    float x[V], most = none, others = 0.0f;
+    int peaks = 0;  // logits equal to the largest: their exponentials are 1
     bool bad = false;  // a NaN beside -inf alone would leave the maximum at -inf
 #pragma unroll
     for (int i = 0; i < V; i++) {
@@ -422,12 +425,23 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_all_kernel(RtPar
     }
 #pragma unroll
     for (int i = 0; i < V; i++) {
+      const bool peak = most > none && x[i] == most;
       x[i] = most > none ? expf(x[i] - most) : 0.0f;
-      sum += x[i];
+      others += peak ? 0.0f : x[i];
+      peaks += peak;
     }
-    sum = rt_warp_sum(sum);
+    others = rt_warp_sum(others);
+    peaks = __reduce_add_sync(kFull, peaks);
+    const float sum = __fadd_rn(others, (float)peaks);
     const float s = id >= 0 ? __fdiv_rn(expf(xj - most), sum) : 0.0f;
-    const float dot = rt_warp_sum(__fmul_rn(g, s));
+    // sum_j g_j p_j, and g - that.  Alone at the top an expert's p may be nearly
+    // 1, and its g (1 - p) - (the others' sum) is taken from the others
+    const float gs = __fmul_rn(g, s);
+    const bool lone = id >= 0 && peaks == 1 && xj == most;
+    const unsigned who = __ballot_sync(kFull, lone);
+    const float rest = rt_warp_sum(lone ? 0.0f : gs);
+    const float dot = who ? __fadd_rn(rest, __shfl_sync(kFull, gs, __ffs(who) - 1)) : rest;
+    const float left = lone ? __fsub_rn(__fmul_rn(g, __fdiv_rn(others, sum)), rest) : __fsub_rn(g, dot);
 #pragma unroll
     for (int i = 0; i < V; i++) {
       const int e = lane + 32 * i;
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_all_kernel(RtPar
         rt_store<DT>(p.d_logits, t * p.experts + e, most > none ? -__fmul_rn(__fdiv_rn(x[i], sum), dot) : 0.0f);
     }
     __syncwarp();
-    if (id >= 0) rt_store<DT>(p.d_logits, t * p.experts + id, __fmul_rn(s, __fsub_rn(g, dot)));
+    if (id >= 0) rt_store<DT>(p.d_logits, t * p.experts + id, __fmul_rn(s, left));
   }
   pdl_launch_dependents();
 }

@@ -85,3 +85,46 @@ def test_gradient_is_nan_where_the_weights_are(experts, top_k, score, renorm, dt
     raw = torch.empty(23 * experts + 1, dtype=dtype, device="cuda")
     off = fq.fp8q_moe_route_backward(bad, r["ids"], d, score, renorm, out=raw[1:].view(23, experts))
     assert torch.equal(torch.nan_to_num(off.float(), nan=7e7), torch.nan_to_num(got.float(), nan=7e7))
+
+
+def dominant(tokens, experts, seed):
+    """Logits of which one a token lies 4 to 24 above the best of the others, which span 8."""
+    g = gen(seed)
+    x = torch.empty(tokens, experts, device="cuda").uniform_(-8, 0, generator=g)
+    at = torch.randint(0, experts, (tokens, 1), device="cuda", generator=g)
+    return x.scatter(1, at, torch.empty(tokens, 1, device="cuda").uniform_(4, 24, generator=g))
+
+
+@pytest.mark.parametrize("experts,top_k", [(2, 1), (8, 2), (64, 8), (100, 12), (256, 32), (500, 4), (1000, 3)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_softmax_gradient_of_a_dominant_expert(experts, top_k, renorm):
+    """One expert has nearly all the probability, so its gradient is what little the others take from it:
+    c share_j sum_i share_i (d_j - d_i), or c p_j (d_j (1 - p_j) - sum_(i != j) d_i p_i) without
+    renormalisation.  Bound: a probability's error, (16 + 2 range + E / 32) u as in the module's sums, twice,
+    and k + 4 additions, of the sum of these terms' magnitudes."""
+    fq = require_cuda()
+    x = dominant(60, experts, experts + top_k)
+    ids = fq.fp8q_moe_route(x, top_k, renormalize=renorm)["ids"].long()
+    d = torch.randn(60, top_k, device="cuda", generator=gen(3))
+    got = fq.fp8q_moe_route_backward(x, ids.int(), d, 0, renorm, 2.5).double()
+    rel = (2 * (16 + 2 * float(x.max() - x.min()) + experts / 32) + top_k + 4) * U
+    dd = d.double()
+    if renorm:
+        share = torch.softmax(x.double().gather(1, ids), 1)
+        apart = dd[:, :, None] - dd[:, None, :]
+        want = torch.zeros_like(x, dtype=torch.float64).scatter(1, ids, 2.5 * share * (share[:, None, :] * apart).sum(2))
+        size = torch.zeros_like(want).scatter(1, ids, 2.5 * share * (share[:, None, :] * apart.abs()).sum(2))
+    else:
+        e = torch.exp(x.double() - x.double().amax(1, keepdim=True))
+        p = e / e.sum(1, keepdim=True)
+        others = torch.stack([e[:, [j for j in range(experts) if j != i]].sum(1) for i in range(experts)], 1) / e.sum(1, keepdim=True)
+        g = torch.zeros_like(p).scatter(1, ids, 2.5 * dd)
+        dot, mag = (g * p).sum(1, keepdim=True), (g * p).abs().sum(1, keepdim=True)
+        rest = torch.stack([torch.where(torch.arange(experts, device="cuda") == i, 0.0, g * p).sum(1) for i in ids.unique().tolist()], 1)
+        mags = torch.stack([torch.where(torch.arange(experts, device="cuda") == i, 0.0, (g * p).abs()).sum(1) for i in ids.unique().tolist()], 1)
+        col = {i: n for n, i in enumerate(ids.unique().tolist())}
+        at = torch.tensor([col.get(i, 0) for i in range(experts)], device="cuda")
+        chosen = torch.zeros_like(p, dtype=torch.bool).scatter(1, ids, True)
+        want = p * torch.where(chosen, g * others - rest[:, at], -dot)
+        size = p * torch.where(chosen, g.abs() * others + mags[:, at], mag)
+    assert ((got - want).abs() <= rel * size + 1e-37).all()
