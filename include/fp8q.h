@@ -524,7 +524,8 @@ FP8Q_API fp8q_status fp8q_matmul_grouped_wgrad(const uint8_t* a_t, const float* 
  *   weight_scale * s_j                           without.
  * A logit that is -inf or NaN, or whose key is, is never chosen (its key
  * counts as -inf in its group); where fewer than top_k are left, the last
- * ids are -1 and their weights 0.  A NaN logit, under softmax also +inf,
+ * ids are -1 and their weights 0.  Weights are 0, too, where renormalize finds
+ * that all chosen sigmoid scores are 0 in FP32 (logits below -88).  A NaN logit, under softmax also +inf,
  * makes all the token's weights NaN.  Arithmetic is FP32.
  *   logits   device BF16 or FP32 (dt) [tokens][experts], experts <= 1024
  *   top_k    1..32, at most experts / num_groups * top_groups

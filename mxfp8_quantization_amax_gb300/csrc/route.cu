@@ -278,7 +278,15 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_kernel(RtParams p) {
     float w = 0.0f;
     if (id >= 0) w = score(rt_load<DT>(p.logits, t * p.experts + id));
     if (p.renorm) {
-      const float s = rt_warp_sum(w);
+      float s = rt_warp_sum(w);
+      // Experts that a bias or a group chose far below the best logit: their
+      // scores run out of FP32, the softmax over them alone does not
+      if (SOFTMAX && !BYLOGIT && s < 0x1p-60f) {
+        const float v = id >= 0 ? rt_load<DT>(p.logits, t * p.experts + id) : none;
+        const float top_v = rt_warp_max(v);
+        w = id >= 0 ? expf(v - top_v) : 0.0f;
+        s = rt_warp_sum(w);
+      }
       w = s > 0.0f ? __fdiv_rn(w, s) : s == 0.0f ? 0.0f : s;
     }
     w = __fmul_rn(w, p.weight_scale);

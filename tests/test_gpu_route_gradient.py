@@ -128,3 +128,28 @@ def test_softmax_gradient_of_a_dominant_expert(experts, top_k, renorm):
         want = p * torch.where(chosen, g * others - rest[:, at], -dot)
         size = p * torch.where(chosen, g.abs() * others + mags[:, at], mag)
     assert ((got - want).abs() <= rel * size + 1e-37).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (4, 2)])
+def test_weights_of_experts_that_a_bias_lifts_over_a_better_one(dtype, groups, top_groups):
+    """A bias that chooses experts 90 to 130 below the best logit: the softmax over the chosen is what it is
+    nearer the top, and agrees with its gradient.  Bound: (16 + 2 range) u, range that of the chosen."""
+    fq = require_cuda()
+    g = gen(4)
+    x = torch.empty(40, 32, device="cuda").uniform_(-130, -90, generator=g)
+    x[:, 31] = 0.0
+    x = x.to(dtype)
+    bias = torch.zeros(32, device="cuda")
+    bias[:6] = torch.arange(9, 3, -1, device="cuda")
+    r = fq.fp8q_moe_route(x, 4, 0, bias, groups, top_groups, weight_scale=2.5)
+    assert (r["ids"] == torch.arange(4, device="cuda")).all()
+    want = 2.5 * torch.softmax(x[:, :4].double(), 1)
+    assert ((r["weights"].double() - want).abs() <= (16 + 2 * 40) * U * want + 1e-37).all()
+    d = torch.randn(40, 4, device="cuda", generator=g)
+    got = fq.fp8q_moe_route_backward(x, r["ids"], d, 0, True, 2.5)
+    leaf = x.double().requires_grad_(True)
+    (2.5 * torch.softmax(leaf[:, :4], 1) * d.double()).sum().backward()
+    size = 2.5 * torch.softmax(x[:, :4].double(), 1) * d.double().abs().sum(1, keepdim=True)
+    tol = 2 * (16 + 2 * 40 + 4) * U * size + leaf.grad[:, :4].abs() * (2.0 ** -8 if dtype == torch.bfloat16 else U)
+    assert ((got[:, :4].double() - leaf.grad[:, :4]).abs() <= tol).all() and (got[:, 4:] == 0).all()
