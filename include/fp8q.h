@@ -110,9 +110,10 @@ FP8Q_API fp8q_status fp8q_check_device(void* stream);
 
 /*
  * Time budget of every bounded device-side wait, in nanoseconds (default
- * 1e9), for kernels launched afterwards on the current device.  Waits never
- * spin longer than this; a stalled pipeline ends its kernel and is reported
- * by fp8q_check_device.
+ * 1e9), for kernels launched afterwards on the current device.  No wait
+ * gives up before its budget is over, nor spins much longer: the clock is
+ * read every 16 tries, in the products from some 100 us on.  A stalled
+ * pipeline ends its kernel and is reported by fp8q_check_device.
  */
 FP8Q_API fp8q_status fp8q_set_wait_budget_ns(uint64_t ns);
 

@@ -57,10 +57,11 @@ __device__ int g_mm_stall_loads;  // test hook: issue no loads
 // Waits that mostly last a few hundred cycles: the clock is looked at only
 // once some 100 us of tries have failed, 64 by a whole warp or 8192 by the one
 // thread that polls, the tensor core's (it is the quicker to see a barrier).
+// From there on the wait has its whole budget.
 constexpr uint32_t kMmTries = 64, kMmPolls = 8192;
+__device__ __forceinline__ uint64_t mm_budget() { return *(volatile unsigned long long*)&g_mm_wait_budget_ns; }
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t tries = kMmTries) {
-  if (mbar_try_loop(bar, parity, tries)) return true;
-  return mbar_wait(bar, parity, *(volatile unsigned long long*)&g_mm_wait_budget_ns);
+  return mbar_try_loop(bar, parity, tries) || mbar_wait(bar, parity, mm_budget());
 }
 
 // What the groups divide: nothing, the rows of A and D, or K.
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ unsigned sums[MODE == kMmRowGroups ? 256 : 1];
   __shared__ __align__(16) float scale[kMmScaleSlots][4][NS];
-  __shared__ volatile int abort_flag, patience;  // the latter: tries of the sums' waits
+  __shared__ volatile int abort_flag;
   unsigned char* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned* first = (unsigned*)(stages + S::kStages * S::kStageBytes);
 
@@ -362,7 +363,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       mbar_init(&sempty[i], kMmEpiWarps);
     }
     abort_flag = 0;
-    patience = (int)min(g_mm_wait_budget_ns / 1400, 2000000000ull);
     fence_barrier_init();
   }
   if (warp == kMmEpiWarps) {
@@ -544,19 +544,21 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     float next = 0.0f, next_col = 0.0f;  // its row's scale, and its half's
     uint32_t r[2][32];
     bool dead = false;
-    // Waits for a block of K and starts its way from tensor memory to
-    // registers.  A failing try sleeps some 1.4 us, so a count of them bounds the
-    // wait.  After one that ran out the warp goes on without waiting, since its
-    // loads are collective; its tile loop ends, and the error word tells that
-    // the output is worthless.
+    // A wait of mm_wait's rule that ends with the other warps', too.  After one
+    // that ran out the warp goes on without waiting, since its loads are
+    // collective; its tile loop ends, and the error word tells that the output
+    // is worthless.
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      for (int n = 0; !mbar_try_wait(bar, parity); n++)
-        if (n >= patience || abort_flag) {
-          abort_flag = 1;  // the other warps' waits end, too
+      if (dead || mbar_try_loop(bar, parity, kMmTries)) return;
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(bar, parity))
+        if (abort_flag || globaltimer_ns() - t0 > mm_budget()) {
+          abort_flag = 1;
           dead = true;
           break;
         }
     };
+    // Waits for a block of K and starts its way from tensor memory to registers.
     const auto fetch = [&](bool new_quad) {
       const uint32_t slot = sit % kMmScaleSlots, b = it & 1u;
       wait(&done[b], (it >> 1) & 1u);

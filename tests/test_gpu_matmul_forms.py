@@ -1,0 +1,87 @@
+"""Products of blockwise FP8 tensors: forms, tiles and limits that the sizes of test_gpu_matmul.py do not reach.
+Its tolerance holds here, too: (128 + KB + 4) * 2^-23 of the sum of the terms' magnitudes and half a unit of
+the output type."""
+import time
+
+import pytest
+import torch
+
+from gpu_util import Guarded, require_cuda
+from test_gpu_matmul import check, codes, gen, scales, values
+
+pytestmark = pytest.mark.gpu
+
+
+FORMS = [(1, 512, 4096, 128), (100, 2048, 2048, 1), (130, 256, 4096, 128), (600, 4096, 2048, 1), (40, 40000, 400, 1)]
+
+
+@pytest.mark.parametrize("m,n,k,block", FORMS)
+@pytest.mark.parametrize("budget_ns", [1, 1000, 100_000])
+def test_a_short_wait_budget_does_not_end_a_healthy_product(m, n, k, block, budget_ns):
+    """A wait may give up once the budget is over and some 100 us have passed; a healthy product's waits last a
+    few microseconds, so it ends as ever however short the budget."""
+    fq = require_cuda()
+    g = gen(m + n)
+    kb = k // 128 + (k % 128 > 0)
+    a, b = codes(g, (m, k), 0), codes(g, (n, k), 0)
+    sa, sb = scales(g, (m, kb)), scales(g, (-(-n // block), kb))
+    want = fq.fp8q_matmul_blockwise(a, sa, b, sb, b_block=block, out_dtype=torch.float32)
+    fq.check_device()
+    try:
+        fq.set_wait_budget_ns(budget_ns)
+        for _ in range(5):
+            got = fq.fp8q_matmul_blockwise(a, sa, b, sb, b_block=block, out_dtype=torch.float32)
+            fq.check_device()
+            assert torch.equal(got, want)
+    finally:
+        fq.set_wait_budget_ns(1_000_000_000)
+
+
+@pytest.mark.parametrize("m,n,k,block", [f for f in FORMS if f[1] != 40000])
+def test_a_wait_lasts_as_long_as_its_budget(m, n, k, block):
+    """Without loads the call takes the budget (no wait gives up before) and not several of them: the waits of
+    one call run side by side, and an expired one ends the others of its CTA."""
+    fq = require_cuda()
+    g = gen(m + n)
+    kb = k // 128
+    a, b = codes(g, (m, k), 0), codes(g, (n, k), 0)
+    sa, sb = scales(g, (m, kb)), scales(g, (-(-n // block), kb))
+    fq.fp8q_matmul_blockwise(a, sa, b, sb, b_block=block)
+    fq.check_device()
+    budget = 0.2
+    try:
+        fq.set_wait_budget_ns(int(budget * 1e9))
+        fq.debug_stall_matmul_loads(True)
+        torch.cuda.synchronize()
+        start = time.perf_counter()
+        fq.fp8q_matmul_blockwise(a, sa, b, sb, b_block=block)
+        torch.cuda.synchronize()
+        took = time.perf_counter() - start
+        with pytest.raises(fq.Fp8qError, match="gave up"):
+            fq.check_device()
+    finally:
+        fq.debug_stall_matmul_loads(False)
+        fq.set_wait_budget_ns(1_000_000_000)
+    assert budget <= took < 5 * budget
+
+
+@pytest.mark.parametrize("rows", [40, 400])
+def test_a_short_wait_budget_does_not_end_a_product_that_waits_for_memory(rows):
+    """Weights of 40 experts, 168 MB, come from HBM: a warp of sums waits for microseconds."""
+    fq = require_cuda()
+    g = gen(rows)
+    b, sb = codes(g, (40, 2048, 2048), 0), scales(g, (40, 16, 16))
+    a, sa = codes(g, (rows, 2048), 0), scales(g, (rows, 16))
+    off = [rows * i // 40 for i in range(41)]
+    flush = torch.empty(512 << 20, dtype=torch.uint8, device="cuda")
+    want = fq.fp8q_matmul_grouped(a, sa, b, sb, off, out_dtype=torch.float32)
+    fq.check_device()
+    try:
+        fq.set_wait_budget_ns(1)
+        for _ in range(5):
+            flush.zero_()
+            got = fq.fp8q_matmul_grouped(a, sa, b, sb, off, out_dtype=torch.float32)
+            fq.check_device()
+            assert torch.equal(got, want)
+    finally:
+        fq.set_wait_budget_ns(1_000_000_000)
