@@ -64,6 +64,16 @@ __device__ __forceinline__ bool mm_wait(uint64_t* bar, uint32_t parity, uint32_t
   return mbar_try_loop(bar, parity, tries) || mbar_wait(bar, parity, mm_budget());
 }
 
+// Notes the time of this warp's n = kMmTries; tells of a later n whether the
+// budget is over since then.
+__device__ __forceinline__ bool mm_late(volatile uint64_t* since, uint32_t n) {
+  if (n < kMmTries) return false;
+  const uint64_t now = globaltimer_ns();
+  since += threadIdx.x >> 5;
+  if (n == kMmTries) *since = now;
+  return now - *since > mm_budget();
+}
+
 // What the groups divide: nothing, the rows of A and D, or K.
 enum : int { kMmDense = 0, kMmRowGroups = 1, kMmKGroups = 2 };
 
@@ -344,6 +354,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __shared__ unsigned sums[MODE == kMmRowGroups ? 256 : 1];
   __shared__ __align__(16) float scale[kMmScaleSlots][4][NS];
   __shared__ volatile int abort_flag;
+  __shared__ uint64_t since[kMmEpiWarps];  // when the sums' warps began to wait long
   unsigned char* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   unsigned* first = (unsigned*)(stages + S::kStages * S::kStageBytes);
 
@@ -544,15 +555,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     float next = 0.0f, next_col = 0.0f;  // its row's scale, and its half's
     uint32_t r[2][32];
     bool dead = false;
-    // A wait of mm_wait's rule that ends with the other warps', too.  After one
-    // that ran out the warp goes on without waiting, since its loads are
-    // collective; its tile loop ends, and the error word tells that the output
-    // is worthless.
+    // A wait of mm_wait's rule that ends with the other warps', too.  Its start is
+    // kept in shared memory, for want of registers, and nothing is asked before
+    // kMmTries (14336 x 4096 x 16384 with column scales: 1130 us, 1142 with a look
+    // at abort_flag each time, 1164 with the clock in registers).  After one that
+    // ran out the warp goes on without waiting, since its loads are collective;
+    // its tile loop ends, and the error word tells that the output is worthless.
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (dead || mbar_try_loop(bar, parity, kMmTries)) return;
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(bar, parity))
-        if (abort_flag || globaltimer_ns() - t0 > mm_budget()) {
+      for (uint32_t n = dead ? kMmTries : 0; !mbar_try_wait(bar, parity); n++)
+        if (n >= kMmTries && (abort_flag || mm_late(since, n))) {
           abort_flag = 1;
           dead = true;
           break;
