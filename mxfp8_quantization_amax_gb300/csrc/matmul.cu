@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
         for (int c = 0; c < COLS; c += 32) {
           uint32_t(&v)[32] = r[(c / 32) & 1];
-          tmem_wait_loads();
+          tmem_wait_loads(v);
           if (c + 32 < COLS) {
             tmem_load32(r[(c / 32 + 1) & 1], taddr + b * kMmCols + c + 32);
           } else {
