@@ -505,6 +505,7 @@ static fp8q_status run_matmul(const MatmulLaunch& L) {
   if (values == 0) return FP8Q_OK;
   if (L.k == 0) {  // empty sums
     if (L.accumulate) return FP8Q_OK;
+    if (L.kind == kMatmulRowGroups) return launch_matmul_zero_groups(L);
     const cudaError_t e = cudaMemsetAsync(L.out, 0, (size_t)values * (L.out_dt == FP8Q_OUT_FP32 ? 4 : 2), L.stream);
     return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, "cudaMemsetAsync");
   }

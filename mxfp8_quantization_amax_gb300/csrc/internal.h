@@ -184,6 +184,8 @@ struct MatmulLaunch {
   cudaStream_t stream;
 };
 fp8q_status launch_matmul(const MatmulLaunch& L);
+// Row groups without a reduction: zeroes the rows of the groups, no others.
+fp8q_status launch_matmul_zero_groups(const MatmulLaunch& L);
 fp8q_status mm_device_status(bool clear, unsigned* word);
 fp8q_status mm_set_wait_budget(unsigned long long ns);
 fp8q_status mm_set_stall_loads(bool on);

@@ -668,6 +668,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   }
 }
 
+// Groups whose reduction is empty: zeros for their rows, which follow one
+// another from the first group's first to the last one's last.
+template <typename T>
+__global__ void zero_groups_kernel(T* out, const int64_t* off, int groups, int64_t rows, int64_t n) {
+  pdl_wait();
+  const int64_t lo = mm_clamped(off, 0, rows) * n, hi = mm_clamped(off, groups, rows) * n;
+  for (int64_t i = lo + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < hi; i += (int64_t)gridDim.x * blockDim.x) out[i] = T(0);
+  pdl_launch_dependents();
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -807,6 +817,17 @@ fp8q_status launch_matmul(const MatmulLaunch& L) {
   return L.b_block == FP8Q_BLOCK_128X128
              ? launch_mm_out<false, kMmDense>(L.a, L.b, p, L.a_fmt, L.b_fmt, L.out_dt, L.stream)
              : launch_mm_out<true, kMmDense>(L.a, L.b, p, L.a_fmt, L.b_fmt, L.out_dt, L.stream);
+}
+
+fp8q_status launch_matmul_zero_groups(const MatmulLaunch& L) {
+  const int64_t ctas = (L.m * L.n + 255) / 256, most = (int64_t)sm_count() * 8;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most)), block(256);
+  const cudaError_t e =
+      L.out_dt == FP8Q_OUT_FP32
+          ? launch_kernel(zero_groups_kernel<float>, grid, block, 0, L.stream, (float*)L.out, L.off, L.groups, L.m, L.n)
+          : launch_kernel(zero_groups_kernel<uint16_t>, grid, block, 0, L.stream, (uint16_t*)L.out, L.off, L.groups, L.m, L.n);
+  if (e != cudaSuccess) return cuda_fail(e, "zero kernel launch");
+  return check_launch("zero kernel");
 }
 
 fp8q_status mm_device_status(bool clear, unsigned* word) {

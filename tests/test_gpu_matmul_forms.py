@@ -85,3 +85,23 @@ def test_a_short_wait_budget_does_not_end_a_product_that_waits_for_memory(rows):
             assert torch.equal(got, want)
     finally:
         fq.set_wait_budget_ns(1_000_000_000)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offsets", [[0, 4, 9], [3, 3, 8], [2, 2, 2], [-4, 5, 100]])
+@pytest.mark.parametrize("n", [48, 37])
+def test_empty_reduction_of_groups_leaves_the_other_rows_alone(out_dtype, offsets, n):
+    """An empty sum is zero for the groups' rows, and rows in no group are not written."""
+    fq = require_cuda()
+    a, sa = torch.empty(12, 0, dtype=torch.uint8, device="cuda"), torch.empty(12, 0, device="cuda")
+    b = torch.empty(2, n, 0, dtype=torch.uint8, device="cuda")
+    sb = torch.empty(2, 1, 0, device="cuda")
+    out = Guarded((12, n), out_dtype)
+    out.t.fill_(7.0)
+    fq.fp8q_matmul_grouped(a, sa, b, sb, offsets, out_dtype=out_dtype, out=out.t)
+    fq.check_device()
+    out.check()
+    lo, hi = max(offsets[0], 0), min(offsets[-1], 12)
+    want = torch.full_like(out.t, 7.0)
+    want[lo:hi] = 0.0
+    assert torch.equal(out.t, want)
