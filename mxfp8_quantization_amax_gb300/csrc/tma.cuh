@@ -62,29 +62,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
   return true;
 }
 
-// At most `tries` tries in a tight loop.  A failing try by a converged warp
-// sleeps up to 1.4 us and wakes when the phase completes; one by a lone lane
-// returns after 15 cycles, so that a lane that polls floods the barrier unit
-// (measured on a GB300).  Wait with whole warps.
-__device__ __forceinline__ bool mbar_try_loop(uint64_t* bar, uint32_t parity, uint32_t tries) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, %3;\n\t"
-      "again:\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "@p bra there;\n\t"
-      "add.u32 n, n, -1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
-      "@q bra again;\n\t"
-      "there:\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(tries)
-      : "memory");
-  return ok != 0;
-}
-
 // Barrier over `count` threads of the CTA (a multiple of 32) on named
 // barrier `id` (0 is __syncthreads).
 __device__ __forceinline__ void named_barrier_sync(int id, int count) {

@@ -22,6 +22,29 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// At most `tries` tries in a tight loop.  A failing try by a converged warp
+// sleeps up to 1.4 us and wakes when the phase completes; one by a lone lane
+// returns after 15 cycles, so that a lane that polls floods the barrier unit
+// (measured on a GB300).  Wait with whole warps.
+__device__ __forceinline__ bool mbar_try_loop(uint64_t* bar, uint32_t parity, uint32_t tries) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n\t"
+      "again:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra there;\n\t"
+      "add.u32 n, n, -1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra again;\n\t"
+      "there:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(tries)
+      : "memory");
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------------------
 // Tensor memory: 128 lanes x 512 columns of 32 bits.  A whole warp allocates
 // (a power of two of columns, at least 32) and the same warp frees.
