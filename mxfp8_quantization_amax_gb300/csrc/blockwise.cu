@@ -283,16 +283,20 @@ static PFN_cuTensorMapEncodeTiled_v12000 bw_encode_fn() {
 template <int FMT, int BLOCK, int DIR>
 static fp8q_status launch_bw_t(const CUtensorMap& map, const BwParams& p, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)kBwStages * kBwStageBytes;
-  static int per_sm = [smem] {
-    int v = 0;
-    if (cudaFuncSetAttribute(blockwise_kernel<FMT, BLOCK, DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, blockwise_kernel<FMT, BLOCK, DIR>, kBwThreads, smem) !=
-            cudaSuccess ||
-        v < 1)
-      v = 1;
-    return v;
-  }();
+  static PerDevice<bool> allowed;
+  const cudaError_t attr = allow_smem(allowed, blockwise_kernel<FMT, BLOCK, DIR>, smem);
+  if (attr != cudaSuccess) return cuda_fail(attr, "blockwise shared memory");
+  static PerDevice<int> resident;
+  int per_sm = 1;
+  resident.get(current_device(), &per_sm, [&](int* v) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, blockwise_kernel<FMT, BLOCK, DIR>, kBwThreads, smem) !=
+        cudaSuccess)
+      cudaGetLastError();
+    else if (*v > 0)
+      return true;
+    *v = 1;
+    return false;
+  });
   int64_t grid = (int64_t)per_sm * sm_count();
   const int64_t tiles = p.tiles_r * p.tiles_c;
   if (grid > tiles) grid = tiles;

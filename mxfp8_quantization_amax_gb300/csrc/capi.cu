@@ -49,6 +49,13 @@ fp8q_status check_launch(const char* what) {
   return e == cudaSuccess ? FP8Q_OK : cuda_fail(e, what);
 }
 
+int current_device() {
+  int dev = -1;
+  if (cudaGetDevice(&dev) == cudaSuccess) return dev;
+  cudaGetLastError();
+  return -1;
+}
+
 int sm_count() {
   static int cache[64];
   static std::mutex mu;

@@ -453,14 +453,10 @@ static cudaError_t launch_dq_t(const DqParams& p, cudaStream_t s) {
     return v;
   }();
   if (smem > 48 * 1024) {
-    static bool opted = false;
-    if (!opted) {
-      const cudaError_t e = cudaFuncSetAttribute(dequant_kernel<KIND, FMT, OUT>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)(sizeof(int) * (FP8Q_MAX_GROUPS + 4) + kDqMaxTabBytes));
-      if (e != cudaSuccess) return e;
-      opted = true;
-    }
+    static PerDevice<bool> allowed;
+    const cudaError_t e =
+        allow_smem(allowed, dequant_kernel<KIND, FMT, OUT>, sizeof(int) * (FP8Q_MAX_GROUPS + 4) + kDqMaxTabBytes);
+    if (e != cudaSuccess) return e;
   }
   int fit = 0;  // CTAs per SM at this launch's shared memory
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, dequant_kernel<KIND, FMT, OUT>, kDqThreads, smem) !=

@@ -402,8 +402,8 @@ __global__ void __launch_bounds__(kDpThreads, 3) dispatch_kernel(DispatchParams 
 
 template <int FMT, int DIR>
 static fp8q_status launch_dispatch_d(DispatchParams p, cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(dispatch_kernel<FMT, DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       2 * kDpTileBytes);
+  static PerDevice<bool> allowed;
+  const cudaError_t attr = allow_smem(allowed, dispatch_kernel<FMT, DIR>, 2 * kDpTileBytes);
   if (attr != cudaSuccess) return cuda_fail(attr, "dispatch shared memory");
   // Runs as long as leave every SM 12 CTAs, at most 16 tiles (65536 rows of
   // 7168, both copies, an earlier form: 311 us; runs of one tile 409, of a whole

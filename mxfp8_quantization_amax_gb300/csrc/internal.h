@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "../../include/fp8q.h"
+#include "per_device.h"
 
 namespace fp8q {
 
@@ -27,6 +28,22 @@ fp8q_status check_cast_args(const void* x, int32_t dt, int64_t rows, int64_t col
                             const unsigned long long* sat_count_out);
 
 int sm_count();
+// The current device, -1 if there is none.
+int current_device();
+
+// Allows `kernel` `bytes` of dynamic shared memory on the current device, once
+// for each device and `done`.
+template <typename K>
+cudaError_t allow_smem(PerDevice<bool>& done, K kernel, size_t bytes) {
+  cudaError_t e = cudaSuccess;
+  bool ok;
+  done.get(current_device(), &ok, [&](bool* out) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) cudaGetLastError();  // reported here, not by a later launch
+    return *out = e == cudaSuccess;
+  });
+  return e;
+}
 
 #ifndef FP8Q_PDL
 #define FP8Q_PDL 1

@@ -717,10 +717,9 @@ static size_t mm_smem(int groups) {
 // of 2, 36 of 4, 15 of 8, since a cluster stays inside one part of the chip).
 template <int CG, bool SPLIT, bool COLSCALE, bool F32, int MODE>
 static int mm_clusters(int size) {
-  static int found[9];
-  static std::mutex mu;
-  std::lock_guard<std::mutex> lock(mu);
-  if (found[size] == 0) {
+  static PerDevice<int> found[9];
+  int clusters;
+  const bool known = found[size].get(current_device(), &clusters, [&](int* n) {
     const auto kernel = matmul_kernel<CG, SPLIT, COLSCALE, F32, MODE>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -732,14 +731,13 @@ static int mm_clusters(int size) {
     cfg.dynamicSmemBytes = mm_smem<CG, MODE>(MODE == kMmRowGroups ? FP8Q_MAX_GROUPS : 1);
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    int n = 0;
-    found[size] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) ==
-                              cudaSuccess &&
-                          cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0
-                      ? n
-                      : 1;
-  }
-  return found[size];
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(n, kernel, &cfg) == cudaSuccess)
+      return *n > 0;
+    cudaGetLastError();
+    return false;
+  });
+  return known ? clusters : 1;
 }
 
 template <int CG, bool SPLIT, bool COLSCALE, bool F32, int MODE>
@@ -753,14 +751,19 @@ static fp8q_status launch_mm_t(const void* a, const void* b, MmParams p, int fmt
   p.tiles_n = (int)((p.n + kMmCols - 1) / kMmCols);
   const size_t smem = mm_smem<CG, MODE>(p.groups);
   const auto kernel = matmul_kernel<CG, SPLIT, COLSCALE, F32, MODE>;
-  static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (int)mm_smem<CG, MODE>(FP8Q_MAX_GROUPS));
+  static PerDevice<bool> allowed;
+  const cudaError_t attr = allow_smem(allowed, kernel, mm_smem<CG, MODE>(FP8Q_MAX_GROUPS));
   if (attr != cudaSuccess) return cuda_fail(attr, "matmul shared memory");
   // the kernel moves registers between its warpgroups: they must be there
-  static const int regs = [&] {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-  }();
+  static PerDevice<int> launch_regs;
+  int regs = 0;
+  if (!launch_regs.get(current_device(), &regs, [&](int* n) {
+        cudaFuncAttributes f;
+        const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+        *n = e == cudaSuccess ? f.numRegs : 0;
+        return e == cudaSuccess;
+      }))
+    return cuda_fail(cudaGetLastError(), "cudaFuncGetAttributes(matmul)");
   if (regs < kMmRegsLaunch) return fail(FP8Q_ERR_CUDA, "matmul kernel built with %d registers a thread", regs);
   const int64_t per = (p.m + S::kTileRows - 1) / S::kTileRows;
   const int64_t tiles = (MODE == kMmRowGroups ? per + p.groups : MODE == kMmKGroups ? per * p.groups : per) * p.tiles_n;

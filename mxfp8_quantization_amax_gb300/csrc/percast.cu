@@ -1202,16 +1202,19 @@ static cudaError_t launch_fused_t(const KParams& p, int64_t slices, cudaStream_t
 #define FP8Q_PT_CLUSTER 1
 #endif
 // Whether current_cluster_kernel<DT, FMT> can be launched here (the cluster
-// size is non-portable): attributes set once, then at least one cluster
-// must fit.
+// size is non-portable): attributes set once for each device, then at least
+// one cluster must fit.
 template <int DT, int FMT>
 static bool cluster_ready() {
-  static const bool ok = [] {
+  static PerDevice<bool> ready;
+  bool ok = false;
+  ready.get(current_device(), &ok, [](bool* out) {
+    *out = false;
     auto k = current_cluster_kernel<DT, FMT>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kClusterMaxBytes) != cudaSuccess) {
       cudaGetLastError();
-      return false;
+      return true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kClusterCtas);
@@ -1227,10 +1230,11 @@ static bool cluster_ready() {
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      return false;
+      return true;
     }
-    return n > 0;
-  }();
+    *out = n > 0;
+    return true;
+  });
   return ok;
 }
 

@@ -901,16 +901,9 @@ static cudaError_t qs_col_tma(const QsParams& p, cudaStream_t stream, bool* used
   }
   auto kernel = qstats_col_tma_kernel<FMT>;
   constexpr size_t smem = 1024 + (size_t)kQtStages * kQtStageBytes;
-  static bool attr = false;
-  static std::mutex mu;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!attr) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-      attr = true;
-    }
-  }
+  static PerDevice<bool> allowed;
+  const cudaError_t attr = allow_smem(allowed, kernel, smem);
+  if (attr != cudaSuccess) return attr;
   const int64_t blocks = p.rows / 32 * ((p.cols + kQtCols - 1) / kQtCols);
   if (blocks >= INT32_MAX) return cudaSuccess;  // block indices are 32-bit in the kernel
   // each CTA a contiguous range of blocks: one wave of resident CTAs (every
