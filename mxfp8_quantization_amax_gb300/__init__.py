@@ -173,14 +173,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# the stream's address without a Stream object around it, where torch has that
+# the stream's address without a Stream object around it, where torch has that,
+# and the current device without a look at whether CUDA is up (with a tensor on it, it is)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream():
+def _stream(device=None):
+    """The current stream of `device` (the current device's by default)."""
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _dt(x: torch.Tensor) -> int:
@@ -689,21 +692,32 @@ def fp8q_quantize_blockwise(x: torch.Tensor, fmt: int = E4M3, block: int = BLOCK
 # ---------------------------------------------------------------------------
 # products of blockwise FP8 tensors
 # ---------------------------------------------------------------------------
-def _codes(t: torch.Tensor, name: str, dims: int):
-    if not t.is_cuda or t.dtype != torch.uint8 or t.dim() != dims or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dims}-D uint8 CUDA tensor")
+# Every tensor of a call lies on the device of its first operand, `at` (a CPU
+# tensor's index is -1), which is the current one: the kernels get addresses.
+def _device(t: torch.Tensor, name: str) -> int:
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if at != _current_device():
+        raise ValueError(f"{name} is on cuda:{at}, which is not the current device")
+    return at
 
 
-def _floats(t: torch.Tensor, name: str, shape: tuple):
-    if not t.is_cuda or t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of shape {shape}")
+def _codes(t: torch.Tensor, name: str, dims: int, at: int):
+    if t.get_device() != at or t.dtype != torch.uint8 or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dims}-D uint8 tensor on cuda:{at}")
+
+
+def _floats(t: torch.Tensor, name: str, shape: tuple, at: int):
+    if t.get_device() != at or t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on cuda:{at}")
 
 
 def _result(out, shape: tuple, dtype, device):
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not out.is_cuda or out.dtype != dtype or out.shape != shape or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous {dtype} CUDA tensor of shape {shape}")
+    if out.device != device or out.dtype != dtype or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {shape} on {device}")
     return out
 
 
@@ -730,21 +744,22 @@ def fp8q_matmul_blockwise(a: torch.Tensor, a_scale_inv: torch.Tensor, b: torch.T
 
     Fprop: x.q, W.q.  Dgrad: dy.q, W.q_t.  Wgrad: dy.q_t, x.q_t with
     BLOCK_1X128.  accumulate adds to a given float32 out."""
-    _codes(a, "a", 2)
-    _codes(b, "b", 2)
+    at = _device(a, "a")
+    _codes(a, "a", 2, at)
+    _codes(b, "b", 2, at)
     m, k = a.shape
     n = b.shape[0]
     if b.shape[1] != k:
         raise ValueError("a and b must have the same reduction length")
     kb = (k + 127) // 128
-    _floats(a_scale_inv, "a_scale_inv", (m, kb))
-    _floats(b_scale_inv, "b_scale_inv", (n if b_block == BLOCK_1X128 else (n + 127) // 128, kb))
+    _floats(a_scale_inv, "a_scale_inv", (m, kb), at)
+    _floats(b_scale_inv, "b_scale_inv", (n if b_block == BLOCK_1X128 else (n + 127) // 128, kb), at)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     y = _result(out, (m, n), out_dtype, a.device)
     st = (_lib or lib()).fp8q_matmul_blockwise(a.data_ptr(), a_scale_inv.data_ptr(), a_fmt, b.data_ptr(),
                                                b_scale_inv.data_ptr(), b_fmt, b_block, m, n, k, _out_dtype(out_dtype),
-                                               1 if accumulate else 0, y.data_ptr(), _stream())
+                                               1 if accumulate else 0, y.data_ptr(), _stream(at))
     if st:
         _check(st, "fp8q_matmul_blockwise")
     return y
@@ -756,21 +771,22 @@ def fp8q_matmul_grouped(a: torch.Tensor, a_scale_inv: torch.Tensor, b: torch.Ten
     """Rows [group_offsets[g], group_offsets[g+1]) of a [rows, k] times b[g]
     (b [groups, n, k], 128x128 blocks) transposed: out [rows, n].  Rows in no
     group are not written."""
-    _codes(a, "a", 2)
-    _codes(b, "b", 3)
+    at = _device(a, "a")
+    _codes(a, "a", 2, at)
+    _codes(b, "b", 3, at)
     rows, k = a.shape
     groups, n = b.shape[:2]
     if b.shape[2] != k:
         raise ValueError("a and b must have the same reduction length")
     kb = (k + 127) // 128
-    _floats(a_scale_inv, "a_scale_inv", (rows, kb))
-    _floats(b_scale_inv, "b_scale_inv", (groups, (n + 127) // 128, kb))
+    _floats(a_scale_inv, "a_scale_inv", (rows, kb), at)
+    _floats(b_scale_inv, "b_scale_inv", (groups, (n + 127) // 128, kb), at)
     off, g = _group_offsets(group_offsets, a.device)
     if g != groups:
         raise ValueError("b must hold one matrix per group")
     y = _result(out, (rows, n), out_dtype, a.device)
     _check(lib().fp8q_matmul_grouped(_ptr(a), _ptr(a_scale_inv), a_fmt, _ptr(b), _ptr(b_scale_inv), b_fmt, _ptr(off),
-                                     groups, rows, n, k, _out_dtype(out_dtype), _ptr(y), _stream()),
+                                     groups, rows, n, k, _out_dtype(out_dtype), _ptr(y), _stream(at)),
            "fp8q_matmul_grouped")
     return y
 
@@ -782,22 +798,23 @@ def fp8q_matmul_grouped_wgrad(a_t: torch.Tensor, a_scale_inv_t: torch.Tensor, b_
     """out[g] = a_t[:, rows of g] times b_t[:, rows of g] transposed, for the
     transposed copies a_t [m, rows] and b_t [n, rows] (128x1 groups along the
     rows): out [groups, m, n].  group_offsets are multiples of 128."""
-    _codes(a_t, "a_t", 2)
-    _codes(b_t, "b_t", 2)
+    at = _device(a_t, "a_t")
+    _codes(a_t, "a_t", 2, at)
+    _codes(b_t, "b_t", 2, at)
     m, rows = a_t.shape
     n = b_t.shape[0]
     if b_t.shape[1] != rows:
         raise ValueError("a_t and b_t must have the same number of rows to reduce over")
     rb = (rows + 127) // 128
-    _floats(a_scale_inv_t, "a_scale_inv_t", (m, rb))
-    _floats(b_scale_inv_t, "b_scale_inv_t", (n, rb))
+    _floats(a_scale_inv_t, "a_scale_inv_t", (m, rb), at)
+    _floats(b_scale_inv_t, "b_scale_inv_t", (n, rb), at)
     off, groups = _group_offsets(group_offsets, a_t.device)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     y = _result(out, (groups, m, n), out_dtype, a_t.device)
     _check(lib().fp8q_matmul_grouped_wgrad(_ptr(a_t), _ptr(a_scale_inv_t), a_fmt, _ptr(b_t), _ptr(b_scale_inv_t),
                                            b_fmt, _ptr(off), groups, rows, m, n, _out_dtype(out_dtype),
-                                           1 if accumulate else 0, _ptr(y), _stream()),
+                                           1 if accumulate else 0, _ptr(y), _stream(at)),
            "fp8q_matmul_grouped_wgrad")
     return y
 
@@ -805,10 +822,10 @@ def fp8q_matmul_grouped_wgrad(a_t: torch.Tensor, a_scale_inv_t: torch.Tensor, b_
 # ---------------------------------------------------------------------------
 # the expert layer: routing, row order, gather, weighted sum
 # ---------------------------------------------------------------------------
-def _matrix(t: torch.Tensor, name: str, dtypes: tuple, shape: tuple | None = None):
-    if not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes or not t.is_contiguous() or (
+def _matrix(t: torch.Tensor, name: str, dtypes: tuple, at: int, shape: tuple | None = None):
+    if t.get_device() != at or t.dim() != 2 or t.dtype not in dtypes or not t.is_contiguous() or (
             shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor of {' or '.join(map(str, dtypes))}"
+        raise ValueError(f"{name} must be a contiguous 2-D tensor of {' or '.join(map(str, dtypes))} on cuda:{at}"
                          + (f" and shape {shape}" if shape is not None else ""))
 
 
@@ -824,11 +841,12 @@ def fp8q_moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX,
 
     Experts are chosen by score + bias among the top_groups best of num_groups
     groups; the weights hold the scores without the bias (see the C header)."""
-    _matrix(logits, "logits", _VALUES)
+    at = _device(logits, "logits")
+    _matrix(logits, "logits", _VALUES, at)
     tokens, experts = logits.shape
-    if bias is not None and (not bias.is_cuda or bias.dtype != torch.float32 or bias.shape != (experts,)
+    if bias is not None and (bias.get_device() != at or bias.dtype != torch.float32 or bias.shape != (experts,)
                              or not bias.is_contiguous()):
-        raise ValueError("bias must be a contiguous float32 CUDA tensor with one value per expert")
+        raise ValueError(f"bias must be a contiguous float32 tensor with one value per expert on cuda:{at}")
     shape, dev = (tokens, top_k), logits.device
     if out is None:
         w, ids = torch.empty(shape, dtype=torch.float32, device=dev), torch.empty(shape, dtype=torch.int32, device=dev)
@@ -836,7 +854,7 @@ def fp8q_moe_route(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX,
         w, ids = _result(out.get("weights"), shape, torch.float32, dev), _result(out.get("ids"), shape, torch.int32, dev)
     st = (_lib or lib()).fp8q_moe_route(logits.data_ptr(), _IN[logits.dtype], tokens, experts, top_k, score, _ptr(bias),
                                         num_groups, top_groups, 1 if renormalize else 0, weight_scale, w.data_ptr(),
-                                        ids.data_ptr(), _stream())
+                                        ids.data_ptr(), _stream(at))
     if st:
         _check(st, "fp8q_moe_route")
     return {"weights": w, "ids": ids}
@@ -847,16 +865,17 @@ def fp8q_moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, d_weights: 
                             out: torch.Tensor | None = None) -> torch.Tensor:
     """The gradient of fp8q_moe_route's weights: d_logits, shaped and typed like
     logits; NaN for every logit of a token whose weights are NaN."""
-    _matrix(logits, "logits", _VALUES)
+    at = _device(logits, "logits")
+    _matrix(logits, "logits", _VALUES, at)
     tokens, experts = logits.shape
-    _matrix(ids, "ids", (torch.int32,))
-    _matrix(d_weights, "d_weights", (torch.float32,), tuple(ids.shape))
+    _matrix(ids, "ids", (torch.int32,), at)
+    _matrix(d_weights, "d_weights", (torch.float32,), at, tuple(ids.shape))
     if ids.shape[0] != tokens:
         raise ValueError("ids must hold one row per token")
     d = torch.empty_like(logits) if out is None else _result(out, (tokens, experts), logits.dtype, logits.device)
     st = (_lib or lib()).fp8q_moe_route_backward(logits.data_ptr(), _IN[logits.dtype], tokens, experts, ids.shape[1], score,
                                                  1 if renormalize else 0, weight_scale, ids.data_ptr(),
-                                                 d_weights.data_ptr(), d.data_ptr(), _stream())
+                                                 d_weights.data_ptr(), d.data_ptr(), _stream(at))
     if st:
         _check(st, "fp8q_moe_route_backward")
     return d
@@ -871,7 +890,8 @@ def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, align: int = 1, out: dict
     """The experts' row order of ids [tokens, top_k]: dict(offsets int64
     [experts + 1], row_of int32 [tokens, top_k], src int32 [rows]), each
     expert's rows padded to a multiple of align."""
-    _matrix(ids, "ids", (torch.int32,))
+    at = _device(ids, "ids")
+    _matrix(ids, "ids", (torch.int32,), at)
     L = lib()
     slots = ids.numel()
     rows = L.fp8q_moe_rows(slots, num_experts, align)
@@ -889,16 +909,16 @@ def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, align: int = 1, out: dict
     need = L.fp8q_moe_plan_workspace_bytes(slots, num_experts)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     st = L.fp8q_moe_plan(ids.data_ptr(), slots, num_experts, align, rows, offsets.data_ptr(), row_of.data_ptr(),
-                         src.data_ptr(), _ptr(ws), need, _stream())
+                         src.data_ptr(), _ptr(ws), need, _stream(at))
     if st:
         _check(st, "fp8q_moe_plan")
     return {"offsets": offsets, "row_of": row_of, "src": src}
 
 
-def _sources(plan: dict):
+def _sources(plan: dict, at: int):
     src = plan["src"]
-    if not src.is_cuda or src.dtype != torch.int32 or src.dim() != 1 or not src.is_contiguous():
-        raise ValueError("the plan's src must be a contiguous 1-D int32 CUDA tensor")
+    if src.get_device() != at or src.dtype != torch.int32 or src.dim() != 1 or not src.is_contiguous():
+        raise ValueError(f"the plan's src must be a contiguous 1-D int32 tensor on cuda:{at}")
     return src
 
 
@@ -907,10 +927,11 @@ def fp8q_moe_dispatch(x: torch.Tensor, plan: dict, fmt: int = E4M3, direction: i
     """x [tokens, cols] gathered in the plan's order and quantized in 1x128
     groups: fp8q_quantize_blockwise's dict for the gathered rows (zeros where
     the plan has padding)."""
-    _matrix(x, "x", (torch.bfloat16,))
+    at = _device(x, "x")
+    _matrix(x, "x", (torch.bfloat16,), at)
     tokens, cols = x.shape
-    src, row_of = _sources(plan), plan["row_of"]
-    _matrix(row_of, "row_of", (torch.int32,))
+    src, row_of = _sources(plan, at), plan["row_of"]
+    _matrix(row_of, "row_of", (torch.int32,), at)
     if row_of.shape[0] != tokens:
         raise ValueError("the plan must have one row of slots per token")
     rows = src.numel()
@@ -925,7 +946,7 @@ def fp8q_moe_dispatch(x: torch.Tensor, plan: dict, fmt: int = E4M3, direction: i
         si_t = _result(o.get("scale_inv_t"), (cols, tr), torch.float32, dev)
     st = (_lib or lib()).fp8q_moe_dispatch(x.data_ptr(), 0, tokens, cols, max(row_of.shape[1], 1), src.data_ptr(), rows, fmt,
                                            1 if pow2_scales else 0, direction, _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t),
-                                           _stream())
+                                           _stream(at))
     if st:
         _check(st, "fp8q_moe_dispatch")
     return {"q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
@@ -935,16 +956,17 @@ def fp8q_moe_combine(y: torch.Tensor, plan: dict, weights: torch.Tensor | None =
                      out: torch.Tensor | None = None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * y[row_of[t, j]] for y [rows, cols] in the
     plan's order; without weights, the gradient of the dispatch."""
-    _matrix(y, "y", _VALUES)
+    at = _device(y, "y")
+    _matrix(y, "y", _VALUES, at)
     row_of = plan["row_of"]
-    _matrix(row_of, "row_of", (torch.int32,))
+    _matrix(row_of, "row_of", (torch.int32,), at)
     if weights is not None:
-        _matrix(weights, "weights", (torch.float32,), tuple(row_of.shape))
+        _matrix(weights, "weights", (torch.float32,), at, tuple(row_of.shape))
     rows, cols = y.shape
     tokens, top_k = row_of.shape
     o = _result(out, (tokens, cols), y.dtype, y.device)
     st = (_lib or lib()).fp8q_moe_combine(y.data_ptr(), _IN[y.dtype], rows, cols, row_of.data_ptr(), _ptr(weights), tokens,
-                                          top_k, o.data_ptr(), _stream())
+                                          top_k, o.data_ptr(), _stream(at))
     if st:
         _check(st, "fp8q_moe_combine")
     return o
@@ -954,13 +976,14 @@ def fp8q_moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, plan: dict, 
                               out: dict | None = None) -> dict:
     """The gradients of fp8q_moe_combine: dict(d_y like y, zero in padding rows;
     d_weights float32 [tokens, top_k])."""
-    _matrix(y, "y", _VALUES)
-    row_of, src = plan["row_of"], _sources(plan)
-    _matrix(row_of, "row_of", (torch.int32,))
+    at = _device(y, "y")
+    _matrix(y, "y", _VALUES, at)
+    row_of, src = plan["row_of"], _sources(plan, at)
+    _matrix(row_of, "row_of", (torch.int32,), at)
     tokens, top_k = row_of.shape
     rows, cols = y.shape
-    _matrix(d_out, "d_out", (y.dtype,), (tokens, cols))
-    _matrix(weights, "weights", (torch.float32,), (tokens, top_k))
+    _matrix(d_out, "d_out", (y.dtype,), at, (tokens, cols))
+    _matrix(weights, "weights", (torch.float32,), at, (tokens, top_k))
     if src.numel() != rows:
         raise ValueError("y must have the plan's rows")
     if out is None:
@@ -970,7 +993,7 @@ def fp8q_moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, plan: dict, 
         d_w = _result(out.get("d_weights"), (tokens, top_k), torch.float32, y.device)
     st = (_lib or lib()).fp8q_moe_combine_backward(d_out.data_ptr(), y.data_ptr(), _IN[y.dtype], rows, cols,
                                                    row_of.data_ptr(), src.data_ptr(), weights.data_ptr(), tokens, top_k,
-                                                   d_y.data_ptr(), d_w.data_ptr(), _stream())
+                                                   d_y.data_ptr(), d_w.data_ptr(), _stream(at))
     if st:
         _check(st, "fp8q_moe_combine_backward")
     return {"d_y": d_y, "d_weights": d_w}
