@@ -153,3 +153,25 @@ def test_weights_of_experts_that_a_bias_lifts_over_a_better_one(dtype, groups, t
     size = 2.5 * torch.softmax(x[:, :4].double(), 1) * d.double().abs().sum(1, keepdim=True)
     tol = 2 * (16 + 2 * 40 + 4) * U * size + leaf.grad[:, :4].abs() * (2.0 ** -8 if dtype == torch.bfloat16 else U)
     assert ((got[:, :4].double() - leaf.grad[:, :4]).abs() <= tol).all() and (got[:, 4:] == 0).all()
+
+
+@pytest.mark.parametrize("experts,top_k", [(8, 2), (33, 4), (64, 8), (128, 6), (200, 5), (256, 8), (512, 16), (1000, 32), (1024, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_plain_softmax_gradient_of_every_expert(experts, top_k, dtype):
+    """dx_e = c p_e (d_e [e chosen] - sum_j d_j p_j), each element to (2 (16 + 2 range + E / 32) + k) u of its own
+    terms and the output's rounding.  The experts not chosen have gradients far above that bound, so that a
+    kernel that leaves them out fails."""
+    fq = require_cuda()
+    x = torch.randn(65, experts, device="cuda", generator=gen(experts + top_k)).to(dtype)
+    ids = fq.fp8q_moe_route(x, top_k, renormalize=False)["ids"]
+    d = torch.randn(65, top_k, device="cuda", generator=gen(5))
+    got = fq.fp8q_moe_route_backward(x, ids, d, 0, False, 2.5).double()
+    p = torch.softmax(x.double(), 1)
+    g = torch.zeros_like(p).scatter(1, ids.long(), 2.5 * d.double())
+    want = p * (g - (g * p).sum(1, keepdim=True))
+    size = p * (g.abs() + (g * p).abs().sum(1, keepdim=True))
+    rel = (2 * (16 + 2 * float(x.float().max() - x.float().min()) + experts / 32) + top_k) * U
+    tol = rel * size + (2.0 ** -8 if dtype == torch.bfloat16 else U) * want.abs()
+    assert ((got - want).abs() <= tol).all()
+    rest = torch.ones_like(p, dtype=torch.bool).scatter(1, ids.long(), False)
+    assert (want[rest].norm() > 50 * tol[rest].norm()) and (got[rest] != 0).all()
