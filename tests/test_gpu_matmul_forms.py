@@ -105,3 +105,69 @@ def test_empty_reduction_of_groups_leaves_the_other_rows_alone(out_dtype, offset
     want = torch.full_like(out.t, 7.0)
     want[lo:hi] = 0.0
     assert torch.equal(out.t, want)
+
+
+@pytest.mark.parametrize("m,n,k", [(2700, 2820, 400), (100, 40000, 400), (2700, 2820, 128)])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_column_scales_over_several_tiles(m, n, k, out_dtype):
+    """More tiles than pairs (11 x 12) or CTAs (157), with reductions that are no multiple of the scales' four
+    blocks or the two of tensor memory: the rings go on from one tile to the next."""
+    fq = require_cuda()
+    g = gen(m + k)
+    kb = -(-k // 128)
+    a, b = codes(g, (m, k), 1), codes(g, (n, k), 0)
+    sa, sb = scales(g, (m, kb)), scales(g, (n, kb))
+    out = Guarded((m, n), out_dtype)
+    fq.fp8q_matmul_blockwise(a, sa, b, sb, 1, 0, 1, out_dtype, out=out.t)
+    fq.check_device()
+    out.check()
+    check(out.t, values(a, sa, 1, 1), values(b, sb, 0, 1))
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grouped_wgrad_over_several_tiles(accumulate):
+    """9 experts of 4 x 5 tiles over 76 pairs, with 0 to 11 blocks of rows each."""
+    fq = require_cuda()
+    g = gen(21)
+    m, n = 1000, 1230
+    blocks = [3, 0, 1, 11, 2, 5, 0, 7, 4]
+    off = [0]
+    for c in blocks:
+        off.append(off[-1] + 128 * c)
+    rows = off[-1]
+    a, b = codes(g, (m, rows), 1), codes(g, (n, rows), 0)
+    sa, sb = scales(g, (m, rows // 128)), scales(g, (n, rows // 128))
+    out = Guarded((len(blocks), m, n), torch.float32)
+    start = torch.randn(len(blocks), m, n, device="cuda", generator=g)
+    out.t.copy_(start)
+    fq.fp8q_matmul_grouped_wgrad(a, sa, b, sb, off, 1, 0, accumulate=accumulate, out=out.t)
+    fq.check_device()
+    out.check()
+    av, bv = values(a, sa, 1, 1), values(b, sb, 0, 1)
+    for i in range(len(blocks)):
+        lo, hi = off[i], off[i + 1]
+        check(out.t[i], av[:, lo:hi], bv[:, lo:hi], start[i].double() if accumulate else None)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("a_fmt", [0, 1])
+def test_grouped_pairs_over_several_tiles(out_dtype, a_fmt):
+    """Groups of more than 128 rows on average take pairs: 14 row tiles of 12 column tiles over 76 pairs, from
+    any row, with groups that are empty or end inside a tile."""
+    fq = require_cuda()
+    g = gen(22)
+    off, n, k = [5, 5, 700, 701, 1500, 1756, 3000], 3000, 656
+    rows = off[-1] + 20
+    a, b = codes(g, (rows, k), a_fmt), codes(g, (6, n, k), 0)
+    sa, sb = scales(g, (rows, 6)), scales(g, (6, 24, 6))
+    out = Guarded((rows, n), out_dtype)
+    out.t.fill_(7.0)
+    fq.fp8q_matmul_grouped(a, sa, b, sb, off, a_fmt, 0, out_dtype, out=out.t)
+    fq.check_device()
+    out.check()
+    av = values(a, sa, a_fmt, 1)
+    for i in range(6):
+        lo, hi = off[i], off[i + 1]
+        if hi > lo:
+            check(out.t[lo:hi], av[lo:hi], values(b[i], sb[i], 0, 128))
+    assert (out.t[:5] == 7.0).all() and (out.t[3000:] == 7.0).all()
