@@ -12,8 +12,8 @@
 //
 // Gradient, with d_j the gradient of w_j and g_j that of s_j:
 //   renormalised  g_j = c * (d_j - sum_i d_i s_i / S) / S,  S = sum_i s_i
-//                 (d less that of the best expert, r: nothing cancels where it
-//                 has nearly all of S)
+//                 (d less that of an expert with more than half of S: nothing
+//                 cancels where it has nearly all)
 //   else          g_j = c * d_j
 //   sigmoid       dx_j = g_j s_j (1 - s_j),  0 for experts not chosen
 //   softmax       dx_e = p_e (g_e - sum_j g_j p_j); renormalised, the last
@@ -366,17 +366,23 @@ __global__ void __launch_bounds__(kRtWarps * 32) route_backward_chosen_kernel(Rt
         rt_store<DT>(row, i, 0.0f);
       }
     }
-    float s = 0.0f, dx, most = x;
+    float s = 0.0f, dx;
+    if constexpr (SOFTMAX) {
+      float most = x;
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-    if (id >= 0) s = SOFTMAX ? expf(x - most) : rt_sigmoid(x);
+      for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+      if (id >= 0) s = expf(x - most);
+    } else if (id >= 0) {
+      s = rt_sigmoid(x);
+    }
     if (p.renorm) {
       const float all = total(s);
       const float share = all != 0.0f ? __fdiv_rn(s, all) : 0.0f;
-      // d less the best expert's, so that what it has of the mean is exactly
-      // 0: of d - mean nothing would be left where its share is nearly 1
-      const uint32_t best = __ballot_sync(kFull, id >= 0 && x == most) >> (lane & -L) & (kFull >> (32 - L));
-      const float r = __shfl_sync(kFull, d, (lane & -L) + (best ? __ffs(best) - 1 : 0));
+      // Less the d of the one expert that may have more than half, so that what
+      // it has of the mean is exactly 0: of its d - mean nothing would be left
+      // where its share is nearly 1.  (Taken off always, one more rounding
+      // makes usual gradients a quarter less exact.)
+      const float r = total(share > 0.5f ? d : 0.0f);
       d = id >= 0 ? __fsub_rn(d, r) : 0.0f;
       const float mean = total(__fmul_rn(d, share));
       // p_j g_j (softmax) and g_j s_j (sigmoid) are both c (d_j - mean) s_j / S
