@@ -27,10 +27,6 @@
 // Consumer barriers are named barriers among the consumer warps only; every
 // bounded wait's outcome is combined over all of them first (bar.red.or), so
 // they give up together and no barrier is left waiting.
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "fp8q_device.cuh"
 #include "internal.h"
 #include "tma.cuh"
@@ -266,20 +262,6 @@ __global__ void __launch_bounds__(kBwThreads, 3) blockwise_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-static PFN_cuTensorMapEncodeTiled_v12000 bw_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
-  });
-  return fn;
-}
-
 template <int FMT, int BLOCK, int DIR>
 static fp8q_status launch_bw_t(const CUtensorMap& map, const BwParams& p, cudaStream_t s) {
   const size_t smem = 1024 + (size_t)kBwStages * kBwStageBytes;
@@ -316,7 +298,7 @@ static fp8q_status launch_bw_dir(const CUtensorMap& map, const BwParams& p, int 
 
 fp8q_status launch_blockwise(const void* x, int64_t rows, int64_t cols, int fmt, int block, int pow2, int dir,
                              uint8_t* q, float* s, uint8_t* q_t, float* s_t, cudaStream_t stream) {
-  auto enc = bw_encode_fn();
+  auto enc = tensor_map_encoder();
   if (!enc) return fail(FP8Q_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   CUtensorMap map;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};

@@ -2,6 +2,7 @@
 // units (not part of the public ABI).
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -28,6 +29,8 @@ fp8q_status check_cast_args(const void* x, int32_t dt, int64_t rows, int64_t col
                             const unsigned long long* sat_count_out);
 
 int sm_count();
+// The driver's cuTensorMapEncodeTiled, null if it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // The current device, -1 if there is none.
 int current_device();
 

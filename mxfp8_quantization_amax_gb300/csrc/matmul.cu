@@ -28,10 +28,6 @@
 // (6.7 TB/s of weights).  128-column tiles with four blocks in tensor memory
 // were slower (174 against 118 us at 4864 x 2048 x 16384): a warp of sums
 // needs some 600 cycles a block whatever its columns.
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "fp8q_device.cuh"
 #include "internal.h"
 #include "umma.cuh"
@@ -681,22 +677,9 @@ __global__ void zero_groups_kernel(T* out, const int64_t* off, int groups, int64
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-static PFN_cuTensorMapEncodeTiled_v12000 mm_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
-  });
-  return fn;
-}
-
 // Codes [rows][k], boxes of 128 codes x box_rows.
 static fp8q_status mm_map(CUtensorMap* map, const void* q, int64_t rows, int64_t k, int box_rows) {
-  auto enc = mm_encode_fn();
+  auto enc = tensor_map_encoder();
   if (!enc) return fail(FP8Q_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)k};

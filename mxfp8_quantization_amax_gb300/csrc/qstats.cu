@@ -31,10 +31,6 @@
 // Totals.  Each CTA writes its partial sums to the workspace; the last CTA
 // to finish (atomic ticket) adds them in a fixed order, so results repeat
 // exactly from run to run on one GPU.
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "fp8q_device.cuh"
 #include "internal.h"
 #include "tma.cuh"
@@ -850,19 +846,6 @@ __global__ void __launch_bounds__(kQtThreads, 4)
   qs_finish<kQtThreads>(p, a);
 }
 
-static PFN_cuTensorMapEncodeTiled_v12000 qs_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
-  });
-  return fn;
-}
-
 // Launches the TMA-fed columnwise kernel; *used = false when the call does
 // not qualify (grouped, FP32, ragged rows, unaligned buffers) or no tensor
 // map could be encoded, and the caller takes the kernel above.
@@ -872,7 +855,7 @@ static cudaError_t qs_col_tma(const QsParams& p, cudaStream_t stream, bool* used
   if (!(p.off == nullptr || p.G <= 1) || p.rows % 32 != 0 || p.rows <= 0 || p.cols <= 0 ||
       ((uintptr_t)p.x & 15u) != 0 || ((uintptr_t)p.q & 15u) != 0)
     return cudaSuccess;
-  auto enc = qs_encode_fn();
+  auto enc = tensor_map_encoder();
   if (!enc) return cudaSuccess;
   CUtensorMap xmap, qmap;
   {
