@@ -469,7 +469,9 @@ FP8Q_API fp8q_status fp8q_quantize_blockwise(const void* x, int32_t dt, int64_t 
  *   out          device BF16 or FP32 [m][n] (out_dt, fp8q_out_dtype)
  *   accumulate   nonzero: out += the product (FP32 output only)
  * m and n are any, k % 16 == 0 (FP8Q_ERR_UNSUPPORTED otherwise); k == 0
- * gives zeros.  NaN and Inf codes propagate as in the sum above.
+ * gives zeros.  NaN and Inf codes propagate as in the sum above.  sa * sb is
+ * formed first, in FP32: where that product leaves FP32's normal range a block
+ * loses digits or overflows, even if its sum would not have.
  */
 FP8Q_API fp8q_status fp8q_matmul_blockwise(const uint8_t* a, const float* a_scale_inv, int32_t a_fmt,
                                            const uint8_t* b, const float* b_scale_inv, int32_t b_fmt,

@@ -22,10 +22,11 @@
 // block's products to the sums' warps 870 cycles, 600 to 800 until its place
 // is free again, 250 until the next issue: 830 cycles a block of K, of which
 // the products are 512.  A packed multiply a value for column scales makes it
-// 1390.  Measured: 12345 x 4096 x 14336 560 us (2.6 PFLOP/s; 615 in a long run
-// under the power limit), FP32 14336 x 4096 x 16384 with column scales 1108 us,
-// 65536 rows over 64 experts of 4096 x 7168 1600 us, 128 rows over them 242 us
-// (6.7 TB/s of weights).  128-column tiles with four blocks in tensor memory
+// 1390; their kernels also spill (56 to 246 bytes a thread).  Measured: 12345 x
+// 4096 x 14336 604 to 620 us (2.3 to 2.4 PFLOP/s, at the power limit), FP32 14336
+// x 4096 x 16384 with column scales 1115 to 1130 us, 65536 rows over 64 experts
+// of 4096 x 7168 1800 to 1870 us, 128 rows over them 234 to 247 us (6.4 to 6.8
+// TB/s of the weights that some row reaches).  128-column tiles with four blocks in tensor memory
 // were slower (174 against 118 us at 4864 x 2048 x 16384): a warp of sums
 // needs some 600 cycles a block whatever its columns.
 #include "fp8q_device.cuh"
