@@ -1562,20 +1562,30 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // Resident CTAs per SM for `kernel` with `smem` dynamic bytes (cached per
-// instantiation; recomputed when a call needs more shared memory).
+// instantiation and device; recomputed when a call needs more shared memory).
+struct MxResident {
+  size_t attr;
+  int per_sm;
+};
 template <typename K>
-static fp8q_status ctas_per_sm(K kernel, int threads, size_t smem, size_t* attr, int* per_sm, std::mutex* mu,
-                               int* out) {
-  std::lock_guard<std::mutex> lock(*mu);
-  if (smem > *attr) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(mxfp8)");
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
-    *per_sm = n;
-    *attr = smem;
+static fp8q_status ctas_per_sm(K kernel, int threads, size_t smem, PerDevice<MxResident>& cache, int* out) {
+  MxResident r = {};
+  cudaError_t e = cudaSuccess;
+  cache.update(current_device(), [&](MxResident* v) {
+    if (smem > v->attr) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return;
+      int n = 0;
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
+      *v = MxResident{smem, n};
+    }
+    r = *v;
+  });
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, "cudaFuncSetAttribute(mxfp8)");
   }
-  *out = *per_sm;
+  *out = r.per_sm;
   return FP8Q_OK;
 }
 
@@ -1602,11 +1612,9 @@ static fp8q_status launch_tma(const MxParams& p, cudaStream_t s) {
   q.super = BAND ? 1 : (p.off != nullptr ? FP8Q_MX_SUPER_GROUPED : FP8Q_MX_SUPER);
   const size_t smem = 1024 + (size_t)kStages * kStageBytes + (LEAN ? 0 : 2 * sizeof(int) * (p.G + 1));
   auto kernel = LEAN ? mx_lean_kernel<FMT, DIR, EXT> : BAND ? mx_band_kernel<FMT, DIR, EXT, MMA> : mx_tma_kernel<FMT, DIR, EXT, MMA>;
-  static size_t attr = 0;
-  static int per_sm_cache = 0;
-  static std::mutex mu;
+  static PerDevice<MxResident> resident;
   int per_sm = 0;
-  fp8q_status st = ctas_per_sm(kernel, kTmaThreads, smem, &attr, &per_sm_cache, &mu, &per_sm);
+  fp8q_status st = ctas_per_sm(kernel, kTmaThreads, smem, resident, &per_sm);
   if (st != FP8Q_OK) return st;
   // units: bands x strips, or (over any valid offsets) blocks per group
   // rounded up to `super`, x strips
@@ -1630,11 +1638,9 @@ static fp8q_status launch_f32(const MxParams& p, cudaStream_t s) {
   MxParams q = p;
   q.super = 1;
   const size_t smem = (size_t)kTileRows * kTileCols * 4 + 2 * sizeof(int) * (p.G + 1);
-  static size_t attr = 0;
-  static int per_sm_cache = 0;
-  static std::mutex mu;
+  static PerDevice<MxResident> resident;
   int per_sm = 0;
-  fp8q_status st = ctas_per_sm(mx_f32_kernel<FMT, DIR>, kConsumers, smem, &attr, &per_sm_cache, &mu, &per_sm);
+  fp8q_status st = ctas_per_sm(mx_f32_kernel<FMT, DIR>, kConsumers, smem, resident, &per_sm);
   if (st != FP8Q_OK) return st;
   const int64_t max_units = ((p.rows + 31) / 32 + p.G) * p.strips;
   int64_t grid = (int64_t)per_sm * sm_count();

@@ -716,20 +716,15 @@ template <int EF, int DIR, bool SAT>
 static cudaError_t lt_launch(const CUtensorMap& map, const LowParams& p, cudaStream_t stream) {
   auto kernel = mxlow_tma_kernel<EF, DIR, SAT>;
   constexpr size_t smem = 1024 + (size_t)kLtStages * kLtStageBytes;
-  static bool attr = false;
-  static int per_sm = 1;
-  static std::mutex mu;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!attr) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kLtThreads, smem) != cudaSuccess ||
-          per_sm < 1)
-        per_sm = 1;
-      attr = true;
-    }
-  }
+  static PerDevice<bool> allowed;
+  const cudaError_t attr = allow_smem(allowed, kernel, smem);
+  if (attr != cudaSuccess) return attr;
+  static PerDevice<int> resident;
+  int per_sm = 1;
+  resident.get(current_device(), &per_sm, [&](int* v) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kernel, kLtThreads, smem) != cudaSuccess || *v < 1) *v = 1;
+    return true;
+  });
   const int64_t units = ((p.rows + 31) / 32 + kLtUnit - 1) / kLtUnit * ((p.cols + kLtCols - 1) / kLtCols);
   // one CTA per unit (the hardware's block scheduler balances the tail), or
   // a persistent grid of every resident slot

@@ -25,6 +25,17 @@ class PerDevice {
     return true;
   }
 
+  // Shows change(T*) the device's value, T{} at first, alone.
+  template <typename F>
+  void update(int device, F change) {
+    if (device < 0 || device >= kDevices) {
+      T v{};
+      return change(&v);
+    }
+    std::lock_guard<std::mutex> lock(mu_);
+    change(&value_[device]);
+  }
+
  private:
   std::mutex mu_;
   bool have_[kDevices] = {};

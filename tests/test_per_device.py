@@ -40,3 +40,33 @@ def test_once_for_each_device(tmp_path):
     inc = os.path.join(ROOT, "mxfp8_quantization_amax_gb300", "csrc")
     subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", inc, "-o", str(exe), str(src)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+UPDATES = r"""
+#include "per_device.h"
+
+int main() {
+  fp8q::PerDevice<int> p;
+  int seen = -1;
+  auto add = [&](int n) { return [&seen, n](int* v) { seen = *v; *v += n; }; };
+  p.update(2, add(5));
+  if (seen != 0) return 1;
+  p.update(2, add(1));
+  if (seen != 5) return 2;
+  p.update(3, add(1));
+  if (seen != 0) return 3;
+  p.update(2, add(0));
+  if (seen != 6) return 4;
+  p.update(64, add(9));
+  p.update(64, add(9));
+  return seen == 0 ? 0 : 5;
+}
+"""
+
+
+def test_updates_are_each_device_s_own(tmp_path):
+    src, exe = tmp_path / "t.cc", tmp_path / "t"
+    src.write_text(UPDATES)
+    inc = os.path.join(ROOT, "mxfp8_quantization_amax_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", inc, "-o", str(exe), str(src)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
