@@ -25,7 +25,7 @@
 // 1390; their kernels also spill (56 to 246 bytes a thread).  Measured: 12345 x
 // 4096 x 14336 604 to 620 us (2.3 to 2.4 PFLOP/s, at the power limit), FP32 14336
 // x 4096 x 16384 with column scales 1115 to 1130 us, 65536 rows over 64 experts
-// of 4096 x 7168 1800 to 1870 us, 128 rows over them 234 to 247 us (6.4 to 6.8
+// of 4096 x 7168 1800 to 1870 us, 128 rows over them 234 to 253 us (6.3 to 6.8
 // TB/s of the weights that some row reaches).  128-column tiles with four blocks in tensor memory
 // were slower (174 against 118 us at 4864 x 2048 x 16384): a warp of sums
 // needs some 600 cycles a block whatever its columns.
