@@ -626,6 +626,86 @@ FP8Q_API fp8q_status fp8q_moe_combine_backward(const void* d_out, const void* y,
                                                float* d_weights, void* stream);
 
 /*
+ * Root-mean-square norm of the rows, with the residual's addition before it
+ * and the 8-bit copies that the next product reads (the pages quantize a
+ * product's input; this makes that input):
+ *   h = x + residual, rounded to the residual's type; x itself without one
+ *   rstd[r] = 1 / sqrt(sum_c h[r][c]^2 / cols + eps)
+ *   y[r][c] = h[r][c] * rstd[r] * weight[c]
+ * The copies are those of fp8q_quantize_blockwise with 1x128 groups for the
+ * FP32 values of y.  Arithmetic is FP32: a row whose sum of squares
+ * overflows FP32 (values from some 1e19 on) gives rstd 0, one without
+ * any nonzero value gives y 0 (NaN with eps 0).
+ *   x          device, type dt (BF16 or FP32), [rows][cols], 1 <= cols <= 32768
+ *   residual   device, type residual_dt, [rows][cols], or NULL
+ *   weight     device, type weight_dt, [cols]
+ *   dir        0 (no copy), MXFP8_ROW, MXFP8_COL or MXFP8_BOTH
+ *   h          device, type residual_dt, [rows][cols]: required with a
+ *              residual, which it may overwrite; not written without
+ *   rstd       device float [rows]
+ *   y          device, type dt, [rows][cols], or NULL
+ *   q, scale_inv, q_t, scale_inv_t: as fp8q_quantize_blockwise; cols % 16 ==
+ *   0 for a copy, rows % 16 == 0 for the transposed one, and every tensor
+ *   but rstd and the scales 16-byte aligned.  Without a copy any sizes and
+ *   alignments do.  Other outputs overlap no input.
+ */
+FP8Q_API fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* residual, int32_t residual_dt,
+                                  const void* weight, int32_t weight_dt, int64_t rows, int64_t cols, float eps,
+                                  int32_t fmt, int32_t dir, int32_t pow2_scales, void* h, float* rstd, void* y,
+                                  uint8_t* q, float* scale_inv, uint8_t* q_t, float* scale_inv_t, void* stream);
+
+/* Bytes of workspace fp8q_rmsnorm_backward needs (contents do not matter). */
+FP8Q_API size_t fp8q_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * The gradients of fp8q_rmsnorm, with g = d_y * weight and u = h * rstd:
+ *   d_x[r][c] = rstd[r] * (g - u * mean_c(g * u)) + d_h[r][c]
+ *   d_weight[c] = sum_r d_y[r][c] * u[r][c]
+ * d_x is the gradient of x and of the residual alike.  Sums are FP32 in a
+ * fixed order; no rows give d_weight 0.
+ *   d_y        device, type dt, [rows][cols]
+ *   h          device, type h_dt, [rows][cols]: the call's h (x without a
+ *              residual), with its rstd
+ *   d_h        device, type h_dt, [rows][cols], or NULL: the gradient that
+ *              reaches h past the norm
+ *   d_x        device, type h_dt, [rows][cols]; may overwrite d_h
+ *   d_weight   device float [cols]
+ *   workspace  device, 16-byte aligned; calls that may overlap on the GPU
+ *              need separate ones
+ */
+FP8Q_API fp8q_status fp8q_rmsnorm_backward(const void* d_y, int32_t dt, const void* h, int32_t h_dt,
+                                           const void* weight, int32_t weight_dt, const float* rstd, const void* d_h,
+                                           int64_t rows, int64_t cols, void* d_x, float* d_weight, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/*
+ * The gated activation between the two products of a block, and its copies:
+ *   a[r][j] = gate * up / (1 + exp(-gate)),  gate = h[r][j], up = h[r][inner + j]
+ * The copies are those of fp8q_quantize_blockwise with 1x128 groups for the
+ * FP32 values of a.
+ *   h    device, type dt (BF16 or FP32), [rows][2 * inner]
+ *   dir  0 (no copy), MXFP8_ROW, MXFP8_COL or MXFP8_BOTH
+ *   a    device, type dt, [rows][inner], or NULL
+ *   q, scale_inv, q_t, scale_inv_t: as there; inner % 16 == 0 for a copy,
+ *   rows % 16 == 0 for the transposed one, h and a 16-byte aligned.  Without
+ *   a copy any sizes and alignments do.  Outputs overlap no input.
+ */
+FP8Q_API fp8q_status fp8q_swiglu(const void* h, int32_t dt, int64_t rows, int64_t inner, int32_t fmt, int32_t dir,
+                                 int32_t pow2_scales, void* a, uint8_t* q, float* scale_inv, uint8_t* q_t,
+                                 float* scale_inv_t, void* stream);
+
+/*
+ * The gradient of fp8q_swiglu with respect to h, with s = 1 / (1 + exp(-gate)):
+ *   d_h[r][j] = d_a * up * s * (1 + gate * (1 - s)),  d_h[r][inner + j] = d_a * gate * s
+ * and its copies (of the [rows][2 * inner] matrix; inner % 8 == 0).
+ *   d_a  device, type dt, [rows][inner]
+ *   d_h  device, type dt, [rows][2 * inner], or NULL
+ */
+FP8Q_API fp8q_status fp8q_swiglu_backward(const void* h, const void* d_a, int32_t dt, int64_t rows, int64_t inner,
+                                          int32_t fmt, int32_t dir, int32_t pow2_scales, void* d_h, uint8_t* q,
+                                          float* scale_inv, uint8_t* q_t, float* scale_inv_t, void* stream);
+
+/*
  * NVFP4 ("混合精度与 FP8 训练" 13.2): E2M1 elements (0, 0.5, 1, 1.5, 2, 3,
  * 4, 6 and negatives), one E4M3 scale per 16 elements along a row, and one
  * FP32 scale for the tensor.  Each step is one IEEE single operation:

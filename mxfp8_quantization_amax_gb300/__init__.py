@@ -35,6 +35,7 @@ __all__ = [
     "fp8q_matmul_blockwise", "fp8q_matmul_grouped", "fp8q_matmul_grouped_wgrad",
     "SCORE_SOFTMAX", "SCORE_SIGMOID", "fp8q_moe_route", "fp8q_moe_route_backward", "fp8q_moe_rows", "fp8q_moe_plan",
     "fp8q_moe_dispatch", "fp8q_moe_combine", "fp8q_moe_combine_backward",
+    "fp8q_rmsnorm", "fp8q_rmsnorm_backward", "fp8q_swiglu", "fp8q_swiglu_backward",
 ]
 
 E4M3 = 0
@@ -90,6 +91,15 @@ _SIGS = {
     "fp8q_moe_combine": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _c.c_int64, _c.c_int32, _P, _P]),
     "fp8q_moe_combine_backward": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _P, _c.c_int64,
                                              _c.c_int32, _P, _P, _P]),
+    "fp8q_rmsnorm": (_c.c_int, [_P, _c.c_int32, _P, _c.c_int32, _P, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_float,
+                                _c.c_int32, _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "fp8q_rmsnorm_backward_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64]),
+    "fp8q_rmsnorm_backward": (_c.c_int, [_P, _c.c_int32, _P, _c.c_int32, _P, _c.c_int32, _P, _P, _c.c_int64, _c.c_int64,
+                                         _P, _P, _P, _c.c_size_t, _P]),
+    "fp8q_swiglu": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32, _P, _P, _P, _P,
+                               _P, _P]),
+    "fp8q_swiglu_backward": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_int32,
+                                        _P, _P, _P, _P, _P, _P]),
     "fp8q_quantize_nvfp4": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _P, _P, _P]),
     "fp8q_dequantize_per_tensor": (_c.c_int, [_P, _c.c_int64, _c.c_int64, _P, _c.c_int32, _c.c_int32, _P,
                                               _c.c_int32, _P, _P]),
@@ -997,6 +1007,121 @@ def fp8q_moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, plan: dict, 
     if st:
         _check(st, "fp8q_moe_combine_backward")
     return {"d_y": d_y, "d_weights": d_w}
+
+
+# ---------------------------------------------------------------------------
+# around the products: norm, gated activation
+# ---------------------------------------------------------------------------
+def _copies(o: dict, direction: int, rows: int, cols: int, dev):
+    """Buffers of the row copy and the transposed copy that `direction` asks for (1x128 groups)."""
+    q = si = q_t = si_t = None
+    if direction & ROW:
+        q = _result(o.get("q"), (rows, cols), torch.uint8, dev)
+        si = _result(o.get("scale_inv"), (rows, (cols + 127) // 128), torch.float32, dev)
+    if direction & COL:
+        q_t = _result(o.get("q_t"), (cols, rows), torch.uint8, dev)
+        si_t = _result(o.get("scale_inv_t"), (cols, (rows + 127) // 128), torch.float32, dev)
+    return q, si, q_t, si_t
+
+
+def _weight(weight: torch.Tensor, cols: int, at: int):
+    if weight.get_device() != at or weight.dtype not in _VALUES or weight.shape != (cols,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of shape ({cols},) on cuda:{at}")
+
+
+def fp8q_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                 fmt: int = E4M3, direction: int = ROW, pow2_scales: bool = False, want_y: bool = False,
+                 out: dict | None = None) -> dict:
+    """h = x + residual in the residual's type (x without one), y = h / sqrt(mean(h^2) + eps) * weight over the
+    rows of x [rows, cols]: dict(y like x (with want_y), h, rstd float32 [rows], and y's copies q, scale_inv,
+    q_t, scale_inv_t as fp8q_quantize_blockwise makes them for 1x128 groups); what `direction` (0: no copy)
+    does not ask for is None.  out["h"] may be the residual."""
+    at = _device(x, "x")
+    _matrix(x, "x", _VALUES, at)
+    rows, cols = x.shape
+    _weight(weight, cols, at)
+    o, dev = out or {}, x.device
+    h = x
+    if residual is not None:
+        _matrix(residual, "residual", _VALUES, at, (rows, cols))
+        h = _result(o.get("h"), (rows, cols), residual.dtype, dev)
+    rstd = _result(o.get("rstd"), (rows,), torch.float32, dev)
+    y = _result(o.get("y"), (rows, cols), x.dtype, dev) if want_y else None
+    q, si, q_t, si_t = _copies(o, direction, rows, cols, dev)
+    st = (_lib or lib()).fp8q_rmsnorm(x.data_ptr(), _IN[x.dtype], _ptr(residual), 0 if residual is None else _IN[residual.dtype],
+                                      weight.data_ptr(), _IN[weight.dtype], rows, cols, eps, fmt, direction,
+                                      1 if pow2_scales else 0, h.data_ptr(), rstd.data_ptr(), _ptr(y), _ptr(q), _ptr(si),
+                                      _ptr(q_t), _ptr(si_t), _stream(at))
+    if st:
+        _check(st, "fp8q_rmsnorm")
+    return {"y": y, "h": h, "rstd": rstd, "q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
+
+
+def fp8q_rmsnorm_backward(d_y: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                          d_h: torch.Tensor | None = None, out: dict | None = None) -> dict:
+    """The gradients of fp8q_rmsnorm from d_y and the call's h and rstd: dict(d_x like h, of x and the residual
+    alike, with d_h, the gradient that reaches h past the norm, added; d_weight float32 [cols])."""
+    at = _device(d_y, "d_y")
+    _matrix(d_y, "d_y", _VALUES, at)
+    rows, cols = d_y.shape
+    _matrix(h, "h", _VALUES, at, (rows, cols))
+    _weight(weight, cols, at)
+    _floats(rstd, "rstd", (rows,), at)
+    if d_h is not None:
+        _matrix(d_h, "d_h", (h.dtype,), at, (rows, cols))
+    o, dev = out or {}, h.device
+    d_x = _result(o.get("d_x"), (rows, cols), h.dtype, dev)
+    d_w = _result(o.get("d_weight"), (cols,), torch.float32, dev)
+    L = _lib or lib()
+    need = L.fp8q_rmsnorm_backward_workspace_bytes(rows, cols)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    st = L.fp8q_rmsnorm_backward(d_y.data_ptr(), _IN[d_y.dtype], h.data_ptr(), _IN[h.dtype], weight.data_ptr(),
+                                 _IN[weight.dtype], rstd.data_ptr(), _ptr(d_h), rows, cols, d_x.data_ptr(), d_w.data_ptr(),
+                                 _ptr(ws), need, _stream(at))
+    if st:
+        _check(st, "fp8q_rmsnorm_backward")
+    return {"d_x": d_x, "d_weight": d_w}
+
+
+def fp8q_swiglu(h: torch.Tensor, fmt: int = E4M3, direction: int = ROW, pow2_scales: bool = False, want_a: bool = False,
+                out: dict | None = None) -> dict:
+    """a = silu(gate) * up for h = [gate | up] [rows, 2 * inner]: dict(a like h (with want_a) and its copies q,
+    scale_inv, q_t, scale_inv_t as fp8q_quantize_blockwise makes them for 1x128 groups); what `direction`
+    (0: no copy) does not ask for is None."""
+    at = _device(h, "h")
+    _matrix(h, "h", _VALUES, at)
+    rows, inner = h.shape[0], h.shape[1] // 2
+    if h.shape[1] != 2 * inner:
+        raise ValueError("h must hold a gate and an up half")
+    o, dev = out or {}, h.device
+    a = _result(o.get("a"), (rows, inner), h.dtype, dev) if want_a else None
+    q, si, q_t, si_t = _copies(o, direction, rows, inner, dev)
+    st = (_lib or lib()).fp8q_swiglu(h.data_ptr(), _IN[h.dtype], rows, inner, fmt, direction, 1 if pow2_scales else 0, _ptr(a),
+                                     _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t), _stream(at))
+    if st:
+        _check(st, "fp8q_swiglu")
+    return {"a": a, "q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
+
+
+def fp8q_swiglu_backward(h: torch.Tensor, d_a: torch.Tensor, fmt: int = E5M2, direction: int = BOTH,
+                         pow2_scales: bool = False, want_d_h: bool = False, out: dict | None = None) -> dict:
+    """The gradient of fp8q_swiglu with respect to h from d_a [rows, inner]: dict(d_h like h (with want_d_h) and
+    its copies, groups of 128 over the 2 * inner columns)."""
+    at = _device(h, "h")
+    _matrix(h, "h", _VALUES, at)
+    rows, cols = h.shape
+    if cols % 2:
+        raise ValueError("h must hold a gate and an up half")
+    _matrix(d_a, "d_a", (h.dtype,), at, (rows, cols // 2))
+    o, dev = out or {}, h.device
+    d_h = _result(o.get("d_h"), (rows, cols), h.dtype, dev) if want_d_h else None
+    q, si, q_t, si_t = _copies(o, direction, rows, cols, dev)
+    st = (_lib or lib()).fp8q_swiglu_backward(h.data_ptr(), d_a.data_ptr(), _IN[h.dtype], rows, cols // 2, fmt, direction,
+                                              1 if pow2_scales else 0, _ptr(d_h), _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t),
+                                              _stream(at))
+    if st:
+        _check(st, "fp8q_swiglu_backward")
+    return {"d_h": d_h, "q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
 
 
 # ---------------------------------------------------------------------------

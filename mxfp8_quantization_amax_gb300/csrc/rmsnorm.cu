@@ -1,0 +1,527 @@
+// rmsnorm.cu -- root-mean-square norm with the residual's addition, the 8-bit
+// copies of its output, and its gradients.
+//
+//   h = x + residual (rounded to the residual's type: the stream that goes on), or x
+//   rstd = 1 / sqrt(mean(h^2) + eps),   y = h * rstd * weight
+//   with g = d_y * weight and u = h * rstd:
+//   d_x = rstd * (g - u * mean(g * u)) + d_h,   d_weight = sum over the rows of d_y * u
+//
+// Sums are FP32 in a fixed order.  The norm is of h as it is stored, so that
+// the gradient, which reads h again, differentiates what was computed.
+#include "quant_tile.cuh"
+
+namespace fp8q {
+
+constexpr int kRnMaxCols = 32768;
+constexpr int kRnThreads = 256;      // of a CTA at least
+constexpr int kRnMaxPartials = 608;  // rows of the weight gradient's partial sums
+constexpr int kNone = -1;
+
+struct RmsNorm {
+  const void* x;
+  const void* residual;  // its type: RT
+  const void* weight;
+  int weight_dt;
+  int64_t rows, cols;
+  int lanes;  // threads of a row
+  float eps;
+  int fmt, pow2, tiles_c;
+  void* h;
+  float* rstd;
+  void* y;
+  uint8_t* q;
+  float* s;
+};
+
+// V values that the kernel may write in place.
+template <int DT, int V>
+__device__ __forceinline__ void rn_load_plain(const void* p, int64_t i, float (&v)[V]) {
+  QtRaw<DT, V> r;
+  if constexpr (V == 8 && DT == kBF16) {
+    r.a = *(const uint4*)((const uint16_t*)p + i);
+  } else if constexpr (V == 8) {
+    r.a = *(const uint4*)((const float*)p + i);
+    r.b = *(const uint4*)((const float*)p + i + 4);
+  } else {
+    r.a.x = DT == kBF16 ? (uint32_t) * ((const uint16_t*)p + i) << 16 : *((const uint32_t*)p + i);
+  }
+  r.get(v);
+}
+
+// V weights; every row reads them, so they may stay in L1.
+template <int V>
+__device__ __forceinline__ void rn_weight(const void* w, int dt, int64_t i, float (&v)[V]) {
+  if (dt == kFP32) {
+    const float* q = (const float*)w + i;
+    if constexpr (V == 8) {
+      const float4 a = __ldg((const float4*)q), b = __ldg((const float4*)q + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      v[0] = __ldg(q);
+    }
+  } else {
+    const uint16_t* q = (const uint16_t*)w + i;
+    if constexpr (V == 8) {
+      const uint4 a = __ldg((const uint4*)q);
+      v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+      v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+    } else {
+      v[0] = __uint_as_float((uint32_t)__ldg(q) << 16);
+    }
+  }
+}
+
+// The sum over the `lanes` threads of a row (a multiple of 32; rows of a CTA
+// lie side by side).  Every thread of the CTA comes here.
+__device__ __forceinline__ float rn_row_sum(float v, int lanes, float* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if (lanes == 32) return v;
+  const int warp = threadIdx.x >> 5, per = lanes >> 5, first = warp / per * per;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[warp] = v;
+  __syncthreads();
+  v = 0.0f;
+  for (int w = 0; w < per; w++) v += sh[first + w];
+  return v;
+}
+
+__device__ __forceinline__ float rn_rstd(float sum, int64_t cols, float eps) {
+  return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)cols), eps)));
+}
+
+// A row in the registers of p.lanes threads, V values in each of N chunks.
+template <int DT, int RT, int V, int N, int T>
+__global__ void __launch_bounds__(T) rmsnorm_kernel(RmsNorm p) {
+  __shared__ float sh[32];
+  const int t = threadIdx.x % p.lanes;
+  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / p.lanes) + threadIdx.x / p.lanes;
+  const bool row_ok = r < p.rows;
+  float v[N][V];
+  float sum = 0.0f;
+  pdl_wait();
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    const int64_t c = (int64_t)(n * p.lanes + t) * V;
+#pragma unroll
+    for (int k = 0; k < V; k++) v[n][k] = 0.0f;
+    if (row_ok && c < p.cols) {
+      QtRaw<DT, V> raw;
+      raw.load(p.x, r * p.cols + c);
+      if constexpr (RT != kNone) {
+        float b[V];
+        rn_load_plain<RT, V>(p.residual, r * p.cols + c, b);
+        raw.get(v[n]);
+#pragma unroll
+        for (int k = 0; k < V; k++) v[n][k] = __fadd_rn(v[n][k], b[k]);
+        qt_store<RT, V>(p.h, r * p.cols + c, v[n], true);
+      } else {
+        raw.get(v[n]);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; n++)
+#pragma unroll
+    for (int k = 0; k < V; k++) sum = __fmaf_rn(v[n][k], v[n][k], sum);
+  const float rstd = rn_rstd(rn_row_sum(sum, p.lanes, sh), p.cols, p.eps);
+  if (row_ok && t == 0) p.rstd[r] = rstd;
+  if (p.y != nullptr || p.q != nullptr) {
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const int64_t c = (int64_t)(n * p.lanes + t) * V;
+      const bool there = row_ok && c < p.cols;
+      if (there) {
+        float w[V];
+        rn_weight<V>(p.weight, p.weight_dt, c, w);
+#pragma unroll
+        for (int k = 0; k < V; k++) v[n][k] = __fmul_rn(__fmul_rn(v[n][k], rstd), w[k]);
+      }
+      if constexpr (V == 8) {
+        if (p.q != nullptr) {  // 16 threads hold a group of 128 columns
+          uint8_t* q = p.q + r * p.cols + c;
+          float* s = p.s + r * p.tiles_c + c / 128;
+          if (p.fmt == kE4M3) qt_group<kE4M3>(v[n], p.pow2, q, s, there, threadIdx.x & 15);
+          else qt_group<kE5M2>(v[n], p.pow2, q, s, there, threadIdx.x & 15);
+        }
+      }
+      if (p.y != nullptr && there) qt_store<DT, V>(p.y, r * p.cols + c, v[n]);
+    }
+  }
+  pdl_launch_dependents();
+}
+
+// The transposed copy needs 128 rows' statistics at a time: a second pass over h.
+template <int DT>
+struct RmsNormTile {
+  static constexpr int kType = DT;
+  const void* h;
+  const void* weight;
+  int weight_dt;
+  const float* rstd;
+  int64_t cols;
+  __device__ __forceinline__ void tile(float (&v)[8][8], int64_t row, int64_t col, int64_t rows) const {
+    QtRaw<DT, 8> raw[8];
+    float s[8], w[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      raw[i].zero();
+      s[i] = 0.0f;
+      if (row + i < rows) {
+        raw[i].load(h, (row + i) * cols + col);
+        s[i] = __ldg(rstd + row + i);
+      }
+    }
+    rn_weight<8>(weight, weight_dt, col, w);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      raw[i].get(v[i]);
+      if (row + i < rows) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[i][k] = __fmul_rn(__fmul_rn(v[i][k], s[i]), w[k]);
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------------------
+// gradients
+// ---------------------------------------------------------------------------
+struct RmsNormBackward {
+  const void* d_y;
+  const void* h;
+  const void* weight;
+  int weight_dt;
+  const float* rstd;
+  const void* d_h;  // or NULL
+  int64_t rows, cols;
+  int lanes;
+  void* d_x;
+  float* partial;  // [groups of threads][cols]
+};
+
+// Each group of p.lanes threads takes every gridDim.x-th set of rows and keeps
+// its columns' sums of the weight gradient.
+template <int DT, int HT, int V, int N, int T>
+__global__ void __launch_bounds__(T) rmsnorm_backward_kernel(RmsNormBackward p) {
+  extern __shared__ float acc_sh[];  // N == 0: the sums of all columns
+  __shared__ float sh[32];
+  const int t = threadIdx.x % p.lanes, per = blockDim.x / p.lanes, mine = threadIdx.x / p.lanes;
+  pdl_wait();
+  if constexpr (N > 0) {
+    float acc[N][V];
+#pragma unroll
+    for (int n = 0; n < N; n++)
+#pragma unroll
+      for (int k = 0; k < V; k++) acc[n][k] = 0.0f;
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per) {
+      const int64_t r = r0 + mine;
+      const bool row_ok = r < p.rows;
+      QtRaw<DT, V> d[N];
+      QtRaw<HT, V> h[N];
+      const float rstd = row_ok ? __ldg(p.rstd + r) : 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        const int64_t c = (int64_t)(n * p.lanes + t) * V;
+        d[n].zero();
+        h[n].zero();
+        if (row_ok && c < p.cols) {
+          d[n].load(p.d_y, r * p.cols + c);
+          h[n].load(p.h, r * p.cols + c);
+        }
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        const int64_t c = (int64_t)(n * p.lanes + t) * V;
+        if (c >= p.cols) continue;
+        float w[V], dv[V], hv[V];
+        rn_weight<V>(p.weight, p.weight_dt, c, w);
+        d[n].get(dv);
+        h[n].get(hv);
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+          const float u = __fmul_rn(hv[k], rstd);
+          sum = __fmaf_rn(__fmul_rn(dv[k], w[k]), u, sum);
+          acc[n][k] = __fmaf_rn(dv[k], u, acc[n][k]);
+        }
+      }
+      const float mean = __fdiv_rn(rn_row_sum(sum, p.lanes, sh), (float)p.cols);
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        const int64_t c = (int64_t)(n * p.lanes + t) * V;
+        if (!row_ok || c >= p.cols) continue;
+        float w[V], dv[V], hv[V], res[V];
+        rn_weight<V>(p.weight, p.weight_dt, c, w);
+        d[n].get(dv);
+        h[n].get(hv);
+        if (p.d_h != nullptr) rn_load_plain<HT, V>(p.d_h, r * p.cols + c, res);
+#pragma unroll
+        for (int k = 0; k < V; k++) {
+          const float u = __fmul_rn(hv[k], rstd);
+          const float g = __fmul_rn(rstd, __fmaf_rn(-u, mean, __fmul_rn(dv[k], w[k])));
+          dv[k] = p.d_h != nullptr ? __fadd_rn(g, res[k]) : g;
+        }
+        qt_store<HT, V>(p.d_x, r * p.cols + c, dv);
+      }
+    }
+    float* to = p.partial + ((int64_t)blockIdx.x * per + mine) * p.cols;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const int64_t c = (int64_t)(n * p.lanes + t) * V;
+      if (c >= p.cols) continue;
+      if constexpr (V == 8) {
+        *(float4*)(to + c) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        *(float4*)(to + c + 4) = make_float4(acc[n][4], acc[n][5], acc[n][6], acc[n][7]);
+      } else {
+        to[c] = acc[n][0];
+      }
+    }
+  } else {  // any columns and alignment: one row a CTA, read twice
+    for (int64_t c = t; c < p.cols; c += p.lanes) acc_sh[c] = 0.0f;
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+      const float rstd = __ldg(p.rstd + r);
+      float sum = 0.0f;
+      for (int64_t c = t; c < p.cols; c += p.lanes) {
+        QtRaw<DT, 1> d;
+        QtRaw<HT, 1> h;
+        float w[1], dv[1], hv[1];
+        d.load(p.d_y, r * p.cols + c);
+        h.load(p.h, r * p.cols + c);
+        rn_weight<1>(p.weight, p.weight_dt, c, w);
+        d.get(dv);
+        h.get(hv);
+        const float u = __fmul_rn(hv[0], rstd);
+        sum = __fmaf_rn(__fmul_rn(dv[0], w[0]), u, sum);
+        acc_sh[c] = __fmaf_rn(dv[0], u, acc_sh[c]);
+      }
+      const float mean = __fdiv_rn(rn_row_sum(sum, p.lanes, sh), (float)p.cols);
+      for (int64_t c = t; c < p.cols; c += p.lanes) {
+        QtRaw<DT, 1> d;
+        QtRaw<HT, 1> h;
+        float w[1], dv[1], hv[1], res[1] = {0.0f};
+        d.load(p.d_y, r * p.cols + c);
+        h.load(p.h, r * p.cols + c);
+        rn_weight<1>(p.weight, p.weight_dt, c, w);
+        d.get(dv);
+        h.get(hv);
+        const float u = __fmul_rn(hv[0], rstd);
+        float g = __fmul_rn(rstd, __fmaf_rn(-u, mean, __fmul_rn(dv[0], w[0])));
+        if (p.d_h != nullptr) {
+          rn_load_plain<HT, 1>(p.d_h, r * p.cols + c, res);
+          g = __fadd_rn(g, res[0]);
+        }
+        float o[1] = {g};
+        qt_store<HT, 1>(p.d_x, r * p.cols + c, o);
+      }
+    }
+    for (int64_t c = t; c < p.cols; c += p.lanes) p.partial[(int64_t)blockIdx.x * p.cols + c] = acc_sh[c];
+  }
+  pdl_launch_dependents();
+}
+
+// d_weight[c] = the sum of `parts` rows of partial sums, eight warps a column in a fixed order.
+constexpr int kRnSumWarps = 8;
+
+__global__ void __launch_bounds__(32 * kRnSumWarps) rmsnorm_weight_kernel(const float* partial, int parts, int64_t cols,
+                                                                           float* d_weight) {
+  __shared__ float sh[kRnSumWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  pdl_wait();
+  float sum = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int i = warp; i < parts; i += kRnSumWarps) sum += partial[(int64_t)i * cols + c];
+  }
+  sh[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+#pragma unroll
+    for (int w = 1; w < kRnSumWarps; w++) sum += sh[w][lane];
+    d_weight[c] = sum;
+  }
+  pdl_launch_dependents();
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+static bool off(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
+static size_t size_of(int32_t dt) { return dt == FP8Q_IN_BF16 ? 2 : 4; }
+static bool type_ok(int32_t dt) { return dt == FP8Q_IN_BF16 || dt == FP8Q_IN_FP32; }
+
+// Threads of a row whose chunks of V values are taken N at a time at most.
+static int row_lanes(int64_t cols, int v, int n) {
+  const int64_t chunks = (cols + v - 1) / v;
+  int lanes = 32;
+  while ((int64_t)lanes * n < chunks) lanes *= 2;
+  return lanes;
+}
+
+template <int DT, int RT, int V, int N>
+static cudaError_t launch_norm_n(RmsNorm& p, cudaStream_t s) {
+  p.lanes = row_lanes(p.cols, V, N);
+  const int threads = p.lanes > kRnThreads ? p.lanes : kRnThreads, per = threads / p.lanes;
+  const dim3 grid((unsigned)((p.rows + per - 1) / per));
+  return launch_kernel(threads == kRnThreads ? rmsnorm_kernel<DT, RT, V, N, kRnThreads> : rmsnorm_kernel<DT, RT, V, N, 1024>, grid,
+                       dim3(threads), 0, s, p);
+}
+
+template <int DT, int RT>
+static cudaError_t launch_norm(RmsNorm& p, bool vec, cudaStream_t s) {
+  if (!vec) return p.cols <= 8192 ? launch_norm_n<DT, RT, 1, 8>(p, s) : launch_norm_n<DT, RT, 1, 32>(p, s);
+  // a row in few threads, or in as many as it has chunks where few rows have the machine to themselves
+  if (p.rows <= 2 * sm_count() && p.cols <= 8192) return launch_norm_n<DT, RT, 8, 1>(p, s);
+  return launch_norm_n<DT, RT, 8, 4>(p, s);
+}
+
+template <int DT, int HT>
+static cudaError_t launch_norm_backward(RmsNormBackward& p, bool vec, int* parts, cudaStream_t s) {
+  if (!vec) {
+    p.lanes = 256;
+    *parts = (int)(p.rows < kRnMaxPartials ? p.rows : kRnMaxPartials);
+    const size_t smem = (size_t)p.cols * sizeof(float);
+    static PerDevice<bool> allowed;
+    const cudaError_t e = allow_smem(allowed, rmsnorm_backward_kernel<DT, HT, 1, 0, 256>, kRnMaxCols * sizeof(float));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(rmsnorm_backward_kernel<DT, HT, 1, 0, 256>, dim3(*parts), dim3(256), smem, s, p);
+  }
+  p.lanes = row_lanes(p.cols, 8, 4);
+  const int threads = p.lanes > kRnThreads ? p.lanes : kRnThreads, per = threads / p.lanes;
+  const int64_t sets = (p.rows + per - 1) / per;
+  int64_t grid = kRnMaxPartials / per;
+  const int64_t fit = (int64_t)sm_count() * (threads <= 256 ? 2 : 1);
+  grid = grid < fit ? grid : fit;
+  grid = grid < sets ? grid : sets;
+  *parts = (int)grid * per;
+  return launch_kernel(threads == kRnThreads ? rmsnorm_backward_kernel<DT, HT, 8, 4, kRnThreads> : rmsnorm_backward_kernel<DT, HT, 8, 4, 1024>,
+                       dim3((unsigned)grid), dim3(threads), 0, s, p);
+}
+
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* residual, int32_t residual_dt,
+                                    const void* weight, int32_t weight_dt, int64_t rows, int64_t cols, float eps,
+                                    int32_t fmt, int32_t dir, int32_t pow2_scales, void* h, float* rstd, void* y,
+                                    uint8_t* q, float* scale_inv, uint8_t* q_t, float* scale_inv_t, void* stream) {
+  clear_error();
+  if (!type_ok(dt) || !type_ok(weight_dt) || (residual && !type_ok(residual_dt)))
+    return fail(FP8Q_ERR_INVALID_ARG, "dt, residual_dt and weight_dt must be FP8Q_IN_BF16 or FP8Q_IN_FP32");
+  if (rows < 0 || cols < 1) return fail(FP8Q_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
+  if (rows > INT32_MAX / 2 || cols > kRnMaxCols) return fail(FP8Q_ERR_UNSUPPORTED, "rows too large, or cols > %d", kRnMaxCols);
+  if (!(eps >= 0.0f) || eps > 3.4e38f) return fail(FP8Q_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  const fp8q_status r = qt_check(rows, cols, fmt, dir, q, scale_inv, q_t, scale_inv_t);
+  if (r != FP8Q_OK) return r;
+  if (rows == 0) return FP8Q_OK;
+  const bool copy = dir != 0;
+  const size_t a_x = copy ? 16 : size_of(dt), a_r = copy ? 16 : size_of(residual_dt), a_w = copy ? 16 : size_of(weight_dt);
+  if (!x || off(x, a_x)) return fail(FP8Q_ERR_INVALID_ARG, "x must be a device pointer, 16-byte aligned for a copy");
+  if (residual && (off(residual, a_r) || !h || off(h, a_r)))
+    return fail(FP8Q_ERR_INVALID_ARG, "a residual needs h, both 16-byte aligned for a copy");
+  if (!weight || off(weight, a_w)) return fail(FP8Q_ERR_INVALID_ARG, "weight must be a device pointer, 16-byte aligned for a copy");
+  if (!rstd || off(rstd, 4)) return fail(FP8Q_ERR_INVALID_ARG, "rstd must be a 4-byte aligned device pointer");
+  if (off(y, a_x)) return fail(FP8Q_ERR_INVALID_ARG, "y must be aligned as x is");
+  RmsNorm p{};
+  p.x = x;
+  p.residual = residual;
+  p.weight = weight;
+  p.weight_dt = weight_dt;
+  p.rows = rows;
+  p.cols = cols;
+  p.eps = eps;
+  p.fmt = fmt;
+  p.pow2 = pow2_scales ? 1 : 0;
+  p.tiles_c = (int)((cols + kQtTile - 1) / kQtTile);
+  p.h = h;
+  p.rstd = rstd;
+  p.y = y;
+  if (dir & MXFP8_ROW) p.q = q, p.s = scale_inv;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const bool vec = cols % 8 == 0 && !off(x, 16) && !off(residual, 16) && !off(residual ? h : nullptr, 16) &&
+                   !off(weight, 16) && !off(y, 16);
+  const int rt = residual ? residual_dt : kNone;
+  cudaError_t e;
+  if (dt == FP8Q_IN_BF16)
+    e = rt == kNone ? launch_norm<kBF16, kNone>(p, vec, s) : rt == kBF16 ? launch_norm<kBF16, kBF16>(p, vec, s) : launch_norm<kBF16, kFP32>(p, vec, s);
+  else
+    e = rt == kNone ? launch_norm<kFP32, kNone>(p, vec, s) : rt == kBF16 ? launch_norm<kFP32, kBF16>(p, vec, s) : launch_norm<kFP32, kFP32>(p, vec, s);
+  if (e != cudaSuccess) return cuda_fail(e, "rmsnorm kernel launch");
+  if (dir & MXFP8_COL) {
+    QtOut o{};
+    o.rows = rows;
+    o.cols = cols;
+    const int64_t tiles_r = (rows + kQtTile - 1) / kQtTile;
+    if (tiles_r * p.tiles_c > INT32_MAX) return fail(FP8Q_ERR_UNSUPPORTED, "rows * cols too large");
+    o.tiles_r = (int)tiles_r;
+    o.tiles_c = p.tiles_c;
+    o.pow2 = p.pow2;
+    o.q_t = q_t;
+    o.s_t = scale_inv_t;
+    const int ht = residual ? residual_dt : dt;
+    const void* from = residual ? h : x;
+    if (ht == FP8Q_IN_BF16) {
+      const RmsNormTile<kBF16> src{from, weight, weight_dt, rstd, cols};
+      e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kBF16>, kE4M3>(src, o, s) : launch_quant_tiles<RmsNormTile<kBF16>, kE5M2>(src, o, s);
+    } else {
+      const RmsNormTile<kFP32> src{from, weight, weight_dt, rstd, cols};
+      e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kFP32>, kE4M3>(src, o, s) : launch_quant_tiles<RmsNormTile<kFP32>, kE5M2>(src, o, s);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "rmsnorm transposed copy launch");
+  }
+  return check_launch("rmsnorm kernel");
+}
+
+extern "C" size_t fp8q_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 1 || cols < 1 || cols > kRnMaxCols) return 0;
+  // a CTA's groups of threads side by side may be more than the rows
+  const int64_t parts = rows + 8 < kRnMaxPartials ? rows + 8 : kRnMaxPartials;
+  return (size_t)parts * cols * sizeof(float);
+}
+
+extern "C" fp8q_status fp8q_rmsnorm_backward(const void* d_y, int32_t dt, const void* h, int32_t h_dt, const void* weight,
+                                             int32_t weight_dt, const float* rstd, const void* d_h, int64_t rows,
+                                             int64_t cols, void* d_x, float* d_weight, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  clear_error();
+  if (!type_ok(dt) || !type_ok(h_dt) || !type_ok(weight_dt))
+    return fail(FP8Q_ERR_INVALID_ARG, "dt, h_dt and weight_dt must be FP8Q_IN_BF16 or FP8Q_IN_FP32");
+  if (rows < 0 || cols < 1) return fail(FP8Q_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
+  if (rows > INT32_MAX / 2 || cols > kRnMaxCols) return fail(FP8Q_ERR_UNSUPPORTED, "rows too large, or cols > %d", kRnMaxCols);
+  if (!d_weight || off(d_weight, 4)) return fail(FP8Q_ERR_INVALID_ARG, "d_weight must be a 4-byte aligned device pointer");
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  int parts = 0;
+  if (rows > 0) {
+    if (!d_y || off(d_y, size_of(dt))) return fail(FP8Q_ERR_INVALID_ARG, "d_y must be a device pointer aligned to its type");
+    if (!h || off(h, size_of(h_dt)) || !d_x || off(d_x, size_of(h_dt)) || off(d_h, size_of(h_dt)))
+      return fail(FP8Q_ERR_INVALID_ARG, "h, d_h and d_x must be device pointers aligned to their type");
+    if (!weight || off(weight, size_of(weight_dt)) || !rstd || off(rstd, 4))
+      return fail(FP8Q_ERR_INVALID_ARG, "weight and rstd must be device pointers aligned to their type");
+    if (!workspace || off(workspace, 16) || workspace_bytes < fp8q_rmsnorm_backward_workspace_bytes(rows, cols))
+      return fail(FP8Q_ERR_INVALID_ARG, "workspace must be 16-byte aligned and of fp8q_rmsnorm_backward_workspace_bytes()");
+    RmsNormBackward p{};
+    p.d_y = d_y;
+    p.h = h;
+    p.weight = weight;
+    p.weight_dt = weight_dt;
+    p.rstd = rstd;
+    p.d_h = d_h;
+    p.rows = rows;
+    p.cols = cols;
+    p.d_x = d_x;
+    p.partial = (float*)workspace;
+    const bool vec = cols % 8 == 0 && !off(d_y, 16) && !off(h, 16) && !off(weight, 16) && !off(d_h, 16) && !off(d_x, 16);
+    if (dt == FP8Q_IN_BF16)
+      e = h_dt == FP8Q_IN_BF16 ? launch_norm_backward<kBF16, kBF16>(p, vec, &parts, s) : launch_norm_backward<kBF16, kFP32>(p, vec, &parts, s);
+    else
+      e = h_dt == FP8Q_IN_BF16 ? launch_norm_backward<kFP32, kBF16>(p, vec, &parts, s) : launch_norm_backward<kFP32, kFP32>(p, vec, &parts, s);
+    if (e != cudaSuccess) return cuda_fail(e, "rmsnorm gradient launch");
+  }
+  e = launch_kernel(rmsnorm_weight_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(32 * kRnSumWarps), 0, s,
+                    (const float*)workspace, parts, cols, d_weight);
+  if (e != cudaSuccess) return cuda_fail(e, "rmsnorm weight gradient launch");
+  return check_launch("rmsnorm gradient kernel");
+}
