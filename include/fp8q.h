@@ -625,6 +625,39 @@ FP8Q_API fp8q_status fp8q_moe_combine_backward(const void* d_out, const void* y,
                                                const float* weights, int64_t tokens, int32_t top_k, void* d_y,
                                                float* d_weights, void* stream);
 
+/* Bytes of workspace fp8q_moe_decode needs (contents do not matter). */
+FP8Q_API size_t fp8q_moe_decode_workspace_bytes(int64_t tokens, int32_t top_k, int64_t inner);
+
+/*
+ * The whole expert layer for a few tokens (1 to 64), as one serving step has
+ * them:
+ *   out[t] = sum_j weights[t][j] * W2[e] a,  e = ids[t][j],
+ *   a = gate * up / (1 + exp(-gate)),  gate = W1[e][:inner] x[t],  up = W1[e][inner:] x[t]
+ * with W1, W2 the values of blockwise codes (128x128 blocks).  Unlike the
+ * path over fp8q_moe_dispatch and the grouped products, tokens and inner
+ * values are not quantized: products and sums are FP32's (inner values keep
+ * 22 bits; a token's values 2^-32 below the largest of their 128 lose
+ * digits).  A slot whose id is no expert's (-1) adds nothing; an expert that
+ * a token names twice counts with the sum of the weights.  Sums have a fixed
+ * order.  Each chosen expert's weights are read once for up to 8 tokens.
+ *   x             device BF16 [tokens][hidden], 16-byte aligned
+ *   ids, weights  device int32, float [tokens][top_k], as fp8q_moe_route
+ *                 writes them; top_k <= 32
+ *   w1            device uint8 [experts][2 * inner][hidden], 16-byte aligned;
+ *                 w1_scale_inv [experts][ceil(2 * inner / 128)][ceil(hidden / 128)]
+ *   w2            device uint8 [experts][hidden][inner], 16-byte aligned;
+ *                 w2_scale_inv [experts][ceil(hidden / 128)][ceil(inner / 128)]
+ *   out           device BF16 or FP32 (out_dt) [tokens][hidden]
+ *   workspace     device, 16-byte aligned; calls that may overlap on the GPU
+ *                 need separate ones
+ * hidden and inner are multiples of 16, experts <= 1024.
+ */
+FP8Q_API fp8q_status fp8q_moe_decode(const void* x, int64_t tokens, int64_t hidden, int64_t inner, int32_t experts,
+                                     int32_t top_k, const int32_t* ids, const float* weights, const uint8_t* w1,
+                                     const float* w1_scale_inv, const uint8_t* w2, const float* w2_scale_inv,
+                                     int32_t w_fmt, int32_t out_dt, void* out, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /*
  * Root-mean-square norm of the rows, with the residual's addition before it
  * and the 8-bit copies that the next product reads (the pages quantize a

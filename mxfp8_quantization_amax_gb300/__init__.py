@@ -36,6 +36,7 @@ __all__ = [
     "SCORE_SOFTMAX", "SCORE_SIGMOID", "fp8q_moe_route", "fp8q_moe_route_backward", "fp8q_moe_rows", "fp8q_moe_plan",
     "fp8q_moe_dispatch", "fp8q_moe_combine", "fp8q_moe_combine_backward",
     "fp8q_rmsnorm", "fp8q_rmsnorm_backward", "fp8q_swiglu", "fp8q_swiglu_backward",
+    "fp8q_moe_decode",
 ]
 
 E4M3 = 0
@@ -91,6 +92,9 @@ _SIGS = {
     "fp8q_moe_combine": (_c.c_int, [_P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _c.c_int64, _c.c_int32, _P, _P]),
     "fp8q_moe_combine_backward": (_c.c_int, [_P, _P, _c.c_int32, _c.c_int64, _c.c_int64, _P, _P, _P, _c.c_int64,
                                              _c.c_int32, _P, _P, _P]),
+    "fp8q_moe_decode_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int32, _c.c_int64]),
+    "fp8q_moe_decode": (_c.c_int, [_P, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P, _P,
+                                   _c.c_int32, _c.c_int32, _P, _P, _c.c_size_t, _P]),
     "fp8q_rmsnorm": (_c.c_int, [_P, _c.c_int32, _P, _c.c_int32, _P, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_float,
                                 _c.c_int32, _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P, _P, _P, _P]),
     "fp8q_rmsnorm_backward_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64]),
@@ -1007,6 +1011,41 @@ def fp8q_moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, plan: dict, 
     if st:
         _check(st, "fp8q_moe_combine_backward")
     return {"d_y": d_y, "d_weights": d_w}
+
+
+def fp8q_moe_decode(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w1: torch.Tensor, w1_scale_inv: torch.Tensor,
+                    w2: torch.Tensor, w2_scale_inv: torch.Tensor, w_fmt: int = E4M3, out_dtype=torch.bfloat16,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The expert layer for up to 64 tokens x [tokens, hidden] BF16: out[t] = sum_j weights[t, j] * W2[e] a with
+    e = ids[t, j] and a = silu(gate) * up of W1[e] x[t]; out [tokens, hidden] in out_dtype.
+
+    ids and weights [tokens, top_k] as fp8q_moe_route makes them; w1 [experts, 2 * inner, hidden] and w2
+    [experts, hidden, inner] codes with their scale_inv in 128x128 blocks."""
+    at = _device(x, "x")
+    _matrix(x, "x", (torch.bfloat16,), at)
+    tokens, hidden = x.shape
+    _matrix(ids, "ids", (torch.int32,), at)
+    _matrix(weights, "weights", (torch.float32,), at, tuple(ids.shape))
+    if ids.shape[0] != tokens:
+        raise ValueError("ids must hold one row per token")
+    _codes(w1, "w1", 3, at)
+    _codes(w2, "w2", 3, at)
+    experts, _, inner = w2.shape
+    if w1.shape != (experts, 2 * inner, hidden) or w2.shape[1] != hidden:
+        raise ValueError("w1 must be [experts, 2 * inner, hidden] and w2 [experts, hidden, inner]")
+    hb, ib = (hidden + 127) // 128, (inner + 127) // 128
+    _floats(w1_scale_inv, "w1_scale_inv", (experts, (2 * inner + 127) // 128, hb), at)
+    _floats(w2_scale_inv, "w2_scale_inv", (experts, hb, ib), at)
+    o = _result(out, (tokens, hidden), out_dtype, x.device)
+    L, top_k = _lib or lib(), ids.shape[1]
+    need = L.fp8q_moe_decode_workspace_bytes(tokens, top_k, inner)
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    st = L.fp8q_moe_decode(x.data_ptr(), tokens, hidden, inner, experts, top_k, ids.data_ptr(), weights.data_ptr(),
+                           w1.data_ptr(), w1_scale_inv.data_ptr(), w2.data_ptr(), w2_scale_inv.data_ptr(), w_fmt,
+                           _out_dtype(out_dtype), o.data_ptr(), _ptr(ws), need, _stream(at))
+    if st:
+        _check(st, "fp8q_moe_decode")
+    return o
 
 
 # ---------------------------------------------------------------------------
