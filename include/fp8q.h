@@ -738,6 +738,35 @@ FP8Q_API fp8q_status fp8q_swiglu_backward(const void* h, const void* d_a, int32_
                                           int32_t fmt, int32_t dir, int32_t pow2_scales, void* d_h, uint8_t* q,
                                           float* scale_inv, uint8_t* q_t, float* scale_inv_t, void* stream);
 
+/* Bytes of workspace fp8q_clip_grads needs for `count` tensors (contents do not matter). */
+FP8Q_API size_t fp8q_clip_grads_workspace_bytes(int32_t count);
+
+/*
+ * The norm of all gradients together, and the gradients scaled to a largest
+ * norm (what follows the weight gradients of a step):
+ *   norm = sqrt(sum over tensors and values of g^2)
+ *   scale = min(1, max_norm / (norm + 1e-6)),  out[i] = grads[i] * scale
+ * Squares are added in FP32 over up to 64 values and in FP64 beyond, in a
+ * fixed order: values from some 1e18 on overflow, those below some 1e-20
+ * count as 0.  A norm of NaN or Inf is reported as it is; Inf gives scale 0,
+ * NaN gives NaN.
+ *   grads, out  host arrays of `count` device pointers; a tensor may be
+ *               overwritten by its own output (out[i] == grads[i]; with
+ *               scale 1 it is then left alone), no other overlap
+ *   sizes       host int64 [count]: values of each tensor (0 for none)
+ *   dts         host int32 [count]: FP8Q_IN_BF16 or FP8Q_IN_FP32, of the
+ *               gradient and its output
+ *   out         NULL: the norm alone (and the scale, if asked for)
+ *   norm        device float[1]
+ *   scale       device float[1], or NULL without out
+ *   workspace   device, 8-byte aligned; calls that may overlap on the GPU
+ *               need separate ones
+ * The arrays are read before the call returns.
+ */
+FP8Q_API fp8q_status fp8q_clip_grads(const void* const* grads, const int64_t* sizes, const int32_t* dts, int32_t count,
+                                     float max_norm, void* const* out, float* norm, float* scale, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /*
  * NVFP4 ("混合精度与 FP8 训练" 13.2): E2M1 elements (0, 0.5, 1, 1.5, 2, 3,
  * 4, 6 and negatives), one E4M3 scale per 16 elements along a row, and one

@@ -36,7 +36,7 @@ __all__ = [
     "SCORE_SOFTMAX", "SCORE_SIGMOID", "fp8q_moe_route", "fp8q_moe_route_backward", "fp8q_moe_rows", "fp8q_moe_plan",
     "fp8q_moe_dispatch", "fp8q_moe_combine", "fp8q_moe_combine_backward",
     "fp8q_rmsnorm", "fp8q_rmsnorm_backward", "fp8q_swiglu", "fp8q_swiglu_backward",
-    "fp8q_moe_decode",
+    "fp8q_moe_decode", "fp8q_grad_norm", "fp8q_clip_grads",
 ]
 
 E4M3 = 0
@@ -95,6 +95,8 @@ _SIGS = {
     "fp8q_moe_decode_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int32, _c.c_int64]),
     "fp8q_moe_decode": (_c.c_int, [_P, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P, _P,
                                    _c.c_int32, _c.c_int32, _P, _P, _c.c_size_t, _P]),
+    "fp8q_clip_grads_workspace_bytes": (_c.c_size_t, [_c.c_int32]),
+    "fp8q_clip_grads": (_c.c_int, [_P, _P, _P, _c.c_int32, _c.c_float, _P, _P, _P, _P, _c.c_size_t, _P]),
     "fp8q_rmsnorm": (_c.c_int, [_P, _c.c_int32, _P, _c.c_int32, _P, _c.c_int32, _c.c_int64, _c.c_int64, _c.c_float,
                                 _c.c_int32, _c.c_int32, _c.c_int32, _P, _P, _P, _P, _P, _P, _P, _P]),
     "fp8q_rmsnorm_backward_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64]),
@@ -1161,6 +1163,50 @@ def fp8q_swiglu_backward(h: torch.Tensor, d_a: torch.Tensor, fmt: int = E5M2, di
     if st:
         _check(st, "fp8q_swiglu_backward")
     return {"d_h": d_h, "q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
+
+
+# ---------------------------------------------------------------------------
+# the gradients' norm
+# ---------------------------------------------------------------------------
+def _clip(grads, max_norm: float, out, want_scale: bool, norm, scale):
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    n, at = len(grads), _device(grads[0], "grads")
+    dts, sizes, ptrs, outs = (_c.c_int32 * n)(), (_c.c_int64 * n)(), (_P * n)(), (_P * n)() if out is not None else None
+    for i, g in enumerate(grads):
+        if g.get_device() != at or g.dtype not in _VALUES or not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be a contiguous bfloat16 or float32 tensor on cuda:{at}")
+        dts[i], sizes[i], ptrs[i] = _IN[g.dtype], g.numel(), g.data_ptr()
+    if out is not None:
+        if len(out) != n:
+            raise ValueError("out must hold one tensor per gradient")
+        for i, (g, o) in enumerate(zip(grads, out)):
+            outs[i] = _result(o, g.shape, g.dtype, g.device).data_ptr()
+    dev = grads[0].device
+    norm = _result(norm, (1,), torch.float32, dev)
+    scale = _result(scale, (1,), torch.float32, dev) if want_scale else None
+    L = _lib or lib()
+    need = L.fp8q_clip_grads_workspace_bytes(n)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    st = L.fp8q_clip_grads(ptrs, sizes, dts, n, max_norm, outs, norm.data_ptr(), _ptr(scale), ws.data_ptr(), need, _stream(at))
+    if st:
+        _check(st, "fp8q_clip_grads")
+    return norm, scale
+
+
+def fp8q_grad_norm(grads, out: torch.Tensor | None = None) -> torch.Tensor:
+    """sqrt of the sum of all squares of the tensors `grads` (BF16 or FP32): float32 [1]."""
+    return _clip(grads, 0.0, None, False, out, None)[0]
+
+
+def fp8q_clip_grads(grads, max_norm: float, out: list | None = None) -> dict:
+    """The tensors `grads` (BF16 or FP32) scaled by min(1, max_norm / (norm + 1e-6)): dict(norm float32 [1], scale
+    float32 [1], grads: a tensor like each).  `out` holds the tensors to write; `grads` itself clips in place."""
+    grads = list(grads)
+    out = [torch.empty_like(g) for g in grads] if out is None else list(out)
+    norm, scale = _clip(grads, max_norm, out, True, None, None)
+    return {"norm": norm, "scale": scale, "grads": out}
 
 
 # ---------------------------------------------------------------------------
