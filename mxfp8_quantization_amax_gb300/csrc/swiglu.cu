@@ -4,37 +4,98 @@
 //   h = [gate | up],  s = 1 / (1 + exp(-gate)),  a = gate * s * up
 //   d_up = d_a * gate * s,   d_gate = d_a * up * s * (1 + gate * (1 - s))
 //
-// With e = exp(-|gate|) and r = 1 / (1 + e), s and 1 - s are r and e r, or the
-// other way round: no difference of near values, no overflow.  FP32 throughout;
-// codes are made from the FP32 values, a dense output is rounded once.
+// With e = exp(-gate), s = 1 / (1 + e) and 1 - s = e s: no difference of near
+// values.  exp(-g) = 2^(-g log2 e), the product as a sum of two FP32 numbers:
+// the larger goes to the exponential instruction, the smaller, l, comes in as
+// 1 + l ln 2.  Where a gate of a thread's eight is beyond +-87 (or is not
+// finite), e = exp(-|gate|) and r = 1 / (1 + e) give s and 1 - s as r and e r, or
+// the other way round, for all eight.  FP32 throughout; codes are made from the
+// FP32 values, a dense output is rounded once.
 #include "quant_tile.cuh"
 
 namespace fp8q {
 
-// s and 1 - s
-__device__ __forceinline__ void sg_sigmoid(float g, float& s, float& t) {
-  const float e = expf(-fabsf(g)), r = __frcp_rn(1.0f + e), er = __fmul_rn(e, r);
-  s = g >= 0.0f ? r : er;
-  t = g >= 0.0f ? er : r;
+// Two values of s and e = (1 - s) / s at a time: packed products and sums.
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float c, float d) {  // a, b = a x + c, b y + d
+  unsigned long long u, v, w;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(a), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(c), "f"(d));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(u) : "l"(v), "l"(w));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(u));
+}
+
+// s and 1 - s (without it, t holds e) of V gates.
+template <bool T, int V>
+__device__ __forceinline__ void sg_sigmoid(const float (&g)[V], float (&s)[V], float (&t)[V]) {
+  constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;  // log2 e = kLog2e + kRest
+  float m;
+  if constexpr (V == 8) m = qt_max8(g);
+  else m = fabsf(g[0]);
+  if (m <= 87.0f) {
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      constexpr int n = V > 1;
+      float t0 = g[k], t1 = g[k + n], l0 = t0, l1 = t1, e0, e1;
+      mul2(t0, t1, -kLog2e, -kLog2e);
+      fma2(l0, l1, kLog2e, kLog2e, t0, t1);  // what the rounding of t took, exactly
+      float r0 = g[k], r1 = g[k + n];
+      fma2(r0, r1, kRest, kRest, l0, l1);
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+      mul2(r0, r1, -kLn2, -kLn2);
+      fma2(r0, r1, e0, e1, e0, e1);
+      float d0 = r0, d1 = r1;
+      fma2(d0, d1, 1.0f, 1.0f, 1.0f, 1.0f);
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d0) : "f"(d0));  // of 1 to 2^126: within one unit
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d1) : "f"(d1));
+      if (T) mul2(r0, r1, d0, d1);
+      s[k] = d0, s[k + n] = d1;
+      t[k] = r0, t[k + n] = r1;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+      const float e = expf(-fabsf(g[k])), r = __frcp_rn(1.0f + e), er = __fmul_rn(e, r);
+      s[k] = g[k] >= 0.0f ? r : er;
+      t[k] = g[k] >= 0.0f ? er : r;
+    }
+  }
 }
 
 template <int V>
 __device__ __forceinline__ void sg_forward(const float (&g)[V], const float (&u)[V], float (&a)[V]) {
+  float s[V], t[V];
+  sg_sigmoid<false>(g, s, t);
 #pragma unroll
-  for (int k = 0; k < V; k++) {
-    float s, t;
-    sg_sigmoid(g[k], s, t);
-    a[k] = __fmul_rn(__fmul_rn(g[k], s), u[k]);
+  for (int k = 0; k < V; k += 2) {
+    constexpr int n = V > 1;
+    float a0 = g[k], a1 = g[k + n];
+    mul2(a0, a1, s[k], s[k + n]);
+    mul2(a0, a1, u[k], u[k + n]);
+    a[k + n] = a1;
+    a[k] = a0;
   }
 }
 
 // One half of d_h: of the gate (UP false) or of the up branch.
-template <bool UP>
-__device__ __forceinline__ float sg_backward(float g, float u, float d) {
-  float s, t;
-  sg_sigmoid(g, s, t);
-  if (UP) return __fmul_rn(d, __fmul_rn(g, s));
-  return __fmul_rn(__fmul_rn(d, u), __fmul_rn(s, __fmaf_rn(g, t, 1.0f)));
+template <bool UP, int V>
+__device__ __forceinline__ void sg_backward(const float (&g)[V], const float (&u)[V], const float (&d)[V], float (&o)[V]) {
+  float s[V], t[V];
+  sg_sigmoid<!UP>(g, s, t);
+#pragma unroll
+  for (int k = 0; k < V; k += 2) {
+    constexpr int n = V > 1;
+    float o0 = g[k], o1 = g[k + n];
+    if (!UP) {
+      fma2(o0, o1, t[k], t[k + n], 1.0f, 1.0f);
+      mul2(o0, o1, u[k], u[k + n]);
+    }
+    mul2(o0, o1, s[k], s[k + n]);
+    mul2(o0, o1, d[k], d[k + n]);
+    o[k + n] = o1;
+    o[k] = o0;
+  }
 }
 
 template <int DT>
@@ -93,8 +154,8 @@ struct SwigluBackward {
     g.get(gv);
     u.get(uv);
     d.get(dv);
-#pragma unroll
-    for (int k = 0; k < V; k++) o[k] = up ? sg_backward<true>(gv[k], uv[k], dv[k]) : sg_backward<false>(gv[k], uv[k], dv[k]);
+    if (up) sg_backward<true>(gv, uv, dv, o);
+    else sg_backward<false>(gv, uv, dv, o);
   }
   __device__ __forceinline__ void tile(float (&v)[8][8], int64_t row, int64_t col, int64_t rows) const {
     const bool up = col >= inner;
@@ -120,13 +181,8 @@ struct SwigluBackward {
         g[i].get(gv);
         u[i].get(uv);
         d[i].get(dv);
-        if (up) {
-#pragma unroll
-          for (int k = 0; k < 8; k++) v[n + i][k] = sg_backward<true>(gv[k], uv[k], dv[k]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; k++) v[n + i][k] = sg_backward<false>(gv[k], uv[k], dv[k]);
-        }
+        if (up) sg_backward<true>(gv, uv, dv, v[n + i]);
+        else sg_backward<false>(gv, uv, dv, v[n + i]);
       }
     }
   }
