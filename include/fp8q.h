@@ -636,10 +636,11 @@ FP8Q_API size_t fp8q_moe_decode_workspace_bytes(int64_t tokens, int32_t top_k, i
  * with W1, W2 the values of blockwise codes (128x128 blocks).  Unlike the
  * path over fp8q_moe_dispatch and the grouped products, tokens and inner
  * values are not quantized: products and sums are FP32's (inner values keep
- * 22 bits; a token's values 2^-32 below the largest of their 128 lose
- * digits).  A slot whose id is no expert's (-1) adds nothing; an expert that
+ * 22 bits for FP32 output, 11 for BF16; a token's values 2^-32 below the
+ * largest of their 128 lose digits).  A slot whose id is no expert's (-1) adds nothing; an expert that
  * a token names twice counts with the sum of the weights.  Sums have a fixed
- * order.  Each chosen expert's weights are read once for up to 8 tokens.
+ * order.  Each chosen expert's weights are read once for up to 8 of its tokens
+ * (16 with more than 8 tokens).
  *   x             device BF16 [tokens][hidden], 16-byte aligned
  *   ids, weights  device int32, float [tokens][top_k], as fp8q_moe_route
  *                 writes them; top_k <= 32

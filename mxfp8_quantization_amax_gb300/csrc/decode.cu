@@ -5,22 +5,18 @@
 // The weights are FP8 codes with one scale for each 128 x 128 block; the tokens
 // and the inner values are not quantized.  With few tokens the weights of the
 // experts that some token chose are nearly all that moves, and each is read
-// once.  A warp takes 32 weight rows against 8 tokens by mma.m16n8k16 in FP16
-// with FP32 sums: a code is an FP16 value as it is, and a BF16 token row
-// becomes FP16 exactly after a power of two for each 128 of it (values 2^-32
-// below their group's largest lose digits).  The inner values are split into
-// two FP16 parts, 22 bits, with a power of two for each 16 of them.
+// once.  A warp takes 32 weight rows and 128 of K against 8 or 16 tokens by
+// mma.m16n8k16 in FP16 with FP32 sums: a code is an FP16 value as it is, and a
+// BF16 token row becomes FP16 exactly after a power of two for each 128 of it
+// (values 2^-32 below their group's largest lose digits).  The inner values
+// are FP16 with a power of two for each 16 or 32 of them; for FP32 output a
+// second FP16 number holds what the first one's rounding (2^-12) left.
 //
-// K is taken in an order that suits the loads: of a block of 128 values the
-// lanes q = 0..3 of a row take 16 q .. 16 q + 15 and 64 beyond, and step s of
-// eight multiplies the four-byte words s & 3 of both, so that 16 K values of a
-// step are {64 (s >> 2) + 16 q + 4 (s & 3) + j}.  The first product's units are
-// those 16 inner values, which is how the second finds them with one scale.
-//
-// First kernel: a unit is 16 inner values of one expert (16 rows of G and of U)
-// for up to 8 of its tokens; the 8 warps of a CTA share K.  Second kernel: a CTA
-// takes 32 output columns of all tokens and sums over the experts, so that every
-// sum has a fixed order; the warps share the experts' blocks of K.
+// First kernel: a unit is 32 inner values of one expert (rows of G and of U)
+// for up to 8 of its tokens, or 16 for up to 16; the 8 warps of a CTA share K.
+// Second kernel: a CTA takes 32 output columns of all tokens and sums over the
+// experts, so that every sum has a fixed order; the warps share the experts'
+// blocks of K.
 #include "fp8q_device.cuh"
 #include "internal.h"
 
@@ -32,8 +28,7 @@ constexpr int kMdTokens = 64;
 constexpr int kMdTopK = 32;
 constexpr int kMdExperts = 1024;
 constexpr int kMdPairs = kMdTokens * kMdTopK;
-constexpr int kMdCols = 8;                                   // tokens of one job
-constexpr int kMdJobs = kMdExperts + kMdPairs / kMdCols;
+constexpr int kMdJobs = kMdExperts + kMdPairs / 8;
 constexpr int kMdPitch = 20;                                 // floats of a column of partial sums (16 rows)
 constexpr int kMdRows = 32;                                  // output columns of a CTA of the second kernel
 constexpr int kMdOutPitch = 36;
@@ -49,13 +44,12 @@ struct MdParams {
   int tokens, top_k, experts, hidden, inner;
   int kb1, kb2, nb1, nb2;
   uint16_t* a_hi;  // [pairs][128 kb2] FP16
-  uint16_t* a_lo;
-  float* a_s;      // [pairs][kb2][8]
-  int out_dt;
+  uint16_t* a_lo;  // or NULL
+  float* a_s;      // [pairs][kb2][8 / GROUPS]
   void* out;
 };
 
-// The (token, expert) pairs in order of expert, and jobs of up to 8 of one expert's.
+// The (token, expert) pairs in order of expert, and jobs of up to COLS of one expert's.
 struct MdLists {
   uint32_t mask[2 * kMdExperts];  // tokens of each expert
   uint32_t job[kMdJobs];          // expert | tokens << 16
@@ -65,6 +59,7 @@ struct MdLists {
   int jobs, pairs;
 };
 
+template <int COLS>
 __device__ __forceinline__ void md_lists(const MdParams& p, MdLists& l) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < 2 * p.experts; i += kMdThreads) l.mask[i] = 0;
@@ -78,7 +73,7 @@ __device__ __forceinline__ void md_lists(const MdParams& p, MdLists& l) {
   int mine = 0;  // jobs << 16 | pairs
   for (int e = e0; e < e1; e++) {
     const int n = __popc(l.mask[2 * e]) + __popc(l.mask[2 * e + 1]);
-    mine += ((n + kMdCols - 1) / kMdCols << 16) + n;
+    mine += ((n + COLS - 1) / COLS << 16) + n;
   }
   int incl = mine;
 #pragma unroll
@@ -97,10 +92,10 @@ __device__ __forceinline__ void md_lists(const MdParams& p, MdLists& l) {
   for (int e = e0; e < e1; e++) {
     uint64_t m = (uint64_t)l.mask[2 * e + 1] << 32 | l.mask[2 * e];
     int n = __popcll(m), pair = at & 0xFFFF, job = at >> 16;
-    at += ((n + kMdCols - 1) / kMdCols << 16) + n;
+    at += ((n + COLS - 1) / COLS << 16) + n;
     for (int i = pair; m; m &= m - 1, i++) l.token[i] = (uint8_t)(__ffsll((long long)m) - 1);
-    for (; n > 0; n -= kMdCols, pair += kMdCols, job++) {
-      l.job[job] = (uint32_t)e | (uint32_t)min(n, kMdCols) << 16;
+    for (; n > 0; n -= COLS, pair += COLS, job++) {
+      l.job[job] = (uint32_t)e | (uint32_t)min(n, COLS) << 16;
       l.first[job] = (uint16_t)pair;
     }
   }
@@ -132,148 +127,282 @@ __device__ __forceinline__ uint32_t md_half2(float lo, float hi) {
   return r;
 }
 
+// The halves of a BF16 pair times a BF16 power of two: the products are exact.
+__device__ __forceinline__ uint32_t md_scaled(uint32_t w, uint32_t power) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 a, b, c;\n\tmov.b32 {a, b}, %2;\n\tcvt.u16.u32 c, %3;\n\t"
+      "fma.rn.f32.bf16 %0, a, c, %4;\n\tfma.rn.f32.bf16 %1, b, c, %4;\n\t}"
+      : "=f"(lo), "=f"(hi) : "r"(w), "r"(power), "f"(-0.0f));
+  return md_half2(lo, hi);
+}
+
 // The power of two that brings magnitudes up to `bits` (FP32) below 2^15, as
 // its exponent field; 254 minus it is its reciprocal's.
 __device__ __forceinline__ uint32_t md_exponent(uint32_t bits) { return min(268u - (bits >> 23), 253u); }
 
-// 128 bytes of K of 32 weight rows: this lane's 32 bytes of rows g and g + 8 of two sets of 16.
-struct MdTile {
-  uint4 v[2][2][2];  // [set][row g, g + 8][K 16 q, 64 + 16 q]
-};
+// A tile: 32 rows of 128 bytes of weights, whose 16-byte chunks are permuted by
+// the row so that the eight rows of a matrix load lie in different banks.  A
+// warp's tiles come by cp.async into a ring of its own; a place is asked for
+// again as soon as its tile has been read.  Step s of a tile multiplies chunk s
+// of all rows: lane q of a row has K values 16 s + 4 q .. 4 q + 3.
+constexpr int kMdStages = 2;
+constexpr int kMdTileBytes = 32 * 128;
+constexpr int kMdRingBytes = kMdStages * kMdTileBytes;  // of one warp
 
-__device__ __forceinline__ uint32_t md_word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+// 16 bytes, or zeros: nothing is asked for where nothing is there.
+__device__ __forceinline__ void md_copy16(uint32_t to, const void* from, bool there) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t"
+      "@!p st.shared.v4.u32 [%0], {%3, %3, %3, %3};\n\t}" ::"r"(to),
+      "l"(from), "r"((uint32_t)there), "r"(0)
+      : "memory");
+}
+__device__ __forceinline__ void md_copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void md_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void md_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t md_smem(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// Asks for rows 0 .. 31 of a tile: 16 rows from `lo` on and 16 from `hi` on, of
+// which n_lo and n_hi are there, and `k` bytes of each (all of 128: most tiles).
+__device__ __forceinline__ void md_tile(uint32_t to, const uint8_t* lo, const uint8_t* hi, int64_t pitch, int n_lo, int n_hi, int k) {
+  const int lane = threadIdx.x & 31, r = lane >> 3, c = lane & 7;
+  const uint32_t even = to + r * 128 + ((c ^ r) << 4), odd = to + r * 128 + ((c ^ (r + 4)) << 4);
+  lo += r * pitch + 16 * c;
+  hi += r * pitch + 16 * c;
+  if (n_lo >= 16 && n_hi >= 16 && k >= 128) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) md_copy16((i & 1 ? odd : even) + i * 512, (i < 4 ? lo : hi) + (i & 3) * 4 * pitch, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const bool there = (i & 3) * 4 + r < (i < 4 ? n_lo : n_hi) && 16 * c < k;
+      md_copy16((i & 1 ? odd : even) + i * 512, (i < 4 ? lo : hi) + (i & 3) * 4 * pitch, there);
+    }
+  }
+}
+
+// Chunk s of the tile: this lane's four codes of rows g, g + 8, g + 16, g + 24.
+// `at`: the tile's start + 128 * lane + 16 * (lane & 7).
+__device__ __forceinline__ void md_chunk(uint32_t at, int s, uint32_t (&w)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(at ^ (s << 4))
+               : "memory");
+}
 
 // ---------------------------------------------------------------------------
 // first product and the activation
 // ---------------------------------------------------------------------------
-// Rows of unit `unit`'s sets (0: gate, 1: up) and where they lie.
+// 16 * GROUPS inner values of an expert from inner0 on, for `count` of its tokens.
 struct MdUnit {
-  int expert, count, first, inner0;  // inner value of row 0; row m is inner0 + 16 (m >> 2) + (m & 3)
+  int expert, count, first, inner0;
 };
 
+template <int GROUPS>
 __device__ __forceinline__ MdUnit md_unit(const MdParams& p, const MdLists& l, int unit) {
-  const int per = p.kb2 * 8, job = unit / per, at = unit - job * per, s = at & 7;
+  const int per = p.kb2 * (8 / GROUPS), job = unit / per;
   MdUnit u;
   u.expert = l.job[job] & 0xFFFF;
   u.count = l.job[job] >> 16;
   u.first = l.first[job];
-  u.inner0 = (at >> 3) * 128 + 64 * (s >> 2) + 4 * (s & 3);
+  u.inner0 = (unit - job * per) * 16 * GROUPS;
   return u;
 }
 
-__device__ __forceinline__ void md_load1(const MdParams& p, const MdUnit& u, int kb, MdTile& t, float (&sc)[2][2]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, k = kb * 128 + 16 * q;
-#pragma unroll
-  for (int set = 0; set < 2; set++)
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const int m = g + 8 * h, i = u.inner0 + 16 * (m >> 2) + (m & 3), row = set * p.inner + i;
-      const bool ok = i < p.inner && kb < p.kb1;
-      const uint8_t* at = p.w1 + ((int64_t)u.expert * 2 * p.inner + row) * p.hidden + k;
-      t.v[set][h][0] = ok && k < p.hidden ? ld_stream(at) : make_uint4(0, 0, 0, 0);
-      t.v[set][h][1] = ok && k + 64 < p.hidden ? ld_stream(at + 64) : make_uint4(0, 0, 0, 0);
-      sc[set][h] = ok ? __ldg(p.s1 + ((int64_t)u.expert * p.nb1 + (row >> 7)) * p.kb1 + kb) : 0.0f;
-    }
+// What a warp asks for next: of one unit after the other the blocks of K warp,
+// warp + 8, ...; with two groups a block takes a tile of gate rows and one of up
+// rows, with one group both are halves of a tile.
+struct MdFeed {
+  int unit, kb, up, rows;  // rows: how many of a tile half are there
+  const uint8_t* gate;     // the unit's first gate row
+  const float* scale;      // lane i < 2 * GROUPS: of set i (gate rows, then up rows)
+};
+
+template <int GROUPS>
+__device__ __forceinline__ void md_feed_unit(const MdParams& p, const MdLists& l, MdFeed& f) {
+  const int lane = threadIdx.x & 31;
+  const MdUnit u = md_unit<GROUPS>(p, l, f.unit);
+  f.rows = p.inner - u.inner0;
+  f.gate = p.w1 + ((int64_t)u.expert * 2 * p.inner + min(u.inner0, p.inner - 16)) * p.hidden;
+  const int row = u.inner0 + 16 * (lane % GROUPS) + (lane / GROUPS ? p.inner : 0);
+  f.scale = p.s1 + ((int64_t)u.expert * p.nb1 + min(row >> 7, p.nb1 - 1)) * p.kb1;
 }
 
-template <int FMT>
+// Asks for the next tile, into `to` (the warp's) and, a block's first, `scales`.
+template <int GROUPS>
+__device__ __forceinline__ void md_feed(const MdParams& p, const MdLists& l, MdFeed& f, int units, int step, uint32_t to,
+                                        uint32_t scales) {
+  if (f.unit < units) {
+    if (f.kb < p.kb1) {
+      const int lane = threadIdx.x & 31, k = f.kb * 128;
+      const int64_t pitch = p.hidden, up = p.inner * pitch;
+      const uint8_t* from = f.gate + k;
+      if (GROUPS == 2) {
+        if (f.up) from += up;
+        md_tile(to, from, from + 16 * pitch, pitch, f.rows, f.rows - 16, p.hidden - k);
+      } else {
+        md_tile(to, from, from + up, pitch, f.rows, f.rows, p.hidden - k);
+      }
+      if (!f.up && lane < 2 * GROUPS) md_copy4(scales + 4 * lane, f.scale + f.kb);
+    }
+    if (GROUPS == 2) f.up ^= 1;
+    if (!f.up) {
+      f.kb += kMdWarps;
+      if (f.kb - (int)(threadIdx.x >> 5) >= p.kb1) {
+        f.kb = threadIdx.x >> 5;
+        f.unit += step;
+        if (f.unit < units) md_feed_unit<GROUPS>(p, l, f);
+      }
+    }
+  }
+  md_commit();
+}
+
+// Units of 32 inner values for 8 tokens (GROUPS 2, NT 1) or of 16 for 16 tokens (1, 2).
+template <int FMT, int GROUPS, int NT>
 __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p) {
+  constexpr int kSets = 2 * GROUPS, kCols = 8 * NT, kSetFloats = kCols * kMdPitch + 16;
+  extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on
   __shared__ MdLists l;
-  __shared__ float part[kMdWarps][2][kMdCols * kMdPitch];
+  __shared__ float part[kMdWarps][kSets * kSetFloats];
+  __shared__ __align__(16) float scales[kMdWarps][kMdStages][4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   pdl_wait();
-  md_lists(p, l);
-  const int units = l.jobs * p.kb2 * 8;
-  int unit = blockIdx.x, kb = warp;
-  if (unit < units) {
-    MdUnit u = md_unit(p, l, unit);
-    MdTile next;
-    float next_sc[2][2];
-    md_load1(p, u, kb, next, next_sc);
-    for (; unit < units; unit += gridDim.x) {
-      float acc[2][4] = {};
-      const int token = g < u.count ? l.token[u.first + g] : -1;
-      for (kb = warp; kb - warp < p.kb1; kb += kMdWarps) {
-        const MdTile tile = next;
-        const float sc[2][2] = {{next_sc[0][0], next_sc[0][1]}, {next_sc[1][0], next_sc[1][1]}};
+  md_lists<kCols>(p, l);
+  // units are dealt out evenly: with fewer CTAs rather than a last round of a few
+  const int units = l.jobs * p.kb2 * (8 / GROUPS), rounds = (units + gridDim.x - 1) / gridDim.x;
+  const int step = rounds ? (units + rounds - 1) / rounds : 0;
+  if ((int)blockIdx.x < step) {
+    const uint32_t ring = ((md_smem(dynamic) + 127) & ~127u) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0][0]);
+    const uint32_t mine = ring + lane * 128 + ((lane & 7) << 4);
+    MdFeed f;
+    f.unit = blockIdx.x;
+    f.kb = warp;
+    f.up = 0;
+    md_feed_unit<GROUPS>(p, l, f);
+#pragma unroll
+    for (int i = 0; i < kMdStages; i++) md_feed<GROUPS>(p, l, f, units, step, ring + i * kMdTileBytes, sc_at + i * 16);
+    int stage = 0;
+    for (int unit = blockIdx.x; unit < units; unit += step) {
+      const MdUnit u = md_unit<GROUPS>(p, l, unit);
+      float acc[NT][kSets][4] = {};
+      const uint16_t* xt[NT];
+      bool there[NT];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        there[n] = g + 8 * n < u.count;
+        xt[n] = p.x + (int64_t)(there[n] ? l.token[u.first + g + 8 * n] : 0) * p.hidden + 4 * q;
+      }
+      for (int kb = warp; kb - warp < p.kb1; kb += kMdWarps) {
         // the tokens' part of this block of K
-        const int k = kb * 128 + 16 * q;
-        uint4 x[4];
+        const int k = kb * 128;
+        uint32_t b[NT][16];
+        float inv[NT][2];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int at = k + 64 * (i >> 1) + 8 * (i & 1);
-          x[i] = token >= 0 && at < p.hidden ? __ldg((const uint4*)(p.x + (int64_t)token * p.hidden + at)) : make_uint4(0, 0, 0, 0);
+        for (int n = 0; n < NT; n++) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int s = 0; s < 8; s++) {
+            const uint2 x = there[n] && k + 16 * s < p.hidden ? __ldg((const uint2*)(xt[n] + k + 16 * s)) : make_uint2(0, 0);
+            b[n][2 * s] = x.x, b[n][2 * s + 1] = x.y;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i++) m = absmax_bf16x2(m, b[n][i]);
+          m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          const uint32_t power = md_exponent(max(m << 16, m & 0xFFFF0000u)), back = (254u - power) << 23;
+          inv[n][0] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q));
+          inv[n][1] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q + 4));
+#pragma unroll
+          for (int i = 0; i < 16; i++) b[n][i] = md_scaled(b[n][i], power << 7);
         }
-        // the next block, of this unit or the next one
-        if (kb - warp + kMdWarps < p.kb1) {
-          md_load1(p, u, kb + kMdWarps, next, next_sc);
-        } else if (unit + gridDim.x < units) {
-          md_load1(p, md_unit(p, l, unit + gridDim.x), warp, next, next_sc);
-        }
-        uint32_t m = 0;
+        float4 sc = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; i++) m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, x[i].x), x[i].y), x[i].z), x[i].w);
-        m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const uint32_t f = md_exponent(max(m << 16, m & 0xFFFF0000u));
-        const float up = __uint_as_float(f << 23);
-        const uint32_t inv = (254u - f) << 23;
-        const float inv0 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, inv, 8 * q)), inv1 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, inv, 8 * q + 4));
-        float d[2][4] = {};
+        for (int tile = 0; tile < GROUPS; tile++) {
+          md_wait<kMdStages - 1>();
+          __syncwarp();
+          if (tile == 0) sc = *(const float4*)scales[warp][stage];
+          float d[NT][2][4] = {};
+          if (kb < p.kb1) {
 #pragma unroll
-        for (int s = 0; s < 8; s++) {
-          const uint4& xv = x[s >> 1];
-          const uint32_t x0 = s & 1 ? xv.z : xv.x, x1 = s & 1 ? xv.w : xv.y;
-          const uint32_t b0 = md_half2(__fmul_rn(bf16_lo(x0), up), __fmul_rn(bf16_hi(x0), up));
-          const uint32_t b1 = md_half2(__fmul_rn(bf16_lo(x1), up), __fmul_rn(bf16_hi(x1), up));
+            for (int s = 0; s < 8; s++) {
+              uint32_t w[4];
+              md_chunk(mine + stage * kMdTileBytes, s, w);
 #pragma unroll
-          for (int set = 0; set < 2; set++) {
-            uint32_t a0, a1, a2, a3;
-            md_codes<FMT>(md_word(tile.v[set][0][s >> 2], s & 3), a0, a2);
-            md_codes<FMT>(md_word(tile.v[set][1][s >> 2], s & 3), a1, a3);
-            md_mma(d[set], a0, a1, a2, a3, b0, b1);
+              for (int set = 0; set < 2; set++) {
+                uint32_t a0, a1, a2, a3;
+                md_codes<FMT>(w[2 * set], a0, a2);
+                md_codes<FMT>(w[2 * set + 1], a1, a3);
+#pragma unroll
+                for (int n = 0; n < NT; n++) md_mma(d[n][set], a0, a1, a2, a3, b[n][2 * s], b[n][2 * s + 1]);
+              }
+            }
+          }
+          __syncwarp();  // all lanes have their codes
+          md_feed<GROUPS>(p, l, f, units, step, ring + stage * kMdTileBytes, sc_at + stage * 16);
+          stage = stage + 1 == kMdStages ? 0 : stage + 1;
+          if (kb < p.kb1) {
+#pragma unroll
+            for (int set = 0; set < 2; set++) {
+              const int at = 2 * tile + set;
+              const float s = at == 0 ? sc.x : at == 1 ? sc.y : at == 2 ? sc.z : sc.w;
+#pragma unroll
+              for (int n = 0; n < NT; n++) {
+                const float f0 = __fmul_rn(s, inv[n][0]), f1 = __fmul_rn(s, inv[n][1]);
+#pragma unroll
+                for (int c = 0; c < 4; c++) acc[n][at][c] = __fmaf_rn(c & 1 ? f1 : f0, d[n][set][c], acc[n][at][c]);
+              }
+            }
           }
         }
-#pragma unroll
-        for (int set = 0; set < 2; set++)
-#pragma unroll
-          for (int c = 0; c < 4; c++)
-            acc[set][c] = __fmaf_rn(__fmul_rn(sc[set][c >> 1], c & 1 ? inv1 : inv0), d[set][c], acc[set][c]);
       }
       __syncthreads();  // the last unit's sums have been read
 #pragma unroll
-      for (int set = 0; set < 2; set++)
+      for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int c = 0; c < 4; c++) part[warp][set][(2 * q + (c & 1)) * kMdPitch + g + 8 * (c >> 1)] = acc[set][c];
+        for (int set = 0; set < kSets; set++)
+#pragma unroll
+          for (int c = 0; c < 4; c++)
+            part[warp][set * kSetFloats + (8 * n + 2 * q + (c & 1)) * kMdPitch + g + 8 * (c >> 1)] = acc[n][set][c];
       __syncthreads();
-      if (tid < kMdCols * 16) {  // inner value tid & 15 of token tid / 16
-        const int m = tid & 15, n = tid >> 4;
+      {  // inner value m for token n: 16 * GROUPS * kCols = 256 of them
+        const int m = tid % (16 * GROUPS), n = tid / (16 * GROUPS), at = n * kMdPitch + (m & 15) + (m >> 4) * kSetFloats;
         float gate = 0.0f, up = 0.0f;
 #pragma unroll
         for (int w = 0; w < kMdWarps; w++) {
-          gate += part[w][0][n * kMdPitch + m];
-          up += part[w][1][n * kMdPitch + m];
+          gate += part[w][at];
+          up += part[w][GROUPS * kSetFloats + at];
         }
         const float e = expf(-fabsf(gate)), r = __frcp_rn(1.0f + e);
         const float a = __fmul_rn(__fmul_rn(gate, gate >= 0.0f ? r : __fmul_rn(e, r)), up);
         uint32_t big = __float_as_uint(a) & 0x7FFFFFFFu;
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-        const uint32_t f = md_exponent(big);
-        const float v = __fmul_rn(a, __uint_as_float(f << 23));
+        for (int o = 1; o < 16 * GROUPS; o <<= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+        const uint32_t power = md_exponent(big);
+        const float v = __fmul_rn(a, __uint_as_float(power << 23));
         const uint32_t hi = md_half2(v, 0.0f) & 0xFFFFu;
-        float back;
-        asm("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(back) : "r"(hi));
-        const uint32_t lo = md_half2((hi & 0x7C00u) == 0x7C00u ? 0.0f : v - back, 0.0f) & 0xFFFFu;
         if (n < u.count) {
-          const int64_t pair = u.first + n, at = pair * p.kb2 * 128 + u.inner0 + 16 * (m >> 2) + (m & 3);
-          p.a_hi[at] = (uint16_t)hi;
-          p.a_lo[at] = (uint16_t)lo;
-          if (m == 0) p.a_s[(pair * p.kb2 + (u.inner0 >> 7)) * 8 + ((u.inner0 >> 4) & 4) + ((u.inner0 >> 2) & 3)] = __uint_as_float((254u - f) << 23);
+          // in the order of the second kernel's lanes: value 16 s + 4 q + j of 128 at 32 q + 4 s + j
+          const int i = u.inner0 + m;
+          const int64_t pair = u.first + n, to = pair * p.kb2 * 128 + (i & ~127) + (i >> 2 & 3) * 32 + (i >> 4 & 7) * 4 + (i & 3);
+          p.a_hi[to] = (uint16_t)hi;
+          if (p.a_lo != nullptr) {
+            float back;
+            asm("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(back) : "r"(hi));
+            p.a_lo[to] = (uint16_t)md_half2((hi & 0x7C00u) == 0x7C00u ? 0.0f : v - back, 0.0f);
+          }
+          if (m == 0) p.a_s[pair * p.kb2 * (8 / GROUPS) + u.inner0 / (16 * GROUPS)] = __uint_as_float((254u - power) << 23);
         }
       }
-      if (unit + gridDim.x < units) u = md_unit(p, l, unit + gridDim.x);
     }
+    md_wait<0>();
   }
   pdl_launch_dependents();
 }
@@ -281,34 +410,66 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
 // ---------------------------------------------------------------------------
 // second product and the weighted sum
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void md_load2(const MdParams& p, const MdLists& l, int at, int row0, MdTile& t, float& sc) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, job = at / p.kb2, kb = at - job * p.kb2;
-  const int e = l.job[job] & 0xFFFF, k = kb * 128 + 16 * q;
-#pragma unroll
-  for (int set = 0; set < 2; set++)
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const int row = row0 + 16 * set + g + 8 * h;
-      const uint8_t* from = p.w2 + ((int64_t)e * p.hidden + row) * p.inner + k;
-      const bool ok = row < p.hidden;
-      t.v[set][h][0] = ok && k < p.inner ? ld_stream(from) : make_uint4(0, 0, 0, 0);
-      t.v[set][h][1] = ok && k + 64 < p.inner ? ld_stream(from + 64) : make_uint4(0, 0, 0, 0);
-    }
-  sc = __ldg(p.s2 + ((int64_t)e * p.nb2 + (row0 >> 7)) * p.kb2 + kb);
+// Asks for block `at` (job, block of K) of rows row0 .. row0 + 31.
+__device__ __forceinline__ void md_feed2(const MdParams& p, const MdLists& l, int at, int end, int row0, uint32_t to, uint32_t scale) {
+  if (at < end) {
+    const int job = at / p.kb2, kb = at - job * p.kb2, e = l.job[job] & 0xFFFF, rows = p.hidden - row0;
+    const uint8_t* from = p.w2 + ((int64_t)e * p.hidden + row0) * p.inner + kb * 128;
+    md_tile(to, from, from + 16 * (int64_t)p.inner, p.inner, rows, rows - 16, p.inner - kb * 128);
+    if ((threadIdx.x & 31) == 0) md_copy4(scale, p.s2 + ((int64_t)e * p.nb2 + (row0 >> 7)) * p.kb2 + kb);
+  }
+  md_commit();
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p) {
-  extern __shared__ float sums[];  // [warps][tokens][kMdOutPitch]
+// The inner values of tokens g, g + 8 and the scales of tokens 2 q, 2 q + 1 (+ 8)
+// for one block of K, 128 / GROUPS / 16 scales each.
+template <int GROUPS, int NT, bool LO>
+struct MdInner {
+  uint4 hi[NT][4], lo[LO ? NT : 1][4];
+  float4 s[NT][2][2 / GROUPS];
+  __device__ __forceinline__ void load(const MdParams& p, const MdLists& l, int at) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, job = at / p.kb2, kb = at - job * p.kb2;
+    const int count = l.job[job] >> 16, first = l.first[job];
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      const int64_t from = (int64_t)(first + g + 8 * n) * p.kb2 * 128 + kb * 128 + 32 * q;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        hi[n][i] = g + 8 * n < count ? *(const uint4*)(p.a_hi + from + 8 * i) : make_uint4(0, 0, 0, 0);
+        if (LO) lo[n][i] = g + 8 * n < count ? *(const uint4*)(p.a_lo + from + 8 * i) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; c++)
+#pragma unroll
+        for (int i = 0; i < 2 / GROUPS; i++)
+          s[n][c][i] = 2 * q + c + 8 * n < count
+                           ? *(const float4*)(p.a_s + ((int64_t)(first + 2 * q + c + 8 * n) * p.kb2 + kb) * (8 / GROUPS) + 4 * i)
+                           : make_float4(0, 0, 0, 0);
+    }
+  }
+};
+
+template <int FMT, int GROUPS, int NT, bool LO>
+__global__ void __launch_bounds__(kMdThreads, NT == 1 ? 2 : 1) decode_second_kernel(MdParams p) {
+  extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on, then the sums
   __shared__ MdLists l;
   __shared__ float weight[kMdPairs];
+  __shared__ float scales[kMdWarps][kMdStages];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int row0 = blockIdx.x * kMdRows;
+  uint8_t* rings = dynamic + (-md_smem(dynamic) & 127u);
+  float* sums = (float*)(rings + kMdWarps * kMdRingBytes);  // [warps][tokens][kMdOutPitch]
   // The first kernel has waited for all before it and writes none of what is read here: only its inner values are waited for below.
-  md_lists(p, l);
+  md_lists<8 * NT>(p, l);
+  const int all = l.jobs * p.kb2;
+  const int begin = (int)((int64_t)all * warp / kMdWarps), end = (int)((int64_t)all * (warp + 1) / kMdWarps);
+  const uint32_t ring = md_smem(rings) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0]);
+  const uint32_t tile_at = ring + lane * 128 + ((lane & 7) << 4);
+#pragma unroll
+  for (int i = 0; i < kMdStages; i++) md_feed2(p, l, begin + i, end, row0, ring + i * kMdTileBytes, sc_at + i * 4);
   for (int i = tid; i < l.pairs; i += kMdThreads) {  // a pair's weight: an expert that a token names twice counts twice
     const int t = l.token[i];
-    int j = 0;  // the pair's expert: the last whose first pair is not behind it
+    int j = 0;  // the pair's job: the last whose first pair is not behind it
     for (int lo = 0, hi = l.jobs; hi - lo > 1;) {
       const int mid = (lo + hi) >> 1;
       if (l.first[mid] <= i) lo = mid; else hi = mid;
@@ -322,67 +483,79 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
   }
   for (int i = tid; i < kMdWarps * p.tokens * kMdOutPitch; i += kMdThreads) sums[i] = 0.0f;
   float* mine = sums + warp * p.tokens * kMdOutPitch;
-  const int all = l.jobs * p.kb2;
-  const int lo = (int)((int64_t)all * warp / kMdWarps), hi = (int)((int64_t)all * (warp + 1) / kMdWarps);
-  MdTile next;
-  float next_sc = 0.0f;
-  if (lo < hi) md_load2(p, l, lo, row0, next, next_sc);
   __syncthreads();
   pdl_wait();
-  float acc[2][4] = {};
-  for (int at = lo; at < hi; at++) {
-    const int job = at / p.kb2, kb = at - job * p.kb2, count = l.job[job] >> 16, first = l.first[job];
-    const MdTile tile = next;
-    const float sc = next_sc;
-    if (at + 1 < hi) md_load2(p, l, at + 1, row0, next, next_sc);
-    const int64_t from = (int64_t)(first + g) * p.kb2 * 128 + kb * 128 + 16 * q;
+  int stage = 0;
+  float acc[NT][2][4] = {};
+  MdInner<GROUPS, NT, LO> next;
+  if (begin < end) next.load(p, l, begin);
+  for (int at = begin; at < end; at++) {
+    const MdInner<GROUPS, NT, LO> a = next;
+    if (at + 1 < end) next.load(p, l, at + 1);
+    md_wait<kMdStages - 1>();
+    __syncwarp();
+    const float sc = scales[warp][stage];
 #pragma unroll
-    for (int half = 0; half < 2; half++) {
-      uint4 bh[2], bl[2];
-      float4 s0 = make_float4(0, 0, 0, 0), s1 = s0;
+    for (int group = 0; group < 8 / GROUPS; group++) {
+      float d[NT][2][4] = {};
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
-        bh[i] = g < count ? *(const uint4*)(p.a_hi + from + 64 * half + 8 * i) : make_uint4(0, 0, 0, 0);
-        bl[i] = g < count ? *(const uint4*)(p.a_lo + from + 64 * half + 8 * i) : make_uint4(0, 0, 0, 0);
-      }
-      if (2 * q < count) s0 = *(const float4*)(p.a_s + ((int64_t)(first + 2 * q) * p.kb2 + kb) * 8 + 4 * half);
-      if (2 * q + 1 < count) s1 = *(const float4*)(p.a_s + ((int64_t)(first + 2 * q + 1) * p.kb2 + kb) * 8 + 4 * half);
-#pragma unroll
-      for (int s = 0; s < 4; s++) {
-        const uint4 &h4 = bh[s >> 1], &l4 = bl[s >> 1];
-        const uint32_t h0 = s & 1 ? h4.z : h4.x, h1 = s & 1 ? h4.w : h4.y, l0 = s & 1 ? l4.z : l4.x, l1 = s & 1 ? l4.w : l4.y;
-        const float f0 = __fmul_rn(sc, s == 0 ? s0.x : s == 1 ? s0.y : s == 2 ? s0.z : s0.w);
-        const float f1 = __fmul_rn(sc, s == 0 ? s1.x : s == 1 ? s1.y : s == 2 ? s1.z : s1.w);
+      for (int s = group * GROUPS; s < (group + 1) * GROUPS; s++) {
+        uint32_t w[4];
+        md_chunk(tile_at + stage * kMdTileBytes, s, w);
 #pragma unroll
         for (int set = 0; set < 2; set++) {
           uint32_t a0, a1, a2, a3;
-          float d[4] = {};
-          md_codes<FMT>(md_word(tile.v[set][0][half], s), a0, a2);
-          md_codes<FMT>(md_word(tile.v[set][1][half], s), a1, a3);
-          md_mma(d, a0, a1, a2, a3, l0, l1);
-          md_mma(d, a0, a1, a2, a3, h0, h1);
+          md_codes<FMT>(w[2 * set], a0, a2);
+          md_codes<FMT>(w[2 * set + 1], a1, a3);
 #pragma unroll
-          for (int c = 0; c < 4; c++) acc[set][c] = __fmaf_rn(c & 1 ? f1 : f0, d[c], acc[set][c]);
+          for (int n = 0; n < NT; n++) {
+            const uint4& h = a.hi[n][s >> 1];
+            if constexpr (LO) {
+              const uint4& v = a.lo[n][s >> 1];
+              md_mma(d[n][set], a0, a1, a2, a3, s & 1 ? v.z : v.x, s & 1 ? v.w : v.y);
+            }
+            md_mma(d[n][set], a0, a1, a2, a3, s & 1 ? h.z : h.x, s & 1 ? h.w : h.y);
+          }
         }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const float4 &s0 = a.s[n][0][group >> 2], &s1 = a.s[n][1][group >> 2];
+        const int i = group & 3;
+        const float f0 = __fmul_rn(sc, i == 0 ? s0.x : i == 1 ? s0.y : i == 2 ? s0.z : s0.w);
+        const float f1 = __fmul_rn(sc, i == 0 ? s1.x : i == 1 ? s1.y : i == 2 ? s1.z : s1.w);
+#pragma unroll
+        for (int set = 0; set < 2; set++)
+#pragma unroll
+          for (int c = 0; c < 4; c++) acc[n][set][c] = __fmaf_rn(c & 1 ? f1 : f0, d[n][set][c], acc[n][set][c]);
       }
     }
-    if (kb == p.kb2 - 1 || at + 1 == hi) {  // on to another job: its tokens' sums leave the registers
+    __syncwarp();  // all lanes have their codes
+    md_feed2(p, l, at + kMdStages, end, row0, ring + stage * kMdTileBytes, sc_at + stage * 4);
+    stage = stage + 1 == kMdStages ? 0 : stage + 1;
+    const int job = at / p.kb2, count = l.job[job] >> 16, first = l.first[job];
+    if (at - job * p.kb2 == p.kb2 - 1 || at + 1 == end) {  // on to another job: its tokens' sums leave the registers
 #pragma unroll
-      for (int n = 0; n < 2; n++) {
-        if (2 * q + n < count) {
-          const float w = weight[first + 2 * q + n];
-          float* to = mine + l.token[first + 2 * q + n] * kMdOutPitch + g;
+      for (int n = 0; n < NT; n++)
 #pragma unroll
-          for (int set = 0; set < 2; set++)
+        for (int c = 0; c < 2; c++) {
+          const int col = 8 * n + 2 * q + c;
+          if (col < count) {
+            const float w = weight[first + col];
+            float* to = mine + l.token[first + col] * kMdOutPitch + g;
 #pragma unroll
-            for (int h = 0; h < 2; h++) to[16 * set + 8 * h] = __fmaf_rn(w, acc[set][2 * h + n], to[16 * set + 8 * h]);
+            for (int set = 0; set < 2; set++)
+#pragma unroll
+              for (int h = 0; h < 2; h++) to[16 * set + 8 * h] = __fmaf_rn(w, acc[n][set][2 * h + c], to[16 * set + 8 * h]);
+          }
         }
-      }
       __syncwarp();
 #pragma unroll
-      for (int set = 0; set < 2; set++)
+      for (int n = 0; n < NT; n++)
 #pragma unroll
-        for (int c = 0; c < 4; c++) acc[set][c] = 0.0f;
+        for (int set = 0; set < 2; set++)
+#pragma unroll
+          for (int c = 0; c < 4; c++) acc[n][set][c] = 0.0f;
     }
   }
   __syncthreads();
@@ -393,12 +566,12 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
 #pragma unroll
     for (int w = 0; w < kMdWarps; w++) v += sums[(w * p.tokens + t) * kMdOutPitch + r];
     const int64_t at = (int64_t)t * p.hidden + row0 + r;
-    if (p.out_dt == FP8Q_OUT_BF16) {
+    if (LO) {
+      ((float*)p.out)[at] = v;
+    } else {
       uint16_t h;
       asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
       ((uint16_t*)p.out)[at] = h;
-    } else {
-      ((float*)p.out)[at] = v;
     }
   }
   pdl_launch_dependents();
@@ -414,21 +587,29 @@ static size_t decode_workspace(int64_t pairs, int64_t inner) {
   return (size_t)(pairs * kb2 * (2 * 2 * 128 + 8 * 4));
 }
 
-template <int FMT>
+template <int FMT, int GROUPS, int NT, bool LO>
 static fp8q_status launch_decode(const MdParams& p, cudaStream_t s) {
+  constexpr size_t kRings = (size_t)kMdWarps * kMdRingBytes + 128, kSums = (size_t)kMdWarps * kMdOutPitch * sizeof(float);
+  static PerDevice<bool> allowed[2];
+  cudaError_t e = allow_smem(allowed[0], decode_first_kernel<FMT, GROUPS, NT>, kRings);
+  if (e == cudaSuccess) e = allow_smem(allowed[1], decode_second_kernel<FMT, GROUPS, NT, LO>, kRings + (NT == 1 ? 8 : kMdTokens) * kSums);
+  if (e != cudaSuccess) return cuda_fail(e, "decode shared memory");
   const int pairs = p.tokens * p.top_k;
-  int64_t units = (int64_t)(pairs < p.experts ? pairs : p.experts + pairs / kMdCols) * p.kb2 * 8;
+  int64_t units = (int64_t)(pairs < p.experts ? pairs : p.experts + pairs / (8 * NT)) * p.kb2 * (8 / GROUPS);  // at most
   const int64_t fit = 2 * (int64_t)sm_count();
   if (units > fit) units = fit;
-  cudaError_t e = launch_kernel(decode_first_kernel<FMT>, dim3((unsigned)units), dim3(kMdThreads), 0, s, p);
+  e = launch_kernel(decode_first_kernel<FMT, GROUPS, NT>, dim3((unsigned)units), dim3(kMdThreads), kRings, s, p);
   if (e != cudaSuccess) return cuda_fail(e, "decode first kernel launch");
-  static PerDevice<bool> allowed;
-  e = allow_smem(allowed, decode_second_kernel<FMT>, (size_t)kMdWarps * kMdTokens * kMdOutPitch * sizeof(float));
-  if (e != cudaSuccess) return cuda_fail(e, "decode shared memory");
-  e = launch_kernel(decode_second_kernel<FMT>, dim3((unsigned)((p.hidden + kMdRows - 1) / kMdRows)), dim3(kMdThreads),
-                    (size_t)kMdWarps * p.tokens * kMdOutPitch * sizeof(float), s, p);
+  e = launch_kernel(decode_second_kernel<FMT, GROUPS, NT, LO>, dim3((unsigned)((p.hidden + kMdRows - 1) / kMdRows)), dim3(kMdThreads),
+                    kRings + p.tokens * kSums, s, p);
   if (e != cudaSuccess) return cuda_fail(e, "decode second kernel launch");
   return check_launch("decode kernel");
+}
+
+template <int FMT>
+static fp8q_status launch_decode_fmt(const MdParams& p, int out_dt, cudaStream_t s) {
+  if (p.tokens <= 8) return out_dt == FP8Q_OUT_FP32 ? launch_decode<FMT, 2, 1, true>(p, s) : launch_decode<FMT, 2, 1, false>(p, s);
+  return out_dt == FP8Q_OUT_FP32 ? launch_decode<FMT, 1, 2, true>(p, s) : launch_decode<FMT, 1, 2, false>(p, s);
 }
 
 }  // namespace fp8q
@@ -483,9 +664,8 @@ extern "C" fp8q_status fp8q_moe_decode(const void* x, int64_t tokens, int64_t hi
   p.nb1 = (int)((2 * inner + 127) / 128);
   p.nb2 = (int)((hidden + 127) / 128);
   p.a_hi = (uint16_t*)workspace;
-  p.a_lo = p.a_hi + pairs * p.kb2 * 128;
-  p.a_s = (float*)(p.a_lo + pairs * p.kb2 * 128);
-  p.out_dt = out_dt;
+  p.a_lo = out_dt == FP8Q_OUT_FP32 ? p.a_hi + pairs * p.kb2 * 128 : nullptr;
+  p.a_s = (float*)(p.a_hi + 2 * pairs * p.kb2 * 128);
   p.out = out;
-  return w_fmt == FP8Q_E4M3 ? launch_decode<kE4M3>(p, (cudaStream_t)stream) : launch_decode<kE5M2>(p, (cudaStream_t)stream);
+  return w_fmt == FP8Q_E4M3 ? launch_decode_fmt<kE4M3>(p, out_dt, (cudaStream_t)stream) : launch_decode_fmt<kE5M2>(p, out_dt, (cudaStream_t)stream);
 }
