@@ -5,18 +5,18 @@
 // The weights are FP8 codes with one scale for each 128 x 128 block; the tokens
 // and the inner values are not quantized.  With few tokens the weights of the
 // experts that some token chose are nearly all that moves, and each is read
-// once.  A warp takes 32 weight rows and 128 of K against 8 or 16 tokens by
+// once.  A warp takes 32 weight rows and 128 of K against 8 tokens by
 // mma.m16n8k16 in FP16 with FP32 sums: a code is an FP16 value as it is, and a
 // BF16 token row becomes FP16 exactly after a power of two for each 128 of it
 // (values 2^-32 below their group's largest lose digits).  The inner values
-// are FP16 with a power of two for each 16 or 32 of them; for FP32 output a
+// are FP16 with a power of two for each 32 of them; for FP32 output a
 // second FP16 number holds what the first one's rounding (2^-12) left.
 //
 // First kernel: a unit is 32 inner values of one expert (rows of G and of U)
-// for up to 8 of its tokens, or 16 for up to 16; the 8 warps of a CTA share K.
-// Second kernel: a CTA takes 32 output columns of all tokens and sums over the
-// experts, so that every sum has a fixed order; the warps share the experts'
-// blocks of K.
+// for up to 8 of its tokens; the 8 warps of a CTA share K.  Second kernel: a
+// CTA takes 32 output columns of all tokens and a share of the experts' blocks
+// of K, and its warps share those; the CTAs of a cluster have the same columns
+// and add up through distributed shared memory.  Every sum has a fixed order.
 #include "fp8q_device.cuh"
 #include "internal.h"
 
@@ -28,8 +28,10 @@ constexpr int kMdTokens = 64;
 constexpr int kMdTopK = 32;
 constexpr int kMdExperts = 1024;
 constexpr int kMdPairs = kMdTokens * kMdTopK;
-constexpr int kMdJobs = kMdExperts + kMdPairs / 8;
+constexpr int kMdCols = 8;                                   // tokens of one job
+constexpr int kMdUnit = 32;                                  // inner values of one unit
 constexpr int kMdPitch = 20;                                 // floats of a column of partial sums (16 rows)
+constexpr int kMdSetFloats = kMdCols * kMdPitch + 16;        // of a set of 16 rows
 constexpr int kMdRows = 32;                                  // output columns of a CTA of the second kernel
 constexpr int kMdOutPitch = 36;
 
@@ -45,35 +47,55 @@ struct MdParams {
   int kb1, kb2, nb1, nb2;
   uint16_t* a_hi;  // [pairs][128 kb2] FP16
   uint16_t* a_lo;  // or NULL
-  float* a_s;      // [pairs][kb2][8 / GROUPS]
+  float* a_s;      // [pairs][kb2][4]
   void* out;
 };
 
-// The (token, expert) pairs in order of expert, and jobs of up to COLS of one expert's.
+// The (token, expert) pairs in order of expert, and jobs of up to 8 of one
+// expert's.  Where the lists lie in shared memory, for `slots` slots:
 struct MdLists {
-  uint32_t mask[2 * kMdExperts];  // tokens of each expert
-  uint32_t job[kMdJobs];          // expert | tokens << 16
-  uint16_t first[kMdJobs];        // first pair
-  uint8_t token[kMdPairs];
-  int warp_sum[kMdWarps];
+  uint32_t* job;     // expert | tokens << 16
+  uint16_t* first;   // first pair of a job
+  uint8_t* token;    // of a pair
+  float* weight;     // of a pair (an expert that a token names twice counts twice); second kernel only
   int jobs, pairs;
 };
 
-template <int COLS>
-__device__ __forceinline__ void md_lists(const MdParams& p, MdLists& l) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 2 * p.experts; i += kMdThreads) l.mask[i] = 0;
+__host__ __device__ constexpr size_t md_list_bytes(int slots) { return (size_t)slots * (4 + 4 + 2 + 1) + 16; }
+
+__device__ __forceinline__ MdLists md_list_places(uint8_t* at, int slots) {
+  MdLists l;
+  l.job = (uint32_t*)at;
+  l.weight = (float*)(at + 4 * slots);
+  l.first = (uint16_t*)(at + 8 * slots);
+  l.token = at + 10 * slots;
+  return l;
+}
+
+// `scratch`: 4 * 2 * experts + 10 * slots bytes that are free again afterwards.
+template <bool WEIGHTS>
+__device__ __forceinline__ void md_lists(const MdParams& p, MdLists& l, uint8_t* scratch, int* warp_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, slots = p.tokens * p.top_k;
+  uint32_t* mask = (uint32_t*)scratch;  // tokens of each expert
+  int* ids = (int*)(mask + 2 * p.experts);
+  float* weights = (float*)(ids + slots);
+  uint16_t* expert = (uint16_t*)(weights + slots);  // of a pair
+  for (int i = tid; i < 2 * p.experts; i += kMdThreads) mask[i] = 0;
+  for (int i = tid; i < slots; i += kMdThreads) {
+    ids[i] = __ldg(p.ids + i);
+    if (WEIGHTS) weights[i] = __ldg(p.weights + i);
+  }
   __syncthreads();
-  for (int i = tid; i < p.tokens * p.top_k; i += kMdThreads) {
-    const int e = __ldg(p.ids + i), t = i / p.top_k;
-    if (e >= 0 && e < p.experts) atomicOr(&l.mask[2 * e + (t >> 5)], 1u << (t & 31));
+  for (int i = tid; i < slots; i += kMdThreads) {
+    const int e = ids[i], t = i / p.top_k;
+    if (e >= 0 && e < p.experts) atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
   }
   __syncthreads();
   const int per = (p.experts + kMdThreads - 1) / kMdThreads, e0 = tid * per, e1 = min(e0 + per, p.experts);
   int mine = 0;  // jobs << 16 | pairs
   for (int e = e0; e < e1; e++) {
-    const int n = __popc(l.mask[2 * e]) + __popc(l.mask[2 * e + 1]);
-    mine += ((n + COLS - 1) / COLS << 16) + n;
+    const int n = __popc(mask[2 * e]) + __popc(mask[2 * e + 1]);
+    mine += ((n + kMdCols - 1) / kMdCols << 16) + n;
   }
   int incl = mine;
 #pragma unroll
@@ -81,26 +103,39 @@ __device__ __forceinline__ void md_lists(const MdParams& p, MdLists& l) {
     const int u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
     if (lane >= o) incl += u;
   }
-  if (lane == 31) l.warp_sum[warp] = incl;
+  if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
   int at = incl - mine, all = 0;
 #pragma unroll
   for (int w = 0; w < kMdWarps; w++) {
-    if (w < warp) at += l.warp_sum[w];
-    all += l.warp_sum[w];
+    if (w < warp) at += warp_sum[w];
+    all += warp_sum[w];
   }
+  l.jobs = all >> 16;
+  l.pairs = all & 0xFFFF;
   for (int e = e0; e < e1; e++) {
-    uint64_t m = (uint64_t)l.mask[2 * e + 1] << 32 | l.mask[2 * e];
+    uint64_t m = (uint64_t)mask[2 * e + 1] << 32 | mask[2 * e];
     int n = __popcll(m), pair = at & 0xFFFF, job = at >> 16;
-    at += ((n + COLS - 1) / COLS << 16) + n;
-    for (int i = pair; m; m &= m - 1, i++) l.token[i] = (uint8_t)(__ffsll((long long)m) - 1);
-    for (; n > 0; n -= COLS, pair += COLS, job++) {
-      l.job[job] = (uint32_t)e | (uint32_t)min(n, COLS) << 16;
+    at += ((n + kMdCols - 1) / kMdCols << 16) + n;
+    for (int i = pair; m; m &= m - 1, i++) {
+      l.token[i] = (uint8_t)(__ffsll((long long)m) - 1);
+      if (WEIGHTS) expert[i] = (uint16_t)e;
+    }
+    for (; n > 0; n -= kMdCols, pair += kMdCols, job++) {
+      l.job[job] = (uint32_t)e | (uint32_t)min(n, kMdCols) << 16;
       l.first[job] = (uint16_t)pair;
     }
   }
-  if (tid == 0) l.jobs = all >> 16, l.pairs = all & 0xFFFF;
   __syncthreads();
+  if (WEIGHTS) {
+    for (int i = tid; i < l.pairs; i += kMdThreads) {
+      const int e = expert[i], from = l.token[i] * p.top_k;
+      float w = 0.0f;
+      for (int k = 0; k < p.top_k; k++) w += ids[from + k] == e ? weights[from + k] : 0.0f;
+      l.weight[i] = w;
+    }
+    __syncthreads();  // the scratch is free
+  }
 }
 
 // Two codes -> two FP16 values, exactly.
@@ -200,211 +235,182 @@ __device__ __forceinline__ void md_chunk(uint32_t at, int s, uint32_t (&w)[4]) {
 // ---------------------------------------------------------------------------
 // first product and the activation
 // ---------------------------------------------------------------------------
-// 16 * GROUPS inner values of an expert from inner0 on, for `count` of its tokens.
+// 32 inner values of an expert from inner0 on, for `count` of its tokens.
 struct MdUnit {
   int expert, count, first, inner0;
 };
 
-template <int GROUPS>
 __device__ __forceinline__ MdUnit md_unit(const MdParams& p, const MdLists& l, int unit) {
-  const int per = p.kb2 * (8 / GROUPS), job = unit / per;
+  const int per = p.kb2 * (128 / kMdUnit), job = unit / per;
   MdUnit u;
   u.expert = l.job[job] & 0xFFFF;
   u.count = l.job[job] >> 16;
   u.first = l.first[job];
-  u.inner0 = (unit - job * per) * 16 * GROUPS;
+  u.inner0 = (unit - job * per) * kMdUnit;
   return u;
 }
 
 // What a warp asks for next: of one unit after the other the blocks of K warp,
-// warp + 8, ...; with two groups a block takes a tile of gate rows and one of up
-// rows, with one group both are halves of a tile.
+// warp + 8, ..., of each a tile of gate rows and one of up rows.
 struct MdFeed {
-  int unit, kb, up, rows;  // rows: how many of a tile half are there
+  int unit, kb, up, rows;  // rows: how many of a tile are there
   const uint8_t* gate;     // the unit's first gate row
-  const float* scale;      // lane i < 2 * GROUPS: of set i (gate rows, then up rows)
+  const float* scale;      // lane i < 4: of rows 0, 16 (gate), 0, 16 (up)
 };
 
-template <int GROUPS>
 __device__ __forceinline__ void md_feed_unit(const MdParams& p, const MdLists& l, MdFeed& f) {
   const int lane = threadIdx.x & 31;
-  const MdUnit u = md_unit<GROUPS>(p, l, f.unit);
+  const MdUnit u = md_unit(p, l, f.unit);
   f.rows = p.inner - u.inner0;
   f.gate = p.w1 + ((int64_t)u.expert * 2 * p.inner + min(u.inner0, p.inner - 16)) * p.hidden;
-  const int row = u.inner0 + 16 * (lane % GROUPS) + (lane / GROUPS ? p.inner : 0);
+  const int row = u.inner0 + 16 * (lane & 1) + (lane & 2 ? p.inner : 0);
   f.scale = p.s1 + ((int64_t)u.expert * p.nb1 + min(row >> 7, p.nb1 - 1)) * p.kb1;
 }
 
 // Asks for the next tile, into `to` (the warp's) and, a block's first, `scales`.
-template <int GROUPS>
 __device__ __forceinline__ void md_feed(const MdParams& p, const MdLists& l, MdFeed& f, int units, int step, uint32_t to,
                                         uint32_t scales) {
   if (f.unit < units) {
     if (f.kb < p.kb1) {
       const int lane = threadIdx.x & 31, k = f.kb * 128;
-      const int64_t pitch = p.hidden, up = p.inner * pitch;
-      const uint8_t* from = f.gate + k;
-      if (GROUPS == 2) {
-        if (f.up) from += up;
-        md_tile(to, from, from + 16 * pitch, pitch, f.rows, f.rows - 16, p.hidden - k);
-      } else {
-        md_tile(to, from, from + up, pitch, f.rows, f.rows, p.hidden - k);
-      }
-      if (!f.up && lane < 2 * GROUPS) md_copy4(scales + 4 * lane, f.scale + f.kb);
+      const int64_t pitch = p.hidden;
+      const uint8_t* from = f.gate + k + (f.up ? p.inner * pitch : 0);
+      md_tile(to, from, from + 16 * pitch, pitch, f.rows, f.rows - 16, p.hidden - k);
+      if (!f.up && lane < 4) md_copy4(scales + 4 * lane, f.scale + f.kb);
     }
-    if (GROUPS == 2) f.up ^= 1;
+    f.up ^= 1;
     if (!f.up) {
       f.kb += kMdWarps;
       if (f.kb - (int)(threadIdx.x >> 5) >= p.kb1) {
         f.kb = threadIdx.x >> 5;
         f.unit += step;
-        if (f.unit < units) md_feed_unit<GROUPS>(p, l, f);
+        if (f.unit < units) md_feed_unit(p, l, f);
       }
     }
   }
   md_commit();
 }
 
-// Units of 32 inner values for 8 tokens (GROUPS 2, NT 1) or of 16 for 16 tokens (1, 2).
-template <int FMT, int GROUPS, int NT>
+template <int FMT>
 __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p) {
-  constexpr int kSets = 2 * GROUPS, kCols = 8 * NT, kSetFloats = kCols * kMdPitch + 16;
-  extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on
-  __shared__ MdLists l;
-  __shared__ float part[kMdWarps][kSets * kSetFloats];
+  extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on, then the lists
+  __shared__ float part[kMdWarps][4 * kMdSetFloats];
   __shared__ __align__(16) float scales[kMdWarps][kMdStages][4];
+  __shared__ int warp_sum[kMdWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  uint8_t* rings = dynamic + (-md_smem(dynamic) & 127u);
+  MdLists l = md_list_places(rings + kMdWarps * kMdRingBytes, p.tokens * p.top_k);
   pdl_wait();
-  md_lists<kCols>(p, l);
+  // The second kernel's CTAs may come as soon as there is room: they ask for
+  // their first weights and wait for this kernel's end before they go on.
+  pdl_launch_dependents();
+  md_lists<false>(p, l, rings, warp_sum);
   // units are dealt out evenly: with fewer CTAs rather than a last round of a few
-  const int units = l.jobs * p.kb2 * (8 / GROUPS), rounds = (units + gridDim.x - 1) / gridDim.x;
+  const int units = l.jobs * p.kb2 * (128 / kMdUnit), rounds = (units + gridDim.x - 1) / gridDim.x;
   const int step = rounds ? (units + rounds - 1) / rounds : 0;
-  if ((int)blockIdx.x < step) {
-    const uint32_t ring = ((md_smem(dynamic) + 127) & ~127u) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0][0]);
-    const uint32_t mine = ring + lane * 128 + ((lane & 7) << 4);
-    MdFeed f;
-    f.unit = blockIdx.x;
-    f.kb = warp;
-    f.up = 0;
-    md_feed_unit<GROUPS>(p, l, f);
+  if ((int)blockIdx.x >= step) return;
+  const uint32_t ring = md_smem(rings) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0][0]);
+  const uint32_t mine = ring + lane * 128 + ((lane & 7) << 4);
+  MdFeed f;
+  f.unit = blockIdx.x;
+  f.kb = warp;
+  f.up = 0;
+  md_feed_unit(p, l, f);
 #pragma unroll
-    for (int i = 0; i < kMdStages; i++) md_feed<GROUPS>(p, l, f, units, step, ring + i * kMdTileBytes, sc_at + i * 16);
-    int stage = 0;
-    for (int unit = blockIdx.x; unit < units; unit += step) {
-      const MdUnit u = md_unit<GROUPS>(p, l, unit);
-      float acc[NT][kSets][4] = {};
-      const uint16_t* xt[NT];
-      bool there[NT];
+  for (int i = 0; i < kMdStages; i++) md_feed(p, l, f, units, step, ring + i * kMdTileBytes, sc_at + i * 16);
+  int stage = 0;
+  for (int unit = blockIdx.x; unit < units; unit += step) {
+    const MdUnit u = md_unit(p, l, unit);
+    float acc[4][4] = {};
+    const bool there = g < u.count;
+    const uint16_t* xt = p.x + (int64_t)(there ? l.token[u.first + g] : 0) * p.hidden + 4 * q;
+    for (int kb = warp; kb - warp < p.kb1; kb += kMdWarps) {
+      // the tokens' part of this block of K
+      const int k = kb * 128;
+      uint32_t b[16], m = 0;
 #pragma unroll
-      for (int n = 0; n < NT; n++) {
-        there[n] = g + 8 * n < u.count;
-        xt[n] = p.x + (int64_t)(there[n] ? l.token[u.first + g + 8 * n] : 0) * p.hidden + 4 * q;
+      for (int s = 0; s < 8; s++) {
+        const uint2 x = there && k + 16 * s < p.hidden ? __ldg((const uint2*)(xt + k + 16 * s)) : make_uint2(0, 0);
+        b[2 * s] = x.x, b[2 * s + 1] = x.y;
       }
-      for (int kb = warp; kb - warp < p.kb1; kb += kMdWarps) {
-        // the tokens' part of this block of K
-        const int k = kb * 128;
-        uint32_t b[NT][16];
-        float inv[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-          uint32_t m = 0;
+      for (int i = 0; i < 16; i++) m = absmax_bf16x2(m, b[i]);
+      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const uint32_t power = md_exponent(max(m << 16, m & 0xFFFF0000u)), back = (254u - power) << 23;
+      const float inv0 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q));
+      const float inv1 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q + 4));
+#pragma unroll
+      for (int i = 0; i < 16; i++) b[i] = md_scaled(b[i], power << 7);
+      float4 sc = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int tile = 0; tile < 2; tile++) {
+        md_wait<kMdStages - 1>();
+        __syncwarp();
+        if (tile == 0) sc = *(const float4*)scales[warp][stage];
+        float d[2][4] = {};
+        if (kb < p.kb1) {  // else the rest of the warps' last round
 #pragma unroll
           for (int s = 0; s < 8; s++) {
-            const uint2 x = there[n] && k + 16 * s < p.hidden ? __ldg((const uint2*)(xt[n] + k + 16 * s)) : make_uint2(0, 0);
-            b[n][2 * s] = x.x, b[n][2 * s + 1] = x.y;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; i++) m = absmax_bf16x2(m, b[n][i]);
-          m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-          m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          const uint32_t power = md_exponent(max(m << 16, m & 0xFFFF0000u)), back = (254u - power) << 23;
-          inv[n][0] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q));
-          inv[n][1] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q + 4));
-#pragma unroll
-          for (int i = 0; i < 16; i++) b[n][i] = md_scaled(b[n][i], power << 7);
-        }
-        float4 sc = make_float4(0, 0, 0, 0);
-#pragma unroll
-        for (int tile = 0; tile < GROUPS; tile++) {
-          md_wait<kMdStages - 1>();
-          __syncwarp();
-          if (tile == 0) sc = *(const float4*)scales[warp][stage];
-          float d[NT][2][4] = {};
-          if (kb < p.kb1) {
-#pragma unroll
-            for (int s = 0; s < 8; s++) {
-              uint32_t w[4];
-              md_chunk(mine + stage * kMdTileBytes, s, w);
-#pragma unroll
-              for (int set = 0; set < 2; set++) {
-                uint32_t a0, a1, a2, a3;
-                md_codes<FMT>(w[2 * set], a0, a2);
-                md_codes<FMT>(w[2 * set + 1], a1, a3);
-#pragma unroll
-                for (int n = 0; n < NT; n++) md_mma(d[n][set], a0, a1, a2, a3, b[n][2 * s], b[n][2 * s + 1]);
-              }
-            }
-          }
-          __syncwarp();  // all lanes have their codes
-          md_feed<GROUPS>(p, l, f, units, step, ring + stage * kMdTileBytes, sc_at + stage * 16);
-          stage = stage + 1 == kMdStages ? 0 : stage + 1;
-          if (kb < p.kb1) {
+            uint32_t w[4];
+            md_chunk(mine + stage * kMdTileBytes, s, w);
 #pragma unroll
             for (int set = 0; set < 2; set++) {
-              const int at = 2 * tile + set;
-              const float s = at == 0 ? sc.x : at == 1 ? sc.y : at == 2 ? sc.z : sc.w;
-#pragma unroll
-              for (int n = 0; n < NT; n++) {
-                const float f0 = __fmul_rn(s, inv[n][0]), f1 = __fmul_rn(s, inv[n][1]);
-#pragma unroll
-                for (int c = 0; c < 4; c++) acc[n][at][c] = __fmaf_rn(c & 1 ? f1 : f0, d[n][set][c], acc[n][at][c]);
-              }
+              uint32_t a0, a1, a2, a3;
+              md_codes<FMT>(w[2 * set], a0, a2);
+              md_codes<FMT>(w[2 * set + 1], a1, a3);
+              md_mma(d[set], a0, a1, a2, a3, b[2 * s], b[2 * s + 1]);
             }
           }
         }
-      }
-      __syncthreads();  // the last unit's sums have been read
+        __syncwarp();  // all lanes have their codes
+        md_feed(p, l, f, units, step, ring + stage * kMdTileBytes, sc_at + stage * 16);
+        stage = stage + 1 == kMdStages ? 0 : stage + 1;
+        if (kb < p.kb1) {
 #pragma unroll
-      for (int n = 0; n < NT; n++)
+          for (int set = 0; set < 2; set++) {
+            const float s = tile ? (set ? sc.w : sc.z) : (set ? sc.y : sc.x);
+            const float f0 = __fmul_rn(s, inv0), f1 = __fmul_rn(s, inv1);
 #pragma unroll
-        for (int set = 0; set < kSets; set++)
-#pragma unroll
-          for (int c = 0; c < 4; c++)
-            part[warp][set * kSetFloats + (8 * n + 2 * q + (c & 1)) * kMdPitch + g + 8 * (c >> 1)] = acc[n][set][c];
-      __syncthreads();
-      {  // inner value m for token n: 16 * GROUPS * kCols = 256 of them
-        const int m = tid % (16 * GROUPS), n = tid / (16 * GROUPS), at = n * kMdPitch + (m & 15) + (m >> 4) * kSetFloats;
-        float gate = 0.0f, up = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kMdWarps; w++) {
-          gate += part[w][at];
-          up += part[w][GROUPS * kSetFloats + at];
-        }
-        const float e = expf(-fabsf(gate)), r = __frcp_rn(1.0f + e);
-        const float a = __fmul_rn(__fmul_rn(gate, gate >= 0.0f ? r : __fmul_rn(e, r)), up);
-        uint32_t big = __float_as_uint(a) & 0x7FFFFFFFu;
-#pragma unroll
-        for (int o = 1; o < 16 * GROUPS; o <<= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
-        const uint32_t power = md_exponent(big);
-        const float v = __fmul_rn(a, __uint_as_float(power << 23));
-        const uint32_t hi = md_half2(v, 0.0f) & 0xFFFFu;
-        if (n < u.count) {
-          // in the order of the second kernel's lanes: value 16 s + 4 q + j of 128 at 32 q + 4 s + j
-          const int i = u.inner0 + m;
-          const int64_t pair = u.first + n, to = pair * p.kb2 * 128 + (i & ~127) + (i >> 2 & 3) * 32 + (i >> 4 & 7) * 4 + (i & 3);
-          p.a_hi[to] = (uint16_t)hi;
-          if (p.a_lo != nullptr) {
-            float back;
-            asm("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(back) : "r"(hi));
-            p.a_lo[to] = (uint16_t)md_half2((hi & 0x7C00u) == 0x7C00u ? 0.0f : v - back, 0.0f);
+            for (int c = 0; c < 4; c++) acc[2 * tile + set][c] = __fmaf_rn(c & 1 ? f1 : f0, d[set][c], acc[2 * tile + set][c]);
           }
-          if (m == 0) p.a_s[pair * p.kb2 * (8 / GROUPS) + u.inner0 / (16 * GROUPS)] = __uint_as_float((254u - power) << 23);
         }
       }
     }
-    md_wait<0>();
+    __syncthreads();  // the last unit's sums have been read
+#pragma unroll
+    for (int set = 0; set < 4; set++)
+#pragma unroll
+      for (int c = 0; c < 4; c++) part[warp][set * kMdSetFloats + (2 * q + (c & 1)) * kMdPitch + g + 8 * (c >> 1)] = acc[set][c];
+    __syncthreads();
+    {  // inner value m for token n: a warp each token
+      const int m = tid % kMdUnit, n = tid / kMdUnit, at = n * kMdPitch + (m & 15) + (m >> 4) * kMdSetFloats;
+      float gate = 0.0f, up = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kMdWarps; w++) {
+        gate += part[w][at];
+        up += part[w][2 * kMdSetFloats + at];
+      }
+      const float e = expf(-fabsf(gate)), r = __frcp_rn(1.0f + e);
+      const float a = __fmul_rn(__fmul_rn(gate, gate >= 0.0f ? r : __fmul_rn(e, r)), up);
+      const uint32_t power = md_exponent(warp_max_u32(__float_as_uint(a) & 0x7FFFFFFFu));
+      const float v = __fmul_rn(a, __uint_as_float(power << 23));
+      const uint32_t hi = md_half2(v, 0.0f) & 0xFFFFu;
+      if (n < u.count) {
+        // in the order of the second kernel's lanes: value 16 s + 4 q + j of 128 at 32 q + 4 s + j
+        const int i = u.inner0 + m;
+        const int64_t pair = u.first + n, to = pair * p.kb2 * 128 + (i & ~127) + (i >> 2 & 3) * 32 + (i >> 4 & 7) * 4 + (i & 3);
+        p.a_hi[to] = (uint16_t)hi;
+        if (p.a_lo != nullptr) {
+          float back;
+          asm("{\n\t.reg .b16 h, z;\n\tmov.b32 {h, z}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(back) : "r"(hi));
+          p.a_lo[to] = (uint16_t)md_half2((hi & 0x7C00u) == 0x7C00u ? 0.0f : v - back, 0.0f);
+        }
+        if (m == 0) p.a_s[pair * p.kb2 * 4 + u.inner0 / kMdUnit] = __uint_as_float((254u - power) << 23);
+      }
+    }
   }
-  pdl_launch_dependents();
+  md_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -421,85 +427,69 @@ __device__ __forceinline__ void md_feed2(const MdParams& p, const MdLists& l, in
   md_commit();
 }
 
-// The inner values of tokens g, g + 8 and the scales of tokens 2 q, 2 q + 1 (+ 8)
-// for one block of K, 128 / GROUPS / 16 scales each.
-template <int GROUPS, int NT, bool LO>
+// The inner values of token g and the scales of tokens 2 q, 2 q + 1 for one block of K.
+template <bool LO>
 struct MdInner {
-  uint4 hi[NT][4], lo[LO ? NT : 1][4];
-  float4 s[NT][2][2 / GROUPS];
+  uint4 hi[4], lo[LO ? 4 : 1];
+  float4 s[2];
   __device__ __forceinline__ void load(const MdParams& p, const MdLists& l, int at) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, job = at / p.kb2, kb = at - job * p.kb2;
     const int count = l.job[job] >> 16, first = l.first[job];
+    const int64_t from = (int64_t)(first + g) * p.kb2 * 128 + kb * 128 + 32 * q;
 #pragma unroll
-    for (int n = 0; n < NT; n++) {
-      const int64_t from = (int64_t)(first + g + 8 * n) * p.kb2 * 128 + kb * 128 + 32 * q;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        hi[n][i] = g + 8 * n < count ? *(const uint4*)(p.a_hi + from + 8 * i) : make_uint4(0, 0, 0, 0);
-        if (LO) lo[n][i] = g + 8 * n < count ? *(const uint4*)(p.a_lo + from + 8 * i) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; c++)
-#pragma unroll
-        for (int i = 0; i < 2 / GROUPS; i++)
-          s[n][c][i] = 2 * q + c + 8 * n < count
-                           ? *(const float4*)(p.a_s + ((int64_t)(first + 2 * q + c + 8 * n) * p.kb2 + kb) * (8 / GROUPS) + 4 * i)
-                           : make_float4(0, 0, 0, 0);
+    for (int i = 0; i < 4; i++) {
+      hi[i] = g < count ? *(const uint4*)(p.a_hi + from + 8 * i) : make_uint4(0, 0, 0, 0);
+      if (LO) lo[i] = g < count ? *(const uint4*)(p.a_lo + from + 8 * i) : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int c = 0; c < 2; c++)
+      s[c] = 2 * q + c < count ? *(const float4*)(p.a_s + ((int64_t)(first + 2 * q + c) * p.kb2 + kb) * 4) : make_float4(0, 0, 0, 0);
   }
 };
 
-template <int FMT, int GROUPS, int NT, bool LO>
-__global__ void __launch_bounds__(kMdThreads, NT == 1 ? 2 : 1) decode_second_kernel(MdParams p) {
-  extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on, then the sums
-  __shared__ MdLists l;
-  __shared__ float weight[kMdPairs];
+__device__ __forceinline__ void md_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int FMT, bool LO>
+__global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p, int shares) {
+  extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on, then the lists and the sums
   __shared__ float scales[kMdWarps][kMdStages];
+  __shared__ int warp_sum[kMdWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int row0 = blockIdx.x * kMdRows;
+  const int row0 = blockIdx.x / shares * kMdRows, rank = blockIdx.x % shares;
   uint8_t* rings = dynamic + (-md_smem(dynamic) & 127u);
   float* sums = (float*)(rings + kMdWarps * kMdRingBytes);  // [warps][tokens][kMdOutPitch]
-  // The first kernel has waited for all before it and writes none of what is read here: only its inner values are waited for below.
-  md_lists<8 * NT>(p, l);
-  const int all = l.jobs * p.kb2;
-  const int begin = (int)((int64_t)all * warp / kMdWarps), end = (int)((int64_t)all * (warp + 1) / kMdWarps);
+  MdLists l = md_list_places((uint8_t*)(sums + kMdWarps * p.tokens * kMdOutPitch), p.tokens * p.top_k);
+  // The first kernel has waited for all before it and writes none of what is
+  // read here: only its inner values are waited for below.
+  md_lists<true>(p, l, rings, warp_sum);
+  const int64_t all = (int64_t)l.jobs * p.kb2;
+  const int parts = kMdWarps * shares, part = rank * kMdWarps + warp;
+  const int begin = (int)(all * part / parts), end = (int)(all * (part + 1) / parts);
   const uint32_t ring = md_smem(rings) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0]);
   const uint32_t tile_at = ring + lane * 128 + ((lane & 7) << 4);
 #pragma unroll
   for (int i = 0; i < kMdStages; i++) md_feed2(p, l, begin + i, end, row0, ring + i * kMdTileBytes, sc_at + i * 4);
-  for (int i = tid; i < l.pairs; i += kMdThreads) {  // a pair's weight: an expert that a token names twice counts twice
-    const int t = l.token[i];
-    int j = 0;  // the pair's job: the last whose first pair is not behind it
-    for (int lo = 0, hi = l.jobs; hi - lo > 1;) {
-      const int mid = (lo + hi) >> 1;
-      if (l.first[mid] <= i) lo = mid; else hi = mid;
-      j = lo;
-    }
-    const int e = l.job[j] & 0xFFFF;
-    float w = 0.0f;
-    for (int k = 0; k < p.top_k; k++)
-      if (__ldg(p.ids + t * p.top_k + k) == e) w += __ldg(p.weights + t * p.top_k + k);
-    weight[i] = w;
-  }
-  for (int i = tid; i < kMdWarps * p.tokens * kMdOutPitch; i += kMdThreads) sums[i] = 0.0f;
   float* mine = sums + warp * p.tokens * kMdOutPitch;
-  __syncthreads();
+  for (int i = lane; i < p.tokens * kMdOutPitch; i += 32) mine[i] = 0.0f;
+  __syncwarp();
   pdl_wait();
   int stage = 0;
-  float acc[NT][2][4] = {};
-  MdInner<GROUPS, NT, LO> next;
+  float acc[2][4] = {};
+  MdInner<LO> next;
   if (begin < end) next.load(p, l, begin);
   for (int at = begin; at < end; at++) {
-    const MdInner<GROUPS, NT, LO> a = next;
+    const MdInner<LO> a = next;
     if (at + 1 < end) next.load(p, l, at + 1);
     md_wait<kMdStages - 1>();
     __syncwarp();
     const float sc = scales[warp][stage];
 #pragma unroll
-    for (int group = 0; group < 8 / GROUPS; group++) {
-      float d[NT][2][4] = {};
+    for (int group = 0; group < 4; group++) {  // 32 inner values with one scale
+      float d[2][4] = {};
 #pragma unroll
-      for (int s = group * GROUPS; s < (group + 1) * GROUPS; s++) {
+      for (int s = 2 * group; s < 2 * group + 2; s++) {
         uint32_t w[4];
         md_chunk(tile_at + stage * kMdTileBytes, s, w);
 #pragma unroll
@@ -507,28 +497,20 @@ __global__ void __launch_bounds__(kMdThreads, NT == 1 ? 2 : 1) decode_second_ker
           uint32_t a0, a1, a2, a3;
           md_codes<FMT>(w[2 * set], a0, a2);
           md_codes<FMT>(w[2 * set + 1], a1, a3);
-#pragma unroll
-          for (int n = 0; n < NT; n++) {
-            const uint4& h = a.hi[n][s >> 1];
-            if constexpr (LO) {
-              const uint4& v = a.lo[n][s >> 1];
-              md_mma(d[n][set], a0, a1, a2, a3, s & 1 ? v.z : v.x, s & 1 ? v.w : v.y);
-            }
-            md_mma(d[n][set], a0, a1, a2, a3, s & 1 ? h.z : h.x, s & 1 ? h.w : h.y);
+          if constexpr (LO) {
+            const uint4& v = a.lo[s >> 1];
+            md_mma(d[set], a0, a1, a2, a3, s & 1 ? v.z : v.x, s & 1 ? v.w : v.y);
           }
+          const uint4& h = a.hi[s >> 1];
+          md_mma(d[set], a0, a1, a2, a3, s & 1 ? h.z : h.x, s & 1 ? h.w : h.y);
         }
       }
+      const float f0 = __fmul_rn(sc, group == 0 ? a.s[0].x : group == 1 ? a.s[0].y : group == 2 ? a.s[0].z : a.s[0].w);
+      const float f1 = __fmul_rn(sc, group == 0 ? a.s[1].x : group == 1 ? a.s[1].y : group == 2 ? a.s[1].z : a.s[1].w);
 #pragma unroll
-      for (int n = 0; n < NT; n++) {
-        const float4 &s0 = a.s[n][0][group >> 2], &s1 = a.s[n][1][group >> 2];
-        const int i = group & 3;
-        const float f0 = __fmul_rn(sc, i == 0 ? s0.x : i == 1 ? s0.y : i == 2 ? s0.z : s0.w);
-        const float f1 = __fmul_rn(sc, i == 0 ? s1.x : i == 1 ? s1.y : i == 2 ? s1.z : s1.w);
+      for (int set = 0; set < 2; set++)
 #pragma unroll
-        for (int set = 0; set < 2; set++)
-#pragma unroll
-          for (int c = 0; c < 4; c++) acc[n][set][c] = __fmaf_rn(c & 1 ? f1 : f0, d[n][set][c], acc[n][set][c]);
-      }
+        for (int c = 0; c < 4; c++) acc[set][c] = __fmaf_rn(c & 1 ? f1 : f0, d[set][c], acc[set][c]);
     }
     __syncwarp();  // all lanes have their codes
     md_feed2(p, l, at + kMdStages, end, row0, ring + stage * kMdTileBytes, sc_at + stage * 4);
@@ -536,35 +518,51 @@ __global__ void __launch_bounds__(kMdThreads, NT == 1 ? 2 : 1) decode_second_ker
     const int job = at / p.kb2, count = l.job[job] >> 16, first = l.first[job];
     if (at - job * p.kb2 == p.kb2 - 1 || at + 1 == end) {  // on to another job: its tokens' sums leave the registers
 #pragma unroll
-      for (int n = 0; n < NT; n++)
+      for (int c = 0; c < 2; c++) {
+        const int col = 2 * q + c;
+        if (col < count) {
+          const float w = l.weight[first + col];
+          float* to = mine + l.token[first + col] * kMdOutPitch + g;
 #pragma unroll
-        for (int c = 0; c < 2; c++) {
-          const int col = 8 * n + 2 * q + c;
-          if (col < count) {
-            const float w = weight[first + col];
-            float* to = mine + l.token[first + col] * kMdOutPitch + g;
+          for (int set = 0; set < 2; set++)
 #pragma unroll
-            for (int set = 0; set < 2; set++)
-#pragma unroll
-              for (int h = 0; h < 2; h++) to[16 * set + 8 * h] = __fmaf_rn(w, acc[n][set][2 * h + c], to[16 * set + 8 * h]);
-          }
+            for (int h = 0; h < 2; h++) to[16 * set + 8 * h] = __fmaf_rn(w, acc[set][2 * h + c], to[16 * set + 8 * h]);
         }
+      }
       __syncwarp();
 #pragma unroll
-      for (int n = 0; n < NT; n++)
+      for (int set = 0; set < 2; set++)
 #pragma unroll
-        for (int set = 0; set < 2; set++)
-#pragma unroll
-          for (int c = 0; c < 4; c++) acc[n][set][c] = 0.0f;
+        for (int c = 0; c < 4; c++) acc[set][c] = 0.0f;
     }
   }
   __syncthreads();
-  for (int i = tid; i < p.tokens * kMdRows; i += kMdThreads) {
-    const int t = i / kMdRows, r = i % kMdRows;
-    if (row0 + r >= p.hidden) continue;
-    float v = 0.0f;
+  const int values = p.tokens * kMdRows;
+  if (shares > 1) {  // this CTA's sums into its first warp's place, where the others read them
+    for (int i = tid; i < values; i += kMdThreads) {
+      float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kMdWarps; w++) v += sums[(w * p.tokens + t) * kMdOutPitch + r];
+      for (int w = 0; w < kMdWarps; w++) v += sums[(w * p.tokens + i / kMdRows) * kMdOutPitch + i % kMdRows];
+      sums[i / kMdRows * kMdOutPitch + i % kMdRows] = v;
+    }
+    md_cluster_sync();
+  }
+  const int copies = shares > 1 ? shares : kMdWarps;
+  for (int i = rank * kMdThreads + tid; i < values; i += shares * kMdThreads) {
+    const int t = i / kMdRows, r = i % kMdRows;
+    float v = 0.0f;
+    for (int c = 0; c < copies; c++) {
+      if (shares > 1) {
+        uint32_t from;
+        float u;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(md_smem(&sums[t * kMdOutPitch + r])), "r"(c));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(from) : "memory");
+        v += u;
+      } else {
+        v += sums[(c * p.tokens + t) * kMdOutPitch + r];
+      }
+    }
+    if (row0 + r >= p.hidden) continue;
     const int64_t at = (int64_t)t * p.hidden + row0 + r;
     if (LO) {
       ((float*)p.out)[at] = v;
@@ -575,6 +573,8 @@ __global__ void __launch_bounds__(kMdThreads, NT == 1 ? 2 : 1) decode_second_ker
     }
   }
   pdl_launch_dependents();
+  __syncwarp();
+  if (shares > 1) md_cluster_sync();  // no CTA leaves while others read its sums
 }
 
 // ---------------------------------------------------------------------------
@@ -584,32 +584,33 @@ static bool off(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0;
 
 static size_t decode_workspace(int64_t pairs, int64_t inner) {
   const int64_t kb2 = (inner + 127) / 128;
-  return (size_t)(pairs * kb2 * (2 * 2 * 128 + 8 * 4));
+  return (size_t)(pairs * kb2 * (2 * 2 * 128 + 4 * 4));
 }
 
-template <int FMT, int GROUPS, int NT, bool LO>
+template <int FMT, bool LO>
 static fp8q_status launch_decode(const MdParams& p, cudaStream_t s) {
-  constexpr size_t kRings = (size_t)kMdWarps * kMdRingBytes + 128, kSums = (size_t)kMdWarps * kMdOutPitch * sizeof(float);
+  const int slots = p.tokens * p.top_k;
+  const size_t rings = (size_t)kMdWarps * kMdRingBytes + 128, first_smem = rings + md_list_bytes(slots);
+  const size_t second_smem = first_smem + (size_t)kMdWarps * p.tokens * kMdOutPitch * sizeof(float);
+  constexpr size_t kMost = (size_t)kMdWarps * kMdRingBytes + 128 + md_list_bytes(kMdPairs) + (size_t)kMdWarps * kMdTokens * kMdOutPitch * sizeof(float);
   static PerDevice<bool> allowed[2];
-  cudaError_t e = allow_smem(allowed[0], decode_first_kernel<FMT, GROUPS, NT>, kRings);
-  if (e == cudaSuccess) e = allow_smem(allowed[1], decode_second_kernel<FMT, GROUPS, NT, LO>, kRings + (NT == 1 ? 8 : kMdTokens) * kSums);
+  cudaError_t e = allow_smem(allowed[0], decode_first_kernel<FMT>, rings + md_list_bytes(kMdPairs));
+  if (e == cudaSuccess) e = allow_smem(allowed[1], decode_second_kernel<FMT, LO>, kMost);
   if (e != cudaSuccess) return cuda_fail(e, "decode shared memory");
-  const int pairs = p.tokens * p.top_k;
-  int64_t units = (int64_t)(pairs < p.experts ? pairs : p.experts + pairs / (8 * NT)) * p.kb2 * (8 / GROUPS);  // at most
+  // at most this many units; two CTAs an SM have room
+  int64_t units = (int64_t)(slots < p.experts ? slots : p.experts + slots / kMdCols) * p.kb2 * (128 / kMdUnit);
   const int64_t fit = 2 * (int64_t)sm_count();
   if (units > fit) units = fit;
-  e = launch_kernel(decode_first_kernel<FMT, GROUPS, NT>, dim3((unsigned)units), dim3(kMdThreads), kRings, s, p);
+  e = launch_kernel(decode_first_kernel<FMT>, dim3((unsigned)units), dim3(kMdThreads), first_smem, s, p);
   if (e != cudaSuccess) return cuda_fail(e, "decode first kernel launch");
-  e = launch_kernel(decode_second_kernel<FMT, GROUPS, NT, LO>, dim3((unsigned)((p.hidden + kMdRows - 1) / kMdRows)), dim3(kMdThreads),
-                    kRings + p.tokens * kSums, s, p);
+  // CTAs of one column tile: as many as there is room for side by side
+  const int tiles = (p.hidden + kMdRows - 1) / kMdRows;
+  const int64_t room = second_smem > 112 * 1024 ? sm_count() : fit;
+  int shares = 1;
+  while (shares < 8 && tiles * 2 * shares <= room) shares *= 2;
+  e = launch_cluster(decode_second_kernel<FMT, LO>, dim3((unsigned)(tiles * shares)), dim3(kMdThreads), shares, second_smem, s, p, shares);
   if (e != cudaSuccess) return cuda_fail(e, "decode second kernel launch");
   return check_launch("decode kernel");
-}
-
-template <int FMT>
-static fp8q_status launch_decode_fmt(const MdParams& p, int out_dt, cudaStream_t s) {
-  if (p.tokens <= 8) return out_dt == FP8Q_OUT_FP32 ? launch_decode<FMT, 2, 1, true>(p, s) : launch_decode<FMT, 2, 1, false>(p, s);
-  return out_dt == FP8Q_OUT_FP32 ? launch_decode<FMT, 1, 2, true>(p, s) : launch_decode<FMT, 1, 2, false>(p, s);
 }
 
 }  // namespace fp8q
@@ -667,5 +668,7 @@ extern "C" fp8q_status fp8q_moe_decode(const void* x, int64_t tokens, int64_t hi
   p.a_lo = out_dt == FP8Q_OUT_FP32 ? p.a_hi + pairs * p.kb2 * 128 : nullptr;
   p.a_s = (float*)(p.a_hi + 2 * pairs * p.kb2 * 128);
   p.out = out;
-  return w_fmt == FP8Q_E4M3 ? launch_decode_fmt<kE4M3>(p, out_dt, (cudaStream_t)stream) : launch_decode_fmt<kE5M2>(p, out_dt, (cudaStream_t)stream);
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (out_dt == FP8Q_OUT_FP32) return w_fmt == FP8Q_E4M3 ? launch_decode<kE4M3, true>(p, s) : launch_decode<kE5M2, true>(p, s);
+  return w_fmt == FP8Q_E4M3 ? launch_decode<kE4M3, false>(p, s) : launch_decode<kE5M2, false>(p, s);
 }
