@@ -184,6 +184,9 @@ constexpr int kMdStages = 2;
 constexpr int kMdTileBytes = 32 * 128;
 constexpr int kMdRingBytes = kMdStages * kMdTileBytes;  // of one warp
 
+__device__ __forceinline__ void md_copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 // 16 bytes, or zeros: nothing is asked for where nothing is there.
 __device__ __forceinline__ void md_copy16(uint32_t to, const void* from, bool there) {
   asm volatile(
@@ -213,7 +216,7 @@ __device__ __forceinline__ void md_tile(uint32_t to, const uint8_t* lo, const ui
   hi += r * pitch + 16 * c;
   if (n_lo >= 16 && n_hi >= 16 && k >= 128) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) md_copy16((i & 1 ? odd : even) + i * 512, (i < 4 ? lo : hi) + (i & 3) * 4 * pitch, true);
+    for (int i = 0; i < 8; i++) md_copy16((i & 1 ? odd : even) + i * 512, (i < 4 ? lo : hi) + (i & 3) * 4 * pitch);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -235,6 +238,23 @@ __device__ __forceinline__ void md_chunk(uint32_t at, int s, uint32_t (&w)[4]) {
 // ---------------------------------------------------------------------------
 // first product and the activation
 // ---------------------------------------------------------------------------
+// This lane's BF16 values of a block of K of one token: 4 of each 16.
+__device__ __forceinline__ void md_token(const uint16_t* x, int left, bool there, uint32_t (&v)[16]) {
+  if (there && left >= 128) {
+#pragma unroll
+    for (int s = 0; s < 8; s++) {
+      const uint2 u = __ldg((const uint2*)(x + 16 * s));
+      v[2 * s] = u.x, v[2 * s + 1] = u.y;
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < 8; s++) {
+      const uint2 u = there && 16 * s < left ? __ldg((const uint2*)(x + 16 * s)) : make_uint2(0, 0);
+      v[2 * s] = u.x, v[2 * s + 1] = u.y;
+    }
+  }
+}
+
 // 32 inner values of an expert from inner0 on, for `count` of its tokens.
 struct MdUnit {
   int expert, count, first, inner0;
@@ -324,24 +344,22 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
     float acc[4][4] = {};
     const bool there = g < u.count;
     const uint16_t* xt = p.x + (int64_t)(there ? l.token[u.first + g] : 0) * p.hidden + 4 * q;
+    uint32_t x[16];
+    md_token(xt + warp * 128, p.hidden - warp * 128, there, x);
     for (int kb = warp; kb - warp < p.kb1; kb += kMdWarps) {
       // the tokens' part of this block of K
-      const int k = kb * 128;
       uint32_t b[16], m = 0;
 #pragma unroll
-      for (int s = 0; s < 8; s++) {
-        const uint2 x = there && k + 16 * s < p.hidden ? __ldg((const uint2*)(xt + k + 16 * s)) : make_uint2(0, 0);
-        b[2 * s] = x.x, b[2 * s + 1] = x.y;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; i++) m = absmax_bf16x2(m, b[i]);
+      for (int i = 0; i < 16; i++) m = absmax_bf16x2(m, x[i]);
       m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       const uint32_t power = md_exponent(max(m << 16, m & 0xFFFF0000u)), back = (254u - power) << 23;
       const float inv0 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q));
       const float inv1 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q + 4));
 #pragma unroll
-      for (int i = 0; i < 16; i++) b[i] = md_scaled(b[i], power << 7);
+      for (int i = 0; i < 16; i++) b[i] = md_scaled(x[i], power << 7);
+      const int k = (kb + kMdWarps) * 128;  // the next block's come while this one is multiplied
+      md_token(xt + k, p.hidden - k, there, x);
       float4 sc = make_float4(0, 0, 0, 0);
 #pragma unroll
       for (int tile = 0; tile < 2; tile++) {
@@ -416,13 +434,44 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
 // ---------------------------------------------------------------------------
 // second product and the weighted sum
 // ---------------------------------------------------------------------------
-// Asks for block `at` (job, block of K) of rows row0 .. row0 + 31.
-__device__ __forceinline__ void md_feed2(const MdParams& p, const MdLists& l, int at, int end, int row0, uint32_t to, uint32_t scale) {
-  if (at < end) {
-    const int job = at / p.kb2, kb = at - job * p.kb2, e = l.job[job] & 0xFFFF, rows = p.hidden - row0;
-    const uint8_t* from = p.w2 + ((int64_t)e * p.hidden + row0) * p.inner + kb * 128;
-    md_tile(to, from, from + 16 * (int64_t)p.inner, p.inner, rows, rows - 16, p.inner - kb * 128);
-    if ((threadIdx.x & 31) == 0) md_copy4(scale, p.s2 + ((int64_t)e * p.nb2 + (row0 >> 7)) * p.kb2 + kb);
+// A place in the list of all jobs' blocks of K.
+struct MdPlace {
+  int job, kb, count, first;
+  __device__ __forceinline__ void at_job(const MdLists& l) {
+    count = l.job[job] >> 16;
+    first = l.first[job];
+  }
+  // to the next block; whether that is another job's
+  __device__ __forceinline__ bool next(const MdParams& p) {
+    if (++kb < p.kb2) return false;
+    kb = 0;
+    job++;
+    return true;
+  }
+};
+
+// What a warp asks for next of rows row0 .. row0 + 31: `left` blocks from `at` on.
+struct MdFeed2 {
+  MdPlace at;
+  int left;
+  const uint8_t* from;
+  const float* scale;
+};
+
+__device__ __forceinline__ void md_feed2_job(const MdParams& p, const MdLists& l, int row0, MdFeed2& f) {
+  const int64_t e = l.job[f.at.job] & 0xFFFF;
+  f.from = p.w2 + (e * p.hidden + row0) * p.inner + f.at.kb * 128;
+  f.scale = p.s2 + (e * p.nb2 + (row0 >> 7)) * p.kb2 + f.at.kb;
+}
+
+__device__ __forceinline__ void md_feed2(const MdParams& p, const MdLists& l, int row0, MdFeed2& f, uint32_t to, uint32_t scale) {
+  if (f.left > 0) {
+    md_tile(to, f.from, f.from + 16 * (int64_t)p.inner, p.inner, p.hidden - row0, p.hidden - row0 - 16, p.inner - f.at.kb * 128);
+    if ((threadIdx.x & 31) == 0) md_copy4(scale, f.scale);
+    f.from += 128;
+    f.scale++;
+    if (f.at.next(p) && f.left > 1) md_feed2_job(p, l, row0, f);
+    f.left--;
   }
   md_commit();
 }
@@ -432,9 +481,8 @@ template <bool LO>
 struct MdInner {
   uint4 hi[4], lo[LO ? 4 : 1];
   float4 s[2];
-  __device__ __forceinline__ void load(const MdParams& p, const MdLists& l, int at) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, job = at / p.kb2, kb = at - job * p.kb2;
-    const int count = l.job[job] >> 16, first = l.first[job];
+  __device__ __forceinline__ void load(const MdParams& p, const MdPlace& at) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3, kb = at.kb, count = at.count, first = at.first;
     const int64_t from = (int64_t)(first + g) * p.kb2 * 128 + kb * 128 + 32 * q;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -469,8 +517,18 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
   const int begin = (int)(all * part / parts), end = (int)(all * (part + 1) / parts);
   const uint32_t ring = md_smem(rings) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0]);
   const uint32_t tile_at = ring + lane * 128 + ((lane & 7) << 4);
+  MdPlace at;  // of the inner values asked for last
+  at.job = begin / p.kb2;
+  at.kb = begin - at.job * p.kb2;
+  MdFeed2 f;
+  f.at = at;
+  f.left = end - begin;
+  if (begin < end) {
+    at.at_job(l);
+    md_feed2_job(p, l, row0, f);
+  }
 #pragma unroll
-  for (int i = 0; i < kMdStages; i++) md_feed2(p, l, begin + i, end, row0, ring + i * kMdTileBytes, sc_at + i * 4);
+  for (int i = 0; i < kMdStages; i++) md_feed2(p, l, row0, f, ring + i * kMdTileBytes, sc_at + i * 4);
   float* mine = sums + warp * p.tokens * kMdOutPitch;
   for (int i = lane; i < p.tokens * kMdOutPitch; i += 32) mine[i] = 0.0f;
   __syncwarp();
@@ -478,10 +536,15 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
   int stage = 0;
   float acc[2][4] = {};
   MdInner<LO> next;
-  if (begin < end) next.load(p, l, begin);
-  for (int at = begin; at < end; at++) {
+  if (begin < end) next.load(p, at);
+  for (int left = end - begin; left > 0; left--) {
     const MdInner<LO> a = next;
-    if (at + 1 < end) next.load(p, l, at + 1);
+    const int count = at.count, first = at.first;
+    const bool last = at.next(p);  // of its job
+    if (left > 1) {
+      if (last) at.at_job(l);
+      next.load(p, at);
+    }
     md_wait<kMdStages - 1>();
     __syncwarp();
     const float sc = scales[warp][stage];
@@ -513,10 +576,9 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
         for (int c = 0; c < 4; c++) acc[set][c] = __fmaf_rn(c & 1 ? f1 : f0, d[set][c], acc[set][c]);
     }
     __syncwarp();  // all lanes have their codes
-    md_feed2(p, l, at + kMdStages, end, row0, ring + stage * kMdTileBytes, sc_at + stage * 4);
+    md_feed2(p, l, row0, f, ring + stage * kMdTileBytes, sc_at + stage * 4);
     stage = stage + 1 == kMdStages ? 0 : stage + 1;
-    const int job = at / p.kb2, count = l.job[job] >> 16, first = l.first[job];
-    if (at - job * p.kb2 == p.kb2 - 1 || at + 1 == end) {  // on to another job: its tokens' sums leave the registers
+    if (last || left == 1) {  // on to another job: its tokens' sums leave the registers
 #pragma unroll
       for (int c = 0; c < 2; c++) {
         const int col = 2 * q + c;
