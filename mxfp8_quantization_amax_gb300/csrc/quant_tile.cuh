@@ -21,6 +21,9 @@ __device__ __forceinline__ float qt_scale(float amax, int pow2) {
   return pow2 ? __uint_as_float(__float_as_uint(s) & 0xFF800000u) : s;  // s is a positive normal float
 }
 
+// Every NaN becomes code 0x7F in both formats: what the conversion itself gives
+// for all payloads and signs.
+
 // The largest of two magnitudes (sign bit 0, NaN above all else), of three values' magnitudes.
 __device__ __forceinline__ float qt_max(float a, float b) {
   return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
@@ -34,10 +37,18 @@ __device__ __forceinline__ float qt_max8(const float (&v)[8]) {
   return qt_max(qt_max(qt_max(v[0], v[1], v[2]), v[3], v[4]), qt_max(v[5], v[6], v[7]));
 }
 
-// V consecutive values of type DT (kBF16, kFP32) as FP32, read once.  V = 8
-// takes 16-byte loads, V = 1 any place.
+// The halves of a BF16 pair as FP32: a mixed addition of -0, exact, which leaves
+// the integer pipe to the conversions and maxima.
+__device__ __forceinline__ void qt_halves(uint32_t w, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tadd.rn.f32.bf16 %0, a, %3;\n\tadd.rn.f32.bf16 %1, b, %3;\n\t}"
+      : "=f"(lo), "=f"(hi) : "r"(w), "f"(-0.0f));
+}
+
+// V consecutive values of type DT (kBF16, kFP32), read once.  V = 8 takes
+// 16-byte loads, V = 1 any place.
 template <int DT, int V>
 struct QtRaw {
+  static constexpr int kPair = V == 8 ? DT : kFP32;  // how pair() gives two values
   uint4 a, b;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     if constexpr (V == 8) {
@@ -52,10 +63,18 @@ struct QtRaw {
     }
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  // values 2 k and 2 k + 1: a BF16 pair in x, or FP32 bits in both
+  __device__ __forceinline__ uint2 pair(int k) const {
+    if constexpr (V == 1) return make_uint2(a.x, a.x);
+    if constexpr (DT == kBF16) return make_uint2(k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : a.w, 0);
+    return k == 0 ? make_uint2(a.x, a.y) : k == 1 ? make_uint2(a.z, a.w) : k == 2 ? make_uint2(b.x, b.y) : make_uint2(b.z, b.w);
+  }
   __device__ __forceinline__ void get(float (&v)[V]) const {
     if constexpr (V == 8 && DT == kBF16) {
-      v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
-      v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+      qt_halves(a.x, v[0], v[1]);
+      qt_halves(a.y, v[2], v[3]);
+      qt_halves(a.z, v[4], v[5]);
+      qt_halves(a.w, v[6], v[7]);
     } else if constexpr (V == 8) {
       v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
       v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
@@ -106,19 +125,45 @@ __device__ __forceinline__ uint32_t qt_codes4(float a, float b, float c, float d
   return cvt4<FMT>(a, b, c, d);
 }
 
-// One row group: 16 lanes (hl = lane & 15) of 8 values each.  All lanes of the
-// warp come here; `there`: the lane's values lie in the matrix (others are 0).
-template <int FMT>
-__device__ __forceinline__ void qt_group(const float (&v)[8], int pow2, uint8_t* q, float* scale_inv, bool there, int hl) {
-  float m = qt_max8(v);
+// The maxima of R row groups over the 16 lanes of a half-warp: at each step a
+// lane hands half of its groups over and keeps the other half, until 16 / R
+// lanes share one.  Lane hl ends with the maximum of group hl / (16 / R), and
+// one division serves a group.
+template <int R>
+__device__ __forceinline__ float qt_group_max(float (&m)[R], int hl) {
+  constexpr int kLanes = 16 / R;
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = qt_max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  const float s = qt_scale<FMT>(m, pow2);
-  uint2 c = make_uint2(qt_codes4<FMT>(v[0], v[1], v[2], v[3], s), qt_codes4<FMT>(v[4], v[5], v[6], v[7], s));
-  if (!(m <= 3.40282346638528859812e+38f)) c = make_uint2(canon_nan4<FMT>(c.x), canon_nan4<FMT>(c.y));
-  if (there) {
-    st_stream(q, c);
-    if (hl == 0) *scale_inv = __frcp_rn(s);
+  for (int n = R / 2; n >= 1; n >>= 1) {
+    const bool up = hl & (kLanes * n);
+#pragma unroll
+    for (int i = 0; i < n; i++) {
+      const float give = up ? m[i] : m[i + n], keep = up ? m[i + n] : m[i];
+      m[i] = qt_max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, kLanes * n));
+    }
+  }
+#pragma unroll
+  for (int n = kLanes / 2; n >= 1; n >>= 1) m[0] = qt_max(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], n));
+  return m[0];
+}
+
+// R row groups: 16 lanes (hl = lane & 15) of 8 values each.  All lanes of the
+// warp come here.  codes(i) is where group i's go and scale(i) its 1 / scale;
+// there(i): the lane's values of group i lie in the matrix (others are 0).
+template <int FMT, int R, class Codes, class Scale, class There>
+__device__ __forceinline__ void qt_groups(const float (&v)[R][8], int pow2, Codes codes, Scale scale, There there) {
+  constexpr int kLanes = 16 / R;
+  const int lane = threadIdx.x & 31, hl = lane & 15;
+  float m[R];
+#pragma unroll
+  for (int i = 0; i < R; i++) m[i] = qt_max8(v[i]);
+  const float s = qt_scale<FMT>(qt_group_max<R>(m, hl), pow2), inv = __frcp_rn(s);
+#pragma unroll
+  for (int i = 0; i < R; i++) {
+    const float si = __shfl_sync(0xFFFFFFFFu, s, (lane & 16) | kLanes * i), vi = __shfl_sync(0xFFFFFFFFu, inv, (lane & 16) | kLanes * i);
+    if (there(i)) {
+      *(uint2*)codes(i) = make_uint2(qt_codes4<FMT>(v[i][0], v[i][1], v[i][2], v[i][3], si), qt_codes4<FMT>(v[i][4], v[i][5], v[i][6], v[i][7], si));
+      if (hl == 0) *scale(i) = vi;
+    }
   }
 }
 
@@ -126,13 +171,16 @@ __device__ __forceinline__ void qt_group(const float (&v)[8], int pow2, uint8_t*
 // tiles
 // ---------------------------------------------------------------------------
 constexpr int kQtTile = 128;
-constexpr int kQtThreads = 256;
+constexpr int kQtRows = 4;                                // rows of a thread
+constexpr int kQtThreads = kQtTile * kQtTile / 8 / kQtRows;
 
 struct QtOut {
   int64_t rows, cols;  // of the quantized matrix
   int tiles_r, tiles_c;
   int pow2;
-  int apart;    // tile columns are taken in the order 0, half, 1, half + 1, ...: two halves of the columns share inputs
+  // the two halves of the columns have the same inputs (with cols / 2 a multiple of 128 one CTA makes both
+  // tiles of them; else tile columns are taken in the order 0, half, 1, half + 1, ...)
+  int halves;
   void* dense;  // the values in the source's type, or NULL
   uint8_t* q;   // row copy, or NULL
   float* s;
@@ -140,141 +188,204 @@ struct QtOut {
   float* s_t;
 };
 
-// A source gives the values of 8 columns of 8 rows; its type is that of the
-// dense output:
-//   static constexpr int kType;
-//   void tile(float (&v)[8][8], int64_t row, int64_t col, int64_t rows) const;   // rows from `rows` on are 0
-template <class Src, int FMT, bool ROW>
-__global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOut o) {
-  __shared__ float part[kQtThreads / 32][kQtTile];
-  __shared__ float scale[kQtTile];
-  __shared__ int odd[1];                               // some group holds Inf or NaN
-  __shared__ __align__(16) uint8_t stage[kQtTile * 128];  // codes of the transposed tile
-  const int tid = threadIdx.x, lane = tid & 31, hl = tid & 15, ty = tid >> 4;
-  pdl_wait();
-  const int64_t tr = blockIdx.x / o.tiles_c;
-  int tc = (int)(blockIdx.x - tr * o.tiles_c);
-  if (o.apart) tc = (tc & 1) ? (o.tiles_c + 1) / 2 + tc / 2 : tc / 2;
-  const int64_t r0 = tr * kQtTile + ty * 8, c0 = (int64_t)tc * kQtTile, c = c0 + hl * 8;
-  const bool col_ok = c < o.cols;
-  float v[8][8];
-  if (col_ok) {
-    src.tile(v, r0, c, o.rows);
-  } else {
+// 16 bytes into shared memory while other work goes on; a thread reads back
+// what it asked for itself, after qt_wait.
+__device__ __forceinline__ void qt_ask(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void qt_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void qt_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ uint4 qt_taken(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// A source gives 8 values of a row (rows come in multiples of 16, columns too)
+// from kInputs runs of 8 inputs of type kType, which is the dense output's too:
+//   bool needs(int input, int64_t col) const;
+//   const void* at(int input, int64_t row, int64_t col) const;
+//   void begin(int64_t row, int64_t col);                   // of kQtRows rows
+//   void values(const QtRaw<kType, 8> (&in)[kInputs], int i, int64_t col, float (&v)[8]) const;   // of row + i
+template <class Src>
+constexpr int kQtPieces = Src::kInputs * (Src::kType == kBF16 ? 1 : 2);  // of 16 bytes, for 8 values
+template <class Src>
+constexpr size_t kQtSmem = (size_t)kQtRows * kQtPieces<Src> * kQtThreads * 16;
+
+template <class Src>
+__device__ __forceinline__ void qt_ask_tile(const Src& src, int64_t row, int64_t col, bool there, uint32_t place) {
+  if (there) {
+    constexpr int kEach = kQtPieces<Src> / Src::kInputs;
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+    for (int n = 0; n < Src::kInputs; n++) {
+      if (!src.needs(n, col)) continue;
 #pragma unroll
-      for (int k = 0; k < 8; k++) v[i][k] = 0.0f;
-  }
-  if (tid == 0) odd[0] = 0;
-  // columns: 8 rows of a thread, 16 of a warp, 128 of the CTA
-  {
-    float m[8];
+      for (int i = 0; i < kQtRows; i++) {
+        const uint8_t* from = (const uint8_t*)src.at(n, row + i, col);
 #pragma unroll
-    for (int k = 0; k < 8; k++)
-      m[k] = qt_max(qt_max(qt_max(v[0][k], v[1][k], v[2][k]), v[3][k], v[4][k]), qt_max(v[5][k], v[6][k], v[7][k]));
-    const bool up = lane & 16;  // each half-warp keeps four of the columns
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const float give = up ? m[k] : m[k + 4], keep = up ? m[k + 4] : m[k];
-      m[k] = qt_max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 16));
-    }
-    *(float4*)&part[tid >> 5][hl * 8 + (up ? 4 : 0)] = make_float4(m[0], m[1], m[2], m[3]);
-  }
-  if (o.dense != nullptr && col_ok) {
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-      if (r0 + i < o.rows) qt_store<Src::kType, 8>(o.dense, (r0 + i) * o.cols + c, v[i]);
-  }
-  __syncthreads();
-  if (tid < kQtTile) {
-    float m = part[0][tid];
-#pragma unroll
-    for (int w = 1; w < kQtThreads / 32; w++) m = qt_max(m, part[w][tid]);
-    const float s = qt_scale<FMT>(m, o.pow2);
-    scale[tid] = s;
-    if (!(m <= 3.40282346638528859812e+38f)) odd[0] = 1;
-    if (c0 + tid < o.cols) o.s_t[(c0 + tid) * o.tiles_r + tr] = __frcp_rn(s);
-  }
-  if constexpr (ROW) {
-    // rows: at each step a lane hands half of its rows over and keeps the other
-    // half; lane hl ends with row (hl >> 1) & 7 of the thread's 8
-    float m[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) m[i] = qt_max8(v[i]);
-#pragma unroll
-    for (int n = 4; n >= 1; n >>= 1) {
-      const bool up = hl & (2 * n);
-#pragma unroll
-      for (int i = 0; i < n; i++) {
-        const float give = up ? m[i] : m[i + n], keep = up ? m[i + n] : m[i];
-        m[i] = qt_max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 2 * n));
+        for (int k = 0; k < kEach; k++) qt_ask(place + ((i * Src::kInputs + n) * kEach + k) * kQtThreads * 16, from + 16 * k);
       }
     }
-    m[0] = qt_max(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 1));
-    const float s = qt_scale<FMT>(m[0], o.pow2);
-    const int64_t mine = r0 + ((hl >> 1) & 7);
-    if (!(hl & 1) && mine < o.rows) o.s[mine * o.tiles_c + tc] = __frcp_rn(s);
-    const bool nan = __any_sync(0xFFFFFFFFu, !(m[0] <= 3.40282346638528859812e+38f));
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const float si = __shfl_sync(0xFFFFFFFFu, s, (lane & 16) | 2 * i);
-      uint2 u = make_uint2(qt_codes4<FMT>(v[i][0], v[i][1], v[i][2], v[i][3], si),
-                           qt_codes4<FMT>(v[i][4], v[i][5], v[i][6], v[i][7], si));
-      if (nan) u = make_uint2(canon_nan4<FMT>(u.x), canon_nan4<FMT>(u.y));
-      if (col_ok && r0 + i < o.rows) *(uint2*)(o.q + (r0 + i) * o.cols + c) = u;
-    }
   }
-  __syncthreads();
-  {
-    const float4 a = *(const float4*)&scale[hl * 8], b = *(const float4*)&scale[hl * 8 + 4];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      mul2(v[i][0], v[i][1], a.x, a.y);
-      mul2(v[i][2], v[i][3], a.z, a.w);
-      mul2(v[i][4], v[i][5], b.x, b.y);
-      mul2(v[i][6], v[i][7], b.z, b.w);
-    }
-    const bool nan = odd[0];
-#pragma unroll
-    for (int k = 0; k < 8; k++) {
-      uint2 u = make_uint2(cvt4<FMT>(v[0][k], v[1][k], v[2][k], v[3][k]), cvt4<FMT>(v[4][k], v[5][k], v[6][k], v[7][k]));
-      if (nan) u = make_uint2(canon_nan4<FMT>(u.x), canon_nan4<FMT>(u.y));
-      // 8-byte piece ty of the column's 128 rows, permuted by the thread's columns: 16 lanes hit 16 places
-      *(uint2*)(stage + (hl * 8 + k) * 128 + ((ty ^ hl) << 3)) = u;
-    }
-  }
-  __syncthreads();
-  const int64_t rt = tr * kQtTile;
+  qt_commit();
+}
+
+// Persistent: the inputs of a CTA's next tile come while it works on this one.
+template <class Src, int FMT, bool ROW>
+__global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOut o) {
+  extern __shared__ __align__(16) uint8_t inputs[];  // [rows of a thread][pieces][threads] of 16 bytes
+  __shared__ float scale[kQtTile];
+  __shared__ __align__(16) uint8_t stage[kQtTile * 128];  // codes of the transposed tile; the warps' column maxima before
+  float(*part)[kQtTile] = (float(*)[kQtTile])stage;
+  const int tid = threadIdx.x, lane = tid & 31, hl = tid & 15, ty = tid >> 4;
+  const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + tid * 16;
+  const bool pair = o.halves && o.cols % (2 * kQtTile) == 0;
+  const int items_c = pair ? o.tiles_c / 2 : o.tiles_c, items = o.tiles_r * items_c;
+  const int64_t cols = pair ? o.cols / 2 : o.cols;
   const bool wide = o.rows % 32 == 0 && ((uintptr_t)o.q_t & 31) == 0;
+  pdl_wait();
+  const auto place_of = [&](int item, int& tr, int& tc) {
+    tr = item / items_c;
+    tc = item - tr * items_c;
+    if (o.halves && !pair) tc = (tc & 1) ? (items_c + 1) / 2 + tc / 2 : tc / 2;
+  };
+  const auto ask = [&](int tr, int tc) {
+    const int64_t row = (int64_t)tr * kQtTile + ty * kQtRows, col = (int64_t)tc * kQtTile + hl * 8;
+    qt_ask_tile(src, row, col, col < cols && row < o.rows, place);
+  };
+  int tr, tc, half = 0, item = blockIdx.x;
+  place_of(item, tr, tc);
+  ask(tr, tc);
+  while (item < items) {
+    const int this_r = tr, this_c = tc + half * items_c;
+    const int64_t rt = (int64_t)tr * kQtTile, r0 = rt + ty * kQtRows, c0 = (int64_t)this_c * kQtTile, c = c0 + hl * 8;
+    const bool there = c < o.cols && r0 < o.rows;
+    float v[kQtRows][8];
+    if (there) src.begin(r0, c);
+    qt_wait();
+    if (there) {
 #pragma unroll
-  for (int n = 0; n < 2; n++) {  // 32 rows of a column: four threads a column
-    const int col = (tid >> 2) + 64 * n, at = tid & 3, flip = col >> 3;
-    const int64_t row = rt + 32 * at;
-    if (c0 + col >= o.cols || row >= o.rows) continue;
-    uint4 a = *(const uint4*)(stage + col * 128 + (((2 * at) ^ (flip >> 1)) << 4));
-    uint4 b = *(const uint4*)(stage + col * 128 + (((2 * at + 1) ^ (flip >> 1)) << 4));
-    if (flip & 1) {
-      a = make_uint4(a.z, a.w, a.x, a.y);
-      b = make_uint4(b.z, b.w, b.x, b.y);
-    }
-    uint8_t* to = o.q_t + (c0 + col) * o.rows + row;
-    if (wide) {
-      const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      st32B(to, d);
+      for (int i = 0; i < kQtRows; i++) {
+        QtRaw<Src::kType, 8> in[Src::kInputs];
+#pragma unroll
+        for (int n = 0; n < Src::kInputs; n++) {
+          if (!src.needs(n, c)) continue;
+          constexpr int kEach = kQtPieces<Src> / Src::kInputs;
+          in[n].a = qt_taken(place + (i * Src::kInputs + n) * kEach * kQtThreads * 16);
+          if (kEach == 2) in[n].b = qt_taken(place + ((i * Src::kInputs + n) * kEach + 1) * kQtThreads * 16);
+        }
+        src.values(in, i, c, v[i]);
+      }
     } else {
-      st_stream(to, a);
-      if (row + 16 < o.rows) st_stream(to + 16, b);
+#pragma unroll
+      for (int i = 0; i < kQtRows; i++)
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[i][k] = 0.0f;
     }
+    if (pair && half == 0) {
+      half = 1;
+    } else {
+      half = 0;
+      item += gridDim.x;
+      if (item < items) {
+        place_of(item, tr, tc);
+        ask(tr, tc);
+      }
+    }
+    // columns: the rows of a thread, twice as many of a warp, 128 of the CTA
+    {
+      float m[8];
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        if constexpr (kQtRows == 8)
+          m[k] = qt_max(qt_max(qt_max(v[0][k], v[1][k], v[2][k]), v[3][k], v[4][k]), qt_max(v[5][k], v[6][k], v[7][k]));
+        else
+          m[k] = qt_max(qt_max(v[0][k], v[1][k], v[2][k]), v[3][k], 0.0f);
+      }
+      const bool up = lane & 16;  // each half-warp keeps four of the columns
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const float give = up ? m[k] : m[k + 4], keep = up ? m[k + 4] : m[k];
+        m[k] = qt_max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, 16));
+      }
+      *(float4*)&part[tid >> 5][hl * 8 + (up ? 4 : 0)] = make_float4(m[0], m[1], m[2], m[3]);
+    }
+    if (o.dense != nullptr && there) {
+#pragma unroll
+      for (int i = 0; i < kQtRows; i++) qt_store<Src::kType, 8>(o.dense, (r0 + i) * o.cols + c, v[i]);
+    }
+    __syncthreads();
+    if (tid < kQtTile) {
+      float m = part[0][tid];
+#pragma unroll
+      for (int w = 1; w < kQtThreads / 32; w++) m = qt_max(m, part[w][tid]);
+      const float s = qt_scale<FMT>(m, o.pow2);
+      scale[tid] = s;
+      if (c0 + tid < o.cols) o.s_t[(c0 + tid) * o.tiles_r + this_r] = __frcp_rn(s);
+    }
+    if constexpr (ROW) {
+      uint8_t* to = o.q + r0 * o.cols + c;
+      float* scale_to = o.s + r0 * o.tiles_c + this_c;
+      qt_groups<FMT, kQtRows>(
+          v, o.pow2, [&](int i) { return to + i * o.cols; }, [&](int i) { return scale_to + (int64_t)i * o.tiles_c; }, [&](int) { return there; });
+    }
+    __syncthreads();
+    {
+      const float4 a = *(const float4*)&scale[hl * 8], b = *(const float4*)&scale[hl * 8 + 4];
+#pragma unroll
+      for (int i = 0; i < kQtRows; i++) {
+        mul2(v[i][0], v[i][1], a.x, a.y);
+        mul2(v[i][2], v[i][3], a.z, a.w);
+        mul2(v[i][4], v[i][5], b.x, b.y);
+        mul2(v[i][6], v[i][7], b.z, b.w);
+      }
+      // 8-byte pieces of the column's 128 rows, permuted by the thread's columns: a warp's lanes hit all banks
+      uint8_t* to = stage + hl * 8 * 128 + (((ty * kQtRows / 8) ^ hl) << 3) + ty * kQtRows % 8;
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const uint32_t lo = cvt4<FMT>(v[0][k], v[1][k], v[2][k], v[3][k]);
+        if constexpr (kQtRows == 8) *(uint2*)(to + k * 128) = make_uint2(lo, cvt4<FMT>(v[4][k], v[5][k], v[6][k], v[7][k]));
+        else *(uint32_t*)(to + k * 128) = lo;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < 512 / kQtThreads; n++) {  // 32 rows of a column: four threads a column
+      const int col = (tid + n * kQtThreads) >> 2, at = tid & 3, flip = col >> 3;
+      const int64_t row = rt + 32 * at;
+      if (c0 + col >= o.cols || row >= o.rows) continue;
+      uint4 a = *(const uint4*)(stage + col * 128 + (((2 * at) ^ (flip >> 1)) << 4));
+      uint4 b = *(const uint4*)(stage + col * 128 + (((2 * at + 1) ^ (flip >> 1)) << 4));
+      if (flip & 1) {
+        a = make_uint4(a.z, a.w, a.x, a.y);
+        b = make_uint4(b.z, b.w, b.x, b.y);
+      }
+      uint8_t* to = o.q_t + (c0 + col) * o.rows + row;
+      if (wide) {
+        const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        st32B(to, d);
+      } else {
+        st_stream(to, a);
+        if (row + 16 < o.rows) st_stream(to + 16, b);
+      }
+    }
+    __syncthreads();  // the codes have been read
   }
   pdl_launch_dependents();
 }
 
+template <class Src, int FMT, bool ROW>
+cudaError_t launch_quant_tiles_row(const Src& src, const QtOut& o, cudaStream_t s) {
+  static PerDevice<bool> allowed;
+  const cudaError_t e = allow_smem(allowed, quant_tile_kernel<Src, FMT, ROW>, kQtSmem<Src>);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)o.tiles_r * o.tiles_c / (o.halves && o.cols % (2 * kQtTile) == 0 ? 2 : 1), fit = (kQtSmem<Src> > 96 * 1024 ? 1 : 2) * (int64_t)sm_count();
+  return launch_kernel(quant_tile_kernel<Src, FMT, ROW>, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kQtThreads), kQtSmem<Src>, s, src, o);
+}
+
 template <class Src, int FMT>
 cudaError_t launch_quant_tiles(const Src& src, const QtOut& o, cudaStream_t s) {
-  const dim3 grid((unsigned)((int64_t)o.tiles_r * o.tiles_c));
-  return o.q ? launch_kernel(quant_tile_kernel<Src, FMT, true>, grid, dim3(kQtThreads), 0, s, src, o)
-             : launch_kernel(quant_tile_kernel<Src, FMT, false>, grid, dim3(kQtThreads), 0, s, src, o);
+  return o.q ? launch_quant_tiles_row<Src, FMT, true>(src, o, s) : launch_quant_tiles_row<Src, FMT, false>(src, o, s);
 }
 
 // Checks of the copies' arguments, for cols columns.

@@ -130,22 +130,29 @@ __global__ void __launch_bounds__(T) rmsnorm_kernel(RmsNorm p) {
 #pragma unroll
     for (int n = 0; n < N; n++) {
       const int64_t c = (int64_t)(n * p.lanes + t) * V;
-      const bool there = row_ok && c < p.cols;
-      if (there) {
-        float w[V];
-        rn_weight<V>(p.weight, p.weight_dt, c, w);
+      if (!row_ok || c >= p.cols) continue;
+      float w[V];
+      rn_weight<V>(p.weight, p.weight_dt, c, w);
 #pragma unroll
-        for (int k = 0; k < V; k++) v[n][k] = __fmul_rn(__fmul_rn(v[n][k], rstd), w[k]);
+      for (int k = 0; k < V; k++) v[n][k] = __fmul_rn(__fmul_rn(v[n][k], rstd), w[k]);
+    }
+    if constexpr (V == 8) {
+      if (p.q != nullptr) {  // 16 threads hold a group of 128 columns, N of them
+        uint8_t* q = p.q + r * p.cols + 8 * t;
+        float* s = p.s + r * p.tiles_c + t / 16;
+        const auto codes = [&](int n) { return q + (int64_t)n * p.lanes * 8; };
+        const auto scale = [&](int n) { return s + n * p.lanes / 16; };
+        const auto there = [&](int n) { return row_ok && (n * p.lanes + t) * 8 < p.cols; };
+        if (p.fmt == kE4M3) qt_groups<kE4M3, N>(v, p.pow2, codes, scale, there);
+        else qt_groups<kE5M2, N>(v, p.pow2, codes, scale, there);
       }
-      if constexpr (V == 8) {
-        if (p.q != nullptr) {  // 16 threads hold a group of 128 columns
-          uint8_t* q = p.q + r * p.cols + c;
-          float* s = p.s + r * p.tiles_c + c / 128;
-          if (p.fmt == kE4M3) qt_group<kE4M3>(v[n], p.pow2, q, s, there, threadIdx.x & 15);
-          else qt_group<kE5M2>(v[n], p.pow2, q, s, there, threadIdx.x & 15);
-        }
+    }
+    if (p.y != nullptr) {
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        const int64_t c = (int64_t)(n * p.lanes + t) * V;
+        if (row_ok && c < p.cols) qt_store<DT, V>(p.y, r * p.cols + c, v[n]);
       }
-      if (p.y != nullptr && there) qt_store<DT, V>(p.y, r * p.cols + c, v[n]);
     }
   }
   pdl_launch_dependents();
@@ -160,26 +167,23 @@ struct RmsNormTile {
   int weight_dt;
   const float* rstd;
   int64_t cols;
-  __device__ __forceinline__ void tile(float (&v)[8][8], int64_t row, int64_t col, int64_t rows) const {
-    QtRaw<DT, 8> raw[8];
-    float s[8], w[8];
+  float s[kQtRows], w[8];
+  static constexpr int kInputs = 1;
+  __device__ __forceinline__ bool needs(int, int64_t) const { return true; }
+  __device__ __forceinline__ const void* at(int, int64_t row, int64_t col) const {
+    return (const uint8_t*)h + (row * cols + col) * (DT == kBF16 ? 2 : 4);
+  }
+  __device__ __forceinline__ void begin(int64_t row, int64_t col) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      raw[i].zero();
-      s[i] = 0.0f;
-      if (row + i < rows) {
-        raw[i].load(h, (row + i) * cols + col);
-        s[i] = __ldg(rstd + row + i);
-      }
-    }
+    for (int i = 0; i < kQtRows; i++) s[i] = __ldg(rstd + row + i);
     rn_weight<8>(weight, weight_dt, col, w);
+  }
+  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[1], int i, int64_t, float (&v)[8]) const {
+    in[0].get(v);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      raw[i].get(v[i]);
-      if (row + i < rows) {
-#pragma unroll
-        for (int k = 0; k < 8; k++) v[i][k] = __fmul_rn(__fmul_rn(v[i][k], s[i]), w[k]);
-      }
+    for (int k = 0; k < 8; k += 2) {
+      mul2(v[k], v[k + 1], s[i], s[i]);
+      mul2(v[k], v[k + 1], w[k], w[k + 1]);
     }
   }
 };
@@ -463,10 +467,10 @@ extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* resid
     const int ht = residual ? residual_dt : dt;
     const void* from = residual ? h : x;
     if (ht == FP8Q_IN_BF16) {
-      const RmsNormTile<kBF16> src{from, weight, weight_dt, rstd, cols};
+      const RmsNormTile<kBF16> src{from, weight, weight_dt, rstd, cols, {}, {}};
       e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kBF16>, kE4M3>(src, o, s) : launch_quant_tiles<RmsNormTile<kBF16>, kE5M2>(src, o, s);
     } else {
-      const RmsNormTile<kFP32> src{from, weight, weight_dt, rstd, cols};
+      const RmsNormTile<kFP32> src{from, weight, weight_dt, rstd, cols, {}, {}};
       e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kFP32>, kE4M3>(src, o, s) : launch_quant_tiles<RmsNormTile<kFP32>, kE5M2>(src, o, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "rmsnorm transposed copy launch");

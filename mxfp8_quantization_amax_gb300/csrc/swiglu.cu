@@ -7,15 +7,14 @@
 // With e = exp(-gate), s = 1 / (1 + e) and 1 - s = e s: no difference of near
 // values.  exp(-g) = 2^(-g log2 e), the product as a sum of two FP32 numbers:
 // the larger goes to the exponential instruction, the smaller, l, comes in as
-// 1 + l ln 2.  Where a gate of a thread's eight is beyond +-87 (or is not
-// finite), e = exp(-|gate|) and r = 1 / (1 + e) give s and 1 - s as r and e r, or
-// the other way round, for all eight.  FP32 throughout; codes are made from the
-// FP32 values, a dense output is rounded once.
+// 1 + l ln 2.  In the exponential a gate counts as one within [-88.5, 127]; s is
+// 0 where it would be below 2^-126 (gates below -87.3).  FP32 throughout, the
+// products of two BF16 inputs exact; codes are made from the FP32 values, a
+// dense output is rounded once.
 #include "quant_tile.cuh"
 
 namespace fp8q {
 
-// Two values of s and e = (1 - s) / s at a time: packed products and sums.
 __device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float c, float d) {  // a, b = a x + c, b y + d
   unsigned long long u, v, w;
   asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(a), "f"(b));
@@ -25,77 +24,95 @@ __device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(u));
 }
 
-// s and 1 - s (without it, t holds e) of V gates.
-template <bool T, int V>
-__device__ __forceinline__ void sg_sigmoid(const float (&g)[V], float (&s)[V], float (&t)[V]) {
-  constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;  // log2 e = kLog2e + kRest
-  float m;
-  if constexpr (V == 8) m = qt_max8(g);
-  else m = fabsf(g[0]);
-  if (m <= 87.0f) {
-#pragma unroll
-    for (int k = 0; k < V; k += 2) {
-      constexpr int n = V > 1;
-      float t0 = g[k], t1 = g[k + n], l0 = t0, l1 = t1, e0, e1;
-      mul2(t0, t1, -kLog2e, -kLog2e);
-      fma2(l0, l1, kLog2e, kLog2e, t0, t1);  // what the rounding of t took, exactly
-      float r0 = g[k], r1 = g[k + n];
-      fma2(r0, r1, kRest, kRest, l0, l1);
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
-      mul2(r0, r1, -kLn2, -kLn2);
-      fma2(r0, r1, e0, e1, e0, e1);
-      float d0 = r0, d1 = r1;
-      fma2(d0, d1, 1.0f, 1.0f, 1.0f, 1.0f);
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d0) : "f"(d0));  // of 1 to 2^126: within one unit
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d1) : "f"(d1));
-      if (T) mul2(r0, r1, d0, d1);
-      s[k] = d0, s[k + n] = d1;
-      t[k] = r0, t[k + n] = r1;
-    }
+// Pairs of inputs as QtRaw::pair gives them: their values, those within [-88.5, 127], products.
+template <int P>
+__device__ __forceinline__ void sg_values(uint2 w, float& x0, float& x1) {
+  if constexpr (P == kBF16) qt_halves(w.x, x0, x1);
+  else x0 = __uint_as_float(w.x), x1 = __uint_as_float(w.y);
+}
+template <int P>
+__device__ __forceinline__ void sg_within(uint2 w, float& x0, float& x1) {
+  if constexpr (P == kBF16) {
+    uint32_t c;
+    asm("{\n\t.reg .b32 t;\n\tmin.bf16x2 t, %1, %2;\n\tmax.bf16x2 %0, t, %3;\n\t}" : "=r"(c) : "r"(w.x), "r"(0x42FE42FEu), "r"(0xC2B1C2B1u));
+    qt_halves(c, x0, x1);
   } else {
-#pragma unroll
-    for (int k = 0; k < V; k++) {
-      const float e = expf(-fabsf(g[k])), r = __frcp_rn(1.0f + e), er = __fmul_rn(e, r);
-      s[k] = g[k] >= 0.0f ? r : er;
-      t[k] = g[k] >= 0.0f ? er : r;
-    }
+    x0 = fmaxf(fminf(__uint_as_float(w.x), 127.0f), -88.5f);
+    x1 = fmaxf(fminf(__uint_as_float(w.y), 127.0f), -88.5f);
+  }
+}
+template <int P>
+__device__ __forceinline__ void sg_product(uint2 a, uint2 b, float& x0, float& x1) {
+  if constexpr (P == kBF16) {
+    asm("{\n\t.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %2;\n\tmov.b32 {c, d}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, a, c, %4;\n\tfma.rn.f32.bf16 %1, b, d, %4;\n\t}"
+        : "=f"(x0), "=f"(x1) : "r"(a.x), "r"(b.x), "f"(-0.0f));
+  } else {
+    x0 = __uint_as_float(a.x), x1 = __uint_as_float(a.y);
+    mul2(x0, x1, __uint_as_float(b.x), __uint_as_float(b.y));
   }
 }
 
-template <int V>
-__device__ __forceinline__ void sg_forward(const float (&g)[V], const float (&u)[V], float (&a)[V]) {
-  float s[V], t[V];
-  sg_sigmoid<false>(g, s, t);
-#pragma unroll
-  for (int k = 0; k < V; k += 2) {
-    constexpr int n = V > 1;
-    float a0 = g[k], a1 = g[k + n];
-    mul2(a0, a1, s[k], s[k + n]);
-    mul2(a0, a1, u[k], u[k + n]);
-    a[k + n] = a1;
-    a[k] = a0;
-  }
+// s and e of two gates.
+template <int P>
+__device__ __forceinline__ void sg_sigmoid(uint2 gate, float& s0, float& s1, float& e0, float& e1) {
+  constexpr float kLog2e = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;  // log2 e = kLog2e + kRest
+  float g0, g1, x0, x1;
+  sg_within<P>(gate, g0, g1);
+  float t0 = g0, t1 = g1, l0 = g0, l1 = g1;
+  mul2(t0, t1, -kLog2e, -kLog2e);
+  fma2(l0, l1, kLog2e, kLog2e, t0, t1);  // what the rounding of t took, exactly
+  fma2(g0, g1, kRest, kRest, l0, l1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x0) : "f"(t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x1) : "f"(t1));
+  mul2(g0, g1, -kLn2, -kLn2);
+  fma2(g0, g1, x0, x1, x0, x1);
+  e0 = g0, e1 = g1;
+  fma2(g0, g1, 1.0f, 1.0f, 1.0f, 1.0f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s0) : "f"(g0));  // within one unit
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(g1));
+}
+
+template <int P>
+__device__ __forceinline__ void sg_forward(uint2 gate, uint2 up, float& a0, float& a1) {
+  float s0, s1, e0, e1;
+  sg_sigmoid<P>(gate, s0, s1, e0, e1);
+  sg_product<P>(gate, up, a0, a1);
+  mul2(a0, a1, s0, s1);
 }
 
 // One half of d_h: of the gate (UP false) or of the up branch.
-template <bool UP, int V>
-__device__ __forceinline__ void sg_backward(const float (&g)[V], const float (&u)[V], const float (&d)[V], float (&o)[V]) {
-  float s[V], t[V];
-  sg_sigmoid<!UP>(g, s, t);
-#pragma unroll
-  for (int k = 0; k < V; k += 2) {
-    constexpr int n = V > 1;
-    float o0 = g[k], o1 = g[k + n];
-    if (!UP) {
-      fma2(o0, o1, t[k], t[k + n], 1.0f, 1.0f);
-      mul2(o0, o1, u[k], u[k + n]);
-    }
-    mul2(o0, o1, s[k], s[k + n]);
-    mul2(o0, o1, d[k], d[k + n]);
-    o[k + n] = o1;
-    o[k] = o0;
+template <bool UP, int P>
+__device__ __forceinline__ void sg_backward(uint2 gate, uint2 up, uint2 d, float& o0, float& o1) {
+  float s0, s1, e0, e1;
+  sg_sigmoid<P>(gate, s0, s1, e0, e1);
+  if constexpr (UP) {
+    sg_product<P>(d, gate, o0, o1);
+  } else {
+    float g0, g1;
+    sg_values<P>(gate, g0, g1);
+    mul2(e0, e1, s0, s1);
+    fma2(g0, g1, e0, e1, 1.0f, 1.0f);
+    sg_product<P>(d, up, o0, o1);
+    mul2(o0, o1, g0, g1);
   }
+  mul2(o0, o1, s0, s1);
+}
+
+// Both.
+template <int P>
+__device__ __forceinline__ void sg_both(uint2 gate, uint2 up, uint2 d, float& g0, float& g1, float& u0, float& u1) {
+  float s0, s1, e0, e1, x0, x1, y0, y1;
+  sg_sigmoid<P>(gate, s0, s1, e0, e1);
+  sg_product<P>(d, gate, y0, y1);
+  mul2(y0, y1, s0, s1);
+  sg_values<P>(gate, x0, x1);
+  mul2(e0, e1, s0, s1);
+  fma2(x0, x1, e0, e1, 1.0f, 1.0f);
+  sg_product<P>(d, up, e0, e1);
+  mul2(e0, e1, x0, x1);
+  mul2(e0, e1, s0, s1);
+  g0 = e0, g1 = e1, u0 = y0, u1 = y1;
 }
 
 template <int DT>
@@ -106,31 +123,26 @@ struct SwigluForward {
   template <int V>
   __device__ __forceinline__ void row(float (&a)[V], int64_t r, int64_t c) const {
     QtRaw<DT, V> g, u;
-    float gv[V], uv[V];
     g.load(h, r * 2 * inner + c);
     u.load(h, r * 2 * inner + inner + c);
-    g.get(gv);
-    u.get(uv);
-    sg_forward<V>(gv, uv, a);
+    values<V>(g, u, a);
   }
-  __device__ __forceinline__ void tile(float (&v)[8][8], int64_t row, int64_t col, int64_t rows) const {
-    QtRaw<DT, 8> g[8], u[8];
+  static constexpr int kInputs = 2;
+  static constexpr bool kHalves = false;
+  __device__ __forceinline__ bool needs(int, int64_t) const { return true; }
+  __device__ __forceinline__ const void* at(int n, int64_t row, int64_t col) const {
+    return (const uint8_t*)h + (row * 2 * inner + n * inner + col) * (DT == kBF16 ? 2 : 4);
+  }
+  __device__ __forceinline__ void begin(int64_t, int64_t) {}
+  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[2], int, int64_t, float (&v)[8]) const { values<8>(in[0], in[1], v); }
+  template <int V>
+  static __device__ __forceinline__ void values(const QtRaw<DT, V>& g, const QtRaw<DT, V>& u, float (&a)[V]) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      if (row + i < rows) {
-        g[i].load(h, (row + i) * 2 * inner + col);
-        u[i].load(h, (row + i) * 2 * inner + inner + col);
-      } else {
-        g[i].zero();
-        u[i].zero();
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      float gv[8], uv[8];
-      g[i].get(gv);
-      u[i].get(uv);
-      sg_forward<8>(gv, uv, v[i]);
+    for (int k = 0; k < (V + 1) / 2; k++) {
+      float a0, a1;
+      sg_forward<QtRaw<DT, V>::kPair>(g.pair(k), u.pair(k), a0, a1);
+      a[2 * k] = a0;
+      if constexpr (V > 1) a[2 * k + 1] = a1;
     }
   }
 };
@@ -147,43 +159,41 @@ struct SwigluBackward {
     const bool up = c >= inner;
     const int64_t j = up ? c - inner : c;
     QtRaw<DT, V> g, u, d;
-    float gv[V], uv[V], dv[V];
     g.load(h, r * 2 * inner + j);
-    u.load(h, r * 2 * inner + inner + j);
+    if (!up) u.load(h, r * 2 * inner + inner + j);
     d.load(d_a, r * inner + j);
-    g.get(gv);
-    u.get(uv);
-    d.get(dv);
-    if (up) sg_backward<true>(gv, uv, dv, o);
-    else sg_backward<false>(gv, uv, dv, o);
+    if (up) values<true, V>(g, g, d, o);
+    else values<false, V>(g, u, d, o);
   }
-  __device__ __forceinline__ void tile(float (&v)[8][8], int64_t row, int64_t col, int64_t rows) const {
-    const bool up = col >= inner;
-    const int64_t j = up ? col - inner : col;
+  static constexpr int kInputs = 3;
+  static constexpr bool kHalves = true;
+  __device__ __forceinline__ bool needs(int n, int64_t col) const { return n != 1 || col < inner; }
+  __device__ __forceinline__ const void* at(int n, int64_t row, int64_t col) const {
+    const int64_t j = col >= inner ? col - inner : col, size = DT == kBF16 ? 2 : 4;
+    return n == 2 ? (const uint8_t*)d_a + (row * inner + j) * size : (const uint8_t*)h + (row * 2 * inner + n * inner + j) * size;
+  }
+  __device__ __forceinline__ void begin(int64_t, int64_t) {}
+  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[3], int, int64_t col, float (&v)[8]) const {
+    if (col >= inner) values<true, 8>(in[0], in[0], in[2], v);
+    else values<false, 8>(in[0], in[1], in[2], v);
+  }
+  // both halves of a row's columns c, c + 1, ... of 8
+  __device__ __forceinline__ void both(float (&o_g)[8], float (&o_u)[8], int64_t r, int64_t c) const {
+    QtRaw<DT, 8> g, u, d;
+    g.load(h, r * 2 * inner + c);
+    u.load(h, r * 2 * inner + inner + c);
+    d.load(d_a, r * inner + c);
 #pragma unroll
-    for (int n = 0; n < 8; n += 4) {  // four rows on their way at a time
-      QtRaw<DT, 8> g[4], u[4], d[4];
+    for (int k = 0; k < 4; k++) sg_both<DT>(g.pair(k), u.pair(k), d.pair(k), o_g[2 * k], o_g[2 * k + 1], o_u[2 * k], o_u[2 * k + 1]);
+  }
+  template <bool UP, int V>
+  static __device__ __forceinline__ void values(const QtRaw<DT, V>& g, const QtRaw<DT, V>& u, const QtRaw<DT, V>& d, float (&o)[V]) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int64_t r = row + n + i;
-        g[i].zero();
-        u[i].zero();
-        d[i].zero();
-        if (r < rows) {
-          g[i].load(h, r * 2 * inner + j);
-          if (!up) u[i].load(h, r * 2 * inner + inner + j);
-          d[i].load(d_a, r * inner + j);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        float gv[8], uv[8], dv[8];
-        g[i].get(gv);
-        u[i].get(uv);
-        d[i].get(dv);
-        if (up) sg_backward<true>(gv, uv, dv, v[n + i]);
-        else sg_backward<false>(gv, uv, dv, v[n + i]);
-      }
+    for (int k = 0; k < (V + 1) / 2; k++) {
+      float o0, o1;
+      sg_backward<UP, QtRaw<DT, V>::kPair>(g.pair(k), u.pair(k), d.pair(k), o0, o1);
+      o[2 * k] = o0;
+      if constexpr (V > 1) o[2 * k + 1] = o1;
     }
   }
 };
@@ -192,41 +202,68 @@ struct SwigluBackward {
 // group of 128 columns (without a copy: any V * 16 columns).
 constexpr int kSgThreads = 256;
 
-template <class Src, int FMT, int V>
-__global__ void __launch_bounds__(kSgThreads) swiglu_rows_kernel(Src src, QtOut o, int64_t groups, int per_row) {
+// U rows of one group of columns a half-warp, all on their way at a time; PAIR:
+// U / 2 rows of a group and of its partner in the other half.
+template <class Src, int FMT, int V, int U, bool PAIR>
+__global__ void __launch_bounds__(kSgThreads) swiglu_rows_kernel(Src src, QtOut o, uint32_t per_row, uint32_t items) {
+  constexpr int kRows = PAIR ? U / 2 : U;
   const int hl = threadIdx.x & 15;
+  const uint32_t item = blockIdx.x * (kSgThreads / 16) + threadIdx.x / 16, block = item / per_row, group = item - block * per_row;
+  const int64_t c = (int64_t)(group * 16 + hl) * V, r0 = (int64_t)block * kRows;
   pdl_wait();
-  for (int64_t g0 = (int64_t)blockIdx.x * (kSgThreads / 16); g0 < groups; g0 += (int64_t)gridDim.x * (kSgThreads / 16)) {
-    const int64_t g = g0 + threadIdx.x / 16;
-    const int64_t r = g / per_row;
-    const int64_t c = ((g - r * per_row) * 16 + hl) * V;
-    const bool there = g < groups && c < o.cols;
-    float v[V];
+  float v[U][V];
 #pragma unroll
-    for (int k = 0; k < V; k++) v[k] = 0.0f;
-    if (there) src.template row<V>(v, r, c);
-    if constexpr (V == 8) {
-      if (o.q != nullptr) qt_group<FMT>(v, o.pow2, o.q + r * o.cols + c, o.s + g, there, hl);
+  for (int i = 0; i < U; i++)
+#pragma unroll
+    for (int k = 0; k < V; k++) v[i][k] = 0.0f;
+  const auto there = [&](int i) { return item < items && c < (PAIR ? o.cols / 2 : o.cols) && r0 + i % kRows < o.rows; };
+  const auto col = [&](int i) { return c + (i >= kRows ? o.cols / 2 : 0); };
+#pragma unroll
+  for (int i = 0; i < kRows; i++) {
+    if (!there(i)) continue;
+    if constexpr (PAIR) src.both(v[i], v[kRows + i], r0 + i, c);
+    else src.template row<V>(v[i], r0 + i, c);
+  }
+  if constexpr (V == 8) {
+    if (o.q != nullptr) {
+      uint8_t* q = o.q + r0 * o.cols;
+      float* s = o.s + r0 * o.tiles_c;
+      qt_groups<FMT, U>(
+          v, o.pow2, [&](int i) { return q + i % kRows * o.cols + col(i); },
+          [&](int i) { return s + i % kRows * o.tiles_c + col(i) / 128; }, there);
     }
-    if (o.dense != nullptr && there) qt_store<Src::kType, V>(o.dense, r * o.cols + c, v);
+  }
+  if (o.dense != nullptr) {
+#pragma unroll
+    for (int i = 0; i < U; i++)
+      if (there(i)) qt_store<Src::kType, V>(o.dense, (r0 + i % kRows) * o.cols + col(i), v[i]);
   }
   pdl_launch_dependents();
 }
 
+template <class Src, int FMT, int V, int U, bool PAIR>
+static fp8q_status launch_swiglu_rows(const Src& src, const QtOut& o, cudaStream_t s) {
+  const int64_t cols = PAIR ? o.cols / 2 : o.cols, rows = PAIR ? U / 2 : U, per_row = (cols + V * 16 - 1) / (V * 16);
+  const int64_t items = (o.rows + rows - 1) / rows * per_row;
+  if (items > UINT32_MAX - kSgThreads) return fail(FP8Q_ERR_UNSUPPORTED, "rows * inner too large");
+  const dim3 grid((unsigned)((items + kSgThreads / 16 - 1) / (kSgThreads / 16)));
+  const cudaError_t e = launch_kernel(swiglu_rows_kernel<Src, FMT, V, U, PAIR>, grid, dim3(kSgThreads), 0, s, src, o, (uint32_t)per_row, (uint32_t)items);
+  return e == cudaSuccess ? check_launch("swiglu kernel") : cuda_fail(e, "swiglu kernel launch");
+}
+
 template <class Src, int FMT>
 static fp8q_status launch_swiglu(const Src& src, const QtOut& o, bool vec, cudaStream_t s) {
-  cudaError_t e;
   if (o.q_t) {
-    e = launch_quant_tiles<Src, FMT>(src, o, s);
-  } else {
-    const int per_row = (int)((o.cols + (vec ? 128 : 16) - 1) / (vec ? 128 : 16));
-    const int64_t groups = o.rows * per_row, ctas = (groups + kSgThreads / 16 - 1) / (kSgThreads / 16);
-    const dim3 grid((unsigned)(ctas < INT32_MAX ? ctas : INT32_MAX));
-    e = vec ? launch_kernel(swiglu_rows_kernel<Src, FMT, 8>, grid, dim3(kSgThreads), 0, s, src, o, groups, per_row)
-            : launch_kernel(swiglu_rows_kernel<Src, FMT, 1>, grid, dim3(kSgThreads), 0, s, src, o, groups, per_row);
+    const cudaError_t e = launch_quant_tiles<Src, FMT>(src, o, s);
+    return e == cudaSuccess ? check_launch("swiglu kernel") : cuda_fail(e, "swiglu kernel launch");
   }
-  if (e != cudaSuccess) return cuda_fail(e, "swiglu kernel launch");
-  return check_launch("swiglu kernel");
+  // four row groups a half-warp where that leaves every SM its share of CTAs, else one (or a pair)
+  const bool four = o.rows * ((o.cols + 127) / 128) >= (int64_t)64 * 16 * sm_count();
+  if (!vec) return four ? launch_swiglu_rows<Src, FMT, 1, 4, false>(src, o, s) : launch_swiglu_rows<Src, FMT, 1, 1, false>(src, o, s);
+  if constexpr (Src::kHalves) {
+    if (o.cols % 256 == 0) return four ? launch_swiglu_rows<Src, FMT, 8, 4, true>(src, o, s) : launch_swiglu_rows<Src, FMT, 8, 2, true>(src, o, s);
+  }
+  return four ? launch_swiglu_rows<Src, FMT, 8, 4, false>(src, o, s) : launch_swiglu_rows<Src, FMT, 8, 1, false>(src, o, s);
 }
 
 template <class Src>
@@ -262,7 +299,7 @@ static fp8q_status swiglu(const void* h, const void* d_a, bool backward, int32_t
   o.tiles_r = (int)tiles_r;
   o.tiles_c = (int)tiles_c;
   o.pow2 = pow2 ? 1 : 0;
-  o.apart = backward;
+  o.halves = backward;
   o.dense = dense;
   if (dir & MXFP8_ROW) o.q = q, o.s = s;
   if (dir & MXFP8_COL) o.q_t = q_t, o.s_t = s_t;

@@ -243,7 +243,8 @@ def test_norm_gradient_against_differences():
 # ---------------------------------------------------------------------------
 # Of exp(-gate): 2 units of the exponential (4 u) and two roundings; 1 + e and its reciprocal (one unit): 3 u;
 # three products.  The gradient's 1 - s takes two roundings more, and 1 + gate (1 - s) another.
-REL, REL_GRAD = 16 * U, 24 * U
+# A sigmoid below 2^-126 counts as 0: a value is off by its other factors times 2^-126, TINY, at most.
+REL, REL_GRAD, TINY = 16 * U, 24 * U, 2.0 ** -126
 
 
 def gate64(h):
@@ -267,7 +268,7 @@ def test_gate(dt, rows, inner, direction):
         a = gate64(h)
         assert (r["a"] is not None) == want_a and (r["q"] is not None) == bool(direction & 1) and (r["q_t"] is not None) == bool(direction & 2)
         if want_a:
-            near(r["a"], a, a.abs() * (HALF[dt] * (1 + 2.0 ** -7) + REL) + 1e-38)
+            near(r["a"], a, a.abs() * (HALF[dt] * (1 + 2.0 ** -7) + REL) + 1e-38 + TINY * (h[:, :inner].double() * h[:, inner:].double()).abs())
         if direction & 1:
             check_copy(r["q"], r["scale_inv"], a, fmt, REL, pow2)
         if direction & 2:
@@ -279,7 +280,9 @@ def gate_grad64(h, d_a):
     d, s, t = d_a.double(), torch.sigmoid(gate), torch.sigmoid(-gate)
     d_g, d_u = d * up * s * (1 + gate * t), d * gate * s
     # 1 + gate (1 - s) has a root near -1.28: its error is of its terms
-    return torch.cat([d_g, d_u], 1), torch.cat([(d * up * s).abs() * (1 + (gate * t).abs()), d_u.abs()], 1)
+    mags = torch.cat([(d * up * s).abs() * (1 + (gate * t).abs()), d_u.abs()], 1)
+    flushed = torch.cat([(d * up).abs() * (1 + gate.abs()), (d * gate).abs()], 1) * (s < 2 * TINY).repeat(1, 2) * TINY
+    return torch.cat([d_g, d_u], 1), mags + flushed / REL_GRAD
 
 
 @pytest.mark.parametrize("dt", [BF16, FP32])
@@ -304,6 +307,8 @@ def test_gate_codes_are_the_quantizer_s():
     fq = require_cuda()
     h = gate_inputs(176, 592, FP32, 7)
     h[11, 100], h[12, 592 + 5], h[13] = float("nan"), float("inf"), 0.0
+    h[14, 7] = torch.tensor(-1, dtype=torch.int32, device="cuda").view(FP32)  # a negative NaN
+    h[15, 9], h[15, 10], h[15, 11] = float("-inf"), 1e38, -1e38
     d_a = torch.randn(176, 592, device="cuda", generator=gen(2))
     r = fq.fp8q_swiglu(h, fmt=0, direction=fq.BOTH, want_a=True)
     b = fq.fp8q_swiglu_backward(h, d_a, fmt=1, direction=fq.BOTH, want_d_h=True)
