@@ -55,8 +55,15 @@ struct QtRaw {
       if constexpr (DT == kBF16) {
         a = ld_stream((const uint16_t*)p + i);
       } else {
-        a = ld_stream((const float*)p + i);
-        b = ld_stream((const float*)p + i + 4);
+        const float* q = (const float*)p + i;
+        if (((uintptr_t)q & 31) == 0) {  // whole sectors
+          asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                       : "l"(q));
+        } else {
+          a = ld_stream(q);
+          b = ld_stream(q + 4);
+        }
       }
     } else {
       a.x = DT == kBF16 ? (uint32_t)__ldg((const uint16_t*)p + i) << 16 : __ldg((const uint32_t*)p + i);
@@ -110,8 +117,14 @@ __device__ __forceinline__ void qt_store(void* p, int64_t i, float (&v)[V], bool
   } else {
     float* q = (float*)p + i;
     if constexpr (V == 8) {
-      st_stream(q, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-      st_stream(q + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+      const uint32_t u[8] = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]),
+                             __float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+      if (((uintptr_t)q & 31) == 0) {  // whole sectors
+        st32B(q, u);
+      } else {
+        st_stream(q, make_uint4(u[0], u[1], u[2], u[3]));
+        st_stream(q + 4, make_uint4(u[4], u[5], u[6], u[7]));
+      }
     } else {
       *q = v[0];
     }
@@ -123,6 +136,43 @@ __device__ __forceinline__ uint32_t qt_codes4(float a, float b, float c, float d
   mul2(a, b, s, s);
   mul2(c, d, s, s);
   return cvt4<FMT>(a, b, c, d);
+}
+
+// 16 bytes into shared memory while other work goes on.
+__device__ __forceinline__ void qt_ask(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void qt_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void qt_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+__device__ __forceinline__ uint4 qt_taken(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+// Eight values for each of G consecutive lanes of a warp (lane g of them), which
+// lie side by side from value i of p on and of which `left` are there: asked
+// for in whole sectors, so that FP32 lanes read what others asked for (with a
+// __syncwarp between, both ways).
+template <int DT>
+constexpr int kQtRunBytes = DT == kBF16 ? 16 : 32;  // of a lane
+
+template <int DT, int G>
+__device__ __forceinline__ void qt_ask8(const void* p, int64_t i, int64_t left, uint32_t place, int g) {
+  const uint8_t* from = (const uint8_t*)p + i * (DT == kBF16 ? 2 : 4);
+#pragma unroll
+  for (int k = 0; k < kQtRunBytes<DT> / 16; k++) {
+    const int u = k * G + g;
+    if (u * (DT == kBF16 ? 8 : 4) < left) qt_ask(place + 16 * u, from + 16 * u);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void qt_taken8(uint32_t place, int g, QtRaw<DT, 8>& raw) {
+  raw.a = qt_taken(place + kQtRunBytes<DT> * g);
+  if constexpr (DT == kFP32) raw.b = qt_taken(place + 32 * g + 16);
 }
 
 // The maxima of R row groups over the 16 lanes of a half-warp: at each step a
@@ -188,19 +238,6 @@ struct QtOut {
   float* s_t;
 };
 
-// 16 bytes into shared memory while other work goes on; a thread reads back
-// what it asked for itself, after qt_wait.
-__device__ __forceinline__ void qt_ask(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void qt_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void qt_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ uint4 qt_taken(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
-
 // A source gives 8 values of a row (rows come in multiples of 16, columns too)
 // from kInputs runs of 8 inputs of type kType, which is the dense output's too:
 //   bool needs(int input, int64_t col) const;
@@ -208,22 +245,29 @@ __device__ __forceinline__ uint4 qt_taken(uint32_t at) {
 //   void begin(int64_t row, int64_t col);                   // of kQtRows rows
 //   void values(const QtRaw<kType, 8> (&in)[kInputs], int i, int64_t col, float (&v)[8]) const;   // of row + i
 template <class Src>
-constexpr int kQtPieces = Src::kInputs * (Src::kType == kBF16 ? 1 : 2);  // of 16 bytes, for 8 values
-template <class Src>
-constexpr size_t kQtSmem = (size_t)kQtRows * kQtPieces<Src> * kQtThreads * 16;
+constexpr size_t kQtSmem = (size_t)kQtRows * Src::kInputs * kQtThreads * kQtRunBytes<Src::kType>;
 
+// What a half-warp asks for: its rows' values from column col on.
 template <class Src>
-__device__ __forceinline__ void qt_ask_tile(const Src& src, int64_t row, int64_t col, bool there, uint32_t place) {
+__device__ __forceinline__ void qt_ask_tile(const Src& src, int64_t row, int64_t col, int64_t cols, bool there, uint32_t place, int hl) {
   if (there) {
-    constexpr int kEach = kQtPieces<Src> / Src::kInputs;
 #pragma unroll
     for (int n = 0; n < Src::kInputs; n++) {
-      if (!src.needs(n, col)) continue;
 #pragma unroll
       for (int i = 0; i < kQtRows; i++) {
-        const uint8_t* from = (const uint8_t*)src.at(n, row + i, col);
+        // (a half-warp's columns may lie in two halves with different inputs: each lane asks for its own then)
+        if constexpr (Src::kType == kBF16) {
+          const int64_t c = col + 8 * hl;
+          if (c < cols && src.needs(n, c))
+            qt_ask(place + (i * Src::kInputs + n) * kQtThreads * 16 + hl * 16, src.at(n, row + i, c));
+        } else {
 #pragma unroll
-        for (int k = 0; k < kEach; k++) qt_ask(place + ((i * Src::kInputs + n) * kEach + k) * kQtThreads * 16, from + 16 * k);
+          for (int k = 0; k < 2; k++) {
+            const int64_t c = col + 4 * (k * 16 + hl);
+            if (c < cols && src.needs(n, c))
+              qt_ask(place + (i * Src::kInputs + n) * kQtThreads * 32 + (k * 16 + hl) * 16, src.at(n, row + i, c));
+          }
+        }
       }
     }
   }
@@ -233,12 +277,12 @@ __device__ __forceinline__ void qt_ask_tile(const Src& src, int64_t row, int64_t
 // Persistent: the inputs of a CTA's next tile come while it works on this one.
 template <class Src, int FMT, bool ROW>
 __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOut o) {
-  extern __shared__ __align__(16) uint8_t inputs[];  // [rows of a thread][pieces][threads] of 16 bytes
+  extern __shared__ __align__(16) uint8_t inputs[];  // [rows of a thread][inputs][threads] of 8 values
   __shared__ float scale[kQtTile];
   __shared__ __align__(16) uint8_t stage[kQtTile * 128];  // codes of the transposed tile; the warps' column maxima before
   float(*part)[kQtTile] = (float(*)[kQtTile])stage;
   const int tid = threadIdx.x, lane = tid & 31, hl = tid & 15, ty = tid >> 4;
-  const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + tid * 16;
+  const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + ty * 16 * kQtRunBytes<Src::kType>;  // of the half-warp
   const bool pair = o.halves && o.cols % (2 * kQtTile) == 0;
   const int items_c = pair ? o.tiles_c / 2 : o.tiles_c, items = o.tiles_r * items_c;
   const int64_t cols = pair ? o.cols / 2 : o.cols;
@@ -250,8 +294,8 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
     if (o.halves && !pair) tc = (tc & 1) ? (items_c + 1) / 2 + tc / 2 : tc / 2;
   };
   const auto ask = [&](int tr, int tc) {
-    const int64_t row = (int64_t)tr * kQtTile + ty * kQtRows, col = (int64_t)tc * kQtTile + hl * 8;
-    qt_ask_tile(src, row, col, col < cols && row < o.rows, place);
+    const int64_t row = (int64_t)tr * kQtTile + ty * kQtRows;
+    qt_ask_tile(src, row, (int64_t)tc * kQtTile, cols, row < o.rows, place, hl);
   };
   int tr, tc, half = 0, item = blockIdx.x;
   place_of(item, tr, tc);
@@ -262,17 +306,15 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
     const bool there = c < o.cols && r0 < o.rows;
     float v[kQtRows][8];
     if (there) src.begin(r0, c);
-    qt_wait();
+    qt_wait<0>();
+    __syncwarp();
     if (there) {
 #pragma unroll
       for (int i = 0; i < kQtRows; i++) {
         QtRaw<Src::kType, 8> in[Src::kInputs];
 #pragma unroll
         for (int n = 0; n < Src::kInputs; n++) {
-          if (!src.needs(n, c)) continue;
-          constexpr int kEach = kQtPieces<Src> / Src::kInputs;
-          in[n].a = qt_taken(place + (i * Src::kInputs + n) * kEach * kQtThreads * 16);
-          if (kEach == 2) in[n].b = qt_taken(place + ((i * Src::kInputs + n) * kEach + 1) * kQtThreads * 16);
+          if (src.needs(n, c)) qt_taken8<Src::kType>(place + (i * Src::kInputs + n) * kQtThreads * kQtRunBytes<Src::kType>, hl, in[n]);
         }
         src.values(in, i, c, v[i]);
       }
@@ -282,6 +324,7 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
 #pragma unroll
         for (int k = 0; k < 8; k++) v[i][k] = 0.0f;
     }
+    __syncwarp();
     if (pair && half == 0) {
       half = 1;
     } else {

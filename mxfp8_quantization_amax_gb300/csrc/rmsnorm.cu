@@ -24,7 +24,7 @@ struct RmsNorm {
   int weight_dt;
   int64_t rows, cols;
   int lanes;  // threads of a row
-  float eps;
+  float eps, one_over_cols;
   int fmt, pow2, tiles_c;
   void* h;
   float* rstd;
@@ -35,8 +35,7 @@ struct RmsNorm {
 
 // V values that the kernel may write in place.
 template <int DT, int V>
-__device__ __forceinline__ void rn_load_plain(const void* p, int64_t i, float (&v)[V]) {
-  QtRaw<DT, V> r;
+__device__ __forceinline__ void rn_load_plain(const void* p, int64_t i, QtRaw<DT, V>& r) {
   if constexpr (V == 8 && DT == kBF16) {
     r.a = *(const uint4*)((const uint16_t*)p + i);
   } else if constexpr (V == 8) {
@@ -45,7 +44,6 @@ __device__ __forceinline__ void rn_load_plain(const void* p, int64_t i, float (&
   } else {
     r.a.x = DT == kBF16 ? (uint32_t) * ((const uint16_t*)p + i) << 16 : *((const uint32_t*)p + i);
   }
-  r.get(v);
 }
 
 // V weights; every row reads them, so they may stay in L1.
@@ -72,13 +70,13 @@ __device__ __forceinline__ void rn_weight(const void* w, int dt, int64_t i, floa
 }
 
 // The sum over the `lanes` threads of a row (a multiple of 32; rows of a CTA
-// lie side by side).  Every thread of the CTA comes here.
+// lie side by side).  Every thread of the CTA comes here; calls in a row take
+// the halves of sh in turn.
 __device__ __forceinline__ float rn_row_sum(float v, int lanes, float* sh) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if (lanes == 32) return v;
   const int warp = threadIdx.x >> 5, per = lanes >> 5, first = warp / per * per;
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) sh[warp] = v;
   __syncthreads();
   v = 0.0f;
@@ -86,74 +84,153 @@ __device__ __forceinline__ float rn_row_sum(float v, int lanes, float* sh) {
   return v;
 }
 
-__device__ __forceinline__ float rn_rstd(float sum, int64_t cols, float eps) {
-  return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, (float)cols), eps)));
+// h = v (+ what is in b) stored and rounded, and the outputs of a row whose h is
+// in the registers of p.lanes threads, V values in each of N chunks.
+template <int RT, int V>
+__device__ __forceinline__ void rn_add(const RmsNorm& p, int64_t at, float (&v)[V], const float (&b)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; k++) v[k] = __fadd_rn(v[k], b[k]);
+  qt_store<RT, V>(p.h, at, v, true);
 }
 
-// A row in the registers of p.lanes threads, V values in each of N chunks.
-template <int DT, int RT, int V, int N, int T>
-__global__ void __launch_bounds__(T) rmsnorm_kernel(RmsNorm p) {
-  __shared__ float sh[32];
-  const int t = threadIdx.x % p.lanes;
-  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / p.lanes) + threadIdx.x / p.lanes;
-  const bool row_ok = r < p.rows;
-  float v[N][V];
+template <int DT, int V, int N, class Weight>
+__device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64_t r, bool row_ok, int t, float* sh, Weight weight) {
   float sum = 0.0f;
-  pdl_wait();
-#pragma unroll
-  for (int n = 0; n < N; n++) {
-    const int64_t c = (int64_t)(n * p.lanes + t) * V;
-#pragma unroll
-    for (int k = 0; k < V; k++) v[n][k] = 0.0f;
-    if (row_ok && c < p.cols) {
-      QtRaw<DT, V> raw;
-      raw.load(p.x, r * p.cols + c);
-      if constexpr (RT != kNone) {
-        float b[V];
-        rn_load_plain<RT, V>(p.residual, r * p.cols + c, b);
-        raw.get(v[n]);
-#pragma unroll
-        for (int k = 0; k < V; k++) v[n][k] = __fadd_rn(v[n][k], b[k]);
-        qt_store<RT, V>(p.h, r * p.cols + c, v[n], true);
-      } else {
-        raw.get(v[n]);
-      }
-    }
-  }
 #pragma unroll
   for (int n = 0; n < N; n++)
 #pragma unroll
     for (int k = 0; k < V; k++) sum = __fmaf_rn(v[n][k], v[n][k], sum);
-  const float rstd = rn_rstd(rn_row_sum(sum, p.lanes, sh), p.cols, p.eps);
+  // rsqrtf is within two units
+  const float rstd = rsqrtf(__fadd_rn(__fmul_rn(rn_row_sum(sum, p.lanes, sh), p.one_over_cols), p.eps));
   if (row_ok && t == 0) p.rstd[r] = rstd;
-  if (p.y != nullptr || p.q != nullptr) {
+  if (p.y == nullptr && p.q == nullptr) return;
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    if (!row_ok || (n * p.lanes + t) * V >= p.cols) continue;
+    float w[V];
+    weight(n, w);
+#pragma unroll
+    for (int k = 0; k < V; k++) v[n][k] = __fmul_rn(__fmul_rn(v[n][k], rstd), w[k]);
+  }
+  if constexpr (V == 8) {
+    if (p.q != nullptr) {  // 16 threads hold a group of 128 columns, N of them
+      uint8_t* q = p.q + r * p.cols + 8 * t;
+      float* s = p.s + r * p.tiles_c + t / 16;
+      const auto codes = [&](int n) { return q + (int64_t)n * p.lanes * 8; };
+      const auto scale = [&](int n) { return s + n * p.lanes / 16; };
+      const auto there = [&](int n) { return row_ok && (n * p.lanes + t) * 8 < p.cols; };
+      if (p.fmt == kE4M3) qt_groups<kE4M3, N>(v, p.pow2, codes, scale, there);
+      else qt_groups<kE5M2, N>(v, p.pow2, codes, scale, there);
+    }
+  }
+  if (p.y != nullptr) {
 #pragma unroll
     for (int n = 0; n < N; n++) {
       const int64_t c = (int64_t)(n * p.lanes + t) * V;
-      if (!row_ok || c >= p.cols) continue;
-      float w[V];
-      rn_weight<V>(p.weight, p.weight_dt, c, w);
-#pragma unroll
-      for (int k = 0; k < V; k++) v[n][k] = __fmul_rn(__fmul_rn(v[n][k], rstd), w[k]);
+      if (row_ok && c < p.cols) qt_store<DT, V>(p.y, r * p.cols + c, v[n]);
     }
-    if constexpr (V == 8) {
-      if (p.q != nullptr) {  // 16 threads hold a group of 128 columns, N of them
-        uint8_t* q = p.q + r * p.cols + 8 * t;
-        float* s = p.s + r * p.tiles_c + t / 16;
-        const auto codes = [&](int n) { return q + (int64_t)n * p.lanes * 8; };
-        const auto scale = [&](int n) { return s + n * p.lanes / 16; };
-        const auto there = [&](int n) { return row_ok && (n * p.lanes + t) * 8 < p.cols; };
-        if (p.fmt == kE4M3) qt_groups<kE4M3, N>(v, p.pow2, codes, scale, there);
-        else qt_groups<kE5M2, N>(v, p.pow2, codes, scale, there);
+  }
+}
+
+// A CTA a row, or a few short rows.
+template <int DT, int RT, int V, int N, int T>
+__global__ void __launch_bounds__(T) rmsnorm_kernel(RmsNorm p) {
+  __shared__ float sh[64];
+  const int t = threadIdx.x % p.lanes;
+  const int64_t r = (int64_t)blockIdx.x * (blockDim.x / p.lanes) + threadIdx.x / p.lanes;
+  const bool row_ok = r < p.rows;
+  // all loads before the first store: where nothing is there the first values are read
+  QtRaw<DT, V> raw[N];
+  QtRaw<RT == kNone ? DT : RT, V> res[N];
+  float v[N][V];
+  const auto at = [&](int n) { return row_ok && (n * p.lanes + t) * V < p.cols ? r * p.cols + (n * p.lanes + t) * V : 0; };
+  pdl_wait();
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    raw[n].load(p.x, at(n));
+    if constexpr (RT != kNone) rn_load_plain<RT, V>(p.residual, at(n), res[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    if (row_ok && (n * p.lanes + t) * V < p.cols) {
+      raw[n].get(v[n]);
+      if constexpr (RT != kNone) {
+        float b[V];
+        res[n].get(b);
+        rn_add<RT, V>(p, at(n), v[n], b);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; k++) v[n][k] = 0.0f;
+    }
+  }
+  rn_row<DT, V, N>(p, v, r, row_ok, t, sh, [&](int n, float (&w)[V]) { rn_weight<V>(p.weight, p.weight_dt, (int64_t)(n * p.lanes + t) * V, w); });
+  pdl_launch_dependents();
+}
+
+// Many rows: CTAs stay, keep the weights in registers and have the next rows on
+// their way.
+constexpr int kRnChunks = 4;
+template <int DT>
+constexpr int kRnBytes = DT == kNone ? 0 : 32 * kQtRunBytes<DT>;  // of a warp's chunk of one input
+
+template <int DT, int RT, int T>
+__global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_kernel(RmsNorm p) {
+  constexpr int kChunk = kRnBytes<DT> + kRnBytes<RT>;
+  extern __shared__ __align__(16) uint8_t inputs[];  // [warps][chunks][kChunk]
+  __shared__ float sh[64];
+  const int t = threadIdx.x % p.lanes, lane = threadIdx.x & 31, per = blockDim.x / p.lanes, cols = (int)p.cols;
+  const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + (threadIdx.x >> 5) * kRnChunks * kChunk;
+  const auto ask = [&](int64_t r) {
+    if (r < p.rows) {
+#pragma unroll
+      for (int n = 0; n < kRnChunks; n++) {
+        const int c = (n * p.lanes + t - lane) * 8;
+        qt_ask8<DT, 32>(p.x, r * cols + c, cols - c, place + n * kChunk, lane);
+        if constexpr (RT != kNone) qt_ask8<RT, 32>(p.residual, r * cols + c, cols - c, place + n * kChunk + kRnBytes<DT>, lane);
       }
     }
-    if (p.y != nullptr) {
+    qt_commit();
+  };
+  pdl_wait();
+  const int64_t step = (int64_t)gridDim.x * per;
+  int64_t r0 = (int64_t)blockIdx.x * per;
+  ask(r0 + threadIdx.x / p.lanes);
+  float w[kRnChunks][8];
 #pragma unroll
-      for (int n = 0; n < N; n++) {
-        const int64_t c = (int64_t)(n * p.lanes + t) * V;
-        if (row_ok && c < p.cols) qt_store<DT, V>(p.y, r * p.cols + c, v[n]);
+  for (int n = 0; n < kRnChunks; n++)
+    if ((n * p.lanes + t) * 8 < cols) rn_weight<8>(p.weight, p.weight_dt, (n * p.lanes + t) * 8, w[n]);
+  int turn = 0;
+  for (; r0 < p.rows; r0 += step) {
+    const int64_t r = r0 + threadIdx.x / p.lanes;
+    const bool row_ok = r < p.rows;
+    float v[kRnChunks][8];
+    qt_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < kRnChunks; n++) {
+      const int c = (n * p.lanes + t) * 8;
+#pragma unroll
+      for (int k = 0; k < 8; k++) v[n][k] = 0.0f;
+      if (row_ok && c < cols) {
+        QtRaw<DT, 8> raw;
+        qt_taken8<DT>(place + n * kChunk, lane, raw);
+        raw.get(v[n]);
+        if constexpr (RT != kNone) {
+          QtRaw<RT, 8> res;
+          float b[8];
+          qt_taken8<RT>(place + n * kChunk + kRnBytes<DT>, lane, res);
+          res.get(b);
+          rn_add<RT, 8>(p, r * cols + c, v[n], b);
+        }
       }
     }
+    __syncwarp();
+    ask(r + step);
+    rn_row<DT, 8, kRnChunks>(p, v, r, row_ok, t, sh + (turn ^= 32), [&](int n, float (&u)[8]) {
+#pragma unroll
+      for (int k = 0; k < 8; k++) u[k] = w[n][k];
+    });
   }
   pdl_launch_dependents();
 }
@@ -200,125 +277,220 @@ struct RmsNormBackward {
   const void* d_h;  // or NULL
   int64_t rows, cols;
   int lanes;
+  float one_over_cols;
   void* d_x;
   float* partial;  // [groups of threads][cols]
 };
 
-// Each group of p.lanes threads takes every gridDim.x-th set of rows and keeps
-// its columns' sums of the weight gradient.
-template <int DT, int HT, int V, int N, int T>
-__global__ void __launch_bounds__(T) rmsnorm_backward_kernel(RmsNormBackward p) {
-  extern __shared__ float acc_sh[];  // N == 0: the sums of all columns
-  __shared__ float sh[32];
-  const int t = threadIdx.x % p.lanes, per = blockDim.x / p.lanes, mine = threadIdx.x / p.lanes;
-  pdl_wait();
-  if constexpr (N > 0) {
-    float acc[N][V];
+// The sums of the CTA's groups of threads, in their order, as one row of partial sums.
+template <int V, int N>
+__device__ __forceinline__ void rn_partial(const RmsNormBackward& p, const float (&acc)[N][V], int t, int per, float* sh) {
+  float* to = p.partial + (int64_t)blockIdx.x * p.cols;
+  __syncthreads();
+  if (per > 1) {  // p.lanes * V * N values, of which cols are there, for each group
 #pragma unroll
     for (int n = 0; n < N; n++)
 #pragma unroll
-      for (int k = 0; k < V; k++) acc[n][k] = 0.0f;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per) {
-      const int64_t r = r0 + mine;
-      const bool row_ok = r < p.rows;
-      QtRaw<DT, V> d[N];
-      QtRaw<HT, V> h[N];
-      const float rstd = row_ok ? __ldg(p.rstd + r) : 0.0f;
-#pragma unroll
-      for (int n = 0; n < N; n++) {
-        const int64_t c = (int64_t)(n * p.lanes + t) * V;
-        d[n].zero();
-        h[n].zero();
-        if (row_ok && c < p.cols) {
-          d[n].load(p.d_y, r * p.cols + c);
-          h[n].load(p.h, r * p.cols + c);
-        }
-      }
+      for (int k = 0; k < V; k++) sh[(threadIdx.x / p.lanes * N + n) * p.lanes * V + t * V + k] = acc[n][k];
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
       float sum = 0.0f;
+      for (int i = 0; i < per; i++) sum += sh[i * N * p.lanes * V + c];
+      to[c] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; n++)
+#pragma unroll
+      for (int k = 0; k < V; k++)
+        if ((n * p.lanes + t) * V + k < p.cols) to[(n * p.lanes + t) * V + k] = acc[n][k];
+  }
+}
+
+// Each group of p.lanes threads takes every gridDim.x-th set of rows and keeps
+// its columns' sums of the weight gradient.  Eight values a chunk; the next
+// rows' inputs are on their way.
+template <int DT, int HT, int T>
+__global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_kernel(RmsNormBackward p) {
+  constexpr int N = kRnChunks, kFirst = kRnBytes<DT> + kRnBytes<HT>, kChunk = kFirst + kRnBytes<HT>;
+  extern __shared__ __align__(16) uint8_t inputs[];  // [warps][chunks][kChunk]
+  __shared__ float sh[64];
+  const int t = threadIdx.x % p.lanes, lane = threadIdx.x & 31, per = blockDim.x / p.lanes, cols = (int)p.cols;
+  const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + (threadIdx.x >> 5) * N * kChunk;
+  const auto ask = [&](int64_t r, bool past) {  // d_y and h, or d_h
+    if (r < p.rows && (!past || p.d_h != nullptr)) {
 #pragma unroll
       for (int n = 0; n < N; n++) {
-        const int64_t c = (int64_t)(n * p.lanes + t) * V;
-        if (c >= p.cols) continue;
-        float w[V], dv[V], hv[V];
-        rn_weight<V>(p.weight, p.weight_dt, c, w);
-        d[n].get(dv);
-        h[n].get(hv);
-#pragma unroll
-        for (int k = 0; k < V; k++) {
-          const float u = __fmul_rn(hv[k], rstd);
-          sum = __fmaf_rn(__fmul_rn(dv[k], w[k]), u, sum);
-          acc[n][k] = __fmaf_rn(dv[k], u, acc[n][k]);
+        const int c = (n * p.lanes + t - lane) * 8;
+        if (past) {
+          qt_ask8<HT, 32>(p.d_h, r * cols + c, cols - c, place + n * kChunk + kFirst, lane);
+        } else {
+          qt_ask8<DT, 32>(p.d_y, r * cols + c, cols - c, place + n * kChunk, lane);
+          qt_ask8<HT, 32>(p.h, r * cols + c, cols - c, place + n * kChunk + kRnBytes<DT>, lane);
         }
-      }
-      const float mean = __fdiv_rn(rn_row_sum(sum, p.lanes, sh), (float)p.cols);
-#pragma unroll
-      for (int n = 0; n < N; n++) {
-        const int64_t c = (int64_t)(n * p.lanes + t) * V;
-        if (!row_ok || c >= p.cols) continue;
-        float w[V], dv[V], hv[V], res[V];
-        rn_weight<V>(p.weight, p.weight_dt, c, w);
-        d[n].get(dv);
-        h[n].get(hv);
-        if (p.d_h != nullptr) rn_load_plain<HT, V>(p.d_h, r * p.cols + c, res);
-#pragma unroll
-        for (int k = 0; k < V; k++) {
-          const float u = __fmul_rn(hv[k], rstd);
-          const float g = __fmul_rn(rstd, __fmaf_rn(-u, mean, __fmul_rn(dv[k], w[k])));
-          dv[k] = p.d_h != nullptr ? __fadd_rn(g, res[k]) : g;
-        }
-        qt_store<HT, V>(p.d_x, r * p.cols + c, dv);
       }
     }
-    float* to = p.partial + ((int64_t)blockIdx.x * per + mine) * p.cols;
+    qt_commit();
+  };
+  pdl_wait();
+  const int64_t step = (int64_t)gridDim.x * per;
+  int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / p.lanes;
+  ask(r, false);
+  ask(r, true);
+  float next_rstd = r < p.rows ? __ldg(p.rstd + r) : 0.0f;
+  int turn = 0;
+  float acc[N][8] = {};
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += step, r += step) {
+    const bool row_ok = r < p.rows;
+    const float rstd = next_rstd;
+    QtRaw<DT, 8> d[N];
+    QtRaw<HT, 8> h[N];
+    qt_wait<1>();
+    __syncwarp();
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      const int64_t c = (int64_t)(n * p.lanes + t) * V;
+      d[n].zero();
+      h[n].zero();
+      if (row_ok && (n * p.lanes + t) * 8 < cols) {
+        qt_taken8<DT>(place + n * kChunk, lane, d[n]);
+        qt_taken8<HT>(place + n * kChunk + kRnBytes<DT>, lane, h[n]);
+      }
+    }
+    __syncwarp();
+    ask(r + step, false);
+    if (r + step < p.rows) next_rstd = __ldg(p.rstd + r + step);
+    float sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const int c = (n * p.lanes + t) * 8;
       if (c >= p.cols) continue;
-      if constexpr (V == 8) {
-        *(float4*)(to + c) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-        *(float4*)(to + c + 4) = make_float4(acc[n][4], acc[n][5], acc[n][6], acc[n][7]);
-      } else {
-        to[c] = acc[n][0];
+      float dv[8], u[8], w[8];
+      rn_weight<8>(p.weight, p.weight_dt, c, w);
+      d[n].get(dv);
+      h[n].get(u);
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        u[k] = __fmul_rn(u[k], rstd);
+        sum = __fmaf_rn(__fmul_rn(dv[k], w[k]), u[k], sum);
+        acc[n][k] = __fmaf_rn(dv[k], u[k], acc[n][k]);
       }
     }
-  } else {  // any columns and alignment: one row a CTA, read twice
+    const float mean = __fmul_rn(rn_row_sum(sum, p.lanes, sh + (turn ^= 32)), p.one_over_cols);
+    qt_wait<1>();
+    __syncwarp();
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+      const int c = (n * p.lanes + t) * 8;
+      if (!row_ok || c >= p.cols) continue;
+      float dv[8], u[8], w[8];
+      rn_weight<8>(p.weight, p.weight_dt, c, w);
+      d[n].get(dv);
+      h[n].get(u);
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        u[k] = __fmul_rn(u[k], rstd);
+        dv[k] = __fmul_rn(rstd, __fmaf_rn(-u[k], mean, __fmul_rn(dv[k], w[k])));
+      }
+      if (p.d_h != nullptr) {
+        QtRaw<HT, 8> past;
+        qt_taken8<HT>(place + n * kChunk + kFirst, lane, past);
+        past.get(u);
+#pragma unroll
+        for (int k = 0; k < 8; k++) dv[k] = __fadd_rn(dv[k], u[k]);
+      }
+      qt_store<HT, 8>(p.d_x, r * p.cols + c, dv);
+    }
+    __syncwarp();
+    ask(r + step, true);
+  }
+  qt_wait<0>();
+  rn_partial<8, N>(p, acc, t, per, (float*)inputs);
+  pdl_launch_dependents();
+}
+
+// Any columns and alignment: value by value, N of them a thread in registers, or
+// (N = 0) any number, read twice, with the columns' sums in shared memory.
+template <int DT, int HT, int N>
+__global__ void __launch_bounds__(512) rmsnorm_backward_any_kernel(RmsNormBackward p) {
+  extern __shared__ float acc_sh[];
+  __shared__ float sh[64];
+  constexpr int M = N > 0 ? N : 1;
+  const int t = threadIdx.x % p.lanes, per = blockDim.x / p.lanes;
+  const auto value = [&](int64_t at, int64_t c, float rstd, float& d, float& g, float& u) {
+    QtRaw<DT, 1> draw;
+    QtRaw<HT, 1> hraw;
+    float dv[1], hv[1], w[1];
+    draw.load(p.d_y, at);
+    hraw.load(p.h, at);
+    rn_weight<1>(p.weight, p.weight_dt, c, w);
+    draw.get(dv);
+    hraw.get(hv);
+    d = dv[0];
+    g = __fmul_rn(dv[0], w[0]);
+    u = __fmul_rn(hv[0], rstd);
+  };
+  const auto past = [&](int64_t at) {
+    QtRaw<HT, 1> raw;
+    float v[1];
+    rn_load_plain<HT, 1>(p.d_h, at, raw);
+    raw.get(v);
+    return v[0];
+  };
+  const auto store = [&](int64_t at, float rstd, float mean, float g, float u, float add) {
+    float o[1] = {__fmul_rn(rstd, __fmaf_rn(-u, mean, g))};
+    if (p.d_h != nullptr) o[0] = __fadd_rn(o[0], add);
+    qt_store<HT, 1>(p.d_x, at, o);
+  };
+  pdl_wait();
+  int turn = 0;
+  float acc[M][1] = {};
+  if (N == 0)
     for (int64_t c = t; c < p.cols; c += p.lanes) acc_sh[c] = 0.0f;
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-      const float rstd = __ldg(p.rstd + r);
-      float sum = 0.0f;
-      for (int64_t c = t; c < p.cols; c += p.lanes) {
-        QtRaw<DT, 1> d;
-        QtRaw<HT, 1> h;
-        float w[1], dv[1], hv[1];
-        d.load(p.d_y, r * p.cols + c);
-        h.load(p.h, r * p.cols + c);
-        rn_weight<1>(p.weight, p.weight_dt, c, w);
-        d.get(dv);
-        h.get(hv);
-        const float u = __fmul_rn(hv[0], rstd);
-        sum = __fmaf_rn(__fmul_rn(dv[0], w[0]), u, sum);
-        acc_sh[c] = __fmaf_rn(dv[0], u, acc_sh[c]);
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per) {
+    const int64_t r = r0 + threadIdx.x / p.lanes, at = r * p.cols;
+    const bool row_ok = r < p.rows;
+    const float rstd = row_ok ? __ldg(p.rstd + r) : 0.0f;
+    float sum = 0.0f, g[M], u[M], d;
+    if constexpr (N > 0) {
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        const int c = n * p.lanes + t;
+        const bool there = row_ok && c < p.cols;  // where nothing is, the first value is read
+        value(there ? at + c : 0, there ? c : 0, rstd, d, g[n], u[n]);
+        if (!there) g[n] = u[n] = d = 0.0f;
+        sum = __fmaf_rn(g[n], u[n], sum);
+        acc[n][0] = __fmaf_rn(d, u[n], acc[n][0]);
       }
-      const float mean = __fdiv_rn(rn_row_sum(sum, p.lanes, sh), (float)p.cols);
+    } else {
       for (int64_t c = t; c < p.cols; c += p.lanes) {
-        QtRaw<DT, 1> d;
-        QtRaw<HT, 1> h;
-        float w[1], dv[1], hv[1], res[1] = {0.0f};
-        d.load(p.d_y, r * p.cols + c);
-        h.load(p.h, r * p.cols + c);
-        rn_weight<1>(p.weight, p.weight_dt, c, w);
-        d.get(dv);
-        h.get(hv);
-        const float u = __fmul_rn(hv[0], rstd);
-        float g = __fmul_rn(rstd, __fmaf_rn(-u, mean, __fmul_rn(dv[0], w[0])));
-        if (p.d_h != nullptr) {
-          rn_load_plain<HT, 1>(p.d_h, r * p.cols + c, res);
-          g = __fadd_rn(g, res[0]);
-        }
-        float o[1] = {g};
-        qt_store<HT, 1>(p.d_x, r * p.cols + c, o);
+        value(at + c, c, rstd, d, g[0], u[0]);
+        sum = __fmaf_rn(g[0], u[0], sum);
+        acc_sh[c] = __fmaf_rn(d, u[0], acc_sh[c]);
       }
     }
+    const float mean = __fmul_rn(rn_row_sum(sum, p.lanes, sh + (turn ^= 32)), p.one_over_cols);
+    if constexpr (N > 0) {
+      float add[M];
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        const int c = n * p.lanes + t;
+        add[n] = p.d_h != nullptr ? past(row_ok && c < p.cols ? at + c : 0) : 0.0f;
+      }
+#pragma unroll
+      for (int n = 0; n < N; n++) {
+        const int c = n * p.lanes + t;
+        if (row_ok && c < p.cols) store(at + c, rstd, mean, g[n], u[n], add[n]);
+      }
+    } else {
+      for (int64_t c = t; c < p.cols; c += p.lanes) {
+        value(at + c, c, rstd, d, g[0], u[0]);
+        store(at + c, rstd, mean, g[0], u[0], p.d_h != nullptr ? past(at + c) : 0.0f);
+      }
+    }
+  }
+  if constexpr (N > 0) {
+    rn_partial<1, N>(p, acc, t, per, acc_sh);
+  } else {
     for (int64_t c = t; c < p.cols; c += p.lanes) p.partial[(int64_t)blockIdx.x * p.cols + c] = acc_sh[c];
   }
   pdl_launch_dependents();
@@ -355,52 +527,78 @@ static bool off(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) != 0;
 static size_t size_of(int32_t dt) { return dt == FP8Q_IN_BF16 ? 2 : 4; }
 static bool type_ok(int32_t dt) { return dt == FP8Q_IN_BF16 || dt == FP8Q_IN_FP32; }
 
-// Threads of a row whose chunks of V values are taken N at a time at most.
-static int row_lanes(int64_t cols, int v, int n) {
-  const int64_t chunks = (cols + v - 1) / v;
-  int lanes = 32;
-  while ((int64_t)lanes * n < chunks) lanes *= 2;
-  return lanes;
-}
+// Threads of a row of which each has N chunks of V values at most: whole warps.
+static int row_lanes(int64_t cols, int v, int n) { return (int)((cols + 32 * v * n - 1) / (32 * v * n)) * 32; }
+// Rows side by side in a CTA of about `threads` threads.
+static int row_groups(int lanes, int threads) { return lanes < threads ? threads / lanes : 1; }
 
 template <int DT, int RT, int V, int N>
-static cudaError_t launch_norm_n(RmsNorm& p, cudaStream_t s) {
+static cudaError_t launch_norm_rows(RmsNorm& p, cudaStream_t s) {
   p.lanes = row_lanes(p.cols, V, N);
-  const int threads = p.lanes > kRnThreads ? p.lanes : kRnThreads, per = threads / p.lanes;
+  const int per = row_groups(p.lanes, kRnThreads), threads = p.lanes * per;
   const dim3 grid((unsigned)((p.rows + per - 1) / per));
-  return launch_kernel(threads == kRnThreads ? rmsnorm_kernel<DT, RT, V, N, kRnThreads> : rmsnorm_kernel<DT, RT, V, N, 1024>, grid,
+  return launch_kernel(threads <= kRnThreads ? rmsnorm_kernel<DT, RT, V, N, kRnThreads> : rmsnorm_kernel<DT, RT, V, N, 1024>, grid,
                        dim3(threads), 0, s, p);
+}
+
+template <int DT, int RT, int T>
+static cudaError_t launch_norm_stream(RmsNorm& p, cudaStream_t s) {
+  constexpr size_t kEach = (size_t)kRnChunks * (kRnBytes<DT> + kRnBytes<RT>) / 32;  // of a thread
+  p.lanes = row_lanes(p.cols, 8, kRnChunks);
+  const int per = row_groups(p.lanes, kRnThreads), threads = p.lanes * per;
+  static PerDevice<bool> allowed;
+  const cudaError_t e = allow_smem(allowed, rmsnorm_stream_kernel<DT, RT, T>, kEach * T);
+  if (e != cudaSuccess) return e;
+  const int64_t sets = (p.rows + per - 1) / per, fit = (T == kRnThreads ? 2 : 1) * (int64_t)sm_count();
+  return launch_kernel(rmsnorm_stream_kernel<DT, RT, T>, dim3((unsigned)(sets < fit ? sets : fit)), dim3(threads), kEach * threads, s, p);
 }
 
 template <int DT, int RT>
 static cudaError_t launch_norm(RmsNorm& p, bool vec, cudaStream_t s) {
-  if (!vec) return p.cols <= 8192 ? launch_norm_n<DT, RT, 1, 8>(p, s) : launch_norm_n<DT, RT, 1, 32>(p, s);
-  // a row in few threads, or in as many as it has chunks where few rows have the machine to themselves
-  if (p.rows <= 2 * sm_count() && p.cols <= 8192) return launch_norm_n<DT, RT, 8, 1>(p, s);
-  return launch_norm_n<DT, RT, 8, 4>(p, s);
+  if (!vec) return p.cols <= 8192 ? launch_norm_rows<DT, RT, 1, 8>(p, s) : launch_norm_rows<DT, RT, 1, 32>(p, s);
+  // few rows: a row in as many threads as it has chunks
+  if (p.rows <= 2 * sm_count() && p.cols <= 8192) return launch_norm_rows<DT, RT, 8, 1>(p, s);
+  if (p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_stream<DT, RT, kRnThreads>(p, s);
+  if (p.cols <= 8 * kRnChunks * 512) return launch_norm_stream<DT, RT, 512>(p, s);
+  return launch_norm_rows<DT, RT, 8, 4>(p, s);
+}
+
+static int64_t backward_grid(int64_t rows, int per, int ctas) {
+  const int64_t sets = (rows + per - 1) / per, fit = (int64_t)sm_count() * ctas, most = fit < kRnMaxPartials ? fit : kRnMaxPartials;
+  return sets < most ? sets : most;
+}
+
+template <int DT, int HT, int T>
+static cudaError_t launch_norm_backward_vec(RmsNormBackward& p, int* parts, cudaStream_t s) {
+  constexpr size_t kEach = (size_t)kRnChunks * (kRnBytes<DT> + 2 * kRnBytes<HT>) / 32;  // of a thread; > the partial sums' 4 * 8 * kRnChunks
+  p.lanes = row_lanes(p.cols, 8, kRnChunks);
+  const int per = row_groups(p.lanes, kRnThreads), threads = p.lanes * per;
+  static PerDevice<bool> allowed;
+  const cudaError_t e = allow_smem(allowed, rmsnorm_backward_kernel<DT, HT, T>, kEach * T);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = backward_grid(p.rows, per, T == kRnThreads ? 2 : 1);
+  *parts = (int)grid;
+  return launch_kernel(rmsnorm_backward_kernel<DT, HT, T>, dim3((unsigned)grid), dim3(threads), kEach * threads, s, p);
+}
+
+template <int DT, int HT, int N>
+static cudaError_t launch_norm_backward_any(RmsNormBackward& p, int* parts, cudaStream_t s) {
+  p.lanes = N > 0 ? row_lanes(p.cols, 1, N) : 512;
+  const int per = row_groups(p.lanes, kRnThreads), threads = p.lanes * per;
+  const size_t smem = N > 0 ? (size_t)threads * N * sizeof(float) : (size_t)p.cols * sizeof(float);
+  static PerDevice<bool> allowed;
+  const cudaError_t e = allow_smem(allowed, rmsnorm_backward_any_kernel<DT, HT, N>, kRnMaxCols * sizeof(float));
+  if (e != cudaSuccess) return e;
+  const int64_t grid = backward_grid(p.rows, per, 4);
+  *parts = (int)grid;
+  return launch_kernel(rmsnorm_backward_any_kernel<DT, HT, N>, dim3((unsigned)grid), dim3(threads), smem, s, p);
 }
 
 template <int DT, int HT>
 static cudaError_t launch_norm_backward(RmsNormBackward& p, bool vec, int* parts, cudaStream_t s) {
-  if (!vec) {
-    p.lanes = 256;
-    *parts = (int)(p.rows < kRnMaxPartials ? p.rows : kRnMaxPartials);
-    const size_t smem = (size_t)p.cols * sizeof(float);
-    static PerDevice<bool> allowed;
-    const cudaError_t e = allow_smem(allowed, rmsnorm_backward_kernel<DT, HT, 1, 0, 256>, kRnMaxCols * sizeof(float));
-    if (e != cudaSuccess) return e;
-    return launch_kernel(rmsnorm_backward_kernel<DT, HT, 1, 0, 256>, dim3(*parts), dim3(256), smem, s, p);
-  }
-  p.lanes = row_lanes(p.cols, 8, 4);
-  const int threads = p.lanes > kRnThreads ? p.lanes : kRnThreads, per = threads / p.lanes;
-  const int64_t sets = (p.rows + per - 1) / per;
-  int64_t grid = kRnMaxPartials / per;
-  const int64_t fit = (int64_t)sm_count() * (threads <= 256 ? 2 : 1);
-  grid = grid < fit ? grid : fit;
-  grid = grid < sets ? grid : sets;
-  *parts = (int)grid * per;
-  return launch_kernel(threads == kRnThreads ? rmsnorm_backward_kernel<DT, HT, 8, 4, kRnThreads> : rmsnorm_backward_kernel<DT, HT, 8, 4, 1024>,
-                       dim3((unsigned)grid), dim3(threads), 0, s, p);
+  if (vec && p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_backward_vec<DT, HT, kRnThreads>(p, parts, s);
+  if (vec && p.cols <= 8 * kRnChunks * 512) return launch_norm_backward_vec<DT, HT, 512>(p, parts, s);
+  return p.cols <= 512 * 16 ? launch_norm_backward_any<DT, HT, 16>(p, parts, s) : launch_norm_backward_any<DT, HT, 0>(p, parts, s);
 }
 
 }  // namespace fp8q
@@ -436,6 +634,7 @@ extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* resid
   p.rows = rows;
   p.cols = cols;
   p.eps = eps;
+  p.one_over_cols = 1.0f / (float)cols;
   p.fmt = fmt;
   p.pow2 = pow2_scales ? 1 : 0;
   p.tiles_c = (int)((cols + kQtTile - 1) / kQtTile);
@@ -480,8 +679,7 @@ extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* resid
 
 extern "C" size_t fp8q_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows < 1 || cols < 1 || cols > kRnMaxCols) return 0;
-  // a CTA's groups of threads side by side may be more than the rows
-  const int64_t parts = rows + 8 < kRnMaxPartials ? rows + 8 : kRnMaxPartials;
+  const int64_t parts = rows < kRnMaxPartials ? rows : kRnMaxPartials;
   return (size_t)parts * cols * sizeof(float);
 }
 
@@ -515,6 +713,7 @@ extern "C" fp8q_status fp8q_rmsnorm_backward(const void* d_y, int32_t dt, const 
     p.d_h = d_h;
     p.rows = rows;
     p.cols = cols;
+    p.one_over_cols = 1.0f / (float)cols;
     p.d_x = d_x;
     p.partial = (float*)workspace;
     const bool vec = cols % 8 == 0 && !off(d_y, 16) && !off(h, 16) && !off(weight, 16) && !off(d_h, 16) && !off(d_x, 16);
