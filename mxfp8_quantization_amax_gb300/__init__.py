@@ -18,6 +18,7 @@ import ctypes
 import math
 import os
 import threading
+from array import array
 
 import torch
 
@@ -729,9 +730,12 @@ def _floats(t: torch.Tensor, name: str, shape: tuple, at: int):
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on cuda:{at}")
 
 
+_empty = torch.empty
+
+
 def _result(out, shape: tuple, dtype, device):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype=dtype, device=device)
     if out.device != device or out.dtype != dtype or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape {shape} on {device}")
     return out
@@ -1168,28 +1172,33 @@ def fp8q_swiglu_backward(h: torch.Tensor, d_a: torch.Tensor, fmt: int = E5M2, di
 # ---------------------------------------------------------------------------
 # the gradients' norm
 # ---------------------------------------------------------------------------
-def _clip(grads, max_norm: float, out, want_scale: bool, norm, scale):
-    grads = list(grads)
+def _tensors(tensors: list, name: str, at: int) -> tuple:
+    """Addresses and input types of contiguous tensors on device `at`, as int64 and int32 arrays."""
+    types = [_IN.get(t.dtype) for t in tensors]
+    if [t.get_device() for t in tensors] != [at] * len(tensors) or None in types or not all([t.is_contiguous() for t in tensors]):
+        raise ValueError(f"{name} must be contiguous bfloat16 or float32 tensors on cuda:{at}")
+    return array("q", [t.data_ptr() for t in tensors]), array("i", types)
+
+
+def _clip(grads: list, max_norm: float, out, norm):
     if not grads:
         raise ValueError("grads must hold at least one tensor")
-    n, at = len(grads), _device(grads[0], "grads")
-    dts, sizes, ptrs, outs = (_c.c_int32 * n)(), (_c.c_int64 * n)(), (_P * n)(), (_P * n)() if out is not None else None
-    for i, g in enumerate(grads):
-        if g.get_device() != at or g.dtype not in _VALUES or not g.is_contiguous():
-            raise ValueError(f"grads[{i}] must be a contiguous bfloat16 or float32 tensor on cuda:{at}")
-        dts[i], sizes[i], ptrs[i] = _IN[g.dtype], g.numel(), g.data_ptr()
+    n, at, dev = len(grads), _device(grads[0], "grads"), grads[0].device
+    ptrs, types = _tensors(grads, "grads", at)
+    sizes = array("q", [g.numel() for g in grads])
+    outs = scale = None
     if out is not None:
-        if len(out) != n:
-            raise ValueError("out must hold one tensor per gradient")
-        for i, (g, o) in enumerate(zip(grads, out)):
-            outs[i] = _result(o, g.shape, g.dtype, g.device).data_ptr()
-    dev = grads[0].device
+        outs, out_types = _tensors(out, "out", at)
+        if out_types != types or [o.shape for o in out] != [g.shape for g in grads]:
+            raise ValueError("out must hold one tensor like each gradient")
+        scale = _empty(1, dtype=torch.float32, device=dev)
     norm = _result(norm, (1,), torch.float32, dev)
-    scale = _result(scale, (1,), torch.float32, dev) if want_scale else None
     L = _lib or lib()
     need = L.fp8q_clip_grads_workspace_bytes(n)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    st = L.fp8q_clip_grads(ptrs, sizes, dts, n, max_norm, outs, norm.data_ptr(), _ptr(scale), ws.data_ptr(), need, _stream(at))
+    ws = _empty(need, dtype=torch.uint8, device=dev)
+    st = L.fp8q_clip_grads(ptrs.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0], n, max_norm,
+                           None if outs is None else outs.buffer_info()[0], norm.data_ptr(), _ptr(scale), ws.data_ptr(), need,
+                           _stream(at))
     if st:
         _check(st, "fp8q_clip_grads")
     return norm, scale
@@ -1197,7 +1206,7 @@ def _clip(grads, max_norm: float, out, want_scale: bool, norm, scale):
 
 def fp8q_grad_norm(grads, out: torch.Tensor | None = None) -> torch.Tensor:
     """sqrt of the sum of all squares of the tensors `grads` (BF16 or FP32): float32 [1]."""
-    return _clip(grads, 0.0, None, False, out, None)[0]
+    return _clip(list(grads), 0.0, None, out)[0]
 
 
 def fp8q_clip_grads(grads, max_norm: float, out: list | None = None) -> dict:
@@ -1205,7 +1214,7 @@ def fp8q_clip_grads(grads, max_norm: float, out: list | None = None) -> dict:
     float32 [1], grads: a tensor like each).  `out` holds the tensors to write; `grads` itself clips in place."""
     grads = list(grads)
     out = [torch.empty_like(g) for g in grads] if out is None else list(out)
-    norm, scale = _clip(grads, max_norm, out, True, None, None)
+    norm, scale = _clip(grads, max_norm, out, None)
     return {"norm": norm, "scale": scale, "grads": out}
 
 

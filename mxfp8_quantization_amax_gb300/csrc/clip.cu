@@ -7,7 +7,9 @@
 // The tensors of a launch come as a table in the kernel's parameters, cut into
 // pieces of 32 KB; a CTA takes pieces by index, so that every sum has a fixed
 // order.  Squares are added in FP32 over at most 64 values of a thread, then in
-// FP64: across pieces, CTAs and launches.
+// FP64: across pieces, CTAs and launches.  The CTAs that write add the partial
+// sums up themselves, all in the same order, and take the pieces from the last
+// on: those are still in L2.
 #include <math.h>
 
 #include "quant_tile.cuh"
@@ -27,6 +29,7 @@ struct ClTable {
   int first[kClTensors + 1];  // first piece of each tensor
   uint8_t wide[kClTensors];   // type | aligned << 1
   int tensors;
+  bool in_place;              // every tensor is its own output
 };
 
 struct ClPiece {
@@ -113,20 +116,26 @@ __global__ void __launch_bounds__(kClThreads) clip_norm_kernel(const __grid_cons
   pdl_launch_dependents();
 }
 
+// Every thread of the CTA gets the norm.
+__device__ __forceinline__ float cl_norm(const double* part, int parts, double* sh) {
+  double sum = 0.0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < parts; i += kClThreads) sum += __ldg(part + i);
+  return (float)sqrt(cl_block_sum(sum, sh));
+}
+__device__ __forceinline__ float cl_scale(float norm, float max_norm) {
+  const float s = __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f));
+  return s > 1.0f ? 1.0f : s;  // NaN stays
+}
+
 __global__ void __launch_bounds__(kClThreads) clip_scale_kernel(const double* part, int parts, float max_norm, float* norm,
                                                                  float* scale) {
   __shared__ double sh[kClThreads / 32];
   pdl_wait();
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kClThreads) sum += part[i];
-  sum = cl_block_sum(sum, sh);
+  const float n = cl_norm(part, parts, sh);
   if (threadIdx.x == 0) {
-    const float n = (float)sqrt(sum);
     *norm = n;
-    if (scale != nullptr) {
-      const float s = __fdiv_rn(max_norm, __fadd_rn(n, 1e-6f));
-      *scale = s > 1.0f ? 1.0f : s;  // NaN stays
-    }
+    if (scale != nullptr) *scale = cl_scale(n, max_norm);
   }
   pdl_launch_dependents();
 }
@@ -169,14 +178,25 @@ __device__ __forceinline__ void cl_write(const ClPiece& p, float scale) {
 }
 
 // In place a scale of 1 leaves nothing to do (NaN payloads apart).
-__global__ void __launch_bounds__(kClThreads) clip_write_kernel(const __grid_constant__ ClTable t, const float* scale_at) {
+__global__ void __launch_bounds__(kClThreads) clip_write_kernel(const __grid_constant__ ClTable t, const double* part, int parts,
+                                                                 float max_norm, float* norm, float* scale_at, bool first) {
+  __shared__ double sh[kClThreads / 32];
   pdl_wait();
-  const float scale = *scale_at;
-  for (int i = blockIdx.x; i < t.first[t.tensors]; i += gridDim.x) {
-    const ClPiece p = cl_piece(t, i);
-    if (scale == 1.0f && p.g == p.out) continue;
-    if (p.type == kBF16) cl_write<kBF16>(p, scale);
-    else cl_write<kFP32>(p, scale);
+  float scale;
+  if (parts > 0) {
+    const float n = cl_norm(part, parts, sh);
+    scale = cl_scale(n, max_norm);
+    if (first && blockIdx.x == 0 && threadIdx.x == 0) *norm = n, *scale_at = scale;
+  } else {
+    scale = *scale_at;
+  }
+  if (!(t.in_place && scale == 1.0f)) {
+    for (int i = t.first[t.tensors] - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
+      const ClPiece p = cl_piece(t, i);
+      if (scale == 1.0f && p.g == p.out) continue;
+      if (p.type == kBF16) cl_write<kBF16>(p, scale);
+      else cl_write<kFP32>(p, scale);
+    }
   }
   pdl_launch_dependents();
 }
@@ -194,6 +214,7 @@ struct ClWalk {
     if (at >= count) return false;
     t->tensors = 0;
     t->first[0] = 0;
+    t->in_place = true;
     for (; at < count && t->tensors < kClTensors; at++) {
       if (n[at] == 0) continue;
       const int i = t->tensors;
@@ -201,6 +222,7 @@ struct ClWalk {
       t->g[i] = g[at];
       t->out[i] = out ? out[at] : nullptr;
       t->n[i] = n[at];
+      t->in_place = t->in_place && t->g[i] == t->out[i];
       t->wide[i] = (uint8_t)(dt[at] | (off(g[at], 16) || (out && off(out[at], 16)) ? 0 : 2));
       t->first[i + 1] = t->first[i] + (int)pieces;
       t->tensors++;
@@ -251,12 +273,18 @@ extern "C" fp8q_status fp8q_clip_grads(const void* const* grads, const int64_t* 
     if (e != cudaSuccess) return cuda_fail(e, "clip norm launch");
     parts += grid;
   }
-  e = launch_kernel(clip_scale_kernel, dim3(1), dim3(kClThreads), 0, s, (const double*)workspace, parts, max_norm, norm, scale);
-  if (e != cudaSuccess) return cuda_fail(e, "clip scale launch");
+  // up to this many partial sums every writing CTA adds up (10 us for all of them)
+  const bool apart = !out || parts == 0 || parts > 4 * kClParts;
+  if (apart) {
+    e = launch_kernel(clip_scale_kernel, dim3(1), dim3(kClThreads), 0, s, (const double*)workspace, parts, max_norm, norm, scale);
+    if (e != cudaSuccess) return cuda_fail(e, "clip scale launch");
+  }
   if (out) {
-    for (ClWalk w{grads, out, sizes, dts, count, 0}; w.next(&t);) {
+    bool first = true;
+    for (ClWalk w{grads, out, sizes, dts, count, 0}; w.next(&t); first = false) {
       const int grid = t.first[t.tensors] < most ? t.first[t.tensors] : most;
-      e = launch_kernel(clip_write_kernel, dim3(grid), dim3(kClThreads), 0, s, t, (const float*)scale);
+      e = launch_kernel(clip_write_kernel, dim3(grid), dim3(kClThreads), 0, s, t, (const double*)workspace, apart ? 0 : parts, max_norm, norm,
+                        scale, first);
       if (e != cudaSuccess) return cuda_fail(e, "clip write launch");
     }
   }

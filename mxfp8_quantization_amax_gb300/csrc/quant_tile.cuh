@@ -231,6 +231,7 @@ struct QtOut {
   // the two halves of the columns have the same inputs (with cols / 2 a multiple of 128 one CTA makes both
   // tiles of them; else tile columns are taken in the order 0, half, 1, half + 1, ...)
   int halves;
+  int backwards;  // the last rows first: those that the kernel before wrote last
   void* dense;  // the values in the source's type, or NULL
   uint8_t* q;   // row copy, or NULL
   float* s;
@@ -291,6 +292,7 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
   const auto place_of = [&](int item, int& tr, int& tc) {
     tr = item / items_c;
     tc = item - tr * items_c;
+    if (o.backwards) tr = o.tiles_r - 1 - tr;
     if (o.halves && !pair) tc = (tc & 1) ? (items_c + 1) / 2 + tc / 2 : tc / 2;
   };
   const auto ask = [&](int tr, int tc) {

@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_k
 // Any columns and alignment: value by value, N of them a thread in registers, or
 // (N = 0) any number, read twice, with the columns' sums in shared memory.
 template <int DT, int HT, int N>
-__global__ void __launch_bounds__(512) rmsnorm_backward_any_kernel(RmsNormBackward p) {
+__global__ void __launch_bounds__(1024) rmsnorm_backward_any_kernel(RmsNormBackward p) {
   extern __shared__ float acc_sh[];
   __shared__ float sh[64];
   constexpr int M = N > 0 ? N : 1;
@@ -598,7 +598,7 @@ template <int DT, int HT>
 static cudaError_t launch_norm_backward(RmsNormBackward& p, bool vec, int* parts, cudaStream_t s) {
   if (vec && p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_backward_vec<DT, HT, kRnThreads>(p, parts, s);
   if (vec && p.cols <= 8 * kRnChunks * 512) return launch_norm_backward_vec<DT, HT, 512>(p, parts, s);
-  return p.cols <= 512 * 16 ? launch_norm_backward_any<DT, HT, 16>(p, parts, s) : launch_norm_backward_any<DT, HT, 0>(p, parts, s);
+  return p.cols <= 1024 * 8 ? launch_norm_backward_any<DT, HT, 8>(p, parts, s) : launch_norm_backward_any<DT, HT, 0>(p, parts, s);
 }
 
 }  // namespace fp8q
@@ -661,6 +661,7 @@ extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* resid
     o.tiles_r = (int)tiles_r;
     o.tiles_c = p.tiles_c;
     o.pow2 = p.pow2;
+    o.backwards = 1;
     o.q_t = q_t;
     o.s_t = scale_inv_t;
     const int ht = residual ? residual_dt : dt;
