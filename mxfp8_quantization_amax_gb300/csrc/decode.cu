@@ -34,6 +34,7 @@ constexpr int kMdPitch = 20;                                 // floats of a colu
 constexpr int kMdSetFloats = kMdCols * kMdPitch + 16;        // of a set of 16 rows
 constexpr int kMdRows = 32;                                  // output columns of a CTA of the second kernel
 constexpr int kMdOutPitch = 36;
+constexpr size_t kMdHalfSm = 112 * 1024;                     // shared memory of a CTA of which two fit an SM
 
 struct MdParams {
   const uint16_t* x;  // [tokens][hidden] BF16
@@ -499,15 +500,17 @@ __device__ __forceinline__ void md_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <int FMT, bool LO>
+// STAGES: tiles of a warp's ring.
+template <int FMT, bool LO, int STAGES>
 __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p, int shares) {
-  extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on, then the lists and the sums
-  __shared__ float scales[kMdWarps][kMdStages];
+  constexpr int kRing = STAGES * kMdTileBytes;
+  extern __shared__ uint8_t dynamic[];  // [warps][kRing], from a multiple of 128 on, then the lists and the sums
+  __shared__ float scales[kMdWarps][STAGES];
   __shared__ int warp_sum[kMdWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int row0 = blockIdx.x / shares * kMdRows, rank = blockIdx.x % shares;
   uint8_t* rings = dynamic + (-md_smem(dynamic) & 127u);
-  float* sums = (float*)(rings + kMdWarps * kMdRingBytes);  // [warps][tokens][kMdOutPitch]
+  float* sums = (float*)(rings + kMdWarps * kRing);  // [warps][tokens][kMdOutPitch]
   MdLists l = md_list_places((uint8_t*)(sums + kMdWarps * p.tokens * kMdOutPitch), p.tokens * p.top_k);
   // The first kernel has waited for all before it and writes none of what is
   // read here: only its inner values are waited for below.
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
   const int64_t all = (int64_t)l.jobs * p.kb2;
   const int parts = kMdWarps * shares, part = rank * kMdWarps + warp;
   const int begin = (int)(all * part / parts), end = (int)(all * (part + 1) / parts);
-  const uint32_t ring = md_smem(rings) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0]);
+  const uint32_t ring = md_smem(rings) + warp * kRing, sc_at = md_smem(&scales[warp][0]);
   const uint32_t tile_at = ring + lane * 128 + ((lane & 7) << 4);
   MdPlace at;  // of the inner values asked for last
   at.job = begin / p.kb2;
@@ -528,7 +531,7 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
     md_feed2_job(p, l, row0, f);
   }
 #pragma unroll
-  for (int i = 0; i < kMdStages; i++) md_feed2(p, l, row0, f, ring + i * kMdTileBytes, sc_at + i * 4);
+  for (int i = 0; i < STAGES; i++) md_feed2(p, l, row0, f, ring + i * kMdTileBytes, sc_at + i * 4);
   float* mine = sums + warp * p.tokens * kMdOutPitch;
   for (int i = lane; i < p.tokens * kMdOutPitch; i += 32) mine[i] = 0.0f;
   __syncwarp();
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
       if (last) at.at_job(l);
       next.load(p, at);
     }
-    md_wait<kMdStages - 1>();
+    md_wait<STAGES - 1>();
     __syncwarp();
     const float sc = scales[warp][stage];
 #pragma unroll
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
     }
     __syncwarp();  // all lanes have their codes
     md_feed2(p, l, row0, f, ring + stage * kMdTileBytes, sc_at + stage * 4);
-    stage = stage + 1 == kMdStages ? 0 : stage + 1;
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
     if (last || left == 1) {  // on to another job: its tokens' sums leave the registers
 #pragma unroll
       for (int c = 0; c < 2; c++) {
@@ -649,28 +652,38 @@ static size_t decode_workspace(int64_t pairs, int64_t inner) {
   return (size_t)(pairs * kb2 * (2 * 2 * 128 + 4 * 4));
 }
 
+// The second kernel with STAGES tiles a warp on their way.
+template <int FMT, bool LO, int STAGES>
+static cudaError_t launch_second(const MdParams& p, cudaStream_t s) {
+  constexpr size_t kRings = (size_t)kMdWarps * STAGES * kMdTileBytes + 128, kSums = (size_t)kMdWarps * kMdOutPitch * sizeof(float);
+  const size_t smem = kRings + md_list_bytes(p.tokens * p.top_k) + p.tokens * kSums;
+  static PerDevice<bool> allowed;
+  const cudaError_t e = allow_smem(allowed, decode_second_kernel<FMT, LO, STAGES>, kRings + md_list_bytes(kMdPairs) + kMdTokens * kSums);
+  if (e != cudaSuccess) return e;
+  // CTAs of one column tile: as many as there is room for side by side
+  const int tiles = (p.hidden + kMdRows - 1) / kMdRows;
+  const int room = (smem > kMdHalfSm ? 1 : 2) * sm_count();
+  int shares = 1;
+  while (shares < 8 && tiles * 2 * shares <= room) shares *= 2;
+  return launch_cluster(decode_second_kernel<FMT, LO, STAGES>, dim3((unsigned)(tiles * shares)), dim3(kMdThreads), shares, smem, s, p, shares);
+}
+
 template <int FMT, bool LO>
 static fp8q_status launch_decode(const MdParams& p, cudaStream_t s) {
   const int slots = p.tokens * p.top_k;
-  const size_t rings = (size_t)kMdWarps * kMdRingBytes + 128, first_smem = rings + md_list_bytes(slots);
-  const size_t second_smem = first_smem + (size_t)kMdWarps * p.tokens * kMdOutPitch * sizeof(float);
-  constexpr size_t kMost = (size_t)kMdWarps * kMdRingBytes + 128 + md_list_bytes(kMdPairs) + (size_t)kMdWarps * kMdTokens * kMdOutPitch * sizeof(float);
-  static PerDevice<bool> allowed[2];
-  cudaError_t e = allow_smem(allowed[0], decode_first_kernel<FMT>, rings + md_list_bytes(kMdPairs));
-  if (e == cudaSuccess) e = allow_smem(allowed[1], decode_second_kernel<FMT, LO>, kMost);
+  constexpr size_t kRings = (size_t)kMdWarps * kMdRingBytes + 128;
+  static PerDevice<bool> allowed;
+  cudaError_t e = allow_smem(allowed, decode_first_kernel<FMT>, kRings + md_list_bytes(kMdPairs));
   if (e != cudaSuccess) return cuda_fail(e, "decode shared memory");
   // at most this many units; two CTAs an SM have room
   int64_t units = (int64_t)(slots < p.experts ? slots : p.experts + slots / kMdCols) * p.kb2 * (128 / kMdUnit);
   const int64_t fit = 2 * (int64_t)sm_count();
   if (units > fit) units = fit;
-  e = launch_kernel(decode_first_kernel<FMT>, dim3((unsigned)units), dim3(kMdThreads), first_smem, s, p);
+  e = launch_kernel(decode_first_kernel<FMT>, dim3((unsigned)units), dim3(kMdThreads), kRings + md_list_bytes(slots), s, p);
   if (e != cudaSuccess) return cuda_fail(e, "decode first kernel launch");
-  // CTAs of one column tile: as many as there is room for side by side
-  const int tiles = (p.hidden + kMdRows - 1) / kMdRows;
-  const int64_t room = second_smem > 112 * 1024 ? sm_count() : fit;
-  int shares = 1;
-  while (shares < 8 && tiles * 2 * shares <= room) shares *= 2;
-  e = launch_cluster(decode_second_kernel<FMT, LO>, dim3((unsigned)(tiles * shares)), dim3(kMdThreads), shares, second_smem, s, p, shares);
+  // two CTAs an SM matter more than a second tile of each warp on its way
+  const size_t smem = kRings + md_list_bytes(slots) + (size_t)kMdWarps * p.tokens * kMdOutPitch * sizeof(float);
+  e = smem <= kMdHalfSm ? launch_second<FMT, LO, 2>(p, s) : launch_second<FMT, LO, 1>(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode second kernel launch");
   return check_launch("decode kernel");
 }
