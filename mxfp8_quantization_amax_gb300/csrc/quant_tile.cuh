@@ -228,9 +228,6 @@ struct QtOut {
   int64_t rows, cols;  // of the quantized matrix
   int tiles_r, tiles_c;
   int pow2;
-  // the two halves of the columns have the same inputs (with cols / 2 a multiple of 128 one CTA makes both
-  // tiles of them; else tile columns are taken in the order 0, half, 1, half + 1, ...)
-  int halves;
   int backwards;  // the last rows first: those that the kernel before wrote last
   void* dense;  // the values in the source's type, or NULL
   uint8_t* q;   // row copy, or NULL
@@ -241,33 +238,32 @@ struct QtOut {
 
 // A source gives 8 values of a row (rows come in multiples of 16, columns too)
 // from kInputs runs of 8 inputs of type kType, which is the dense output's too:
-//   bool needs(int input, int64_t col) const;
-//   const void* at(int input, int64_t row, int64_t col) const;
-//   void begin(int64_t row, int64_t col);                   // of kQtRows rows
-//   void values(const QtRaw<kType, 8> (&in)[kInputs], int i, int64_t col, float (&v)[8]) const;   // of row + i
+//   bool needs(int input, int col) const;
+//   const void* at(int input, int row, int col) const;
+//   int pitch(int input) const;                             // values from a row to the next
+//   void begin(int row, int col);                           // of kQtRows rows
+//   void values(const QtRaw<kType, 8> (&in)[kInputs], int i, int col, float (&v)[8]) const;   // of row + i
+// and, where both halves of the columns have the same inputs (kHalves),
+//   void both(const QtRaw<kType, 8> (&in)[kInputs], float (&first)[8], float (&second)[8]) const;
 template <class Src>
 constexpr size_t kQtSmem = (size_t)kQtRows * Src::kInputs * kQtThreads * kQtRunBytes<Src::kType>;
 
 // What a half-warp asks for: its rows' values from column col on.
 template <class Src>
-__device__ __forceinline__ void qt_ask_tile(const Src& src, int64_t row, int64_t col, int64_t cols, bool there, uint32_t place, int hl) {
+__device__ __forceinline__ void qt_ask_tile(const Src& src, int row, int col, int cols, bool there, uint32_t place, int hl) {
+  constexpr int kSize = Src::kType == kBF16 ? 2 : 4, kRun = kQtRunBytes<Src::kType>;
   if (there) {
 #pragma unroll
     for (int n = 0; n < Src::kInputs; n++) {
 #pragma unroll
-      for (int i = 0; i < kQtRows; i++) {
+      for (int k = 0; k < kRun / 16; k++) {
         // (a half-warp's columns may lie in two halves with different inputs: each lane asks for its own then)
-        if constexpr (Src::kType == kBF16) {
-          const int64_t c = col + 8 * hl;
-          if (c < cols && src.needs(n, c))
-            qt_ask(place + (i * Src::kInputs + n) * kQtThreads * 16 + hl * 16, src.at(n, row + i, c));
-        } else {
+        const int c = col + (k * 16 + hl) * (16 / kSize);
+        if (c < cols && src.needs(n, c)) {
+          const uint8_t* from = (const uint8_t*)src.at(n, row, c);
+          const int64_t pitch = (int64_t)src.pitch(n) * kSize;
 #pragma unroll
-          for (int k = 0; k < 2; k++) {
-            const int64_t c = col + 4 * (k * 16 + hl);
-            if (c < cols && src.needs(n, c))
-              qt_ask(place + (i * Src::kInputs + n) * kQtThreads * 32 + (k * 16 + hl) * 16, src.at(n, row + i, c));
-          }
+          for (int i = 0; i < kQtRows; i++) qt_ask(place + (i * Src::kInputs + n) * kQtThreads * kRun + (k * 16 + hl) * 16, from + i * pitch);
         }
       }
     }
@@ -276,58 +272,82 @@ __device__ __forceinline__ void qt_ask_tile(const Src& src, int64_t row, int64_t
 }
 
 // Persistent: the inputs of a CTA's next tile come while it works on this one.
-template <class Src, int FMT, bool ROW>
+// PAIR: the tiles of both halves come from one set of inputs; the second half's
+// values wait where its inputs were.
+template <class Src, int FMT, bool ROW, bool PAIR>
 __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOut o) {
   extern __shared__ __align__(16) uint8_t inputs[];  // [rows of a thread][inputs][threads] of 8 values
   __shared__ float scale[kQtTile];
   __shared__ __align__(16) uint8_t stage[kQtTile * 128];  // codes of the transposed tile; the warps' column maxima before
   float(*part)[kQtTile] = (float(*)[kQtTile])stage;
-  const int tid = threadIdx.x, lane = tid & 31, hl = tid & 15, ty = tid >> 4;
-  const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + ty * 16 * kQtRunBytes<Src::kType>;  // of the half-warp
-  const bool pair = o.halves && o.cols % (2 * kQtTile) == 0;
-  const int items_c = pair ? o.tiles_c / 2 : o.tiles_c, items = o.tiles_r * items_c;
-  const int64_t cols = pair ? o.cols / 2 : o.cols;
-  const bool wide = o.rows % 32 == 0 && ((uintptr_t)o.q_t & 31) == 0;
+  constexpr int kRun = kQtRunBytes<Src::kType>;
+  const int tid = threadIdx.x, lane = tid & 31, hl = tid & 15, ty = tid >> 4, all_rows = (int)o.rows, all_cols = (int)o.cols;
+  const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + ty * 16 * kRun;  // of the half-warp
+  const int items_c = PAIR ? o.tiles_c / 2 : o.tiles_c, items = o.tiles_r * items_c, cols = PAIR ? all_cols / 2 : all_cols;
+  const bool wide = all_rows % 32 == 0 && ((uintptr_t)o.q_t & 31) == 0;
   pdl_wait();
   const auto place_of = [&](int item, int& tr, int& tc) {
     tr = item / items_c;
     tc = item - tr * items_c;
     if (o.backwards) tr = o.tiles_r - 1 - tr;
-    if (o.halves && !pair) tc = (tc & 1) ? (items_c + 1) / 2 + tc / 2 : tc / 2;
+    if (Src::kHalves && !PAIR) tc = (tc & 1) ? (items_c + 1) / 2 + tc / 2 : tc / 2;
   };
   const auto ask = [&](int tr, int tc) {
-    const int64_t row = (int64_t)tr * kQtTile + ty * kQtRows;
-    qt_ask_tile(src, row, (int64_t)tc * kQtTile, cols, row < o.rows, place, hl);
+    const int row = tr * kQtTile + ty * kQtRows;
+    qt_ask_tile(src, row, tc * kQtTile, cols, row < all_rows, place, hl);
+  };
+  // where the second half's values of row i wait: 32 bytes of the thread's own
+  const auto waits = [&](int i, int k) {
+    return kRun == 32 ? place + i * Src::kInputs * kQtThreads * 32 + hl * 32 + k * 16 : place + (i * Src::kInputs + k) * kQtThreads * 16 + hl * 16;
   };
   int tr, tc, half = 0, item = blockIdx.x;
   place_of(item, tr, tc);
   ask(tr, tc);
   while (item < items) {
     const int this_r = tr, this_c = tc + half * items_c;
-    const int64_t rt = (int64_t)tr * kQtTile, r0 = rt + ty * kQtRows, c0 = (int64_t)this_c * kQtTile, c = c0 + hl * 8;
-    const bool there = c < o.cols && r0 < o.rows;
+    const int rt = tr * kQtTile, r0 = rt + ty * kQtRows, c0 = this_c * kQtTile, c = c0 + hl * 8;
+    const bool there = c < all_cols && r0 < all_rows;
     float v[kQtRows][8];
     if (there) src.begin(r0, c);
-    qt_wait<0>();
-    __syncwarp();
-    if (there) {
+    if (!PAIR || half == 0) {
+      qt_wait<0>();
+      __syncwarp();
+      if (there) {
+#pragma unroll
+        for (int i = 0; i < kQtRows; i++) {
+          QtRaw<Src::kType, 8> in[Src::kInputs];
+#pragma unroll
+          for (int n = 0; n < Src::kInputs; n++)
+            if (PAIR || src.needs(n, c)) qt_taken8<Src::kType>(place + (i * Src::kInputs + n) * kQtThreads * kRun, hl, in[n]);
+          if constexpr (PAIR) {
+            float second[8];
+            src.both(in, v[i], second);
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(waits(i, k)), "f"(second[4 * k]), "f"(second[4 * k + 1]),
+                           "f"(second[4 * k + 2]), "f"(second[4 * k + 3])
+                           : "memory");
+          } else {
+            src.values(in, i, c, v[i]);
+          }
+        }
+      }
+    } else if (there) {
 #pragma unroll
       for (int i = 0; i < kQtRows; i++) {
-        QtRaw<Src::kType, 8> in[Src::kInputs];
-#pragma unroll
-        for (int n = 0; n < Src::kInputs; n++) {
-          if (src.needs(n, c)) qt_taken8<Src::kType>(place + (i * Src::kInputs + n) * kQtThreads * kQtRunBytes<Src::kType>, hl, in[n]);
-        }
-        src.values(in, i, c, v[i]);
+        const uint4 a = qt_taken(waits(i, 0)), b = qt_taken(waits(i, 1));
+        v[i][0] = __uint_as_float(a.x), v[i][1] = __uint_as_float(a.y), v[i][2] = __uint_as_float(a.z), v[i][3] = __uint_as_float(a.w);
+        v[i][4] = __uint_as_float(b.x), v[i][5] = __uint_as_float(b.y), v[i][6] = __uint_as_float(b.z), v[i][7] = __uint_as_float(b.w);
       }
-    } else {
+    }
+    if (!there) {
 #pragma unroll
       for (int i = 0; i < kQtRows; i++)
 #pragma unroll
         for (int k = 0; k < 8; k++) v[i][k] = 0.0f;
     }
     __syncwarp();
-    if (pair && half == 0) {
+    if (PAIR && half == 0) {
       half = 1;
     } else {
       half = 0;
@@ -357,7 +377,7 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
     }
     if (o.dense != nullptr && there) {
 #pragma unroll
-      for (int i = 0; i < kQtRows; i++) qt_store<Src::kType, 8>(o.dense, (r0 + i) * o.cols + c, v[i]);
+      for (int i = 0; i < kQtRows; i++) qt_store<Src::kType, 8>(o.dense, (int64_t)(r0 + i) * all_cols + c, v[i]);
     }
     __syncthreads();
     if (tid < kQtTile) {
@@ -366,13 +386,14 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
       for (int w = 1; w < kQtThreads / 32; w++) m = qt_max(m, part[w][tid]);
       const float s = qt_scale<FMT>(m, o.pow2);
       scale[tid] = s;
-      if (c0 + tid < o.cols) o.s_t[(c0 + tid) * o.tiles_r + this_r] = __frcp_rn(s);
+      if (c0 + tid < all_cols) o.s_t[(int64_t)(c0 + tid) * o.tiles_r + this_r] = __frcp_rn(s);
     }
     if constexpr (ROW) {
-      uint8_t* to = o.q + r0 * o.cols + c;
-      float* scale_to = o.s + r0 * o.tiles_c + this_c;
+      uint8_t* to = o.q + (int64_t)r0 * all_cols + c;
+      float* scale_to = o.s + (int64_t)r0 * o.tiles_c + this_c;
       qt_groups<FMT, kQtRows>(
-          v, o.pow2, [&](int i) { return to + i * o.cols; }, [&](int i) { return scale_to + (int64_t)i * o.tiles_c; }, [&](int) { return there; });
+          v, o.pow2, [&](int i) { return to + (int64_t)i * all_cols; }, [&](int i) { return scale_to + (int64_t)i * o.tiles_c; },
+          [&](int) { return there; });
     }
     __syncthreads();
     {
@@ -397,21 +418,21 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
 #pragma unroll
     for (int n = 0; n < 512 / kQtThreads; n++) {  // 32 rows of a column: four threads a column
       const int col = (tid + n * kQtThreads) >> 2, at = tid & 3, flip = col >> 3;
-      const int64_t row = rt + 32 * at;
-      if (c0 + col >= o.cols || row >= o.rows) continue;
+      const int row = rt + 32 * at;
+      if (c0 + col >= all_cols || row >= all_rows) continue;
       uint4 a = *(const uint4*)(stage + col * 128 + (((2 * at) ^ (flip >> 1)) << 4));
       uint4 b = *(const uint4*)(stage + col * 128 + (((2 * at + 1) ^ (flip >> 1)) << 4));
       if (flip & 1) {
         a = make_uint4(a.z, a.w, a.x, a.y);
         b = make_uint4(b.z, b.w, b.x, b.y);
       }
-      uint8_t* to = o.q_t + (c0 + col) * o.rows + row;
+      uint8_t* to = o.q_t + (int64_t)(c0 + col) * all_rows + row;
       if (wide) {
         const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         st32B(to, d);
       } else {
         st_stream(to, a);
-        if (row + 16 < o.rows) st_stream(to + 16, b);
+        if (row + 16 < all_rows) st_stream(to + 16, b);
       }
     }
     __syncthreads();  // the codes have been read
@@ -419,18 +440,23 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
   pdl_launch_dependents();
 }
 
-template <class Src, int FMT, bool ROW>
-cudaError_t launch_quant_tiles_row(const Src& src, const QtOut& o, cudaStream_t s) {
+template <class Src, int FMT, bool ROW, bool PAIR>
+cudaError_t launch_quant_tiles_t(const Src& src, const QtOut& o, cudaStream_t s) {
   static PerDevice<bool> allowed;
-  const cudaError_t e = allow_smem(allowed, quant_tile_kernel<Src, FMT, ROW>, kQtSmem<Src>);
+  const cudaError_t e = allow_smem(allowed, quant_tile_kernel<Src, FMT, ROW, PAIR>, kQtSmem<Src>);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)o.tiles_r * o.tiles_c / (o.halves && o.cols % (2 * kQtTile) == 0 ? 2 : 1), fit = (kQtSmem<Src> > 96 * 1024 ? 1 : 2) * (int64_t)sm_count();
-  return launch_kernel(quant_tile_kernel<Src, FMT, ROW>, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kQtThreads), kQtSmem<Src>, s, src, o);
+  const int64_t tiles = (int64_t)o.tiles_r * o.tiles_c / (PAIR ? 2 : 1), fit = (kQtSmem<Src> > 96 * 1024 ? 1 : 2) * (int64_t)sm_count();
+  return launch_kernel(quant_tile_kernel<Src, FMT, ROW, PAIR>, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kQtThreads), kQtSmem<Src>, s, src, o);
 }
 
+// Halves with the same inputs: where they are whole tiles one CTA makes both
+// tiles of them; else tile columns are taken in the order 0, half, 1, half + 1, ...
 template <class Src, int FMT>
 cudaError_t launch_quant_tiles(const Src& src, const QtOut& o, cudaStream_t s) {
-  return o.q ? launch_quant_tiles_row<Src, FMT, true>(src, o, s) : launch_quant_tiles_row<Src, FMT, false>(src, o, s);
+  if constexpr (Src::kHalves) {
+    if (o.cols % (2 * kQtTile) == 0) return o.q ? launch_quant_tiles_t<Src, FMT, true, true>(src, o, s) : launch_quant_tiles_t<Src, FMT, false, true>(src, o, s);
+  }
+  return o.q ? launch_quant_tiles_t<Src, FMT, true, false>(src, o, s) : launch_quant_tiles_t<Src, FMT, false, false>(src, o, s);
 }
 
 // Checks of the copies' arguments, for cols columns.

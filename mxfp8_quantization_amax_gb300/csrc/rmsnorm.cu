@@ -246,16 +246,18 @@ struct RmsNormTile {
   int64_t cols;
   float s[kQtRows], w[8];
   static constexpr int kInputs = 1;
-  __device__ __forceinline__ bool needs(int, int64_t) const { return true; }
-  __device__ __forceinline__ const void* at(int, int64_t row, int64_t col) const {
+  static constexpr bool kHalves = false;
+  __device__ __forceinline__ bool needs(int, int) const { return true; }
+  __device__ __forceinline__ const void* at(int, int row, int col) const {
     return (const uint8_t*)h + (row * cols + col) * (DT == kBF16 ? 2 : 4);
   }
-  __device__ __forceinline__ void begin(int64_t row, int64_t col) {
+  __device__ __forceinline__ int pitch(int) const { return (int)cols; }
+  __device__ __forceinline__ void begin(int row, int col) {
 #pragma unroll
     for (int i = 0; i < kQtRows; i++) s[i] = __ldg(rstd + row + i);
     rn_weight<8>(weight, weight_dt, col, w);
   }
-  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[1], int i, int64_t, float (&v)[8]) const {
+  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[1], int i, int, float (&v)[8]) const {
     in[0].get(v);
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {

@@ -129,12 +129,13 @@ struct SwigluForward {
   }
   static constexpr int kInputs = 2;
   static constexpr bool kHalves = false;
-  __device__ __forceinline__ bool needs(int, int64_t) const { return true; }
-  __device__ __forceinline__ const void* at(int n, int64_t row, int64_t col) const {
+  __device__ __forceinline__ bool needs(int, int) const { return true; }
+  __device__ __forceinline__ const void* at(int n, int row, int col) const {
     return (const uint8_t*)h + (row * 2 * inner + n * inner + col) * (DT == kBF16 ? 2 : 4);
   }
-  __device__ __forceinline__ void begin(int64_t, int64_t) {}
-  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[2], int, int64_t, float (&v)[8]) const { values<8>(in[0], in[1], v); }
+  __device__ __forceinline__ int pitch(int) const { return (int)(2 * inner); }
+  __device__ __forceinline__ void begin(int, int) {}
+  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[2], int, int, float (&v)[8]) const { values<8>(in[0], in[1], v); }
   template <int V>
   static __device__ __forceinline__ void values(const QtRaw<DT, V>& g, const QtRaw<DT, V>& u, float (&a)[V]) {
 #pragma unroll
@@ -167,24 +168,29 @@ struct SwigluBackward {
   }
   static constexpr int kInputs = 3;
   static constexpr bool kHalves = true;
-  __device__ __forceinline__ bool needs(int n, int64_t col) const { return n != 1 || col < inner; }
-  __device__ __forceinline__ const void* at(int n, int64_t row, int64_t col) const {
+  __device__ __forceinline__ bool needs(int n, int col) const { return n != 1 || col < inner; }
+  __device__ __forceinline__ const void* at(int n, int row, int col) const {
     const int64_t j = col >= inner ? col - inner : col, size = DT == kBF16 ? 2 : 4;
     return n == 2 ? (const uint8_t*)d_a + (row * inner + j) * size : (const uint8_t*)h + (row * 2 * inner + n * inner + j) * size;
   }
-  __device__ __forceinline__ void begin(int64_t, int64_t) {}
-  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[3], int, int64_t col, float (&v)[8]) const {
+  __device__ __forceinline__ int pitch(int n) const { return (int)(n == 2 ? inner : 2 * inner); }
+  __device__ __forceinline__ void begin(int, int) {}
+  __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[3], int, int col, float (&v)[8]) const {
     if (col >= inner) values<true, 8>(in[0], in[0], in[2], v);
     else values<false, 8>(in[0], in[1], in[2], v);
   }
-  // both halves of a row's columns c, c + 1, ... of 8
-  __device__ __forceinline__ void both(float (&o_g)[8], float (&o_u)[8], int64_t r, int64_t c) const {
-    QtRaw<DT, 8> g, u, d;
-    g.load(h, r * 2 * inner + c);
-    u.load(h, r * 2 * inner + inner + c);
-    d.load(d_a, r * inner + c);
+  static __device__ __forceinline__ void both(const QtRaw<DT, 8> (&in)[3], float (&o_g)[8], float (&o_u)[8]) {
 #pragma unroll
-    for (int k = 0; k < 4; k++) sg_both<DT>(g.pair(k), u.pair(k), d.pair(k), o_g[2 * k], o_g[2 * k + 1], o_u[2 * k], o_u[2 * k + 1]);
+    for (int k = 0; k < 4; k++)
+      sg_both<DT>(in[0].pair(k), in[1].pair(k), in[2].pair(k), o_g[2 * k], o_g[2 * k + 1], o_u[2 * k], o_u[2 * k + 1]);
+  }
+  // both halves of a row's columns c .. c + 7
+  __device__ __forceinline__ void row_both(float (&o_g)[8], float (&o_u)[8], int64_t r, int64_t c) const {
+    QtRaw<DT, 8> in[3];
+    in[0].load(h, r * 2 * inner + c);
+    in[1].load(h, r * 2 * inner + inner + c);
+    in[2].load(d_a, r * inner + c);
+    both(in, o_g, o_u);
   }
   template <bool UP, int V>
   static __device__ __forceinline__ void values(const QtRaw<DT, V>& g, const QtRaw<DT, V>& u, const QtRaw<DT, V>& d, float (&o)[V]) {
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(kSgThreads) swiglu_rows_kernel(Src src, QtOut 
 #pragma unroll
   for (int i = 0; i < kRows; i++) {
     if (!there(i)) continue;
-    if constexpr (PAIR) src.both(v[i], v[kRows + i], r0 + i, c);
+    if constexpr (PAIR) src.row_both(v[i], v[kRows + i], r0 + i, c);
     else src.template row<V>(v[i], r0 + i, c);
   }
   if constexpr (V == 8) {
@@ -299,7 +305,6 @@ static fp8q_status swiglu(const void* h, const void* d_a, bool backward, int32_t
   o.tiles_r = (int)tiles_r;
   o.tiles_c = (int)tiles_c;
   o.pow2 = pow2 ? 1 : 0;
-  o.halves = backward;
   o.dense = dense;
   if (dir & MXFP8_ROW) o.q = q, o.s = s;
   if (dir & MXFP8_COL) o.q_t = q_t, o.s_t = s_t;
