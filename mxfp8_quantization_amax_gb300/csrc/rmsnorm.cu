@@ -109,8 +109,15 @@ __device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64
     if (!row_ok || (n * p.lanes + t) * V >= p.cols) continue;
     float w[V];
     weight(n, w);
+    if constexpr (V == 8) {
 #pragma unroll
-    for (int k = 0; k < V; k++) v[n][k] = __fmul_rn(__fmul_rn(v[n][k], rstd), w[k]);
+      for (int k = 0; k < V; k += 2) {
+        mul2(v[n][k], v[n][k + 1], rstd, rstd);
+        mul2(v[n][k], v[n][k + 1], w[k], w[k + 1]);
+      }
+    } else {
+      v[n][0] = __fmul_rn(__fmul_rn(v[n][0], rstd), w[0]);
+    }
   }
   if constexpr (V == 8) {
     if (p.q != nullptr) {  // 16 threads hold a group of 128 columns, N of them
@@ -285,27 +292,27 @@ struct RmsNormBackward {
 };
 
 // The sums of the CTA's groups of threads, in their order, as one row of partial sums.
-template <int V, int N>
-__device__ __forceinline__ void rn_partial(const RmsNormBackward& p, const float (&acc)[N][V], int t, int per, float* sh) {
+template <int N>
+__device__ __forceinline__ void rn_partial(const RmsNormBackward& p, const float (&acc)[N][8], int t, int per, float* sh) {
   float* to = p.partial + (int64_t)blockIdx.x * p.cols;
   __syncthreads();
-  if (per > 1) {  // p.lanes * V * N values, of which cols are there, for each group
+  if (per > 1) {  // p.lanes * 8 * N values, of which cols are there, for each group
 #pragma unroll
     for (int n = 0; n < N; n++)
 #pragma unroll
-      for (int k = 0; k < V; k++) sh[(threadIdx.x / p.lanes * N + n) * p.lanes * V + t * V + k] = acc[n][k];
+      for (int k = 0; k < 8; k++) sh[(threadIdx.x / p.lanes * N + n) * p.lanes * 8 + t * 8 + k] = acc[n][k];
     __syncthreads();
     for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
       float sum = 0.0f;
-      for (int i = 0; i < per; i++) sum += sh[i * N * p.lanes * V + c];
+      for (int i = 0; i < per; i++) sum += sh[i * N * p.lanes * 8 + c];
       to[c] = sum;
     }
   } else {
 #pragma unroll
     for (int n = 0; n < N; n++)
+      if ((n * p.lanes + t) * 8 < p.cols)
 #pragma unroll
-      for (int k = 0; k < V; k++)
-        if ((n * p.lanes + t) * V + k < p.cols) to[(n * p.lanes + t) * V + k] = acc[n][k];
+        for (int k = 0; k < 8; k++) to[(n * p.lanes + t) * 8 + k] = acc[n][k];
   }
 }
 
@@ -406,94 +413,88 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_k
     ask(r + step, true);
   }
   qt_wait<0>();
-  rn_partial<8, N>(p, acc, t, per, (float*)inputs);
+  rn_partial<N>(p, acc, t, per, (float*)inputs);
   pdl_launch_dependents();
 }
 
-// Any columns and alignment: value by value, N of them a thread in registers, or
-// (N = 0) any number, read twice, with the columns' sums in shared memory.
-template <int DT, int HT, int N>
-__global__ void __launch_bounds__(1024) rmsnorm_backward_any_kernel(RmsNormBackward p) {
-  extern __shared__ float acc_sh[];
+// Any columns and alignment: value by value, kRnBatch of a thread on their way at
+// a time, each row read twice; the columns' sums in shared memory, for each
+// group of threads its own.
+constexpr int kRnBatch = 4;
+constexpr int kRnAnyLanes = 128;
+
+template <int DT, int HT>
+__global__ void __launch_bounds__(kRnThreads) rmsnorm_backward_any_kernel(RmsNormBackward p) {
+  extern __shared__ float acc_sh[];  // [groups of threads][cols]
   __shared__ float sh[64];
-  constexpr int M = N > 0 ? N : 1;
-  const int t = threadIdx.x % p.lanes, per = blockDim.x / p.lanes;
-  const auto value = [&](int64_t at, int64_t c, float rstd, float& d, float& g, float& u) {
-    QtRaw<DT, 1> draw;
-    QtRaw<HT, 1> hraw;
-    float dv[1], hv[1], w[1];
-    draw.load(p.d_y, at);
-    hraw.load(p.h, at);
-    rn_weight<1>(p.weight, p.weight_dt, c, w);
-    draw.get(dv);
-    hraw.get(hv);
-    d = dv[0];
-    g = __fmul_rn(dv[0], w[0]);
-    u = __fmul_rn(hv[0], rstd);
-  };
-  const auto past = [&](int64_t at) {
-    QtRaw<HT, 1> raw;
-    float v[1];
-    rn_load_plain<HT, 1>(p.d_h, at, raw);
-    raw.get(v);
-    return v[0];
-  };
-  const auto store = [&](int64_t at, float rstd, float mean, float g, float u, float add) {
-    float o[1] = {__fmul_rn(rstd, __fmaf_rn(-u, mean, g))};
-    if (p.d_h != nullptr) o[0] = __fadd_rn(o[0], add);
-    qt_store<HT, 1>(p.d_x, at, o);
+  const int t = threadIdx.x % p.lanes, per = blockDim.x / p.lanes, cols = (int)p.cols;
+  float* mine = acc_sh + threadIdx.x / p.lanes * cols;
+  // the row's values of columns c, c + lanes, ...: where nothing is, the first is read
+  const auto values = [&](int64_t row, int c, float rstd, float (&d)[kRnBatch], float (&g)[kRnBatch], float (&u)[kRnBatch]) {
+    QtRaw<DT, 1> draw[kRnBatch];
+    QtRaw<HT, 1> hraw[kRnBatch];
+    float w[kRnBatch][1];
+#pragma unroll
+    for (int i = 0; i < kRnBatch; i++) {
+      const int at = c + i * p.lanes < cols ? c + i * p.lanes : 0;
+      draw[i].load(p.d_y, row + at);
+      hraw[i].load(p.h, row + at);
+      rn_weight<1>(p.weight, p.weight_dt, at, w[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRnBatch; i++) {
+      float v[1];
+      draw[i].get(v);
+      d[i] = v[0];
+      g[i] = __fmul_rn(v[0], w[i][0]);
+      hraw[i].get(v);
+      u[i] = __fmul_rn(v[0], rstd);
+    }
   };
   pdl_wait();
   int turn = 0;
-  float acc[M][1] = {};
-  if (N == 0)
-    for (int64_t c = t; c < p.cols; c += p.lanes) acc_sh[c] = 0.0f;
+  for (int c = t; c < cols; c += p.lanes) mine[c] = 0.0f;
   for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < p.rows; r0 += (int64_t)gridDim.x * per) {
-    const int64_t r = r0 + threadIdx.x / p.lanes, at = r * p.cols;
+    const int64_t r = r0 + threadIdx.x / p.lanes;
     const bool row_ok = r < p.rows;
+    const int64_t row = row_ok ? r * cols : 0;
     const float rstd = row_ok ? __ldg(p.rstd + r) : 0.0f;
-    float sum = 0.0f, g[M], u[M], d;
-    if constexpr (N > 0) {
+    float sum = 0.0f, d[kRnBatch], g[kRnBatch], u[kRnBatch];
+    for (int c = t; c < cols; c += kRnBatch * p.lanes) {
+      values(row, c, rstd, d, g, u);
 #pragma unroll
-      for (int n = 0; n < N; n++) {
-        const int c = n * p.lanes + t;
-        const bool there = row_ok && c < p.cols;  // where nothing is, the first value is read
-        value(there ? at + c : 0, there ? c : 0, rstd, d, g[n], u[n]);
-        if (!there) g[n] = u[n] = d = 0.0f;
-        sum = __fmaf_rn(g[n], u[n], sum);
-        acc[n][0] = __fmaf_rn(d, u[n], acc[n][0]);
-      }
-    } else {
-      for (int64_t c = t; c < p.cols; c += p.lanes) {
-        value(at + c, c, rstd, d, g[0], u[0]);
-        sum = __fmaf_rn(g[0], u[0], sum);
-        acc_sh[c] = __fmaf_rn(d, u[0], acc_sh[c]);
+      for (int i = 0; i < kRnBatch; i++) {
+        if (c + i * p.lanes >= cols || !row_ok) continue;
+        sum = __fmaf_rn(g[i], u[i], sum);
+        mine[c + i * p.lanes] = __fmaf_rn(d[i], u[i], mine[c + i * p.lanes]);
       }
     }
     const float mean = __fmul_rn(rn_row_sum(sum, p.lanes, sh + (turn ^= 32)), p.one_over_cols);
-    if constexpr (N > 0) {
-      float add[M];
+    for (int c = t; c < cols && row_ok; c += kRnBatch * p.lanes) {
+      float past[kRnBatch][1];
+      values(row, c, rstd, d, g, u);
 #pragma unroll
-      for (int n = 0; n < N; n++) {
-        const int c = n * p.lanes + t;
-        add[n] = p.d_h != nullptr ? past(row_ok && c < p.cols ? at + c : 0) : 0.0f;
+      for (int i = 0; i < kRnBatch; i++) {
+        past[i][0] = 0.0f;
+        if (p.d_h != nullptr) {
+          QtRaw<HT, 1> raw;
+          rn_load_plain<HT, 1>(p.d_h, row + (c + i * p.lanes < cols ? c + i * p.lanes : t), raw);
+          raw.get(past[i]);
+        }
       }
 #pragma unroll
-      for (int n = 0; n < N; n++) {
-        const int c = n * p.lanes + t;
-        if (row_ok && c < p.cols) store(at + c, rstd, mean, g[n], u[n], add[n]);
-      }
-    } else {
-      for (int64_t c = t; c < p.cols; c += p.lanes) {
-        value(at + c, c, rstd, d, g[0], u[0]);
-        store(at + c, rstd, mean, g[0], u[0], p.d_h != nullptr ? past(at + c) : 0.0f);
+      for (int i = 0; i < kRnBatch; i++) {
+        float o[1] = {__fmul_rn(rstd, __fmaf_rn(-u[i], mean, g[i]))};
+        if (p.d_h != nullptr) o[0] = __fadd_rn(o[0], past[i][0]);
+        if (c + i * p.lanes < cols) qt_store<HT, 1>(p.d_x, row + c + i * p.lanes, o);
       }
     }
   }
-  if constexpr (N > 0) {
-    rn_partial<1, N>(p, acc, t, per, acc_sh);
-  } else {
-    for (int64_t c = t; c < p.cols; c += p.lanes) p.partial[(int64_t)blockIdx.x * p.cols + c] = acc_sh[c];
+  __syncthreads();
+  for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+    float sum = 0.0f;
+    for (int i = 0; i < per; i++) sum += acc_sh[i * cols + c];
+    p.partial[(int64_t)blockIdx.x * cols + c] = sum;
   }
   pdl_launch_dependents();
 }
@@ -583,24 +584,24 @@ static cudaError_t launch_norm_backward_vec(RmsNormBackward& p, int* parts, cuda
   return launch_kernel(rmsnorm_backward_kernel<DT, HT, T>, dim3((unsigned)grid), dim3(threads), kEach * threads, s, p);
 }
 
-template <int DT, int HT, int N>
+template <int DT, int HT>
 static cudaError_t launch_norm_backward_any(RmsNormBackward& p, int* parts, cudaStream_t s) {
-  p.lanes = N > 0 ? row_lanes(p.cols, 1, N) : 512;
-  const int per = row_groups(p.lanes, kRnThreads), threads = p.lanes * per;
-  const size_t smem = N > 0 ? (size_t)threads * N * sizeof(float) : (size_t)p.cols * sizeof(float);
+  const int per = p.cols <= kRnMaxCols / 4 ? kRnThreads / kRnAnyLanes : 1;
+  p.lanes = kRnThreads / per;
+  const size_t smem = (size_t)per * p.cols * sizeof(float);
   static PerDevice<bool> allowed;
-  const cudaError_t e = allow_smem(allowed, rmsnorm_backward_any_kernel<DT, HT, N>, kRnMaxCols * sizeof(float));
+  const cudaError_t e = allow_smem(allowed, rmsnorm_backward_any_kernel<DT, HT>, kRnMaxCols * sizeof(float));
   if (e != cudaSuccess) return e;
   const int64_t grid = backward_grid(p.rows, per, 4);
   *parts = (int)grid;
-  return launch_kernel(rmsnorm_backward_any_kernel<DT, HT, N>, dim3((unsigned)grid), dim3(threads), smem, s, p);
+  return launch_kernel(rmsnorm_backward_any_kernel<DT, HT>, dim3((unsigned)grid), dim3(kRnThreads), smem, s, p);
 }
 
 template <int DT, int HT>
 static cudaError_t launch_norm_backward(RmsNormBackward& p, bool vec, int* parts, cudaStream_t s) {
   if (vec && p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_backward_vec<DT, HT, kRnThreads>(p, parts, s);
   if (vec && p.cols <= 8 * kRnChunks * 512) return launch_norm_backward_vec<DT, HT, 512>(p, parts, s);
-  return p.cols <= 1024 * 8 ? launch_norm_backward_any<DT, HT, 8>(p, parts, s) : launch_norm_backward_any<DT, HT, 0>(p, parts, s);
+  return launch_norm_backward_any<DT, HT>(p, parts, s);
 }
 
 }  // namespace fp8q
@@ -663,7 +664,6 @@ extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* resid
     o.tiles_r = (int)tiles_r;
     o.tiles_c = p.tiles_c;
     o.pow2 = p.pow2;
-    o.backwards = 1;
     o.q_t = q_t;
     o.s_t = scale_inv_t;
     const int ht = residual ? residual_dt : dt;
