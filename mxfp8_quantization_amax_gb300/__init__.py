@@ -1061,12 +1061,22 @@ def _copies(o: dict, direction: int, rows: int, cols: int, dev):
     """Buffers of the row copy and the transposed copy that `direction` asks for (1x128 groups)."""
     q = si = q_t = si_t = None
     if direction & ROW:
-        q = _result(o.get("q"), (rows, cols), torch.uint8, dev)
-        si = _result(o.get("scale_inv"), (rows, (cols + 127) // 128), torch.float32, dev)
+        shape, groups = (rows, cols), (rows, (cols + 127) // 128)
+        if o:
+            q, si = _result(o.get("q"), shape, torch.uint8, dev), _result(o.get("scale_inv"), groups, torch.float32, dev)
+        else:
+            q, si = _empty(shape, dtype=torch.uint8, device=dev), _empty(groups, dtype=torch.float32, device=dev)
     if direction & COL:
-        q_t = _result(o.get("q_t"), (cols, rows), torch.uint8, dev)
-        si_t = _result(o.get("scale_inv_t"), (cols, (rows + 127) // 128), torch.float32, dev)
+        shape, groups = (cols, rows), (cols, (rows + 127) // 128)
+        if o:
+            q_t, si_t = _result(o.get("q_t"), shape, torch.uint8, dev), _result(o.get("scale_inv_t"), groups, torch.float32, dev)
+        else:
+            q_t, si_t = _empty(shape, dtype=torch.uint8, device=dev), _empty(groups, dtype=torch.float32, device=dev)
     return q, si, q_t, si_t
+
+
+def _addresses(*tensors):
+    return [None if t is None else t.data_ptr() for t in tensors]
 
 
 def _weight(weight: torch.Tensor, cols: int, at: int):
@@ -1085,18 +1095,18 @@ def fp8q_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     _matrix(x, "x", _VALUES, at)
     rows, cols = x.shape
     _weight(weight, cols, at)
-    o, dev = out or {}, x.device
-    h = x
+    o, dev, h, res, res_dt, y = out or {}, x.device, x, None, 0, None
     if residual is not None:
         _matrix(residual, "residual", _VALUES, at, (rows, cols))
-        h = _result(o.get("h"), (rows, cols), residual.dtype, dev)
+        res, res_dt = residual.data_ptr(), _IN[residual.dtype]
+        h = _result(o.get("h"), (rows, cols), residual.dtype, dev) if o else torch.empty_like(residual)
     rstd = _result(o.get("rstd"), (rows,), torch.float32, dev)
-    y = _result(o.get("y"), (rows, cols), x.dtype, dev) if want_y else None
+    if want_y:
+        y = _result(o.get("y"), (rows, cols), x.dtype, dev) if o else torch.empty_like(x)
     q, si, q_t, si_t = _copies(o, direction, rows, cols, dev)
-    st = (_lib or lib()).fp8q_rmsnorm(x.data_ptr(), _IN[x.dtype], _ptr(residual), 0 if residual is None else _IN[residual.dtype],
-                                      weight.data_ptr(), _IN[weight.dtype], rows, cols, eps, fmt, direction,
-                                      1 if pow2_scales else 0, h.data_ptr(), rstd.data_ptr(), _ptr(y), _ptr(q), _ptr(si),
-                                      _ptr(q_t), _ptr(si_t), _stream(at))
+    st = (_lib or lib()).fp8q_rmsnorm(x.data_ptr(), _IN[x.dtype], res, res_dt, weight.data_ptr(), _IN[weight.dtype], rows, cols,
+                                      eps, fmt, direction, 1 if pow2_scales else 0, h.data_ptr(), rstd.data_ptr(),
+                                      *_addresses(y, q, si, q_t, si_t), _stream(at))
     if st:
         _check(st, "fp8q_rmsnorm")
     return {"y": y, "h": h, "rstd": rstd, "q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
@@ -1141,8 +1151,8 @@ def fp8q_swiglu(h: torch.Tensor, fmt: int = E4M3, direction: int = ROW, pow2_sca
     o, dev = out or {}, h.device
     a = _result(o.get("a"), (rows, inner), h.dtype, dev) if want_a else None
     q, si, q_t, si_t = _copies(o, direction, rows, inner, dev)
-    st = (_lib or lib()).fp8q_swiglu(h.data_ptr(), _IN[h.dtype], rows, inner, fmt, direction, 1 if pow2_scales else 0, _ptr(a),
-                                     _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t), _stream(at))
+    st = (_lib or lib()).fp8q_swiglu(h.data_ptr(), _IN[h.dtype], rows, inner, fmt, direction, 1 if pow2_scales else 0, *_addresses(a, q, si, q_t, si_t),
+                                     _stream(at))
     if st:
         _check(st, "fp8q_swiglu")
     return {"a": a, "q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
@@ -1162,8 +1172,7 @@ def fp8q_swiglu_backward(h: torch.Tensor, d_a: torch.Tensor, fmt: int = E5M2, di
     d_h = _result(o.get("d_h"), (rows, cols), h.dtype, dev) if want_d_h else None
     q, si, q_t, si_t = _copies(o, direction, rows, cols, dev)
     st = (_lib or lib()).fp8q_swiglu_backward(h.data_ptr(), d_a.data_ptr(), _IN[h.dtype], rows, cols // 2, fmt, direction,
-                                              1 if pow2_scales else 0, _ptr(d_h), _ptr(q), _ptr(si), _ptr(q_t), _ptr(si_t),
-                                              _stream(at))
+                                              1 if pow2_scales else 0, *_addresses(d_h, q, si, q_t, si_t), _stream(at))
     if st:
         _check(st, "fp8q_swiglu_backward")
     return {"d_h": d_h, "q": q, "scale_inv": si, "q_t": q_t, "scale_inv_t": si_t}
@@ -1191,6 +1200,9 @@ def _clip(grads: list, max_norm: float, out, norm):
         outs, out_types = _tensors(out, "out", at)
         if out_types != types or [o.shape for o in out] != [g.shape for g in grads]:
             raise ValueError("out must hold one tensor like each gradient")
+        written = [a for a, n_i in zip(outs, sizes) if n_i]
+        if len(set(written)) != len(written):
+            raise ValueError("out holds a tensor twice")
         scale = _empty(1, dtype=torch.float32, device=dev)
     norm = _result(norm, (1,), torch.float32, dev)
     L = _lib or lib()

@@ -122,8 +122,13 @@ def test_refusals():
     a = torch.randn(8, 8, device="cuda")
     for call in (lambda: fq.fp8q_clip_grads([], 1.0), lambda: fq.fp8q_clip_grads([a.half()], 1.0), lambda: fq.fp8q_clip_grads([a[:, :4]], 1.0),
                  lambda: fq.fp8q_clip_grads([a, a.cpu()], 1.0), lambda: fq.fp8q_clip_grads([a], 1.0, out=[]),
-                 lambda: fq.fp8q_clip_grads([a], 1.0, out=[a.bfloat16()]), lambda: fq.fp8q_grad_norm([a.cpu()])):
+                 lambda: fq.fp8q_clip_grads([a, a], 1.0, out=[a, a]), lambda: fq.fp8q_clip_grads([a], 1.0, out=[a.bfloat16()]), lambda: fq.fp8q_grad_norm([a.cpu()])):
         with pytest.raises(ValueError):
             call()
     with pytest.raises(fq.Fp8qError):
         fq.fp8q_clip_grads([a], -1.0)
+    empty = torch.empty(0, device="cuda")  # nothing of it is written
+    assert float(fq.fp8q_clip_grads([empty, a, empty], 1.0, out=[empty, a.clone(), empty])["scale"]) < 1
+    # a gradient twice counts twice
+    twice = fq.fp8q_grad_norm([a, a])
+    assert abs(float(twice) - 2 ** 0.5 * float(fq.fp8q_grad_norm([a]))) <= 2 ** -22 * float(twice)

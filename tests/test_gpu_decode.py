@@ -84,7 +84,7 @@ def case(tokens, top, experts, hidden, inner, fmt, seed):
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("tokens,top,experts,hidden,inner", [
     (1, 1, 1, 16, 16), (1, 8, 64, 1024, 256), (7, 3, 5, 272, 144), (8, 2, 2, 128, 128), (9, 1, 1, 2064, 80), (16, 8, 40, 512, 512),
-    (33, 4, 300, 144, 272), (64, 6, 17, 1040, 336), (64, 32, 40, 256, 48), (5, 2, 1024, 32, 16)])
+    (33, 4, 300, 144, 272), (64, 6, 17, 1040, 336), (64, 32, 40, 256, 48), (64, 32, 1024, 32, 16), (5, 2, 1024, 32, 16), (48, 2, 3, 96, 2064)])
 def test_layer(tokens, top, experts, hidden, inner, fmt):
     fq = require_cuda()
     for out_dtype in (torch.float32, torch.bfloat16):

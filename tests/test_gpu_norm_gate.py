@@ -309,6 +309,7 @@ def test_gate_codes_are_the_quantizer_s():
     h[11, 100], h[12, 592 + 5], h[13] = float("nan"), float("inf"), 0.0
     h[14, 7] = torch.tensor(-1, dtype=torch.int32, device="cuda").view(FP32)  # a negative NaN
     h[15, 9], h[15, 10], h[15, 11] = float("-inf"), 1e38, -1e38
+    h[20], h[21, :592], h[22, 592:] = h[20] * 1e-20, 1e-22, 3e-38  # groups whose scale is the largest FP32 number
     d_a = torch.randn(176, 592, device="cuda", generator=gen(2))
     r = fq.fp8q_swiglu(h, fmt=0, direction=fq.BOTH, want_a=True)
     b = fq.fp8q_swiglu_backward(h, d_a, fmt=1, direction=fq.BOTH, want_d_h=True)
@@ -344,6 +345,32 @@ def test_guards_of_the_copies():
     fq.fp8q_swiglu_backward(h, d_a, want_d_h=True, out={k: b.t for k, b in bufs.items()})
     for b in bufs.values():
         b.check()
+
+
+# ---------------------------------------------------------------------------
+# past 32 bits
+# ---------------------------------------------------------------------------
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows (the last 128 of the transposed copies' groups) are those of a call on them alone."""
+    fq = require_cuda()
+    rows, cols, tail = 135168, 16384, 256
+    h = torch.empty(rows, cols, dtype=BF16, device="cuda").normal_(generator=gen(50))
+    assert h.numel() > 2 ** 31
+    w = torch.rand(cols, device="cuda", generator=gen(51))
+    last = h[-tail:].contiguous()
+    big, small = fq.fp8q_swiglu(h, direction=fq.BOTH), fq.fp8q_swiglu(last, direction=fq.BOTH)
+    for name in ("q", "scale_inv"):
+        assert torch.equal(big[name][-tail:], small[name])
+    assert torch.equal(big["q_t"][:, -tail:], small["q_t"]) and torch.equal(big["scale_inv_t"][:, -tail // 128:], small["scale_inv_t"])
+    d_a = torch.empty(rows, cols // 2, dtype=BF16, device="cuda").normal_(generator=gen(52))
+    big, small = fq.fp8q_swiglu_backward(h, d_a), fq.fp8q_swiglu_backward(last, d_a[-tail:].contiguous())
+    assert torch.equal(big["q"][-tail:], small["q"]) and torch.equal(big["q_t"][:, -tail:], small["q_t"])
+    del big, d_a
+    big, small = fq.fp8q_rmsnorm(h, w, h, direction=fq.BOTH), fq.fp8q_rmsnorm(last, w, last, direction=fq.BOTH)
+    assert torch.equal(big["h"][-tail:], small["h"]) and torch.equal(big["q"][-tail:], small["q"])
+    assert torch.equal(big["q_t"][:, -tail:], small["q_t"])
+    d, e = fq.fp8q_rmsnorm_backward(h, big["h"], w, big["rstd"]), fq.fp8q_rmsnorm_backward(last, small["h"], w, small["rstd"])
+    assert torch.equal(d["d_x"][-tail:], e["d_x"])
 
 
 # ---------------------------------------------------------------------------
