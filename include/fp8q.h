@@ -9,7 +9,9 @@
  *     rowwise and columnwise (transposed), optionally per ragged group;
  * and the steps around it: dequantization, blockwise FP8, NVFP4, the
  * SQNR / zero-rate statistics of a quantized copy, the products of blockwise
- * copies, and the expert layer that feeds and joins them.
+ * copies, the expert layer that feeds and joins them, and what stands around
+ * it in a block: the norm with the residual, the gated activation, the layer
+ * for a few tokens in one call, the gradients' norm and clip.
  *
  * Conventions for every entry point:
  *   - Pointers documented as "device" are CUDA device pointers owned by the

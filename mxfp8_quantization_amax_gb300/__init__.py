@@ -1,5 +1,6 @@
 """Python binding of libfp8q: FP8 / MXFP8 quantization kernels for GB300, the
-products of blockwise FP8 tensors, and the expert layer around them.
+products of blockwise FP8 tensors, the expert layer around them, and the block
+around that: norm, gated activation, few-token serving, gradient clipping.
 
 Thin ctypes marshalling over the C ABI declared in include/fp8q.h: every
 function takes torch CUDA tensors, checks shapes and dtypes, allocates the

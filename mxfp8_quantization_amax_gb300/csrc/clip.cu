@@ -10,6 +10,10 @@
 // FP64: across pieces, CTAs and launches.  The CTAs that write add the partial
 // sums up themselves, all in the same order, and take the pieces from the last
 // on: those are still in L2.
+//
+// Bound by memory: the norm has to be known before the first value is written,
+// so that all but what L2 keeps is read twice.  705M FP32 values 1230 us (385 to
+// read, 7.3 TB/s; 845 to read and write, 6.7 TB/s), 180M BF16 values 163 us.
 #include <math.h>
 
 #include "quant_tile.cuh"

@@ -17,6 +17,14 @@
 // CTA takes 32 output columns of all tokens and a share of the experts' blocks
 // of K, and its warps share those; the CTAs of a cluster have the same columns
 // and add up through distributed shared memory.  Every sum has a fixed order.
+//
+// Bound by the weights' bytes: 64 experts of 7168 x 2048, 8 a token: 1 token 60
+// us (352 MB, 5.8 TB/s; some 7 us are the two kernels' start, lists and end), 4
+// tokens 178, 16 tokens 380 (6.6 TB/s).  Beyond 8 tokens an expert its weights are
+// read again, from L2, and converted again: 64 tokens 560 us (floor 421).  Sizes
+// whose K leaves warps idle cost more: 61 tokens, 40 experts of 2064 x 1360 107
+// us (floor 50).  Jobs of 16 tokens were slower everywhere (64 tokens 767 then
+// against 677): their registers leave one CTA an SM.
 #include "fp8q_device.cuh"
 #include "internal.h"
 

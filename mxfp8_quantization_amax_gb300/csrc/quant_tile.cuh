@@ -8,6 +8,9 @@
 // (or the transposed one): a CTA of 256 threads holds a tile of 128 x 128, a
 // thread 8 x 8 of it, so that row groups meet in a half-warp and column groups
 // in shared memory, and neither copy needs the values a second time.
+//
+// Bound by memory and issue together: the activation of 65536 x 2048 in both
+// copies 124 us (6.6 TB/s); one CTA a tile without the inputs on their way 158.
 #pragma once
 
 #include "fp8q_device.cuh"
@@ -235,7 +238,7 @@ struct QtOut {
   float* s_t;
 };
 
-// A source gives 8 values of a row (rows come in multiples of 16, columns too)
+// A source gives 8 values of a row (columns come in multiples of 16, and for the transposed copy rows do)
 // from kInputs runs of 8 inputs of type kType, which is the dense output's too:
 //   bool needs(int input, int col) const;
 //   const void* at(int input, int row, int col) const;
@@ -247,11 +250,12 @@ struct QtOut {
 template <class Src>
 constexpr size_t kQtSmem = (size_t)kQtRows * Src::kInputs * kQtThreads * kQtRunBytes<Src::kType>;
 
-// What a half-warp asks for: its rows' values from column col on.
-template <class Src>
-__device__ __forceinline__ void qt_ask_tile(const Src& src, int row, int col, int cols, bool there, uint32_t place, int hl) {
+// What a half-warp asks for: the values of its `rows` rows (ALL: kQtRows or none)
+// from column col on.
+template <class Src, bool ALL>
+__device__ __forceinline__ void qt_ask_tile(const Src& src, int row, int col, int cols, int rows, uint32_t place, int hl) {
   constexpr int kSize = Src::kType == kBF16 ? 2 : 4, kRun = kQtRunBytes<Src::kType>;
-  if (there) {
+  if (rows > 0) {
 #pragma unroll
     for (int n = 0; n < Src::kInputs; n++) {
 #pragma unroll
@@ -262,7 +266,8 @@ __device__ __forceinline__ void qt_ask_tile(const Src& src, int row, int col, in
           const uint8_t* from = (const uint8_t*)src.at(n, row, c);
           const int64_t pitch = (int64_t)src.pitch(n) * kSize;
 #pragma unroll
-          for (int i = 0; i < kQtRows; i++) qt_ask(place + (i * Src::kInputs + n) * kQtThreads * kRun + (k * 16 + hl) * 16, from + i * pitch);
+          for (int i = 0; i < kQtRows; i++)
+            if (ALL || i < rows) qt_ask(place + (i * Src::kInputs + n) * kQtThreads * kRun + (k * 16 + hl) * 16, from + i * pitch);
         }
       }
     }
@@ -272,12 +277,13 @@ __device__ __forceinline__ void qt_ask_tile(const Src& src, int row, int col, in
 
 // Persistent: the inputs of a CTA's next tile come while it works on this one.
 // PAIR: the tiles of both halves come from one set of inputs; the second half's
-// values wait where its inputs were.
-template <class Src, int FMT, bool ROW, bool PAIR>
+// values wait where its inputs were.  Without COL (any number of rows) no barrier
+// is left: a half-warp has its rows to itself.
+template <class Src, int FMT, bool ROW, bool COL, bool PAIR>
 __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOut o) {
   extern __shared__ __align__(16) uint8_t inputs[];  // [rows of a thread][inputs][threads] of 8 values
-  __shared__ float scale[kQtTile];
-  __shared__ __align__(16) uint8_t stage[kQtTile * 128];  // codes of the transposed tile; the warps' column maxima before
+  __shared__ float scale[COL ? kQtTile : 1];
+  __shared__ __align__(16) uint8_t stage[COL ? kQtTile * 128 : 16];  // codes of the transposed tile; the warps' column maxima before
   float(*part)[kQtTile] = (float(*)[kQtTile])stage;
   constexpr int kRun = kQtRunBytes<Src::kType>;
   const int tid = threadIdx.x, lane = tid & 31, hl = tid & 15, ty = tid >> 4, all_rows = (int)o.rows, all_cols = (int)o.cols;
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
   };
   const auto ask = [&](int tr, int tc) {
     const int row = tr * kQtTile + ty * kQtRows;
-    qt_ask_tile(src, row, tc * kQtTile, cols, row < all_rows, place, hl);
+    qt_ask_tile<Src, COL>(src, row, tc * kQtTile, cols, all_rows - row, place, hl);
   };
   // where the second half's values of row i wait: 32 bytes of the thread's own
   const auto waits = [&](int i, int k) {
@@ -305,6 +311,7 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
     const int this_r = tr, this_c = tc + half * items_c;
     const int rt = tr * kQtTile, r0 = rt + ty * kQtRows, c0 = this_c * kQtTile, c = c0 + hl * 8;
     const bool there = c < all_cols && r0 < all_rows;
+    const int rows = COL ? kQtRows : all_rows - r0;  // of the thread's; of others the values are anything
     float v[kQtRows][8];
     if (there) src.begin(r0, c);
     if (!PAIR || half == 0) {
@@ -355,8 +362,7 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
         ask(tr, tc);
       }
     }
-    // columns: the rows of a thread, twice as many of a warp, 128 of the CTA
-    {
+    if constexpr (COL) {  // columns: the rows of a thread, twice as many of a warp, 128 of the CTA
       float m[8];
 #pragma unroll
       for (int k = 0; k < 8; k++)
@@ -371,10 +377,11 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
     }
     if (o.dense != nullptr && there) {
 #pragma unroll
-      for (int i = 0; i < kQtRows; i++) qt_store<Src::kType, 8>(o.dense, (int64_t)(r0 + i) * all_cols + c, v[i]);
+      for (int i = 0; i < kQtRows; i++)
+        if (COL || i < rows) qt_store<Src::kType, 8>(o.dense, (int64_t)(r0 + i) * all_cols + c, v[i]);
     }
-    __syncthreads();
-    if (tid < kQtTile) {
+    if constexpr (COL) __syncthreads();
+    if (COL && tid < kQtTile) {
       float m = part[0][tid];
 #pragma unroll
       for (int w = 1; w < kQtThreads / 32; w++) m = qt_max(m, part[w][tid]);
@@ -387,67 +394,70 @@ __global__ void __launch_bounds__(kQtThreads, 2) quant_tile_kernel(Src src, QtOu
       float* scale_to = o.s + (int64_t)r0 * o.tiles_c + this_c;
       qt_groups<FMT, kQtRows>(
           v, o.pow2, [&](int i) { return to + (int64_t)i * all_cols; }, [&](int i) { return scale_to + (int64_t)i * o.tiles_c; },
-          [&](int) { return there; });
+          [&](int i) { return there && (COL || i < rows); });
     }
-    __syncthreads();
-    {
-      const float4 a = *(const float4*)&scale[hl * 8], b = *(const float4*)&scale[hl * 8 + 4];
+    if constexpr (COL) {
+      __syncthreads();
+      {
+        const float4 a = *(const float4*)&scale[hl * 8], b = *(const float4*)&scale[hl * 8 + 4];
 #pragma unroll
-      for (int i = 0; i < kQtRows; i++) {
-        mul2(v[i][0], v[i][1], a.x, a.y);
-        mul2(v[i][2], v[i][3], a.z, a.w);
-        mul2(v[i][4], v[i][5], b.x, b.y);
-        mul2(v[i][6], v[i][7], b.z, b.w);
+        for (int i = 0; i < kQtRows; i++) {
+          mul2(v[i][0], v[i][1], a.x, a.y);
+          mul2(v[i][2], v[i][3], a.z, a.w);
+          mul2(v[i][4], v[i][5], b.x, b.y);
+          mul2(v[i][6], v[i][7], b.z, b.w);
+        }
+        // 8-byte pieces of the column's 128 rows, permuted by the thread's columns: 16 lanes hit 16 places
+        uint8_t* to = stage + hl * 8 * 128 + ((ty ^ hl) << 3);
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+          *(uint2*)(to + k * 128) = make_uint2(cvt4<FMT>(v[0][k], v[1][k], v[2][k], v[3][k]), cvt4<FMT>(v[4][k], v[5][k], v[6][k], v[7][k]));
       }
-      // 8-byte pieces of the column's 128 rows, permuted by the thread's columns: 16 lanes hit 16 places
-      uint8_t* to = stage + hl * 8 * 128 + ((ty ^ hl) << 3);
+      __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 8; k++)
-        *(uint2*)(to + k * 128) = make_uint2(cvt4<FMT>(v[0][k], v[1][k], v[2][k], v[3][k]), cvt4<FMT>(v[4][k], v[5][k], v[6][k], v[7][k]));
+      for (int n = 0; n < 512 / kQtThreads; n++) {  // 32 rows of a column: four threads a column
+        const int col = (tid + n * kQtThreads) >> 2, at = tid & 3, flip = col >> 3;
+        const int row = rt + 32 * at;
+        if (c0 + col >= all_cols || row >= all_rows) continue;
+        uint4 a = *(const uint4*)(stage + col * 128 + (((2 * at) ^ (flip >> 1)) << 4));
+        uint4 b = *(const uint4*)(stage + col * 128 + (((2 * at + 1) ^ (flip >> 1)) << 4));
+        if (flip & 1) {
+          a = make_uint4(a.z, a.w, a.x, a.y);
+          b = make_uint4(b.z, b.w, b.x, b.y);
+        }
+        uint8_t* to = o.q_t + (int64_t)(c0 + col) * all_rows + row;
+        if (wide) {
+          const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          st32B(to, d);
+        } else {
+          st_stream(to, a);
+          if (row + 16 < all_rows) st_stream(to + 16, b);
+        }
+      }
+      __syncthreads();  // the codes have been read
     }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < 512 / kQtThreads; n++) {  // 32 rows of a column: four threads a column
-      const int col = (tid + n * kQtThreads) >> 2, at = tid & 3, flip = col >> 3;
-      const int row = rt + 32 * at;
-      if (c0 + col >= all_cols || row >= all_rows) continue;
-      uint4 a = *(const uint4*)(stage + col * 128 + (((2 * at) ^ (flip >> 1)) << 4));
-      uint4 b = *(const uint4*)(stage + col * 128 + (((2 * at + 1) ^ (flip >> 1)) << 4));
-      if (flip & 1) {
-        a = make_uint4(a.z, a.w, a.x, a.y);
-        b = make_uint4(b.z, b.w, b.x, b.y);
-      }
-      uint8_t* to = o.q_t + (int64_t)(c0 + col) * all_rows + row;
-      if (wide) {
-        const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        st32B(to, d);
-      } else {
-        st_stream(to, a);
-        if (row + 16 < all_rows) st_stream(to + 16, b);
-      }
-    }
-    __syncthreads();  // the codes have been read
   }
   pdl_launch_dependents();
 }
 
-template <class Src, int FMT, bool ROW, bool PAIR>
+template <class Src, int FMT, bool ROW, bool COL, bool PAIR>
 cudaError_t launch_quant_tiles_t(const Src& src, const QtOut& o, cudaStream_t s) {
+  const auto kernel = quant_tile_kernel<Src, FMT, ROW, COL, PAIR>;
   static PerDevice<bool> allowed;
-  const cudaError_t e = allow_smem(allowed, quant_tile_kernel<Src, FMT, ROW, PAIR>, kQtSmem<Src>);
+  const cudaError_t e = allow_smem(allowed, kernel, kQtSmem<Src>);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)o.tiles_r * o.tiles_c / (PAIR ? 2 : 1), fit = (kQtSmem<Src> > 96 * 1024 ? 1 : 2) * (int64_t)sm_count();
-  return launch_kernel(quant_tile_kernel<Src, FMT, ROW, PAIR>, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kQtThreads), kQtSmem<Src>, s, src, o);
+  return launch_kernel(kernel, dim3((unsigned)(tiles < fit ? tiles : fit)), dim3(kQtThreads), kQtSmem<Src>, s, src, o);
 }
 
 // Halves with the same inputs: where they are whole tiles one CTA makes both
 // tiles of them; else tile columns are taken in the order 0, half, 1, half + 1, ...
-template <class Src, int FMT>
+template <class Src, int FMT, bool ROW, bool COL>
 cudaError_t launch_quant_tiles(const Src& src, const QtOut& o, cudaStream_t s) {
   if constexpr (Src::kHalves) {
-    if (o.cols % (2 * kQtTile) == 0) return o.q ? launch_quant_tiles_t<Src, FMT, true, true>(src, o, s) : launch_quant_tiles_t<Src, FMT, false, true>(src, o, s);
+    if (o.cols % (2 * kQtTile) == 0) return launch_quant_tiles_t<Src, FMT, ROW, COL, true>(src, o, s);
   }
-  return o.q ? launch_quant_tiles_t<Src, FMT, true, false>(src, o, s) : launch_quant_tiles_t<Src, FMT, false, false>(src, o, s);
+  return launch_quant_tiles_t<Src, FMT, ROW, COL, false>(src, o, s);
 }
 
 // Checks of the copies' arguments, for cols columns.

@@ -8,13 +8,22 @@
 //
 // Sums are FP32 in a fixed order.  The norm is of h as it is stored, so that
 // the gradient, which reads h again, differentiates what was computed.
+//
+// Bound by memory where rows are many: CTAs stay and have the next rows' inputs
+// on their way.  16384 x 4096 BF16 with the residual: row copy 71 us (6.6 TB/s;
+// 120 with a CTA a row), gradients 89 us (6.0 TB/s), the transposed copy 34 us
+// more: it needs the statistics of 128 rows, and 128 rows of 4096 do not fit an
+// SM, so h is read again.  12345 x 7168, FP32 stream, y and row copy 188 us (6.1
+// TB/s).  Without a residual issue bounds it (16384 x 7168 90 us, 3.9 TB/s).  Any
+// columns, value by value: 12345 x 4097 159 us, gradients 295 us (1.0 TB/s).  One
+// row of 7168: 3.1 us, latency.
 #include "quant_tile.cuh"
 
 namespace fp8q {
 
 constexpr int kRnMaxCols = 32768;
 constexpr int kRnThreads = 256;      // of a CTA at least
-constexpr int kRnMaxPartials = 608;  // rows of the weight gradient's partial sums
+constexpr int kRnMaxPartials = 608;  // rows of the weight gradient's partial sums: one a CTA
 constexpr int kNone = -1;
 
 struct RmsNorm {
@@ -670,10 +679,12 @@ extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* resid
     const void* from = residual ? h : x;
     if (ht == FP8Q_IN_BF16) {
       const RmsNormTile<kBF16> src{from, weight, weight_dt, rstd, cols, {}, {}};
-      e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kBF16>, kE4M3>(src, o, s) : launch_quant_tiles<RmsNormTile<kBF16>, kE5M2>(src, o, s);
+      e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kBF16>, kE4M3, false, true>(src, o, s)
+                           : launch_quant_tiles<RmsNormTile<kBF16>, kE5M2, false, true>(src, o, s);
     } else {
       const RmsNormTile<kFP32> src{from, weight, weight_dt, rstd, cols, {}, {}};
-      e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kFP32>, kE4M3>(src, o, s) : launch_quant_tiles<RmsNormTile<kFP32>, kE5M2>(src, o, s);
+      e = fmt == FP8Q_E4M3 ? launch_quant_tiles<RmsNormTile<kFP32>, kE4M3, false, true>(src, o, s)
+                           : launch_quant_tiles<RmsNormTile<kFP32>, kE5M2, false, true>(src, o, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "rmsnorm transposed copy launch");
   }

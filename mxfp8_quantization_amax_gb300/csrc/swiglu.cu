@@ -11,6 +11,11 @@
 // 0 where it would be below 2^-126 (gates below -87.3).  FP32 throughout, the
 // products of two BF16 inputs exact; codes are made from the FP32 values, a
 // dense output is rounded once.
+//
+// Both copies: tiles (quant_tile.cuh).  65536 x 2048 124 us (6.6 TB/s), the
+// gradient of 16384 x 14336 403 us (5.9 TB/s, issue 67%; 690 with a sigmoid and
+// a read of the inputs for each half).  The row copy alone 100 us (6.7 TB/s) and
+// 276 us (6.9 TB/s).  128 rows of 2048: 1.4 us, in a call of 17.
 #include "quant_tile.cuh"
 
 namespace fp8q {
@@ -204,72 +209,64 @@ struct SwigluBackward {
   }
 };
 
-// Rows alone: the dense output, the row copy or both.  A half-warp takes a row
-// group of 128 columns (without a copy: any V * 16 columns).
+// Few rows, or no copy: a half-warp takes a row's group of 128 columns (without a
+// copy: 16 V columns); PAIR: that group and its partner in the other half.
 constexpr int kSgThreads = 256;
 
-// U rows of one group of columns a half-warp, all on their way at a time; PAIR:
-// U / 2 rows of a group and of its partner in the other half.
-template <class Src, int FMT, int V, int U, bool PAIR>
+template <class Src, int FMT, int V, bool PAIR>
 __global__ void __launch_bounds__(kSgThreads) swiglu_rows_kernel(Src src, QtOut o, uint32_t per_row, uint32_t items) {
-  constexpr int kRows = PAIR ? U / 2 : U;
+  constexpr int U = PAIR ? 2 : 1;
   const int hl = threadIdx.x & 15;
-  const uint32_t item = blockIdx.x * (kSgThreads / 16) + threadIdx.x / 16, block = item / per_row, group = item - block * per_row;
-  const int64_t c = (int64_t)(group * 16 + hl) * V, r0 = (int64_t)block * kRows;
+  const uint32_t item = blockIdx.x * (kSgThreads / 16) + threadIdx.x / 16, r = item / per_row, group = item - r * per_row;
+  const int64_t cols = PAIR ? o.cols / 2 : o.cols, c = (int64_t)(group * 16 + hl) * V;
+  const bool ok = item < items && c < cols;
   pdl_wait();
-  float v[U][V];
-#pragma unroll
-  for (int i = 0; i < U; i++)
-#pragma unroll
-    for (int k = 0; k < V; k++) v[i][k] = 0.0f;
-  const auto there = [&](int i) { return item < items && c < (PAIR ? o.cols / 2 : o.cols) && r0 + i % kRows < o.rows; };
-  const auto col = [&](int i) { return c + (i >= kRows ? o.cols / 2 : 0); };
-#pragma unroll
-  for (int i = 0; i < kRows; i++) {
-    if (!there(i)) continue;
-    if constexpr (PAIR) src.row_both(v[i], v[kRows + i], r0 + i, c);
-    else src.template row<V>(v[i], r0 + i, c);
+  float v[U][V] = {};
+  if (ok) {
+    if constexpr (PAIR) src.row_both(v[0], v[1], r, c);
+    else src.template row<V>(v[0], r, c);
   }
   if constexpr (V == 8) {
     if (o.q != nullptr) {
-      uint8_t* q = o.q + r0 * o.cols;
-      float* s = o.s + r0 * o.tiles_c;
+      uint8_t* q = o.q + r * o.cols + c;
+      float* s = o.s + (int64_t)r * o.tiles_c + c / 128;
       qt_groups<FMT, U>(
-          v, o.pow2, [&](int i) { return q + i % kRows * o.cols + col(i); },
-          [&](int i) { return s + i % kRows * o.tiles_c + col(i) / 128; }, there);
+          v, o.pow2, [&](int i) { return q + i * cols; }, [&](int i) { return s + i * cols / 128; }, [&](int) { return ok; });
     }
   }
-  if (o.dense != nullptr) {
+  if (o.dense != nullptr && ok) {
 #pragma unroll
-    for (int i = 0; i < U; i++)
-      if (there(i)) qt_store<Src::kType, V>(o.dense, (r0 + i % kRows) * o.cols + col(i), v[i]);
+    for (int i = 0; i < U; i++) qt_store<Src::kType, V>(o.dense, r * o.cols + i * cols + c, v[i]);
   }
   pdl_launch_dependents();
 }
 
-template <class Src, int FMT, int V, int U, bool PAIR>
+template <class Src, int FMT, int V, bool PAIR>
 static fp8q_status launch_swiglu_rows(const Src& src, const QtOut& o, cudaStream_t s) {
-  const int64_t cols = PAIR ? o.cols / 2 : o.cols, rows = PAIR ? U / 2 : U, per_row = (cols + V * 16 - 1) / (V * 16);
-  const int64_t items = (o.rows + rows - 1) / rows * per_row;
+  const int64_t cols = PAIR ? o.cols / 2 : o.cols, per_row = (cols + V * 16 - 1) / (V * 16), items = o.rows * per_row;
   if (items > UINT32_MAX - kSgThreads) return fail(FP8Q_ERR_UNSUPPORTED, "rows * inner too large");
   const dim3 grid((unsigned)((items + kSgThreads / 16 - 1) / (kSgThreads / 16)));
-  const cudaError_t e = launch_kernel(swiglu_rows_kernel<Src, FMT, V, U, PAIR>, grid, dim3(kSgThreads), 0, s, src, o, (uint32_t)per_row, (uint32_t)items);
+  const cudaError_t e = launch_kernel(swiglu_rows_kernel<Src, FMT, V, PAIR>, grid, dim3(kSgThreads), 0, s, src, o, (uint32_t)per_row, (uint32_t)items);
   return e == cudaSuccess ? check_launch("swiglu kernel") : cuda_fail(e, "swiglu kernel launch");
 }
 
 template <class Src, int FMT>
 static fp8q_status launch_swiglu(const Src& src, const QtOut& o, bool vec, cudaStream_t s) {
-  if (o.q_t) {
-    const cudaError_t e = launch_quant_tiles<Src, FMT>(src, o, s);
+  // The row copy alone by tiles where every SM gets some (4096 x 2048: 7.6 us, 8.8 a half-warp a group;
+  // 65536 x 2048: 100 and 135), else a half-warp a group (2000 x 2048: 4.4 us, 4.6 by tiles; its gradient 6.0, 7.2)
+  const int64_t tiles = (int64_t)o.tiles_r * o.tiles_c;
+  const bool many = (Src::kHalves && o.cols % (2 * kQtTile) == 0 ? tiles / 2 : tiles) >= 3 * sm_count();
+  if (o.q_t || (o.q && many)) {
+    const cudaError_t e = !o.q_t ? launch_quant_tiles<Src, FMT, true, false>(src, o, s)
+                          : o.q  ? launch_quant_tiles<Src, FMT, true, true>(src, o, s)
+                                 : launch_quant_tiles<Src, FMT, false, true>(src, o, s);
     return e == cudaSuccess ? check_launch("swiglu kernel") : cuda_fail(e, "swiglu kernel launch");
   }
-  // four row groups a half-warp where that leaves every SM its share of CTAs, else one (or a pair)
-  const bool four = o.rows * ((o.cols + 127) / 128) >= (int64_t)64 * 16 * sm_count();
-  if (!vec) return four ? launch_swiglu_rows<Src, FMT, 1, 4, false>(src, o, s) : launch_swiglu_rows<Src, FMT, 1, 1, false>(src, o, s);
+  if (!vec) return launch_swiglu_rows<Src, FMT, 1, false>(src, o, s);
   if constexpr (Src::kHalves) {
-    if (o.cols % 256 == 0) return four ? launch_swiglu_rows<Src, FMT, 8, 4, true>(src, o, s) : launch_swiglu_rows<Src, FMT, 8, 2, true>(src, o, s);
+    if (o.cols % 256 == 0) return launch_swiglu_rows<Src, FMT, 8, true>(src, o, s);
   }
-  return four ? launch_swiglu_rows<Src, FMT, 8, 4, false>(src, o, s) : launch_swiglu_rows<Src, FMT, 8, 1, false>(src, o, s);
+  return launch_swiglu_rows<Src, FMT, 8, false>(src, o, s);
 }
 
 template <class Src>
