@@ -13,7 +13,7 @@
 // second FP16 number holds what the first one's rounding (2^-12) left.
 //
 // First kernel: a unit is 32 inner values of one expert (rows of G and of U)
-// for up to 8 of its tokens; the 8 warps of a CTA share K.  Second kernel: a
+// for up to 8 of its tokens; 8 or 4 warps of a CTA share K.  Second kernel: a
 // CTA takes 32 output columns of all tokens and a share of the experts' blocks
 // of K, and its warps share those; the CTAs of a cluster have the same columns
 // and add up through distributed shared memory.  Every sum has a fixed order.
@@ -22,7 +22,7 @@
 // us (352 MB, 5.8 TB/s; some 7 us are the two kernels' start, lists and end), 4
 // tokens 178, 16 tokens 380 (6.6 TB/s).  Beyond 8 tokens an expert its weights are
 // read again, from L2, and converted again: 64 tokens 560 us (floor 421).  Sizes
-// whose K leaves warps idle cost more: 61 tokens, 40 experts of 2064 x 1360 107
+// whose K leaves warps idle cost more: 61 tokens, 40 experts of 2064 x 1360 97
 // us (floor 50).  Jobs of 16 tokens were slower everywhere (64 tokens 767 then
 // against 677): their registers leave one CTA an SM.
 #include "fp8q_device.cuh"
@@ -296,9 +296,10 @@ __device__ __forceinline__ void md_feed_unit(const MdParams& p, const MdLists& l
   f.scale = p.s1 + ((int64_t)u.expert * p.nb1 + min(row >> 7, p.nb1 - 1)) * p.kb1;
 }
 
-// Asks for the next tile, into `to` (the warp's) and, a block's first, `scales`.
-__device__ __forceinline__ void md_feed(const MdParams& p, const MdLists& l, MdFeed& f, int units, int step, uint32_t to,
-                                        uint32_t scales) {
+// Asks for the next tile, into `to` (the warp's) and, a block's first, `scales`;
+// `warp`, `warps`: the warp's place among those that share K.
+__device__ __forceinline__ void md_feed(const MdParams& p, const MdLists& l, MdFeed& f, int units, int step, int warp, int warps,
+                                        uint32_t to, uint32_t scales) {
   if (f.unit < units) {
     if (f.kb < p.kb1) {
       const int lane = threadIdx.x & 31, k = f.kb * 128;
@@ -309,9 +310,9 @@ __device__ __forceinline__ void md_feed(const MdParams& p, const MdLists& l, MdF
     }
     f.up ^= 1;
     if (!f.up) {
-      f.kb += kMdWarps;
-      if (f.kb - (int)(threadIdx.x >> 5) >= p.kb1) {
-        f.kb = threadIdx.x >> 5;
+      f.kb += warps;
+      if (f.kb - warp >= p.kb1) {
+        f.kb = warp;
         f.unit += step;
         if (f.unit < units) md_feed_unit(p, l, f);
       }
@@ -320,13 +321,15 @@ __device__ __forceinline__ void md_feed(const MdParams& p, const MdLists& l, MdF
   md_commit();
 }
 
-template <int FMT>
+// WARPS share a unit's K: a CTA works on 8 / WARPS units at a time.
+template <int FMT, int WARPS>
 __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p) {
   extern __shared__ uint8_t dynamic[];  // [warps][kMdRingBytes], from a multiple of 128 on, then the lists
   __shared__ float part[kMdWarps][4 * kMdSetFloats];
   __shared__ __align__(16) float scales[kMdWarps][kMdStages][4];
   __shared__ int warp_sum[kMdWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int cta_warp = tid >> 5, group = cta_warp / WARPS, warp = cta_warp % WARPS;
   uint8_t* rings = dynamic + (-md_smem(dynamic) & 127u);
   MdLists l = md_list_places(rings + kMdWarps * kMdRingBytes, p.tokens * p.top_k);
   pdl_wait();
@@ -334,28 +337,29 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
   // their first weights and wait for this kernel's end before they go on.
   pdl_launch_dependents();
   md_lists<false>(p, l, rings, warp_sum);
-  // units are dealt out evenly: with fewer CTAs rather than a last round of a few
-  const int units = l.jobs * p.kb2 * (128 / kMdUnit), rounds = (units + gridDim.x - 1) / gridDim.x;
-  const int step = rounds ? (units + rounds - 1) / rounds : 0;
-  if ((int)blockIdx.x >= step) return;
-  const uint32_t ring = md_smem(rings) + warp * kMdRingBytes, sc_at = md_smem(&scales[warp][0][0]);
+  // units are dealt out evenly: to fewer groups of warps rather than in a last round of a few
+  const int units = l.jobs * p.kb2 * (128 / kMdUnit), groups = gridDim.x * (kMdWarps / WARPS), rounds = (units + groups - 1) / groups;
+  const int step = rounds ? (units + rounds - 1) / rounds : 0, mine_first = blockIdx.x + group * gridDim.x;
+  if (mine_first >= step) return;
+  const auto meet = [&] { asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * WARPS) : "memory"); };  // the group's warps
+  const uint32_t ring = md_smem(rings) + cta_warp * kMdRingBytes, sc_at = md_smem(&scales[cta_warp][0][0]);
   const uint32_t mine = ring + lane * 128 + ((lane & 7) << 4);
   MdFeed f;
-  f.unit = blockIdx.x;
+  f.unit = mine_first;
   f.kb = warp;
   f.up = 0;
   md_feed_unit(p, l, f);
 #pragma unroll
-  for (int i = 0; i < kMdStages; i++) md_feed(p, l, f, units, step, ring + i * kMdTileBytes, sc_at + i * 16);
+  for (int i = 0; i < kMdStages; i++) md_feed(p, l, f, units, step, warp, WARPS, ring + i * kMdTileBytes, sc_at + i * 16);
   int stage = 0;
-  for (int unit = blockIdx.x; unit < units; unit += step) {
+  for (int unit = mine_first; unit < units; unit += step) {
     const MdUnit u = md_unit(p, l, unit);
     float acc[4][4] = {};
     const bool there = g < u.count;
     const uint16_t* xt = p.x + (int64_t)(there ? l.token[u.first + g] : 0) * p.hidden + 4 * q;
     uint32_t x[16];
     md_token(xt + warp * 128, p.hidden - warp * 128, there, x);
-    for (int kb = warp; kb - warp < p.kb1; kb += kMdWarps) {
+    for (int kb = warp; kb - warp < p.kb1; kb += WARPS) {
       // the tokens' part of this block of K
       uint32_t b[16], m = 0;
 #pragma unroll
@@ -367,14 +371,14 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
       const float inv1 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, back, 8 * q + 4));
 #pragma unroll
       for (int i = 0; i < 16; i++) b[i] = md_scaled(x[i], power << 7);
-      const int k = (kb + kMdWarps) * 128;  // the next block's come while this one is multiplied
+      const int k = (kb + WARPS) * 128;  // the next block's come while this one is multiplied
       md_token(xt + k, p.hidden - k, there, x);
       float4 sc = make_float4(0, 0, 0, 0);
 #pragma unroll
       for (int tile = 0; tile < 2; tile++) {
         md_wait<kMdStages - 1>();
         __syncwarp();
-        if (tile == 0) sc = *(const float4*)scales[warp][stage];
+        if (tile == 0) sc = *(const float4*)scales[cta_warp][stage];
         float d[2][4] = {};
         if (kb < p.kb1) {  // else the rest of the warps' last round
 #pragma unroll
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
           }
         }
         __syncwarp();  // all lanes have their codes
-        md_feed(p, l, f, units, step, ring + stage * kMdTileBytes, sc_at + stage * 16);
+        md_feed(p, l, f, units, step, warp, WARPS, ring + stage * kMdTileBytes, sc_at + stage * 16);
         stage = stage + 1 == kMdStages ? 0 : stage + 1;
         if (kb < p.kb1) {
 #pragma unroll
@@ -404,19 +408,20 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
         }
       }
     }
-    __syncthreads();  // the last unit's sums have been read
+    meet();  // the last unit's sums have been read
 #pragma unroll
     for (int set = 0; set < 4; set++)
 #pragma unroll
-      for (int c = 0; c < 4; c++) part[warp][set * kMdSetFloats + (2 * q + (c & 1)) * kMdPitch + g + 8 * (c >> 1)] = acc[set][c];
-    __syncthreads();
-    {  // inner value m for token n: a warp each token
-      const int m = tid % kMdUnit, n = tid / kMdUnit, at = n * kMdPitch + (m & 15) + (m >> 4) * kMdSetFloats;
+      for (int c = 0; c < 4; c++) part[cta_warp][set * kMdSetFloats + (2 * q + (c & 1)) * kMdPitch + g + 8 * (c >> 1)] = acc[set][c];
+    meet();
+#pragma unroll
+    for (int n = warp; n < kMdCols; n += WARPS) {  // inner value m for token n: a warp each token
+      const int m = lane, at = n * kMdPitch + (m & 15) + (m >> 4) * kMdSetFloats;
       float gate = 0.0f, up = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kMdWarps; w++) {
-        gate += part[w][at];
-        up += part[w][2 * kMdSetFloats + at];
+      for (int w = 0; w < WARPS; w++) {
+        gate += part[group * WARPS + w][at];
+        up += part[group * WARPS + w][2 * kMdSetFloats + at];
       }
       const float e = expf(-fabsf(gate)), r = __frcp_rn(1.0f + e);
       const float a = __fmul_rn(__fmul_rn(gate, gate >= 0.0f ? r : __fmul_rn(e, r)), up);
@@ -676,21 +681,31 @@ static cudaError_t launch_second(const MdParams& p, cudaStream_t s) {
   return launch_cluster(decode_second_kernel<FMT, LO, STAGES>, dim3((unsigned)(tiles * shares)), dim3(kMdThreads), shares, smem, s, p, shares);
 }
 
+// The first kernel, WARPS warps a unit.
+template <int FMT, int WARPS>
+static cudaError_t launch_first(const MdParams& p, int64_t units, cudaStream_t s) {
+  constexpr size_t kRings = (size_t)kMdWarps * kMdRingBytes + 128;
+  static PerDevice<bool> allowed;
+  const cudaError_t e = allow_smem(allowed, decode_first_kernel<FMT, WARPS>, kRings + md_list_bytes(kMdPairs));
+  if (e != cudaSuccess) return e;
+  const int64_t fit = 2 * (int64_t)sm_count(), ctas = (units + kMdWarps / WARPS - 1) / (kMdWarps / WARPS);  // two an SM have room
+  return launch_kernel(decode_first_kernel<FMT, WARPS>, dim3((unsigned)(ctas < fit ? ctas : fit)), dim3(kMdThreads),
+                       kRings + md_list_bytes(p.tokens * p.top_k), s, p);
+}
+
 template <int FMT, bool LO>
 static fp8q_status launch_decode(const MdParams& p, cudaStream_t s) {
   const int slots = p.tokens * p.top_k;
-  constexpr size_t kRings = (size_t)kMdWarps * kMdRingBytes + 128;
-  static PerDevice<bool> allowed;
-  cudaError_t e = allow_smem(allowed, decode_first_kernel<FMT>, kRings + md_list_bytes(kMdPairs));
-  if (e != cudaSuccess) return cuda_fail(e, "decode shared memory");
-  // at most this many units; two CTAs an SM have room
-  int64_t units = (int64_t)(slots < p.experts ? slots : p.experts + slots / kMdCols) * p.kb2 * (128 / kMdUnit);
-  const int64_t fit = 2 * (int64_t)sm_count();
-  if (units > fit) units = fit;
-  e = launch_kernel(decode_first_kernel<FMT>, dim3((unsigned)units), dim3(kMdThreads), kRings + md_list_bytes(slots), s, p);
+  const int64_t per_job = (int64_t)p.kb2 * (128 / kMdUnit);
+  const int64_t units = (slots < p.experts ? slots : p.experts + slots / kMdCols) * per_job;  // at most
+  // Half the warps a unit where K's blocks leave many of 8 warps idle and there are units enough (61 tokens, 40 experts
+  // of 2064 x 1360: 17 blocks, 97 us, 106 with 8; 16 tokens, 64 experts of 7168 x 2048: 56 blocks, 387 us, 380 with 8)
+  const int idle8 = (8 - p.kb1 % 8) % 8, idle4 = (4 - p.kb1 % 4) % 4;
+  const bool four = (idle8 - idle4) * 8 > p.kb1 && (slots < p.experts ? slots : p.experts) * per_job >= 8 * (int64_t)sm_count();
+  cudaError_t e = four ? launch_first<FMT, 4>(p, units, s) : launch_first<FMT, 8>(p, units, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode first kernel launch");
   // two CTAs an SM matter more than a second tile of each warp on its way
-  const size_t smem = kRings + md_list_bytes(slots) + (size_t)kMdWarps * p.tokens * kMdOutPitch * sizeof(float);
+  const size_t smem = (size_t)kMdWarps * kMdRingBytes + 128 + md_list_bytes(slots) + (size_t)kMdWarps * p.tokens * kMdOutPitch * sizeof(float);
   e = smem <= kMdHalfSm ? launch_second<FMT, LO, 2>(p, s) : launch_second<FMT, LO, 1>(p, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode second kernel launch");
   return check_launch("decode kernel");
