@@ -641,8 +641,7 @@ FP8Q_API size_t fp8q_moe_decode_workspace_bytes(int64_t tokens, int32_t top_k, i
  * 22 bits for FP32 output, 11 for BF16; a token's values 2^-32 below the
  * largest of their 128 lose digits).  A slot whose id is no expert's (-1) adds nothing; an expert that
  * a token names twice counts with the sum of the weights.  Sums have a fixed
- * order.  Each chosen expert's weights are read once for up to 8 of its tokens
- * (16 with more than 8 tokens).
+ * order.  Each chosen expert's weights are read once for up to 8 of its tokens.
  *   x             device BF16 [tokens][hidden], 16-byte aligned
  *   ids, weights  device int32, float [tokens][top_k], as fp8q_moe_route
  *                 writes them; top_k <= 32
@@ -718,7 +717,8 @@ FP8Q_API fp8q_status fp8q_rmsnorm_backward(const void* d_y, int32_t dt, const vo
  * The gated activation between the two products of a block, and its copies:
  *   a[r][j] = gate * up / (1 + exp(-gate)),  gate = h[r][j], up = h[r][inner + j]
  * The copies are those of fp8q_quantize_blockwise with 1x128 groups for the
- * FP32 values of a.
+ * FP32 values of a.  1 / (1 + exp(-gate)) counts as 0 below 2^-126 (gates
+ * below some -87.3); a gate of -Inf gives NaN, as -Inf * 0 does.
  *   h    device, type dt (BF16 or FP32), [rows][2 * inner]
  *   dir  0 (no copy), MXFP8_ROW, MXFP8_COL or MXFP8_BOTH
  *   a    device, type dt, [rows][inner], or NULL

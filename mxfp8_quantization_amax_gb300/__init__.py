@@ -1096,16 +1096,16 @@ def fp8q_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     _matrix(x, "x", _VALUES, at)
     rows, cols = x.shape
     _weight(weight, cols, at)
-    o, dev, h, res, res_dt, y = out or {}, x.device, x, None, 0, None
+    o, dev, h, res_dt, y = out or {}, x.device, x, 0, None
     if residual is not None:
         _matrix(residual, "residual", _VALUES, at, (rows, cols))
-        res, res_dt = residual.data_ptr(), _IN[residual.dtype]
+        res_dt = _IN[residual.dtype]
         h = _result(o.get("h"), (rows, cols), residual.dtype, dev) if o else torch.empty_like(residual)
     rstd = _result(o.get("rstd"), (rows,), torch.float32, dev)
     if want_y:
         y = _result(o.get("y"), (rows, cols), x.dtype, dev) if o else torch.empty_like(x)
     q, si, q_t, si_t = _copies(o, direction, rows, cols, dev)
-    st = (_lib or lib()).fp8q_rmsnorm(x.data_ptr(), _IN[x.dtype], res, res_dt, weight.data_ptr(), _IN[weight.dtype], rows, cols,
+    st = (_lib or lib()).fp8q_rmsnorm(x.data_ptr(), _IN[x.dtype], _ptr(residual), res_dt, weight.data_ptr(), _IN[weight.dtype], rows, cols,
                                       eps, fmt, direction, 1 if pow2_scales else 0, h.data_ptr(), rstd.data_ptr(),
                                       *_addresses(y, q, si, q_t, si_t), _stream(at))
     if st:
@@ -1182,33 +1182,33 @@ def fp8q_swiglu_backward(h: torch.Tensor, d_a: torch.Tensor, fmt: int = E5M2, di
 # ---------------------------------------------------------------------------
 # the gradients' norm
 # ---------------------------------------------------------------------------
-def _tensors(tensors: list, name: str, at: int) -> tuple:
-    """Addresses and input types of contiguous tensors on device `at`, as int64 and int32 arrays."""
+def _types(tensors: list, name: str, at: int) -> list:
+    """The input types of contiguous tensors on device `at`."""
     types = [_IN.get(t.dtype) for t in tensors]
     if [t.get_device() for t in tensors] != [at] * len(tensors) or None in types or not all([t.is_contiguous() for t in tensors]):
         raise ValueError(f"{name} must be contiguous bfloat16 or float32 tensors on cuda:{at}")
-    return array("q", [t.data_ptr() for t in tensors]), array("i", types)
+    return types
 
 
 def _clip(grads: list, max_norm: float, out, norm):
     if not grads:
         raise ValueError("grads must hold at least one tensor")
     n, at, dev = len(grads), _device(grads[0], "grads"), grads[0].device
-    ptrs, types = _tensors(grads, "grads", at)
-    sizes = array("q", [g.numel() for g in grads])
+    types, sizes = _types(grads, "grads", at), [g.numel() for g in grads]
     outs = scale = None
+    if out is not None and (_types(out, "out", at) != types or [o.shape for o in out] != [g.shape for g in grads]):
+        raise ValueError("out must hold one tensor like each gradient")
+    norm = _result(norm, (1,), torch.float32, dev)
     if out is not None:
-        outs, out_types = _tensors(out, "out", at)
-        if out_types != types or [o.shape for o in out] != [g.shape for g in grads]:
-            raise ValueError("out must hold one tensor like each gradient")
-        written = [a for a, n_i in zip(outs, sizes) if n_i]
+        outs = [o.data_ptr() for o in out]
+        written = [a for a, size in zip(outs, sizes) if size]
         if len(set(written)) != len(written):
             raise ValueError("out holds a tensor twice")
-        scale = _empty(1, dtype=torch.float32, device=dev)
-    norm = _result(norm, (1,), torch.float32, dev)
+        outs, scale = array("q", outs), _empty(1, dtype=torch.float32, device=dev)
     L = _lib or lib()
     need = L.fp8q_clip_grads_workspace_bytes(n)
     ws = _empty(need, dtype=torch.uint8, device=dev)
+    ptrs, sizes, types = array("q", [g.data_ptr() for g in grads]), array("q", sizes), array("i", types)
     st = L.fp8q_clip_grads(ptrs.buffer_info()[0], sizes.buffer_info()[0], types.buffer_info()[0], n, max_norm,
                            None if outs is None else outs.buffer_info()[0], norm.data_ptr(), _ptr(scale), ws.data_ptr(), need,
                            _stream(at))

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kClThreads) clip_norm_kernel(const __grid_cons
 __device__ __forceinline__ float cl_norm(const double* part, int parts, double* sh) {
   double sum = 0.0;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < parts; i += kClThreads) sum += __ldg(part + i);
+  for (int i = threadIdx.x; i < parts; i += kClThreads) sum += part[i];  // written by the kernel before: no read-only load
   return (float)sqrt(cl_block_sum(sum, sh));
 }
 __device__ __forceinline__ float cl_scale(float norm, float max_norm) {

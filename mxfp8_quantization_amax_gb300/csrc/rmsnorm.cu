@@ -270,7 +270,7 @@ struct RmsNormTile {
   __device__ __forceinline__ int pitch(int) const { return (int)cols; }
   __device__ __forceinline__ void begin(int row, int col) {
 #pragma unroll
-    for (int i = 0; i < kQtRows; i++) s[i] = __ldg(rstd + row + i);
+    for (int i = 0; i < kQtRows; i++) s[i] = rstd[row + i];  // written by the kernel before: no read-only load
     rn_weight<8>(weight, weight_dt, col, w);
   }
   __device__ __forceinline__ void values(const QtRaw<DT, 8> (&in)[1], int i, int, float (&v)[8]) const {
