@@ -145,6 +145,10 @@ __device__ __forceinline__ uint32_t qt_codes4(float a, float b, float c, float d
 __device__ __forceinline__ void qt_ask(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+// The first `bytes` of them, zeros behind.
+__device__ __forceinline__ void qt_ask(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void qt_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
 __device__ __forceinline__ void qt_wait() {
@@ -159,17 +163,20 @@ __device__ __forceinline__ uint4 qt_taken(uint32_t at) {
 // Eight values for each of G consecutive lanes of a warp (lane g of them), which
 // lie side by side from value i of p on and of which `left` are there: asked
 // for in whole sectors, so that FP32 lanes read what others asked for (with a
-// __syncwarp between, both ways).
+// __syncwarp between, both ways).  ENDS: the run may end anywhere.
 template <int DT>
 constexpr int kQtRunBytes = DT == kBF16 ? 16 : 32;  // of a lane
 
-template <int DT, int G>
+template <int DT, int G, bool ENDS = false>
 __device__ __forceinline__ void qt_ask8(const void* p, int64_t i, int64_t left, uint32_t place, int g) {
   const uint8_t* from = (const uint8_t*)p + i * (DT == kBF16 ? 2 : 4);
 #pragma unroll
   for (int k = 0; k < kQtRunBytes<DT> / 16; k++) {
     const int u = k * G + g;
-    if (u * (DT == kBF16 ? 8 : 4) < left) qt_ask(place + 16 * u, from + 16 * u);
+    if (u * (DT == kBF16 ? 8 : 4) < left) {
+      if constexpr (ENDS) qt_ask(place + 16 * u, from + 16 * u, (int)min((int64_t)16, left * (DT == kBF16 ? 2 : 4) - 16 * u));
+      else qt_ask(place + 16 * u, from + 16 * u);
+    }
   }
 }
 template <int DT>

@@ -14,9 +14,10 @@
 // 120 with a CTA a row), gradients 89 us (6.0 TB/s), the transposed copy 34 us
 // more: it needs the statistics of 128 rows, and 128 rows of 4096 do not fit an
 // SM, so h is read again.  12345 x 7168, FP32 stream, y and row copy 188 us (6.1
-// TB/s).  Without a residual issue bounds it (16384 x 7168 90 us, 3.9 TB/s).  Any
-// columns, value by value: 12345 x 4097 159 us, gradients 295 us (1.0 TB/s).  One
-// row of 7168: 3.1 us, latency.
+// TB/s).  Without a residual issue bounds it (16384 x 7168 90 us, 3.9 TB/s).  Odd
+// columns: 12345 x 4097 80 us (5.0 TB/s), gradients 108 us (2.8 TB/s); value by
+// value, as unaligned tensors are taken, 159 and 295.  One row of 7168: 3.1 us,
+// latency.
 #include "quant_tile.cuh"
 
 namespace fp8q {
@@ -93,17 +94,43 @@ __device__ __forceinline__ float rn_row_sum(float v, int lanes, float* sh) {
   return v;
 }
 
+// Rows of any number of columns: a thread's chunks of eight lie on multiples of
+// eight values of memory, so the first starts `shift` = (r * cols) % 8 columns
+// before the row and the last may end behind it.  A group of threads whose rows
+// are a multiple of eight apart has one shift, and so the same columns in every row.
+// What of a chunk that starts at column c is not the row's becomes 0.
+template <bool ODD>
+__device__ __forceinline__ void rn_clear(int c, int cols, float (&v)[8]) {
+  if (ODD && (c < 0 || c + 8 > cols)) {
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (c + k < 0 || c + k >= cols) v[k] = 0.0f;
+  }
+}
+template <int DT, bool ODD, int V>
+__device__ __forceinline__ void rn_store(void* to, int64_t row, int c, int cols, float (&v)[V], bool back = false) {
+  if (ODD && (c < 0 || c + V > cols)) {
+#pragma unroll
+    for (int k = 0; k < V; k++) {
+      float one[1] = {v[k]};
+      if (c + k >= 0 && c + k < cols) qt_store<DT, 1>(to, row + c + k, one, back);
+      v[k] = one[0];
+    }
+  } else {
+    qt_store<DT, V>(to, row + c, v, back);
+  }
+}
+
 // h = v (+ what is in b) stored and rounded, and the outputs of a row whose h is
 // in the registers of p.lanes threads, V values in each of N chunks.
 template <int RT, int V>
-__device__ __forceinline__ void rn_add(const RmsNorm& p, int64_t at, float (&v)[V], const float (&b)[V]) {
+__device__ __forceinline__ void rn_add(float (&v)[V], const float (&b)[V]) {
 #pragma unroll
   for (int k = 0; k < V; k++) v[k] = __fadd_rn(v[k], b[k]);
-  qt_store<RT, V>(p.h, at, v, true);
 }
 
-template <int DT, int V, int N, class Weight>
-__device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64_t r, bool row_ok, int t, float* sh, Weight weight) {
+template <int DT, int V, int N, bool ODD, class Weight>
+__device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64_t r, bool row_ok, int t, int shift, float* sh, Weight weight) {
   float sum = 0.0f;
 #pragma unroll
   for (int n = 0; n < N; n++)
@@ -115,7 +142,7 @@ __device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64
   if (p.y == nullptr && p.q == nullptr) return;
 #pragma unroll
   for (int n = 0; n < N; n++) {
-    if (!row_ok || (n * p.lanes + t) * V >= p.cols) continue;
+    if (!row_ok || (n * p.lanes + t) * V - shift >= p.cols) continue;
     float w[V];
     weight(n, w);
     if constexpr (V == 8) {
@@ -128,7 +155,7 @@ __device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64
       v[n][0] = __fmul_rn(__fmul_rn(v[n][0], rstd), w[0]);
     }
   }
-  if constexpr (V == 8) {
+  if constexpr (V == 8 && !ODD) {
     if (p.q != nullptr) {  // 16 threads hold a group of 128 columns, N of them
       uint8_t* q = p.q + r * p.cols + 8 * t;
       float* s = p.s + r * p.tiles_c + t / 16;
@@ -142,8 +169,8 @@ __device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64
   if (p.y != nullptr) {
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      const int64_t c = (int64_t)(n * p.lanes + t) * V;
-      if (row_ok && c < p.cols) qt_store<DT, V>(p.y, r * p.cols + c, v[n]);
+      const int c = (n * p.lanes + t) * V - shift;
+      if (row_ok && c < p.cols) rn_store<DT, ODD, V>(p.y, r * p.cols, c, (int)p.cols, v[n]);
     }
   }
 }
@@ -173,49 +200,63 @@ __global__ void __launch_bounds__(T) rmsnorm_kernel(RmsNorm p) {
       if constexpr (RT != kNone) {
         float b[V];
         res[n].get(b);
-        rn_add<RT, V>(p, at(n), v[n], b);
+        rn_add<RT, V>(v[n], b);
+        qt_store<RT, V>(p.h, at(n), v[n], true);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < V; k++) v[n][k] = 0.0f;
     }
   }
-  rn_row<DT, V, N>(p, v, r, row_ok, t, sh, [&](int n, float (&w)[V]) { rn_weight<V>(p.weight, p.weight_dt, (int64_t)(n * p.lanes + t) * V, w); });
+  rn_row<DT, V, N, false>(p, v, r, row_ok, t, 0, sh, [&](int n, float (&w)[V]) { rn_weight<V>(p.weight, p.weight_dt, (int64_t)(n * p.lanes + t) * V, w); });
   pdl_launch_dependents();
 }
 
 // Many rows: CTAs stay, keep the weights in registers and have the next rows on
-// their way.
+// their way.  (More rows on their way, more CTAs with the weights in L1 instead:
+// slower.)
 constexpr int kRnChunks = 4;
 template <int DT>
 constexpr int kRnBytes = DT == kNone ? 0 : 32 * kQtRunBytes<DT>;  // of a warp's chunk of one input
 
-template <int DT, int RT, int T>
+template <int DT, int RT, int T, bool ODD>
 __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_kernel(RmsNorm p) {
   constexpr int kChunk = kRnBytes<DT> + kRnBytes<RT>;
   extern __shared__ __align__(16) uint8_t inputs[];  // [warps][chunks][kChunk]
   __shared__ float sh[64];
   const int t = threadIdx.x % p.lanes, lane = threadIdx.x & 31, per = blockDim.x / p.lanes, cols = (int)p.cols;
   const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + (threadIdx.x >> 5) * kRnChunks * kChunk;
+  const int64_t step = (int64_t)gridDim.x * per;
+  int64_t r0 = (int64_t)blockIdx.x * per;
+  const int shift = ODD ? (int)((r0 + threadIdx.x / p.lanes) * cols & 7) : 0;
   const auto ask = [&](int64_t r) {
     if (r < p.rows) {
 #pragma unroll
       for (int n = 0; n < kRnChunks; n++) {
-        const int c = (n * p.lanes + t - lane) * 8;
-        qt_ask8<DT, 32>(p.x, r * cols + c, cols - c, place + n * kChunk, lane);
-        if constexpr (RT != kNone) qt_ask8<RT, 32>(p.residual, r * cols + c, cols - c, place + n * kChunk + kRnBytes<DT>, lane);
+        const int c = (n * p.lanes + t - lane) * 8 - shift;
+        qt_ask8<DT, 32, ODD>(p.x, r * cols + c, cols - c, place + n * kChunk, lane);
+        if constexpr (RT != kNone) qt_ask8<RT, 32, ODD>(p.residual, r * cols + c, cols - c, place + n * kChunk + kRnBytes<DT>, lane);
       }
     }
     qt_commit();
   };
   pdl_wait();
-  const int64_t step = (int64_t)gridDim.x * per;
-  int64_t r0 = (int64_t)blockIdx.x * per;
   ask(r0 + threadIdx.x / p.lanes);
   float w[kRnChunks][8];
 #pragma unroll
-  for (int n = 0; n < kRnChunks; n++)
-    if ((n * p.lanes + t) * 8 < cols) rn_weight<8>(p.weight, p.weight_dt, (n * p.lanes + t) * 8, w[n]);
+  for (int n = 0; n < kRnChunks; n++) {
+    const int c = (n * p.lanes + t) * 8 - shift;
+    if (ODD) {
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        float one[1] = {0.0f};
+        if (c + k >= 0 && c + k < cols) rn_weight<1>(p.weight, p.weight_dt, c + k, one);
+        w[n][k] = one[0];
+      }
+    } else if (c < cols) {
+      rn_weight<8>(p.weight, p.weight_dt, c, w[n]);
+    }
+  }
   int turn = 0;
   for (; r0 < p.rows; r0 += step) {
     const int64_t r = r0 + threadIdx.x / p.lanes;
@@ -225,7 +266,7 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_ker
     __syncwarp();
 #pragma unroll
     for (int n = 0; n < kRnChunks; n++) {
-      const int c = (n * p.lanes + t) * 8;
+      const int c = (n * p.lanes + t) * 8 - shift;
 #pragma unroll
       for (int k = 0; k < 8; k++) v[n][k] = 0.0f;
       if (row_ok && c < cols) {
@@ -237,13 +278,15 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_ker
           float b[8];
           qt_taken8<RT>(place + n * kChunk + kRnBytes<DT>, lane, res);
           res.get(b);
-          rn_add<RT, 8>(p, r * cols + c, v[n], b);
+          rn_add<RT, 8>(v[n], b);
+          rn_store<RT, ODD, 8>(p.h, r * cols, c, cols, v[n], true);
         }
+        rn_clear<ODD>(c, cols, v[n]);
       }
     }
     __syncwarp();
     ask(r + step);
-    rn_row<DT, 8, kRnChunks>(p, v, r, row_ok, t, sh + (turn ^= 32), [&](int n, float (&u)[8]) {
+    rn_row<DT, 8, kRnChunks, ODD>(p, v, r, row_ok, t, shift, sh + (turn ^= 32), [&](int n, float (&u)[8]) {
 #pragma unroll
       for (int k = 0; k < 8; k++) u[k] = w[n][k];
     });
@@ -301,8 +344,8 @@ struct RmsNormBackward {
 };
 
 // The sums of the CTA's groups of threads, in their order, as one row of partial sums.
-template <int N>
-__device__ __forceinline__ void rn_partial(const RmsNormBackward& p, const float (&acc)[N][8], int t, int per, float* sh) {
+template <int N, bool ODD>
+__device__ __forceinline__ void rn_partial(const RmsNormBackward& p, const float (&acc)[N][8], int t, int per, int shift, float* sh) {
   float* to = p.partial + (int64_t)blockIdx.x * p.cols;
   __syncthreads();
   if (per > 1) {  // p.lanes * 8 * N values, of which cols are there, for each group
@@ -313,48 +356,68 @@ __device__ __forceinline__ void rn_partial(const RmsNormBackward& p, const float
     __syncthreads();
     for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
       float sum = 0.0f;
-      for (int i = 0; i < per; i++) sum += sh[i * N * p.lanes * 8 + c];
+      for (int i = 0; i < per; i++) sum += sh[i * N * p.lanes * 8 + c + (ODD ? (int)(((int64_t)blockIdx.x * per + i) * p.cols & 7) : 0)];
       to[c] = sum;
     }
   } else {
 #pragma unroll
     for (int n = 0; n < N; n++)
-      if ((n * p.lanes + t) * 8 < p.cols)
 #pragma unroll
-        for (int k = 0; k < 8; k++) to[(n * p.lanes + t) * 8 + k] = acc[n][k];
+      for (int k = 0; k < 8; k++) {
+        const int c = (n * p.lanes + t) * 8 + k - shift;
+        if (c < p.cols && (!ODD || c >= 0)) to[c] = acc[n][k];
+      }
   }
 }
 
 // Each group of p.lanes threads takes every gridDim.x-th set of rows and keeps
 // its columns' sums of the weight gradient.  Eight values a chunk; the next
 // rows' inputs are on their way.
-template <int DT, int HT, int T>
+template <int DT, int HT, int T, bool ODD>
 __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_kernel(RmsNormBackward p) {
   constexpr int N = kRnChunks, kFirst = kRnBytes<DT> + kRnBytes<HT>, kChunk = kFirst + kRnBytes<HT>;
   extern __shared__ __align__(16) uint8_t inputs[];  // [warps][chunks][kChunk]
   __shared__ float sh[64];
   const int t = threadIdx.x % p.lanes, lane = threadIdx.x & 31, per = blockDim.x / p.lanes, cols = (int)p.cols;
   const uint32_t place = (uint32_t)__cvta_generic_to_shared(inputs) + (threadIdx.x >> 5) * N * kChunk;
+  const int64_t step = (int64_t)gridDim.x * per;
+  int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / p.lanes;
+  const int shift = ODD ? (int)(r * cols & 7) : 0;
+  float* weights = (float*)(inputs + (T / 32) * N * kChunk) + (threadIdx.x - t) * N * 8;  // ODD: of the group's columns
+  const auto weight = [&](int n, int c, float (&w)[8]) {
+    if constexpr (ODD) {
+      const float4 a = *(const float4*)(weights + (n * p.lanes + t) * 8), b = *(const float4*)(weights + (n * p.lanes + t) * 8 + 4);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+      rn_weight<8>(p.weight, p.weight_dt, c, w);
+    }
+  };
   const auto ask = [&](int64_t r, bool past) {  // d_y and h, or d_h
     if (r < p.rows && (!past || p.d_h != nullptr)) {
 #pragma unroll
       for (int n = 0; n < N; n++) {
-        const int c = (n * p.lanes + t - lane) * 8;
+        const int c = (n * p.lanes + t - lane) * 8 - shift;
         if (past) {
-          qt_ask8<HT, 32>(p.d_h, r * cols + c, cols - c, place + n * kChunk + kFirst, lane);
+          qt_ask8<HT, 32, ODD>(p.d_h, r * cols + c, cols - c, place + n * kChunk + kFirst, lane);
         } else {
-          qt_ask8<DT, 32>(p.d_y, r * cols + c, cols - c, place + n * kChunk, lane);
-          qt_ask8<HT, 32>(p.h, r * cols + c, cols - c, place + n * kChunk + kRnBytes<DT>, lane);
+          qt_ask8<DT, 32, ODD>(p.d_y, r * cols + c, cols - c, place + n * kChunk, lane);
+          qt_ask8<HT, 32, ODD>(p.h, r * cols + c, cols - c, place + n * kChunk + kRnBytes<DT>, lane);
         }
       }
     }
     qt_commit();
   };
   pdl_wait();
-  const int64_t step = (int64_t)gridDim.x * per;
-  int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / p.lanes;
   ask(r, false);
   ask(r, true);
+  if constexpr (ODD) {
+    for (int i = t; i < N * p.lanes * 8; i += p.lanes) {
+      float one[1] = {0.0f};
+      if (i >= shift && i - shift < cols) rn_weight<1>(p.weight, p.weight_dt, i - shift, one);
+      weights[i] = one[0];
+    }
+    __syncthreads();
+  }
   float next_rstd = r < p.rows ? __ldg(p.rstd + r) : 0.0f;
   int turn = 0;
   float acc[N][8] = {};
@@ -369,7 +432,7 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_k
     for (int n = 0; n < N; n++) {
       d[n].zero();
       h[n].zero();
-      if (row_ok && (n * p.lanes + t) * 8 < cols) {
+      if (row_ok && (n * p.lanes + t) * 8 - shift < cols) {
         qt_taken8<DT>(place + n * kChunk, lane, d[n]);
         qt_taken8<HT>(place + n * kChunk + kRnBytes<DT>, lane, h[n]);
       }
@@ -380,12 +443,14 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_k
     float sum = 0.0f;
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      const int c = (n * p.lanes + t) * 8;
+      const int c = (n * p.lanes + t) * 8 - shift;
       if (c >= p.cols) continue;
       float dv[8], u[8], w[8];
-      rn_weight<8>(p.weight, p.weight_dt, c, w);
+      weight(n, c, w);
       d[n].get(dv);
       h[n].get(u);
+      rn_clear<ODD>(c, cols, dv);
+      rn_clear<ODD>(c, cols, u);
 #pragma unroll
       for (int k = 0; k < 8; k++) {
         u[k] = __fmul_rn(u[k], rstd);
@@ -398,10 +463,10 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_k
     __syncwarp();
 #pragma unroll
     for (int n = 0; n < N; n++) {
-      const int c = (n * p.lanes + t) * 8;
+      const int c = (n * p.lanes + t) * 8 - shift;
       if (!row_ok || c >= p.cols) continue;
       float dv[8], u[8], w[8];
-      rn_weight<8>(p.weight, p.weight_dt, c, w);
+      weight(n, c, w);
       d[n].get(dv);
       h[n].get(u);
 #pragma unroll
@@ -416,17 +481,17 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_backward_k
 #pragma unroll
         for (int k = 0; k < 8; k++) dv[k] = __fadd_rn(dv[k], u[k]);
       }
-      qt_store<HT, 8>(p.d_x, r * p.cols + c, dv);
+      rn_store<HT, ODD, 8>(p.d_x, r * p.cols, c, cols, dv);
     }
     __syncwarp();
     ask(r + step, true);
   }
   qt_wait<0>();
-  rn_partial<N>(p, acc, t, per, (float*)inputs);
+  rn_partial<N, ODD>(p, acc, t, per, shift, (float*)inputs);
   pdl_launch_dependents();
 }
 
-// Any columns and alignment: value by value, kRnBatch of a thread on their way at
+// Any alignment, and rows too wide for the kernel before: value by value, kRnBatch of a thread on their way at
 // a time, each row read twice; the columns' sums in shared memory, for each
 // group of threads its own.
 constexpr int kRnBatch = 4;
@@ -541,6 +606,8 @@ static bool type_ok(int32_t dt) { return dt == FP8Q_IN_BF16 || dt == FP8Q_IN_FP3
 
 // Threads of a row of which each has N chunks of V values at most: whole warps.
 static int row_lanes(int64_t cols, int v, int n) { return (int)((cols + 32 * v * n - 1) / (32 * v * n)) * 32; }
+// CTAs of kernels that stay; odd columns: groups of threads keep their shift.
+static int64_t stream_grid(int64_t sets, int64_t fit) { return sets < fit ? sets : fit & ~(int64_t)7; }
 // Rows side by side in a CTA of about `threads` threads.
 static int row_groups(int lanes, int threads) { return lanes < threads ? threads / lanes : 1; }
 
@@ -553,44 +620,47 @@ static cudaError_t launch_norm_rows(RmsNorm& p, cudaStream_t s) {
                        dim3(threads), 0, s, p);
 }
 
-template <int DT, int RT, int T>
+template <int DT, int RT, int T, bool ODD>
 static cudaError_t launch_norm_stream(RmsNorm& p, cudaStream_t s) {
   constexpr size_t kEach = (size_t)kRnChunks * (kRnBytes<DT> + kRnBytes<RT>) / 32;  // of a thread
-  p.lanes = row_lanes(p.cols, 8, kRnChunks);
+  p.lanes = row_lanes(p.cols + (ODD ? 7 : 0), 8, kRnChunks);
   const int per = row_groups(p.lanes, kRnThreads), threads = p.lanes * per;
   static PerDevice<bool> allowed;
-  const cudaError_t e = allow_smem(allowed, rmsnorm_stream_kernel<DT, RT, T>, kEach * T);
+  const cudaError_t e = allow_smem(allowed, rmsnorm_stream_kernel<DT, RT, T, ODD>, kEach * T);
   if (e != cudaSuccess) return e;
   const int64_t sets = (p.rows + per - 1) / per, fit = (T == kRnThreads ? 2 : 1) * (int64_t)sm_count();
-  return launch_kernel(rmsnorm_stream_kernel<DT, RT, T>, dim3((unsigned)(sets < fit ? sets : fit)), dim3(threads), kEach * threads, s, p);
+  return launch_kernel(rmsnorm_stream_kernel<DT, RT, T, ODD>, dim3((unsigned)stream_grid(sets, fit)), dim3(threads), kEach * threads, s, p);
 }
 
 template <int DT, int RT>
-static cudaError_t launch_norm(RmsNorm& p, bool vec, cudaStream_t s) {
-  if (!vec) return p.cols <= 8192 ? launch_norm_rows<DT, RT, 1, 8>(p, s) : launch_norm_rows<DT, RT, 1, 32>(p, s);
+static cudaError_t launch_norm(RmsNorm& p, bool aligned, cudaStream_t s) {
+  if (aligned && p.cols % 8 != 0 && p.rows > 2 * sm_count() && p.cols + 7 <= 8 * kRnChunks * kRnThreads)
+    return launch_norm_stream<DT, RT, kRnThreads, true>(p, s);
+  if (!aligned || p.cols % 8 != 0) return p.cols <= 8192 ? launch_norm_rows<DT, RT, 1, 8>(p, s) : launch_norm_rows<DT, RT, 1, 32>(p, s);
   // few rows: a row in as many threads as it has chunks
   if (p.rows <= 2 * sm_count() && p.cols <= 8192) return launch_norm_rows<DT, RT, 8, 1>(p, s);
-  if (p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_stream<DT, RT, kRnThreads>(p, s);
-  if (p.cols <= 8 * kRnChunks * 512) return launch_norm_stream<DT, RT, 512>(p, s);
+  if (p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_stream<DT, RT, kRnThreads, false>(p, s);
+  if (p.cols <= 8 * kRnChunks * 512) return launch_norm_stream<DT, RT, 512, false>(p, s);
   return launch_norm_rows<DT, RT, 8, 4>(p, s);
 }
 
 static int64_t backward_grid(int64_t rows, int per, int ctas) {
   const int64_t sets = (rows + per - 1) / per, fit = (int64_t)sm_count() * ctas, most = fit < kRnMaxPartials ? fit : kRnMaxPartials;
-  return sets < most ? sets : most;
+  return stream_grid(sets, most);
 }
 
-template <int DT, int HT, int T>
+template <int DT, int HT, int T, bool ODD>
 static cudaError_t launch_norm_backward_vec(RmsNormBackward& p, int* parts, cudaStream_t s) {
-  constexpr size_t kEach = (size_t)kRnChunks * (kRnBytes<DT> + 2 * kRnBytes<HT>) / 32;  // of a thread; > the partial sums' 4 * 8 * kRnChunks
-  p.lanes = row_lanes(p.cols, 8, kRnChunks);
+  constexpr size_t kInputs = (size_t)kRnChunks * (kRnBytes<DT> + 2 * kRnBytes<HT>) / 32;  // of a thread; > the partial sums' 4 * 8 * kRnChunks
+  constexpr size_t kEach = kInputs + (ODD ? kRnChunks * 8 * sizeof(float) : 0);
+  p.lanes = row_lanes(p.cols + (ODD ? 7 : 0), 8, kRnChunks);
   const int per = row_groups(p.lanes, kRnThreads), threads = p.lanes * per;
   static PerDevice<bool> allowed;
-  const cudaError_t e = allow_smem(allowed, rmsnorm_backward_kernel<DT, HT, T>, kEach * T);
+  const cudaError_t e = allow_smem(allowed, rmsnorm_backward_kernel<DT, HT, T, ODD>, kEach * T);
   if (e != cudaSuccess) return e;
   const int64_t grid = backward_grid(p.rows, per, T == kRnThreads ? 2 : 1);
   *parts = (int)grid;
-  return launch_kernel(rmsnorm_backward_kernel<DT, HT, T>, dim3((unsigned)grid), dim3(threads), kEach * threads, s, p);
+  return launch_kernel(rmsnorm_backward_kernel<DT, HT, T, ODD>, dim3((unsigned)grid), dim3(threads), ODD ? kEach * T : kEach * threads, s, p);
 }
 
 template <int DT, int HT>
@@ -607,9 +677,11 @@ static cudaError_t launch_norm_backward_any(RmsNormBackward& p, int* parts, cuda
 }
 
 template <int DT, int HT>
-static cudaError_t launch_norm_backward(RmsNormBackward& p, bool vec, int* parts, cudaStream_t s) {
-  if (vec && p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_backward_vec<DT, HT, kRnThreads>(p, parts, s);
-  if (vec && p.cols <= 8 * kRnChunks * 512) return launch_norm_backward_vec<DT, HT, 512>(p, parts, s);
+static cudaError_t launch_norm_backward(RmsNormBackward& p, bool aligned, int* parts, cudaStream_t s) {
+  const bool vec = aligned && p.cols % 8 == 0;
+  if (aligned && !vec && p.cols + 7 <= 8 * kRnChunks * kRnThreads) return launch_norm_backward_vec<DT, HT, kRnThreads, true>(p, parts, s);
+  if (vec && p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_backward_vec<DT, HT, kRnThreads, false>(p, parts, s);
+  if (vec && p.cols <= 8 * kRnChunks * 512) return launch_norm_backward_vec<DT, HT, 512, false>(p, parts, s);
   return launch_norm_backward_any<DT, HT>(p, parts, s);
 }
 
@@ -655,14 +727,14 @@ extern "C" fp8q_status fp8q_rmsnorm(const void* x, int32_t dt, const void* resid
   p.y = y;
   if (dir & MXFP8_ROW) p.q = q, p.s = scale_inv;
   const cudaStream_t s = (cudaStream_t)stream;
-  const bool vec = cols % 8 == 0 && !off(x, 16) && !off(residual, 16) && !off(residual ? h : nullptr, 16) &&
+  const bool aligned = !off(x, 16) && !off(residual, 16) && !off(residual ? h : nullptr, 16) &&
                    !off(weight, 16) && !off(y, 16);
   const int rt = residual ? residual_dt : kNone;
   cudaError_t e;
   if (dt == FP8Q_IN_BF16)
-    e = rt == kNone ? launch_norm<kBF16, kNone>(p, vec, s) : rt == kBF16 ? launch_norm<kBF16, kBF16>(p, vec, s) : launch_norm<kBF16, kFP32>(p, vec, s);
+    e = rt == kNone ? launch_norm<kBF16, kNone>(p, aligned, s) : rt == kBF16 ? launch_norm<kBF16, kBF16>(p, aligned, s) : launch_norm<kBF16, kFP32>(p, aligned, s);
   else
-    e = rt == kNone ? launch_norm<kFP32, kNone>(p, vec, s) : rt == kBF16 ? launch_norm<kFP32, kBF16>(p, vec, s) : launch_norm<kFP32, kFP32>(p, vec, s);
+    e = rt == kNone ? launch_norm<kFP32, kNone>(p, aligned, s) : rt == kBF16 ? launch_norm<kFP32, kBF16>(p, aligned, s) : launch_norm<kFP32, kFP32>(p, aligned, s);
   if (e != cudaSuccess) return cuda_fail(e, "rmsnorm kernel launch");
   if (dir & MXFP8_COL) {
     QtOut o{};
@@ -730,11 +802,11 @@ extern "C" fp8q_status fp8q_rmsnorm_backward(const void* d_y, int32_t dt, const 
     p.one_over_cols = 1.0f / (float)cols;
     p.d_x = d_x;
     p.partial = (float*)workspace;
-    const bool vec = cols % 8 == 0 && !off(d_y, 16) && !off(h, 16) && !off(weight, 16) && !off(d_h, 16) && !off(d_x, 16);
+    const bool aligned = !off(d_y, 16) && !off(h, 16) && !off(weight, 16) && !off(d_h, 16) && !off(d_x, 16);
     if (dt == FP8Q_IN_BF16)
-      e = h_dt == FP8Q_IN_BF16 ? launch_norm_backward<kBF16, kBF16>(p, vec, &parts, s) : launch_norm_backward<kBF16, kFP32>(p, vec, &parts, s);
+      e = h_dt == FP8Q_IN_BF16 ? launch_norm_backward<kBF16, kBF16>(p, aligned, &parts, s) : launch_norm_backward<kBF16, kFP32>(p, aligned, &parts, s);
     else
-      e = h_dt == FP8Q_IN_BF16 ? launch_norm_backward<kFP32, kBF16>(p, vec, &parts, s) : launch_norm_backward<kFP32, kFP32>(p, vec, &parts, s);
+      e = h_dt == FP8Q_IN_BF16 ? launch_norm_backward<kFP32, kBF16>(p, aligned, &parts, s) : launch_norm_backward<kFP32, kFP32>(p, aligned, &parts, s);
     if (e != cudaSuccess) return cuda_fail(e, "rmsnorm gradient launch");
   }
   e = launch_kernel(rmsnorm_weight_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(32 * kRnSumWarps), 0, s,

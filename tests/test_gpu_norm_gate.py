@@ -218,6 +218,53 @@ def test_norm_backward(dt, ht, wt, rows, cols):
         assert torch.equal(fq.fp8q_rmsnorm_backward(d_y, h, w, rstd, d_h, out={"d_x": d_h})["d_x"], want)
 
 
+# rows enough for CTAs that stay; columns whose rows start at every place of eight, the widest that stay and beyond
+ODD = [(2500, 1), (2501, 7), (1219, 250), (3001, 1023), (700, 4097), (650, 4100), (333, 8185), (340, 8186)]
+
+
+@pytest.mark.parametrize("dt,rt", [(BF16, None), (BF16, BF16), (FP32, FP32), (BF16, FP32), (FP32, None), (FP32, BF16)])
+@pytest.mark.parametrize("rows,cols", ODD)
+def test_norm_many_rows_of_any_columns(dt, rt, rows, cols):
+    """A row's neighbours in its first and last eight values do not reach it, and are not written."""
+    fq = require_cuda()
+    x, res, w = norm_inputs(rows, cols, dt, rt, FP32 if cols % 2 else BF16, cols)
+    x[17] = float("nan")
+    x[rows - 2] = float("inf")
+    bufs = {"y": Guarded((rows, cols), dt), "rstd": Guarded((rows,), FP32)} | ({"h": Guarded((rows, cols), rt)} if rt else {})
+    r = fq.fp8q_rmsnorm(x, w, res, direction=0, want_y=True, out={k: b.t for k, b in bufs.items()})
+    assert torch.isnan(r["y"][17]).all() and torch.isnan(r["y"]).sum(1).count_nonzero() == 2 and torch.isnan(r["rstd"]).sum() == 1
+    keep = torch.tensor([i for i in range(rows) if i not in (17, rows - 2)], device="cuda")
+    check_norm({k: r[k][keep] if k in ("h", "rstd", "y") else None for k in r}, x[keep], None if rt is None else res[keep], w, 1e-6, 0, 0, True)
+    for b in bufs.values():
+        b.check()
+    if rt:  # in place, and the same values
+        again = fq.fp8q_rmsnorm(x, w, res, direction=0, want_y=True, out={"h": res})
+        for k in ("h", "rstd", "y"):
+            assert torch.equal(again[k].nan_to_num(7.0), r[k].nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dt,ht", [(BF16, BF16), (BF16, FP32), (FP32, BF16), (FP32, FP32)])
+@pytest.mark.parametrize("rows,cols", ODD)
+def test_norm_backward_many_rows_of_any_columns(dt, ht, rows, cols):
+    fq = require_cuda()
+    g = gen(rows + cols)
+    h = (3 * torch.randn(rows, cols, device="cuda", generator=g)).to(ht)
+    d_y = torch.randn(rows, cols, device="cuda", generator=g).to(dt)
+    w = (1 + 0.3 * torch.randn(cols, device="cuda", generator=g)).to(ht)
+    rstd = 1 / (h.float().square().mean(1) + 1e-6).sqrt()
+    d_h = None if rows % 2 else torch.randn(rows, cols, device="cuda", generator=g).to(ht)
+    out = {"d_x": Guarded((rows, cols), ht), "d_weight": Guarded((cols,), FP32)}
+    got = fq.fp8q_rmsnorm_backward(d_y, h, w, rstd, d_h, out={k: b.t for k, b in out.items()})
+    check_norm_backward(got, d_y, h, w, rstd, d_h)
+    for b in out.values():
+        b.check()
+    d_y[21] = float("nan")  # stays in its row
+    poisoned = fq.fp8q_rmsnorm_backward(d_y, h, w, rstd, d_h, out=None if d_h is None else {"d_x": d_h})
+    keep = torch.arange(rows, device="cuda") != 21
+    assert torch.equal(poisoned["d_x"][keep], got["d_x"][keep]) and torch.isnan(poisoned["d_x"][21]).all()
+    assert torch.isnan(poisoned["d_weight"]).all()
+
+
 def test_norm_gradient_against_differences():
     """A step of 2^-12 both ways in 64 bits: its error is some 2^-24 of the third derivative, far below the bound
     of 2^-14 of the sum of magnitudes, which also covers FP32."""
