@@ -11,11 +11,11 @@
 //
 // Bound by memory where rows are many: CTAs stay and have the next rows' inputs
 // on their way.  16384 x 4096 BF16 with the residual: row copy 71 us (6.6 TB/s;
-// 120 with a CTA a row), gradients 89 us (6.0 TB/s), the transposed copy 34 us
+// 120 with a CTA a row), gradients 87 us (6.2 TB/s), the transposed copy 34 us
 // more: it needs the statistics of 128 rows, and 128 rows of 4096 do not fit an
 // SM, so h is read again.  12345 x 7168, FP32 stream, y and row copy 188 us (6.1
 // TB/s).  Without a residual issue bounds it (16384 x 7168 90 us, 3.9 TB/s).  Odd
-// columns: 12345 x 4097 80 us (5.0 TB/s), gradients 108 us (2.8 TB/s); value by
+// columns: 12345 x 4097 80 us (5.0 TB/s), gradients 107 us (2.8 TB/s); value by
 // value, as unaligned tensors are taken, 159 and 295.  One row of 7168: 3.1 us,
 // latency.
 #include "quant_tile.cuh"
@@ -573,8 +573,8 @@ __global__ void __launch_bounds__(kRnThreads) rmsnorm_backward_any_kernel(RmsNor
   pdl_launch_dependents();
 }
 
-// d_weight[c] = the sum of `parts` rows of partial sums, eight warps a column in a fixed order.
-constexpr int kRnSumWarps = 8;
+// d_weight[c] = the sum of `parts` rows of partial sums, kRnSumWarps warps to 32 columns in a fixed order.
+constexpr int kRnSumWarps = 32;  // 8: 2 us slower
 
 __global__ void __launch_bounds__(32 * kRnSumWarps) rmsnorm_weight_kernel(const float* partial, int parts, int64_t cols,
                                                                            float* d_weight) {
