@@ -21,7 +21,7 @@
 // Bound by the weights' bytes: 64 experts of 7168 x 2048, 8 a token: 1 token 60
 // us (352 MB, 5.8 TB/s; some 7 us are the two kernels' start, lists and end), 4
 // tokens 178, 16 tokens 380 (6.6 TB/s).  Beyond 8 tokens an expert its weights are
-// read again, from L2, and converted again: 64 tokens 560 us (floor 421).  Sizes
+// read again, from L2, and converted again: 64 tokens 548 us (floor 421).  Sizes
 // whose K leaves warps idle cost more: 61 tokens, 40 experts of 2064 x 1360 97
 // us (floor 50).  Jobs of 16 tokens were slower everywhere (64 tokens 767 then
 // against 677): their registers leave one CTA an SM.
@@ -63,7 +63,7 @@ struct MdParams {
 // The (token, expert) pairs in order of expert, and jobs of up to 8 of one
 // expert's.  Where the lists lie in shared memory, for `slots` slots:
 struct MdLists {
-  uint32_t* job;     // expert | tokens << 16
+  uint32_t* job;     // expert | tokens << 16 | place among the expert's jobs << 20 | their number << 24
   uint16_t* first;   // first pair of a job
   uint8_t* token;    // of a pair
   float* weight;     // of a pair (an expert that a token names twice counts twice); second kernel only
@@ -130,8 +130,9 @@ __device__ __forceinline__ void md_lists(const MdParams& p, MdLists& l, uint8_t*
       l.token[i] = (uint8_t)(__ffsll((long long)m) - 1);
       if (WEIGHTS) expert[i] = (uint16_t)e;
     }
-    for (; n > 0; n -= kMdCols, pair += kMdCols, job++) {
-      l.job[job] = (uint32_t)e | (uint32_t)min(n, kMdCols) << 16;
+    const uint32_t jobs = (n + kMdCols - 1) / kMdCols;
+    for (uint32_t place = 0; n > 0; n -= kMdCols, pair += kMdCols, job++, place++) {
+      l.job[job] = (uint32_t)e | (uint32_t)min(n, kMdCols) << 16 | place << 20 | jobs << 24;
       l.first[job] = (uint16_t)pair;
     }
   }
@@ -273,7 +274,7 @@ __device__ __forceinline__ MdUnit md_unit(const MdParams& p, const MdLists& l, i
   const int per = p.kb2 * (128 / kMdUnit), job = unit / per;
   MdUnit u;
   u.expert = l.job[job] & 0xFFFF;
-  u.count = l.job[job] >> 16;
+  u.count = l.job[job] >> 16 & 15;
   u.first = l.first[job];
   u.inner0 = (unit - job * per) * kMdUnit;
   return u;
@@ -448,18 +449,45 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_first_kernel(MdParams p)
 // ---------------------------------------------------------------------------
 // second product and the weighted sum
 // ---------------------------------------------------------------------------
-// A place in the list of all jobs' blocks of K.
+// A place in the list of all jobs' blocks of K.  The jobs of one expert take
+// turns every kMdTurn blocks, so that the second finds the weights in L2: all
+// warps together read some 150 MB in 16 blocks (64 tokens, 64 experts of 7168 x 2048
+// 548 us, 562 without turns, 553 with 4 blocks each).
+constexpr int kMdTurn = 8;
+
 struct MdPlace {
   int job, kb, count, first;
+  __device__ __forceinline__ void start(const MdParams& p, const MdLists& l, int at) {
+    job = at / p.kb2;
+    const int place = l.job[job] >> 20 & 15, jobs = l.job[job] >> 24;
+    job -= place;
+    at -= job * p.kb2;  // among the expert's
+    kb = 0;
+    if (jobs > 1) kb = at / (jobs * kMdTurn) * kMdTurn;
+    at -= kb * jobs;
+    const int turn = jobs > 1 ? min(kMdTurn, p.kb2 - kb) : p.kb2;
+    job += at / turn;
+    kb += at % turn;
+  }
   __device__ __forceinline__ void at_job(const MdLists& l) {
-    count = l.job[job] >> 16;
+    count = l.job[job] >> 16 & 15;
     first = l.first[job];
   }
   // to the next block; whether that is another job's
-  __device__ __forceinline__ bool next(const MdParams& p) {
-    if (++kb < p.kb2) return false;
-    kb = 0;
-    job++;
+  __device__ __forceinline__ bool next(const MdParams& p, const MdLists& l) {
+    kb++;
+    if (kb < p.kb2 && kb % kMdTurn != 0) return false;
+    const uint32_t place = l.job[job] >> 20 & 15, jobs = l.job[job] >> 24;
+    if (place + 1 < jobs) {  // the expert's next job, from where this turn began
+      job++;
+      kb = (kb - 1) / kMdTurn * kMdTurn;
+    } else if (kb < p.kb2) {  // the expert's next turn
+      job -= place;
+      return jobs > 1;
+    } else {
+      job++;
+      kb = 0;
+    }
     return true;
   }
 };
@@ -484,7 +512,7 @@ __device__ __forceinline__ void md_feed2(const MdParams& p, const MdLists& l, in
     if ((threadIdx.x & 31) == 0) md_copy4(scale, f.scale);
     f.from += 128;
     f.scale++;
-    if (f.at.next(p) && f.left > 1) md_feed2_job(p, l, row0, f);
+    if (f.at.next(p, l) && f.left > 1) md_feed2_job(p, l, row0, f);
     f.left--;
   }
   md_commit();
@@ -534,13 +562,12 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
   const uint32_t ring = md_smem(rings) + warp * kRing, sc_at = md_smem(&scales[warp][0]);
   const uint32_t tile_at = ring + lane * 128 + ((lane & 7) << 4);
   MdPlace at;  // of the inner values asked for last
-  at.job = begin / p.kb2;
-  at.kb = begin - at.job * p.kb2;
   MdFeed2 f;
-  f.at = at;
   f.left = end - begin;
   if (begin < end) {
+    at.start(p, l, begin);
     at.at_job(l);
+    f.at = at;
     md_feed2_job(p, l, row0, f);
   }
 #pragma unroll
@@ -556,7 +583,7 @@ __global__ void __launch_bounds__(kMdThreads, 2) decode_second_kernel(MdParams p
   for (int left = end - begin; left > 0; left--) {
     const MdInner<LO> a = next;
     const int count = at.count, first = at.first;
-    const bool last = at.next(p);  // of its job
+    const bool last = at.next(p, l);  // of its job's turn
     if (left > 1) {
       if (last) at.at_job(l);
       next.load(p, at);
