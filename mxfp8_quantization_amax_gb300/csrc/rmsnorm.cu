@@ -14,7 +14,7 @@
 // 120 with a CTA a row), gradients 87 us (6.2 TB/s), the transposed copy 34 us
 // more: it needs the statistics of 128 rows, and 128 rows of 4096 do not fit an
 // SM, so h is read again.  12345 x 7168, FP32 stream, y and row copy 188 us (6.1
-// TB/s).  Without a residual issue bounds it (16384 x 7168 90 us, 3.9 TB/s).  Odd
+// TB/s).  Without a residual issue bounds it (16384 x 7168 78 us, 4.5 TB/s).  Odd
 // columns: 12345 x 4097 80 us (5.0 TB/s), gradients 107 us (2.8 TB/s); value by
 // value, as unaligned tensors are taken, 159 and 295.  One row of 7168: 3.1 us,
 // latency.
@@ -222,6 +222,8 @@ constexpr int kRnBytes = DT == kNone ? 0 : 32 * kQtRunBytes<DT>;  // of a warp's
 template <int DT, int RT, int T, bool ODD>
 __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_kernel(RmsNorm p) {
   constexpr int kChunk = kRnBytes<DT> + kRnBytes<RT>;
+  // Without a residual instructions bound it: addresses go from row to row, and chunks behind the row are 0 from the start.
+  constexpr bool kLean = RT == kNone && !ODD;
   extern __shared__ __align__(16) uint8_t inputs[];  // [warps][chunks][kChunk]
   __shared__ float sh[64];
   const int t = threadIdx.x % p.lanes, lane = threadIdx.x & 31, per = blockDim.x / p.lanes, cols = (int)p.cols;
@@ -229,8 +231,21 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_ker
   const int64_t step = (int64_t)gridDim.x * per;
   int64_t r0 = (int64_t)blockIdx.x * per;
   const int shift = ODD ? (int)((r0 + threadIdx.x / p.lanes) * cols & 7) : 0;
+  constexpr int kSize = DT == kBF16 ? 2 : 4;
+  const uint8_t* from = (const uint8_t*)p.x + ((r0 + threadIdx.x / p.lanes) * cols + (t - lane) * 8) * kSize + lane * 16;
+  const int64_t from_step = step * cols * kSize;
   const auto ask = [&](int64_t r) {
-    if (r < p.rows) {
+    if (kLean) {
+      if (r < p.rows) {
+#pragma unroll
+        for (int n = 0; n < kRnChunks; n++)
+#pragma unroll
+          for (int k = 0; k < kSize / 2; k++)
+            if ((n * p.lanes + t - lane) * 8 + (k * 32 + lane) * (16 / kSize) < cols)
+              qt_ask(place + n * kChunk + (k * 32 + lane) * 16, from + n * p.lanes * 8 * kSize + k * 512);
+        from += from_step;
+      }
+    } else if (r < p.rows) {
 #pragma unroll
       for (int n = 0; n < kRnChunks; n++) {
         const int c = (n * p.lanes + t - lane) * 8 - shift;
@@ -241,6 +256,10 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_ker
     qt_commit();
   };
   pdl_wait();
+  if constexpr (kLean) {
+    for (unsigned i = threadIdx.x; i < blockDim.x / 32 * kRnChunks * kChunk / 16; i += blockDim.x) ((uint4*)inputs)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
   ask(r0 + threadIdx.x / p.lanes);
   float w[kRnChunks][8];
 #pragma unroll
@@ -269,7 +288,7 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_ker
       const int c = (n * p.lanes + t) * 8 - shift;
 #pragma unroll
       for (int k = 0; k < 8; k++) v[n][k] = 0.0f;
-      if (row_ok && c < cols) {
+      if (kLean || (row_ok && c < cols)) {
         QtRaw<DT, 8> raw;
         qt_taken8<DT>(place + n * kChunk, lane, raw);
         raw.get(v[n]);
