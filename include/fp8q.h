@@ -733,7 +733,9 @@ FP8Q_API fp8q_status fp8q_swiglu(const void* h, int32_t dt, int64_t rows, int64_
 /*
  * The gradient of fp8q_swiglu with respect to h, with s = 1 / (1 + exp(-gate)):
  *   d_h[r][j] = d_a * up * s * (1 + gate * (1 - s)),  d_h[r][inner + j] = d_a * gate * s
- * and its copies (of the [rows][2 * inner] matrix; inner % 8 == 0).
+ * and its copies (of the [rows][2 * inner] matrix; inner % 8 == 0).  The slope
+ * of the activation reaches 1.1: the gate's half may be Inf where up or d_a is
+ * beyond 3e38 and the other one below 1.
  *   d_a  device, type dt, [rows][inner]
  *   d_h  device, type dt, [rows][2 * inner], or NULL
  */

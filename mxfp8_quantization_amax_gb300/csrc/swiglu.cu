@@ -8,14 +8,14 @@
 // values.  exp(-g) = 2^(-g log2 e), the product as a sum of two FP32 numbers:
 // the larger goes to the exponential instruction, the smaller, l, comes in as
 // 1 + l ln 2.  In the exponential a gate counts as one within [-88.5, 127]; s is
-// 0 where it would be below 2^-126 (gates below -87.3).  FP32 throughout, the
-// products of two BF16 inputs exact; codes are made from the FP32 values, a
-// dense output is rounded once.
+// 0 where it would be below 2^-126 (gates below -87.3).  FP32 throughout;
+// codes are made from the FP32 values, a dense output is rounded once.
 //
-// Both copies: tiles (quant_tile.cuh).  65536 x 2048 124 us (6.6 TB/s), the
-// gradient of 16384 x 14336 403 us (5.9 TB/s, issue 67%; 690 with a sigmoid and
-// a read of the inputs for each half).  The row copy alone 100 us (6.7 TB/s) and
-// 276 us (6.9 TB/s).  128 rows of 2048: 1.4 us, in a call of 17.
+// Both copies: tiles (quant_tile.cuh).  65536 x 2048 128 us (6.3 TB/s), the
+// gradient of 16384 x 14336 419 us (5.7 TB/s; an earlier form 690 with a sigmoid
+// and a read of the inputs for each half, 486 with one for both).  The row copy
+// alone 101 us (6.7 TB/s) and 286 us (6.6 TB/s).  128 rows of 2048: 1.4 us, in a
+// call of 17.
 #include "quant_tile.cuh"
 
 namespace fp8q {
@@ -29,7 +29,7 @@ __device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(u));
 }
 
-// Pairs of inputs as QtRaw::pair gives them: their values, those within [-88.5, 127], products.
+// Pairs of inputs as QtRaw::pair gives them: their values, those within [-88.5, 127].
 template <int P>
 __device__ __forceinline__ void sg_values(uint2 w, float& x0, float& x1) {
   if constexpr (P == kBF16) qt_halves(w.x, x0, x1);
@@ -46,15 +46,19 @@ __device__ __forceinline__ void sg_within(uint2 w, float& x0, float& x1) {
     x1 = fmaxf(fminf(__uint_as_float(w.y), 127.0f), -88.5f);
   }
 }
+// The larger magnitude of each of two pairs with the sign of their product, and the smaller magnitude; NaN stays.
 template <int P>
-__device__ __forceinline__ void sg_product(uint2 a, uint2 b, float& x0, float& x1) {
+__device__ __forceinline__ void sg_order(uint2 a, uint2 b, uint2& big, uint2& small) {
   if constexpr (P == kBF16) {
-    asm("{\n\t.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %2;\n\tmov.b32 {c, d}, %3;\n\t"
-        "fma.rn.f32.bf16 %0, a, c, %4;\n\tfma.rn.f32.bf16 %1, b, d, %4;\n\t}"
-        : "=f"(x0), "=f"(x1) : "r"(a.x), "r"(b.x), "f"(-0.0f));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(big.x) : "r"(a.x), "r"(b.x));
+    asm("min.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(small.x) : "r"(a.x), "r"(b.x));
+    small.x &= 0x7FFF7FFFu;
   } else {
-    x0 = __uint_as_float(a.x), x1 = __uint_as_float(a.y);
-    mul2(x0, x1, __uint_as_float(b.x), __uint_as_float(b.y));
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=r"(big.x) : "r"(a.x), "r"(b.x));
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=r"(big.y) : "r"(a.y), "r"(b.y));
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=r"(small.x) : "r"(a.x), "r"(b.x));
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=r"(small.y) : "r"(a.y), "r"(b.y));
+    small.x &= 0x7FFFFFFFu, small.y &= 0x7FFFFFFFu;
   }
 }
 
@@ -78,46 +82,67 @@ __device__ __forceinline__ void sg_sigmoid(uint2 gate, float& s0, float& s1, flo
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s1) : "f"(g1));
 }
 
+// x0, x1 = values of w times x0, x1.
+template <int P>
+__device__ __forceinline__ void sg_times(uint2 w, float& x0, float& x1) {
+  float v0, v1;
+  sg_values<P>(w, v0, v1);
+  mul2(x0, x1, v0, v1);
+}
+
+// The sigmoid comes first in every product, so that none leaves FP32's range
+// where the result does not: gate * s lies between -0.28 and the gate.
 template <int P>
 __device__ __forceinline__ void sg_forward(uint2 gate, uint2 up, float& a0, float& a1) {
   float s0, s1, e0, e1;
   sg_sigmoid<P>(gate, s0, s1, e0, e1);
-  sg_product<P>(gate, up, a0, a1);
+  sg_values<P>(gate, a0, a1);
   mul2(a0, a1, s0, s1);
+  sg_times<P>(up, a0, a1);
+}
+
+// The slope of gate * s, s (1 + gate (1 - s)), lies between -0.1 and 1.1; of up and
+// d_a the larger comes first, as slope * smaller could fall below the range.  (The
+// products of two inputs first, again with the sigmoid first where that gave Inf
+// or NaN: no faster, 131 us against 128 for 65536 x 2048 in both copies.)
+template <int P>
+__device__ __forceinline__ void sg_slope(uint2 up, uint2 d, float g0, float g1, float s0, float s1, float e0, float e1, float& o0, float& o1) {
+  mul2(e0, e1, s0, s1);
+  fma2(g0, g1, e0, e1, 1.0f, 1.0f);
+  mul2(g0, g1, s0, s1);
+  uint2 big, small;
+  sg_order<P>(up, d, big, small);
+  sg_times<P>(big, g0, g1);
+  sg_times<P>(small, g0, g1);
+  o0 = g0, o1 = g1;
 }
 
 // One half of d_h: of the gate (UP false) or of the up branch.
 template <bool UP, int P>
 __device__ __forceinline__ void sg_backward(uint2 gate, uint2 up, uint2 d, float& o0, float& o1) {
-  float s0, s1, e0, e1;
+  float s0, s1, e0, e1, g0, g1;
   sg_sigmoid<P>(gate, s0, s1, e0, e1);
+  sg_values<P>(gate, g0, g1);
   if constexpr (UP) {
-    sg_product<P>(d, gate, o0, o1);
+    mul2(g0, g1, s0, s1);
+    sg_times<P>(d, g0, g1);
+    o0 = g0, o1 = g1;
   } else {
-    float g0, g1;
-    sg_values<P>(gate, g0, g1);
-    mul2(e0, e1, s0, s1);
-    fma2(g0, g1, e0, e1, 1.0f, 1.0f);
-    sg_product<P>(d, up, o0, o1);
-    mul2(o0, o1, g0, g1);
+    sg_slope<P>(up, d, g0, g1, s0, s1, e0, e1, o0, o1);
   }
-  mul2(o0, o1, s0, s1);
 }
 
 // Both.
 template <int P>
 __device__ __forceinline__ void sg_both(uint2 gate, uint2 up, uint2 d, float& g0, float& g1, float& u0, float& u1) {
-  float s0, s1, e0, e1, x0, x1, y0, y1;
+  float s0, s1, e0, e1, x0, x1;
   sg_sigmoid<P>(gate, s0, s1, e0, e1);
-  sg_product<P>(d, gate, y0, y1);
-  mul2(y0, y1, s0, s1);
   sg_values<P>(gate, x0, x1);
-  mul2(e0, e1, s0, s1);
-  fma2(x0, x1, e0, e1, 1.0f, 1.0f);
-  sg_product<P>(d, up, e0, e1);
-  mul2(e0, e1, x0, x1);
-  mul2(e0, e1, s0, s1);
-  g0 = e0, g1 = e1, u0 = y0, u1 = y1;
+  float y0 = x0, y1 = x1;
+  mul2(y0, y1, s0, s1);
+  sg_times<P>(d, y0, y1);
+  sg_slope<P>(up, d, x0, x1, s0, s1, e0, e1, g0, g1);
+  u0 = y0, u1 = y1;
 }
 
 template <int DT>
