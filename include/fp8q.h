@@ -757,9 +757,8 @@ FP8Q_API size_t fp8q_clip_grads_workspace_bytes(int32_t count);
  * NaN gives NaN.
  *   grads, out  host arrays of `count` device pointers; a tensor may be
  *               overwritten by its own output (out[i] == grads[i]; with
- *               scale 1 it is then left alone), no other overlap; the same
- *               gradient twice counts twice, the same output twice is not
- *               allowed
+ *               scale 1 it is then left alone); an output that overlaps
+ *               another tensor is refused; the same gradient twice counts twice
  *   sizes       host int64 [count]: values of each tensor (0 for none)
  *   dts         host int32 [count]: FP8Q_IN_BF16 or FP8Q_IN_FP32, of the
  *               gradient and its output

@@ -1224,7 +1224,8 @@ def fp8q_grad_norm(grads, out: torch.Tensor | None = None) -> torch.Tensor:
 
 def fp8q_clip_grads(grads, max_norm: float, out: list | None = None) -> dict:
     """The tensors `grads` (BF16 or FP32) scaled by min(1, max_norm / (norm + 1e-6)): dict(norm float32 [1], scale
-    float32 [1], grads: a tensor like each).  `out` holds the tensors to write; `grads` itself clips in place."""
+    float32 [1], grads: a tensor like each).  `out` holds the tensors to write, none of which may
+    overlap another one; `grads` itself clips in place."""
     grads = list(grads)
     out = [torch.empty_like(g) for g in grads] if out is None else list(out)
     norm, scale = _clip(grads, max_norm, out, None)

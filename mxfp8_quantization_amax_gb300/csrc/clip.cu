@@ -16,6 +16,9 @@
 // read, 7.3 TB/s; 845 to read and write, 6.7 TB/s), 180M BF16 values 163 us.
 #include <math.h>
 
+#include <algorithm>
+#include <new>
+
 #include "quant_tile.cuh"
 
 namespace fp8q {
@@ -235,6 +238,32 @@ struct ClWalk {
   }
 };
 
+// Bytes of a gradient, of an output, or of a tensor that is both.
+struct ClRange {
+  uintptr_t lo, hi;
+  bool out;
+};
+
+// Whether an output overlaps another tensor.  In the order of their starts a
+// range overlaps one before it if that one ends behind its start.
+static bool overlapping(const void* const* g, void* const* out, const int64_t* n, const int32_t* dt, int count, ClRange* r) {
+  int ranges = 0;
+  for (int i = 0; i < count; i++) {
+    if (n[i] == 0) continue;
+    const uintptr_t bytes = (uintptr_t)n[i] * (dt[i] == FP8Q_IN_BF16 ? 2 : 4), from = (uintptr_t)g[i], to = (uintptr_t)out[i];
+    r[ranges++] = ClRange{to, to + bytes, true};
+    if (from != to) r[ranges++] = ClRange{from, from + bytes, false};
+  }
+  std::sort(r, r + ranges, [](const ClRange& a, const ClRange& b) { return a.lo < b.lo; });
+  uintptr_t read = 0, written = 0;  // ends of the ranges so far
+  for (int i = 0; i < ranges; i++) {
+    if (r[i].lo < written || (r[i].out && r[i].lo < read)) return true;
+    uintptr_t& end = r[i].out ? written : read;
+    end = std::max(end, r[i].hi);
+  }
+  return false;
+}
+
 }  // namespace fp8q
 
 using namespace fp8q;
@@ -266,6 +295,13 @@ extern "C" fp8q_status fp8q_clip_grads(const void* const* grads, const int64_t* 
   }
   if (!workspace || off(workspace, 8) || workspace_bytes < fp8q_clip_grads_workspace_bytes(count))
     return fail(FP8Q_ERR_INVALID_ARG, "workspace must be 8-byte aligned and of fp8q_clip_grads_workspace_bytes()");
+  if (out) {
+    ClRange few[128], *ranges = count <= 64 ? few : new (std::nothrow) ClRange[2 * (size_t)count];
+    if (!ranges) return fail(FP8Q_ERR_UNSUPPORTED, "no host memory for %d tensors", count);
+    const bool bad = overlapping(grads, out, sizes, dts, count, ranges);
+    if (ranges != few) delete[] ranges;
+    if (bad) return fail(FP8Q_ERR_INVALID_ARG, "an output overlaps another tensor");
+  }
   const cudaStream_t s = (cudaStream_t)stream;
   const int most = 8 * sm_count() < kClParts ? 8 * sm_count() : kClParts;
   ClTable t;
