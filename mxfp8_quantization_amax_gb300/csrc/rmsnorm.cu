@@ -16,7 +16,7 @@
 // SM, so h is read again.  12345 x 7168, FP32 stream, y and row copy 188 us (6.1
 // TB/s).  Without a residual issue bounds it (16384 x 7168 78 us, 4.5 TB/s).  Odd
 // columns: 12345 x 4097 80 us (5.0 TB/s), gradients 107 us (2.8 TB/s); value by
-// value, as unaligned tensors are taken, 159 and 295.  One row of 7168: 3.1 us,
+// value, as unaligned tensors are taken, 159 and 295.  One row of 7168: 2.8 us,
 // latency.
 #include "quant_tile.cuh"
 
@@ -121,14 +121,13 @@ __device__ __forceinline__ void rn_store(void* to, int64_t row, int c, int cols,
   }
 }
 
-// h = v (+ what is in b) stored and rounded, and the outputs of a row whose h is
-// in the registers of p.lanes threads, V values in each of N chunks.
-template <int RT, int V>
+template <int V>
 __device__ __forceinline__ void rn_add(float (&v)[V], const float (&b)[V]) {
 #pragma unroll
   for (int k = 0; k < V; k++) v[k] = __fadd_rn(v[k], b[k]);
 }
 
+// The outputs of a row whose h is in the registers of p.lanes threads, V values in each of N chunks.
 template <int DT, int V, int N, bool ODD, class Weight>
 __device__ __forceinline__ void rn_row(const RmsNorm& p, float (&v)[N][V], int64_t r, bool row_ok, int t, int shift, float* sh, Weight weight) {
   float sum = 0.0f;
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__(T) rmsnorm_kernel(RmsNorm p) {
       if constexpr (RT != kNone) {
         float b[V];
         res[n].get(b);
-        rn_add<RT, V>(v[n], b);
+        rn_add<V>(v[n], b);
         qt_store<RT, V>(p.h, at(n), v[n], true);
       }
     } else {
@@ -297,7 +296,7 @@ __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_ker
           float b[8];
           qt_taken8<RT>(place + n * kChunk + kRnBytes<DT>, lane, res);
           res.get(b);
-          rn_add<RT, 8>(v[n], b);
+          rn_add<8>(v[n], b);
           rn_store<RT, ODD, 8>(p.h, r * cols, c, cols, v[n], true);
         }
         rn_clear<ODD>(c, cols, v[n]);
@@ -651,13 +650,24 @@ static cudaError_t launch_norm_stream(RmsNorm& p, cudaStream_t s) {
   return launch_kernel(rmsnorm_stream_kernel<DT, RT, T, ODD>, dim3((unsigned)stream_grid(sets, fit)), dim3(threads), kEach * threads, s, p);
 }
 
+// Which kernel; each edge with both sides measured (us, BF16, in a graph).
+// Few short rows: a row in as many threads as it has chunks, nothing on its way;
+//   row copy, residual: 64 x 2048 2.1 (2.8 by CTAs that stay), 304 x 2048 2.4 (2.7),
+//   608 x 2048 2.9 (2.9), 64 x 4096 2.4 (2.7), 304 x 4096 3.2 (2.9), 64 x 5120 2.7 (2.7),
+//   64 x 7168 3.2 (2.7), 1 x 7168 3.0 (2.6);
+//   y of odd columns: 304 x 1001 4.0 (4.7), 304 x 4097 5.5 (4.9), 64 x 8185 6.1 (4.7).
+// More than 8192 columns: 512 threads that stay, against 1024 that go, 4000 rows, residual
+//   (without): 8208 49 and 57 (35 and 29), 12288 58 and 86 (37 and 44), 16384 70 and 105 (43 and 54).
+// More than 16384 columns: 1024 threads, whose 64 registers spill: 4000 x 32768 228 (floor 138).
+// Unaligned, or odd columns beyond 8185: value by value (y of 4000 x 32767 651, floor 157).
 template <int DT, int RT>
 static cudaError_t launch_norm(RmsNorm& p, bool aligned, cudaStream_t s) {
-  if (aligned && p.cols % 8 != 0 && p.rows > 2 * sm_count() && p.cols + 7 <= 8 * kRnChunks * kRnThreads)
-    return launch_norm_stream<DT, RT, kRnThreads, true>(p, s);
-  if (!aligned || p.cols % 8 != 0) return p.cols <= 8192 ? launch_norm_rows<DT, RT, 1, 8>(p, s) : launch_norm_rows<DT, RT, 1, 32>(p, s);
-  // few rows: a row in as many threads as it has chunks
-  if (p.rows <= 2 * sm_count() && p.cols <= 8192) return launch_norm_rows<DT, RT, 8, 1>(p, s);
+  const bool few = p.rows <= 2 * sm_count() && p.cols <= 4096;
+  if (!aligned || p.cols % 8 != 0) {
+    if (aligned && !few && p.cols + 7 <= 8 * kRnChunks * kRnThreads) return launch_norm_stream<DT, RT, kRnThreads, true>(p, s);
+    return p.cols <= 8192 ? launch_norm_rows<DT, RT, 1, 8>(p, s) : launch_norm_rows<DT, RT, 1, 32>(p, s);
+  }
+  if (few) return launch_norm_rows<DT, RT, 8, 1>(p, s);
   if (p.cols <= 8 * kRnChunks * kRnThreads) return launch_norm_stream<DT, RT, kRnThreads, false>(p, s);
   if (p.cols <= 8 * kRnChunks * 512) return launch_norm_stream<DT, RT, 512, false>(p, s);
   return launch_norm_rows<DT, RT, 8, 4>(p, s);

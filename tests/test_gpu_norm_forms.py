@@ -70,3 +70,21 @@ def test_a_linear_layer_on_the_copies():
     wgrad = fq.fp8q_matmul_blockwise(qd["q_t"], qd["scale_inv_t"], n["q_t"], n["scale_inv_t"], a_fmt=fq.E5M2, b_block=fq.BLOCK_1X128)
     for got, want, off in ((fprop, y @ weight.float().t(), (2 ** -7) ** 0.5), (wgrad, d_out.float().t() @ y, (2 ** -6 + 2 ** -8) ** 0.5)):
         assert got.shape == want.shape and (got.float() - want).norm() < (off + 2 ** -7) * want.norm()
+
+
+@pytest.mark.parametrize("dt,rt", [(BF16, BF16), (BF16, None), (FP32, FP32), (FP32, None)])
+@pytest.mark.parametrize("rows,cols", [(1, 4097), (2, 4096), (1, 4104), (3, 4112), (304, 4112), (2, 5121), (5, 8185), (303, 8191), (7, 8192)])
+def test_few_rows_on_both_sides_of_4096_columns(dt, rt, rows, cols):
+    fq = require_cuda()
+    x, res, w = norm_inputs(rows, cols, dt, rt, FP32, rows + cols)
+    row = cols % 16 == 0
+    buf = {"y": Guarded((rows, cols), dt), "rstd": Guarded((rows,), FP32)} | ({"h": Guarded((rows, cols), rt)} if rt else {})
+    if row:
+        buf |= {"q": Guarded((rows, cols)), "scale_inv": Guarded((rows, -(-cols // 128)), FP32)}
+    r = fq.fp8q_rmsnorm(x, w, res, direction=fq.ROW if row else 0, want_y=True, out={k: b.t for k, b in buf.items()})
+    for b in buf.values():
+        b.check()
+    check_norm(r, x, res, w, 1e-6, 0, int(row), True)
+    if rt:  # in place
+        again = fq.fp8q_rmsnorm(x, w, res, direction=fq.ROW if row else 0, want_y=True, out={"h": res})
+        assert torch.equal(again["h"], r["h"]) and torch.equal(again["y"], r["y"])
