@@ -637,11 +637,14 @@ FP8Q_API size_t fp8q_moe_decode_workspace_bytes(int64_t tokens, int32_t top_k, i
  *   a = gate * up / (1 + exp(-gate)),  gate = W1[e][:inner] x[t],  up = W1[e][inner:] x[t]
  * with W1, W2 the values of blockwise codes (128x128 blocks).  Unlike the
  * path over fp8q_moe_dispatch and the grouped products, tokens and inner
- * values are not quantized: products and sums are FP32's (inner values keep
- * 22 bits for FP32 output, 11 for BF16; a token's values 2^-32 below the
- * largest of their 128 lose digits).  A slot whose id is no expert's (-1) adds nothing; an expert that
- * a token names twice counts with the sum of the weights.  Sums have a fixed
- * order.  Each chosen expert's weights are read once for up to 8 of its tokens.
+ * values are not quantized: products and sums are FP32's.  Inner values are off
+ * by 2^-22 of themselves for FP32 output and by 2^-11 for BF16, or by 2^-38 of
+ * the largest of their 32; a token's values are exact down to 2^-32 of the
+ * largest of their 128.  Where such a largest value times its scale_inv is
+ * below some 2^-111 all of them lose digits.  A slot whose id is no expert's
+ * (-1) adds nothing; an expert that a token names twice counts with the sum of
+ * the weights.  Sums have a fixed order.  Each chosen expert's weights are read
+ * once for up to 8 of its tokens.
  *   x             device BF16 [tokens][hidden], 16-byte aligned
  *   ids, weights  device int32, float [tokens][top_k], as fp8q_moe_route
  *                 writes them; top_k <= 32
@@ -668,9 +671,11 @@ FP8Q_API fp8q_status fp8q_moe_decode(const void* x, int64_t tokens, int64_t hidd
  *   rstd[r] = 1 / sqrt(sum_c h[r][c]^2 / cols + eps)
  *   y[r][c] = h[r][c] * rstd[r] * weight[c]
  * The copies are those of fp8q_quantize_blockwise with 1x128 groups for the
- * FP32 values of y.  Arithmetic is FP32: a row whose sum of squares
- * overflows FP32 (values from some 1e19 on) gives rstd 0, one without
- * any nonzero value gives y 0 (NaN with eps 0).
+ * FP32 values of y.  Arithmetic is FP32: a row whose sum of squares passes
+ * FP32's largest number (equal values from some 1.8e19 / sqrt(cols) on) gives
+ * rstd 0 and so y 0; squares below 2^-126 (of values below some 1e-19) lose
+ * digits, which shows where eps is no larger; a row without any nonzero value
+ * gives y 0 (NaN with eps 0).
  *   x          device, type dt (BF16 or FP32), [rows][cols], 1 <= cols <= 32768
  *   residual   device, type residual_dt, [rows][cols], or NULL
  *   weight     device, type weight_dt, [cols]

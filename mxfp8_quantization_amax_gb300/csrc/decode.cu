@@ -10,7 +10,9 @@
 // BF16 token row becomes FP16 exactly after a power of two for each 128 of it
 // (values 2^-32 below their group's largest lose digits).  The inner values
 // are FP16 with a power of two for each 32 of them; for FP32 output a
-// second FP16 number holds what the first one's rounding (2^-12) left.
+// second FP16 number holds what the first one's rounding (2^-11) left.  BF16
+// output, which rounds by 2^-8 at the end, does without: the second number's
+// products and loads are 12 to 16% of the layer (16 tokens 431 us against 382).
 //
 // First kernel: a unit is 32 inner values of one expert (rows of G and of U)
 // for up to 8 of its tokens; 8 or 4 warps of a CTA share K.  Second kernel: a
@@ -18,13 +20,14 @@
 // of K, and its warps share those; the CTAs of a cluster have the same columns
 // and add up through distributed shared memory.  Every sum has a fixed order.
 //
-// Bound by the weights' bytes: 64 experts of 7168 x 2048, 8 a token: 1 token 60
-// us (352 MB, 5.8 TB/s; some 7 us are the two kernels' start, lists and end), 4
-// tokens 178, 16 tokens 380 (6.6 TB/s).  Beyond 8 tokens an expert its weights are
-// read again, from L2, and converted again: 64 tokens 548 us (floor 421).  Sizes
-// whose K leaves warps idle cost more: 61 tokens, 40 experts of 2064 x 1360 97
-// us (floor 50).  Jobs of 16 tokens were slower everywhere (64 tokens 767 then
-// against 677): their registers leave one CTA an SM.
+// Bound by the weights' bytes.  64 experts of 7168 x 2048, 8 a token, BF16 (FP32)
+// output: 1 token 61 us (69; 352 MB, 5.8 TB/s; some 7 us are the two kernels'
+// start, lists and end), 4 tokens 185 (210), 16 tokens 382 (431; 6.6 TB/s).
+// Beyond 8 tokens an expert its weights are read again, from L2, and converted
+// again: 64 tokens 557 (646; floor 421).  Sizes whose K leaves warps idle cost
+// more: 61 tokens, 40 experts of 2064 x 1360 98 (110; floor 50).  Jobs of 16
+// tokens were slower everywhere (64 tokens 767 then against 677): their
+// registers leave one CTA an SM.
 #include "fp8q_device.cuh"
 #include "internal.h"
 
@@ -725,8 +728,8 @@ static fp8q_status launch_decode(const MdParams& p, cudaStream_t s) {
   const int slots = p.tokens * p.top_k;
   const int64_t per_job = (int64_t)p.kb2 * (128 / kMdUnit);
   const int64_t units = (slots < p.experts ? slots : p.experts + slots / kMdCols) * per_job;  // at most
-  // Half the warps a unit where K's blocks leave many of 8 warps idle and there are units enough (61 tokens, 40 experts
-  // of 2064 x 1360: 17 blocks, 97 us, 106 with 8; 16 tokens, 64 experts of 7168 x 2048: 56 blocks, 387 us, 380 with 8)
+  // Half the warps a unit where K's blocks leave many of 8 warps idle and there are units enough (BF16 output: 61 tokens, 40
+  // experts of 2064 x 1360: 17 blocks, 97 us, 106 with 8; 16 tokens, 64 experts of 7168 x 2048: 56 blocks, 387 us, 380 with 8)
   const int idle8 = (8 - p.kb1 % 8) % 8, idle4 = (4 - p.kb1 % 4) % 4;
   const bool four = (idle8 - idle4) * 8 > p.kb1 && (slots < p.experts ? slots : p.experts) * per_job >= 8 * (int64_t)sm_count();
   cudaError_t e = four ? launch_first<FMT, 4>(p, units, s) : launch_first<FMT, 8>(p, units, s);
