@@ -137,6 +137,12 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
 // next grid's CTAs then take the slots of CTAs that have finished instead
 // of crowding onto whichever SMs had room first, which would unbalance a
 // persistent grid whose work is dealt out by CTA index.
+// The one exception is the few-token expert layer (decode.cu).  Its first
+// kernel lets dependents start directly after its own pdl_wait(), and its
+// second reads the call's inputs before its pdl_wait().  That is sound because
+// a grid starts early only when every CTA of the one before it has said so:
+// whichever library kernel that is, it has waited for all earlier ones by then,
+// and the first kernel writes none of what the second reads early.
 __device__ __forceinline__ void pdl_wait() {
 #if FP8Q_PDL
   asm volatile("griddepcontrol.wait;" ::: "memory");
