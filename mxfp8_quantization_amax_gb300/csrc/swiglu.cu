@@ -277,10 +277,12 @@ static fp8q_status launch_swiglu_rows(const Src& src, const QtOut& o, cudaStream
 
 template <class Src, int FMT>
 static fp8q_status launch_swiglu(const Src& src, const QtOut& o, bool vec, cudaStream_t s) {
-  // The row copy alone by tiles where every SM gets some (4096 x 2048: 7.6 us, 8.8 a half-warp a group;
-  // 65536 x 2048: 100 and 135), else a half-warp a group (2000 x 2048: 4.4 us, 4.6 by tiles; its gradient 6.0, 7.2)
+  // The row copy alone by tiles from 3 an SM on, else a half-warp a group (us: 2000 x 2048 4.9 and 4.8, 4096 x 2048 8.1 and 8.4,
+  // 65536 x 2048 101 and 127; the gradient of 4099 x 1936 17.2 and 18.1).  Where one set of inputs gives two tiles the
+  // half-warp saves the second read too, and tiles win from 8 pairs an SM on (gradient of 4096 x 2048 13.4 and 12.0,
+  // 8192 x 2048 27.2 and 26.3, 10000 x 2048 31.9 and 32.1, 24576 x 2048 67 and 75).
   const int64_t tiles = (int64_t)o.tiles_r * o.tiles_c;
-  const bool many = (Src::kHalves && o.cols % (2 * kQtTile) == 0 ? tiles / 2 : tiles) >= 3 * sm_count();
+  const bool pairs = Src::kHalves && o.cols % (2 * kQtTile) == 0, many = pairs ? tiles / 2 >= 8 * sm_count() : tiles >= 3 * sm_count();
   if (o.q_t || (o.q && many)) {
     const cudaError_t e = !o.q_t ? launch_quant_tiles<Src, FMT, true, false>(src, o, s)
                           : o.q  ? launch_quant_tiles<Src, FMT, true, true>(src, o, s)

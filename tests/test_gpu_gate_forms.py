@@ -46,7 +46,7 @@ def without_dense(fn, r, buf, **kw):
 
 # rows that end inside a tile and inside a thread's eight, groups that end inside a tile
 FORWARD = [(4099, 2048, 1), (7301, 1040, 1), (12345, 656, 1), (4112, 2048, 3), (7312, 1040, 3), (7312, 1040, 2)]
-BACKWARD = [(4099, 2048, 1), (12345, 640, 1), (4099, 1928, 1), (7301, 520, 1), (4112, 2048, 3), (6160, 1032, 3), (7312, 1024, 2)]
+BACKWARD = [(9731, 2048, 1), (31111, 640, 1), (4099, 1928, 1), (7301, 520, 1), (4112, 2048, 3), (6160, 1032, 3), (7312, 1024, 2)]
 
 
 @pytest.mark.parametrize("dt", [BF16, FP32])
@@ -76,7 +76,8 @@ def test_tiles(dt, rows, inner, direction):
 @pytest.mark.parametrize("rows,inner,direction", BACKWARD)
 def test_gradient_tiles(dt, rows, inner, direction):
     fq = require_cuda()
-    assert tiles(rows, 2 * inner) // (1 if inner % 128 else 2) >= 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    pairs = inner % 128 == 0
+    assert tiles(rows, 2 * inner) // (2 if pairs else 1) >= (8 if pairs and direction == 1 else 3) * torch.cuda.get_device_properties(0).multi_processor_count
     h = gate_inputs(rows, inner, dt, rows)
     d_a = torch.randn(rows, inner, device="cuda", generator=gen(1)).to(dt)
     h[rows - 1] = 0.0
