@@ -758,8 +758,8 @@ FP8Q_API size_t fp8q_clip_grads_workspace_bytes(int32_t count);
  *   scale = min(1, max_norm / (norm + 1e-6)),  out[i] = grads[i] * scale
  * Squares are added in FP32 over up to 64 values and in FP64 beyond, in a
  * fixed order: values from some 1e18 on overflow, those below some 1e-20
- * count as 0.  A norm of NaN or Inf is reported as it is; Inf gives scale 0,
- * NaN gives NaN.
+ * count as 0.  A norm of NaN or Inf is reported as it is; Inf gives scale 0
+ * (NaN where max_norm is Inf too), NaN gives NaN.
  *   grads, out  host arrays of `count` device pointers; a tensor may be
  *               overwritten by its own output (out[i] == grads[i]; with
  *               scale 1 it is then left alone); an output that overlaps

@@ -10,7 +10,8 @@
 // in shared memory, and neither copy needs the values a second time.
 //
 // Bound by memory and issue together: the activation of 65536 x 2048 in both
-// copies 124 us (6.6 TB/s); one CTA a tile without the inputs on their way 158.
+// copies 128 us (6.3 TB/s); an earlier form 158 with a CTA a tile, 124 with CTAs
+// that stay and have the next inputs on their way.
 #pragma once
 
 #include "fp8q_device.cuh"
