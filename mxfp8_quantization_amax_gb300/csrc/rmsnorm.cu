@@ -14,7 +14,8 @@
 // 120 with a CTA a row), gradients 87 us (6.2 TB/s), the transposed copy 34 us
 // more: it needs the statistics of 128 rows, and 128 rows of 4096 do not fit an
 // SM, so h is read again.  12345 x 7168, FP32 stream, y and row copy 188 us (6.1
-// TB/s).  Without a residual issue bounds it (16384 x 7168 78 us, 4.5 TB/s).  Odd
+// TB/s).  Without a residual dependent chains on 16 warps an SM bound it
+// (16384 x 7168 78 us, 4.5 TB/s; issue 62%).  Odd
 // columns: 12345 x 4097 80 us (5.0 TB/s), gradients 107 us (2.8 TB/s); value by
 // value, as unaligned tensors are taken, 159 and 295.  One row of 7168: 2.8 us,
 // latency.
@@ -221,7 +222,7 @@ constexpr int kRnBytes = DT == kNone ? 0 : 32 * kQtRunBytes<DT>;  // of a warp's
 template <int DT, int RT, int T, bool ODD>
 __global__ void __launch_bounds__(T, T == kRnThreads ? 2 : 1) rmsnorm_stream_kernel(RmsNorm p) {
   constexpr int kChunk = kRnBytes<DT> + kRnBytes<RT>;
-  // Without a residual instructions bound it: addresses go from row to row, and chunks behind the row are 0 from the start.
+  // Without a residual a row's chain of instructions bounds it: addresses go from row to row, and chunks behind the row are 0 from the start.
   constexpr bool kLean = RT == kNone && !ODD;
   extern __shared__ __align__(16) uint8_t inputs[];  // [warps][chunks][kChunk]
   __shared__ float sh[64];
